@@ -18,7 +18,13 @@
  *   mla_decompress_k_paged_fp8_qcache  the FP8 decompress reading a quantised paged cache.
  *   mla_cache_write_paged[_qcache]     the cache-write side of mla_prefill_decode_graph_fp8
  *                               (kv_norm_gamma, epsilon, freqs_cis): RMSNorm and RoPE of new
- *                               latent rows stored into a bf16 or a quantised paged cache.
+ *                               latent rows stored into a bf16 or a quantised paged cache
+ *                               (+ _at: rotary positions given apart from the slots).
+ *   mla_tree_attention_paged[_qcache]  the decode attention of mla_prefill_decode_graph_fp8
+ *                               (kv_collection, scale, output) in latent space: new tokens
+ *                               (one, a chain or a drafted tree) over the paged cache.
+ *   mla_rope_heads              its query rotation (freqs_cis) at given positions.
+ *   mla_cache_compact_paged[_qcache]  accepted drafts moved to the front of their region.
  *   kv_matmul_paged[_fp8]       kv_matmul_ragged_paged (nn/kv_cache_ragged; description and
  *                               Args): Y = hidden_state . weight on the ragged rows, with
  *                               row i of request b written into the paged K/V cache at
@@ -83,9 +89,10 @@ typedef enum {
  *                     num_kv_heads*head_size for kv_matmul_paged (per plane).
  *   page_table        device uint32 [batch, max_pages_per_seq], row-major.
  *   cache_lengths     device uint32 [batch]: tokens already in the cache per request.  Read
- *                     by kv_matmul_paged only (and never updated by it); may be NULL for
- *                     the decompress entry points.
- *   kv_stride         offset of the V plane from the K plane; kv_matmul_paged only.
+ *                     by every entry point but the decompress ones (and never updated);
+ *                     may be NULL for the decompress entry points.
+ *   kv_stride         offset of the V plane from the K plane; kv_matmul_paged, and
+ *                     mla_cache_compact_paged (0: the cache has one plane).
  */
 typedef struct {
     void* data;
@@ -313,6 +320,178 @@ pkm_status mla_cache_write_paged(const void* latent, const uint32_t* input_row_o
                                  const float* freqs_cis, int32_t max_seq_len,
                                  const pkm_paged_cache* cache, uint32_t layer_idx,
                                  int32_t* dev_status, void* stream);
+
+/*
+ * mla_cache_write_paged for rows whose rotary position is not their cache position.
+ * Source: mla_prefill_decode_graph_fp8 -- Args freqs_cis, input_row_offsets, kv_collection
+ * (as for mla_cache_write_paged; the pages place every new token at its cache position).
+ *
+ * The tokens of a drafted tree occupy consecutive slots cache_lengths[b] + i, but a token at
+ * depth d of the tree is the sequence's token cache_lengths[b] + d.  Row r is stored where
+ * mla_cache_write_paged stores it and rotated by freqs_cis[positions[r]].
+ *
+ *   positions       device uint32 [total_rows], below max_seq_len (a larger one sets
+ *                   PKM_ERR_OUT_OF_RANGE and leaves that row unwritten).
+ *   other arguments and errors as for mla_cache_write_paged; with positions[r] =
+ *   cache_lengths[b] + i the two calls write the same bits.
+ */
+pkm_status mla_cache_write_paged_at(const void* latent, const uint32_t* input_row_offsets,
+                                    const uint32_t* positions, int32_t batch,
+                                    int32_t total_rows, int32_t kv_lora_rank, int32_t rope_dim,
+                                    const float* kv_norm_gamma, float epsilon,
+                                    const float* freqs_cis, int32_t max_seq_len,
+                                    const pkm_paged_cache* cache, uint32_t layer_idx,
+                                    int32_t* dev_status, void* stream);
+
+/* mla_cache_write_paged_at into a quantised cache (mla_cache_write_paged_qcache's slots). */
+pkm_status mla_cache_write_paged_qcache_at(const void* latent,
+                                           const uint32_t* input_row_offsets,
+                                           const uint32_t* positions, int32_t batch,
+                                           int32_t total_rows, const float* kv_norm_gamma,
+                                           float epsilon, const float* freqs_cis,
+                                           int32_t max_seq_len, const pkm_quant_cache* cache,
+                                           uint32_t layer_idx, int32_t* dev_status,
+                                           void* stream);
+
+/*
+ * Position rotation of the queries' rope columns.
+ * Source: mla_prefill_decode_graph_fp8 -- Args q (rows of num_heads heads whose last
+ * qk_rope_head_dim columns carry the position) and freqs_cis.
+ *
+ * For every row r < total_rows and head h < num_heads, with (c, s) the pairs of
+ * freqs_cis[positions[r]] and P = rope_dim:
+ *     half = 0: (y[2j], y[2j+1])   = (x[2j] c_j - x[2j+1] s_j, x[2j] s_j + x[2j+1] c_j)
+ *     half = 1: (y[j], y[j+P/2])   = (x[j] c_j - x[j+P/2] s_j, x[j] s_j + x[j+P/2] c_j)
+ * for j < P/2, where x and y are the P columns at x + r * x_row_stride + h * x_head_stride
+ * and y + r * y_row_stride + h * y_head_stride.  fp32 arithmetic, one rounding to bf16.
+ * Only those columns of y are written, so x can point into the query projection's output
+ * [rows, heads, nope + P] and y into the attention's query [rows, heads, R + P].  A table
+ * stretched for long contexts, its values scaled or not, is passed like any other.
+ *
+ *   x               device bf16, 16-byte aligned, the first rope column of row 0, head 0.
+ *   x_*_stride      elements, multiples of 8 (>= 0; 0 broadcasts).
+ *   positions       device uint32 [total_rows]; an entry >= max_seq_len sets
+ *                   PKM_ERR_OUT_OF_RANGE in dev_status and leaves that row unwritten.
+ *   rope_dim        P: a multiple of 8, at most 256.
+ *   freqs_cis       device fp32 [max_seq_len, P], 16-byte aligned: P/2 (cos, sin) pairs per
+ *                   position, pair j being the layout's pair j.
+ *   y               device bf16, 16-byte aligned; y_*_stride multiples of 8 for which no two
+ *                   (row, head) blocks overlap (PKM_ERR_INVALID_ARG otherwise).  y may be x
+ *                   with the same strides (in place), and may not overlap it otherwise.
+ */
+pkm_status mla_rope_heads(const void* x, int64_t x_row_stride, int64_t x_head_stride,
+                          const uint32_t* positions, int32_t total_rows, int32_t num_heads,
+                          int32_t rope_dim, const float* freqs_cis, int32_t max_seq_len,
+                          int32_t half, void* y, int64_t y_row_stride, int64_t y_head_stride,
+                          int32_t* dev_status, void* stream);
+
+/*
+ * Bytes of device workspace mla_tree_attention_paged[_qcache] needs (0 for invalid sizes).
+ * It holds the partial results of requests that several CTAs share; its contents need not
+ * be kept or cleared between calls, but calls that may overlap need one each.
+ */
+size_t mla_tree_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
+                                               int32_t kv_lora_rank);
+
+/*
+ * Attention of new tokens -- one per request, a chain, or a tree of drafts -- over the paged
+ * latent cache.
+ * Source: mla_prefill_decode_graph_fp8 -- Args q, input_row_offsets, kv_collection,
+ * layer_idx, Parameters scale and mask_str, and the output: its decode path, with the query
+ * already projected into latent space (Args w_uk) and the output left there (Args w_uv).
+ * Every head reads the same row of the cache, as key in all its C = R + P columns and as
+ * value in its first R.
+ *
+ * Request b has n_b = input_row_offsets[b+1] - input_row_offsets[b] new tokens, whose rows
+ * the cache write has already put at positions cache_lengths[b] + j.  For its token i, with
+ * r = input_row_offsets[b] + i (skipped when r >= total_rows) and head h, over the positions
+ *     t < cache_lengths[b], and t = cache_lengths[b] + j (j < n_b) for which
+ *       tree_mask != NULL: bit j % 32 of tree_mask[r, j / 32] is set (j < 32 * mask_words)
+ *       tree_mask == NULL: j <= i
+ * it computes
+ *     w_t = softmax_t(softmax_scale * sum_{c < C} q[r, h, c] * slot(t)[c])
+ *     out[r, h, c] = bf16( sum_t w_t * slot(t)[c] ),  c < R
+ *     lse[r, h]    = log sum_t exp(softmax_scale * sum_c q[r, h, c] * slot(t)[c])
+ * A row without any such position gets out = 0 and lse = -infinity.  A draft that a row does
+ * not attend has no influence on it, whatever its slot holds (NaN and infinities included).
+ * Rows that no request covers are left untouched.  Scores and sums are fp32; the weights are
+ * rounded to bf16 for the second product.  Two calls with the same arguments on the same
+ * device give the same bits.
+ *
+ *   q               device bf16 [total_rows, num_heads, C], 16-byte aligned.
+ *   input_row_offsets  device uint32 [batch+1], non-decreasing (pkm_validate_row_offsets).
+ *   num_heads       > 0; total_rows * num_heads at most 2^31 - 257.
+ *   kv_lora_rank    R: a multiple of 64, 64..512.
+ *   rope_dim        P: a multiple of 8 with R + P <= 576.
+ *   softmax_scale   finite.
+ *   tree_mask       device uint32 [total_rows, mask_words], or NULL.
+ *   cache           row_elems = R + P; cache_lengths required.
+ *   out             device bf16 [total_rows, num_heads, R], 16-byte aligned.
+ *   lse             device fp32 [total_rows, num_heads], or NULL.
+ *   workspace       device, >= mla_tree_attention_paged_workspace_size(...) bytes, 256-byte
+ *                   aligned.
+ * A position past the page-table row or in a page id >= num_pages sets PKM_ERR_OUT_OF_RANGE
+ * in dev_status and is not read; the rows of that request then hold unspecified values.
+ */
+pkm_status mla_tree_attention_paged(const void* q, const uint32_t* input_row_offsets,
+                                    int32_t batch, int32_t total_rows, int32_t num_heads,
+                                    int32_t kv_lora_rank, int32_t rope_dim, float softmax_scale,
+                                    const uint32_t* tree_mask, int32_t mask_words,
+                                    const pkm_paged_cache* cache, uint32_t layer_idx, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, void* stream);
+
+/*
+ * mla_tree_attention_paged over a quantised cache: slot(t) is the row that
+ * mla_decompress_k_paged_fp8_qcache returns in k_latent_buffer (bf16_rne(fl32(e4m3(code) *
+ * scale)) in its first R columns, the bf16 rope columns behind them).  R and P come from the
+ * descriptor (R a multiple of 128, at most 512; R + P <= 576; cache_lengths required).
+ */
+pkm_status mla_tree_attention_paged_qcache(const void* q, const uint32_t* input_row_offsets,
+                                           int32_t batch, int32_t total_rows,
+                                           int32_t num_heads, float softmax_scale,
+                                           const uint32_t* tree_mask, int32_t mask_words,
+                                           const pkm_quant_cache* cache, uint32_t layer_idx,
+                                           void* out, float* lse, void* workspace,
+                                           size_t workspace_bytes, int32_t* dev_status,
+                                           void* stream);
+
+/*
+ * Accepted drafts move to the front of their request's drafted region.
+ * Source: the paged cache of kv_matmul_ragged_paged and mla_prefill_decode_graph_fp8 (Args
+ * kv_collection, cache_lengths); the pages do not describe what follows a rejected draft.
+ *
+ * Request b's drafts are at positions cache_lengths[b] + i.  With m = accepted_counts[b] and
+ * its accepted drafts a_j = accepted[b * max_accepted + j], j < m, strictly increasing (a
+ * path of a tree whose parents come before their children), in each layer of
+ * [layer_begin, layer_begin + layer_count):
+ *     slot(cache_lengths[b] + j) = slot(cache_lengths[b] + a_j)      for j < m, bit for bit,
+ * every source as it was before the call, and new_lengths[b] = cache_lengths[b] + m.  No
+ * other slot changes; with kv_stride != 0 both planes move.  A drafted region belongs to one
+ * request: no other request of the batch may hold its pages' drafted slots.
+ *
+ *   max_accepted     row length of `accepted` (> 0).
+ *   accepted         device uint32 [batch, max_accepted].
+ *   accepted_counts  device uint32 [batch].
+ *   new_lengths      device uint32 [batch], or NULL; not cache->cache_lengths.
+ *   cache            row_elems a multiple of 8; cache_lengths required.
+ * A request whose count exceeds max_accepted or whose drafts do not increase sets
+ * PKM_ERR_INVALID_ARG in dev_status, one with a position outside the page table or the cache
+ * PKM_ERR_OUT_OF_RANGE; such a request moves nothing and keeps its length.
+ */
+pkm_status mla_cache_compact_paged(const pkm_paged_cache* cache, uint32_t layer_begin,
+                                   int32_t layer_count, int32_t batch,
+                                   const uint32_t* accepted, int32_t max_accepted,
+                                   const uint32_t* accepted_counts, uint32_t* new_lengths,
+                                   int32_t* dev_status, void* stream);
+
+/* mla_cache_compact_paged for a quantised cache (the payload bytes of every slot move). */
+pkm_status mla_cache_compact_paged_qcache(const pkm_quant_cache* cache, uint32_t layer_begin,
+                                          int32_t layer_count, int32_t batch,
+                                          const uint32_t* accepted, int32_t max_accepted,
+                                          const uint32_t* accepted_counts,
+                                          uint32_t* new_lengths, int32_t* dev_status,
+                                          void* stream);
 
 /*
  * FP8 latent-K decompress from a quantised paged cache.

@@ -15,6 +15,12 @@ Entry points (same names as the C ABI in include/paged_kv_mla.h):
   mla_decompress_k_paged_fp8_qcache   the FP8 decompress reading a quantised paged cache
   mla_cache_write_paged               RMSNorm + RoPE of new latent rows into the paged cache
   mla_cache_write_paged_qcache        the same into a quantised paged cache
+  mla_cache_write_paged_at            both with rotary positions given apart from the slots
+    (+ _qcache_at)
+  mla_tree_attention_paged            attention of new tokens (one, a chain, a drafted tree)
+    (+ _qcache, _workspace_size)      over the paged latent cache, in latent space
+  mla_rope_heads                      rotation of the queries' rope columns at given positions
+  mla_cache_compact_paged (+ _qcache) accepted drafts moved to the front of their region
   kv_matmul_paged                     kv_matmul_ragged_paged (bf16)
   kv_matmul_paged_fp8                 its FP8 block-scaled form (+ kv_matmul_paged_fp8_workspace_size)
   pkm_check_wait_timeout              the bounded-wait self-check
@@ -96,6 +102,32 @@ _lib.mla_decompress_k_paged_fp8_qcache.restype = ctypes.c_int
 _lib.mla_cache_write_paged_qcache.argtypes = [_vp, _vp, _i32, _i32, _vp, ctypes.c_float, _vp,
                                               _i32, ctypes.POINTER(_CQuantCache), _u32, _vp, _vp]
 _lib.mla_cache_write_paged_qcache.restype = ctypes.c_int
+_f32, _i64 = ctypes.c_float, ctypes.c_int64
+_lib.mla_cache_write_paged_at.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _f32, _vp,
+                                          _i32, ctypes.POINTER(_CCache), _u32, _vp, _vp]
+_lib.mla_cache_write_paged_at.restype = ctypes.c_int
+_lib.mla_cache_write_paged_qcache_at.argtypes = [_vp, _vp, _vp, _i32, _i32, _vp, _f32, _vp, _i32,
+                                                 ctypes.POINTER(_CQuantCache), _u32, _vp, _vp]
+_lib.mla_cache_write_paged_qcache_at.restype = ctypes.c_int
+_lib.mla_rope_heads.argtypes = [_vp, _i64, _i64, _vp, _i32, _i32, _i32, _vp, _i32, _i32, _vp, _i64,
+                                _i64, _vp, _vp]
+_lib.mla_rope_heads.restype = ctypes.c_int
+_lib.mla_tree_attention_paged_workspace_size.argtypes = [_i32, _i32, _i32]
+_lib.mla_tree_attention_paged_workspace_size.restype = _sz
+_lib.mla_tree_attention_paged.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32,
+                                          ctypes.POINTER(_CCache), _u32, _vp, _vp, _vp, _sz, _vp,
+                                          _vp]
+_lib.mla_tree_attention_paged.restype = ctypes.c_int
+_lib.mla_tree_attention_paged_qcache.argtypes = [_vp, _vp, _i32, _i32, _i32, _f32, _vp, _i32,
+                                                 ctypes.POINTER(_CQuantCache), _u32, _vp, _vp,
+                                                 _vp, _sz, _vp, _vp]
+_lib.mla_tree_attention_paged_qcache.restype = ctypes.c_int
+_lib.mla_cache_compact_paged.argtypes = [ctypes.POINTER(_CCache), _u32, _i32, _i32, _vp, _i32, _vp,
+                                         _vp, _vp, _vp]
+_lib.mla_cache_compact_paged.restype = ctypes.c_int
+_lib.mla_cache_compact_paged_qcache.argtypes = [ctypes.POINTER(_CQuantCache), _u32, _i32, _i32,
+                                                _vp, _i32, _vp, _vp, _vp, _vp]
+_lib.mla_cache_compact_paged_qcache.restype = ctypes.c_int
 _lib.mla_decompress_kv_paged.argtypes = [ctypes.POINTER(_CCache), _u32, _vp, _vp, _i32, _i32, _i32,
                                          _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
 _lib.mla_decompress_kv_paged.restype = ctypes.c_int
@@ -156,7 +188,7 @@ class PagedCache:
 
     data: bf16 storage (any shape; only its base pointer is used).
     page_table: uint32/int32 [batch, max_pages_per_seq].
-    cache_lengths: uint32/int32 [batch] (kv_matmul_paged only).
+    cache_lengths: uint32/int32 [batch] (every call but the decompress ones).
     """
     data: torch.Tensor
     page_table: torch.Tensor
@@ -347,6 +379,149 @@ def mla_cache_write_paged(latent: torch.Tensor, input_row_offsets: torch.Tensor,
     return _check(code, "mla_cache_write_paged", check)
 
 
+def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tensor,
+                             positions: torch.Tensor, kv_norm_gamma: torch.Tensor,
+                             epsilon: float, freqs_cis: torch.Tensor, cache: PagedCache,
+                             layer_idx: int, kv_lora_rank: int, rope_dim: int,
+                             dev_status: Optional[torch.Tensor] = None, stream=None,
+                             check: bool = True) -> int:
+    """mla_cache_write_paged with row r rotated by freqs_cis[positions[r]] (positions:
+    uint32/int32 [total_rows]), wherever its slot is."""
+    c = cache.c_struct()
+    batch = int(input_row_offsets.shape[0]) - 1
+    code = _lib.mla_cache_write_paged_at(_ptr(latent), _ptr(input_row_offsets), _ptr(positions),
+                                         batch, int(latent.shape[0]), int(kv_lora_rank),
+                                         int(rope_dim), _ptr(kv_norm_gamma), float(epsilon),
+                                         _ptr(freqs_cis), int(freqs_cis.shape[0]),
+                                         ctypes.byref(c), int(layer_idx), _ptr(dev_status),
+                                         _stream(stream))
+    return _check(code, "mla_cache_write_paged_at", check)
+
+
+def mla_cache_write_paged_qcache_at(latent: torch.Tensor, input_row_offsets: torch.Tensor,
+                                    positions: torch.Tensor, kv_norm_gamma: torch.Tensor,
+                                    epsilon: float, freqs_cis: torch.Tensor, cache: QuantCache,
+                                    layer_idx: int, dev_status: Optional[torch.Tensor] = None,
+                                    stream=None, check: bool = True) -> int:
+    """mla_cache_write_paged_qcache with row r rotated by freqs_cis[positions[r]]."""
+    c = cache.c_struct()
+    batch = int(input_row_offsets.shape[0]) - 1
+    code = _lib.mla_cache_write_paged_qcache_at(_ptr(latent), _ptr(input_row_offsets),
+                                                _ptr(positions), batch, int(latent.shape[0]),
+                                                _ptr(kv_norm_gamma), float(epsilon),
+                                                _ptr(freqs_cis), int(freqs_cis.shape[0]),
+                                                ctypes.byref(c), int(layer_idx),
+                                                _ptr(dev_status), _stream(stream))
+    return _check(code, "mla_cache_write_paged_qcache_at", check)
+
+
+def mla_rope_heads(x: torch.Tensor, positions: torch.Tensor, freqs_cis: torch.Tensor,
+                   y: torch.Tensor, half: bool = False,
+                   dev_status: Optional[torch.Tensor] = None, stream=None,
+                   check: bool = True) -> int:
+    """Rotates x [rows, heads, P] into y [rows, heads, P] (bf16 views with contiguous last
+    dimensions; y may be x) by the (cos, sin) pairs of freqs_cis[positions[row]]: pairs
+    (2j, 2j + 1), or (j, j + P/2) with `half`."""
+    if x.shape != y.shape or x.dim() != 3 or positions.numel() != x.shape[0] \
+            or freqs_cis.shape[-1] != x.shape[-1] or x.stride(-1) != 1 or y.stride(-1) != 1:
+        return _check(PKM_ERR_INVALID_ARG, "mla_rope_heads", check)
+    code = _lib.mla_rope_heads(_ptr(x), x.stride(0), x.stride(1), _ptr(positions),
+                               int(x.shape[0]), int(x.shape[1]), int(x.shape[2]),
+                               _ptr(freqs_cis), int(freqs_cis.shape[0]), int(bool(half)), _ptr(y),
+                               y.stride(0), y.stride(1), _ptr(dev_status), _stream(stream))
+    return _check(code, "mla_rope_heads", check)
+
+
+def mla_tree_attention_paged_workspace_size(total_rows: int, num_heads: int,
+                                            kv_lora_rank: int) -> int:
+    return int(_lib.mla_tree_attention_paged_workspace_size(int(total_rows), int(num_heads),
+                                                            int(kv_lora_rank)))
+
+
+def _tree_shapes_ok(q, tree_mask, out, lse) -> bool:
+    """Shapes that the C call cannot see; an empty mask would pass for no mask there."""
+    rows, heads = q.shape[0], q.shape[1]
+    return (out.shape[:2] == (rows, heads) and (lse is None or lse.shape == (rows, heads)) and
+            (tree_mask is None or (tree_mask.dim() == 2 and tree_mask.shape[0] == rows and
+                                   tree_mask.shape[1] > 0)))
+
+
+def mla_tree_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
+                             softmax_scale: float, cache: PagedCache, layer_idx: int,
+                             kv_lora_rank: int, rope_dim: int, out: torch.Tensor,
+                             workspace: torch.Tensor, tree_mask: Optional[torch.Tensor] = None,
+                             lse: Optional[torch.Tensor] = None,
+                             dev_status: Optional[torch.Tensor] = None, stream=None,
+                             check: bool = True) -> int:
+    """Attention of the new tokens' latent-space queries q [total_rows, heads, R + P] over the
+    cache: each over its request's cached tokens and those new ones that its tree_mask row
+    (uint32/int32 [total_rows, words], one bit a token; None: the tokens up to itself) names.
+    out [total_rows, heads, R] bf16, lse [total_rows, heads] fp32 or None."""
+    if not _tree_shapes_ok(q, tree_mask, out, lse):
+        return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged", check)
+    c = cache.c_struct()
+    batch = int(input_row_offsets.shape[0]) - 1
+    code = _lib.mla_tree_attention_paged(
+        _ptr(q), _ptr(input_row_offsets), batch, int(q.shape[0]), int(q.shape[1]),
+        int(kv_lora_rank), int(rope_dim), float(softmax_scale), _ptr(tree_mask),
+        0 if tree_mask is None else int(tree_mask.shape[-1]), ctypes.byref(c), int(layer_idx),
+        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(dev_status), _stream(stream))
+    return _check(code, "mla_tree_attention_paged", check)
+
+
+def mla_tree_attention_paged_qcache(q: torch.Tensor, input_row_offsets: torch.Tensor,
+                                    softmax_scale: float, cache: QuantCache, layer_idx: int,
+                                    out: torch.Tensor, workspace: torch.Tensor,
+                                    tree_mask: Optional[torch.Tensor] = None,
+                                    lse: Optional[torch.Tensor] = None,
+                                    dev_status: Optional[torch.Tensor] = None, stream=None,
+                                    check: bool = True) -> int:
+    """mla_tree_attention_paged over a quantised cache."""
+    if not _tree_shapes_ok(q, tree_mask, out, lse):
+        return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged_qcache", check)
+    c = cache.c_struct()
+    batch = int(input_row_offsets.shape[0]) - 1
+    code = _lib.mla_tree_attention_paged_qcache(
+        _ptr(q), _ptr(input_row_offsets), batch, int(q.shape[0]), int(q.shape[1]),
+        float(softmax_scale), _ptr(tree_mask),
+        0 if tree_mask is None else int(tree_mask.shape[-1]), ctypes.byref(c), int(layer_idx),
+        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(dev_status), _stream(stream))
+    return _check(code, "mla_tree_attention_paged_qcache", check)
+
+
+def mla_cache_compact_paged(cache: PagedCache, layer_begin: int, layer_count: int,
+                            accepted: torch.Tensor, accepted_counts: torch.Tensor,
+                            new_lengths: Optional[torch.Tensor] = None,
+                            dev_status: Optional[torch.Tensor] = None, stream=None,
+                            check: bool = True) -> int:
+    """Moves request b's accepted drafts accepted[b, :accepted_counts[b]] (strictly increasing
+    indices behind cache_lengths[b]) to the front of its drafted region in every layer of the
+    range, and writes the grown lengths to new_lengths."""
+    c = cache.c_struct()
+    code = _lib.mla_cache_compact_paged(ctypes.byref(c), int(layer_begin), int(layer_count),
+                                        int(accepted.shape[0]), _ptr(accepted),
+                                        int(accepted.shape[1]), _ptr(accepted_counts),
+                                        _ptr(new_lengths), _ptr(dev_status), _stream(stream))
+    return _check(code, "mla_cache_compact_paged", check)
+
+
+def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_count: int,
+                                   accepted: torch.Tensor, accepted_counts: torch.Tensor,
+                                   new_lengths: Optional[torch.Tensor] = None,
+                                   dev_status: Optional[torch.Tensor] = None, stream=None,
+                                   check: bool = True) -> int:
+    """mla_cache_compact_paged for a quantised cache."""
+    c = cache.c_struct()
+    code = _lib.mla_cache_compact_paged_qcache(ctypes.byref(c), int(layer_begin),
+                                               int(layer_count), int(accepted.shape[0]),
+                                               _ptr(accepted), int(accepted.shape[1]),
+                                               _ptr(accepted_counts), _ptr(new_lengths),
+                                               _ptr(dev_status), _stream(stream))
+    return _check(code, "mla_cache_compact_paged_qcache", check)
+
+
 def kv_matmul_paged_fp8_workspace_size(total_rows: int, k_in: int) -> int:
     return int(_lib.kv_matmul_paged_fp8_workspace_size(int(total_rows), int(k_in)))
 
@@ -411,7 +586,10 @@ def pkm_check_wait_timeout(dev_status: torch.Tensor, timeout_ms: int, stream=Non
 __all__ = ["pkm_check_wait_timeout", "mla_decompress_k_paged_fp8_noalloc",
            "FP8_NOALLOC_SCRATCH_BYTES", "PagedCache", "PkmError", "mla_decompress_k_paged", "mla_decompress_k_paged_fp8",
            "mla_decompress_k_paged_fp8_workspace_size", "fp8_workspace_views", "kv_matmul_paged",
-           "status_string", "LIB_PATH", "PKM_OK", "PKM_ERR_INVALID_ARG", "PKM_ERR_UNSUPPORTED",
+           "mla_cache_write_paged_at", "mla_cache_write_paged_qcache_at", "mla_rope_heads",
+           "mla_tree_attention_paged", "mla_tree_attention_paged_qcache",
+           "mla_tree_attention_paged_workspace_size", "mla_cache_compact_paged",
+           "mla_cache_compact_paged_qcache", "status_string", "LIB_PATH", "PKM_OK", "PKM_ERR_INVALID_ARG", "PKM_ERR_UNSUPPORTED",
            "PKM_ERR_CUDA", "PKM_ERR_OUT_OF_RANGE", "PKM_ERR_TIMEOUT"]
 
 

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
@@ -20,6 +21,9 @@ using pkm::Fp8Extra;
 using pkm::CacheWriteArgs;
 using pkm::KvMatmulArgs;
 using pkm::KvFp8Extra;
+using pkm::RopeHeadsArgs;
+using pkm::CompactArgs;
+using pkm::TreeAttentionArgs;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool mult8(int64_t v) { return v >= 0 && (v % 8) == 0; }
@@ -580,13 +584,14 @@ pkm_status mla_decompress_k_paged_fp8_qcache(const pkm_quant_cache* cache, uint3
 
 namespace {
 
-// Body of both cache-write entry points: a bf16 cache, or (qcache) a quantised one.
+// Body of the cache-write entry points: a bf16 cache, or (qcache) a quantised one; rotary
+// positions from an array, or (null) the rows' cache positions.
 pkm_status cache_write(const void* latent, const uint32_t* input_row_offsets, int32_t batch,
                        int32_t total_rows, int32_t kv_lora_rank, int32_t rope_dim,
                        const float* kv_norm_gamma, float epsilon, const float* freqs_cis,
                        int32_t max_seq_len, const pkm_paged_cache* cache,
                        const pkm_quant_cache* qcache, uint32_t layer_idx, int32_t* dev_status,
-                       void* stream) {
+                       void* stream, const uint32_t* positions = nullptr) {
     if (batch < 0 || total_rows < 0 || kv_lora_rank <= 0 || rope_dim < 0 || max_seq_len <= 0)
         return PKM_ERR_INVALID_ARG;
     if (batch == 0 || total_rows == 0) return PKM_OK;
@@ -653,6 +658,7 @@ pkm_status cache_write(const void* latent, const uint32_t* input_row_offsets, in
     a.epsilon = epsilon;
     a.freqs = freqs_cis;
     a.max_seq_len = max_seq_len;
+    a.positions = positions;
     a.status = dev_status;
     a.timeout_ns = wait_timeout_ns();
     int sms = 0;
@@ -687,6 +693,319 @@ pkm_status mla_cache_write_paged_qcache(const void* latent, const uint32_t* inpu
     return cache_write(latent, input_row_offsets, batch, total_rows, cache->kv_lora_rank,
                        cache->rope_dim, kv_norm_gamma, epsilon, freqs_cis, max_seq_len, nullptr,
                        cache, layer_idx, dev_status, stream);
+}
+
+pkm_status mla_cache_write_paged_at(const void* latent, const uint32_t* input_row_offsets,
+                                    const uint32_t* positions, int32_t batch,
+                                    int32_t total_rows, int32_t kv_lora_rank, int32_t rope_dim,
+                                    const float* kv_norm_gamma, float epsilon,
+                                    const float* freqs_cis, int32_t max_seq_len,
+                                    const pkm_paged_cache* cache, uint32_t layer_idx,
+                                    int32_t* dev_status, void* stream) {
+    if (positions == nullptr && batch > 0 && total_rows > 0) return PKM_ERR_INVALID_ARG;
+    return cache_write(latent, input_row_offsets, batch, total_rows, kv_lora_rank, rope_dim,
+                       kv_norm_gamma, epsilon, freqs_cis, max_seq_len, cache, nullptr,
+                       layer_idx, dev_status, stream, positions);
+}
+
+pkm_status mla_cache_write_paged_qcache_at(const void* latent,
+                                           const uint32_t* input_row_offsets,
+                                           const uint32_t* positions, int32_t batch,
+                                           int32_t total_rows, const float* kv_norm_gamma,
+                                           float epsilon, const float* freqs_cis,
+                                           int32_t max_seq_len, const pkm_quant_cache* cache,
+                                           uint32_t layer_idx, int32_t* dev_status,
+                                           void* stream) {
+    if (cache == nullptr) return PKM_ERR_INVALID_ARG;
+    if (positions == nullptr && batch > 0 && total_rows > 0) return PKM_ERR_INVALID_ARG;
+    return cache_write(latent, input_row_offsets, batch, total_rows, cache->kv_lora_rank,
+                       cache->rope_dim, kv_norm_gamma, epsilon, freqs_cis, max_seq_len, nullptr,
+                       cache, layer_idx, dev_status, stream, positions);
+}
+
+pkm_status mla_rope_heads(const void* x, int64_t x_row_stride, int64_t x_head_stride,
+                          const uint32_t* positions, int32_t total_rows, int32_t num_heads,
+                          int32_t rope_dim, const float* freqs_cis, int32_t max_seq_len,
+                          int32_t half, void* y, int64_t y_row_stride, int64_t y_head_stride,
+                          int32_t* dev_status, void* stream) {
+    if (total_rows < 0 || num_heads < 0 || rope_dim <= 0 || max_seq_len <= 0)
+        return PKM_ERR_INVALID_ARG;
+    if (total_rows == 0 || num_heads == 0) return PKM_OK;
+    if (x == nullptr || y == nullptr || positions == nullptr || freqs_cis == nullptr)
+        return PKM_ERR_INVALID_ARG;
+    if (half != 0 && half != 1) return PKM_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(freqs_cis)) return PKM_ERR_INVALID_ARG;
+    if (!mult8(x_row_stride) || !mult8(x_head_stride) || !mult8(y_row_stride) ||
+        !mult8(y_head_stride))
+        return PKM_ERR_INVALID_ARG;
+    if (rope_dim % 8 != 0 || rope_dim > 256) return PKM_ERR_UNSUPPORTED;
+    // the rows and heads of y must not overlap: heads inside rows, or rows inside heads
+    const int64_t r1 = total_rows - 1, h1 = num_heads - 1, p = rope_dim;
+    const int64_t wide = static_cast<int64_t>(1) << 62;
+    const auto spans = [&](int64_t n, int64_t stride) {  // n * stride + p, saturated
+        return stride > 0 && n > (wide - p) / stride ? wide : n * stride + p;
+    };
+    const bool heads_inside = (h1 == 0 || y_head_stride >= p) &&
+                              (r1 == 0 || y_row_stride >= spans(h1, y_head_stride));
+    const bool rows_inside = (r1 == 0 || y_row_stride >= p) &&
+                             (h1 == 0 || y_head_stride >= spans(r1, y_row_stride));
+    if (!heads_inside && !rows_inside) return PKM_ERR_INVALID_ARG;
+    if (x == y && ((r1 > 0 && x_row_stride != y_row_stride) ||
+                   (h1 > 0 && x_head_stride != y_head_stride)))
+        return PKM_ERR_INVALID_ARG;
+    RopeHeadsArgs a{};
+    a.x = static_cast<const uint16_t*>(x);
+    a.y = static_cast<uint16_t*>(y);
+    a.x_row_stride = x_row_stride;
+    a.x_head_stride = x_head_stride;
+    a.y_row_stride = y_row_stride;
+    a.y_head_stride = y_head_stride;
+    a.positions = positions;
+    a.total_rows = total_rows;
+    a.num_heads = num_heads;
+    a.rope_dim = rope_dim;
+    a.freqs = freqs_cis;
+    a.max_seq_len = max_seq_len;
+    a.half = half;
+    a.status = dev_status;
+    int sms = 0;
+    if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
+    return cuda_status(pkm::launch_rope_heads(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Body of both compaction entry points, once the cache is described in bytes.
+pkm_status cache_compact(CompactArgs a, const uint32_t* accepted, int32_t max_accepted,
+                         const uint32_t* accepted_counts, uint32_t* new_lengths,
+                         int32_t* dev_status, void* stream) {
+    if (accepted == nullptr || accepted_counts == nullptr || a.data == nullptr ||
+        a.page_table == nullptr || a.cache_lengths == nullptr)
+        return PKM_ERR_INVALID_ARG;
+    if (new_lengths == a.cache_lengths) return PKM_ERR_INVALID_ARG;
+    a.accepted = accepted;
+    a.max_accepted = max_accepted;
+    a.counts = accepted_counts;
+    a.new_lengths = new_lengths;
+    a.status = dev_status;
+    return cuda_status(pkm::launch_cache_compact(a, static_cast<cudaStream_t>(stream)));
+}
+
+bool layers_inside(uint32_t begin, int32_t count, int32_t num_layers) {
+    return num_layers > 0 && begin < static_cast<uint32_t>(num_layers) &&
+           count <= num_layers - static_cast<int32_t>(begin);
+}
+
+}  // namespace
+
+extern "C" {
+
+pkm_status mla_cache_compact_paged(const pkm_paged_cache* cache, uint32_t layer_begin,
+                                   int32_t layer_count, int32_t batch,
+                                   const uint32_t* accepted, int32_t max_accepted,
+                                   const uint32_t* accepted_counts, uint32_t* new_lengths,
+                                   int32_t* dev_status, void* stream) {
+    if (batch < 0 || layer_count < 0 || max_accepted <= 0) return PKM_ERR_INVALID_ARG;
+    if (batch == 0 || layer_count == 0) return PKM_OK;
+    if (cache == nullptr || !layers_inside(layer_begin, layer_count, cache->num_layers) ||
+        cache->num_pages <= 0 || cache->page_size <= 0 || cache->max_pages_per_seq <= 0 ||
+        cache->row_elems <= 0)
+        return PKM_ERR_INVALID_ARG;
+    if (!mult8(cache->layer_stride) || !mult8(cache->page_stride) ||
+        !mult8(cache->slot_stride) || !mult8(cache->kv_stride) || !aligned16(cache->data))
+        return PKM_ERR_INVALID_ARG;
+    if (cache->row_elems % 8 != 0 || cache->row_elems > (1 << 28)) return PKM_ERR_UNSUPPORTED;
+    CompactArgs a{};
+    a.data = static_cast<uint8_t*>(cache->data) +
+             2 * static_cast<int64_t>(layer_begin) * cache->layer_stride;
+    a.layer_stride = 2 * cache->layer_stride;
+    a.page_stride = 2 * cache->page_stride;
+    a.slot_stride = 2 * cache->slot_stride;
+    a.kv_stride = 2 * cache->kv_stride;
+    a.planes = cache->kv_stride != 0 ? 2 : 1;
+    a.layer_count = layer_count;
+    a.payload = 2 * cache->row_elems;
+    a.num_pages = cache->num_pages;
+    a.page_size = cache->page_size;
+    a.max_pages = cache->max_pages_per_seq;
+    a.page_table = cache->page_table;
+    a.cache_lengths = cache->cache_lengths;
+    a.batch = batch;
+    return cache_compact(a, accepted, max_accepted, accepted_counts, new_lengths, dev_status,
+                         stream);
+}
+
+pkm_status mla_cache_compact_paged_qcache(const pkm_quant_cache* cache, uint32_t layer_begin,
+                                          int32_t layer_count, int32_t batch,
+                                          const uint32_t* accepted, int32_t max_accepted,
+                                          const uint32_t* accepted_counts,
+                                          uint32_t* new_lengths, int32_t* dev_status,
+                                          void* stream) {
+    if (batch < 0 || layer_count < 0 || max_accepted <= 0) return PKM_ERR_INVALID_ARG;
+    if (batch == 0 || layer_count == 0) return PKM_OK;
+    if (cache == nullptr || !layers_inside(layer_begin, layer_count, cache->num_layers) ||
+        cache->num_pages <= 0 || cache->page_size <= 0 || cache->max_pages_per_seq <= 0 ||
+        cache->kv_lora_rank <= 0 || cache->rope_dim < 0)
+        return PKM_ERR_INVALID_ARG;
+    if (cache->kv_lora_rank % 128 != 0 || cache->kv_lora_rank > 1024 ||
+        cache->rope_dim % 8 != 0 || cache->rope_dim > 256)
+        return PKM_ERR_UNSUPPORTED;
+    const int32_t payload =
+        cache->kv_lora_rank + 2 * cache->rope_dim + 4 * (cache->kv_lora_rank / 128);
+    if (cache->layer_stride < 0 || cache->layer_stride % 16 != 0 || cache->page_stride < 0 ||
+        cache->page_stride % 16 != 0 || cache->slot_stride % 16 != 0 ||
+        cache->slot_stride < payload || !aligned16(cache->data))
+        return PKM_ERR_INVALID_ARG;
+    CompactArgs a{};
+    a.data = static_cast<uint8_t*>(cache->data) +
+             static_cast<int64_t>(layer_begin) * cache->layer_stride;
+    a.layer_stride = cache->layer_stride;
+    a.page_stride = cache->page_stride;
+    a.slot_stride = cache->slot_stride;
+    a.planes = 1;
+    a.layer_count = layer_count;
+    a.payload = payload;
+    a.num_pages = cache->num_pages;
+    a.page_size = cache->page_size;
+    a.max_pages = cache->max_pages_per_seq;
+    a.page_table = cache->page_table;
+    a.cache_lengths = cache->cache_lengths;
+    a.batch = batch;
+    return cache_compact(a, accepted, max_accepted, accepted_counts, new_lengths, dev_status,
+                         stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Body of both attention entry points, once the cache's part of `a` is filled in.
+pkm_status tree_attention(TreeAttentionArgs a, const void* q, const uint32_t* input_row_offsets,
+                          int32_t batch, int32_t total_rows, int32_t num_heads,
+                          int32_t kv_lora_rank, int32_t rope_dim, float softmax_scale,
+                          const uint32_t* tree_mask, int32_t mask_words, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                          void* stream) {
+    if (q == nullptr || input_row_offsets == nullptr || out == nullptr || workspace == nullptr)
+        return PKM_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale)) return PKM_ERR_INVALID_ARG;
+    if (tree_mask != nullptr && mask_words <= 0) return PKM_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return PKM_ERR_INVALID_ARG;
+    if (kv_lora_rank % 64 != 0 || kv_lora_rank > 512 || rope_dim % 8 != 0 ||
+        kv_lora_rank + rope_dim > 576)
+        return PKM_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(total_rows) * num_heads > INT32_MAX - 256)
+        return PKM_ERR_UNSUPPORTED;
+    if (workspace_bytes <
+        mla_tree_attention_paged_workspace_size(total_rows, num_heads, kv_lora_rank))
+        return PKM_ERR_INVALID_ARG;
+    a.q = static_cast<const uint16_t*>(q);
+    a.row_offsets = input_row_offsets;
+    a.batch = batch;
+    a.total_rows = total_rows;
+    a.num_heads = num_heads;
+    a.kv_lora_rank = kv_lora_rank;
+    a.cols = kv_lora_rank + rope_dim;
+    a.scale = softmax_scale;
+    a.mask = tree_mask;
+    a.mask_words = mask_words;
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.workspace = static_cast<uint8_t*>(workspace);
+    a.status = dev_status;
+    a.timeout_ns = wait_timeout_ns();
+    int sms = 0;
+    if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
+    if (const cudaError_t e = debug_validate(input_row_offsets, batch, dev_status, stream))
+        return cuda_status(e);
+    return cuda_status(pkm::launch_tree_attention(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mla_tree_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
+                                               int32_t kv_lora_rank) {
+    if (total_rows < 0 || num_heads <= 0 || kv_lora_rank <= 0) return 0;
+    return pkm::tree_workspace(total_rows, num_heads, kv_lora_rank).bytes;
+}
+
+pkm_status mla_tree_attention_paged(const void* q, const uint32_t* input_row_offsets,
+                                    int32_t batch, int32_t total_rows, int32_t num_heads,
+                                    int32_t kv_lora_rank, int32_t rope_dim, float softmax_scale,
+                                    const uint32_t* tree_mask, int32_t mask_words,
+                                    const pkm_paged_cache* cache, uint32_t layer_idx, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, void* stream) {
+    if (batch < 0 || total_rows < 0 || num_heads <= 0 || kv_lora_rank <= 0 || rope_dim < 0)
+        return PKM_ERR_INVALID_ARG;
+    if (batch == 0 || total_rows == 0) return PKM_OK;
+    if (cache == nullptr || cache->data == nullptr || cache->page_table == nullptr ||
+        cache->cache_lengths == nullptr)
+        return PKM_ERR_INVALID_ARG;
+    if (cache->num_layers <= 0 || layer_idx >= static_cast<uint32_t>(cache->num_layers) ||
+        cache->num_pages <= 0 || cache->page_size <= 0 || cache->max_pages_per_seq <= 0 ||
+        cache->row_elems != kv_lora_rank + rope_dim)
+        return PKM_ERR_INVALID_ARG;
+    if (!mult8(cache->layer_stride) || !mult8(cache->page_stride) ||
+        !mult8(cache->slot_stride) || !aligned16(cache->data))
+        return PKM_ERR_INVALID_ARG;
+    TreeAttentionArgs a{};
+    a.cache_layer = static_cast<const uint16_t*>(cache->data) +
+                    static_cast<int64_t>(layer_idx) * cache->layer_stride;
+    a.page_stride = cache->page_stride;
+    a.slot_stride = cache->slot_stride;
+    a.num_pages = cache->num_pages;
+    a.page_size = cache->page_size;
+    a.max_pages = cache->max_pages_per_seq;
+    a.page_table = cache->page_table;
+    a.cache_lengths = cache->cache_lengths;
+    return tree_attention(a, q, input_row_offsets, batch, total_rows, num_heads, kv_lora_rank,
+                          rope_dim, softmax_scale, tree_mask, mask_words, out, lse, workspace,
+                          workspace_bytes, dev_status, stream);
+}
+
+pkm_status mla_tree_attention_paged_qcache(const void* q, const uint32_t* input_row_offsets,
+                                           int32_t batch, int32_t total_rows,
+                                           int32_t num_heads, float softmax_scale,
+                                           const uint32_t* tree_mask, int32_t mask_words,
+                                           const pkm_quant_cache* cache, uint32_t layer_idx,
+                                           void* out, float* lse, void* workspace,
+                                           size_t workspace_bytes, int32_t* dev_status,
+                                           void* stream) {
+    if (cache == nullptr) return PKM_ERR_INVALID_ARG;
+    const int32_t rank = cache->kv_lora_rank, rope = cache->rope_dim;
+    if (batch < 0 || total_rows < 0 || num_heads <= 0 || rank <= 0 || rope < 0)
+        return PKM_ERR_INVALID_ARG;
+    if (batch == 0 || total_rows == 0) return PKM_OK;
+    if (cache->data == nullptr || cache->page_table == nullptr ||
+        cache->cache_lengths == nullptr)
+        return PKM_ERR_INVALID_ARG;
+    if (cache->num_layers <= 0 || layer_idx >= static_cast<uint32_t>(cache->num_layers) ||
+        cache->num_pages <= 0 || cache->page_size <= 0 || cache->max_pages_per_seq <= 0)
+        return PKM_ERR_INVALID_ARG;
+    if (rank % 128 != 0 || rank > 512 || rope % 8 != 0 || rope > 256) return PKM_ERR_UNSUPPORTED;
+    if (cache->layer_stride < 0 || cache->layer_stride % 16 != 0 || cache->page_stride < 0 ||
+        cache->page_stride % 16 != 0 || cache->slot_stride % 16 != 0 ||
+        cache->slot_stride < rank + 2 * rope + 4 * (rank / 128) || !aligned16(cache->data))
+        return PKM_ERR_INVALID_ARG;
+    TreeAttentionArgs a{};
+    a.qcache_layer = static_cast<const uint8_t*>(cache->data) +
+                     static_cast<int64_t>(layer_idx) * cache->layer_stride;
+    a.page_stride = cache->page_stride;
+    a.slot_stride = cache->slot_stride;
+    a.num_pages = cache->num_pages;
+    a.page_size = cache->page_size;
+    a.max_pages = cache->max_pages_per_seq;
+    a.page_table = cache->page_table;
+    a.cache_lengths = cache->cache_lengths;
+    return tree_attention(a, q, input_row_offsets, batch, total_rows, num_heads, rank, rope,
+                          softmax_scale, tree_mask, mask_words, out, lse, workspace,
+                          workspace_bytes, dev_status, stream);
 }
 
 pkm_status kv_matmul_paged(const void* hidden_state, const uint32_t* input_row_offsets,

@@ -21,7 +21,9 @@
 // consumer warps then takes two rows of the chunk out of shared memory, frees the stage,
 // reduces the sum of squares across the warp and writes the normalised and rotated rows
 // (fp32 arithmetic, rounded to bf16) straight into their slots with 16-byte stores.
-// Nothing else in the cache is written.
+// Nothing else in the cache is written.  The tokens of a drafted tree take their rotary
+// positions (length + depth) from an array instead: siblings share one, while their slots
+// stay consecutive.
 //
 // Into a quantised cache (PagedKVCacheCollection's scale_dtype_ / quantization_granularity_)
 // the rounded bf16 values of each 128-column block are quantised on the spot, the block
@@ -137,11 +139,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t r = r0 + lane;
             int32_t slot = kSlotNone, req = -1;
             uint32_t page = 0;
-            uint64_t pos = 0;
+            uint64_t rot = 0;  // the row's freqs_cis row: its position unless given apart
             if (lane < kChunkRows && r < covered && q.seek(a, r)) {
-                pos = static_cast<uint64_t>(q.cl) + static_cast<uint64_t>(r - q.lo);
+                const uint64_t pos = static_cast<uint64_t>(q.cl) + static_cast<uint64_t>(r - q.lo);
                 const uint64_t lp = pos / static_cast<uint64_t>(a.page_size);
-                if (pos >= static_cast<uint64_t>(a.max_seq_len) ||
+                rot = a.positions != nullptr ? __ldg(a.positions + r) : pos;
+                if (rot >= static_cast<uint64_t>(a.max_seq_len) ||
                     lp >= static_cast<uint64_t>(a.max_pages)) {
                     slot = kSlotOutOfRange;
                 } else {
@@ -161,17 +164,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 reinterpret_cast<uint32_t*>(stage + L.page)[lane] = page;
             }
             // freqs_cis rows: one bulk copy per run of rows of one request (consecutive
-            // positions, so consecutive freqs_cis rows)
+            // positions, so consecutive freqs_cis rows); with positions given apart a run
+            // also ends where they are not consecutive
             const bool live = slot >= 0;
             const int prev_live = __shfl_up_sync(0xffffffffu, live ? 1 : 0, 1);
             const int prev_req = __shfl_up_sync(0xffffffffu, req, 1);
-            const bool run_start = live && (lane == 0 || !prev_live || prev_req != req);
+            bool run_start = live && (lane == 0 || !prev_live || prev_req != req);
+            if (a.positions != nullptr) {
+                const uint64_t prev_rot = __shfl_up_sync(0xffffffffu, rot, 1);
+                run_start = run_start || (live && rot != prev_rot + 1);
+            }
             const uint32_t live_mask = __ballot_sync(0xffffffffu, live);
             const uint32_t bound = __ballot_sync(0xffffffffu, !live || run_start);
             if (run_start && P > 0) {
                 const uint32_t after = bound & ~((2u << lane) - 1u);  // lane < 30 here
                 const int len = __ffs(after) - 1 - lane;
-                bulk_load_1d(stage + L.freqs + lane * P * 4, a.freqs + pos * P,
+                bulk_load_1d(stage + L.freqs + lane * P * 4, a.freqs + rot * P,
                              static_cast<uint32_t>(len * P * 4), full);
             }
             if (lane == 0)

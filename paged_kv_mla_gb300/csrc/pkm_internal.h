@@ -69,6 +69,58 @@ struct CacheWriteArgs {
     int32_t* status;
     uint64_t timeout_ns;
     uint8_t* qcache_layer;         // quantised destination (byte strides), or null
+    const uint32_t* positions;     // rotary position of every row, or null: the cache position
+};
+
+// One rotation of the queries' rope columns, already validated (strides in elements).
+struct RopeHeadsArgs {
+    const uint16_t* x;             // first rope column of row 0, head 0
+    uint16_t* y;
+    int64_t x_row_stride, x_head_stride, y_row_stride, y_head_stride;
+    const uint32_t* positions;     // [total_rows]
+    int32_t total_rows, num_heads, rope_dim;
+    const float* freqs;            // [max_seq_len, P]
+    int32_t max_seq_len;
+    int32_t half;                  // pairs (j, j + P/2) instead of (2j, 2j + 1)
+    int32_t* status;
+};
+
+// One compaction of accepted drafts, already validated.  Strides and payload in bytes.
+struct CompactArgs {
+    uint8_t* data;                 // first layer to be compacted
+    int64_t layer_stride, page_stride, slot_stride, kv_stride;
+    int32_t layer_count, planes;   // planes: 1, or 2 with a V plane at kv_stride
+    int32_t payload;               // bytes of a slot that hold the row (a multiple of 4)
+    int32_t num_pages, page_size, max_pages;
+    const uint32_t* page_table;
+    const uint32_t* cache_lengths;
+    int32_t batch;
+    const uint32_t* accepted;      // [batch, max_accepted]
+    int32_t max_accepted;
+    const uint32_t* counts;        // [batch]
+    uint32_t* new_lengths;         // [batch], or null
+    int32_t* status;
+};
+
+// One tree attention, already validated.  Strides in elements (bytes for a quantised cache).
+struct TreeAttentionArgs {
+    const uint16_t* q;             // [total_rows, num_heads, C]
+    const uint32_t* row_offsets;   // [batch + 1]
+    int32_t batch, total_rows, num_heads, kv_lora_rank, cols;
+    float scale;
+    const uint32_t* mask;          // [total_rows, mask_words], or null: j <= i
+    int32_t mask_words;
+    const uint16_t* cache_layer;   // bf16 cache layer, or null
+    const uint8_t* qcache_layer;   // quantised cache layer, or null
+    int64_t page_stride, slot_stride;
+    int32_t num_pages, page_size, max_pages;
+    const uint32_t* page_table;
+    const uint32_t* cache_lengths;
+    uint16_t* out;                 // [total_rows, num_heads, R]
+    float* lse;                    // [total_rows, num_heads], or null
+    uint8_t* workspace;
+    int32_t* status;
+    uint64_t timeout_ns;
 };
 
 // One kv_matmul problem, already validated.
@@ -97,6 +149,30 @@ struct KvFp8Extra {
     float* q_scale;                // [M, k_in/128] (workspace)
     const float* w_scale;          // [n_out/128, k_in/128]
 };
+
+// Workspace of the tree attention: what CTA pairs that share an item (one 128-row tile of one
+// request) leave for the kernel that joins their parts.  A pair starts at most one item that
+// it does not finish and finishes at most one that it did not start, so it has two slots.
+constexpr int kTreeMaxPairs = 80;
+struct TreeWorkspace {
+    int32_t rows;       // rows a slot holds
+    size_t parts;       // fp32 [2 * kTreeMaxPairs, rows, R], unnormalised
+    size_t stats;       // fp32 [2 * kTreeMaxPairs, rows, 2]: maximum (base 2) and sum
+    size_t items;       // int32 [kTreeMaxPairs, 4]: item a pair starts and leaves unfinished
+    size_t bytes;
+};
+
+inline TreeWorkspace tree_workspace(int32_t total_rows, int32_t num_heads, int32_t rank) {
+    const auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
+    const int64_t all = static_cast<int64_t>(total_rows) * num_heads;
+    TreeWorkspace w{};
+    w.rows = static_cast<int32_t>(all < 128 ? all : 128);
+    const size_t slots = 2 * kTreeMaxPairs;
+    w.stats = up(slots * w.rows * rank * sizeof(float));
+    w.items = w.stats + up(slots * w.rows * 2 * sizeof(float));
+    w.bytes = w.items + up(kTreeMaxPairs * 4 * sizeof(int32_t));
+    return w;
+}
 
 // Launches `kernel` as a programmatic dependent of the work before it on `stream`: it may
 // start while the previous kernel (a prepass that triggers its dependents) still runs, and
@@ -139,6 +215,9 @@ cudaError_t launch_kv_matmul_fp8(const CUtensorMap& tm_q, const CUtensorMap& tm_
                                  KvMatmulArgs args, KvFp8Extra extra, int num_sms,
                                  cudaStream_t stream);
 cudaError_t launch_cache_write(CacheWriteArgs args, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope_heads(RopeHeadsArgs args, int num_sms, cudaStream_t stream);
+cudaError_t launch_cache_compact(CompactArgs args, cudaStream_t stream);
+cudaError_t launch_tree_attention(TreeAttentionArgs args, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_timeout_check(int32_t* status, uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t launch_validate_offsets(const uint32_t* offsets, int32_t batch, int32_t* status,
                                     cudaStream_t stream);
