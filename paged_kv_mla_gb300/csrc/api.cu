@@ -132,6 +132,26 @@ bool encode_cache_gather(CUtensorMap* map, const void* layer, int32_t page_size,
            CUDA_SUCCESS;
 }
 
+// One layer of the paged latent cache as a 3-D tensor {column, slot, page}, boxes of
+// {64, box_slots, 1}: 64 columns of consecutive slots of one page, 128-byte swizzled, zeros
+// past the row's columns and for pages that do not exist.
+bool encode_cache_pages(CUtensorMap* map, const void* layer, int32_t cols, int32_t page_size,
+                        int32_t num_pages, int64_t slot_stride, int64_t page_stride,
+                        uint32_t box_slots) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(page_size),
+                                static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(slot_stride) * 2,
+                                   static_cast<cuuint64_t>(page_stride) * 2};
+    const cuuint32_t box[3] = {64, box_slots, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(layer), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 // Checks shared by both decompress entry points.  Returns PKM_OK or the error.
 pkm_status check_decompress(const pkm_paged_cache* cache, uint32_t layer_idx, const uint32_t* bro,
                             const uint32_t* co, int32_t batch, int32_t buffer_length,
@@ -919,9 +939,24 @@ pkm_status tree_attention(TreeAttentionArgs a, const void* q, const uint32_t* in
     a.timeout_ns = wait_timeout_ns();
     int sms = 0;
     if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
+    // Query rows and, where the pages are divided by boxes of at least 8 slots (whole swizzle
+    // atoms), the cache come by TMA; other pages and quantised rows are loaded row by row.
+    int box = 64;
+    while (box > 1 && a.page_size % box != 0) box /= 2;
+    alignas(64) CUtensorMap tm_q, tm_c;
+    if (!encode_2d(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, a.cols,
+                   static_cast<uint64_t>(total_rows) * num_heads,
+                   static_cast<uint64_t>(a.cols) * 2, 64, 64))
+        return encode_failed();
+    if (a.qcache_layer != nullptr || box < 8)
+        tm_c = tm_q;
+    else if (!encode_cache_pages(&tm_c, a.cache_layer, a.cols, a.page_size, a.num_pages,
+                                 a.slot_stride, a.page_stride, static_cast<uint32_t>(box)))
+        return encode_failed();
     if (const cudaError_t e = debug_validate(input_row_offsets, batch, dev_status, stream))
         return cuda_status(e);
-    return cuda_status(pkm::launch_tree_attention(a, sms, static_cast<cudaStream_t>(stream)));
+    return cuda_status(pkm::launch_tree_attention(tm_q, tm_c, a, box, sms,
+                                                  static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace

@@ -154,11 +154,15 @@ struct KvFp8Extra {
 // request) leave for the kernel that joins their parts.  A pair starts at most one item that
 // it does not finish and finishes at most one that it did not start, so it has two slots.
 constexpr int kTreeMaxPairs = 80;
+struct TreeItem {       // an item that a pair starts and leaves unfinished (rows = 0: none)
+    int64_t first;      // first of its rows (token, head)
+    int32_t rows, parts;
+};
 struct TreeWorkspace {
     int32_t rows;       // rows a slot holds
     size_t parts;       // fp32 [2 * kTreeMaxPairs, rows, R], unnormalised
     size_t stats;       // fp32 [2 * kTreeMaxPairs, rows, 2]: maximum (base 2) and sum
-    size_t items;       // int32 [kTreeMaxPairs, 4]: item a pair starts and leaves unfinished
+    size_t items;       // TreeItem [kTreeMaxPairs]
     size_t bytes;
 };
 
@@ -170,7 +174,7 @@ inline TreeWorkspace tree_workspace(int32_t total_rows, int32_t num_heads, int32
     const size_t slots = 2 * kTreeMaxPairs;
     w.stats = up(slots * w.rows * rank * sizeof(float));
     w.items = w.stats + up(slots * w.rows * 2 * sizeof(float));
-    w.bytes = w.items + up(kTreeMaxPairs * 4 * sizeof(int32_t));
+    w.bytes = w.items + up(kTreeMaxPairs * sizeof(TreeItem));
     return w;
 }
 
@@ -217,7 +221,9 @@ cudaError_t launch_kv_matmul_fp8(const CUtensorMap& tm_q, const CUtensorMap& tm_
 cudaError_t launch_cache_write(CacheWriteArgs args, int num_sms, cudaStream_t stream);
 cudaError_t launch_rope_heads(RopeHeadsArgs args, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_compact(CompactArgs args, cudaStream_t stream);
-cudaError_t launch_tree_attention(TreeAttentionArgs args, int num_sms, cudaStream_t stream);
+cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_cache,
+                                  TreeAttentionArgs args, int box, int num_sms,
+                                  cudaStream_t stream);
 cudaError_t launch_wait_timeout_check(int32_t* status, uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t launch_validate_offsets(const uint32_t* offsets, int32_t batch, int32_t* status,
                                     cudaStream_t stream);

@@ -1,124 +1,881 @@
-// tree_attention.cu -- absorbed MLA attention of new (drafted) tokens over the paged latent
-// cache: one warp per (token, head), online softmax, fp32 throughout.
+// tree_attention.cu -- absorbed MLA attention of new tokens (one, a chain, a drafted tree)
+// over the paged latent cache, on CTA pairs.
+//
+// mla_prefill_decode_graph_fp8 (Modular MAX, attention/gpu/mla_graph), its decode path: Args
+// q, input_row_offsets, kv_collection, layer_idx, Parameters scale, mask_str.  Every head of
+// a request reads the same latent row L_t (C = R + P columns), so the new tokens' heads are
+// the rows of one matrix product, and the same tile of L serves twice:
+//     S = Q L^T                  [rows x keys], all C columns
+//     O = softmax(scale S) L     [rows x R],    the first R columns of L
+//
+// An item is 128 query rows (token, head) of one request.  The fp32 accumulator of 128 rows
+// x 512 columns would fill the whole tensor memory of an SM, so a pair of CTAs shares an
+// item: with tcgen05.mma.cta_group::2, M = 128, each CTA holds 64 rows, spread over all 128
+// lanes (lanes 0-63 hold the first half of the columns, lanes 64-127 the second), and 512
+// columns of O take 256 TMEM columns, next to two 128-key score tiles of 64.  For S the pair
+// splits the keys (each CTA loads 64 keys, all columns), for O the columns (each CTA loads
+// all 128 keys, half the columns): a latent value comes from L2 once as key and once as
+// value.  What the values cost in loads, the full-rate MMA gives back: the 64-row form of a
+// single CTA runs at half the rate.
+//
+// The key axis of all items is one line of 128-key tiles, cut into equal parts, one for each
+// pair: a pair starts at most one item that it does not finish and finishes at most one that
+// it did not start.  Such parts leave unnormalised fp32 sums, maxima and totals in the
+// workspace and a second kernel joins them; whole items are written directly.
+//
+// Roles of a CTA (14 warps): 0-3 softmax and epilogue, 4 MMA issue (even CTA), 5-8 keys,
+// 9-12 values, 13 queries.  Scores are kept in base 2; the running maximum moves only when
+// a row's new maximum exceeds it by 2^8, since any reference works as long as nothing
+// overflows, so the accumulator is hardly ever rescaled.
+#include <cuda_fp16.h>
+
 #include "pkm_device.cuh"
 #include "pkm_internal.h"
 
 namespace pkm {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kPieces = 3;  // 8-column pieces a lane holds of a row of up to 768 columns
+constexpr int kSoftWarps = 4, kMmaWarp = 4, kKeyWarp = 5, kValueWarp = 9, kQueryWarp = 13;
+constexpr int kThreads = 14 * 32;
+constexpr int kKeys = 128;          // keys of a tile (64 loaded by each CTA as keys)
+constexpr int kBlocks = 9;          // 64-column blocks of a latent row
+constexpr int kBlockBytes = 64 * 128;
+constexpr int kValueBlocks = 4;     // 64-column value blocks a CTA loads
+constexpr int kValueBytes = kKeys * 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScoreCol = 256; // TMEM column of the first score tile
+constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
-    bf16x2_to_f32(v.x, f[0], f[1]);
-    bf16x2_to_f32(v.y, f[2], f[3]);
-    bf16x2_to_f32(v.z, f[4], f[5]);
-    bf16x2_to_f32(v.w, f[6], f[7]);
+enum Source { kTma, kRows, kCodes };  // pages by TMA, bf16 rows by loads, quantised rows
+
+struct Bars {
+    uint64_t k_full[kBlocks];   // even CTA: a 64-column block of both CTAs' keys is there
+    uint64_t k_empty[kBlocks];  // both: its MMAs are done
+    uint64_t v_full[2];         // even CTA: two value blocks of both CTAs are there
+    uint64_t v_empty[2];        // both
+    uint64_t q_full, q_empty;   // the item's query rows
+    uint64_t s_full[2];         // both: a score tile is complete
+    uint64_t p_full;            // even CTA: both CTAs' weights are written
+    uint64_t o_full;            // both: the tile's weights are used up and O is current
+    uint64_t o_empty;           // even CTA: both CTAs' epilogues have read O
+    uint64_t mma_done;
+    int64_t units;              // tiles of all items
+    int64_t start_unit;         // first tile of the request that holds this pair's first
+    int32_t start_request;
+    uint32_t tmem_base;
+    int abort_flag;
+    int k_go, v_go;             // the leading key / value warp's verdict on a wait
+};
+
+constexpr size_t kOffQ = 0;
+constexpr size_t kOffK = kOffQ + size_t(kBlocks) * kBlockBytes;
+constexpr size_t kOffV = kOffK + size_t(kBlocks) * kBlockBytes;
+constexpr size_t kOffP = kOffV + size_t(kValueBlocks) * kValueBytes;
+constexpr size_t kOffMax = kOffP + 2 * size_t(kBlockBytes);
+constexpr size_t kOffSum = kOffMax + 2 * 128 * sizeof(float);
+constexpr size_t kOffBars = kOffSum + 128 * sizeof(float);
+constexpr size_t kSmemBytes = kOffBars + sizeof(Bars) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103a CTA");
+
+// One request as the schedule sees it.
+struct Request {
+    int64_t first;   // its first row
+    int32_t n;       // its new tokens
+    int64_t len;     // cached tokens before them
+    int64_t kv;      // positions that exist: len + n, cut at the page-table row
+    int64_t tiles;   // 128-key tiles
+    int64_t items;   // 128-row items
+
+    __device__ __forceinline__ void load(const TreeAttentionArgs& a, int b) {
+        const int64_t lo = min(static_cast<int64_t>(__ldg(a.row_offsets + b)),
+                               static_cast<int64_t>(a.total_rows));
+        const int64_t hi = min(static_cast<int64_t>(__ldg(a.row_offsets + b + 1)),
+                               static_cast<int64_t>(a.total_rows));
+        first = lo;
+        n = hi > lo ? static_cast<int32_t>(hi - lo) : 0;
+        len = __ldg(a.cache_lengths + b);
+        kv = min(len + n, static_cast<int64_t>(a.max_pages) * a.page_size);
+        tiles = (kv + kKeys - 1) / kKeys;
+        items = (static_cast<int64_t>(n) * a.num_heads + 127) / 128;
+    }
+    __device__ __forceinline__ int64_t units() const { return n > 0 ? tiles * items : 0; }
+};
+
+// A pair's share [u, end) of the tiles of all items, walked item by item.  After next()
+// returned true, the part is tiles [kt0, kt1) of item `item` of request r.
+struct Walk {
+    int64_t u, end, base;  // base: first unit of the request
+    int b, batch;
+    Request r;
+    int64_t item, kt0, kt1;
+
+    __device__ __forceinline__ Walk(const TreeAttentionArgs& a, const Bars* bars, int64_t pair,
+                                    int64_t pairs) {
+        u = min(pair, pairs) * bars->units / max(pairs, static_cast<int64_t>(1));
+        end = min(pair + 1, pairs) * bars->units / max(pairs, static_cast<int64_t>(1));
+        base = bars->start_unit;
+        b = bars->start_request;
+        batch = a.batch;
+        if (u < end) r.load(a, b);
+    }
+    __device__ __forceinline__ bool next(const TreeAttentionArgs& a) {
+        if (u >= end) return false;
+        while (u >= base + r.units()) {  // u < units: a request further on holds it
+            base += r.units();
+            r.load(a, ++b);
+        }
+        item = (u - base) / r.tiles;
+        kt0 = (u - base) % r.tiles;
+        kt1 = min(r.tiles, kt0 + (end - u));
+        u += kt1 - kt0;
+        return true;
+    }
+    // First tile whose keys are not all cached tokens that every row attends.
+    __device__ __forceinline__ bool partial(int64_t kt) const {
+        return (kt + 1) * kKeys > min(r.len, r.kv);
+    }
+};
+
+// Counts the tiles of all requests and finds the request of the pair's first one; every
+// thread sums a run of requests.  `scratch`: 16 int64 of shared memory.
+__device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int64_t* scratch,
+                                     int64_t pair, int64_t pairs, bool report_range) {
+    const int per = (a.batch + kThreads - 1) / kThreads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, a.batch), b1 = min(b0 + per, a.batch);
+    int64_t sum = 0;
+    Request r;
+    for (int b = b0; b < b1; ++b) {
+        r.load(a, b);
+        sum += r.units();
+        if (report_range && r.n > 0 && r.kv < r.len + r.n) report(a.status, PKM_ERR_OUT_OF_RANGE);
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = sum;
+#pragma unroll
+    for (int sh = 1; sh < 32; sh <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, sh);
+        if (lane >= sh) incl += o;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    pairs = min(pairs, total);  // no pair without a tile lies between two that share an item
+    const int64_t u = pair < pairs ? total * pair / pairs : total;
+    int64_t at = before + incl - sum;
+    if (threadIdx.x == 0) bars->units = total;
+    if (u < total && at <= u && u < at + sum)
+        for (int b = b0; b < b1; ++b) {
+            r.load(a, b);
+            if (u < at + r.units()) {
+                bars->start_request = b;
+                bars->start_unit = at;
+                break;
+            }
+            at += r.units();
+        }
 }
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-    const uint32_t e = (c >> 3) & 15u, m = c & 7u;
-    float v = e == 0 ? static_cast<float>(m) * 0x1p-9f
-                     : (1.0f + static_cast<float>(m) * 0.125f) * exp2f(static_cast<float>(e) - 7.0f);
-    if (e == 15 && m == 7) v = __int_as_float(0x7fffffff);
-    return (c & 128u) ? -v : v;
+// Page id of position pos of request b: -1 (loads as zeros) at or past kv and for ids that the
+// cache does not have, which are reported.
+__device__ __forceinline__ int32_t page_of(const TreeAttentionArgs& a, int b, int64_t pos,
+                                           int64_t kv) {
+    if (pos >= kv) return -1;
+    const uint32_t page =
+        __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + pos / a.page_size);
+    if (page >= static_cast<uint32_t>(a.num_pages)) {
+        report(a.status, PKM_ERR_OUT_OF_RANGE);
+        return -1;
+    }
+    return static_cast<int32_t>(page);
 }
 
-__global__ void __launch_bounds__(kThreads) tree_attention_kernel(const TreeAttentionArgs a) {
+// Offset of a position's slot in the layer, -1 where page_of has none.
+__device__ __forceinline__ int64_t slot_of(const TreeAttentionArgs& a, int b, int64_t pos,
+                                           int64_t kv) {
+    const int32_t page = page_of(a, b, pos, kv);
+    if (page < 0) return -1;
+    return page * a.page_stride + (pos % a.page_size) * a.slot_stride;
+}
+
+// Infinities and NaN of a packed pair of bf16 become zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+    return w;
+}
+
+__device__ __forceinline__ uint4 finite8(uint4 v) {
+    return make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+}
+
+// Four e4m3 codes times a scale, each product rounded to fp32 and then to bf16.
+__device__ __forceinline__ uint2 dequant4(uint32_t codes, float scale) {
+    uint32_t h0, h1;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(h0), "=r"(h1)
+        : "r"(codes));
+    const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&h0));
+    const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&h1));
+    float a, b, c, d;
+    mul2(a, b, f0.x, f0.y, scale, scale);
+    mul2(c, d, f1.x, f1.y, scale, scale);
+    return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+
+// Eight columns c .. c+7 of a latent row as bf16; zeros past the row's columns.
+template <Source SRC>
+__device__ __forceinline__ uint4 row_piece(const TreeAttentionArgs& a, int64_t slot, int c) {
+    if (slot < 0 || c >= a.cols) return make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (SRC == kCodes) {
+        const uint8_t* p = a.qcache_layer + slot;
+        const int R = a.kv_lora_rank;
+        if (c >= R) return ld_nc_v4(p + R + 2 * (c - R));
+        const uint2 q = *reinterpret_cast<const uint2*>(p + c);
+        const float scale =
+            *reinterpret_cast<const float*>(p + R + 2 * (a.cols - R) + 4 * (c / 128));
+        const uint2 lo = dequant4(q.x, scale), hi = dequant4(q.y, scale);
+        return make_uint4(lo.x, lo.y, hi.x, hi.y);
+    } else {
+        return ld_nc_v4(a.cache_layer + slot + c);
+    }
+}
+
+// Bits k of the 64 keys c0 .. c0+63 that token i of the request may attend.
+__device__ __forceinline__ uint64_t attended(const TreeAttentionArgs& a, const Request& r,
+                                             int32_t i, int64_t c0) {
+    const auto low = [](int64_t n) -> uint64_t {
+        return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+    };
+    const uint64_t exist = low(r.kv - c0);
+    if (a.mask == nullptr) return exist & low(r.len + i + 1 - c0);
+    const int64_t j0 = c0 - r.len;  // draft of the first key
+    uint64_t bits = low(-j0);
+    if (j0 > -64) {
+        const uint32_t* row = a.mask + (r.first + i) * a.mask_words;
+        const int64_t w0 = j0 > 0 ? j0 >> 5 : 0;
+        const auto word = [&](int64_t w) -> uint64_t {
+            return w < a.mask_words ? __ldg(row + w) : 0u;
+        };
+        const uint64_t lo = word(w0) | (word(w0 + 1) << 32);
+        const int sh = static_cast<int>(j0 > 0 ? j0 & 31 : 0);
+        uint64_t m = lo >> sh;
+        if (sh > 0) m |= word(w0 + 2) << (64 - sh);
+        bits |= j0 >= 0 ? m : m << -j0;
+    }
+    return exist & bits;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <Source SRC>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_c, const TreeAttentionArgs a,
+                          const TreeWorkspace ws, const int box) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* sQ = smem + kOffQ;
+    uint8_t* sK = smem + kOffK;
+    uint8_t* sV = smem + kOffV;
+    uint8_t* sP = smem + kOffP;
+    float* s_max = reinterpret_cast<float*>(smem + kOffMax);
+    float* s_sum = reinterpret_cast<float*>(smem + kOffSum);
+    Bars* bars = reinterpret_cast<Bars*>(smem + kOffBars);
+
+    const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (row >= static_cast<int64_t>(a.total_rows) * a.num_heads) return;
-    const int64_t r = row / a.num_heads;
-    const uint32_t* iro = a.row_offsets;
-    const int64_t end = min(static_cast<int64_t>(__ldg(iro + a.batch)), static_cast<int64_t>(a.total_rows));
-    if (r >= end || r < static_cast<int64_t>(__ldg(iro))) return;
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (static_cast<int64_t>(__ldg(iro + mid)) <= r) lo = mid;
-        else hi = mid;
-    }
-    const int b = lo;
-    const int64_t first = __ldg(iro + b);
-    const int64_t n = min(static_cast<int64_t>(__ldg(iro + b + 1)), end) - first;
-    const int64_t i = r - first;
-    const int64_t len = __ldg(a.cache_lengths + b);
-    int64_t kv = len + n;
-    const int64_t held = static_cast<int64_t>(a.max_pages) * a.page_size;
-    if (kv > held) {
-        kv = held;
-        if (lane == 0) report(a.status, PKM_ERR_OUT_OF_RANGE);
-    }
-    const int cols = a.cols, rank = a.kv_lora_rank;
-    float q[kPieces][8], o[kPieces][8] = {};
-    for (int p = 0; p < kPieces; ++p) {
-        const int c = (lane + 32 * p) * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c < cols) v = *reinterpret_cast<const uint4*>(a.q + row * cols + c);
-        unpack8(v, q[p]);
-    }
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t t = 0; t < kv; ++t) {
-        if (t >= len) {
-            const int64_t j = t - len;
-            bool seen = j <= i;
-            if (a.mask != nullptr)
-                seen = j < 32 * static_cast<int64_t>(a.mask_words) &&
-                       ((__ldg(a.mask + r * a.mask_words + j / 32) >> (j % 32)) & 1u);
-            if (!seen) continue;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int64_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int R = a.kv_lora_rank;
+    const int kblocks = (a.cols + 63) / 64;
+    const int vblocks = (R + 127) / 128;        // value blocks of each CTA
+    const int vgroups = (vblocks + 1) / 2;      // groups of two blocks, one MMA width each
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBlocks; ++i) {
+            mbar_init(&bars->k_full[i], SRC == kTma ? 1 : 2);
+            mbar_init(&bars->k_empty[i], 1);
         }
-        const uint32_t page = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + t / a.page_size);
-        if (page >= static_cast<uint32_t>(a.num_pages)) {
-            if (lane == 0) report(a.status, PKM_ERR_OUT_OF_RANGE);
-            continue;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->v_full[i], 2);
+            mbar_init(&bars->v_empty[i], 1);
+            mbar_init(&bars->s_full[i], 1);
         }
-        const int64_t off = page * a.page_stride + (t % a.page_size) * a.slot_stride;
-        float k[kPieces][8], s = 0.0f;
-        for (int p = 0; p < kPieces; ++p) {
-            const int c = (lane + 32 * p) * 8;
-            for (int e = 0; e < 8; ++e) k[p][e] = 0.0f;
-            if (c < cols) {
-                if (a.qcache_layer == nullptr) {
-                    unpack8(*reinterpret_cast<const uint4*>(a.cache_layer + off + c), k[p]);
-                } else if (c >= rank) {
-                    unpack8(*reinterpret_cast<const uint4*>(a.qcache_layer + off + rank + 2 * (c - rank)), k[p]);
-                } else {
-                    const float scale = *reinterpret_cast<const float*>(
-                        a.qcache_layer + off + rank + 2 * (cols - rank) + 4 * (c / 128));
-                    for (int e = 0; e < 8; ++e)
-                        k[p][e] = __bfloat162float(__float2bfloat16_rn(
-                            e4m3_value(a.qcache_layer[off + c + e]) * scale));
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_empty, 1);
+        mbar_init(&bars->p_full, 2 * kSoftWarps);
+        mbar_init(&bars->o_full, 1);
+        mbar_init(&bars->o_empty, 2 * kSoftWarps);
+        mbar_init(&bars->mma_done, 1);
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc_pair(&bars->tmem_base, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    plan(a, bars, reinterpret_cast<int64_t*>(s_max), pair, pairs, blockIdx.x == 0);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    const WaitCtl wc{&bars->abort_flag, a.status, a.timeout_ns};
+    const int64_t sharing = min(pairs, bars->units);  // pairs with a share
+    Walk w(a, bars, pair, sharing);
+
+    if (warp < kSoftWarps) {
+        // ---------------- softmax and epilogue: row = lane of the CTA's 64 ----------------
+        const int half = warp >> 1;                   // which 64 keys, which half of O's columns
+        const int row = (warp & 1) * 32 + lane;       // of this CTA's 64
+        const float scale2 = a.scale * kLog2e;
+        const uint32_t tlane = static_cast<uint32_t>(warp * 32) << 16;
+        const uint32_t p_row = smem_u32(sP) + half * kBlockBytes + row * 128;
+        const uint32_t stage = smem_u32(sP) + warp * 4096;
+        const uint32_t p_full = mapa_shared(smem_u32(&bars->p_full), 0);
+        const uint32_t o_empty = mapa_shared(smem_u32(&bars->o_empty), 0);
+        uint32_t g = 0;
+        int32_t left_rows = 0, left_parts = 0;
+        int64_t left_first = 0;
+        bool ok = true;
+        while (ok && w.next(a)) {
+            const int64_t rows_all = static_cast<int64_t>(w.r.n) * a.num_heads;
+            const int64_t rr = w.item * 128 + rank * 64 + row;
+            const int32_t token =
+                static_cast<int32_t>(min(rr / a.num_heads, static_cast<int64_t>(w.r.n - 1)));
+            float m = -INFINITY, l = 0.0f;
+            for (int64_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[g & 1], (g >> 1) & 1, wc))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t x0[32], x1[32];
+                tmem_ld_x32(tmem + tlane + kScoreCol + (g & 1) * 64, x0);
+                tmem_ld_x32(tmem + tlane + kScoreCol + (g & 1) * 64 + 32, x1);
+                uint32_t lo = ~0u, hi = ~0u;
+                const bool partial = w.partial(kt);
+                if (partial) {
+                    const uint64_t bits = attended(a, w.r, token, kt * kKeys + half * 64);
+                    lo = static_cast<uint32_t>(bits);
+                    hi = static_cast<uint32_t>(bits >> 32);
+                }
+                tmem_ld_wait();
+                float s[64];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    mul2(s[2 * k], s[2 * k + 1], __uint_as_float(x0[2 * k]),
+                         __uint_as_float(x0[2 * k + 1]), scale2, scale2);
+                    mul2(s[32 + 2 * k], s[33 + 2 * k], __uint_as_float(x1[2 * k]),
+                         __uint_as_float(x1[2 * k + 1]), scale2, scale2);
+                }
+                if (partial) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        s[k] = (lo >> k) & 1u ? s[k] : -INFINITY;
+                        s[32 + k] = (hi >> k) & 1u ? s[32 + k] : -INFINITY;
+                    }
+                }
+                float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+#pragma unroll
+                for (int k = 4; k < 64; k += 4) {
+                    t0 = fmaxf(t0, s[k]);
+                    t1 = fmaxf(t1, s[k + 1]);
+                    t2 = fmaxf(t2, s[k + 2]);
+                    t3 = fmaxf(t3, s[k + 3]);
+                }
+                float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+                // the row's other 64 keys are with lane row + 64 (warp ^ 2)
+                float* mx = s_max + (g & 1) * 128;
+                mx[half * 64 + row] = top;
+                named_bar_sync(3 + (warp & 1), 64);
+                if (*wc.abort_flag) {
+                    ok = false;
+                    break;
+                }
+                top = fmaxf(top, mx[(half ^ 1) * 64 + row]);
+                const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+                const float m_new = move ? top : m;
+                const float back = move && m > -INFINITY ? exp2_approx(m - m_new) : move ? 0.0f : 1.0f;
+                m = m_new;
+                const float ref = m == -INFINITY ? 0.0f : m;
+                float sum0 = 0.0f, sum1 = 0.0f;
+                uint32_t p[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float e0 = exp2_approx(s[2 * k] - ref);
+                    const float e1 = exp2_approx(s[2 * k + 1] - ref);
+                    sum0 += e0;
+                    sum1 += e1;
+                    p[k] = pack_bf16x2(e0, e1);
+                }
+                l = l * back + (sum0 + sum1);
+                // the previous tile's weights are used up, and O holds it
+                if (g > 0 &&
+                    !__all_sync(0xffffffffu, mbar_wait(&bars->o_full, (g - 1) & 1, wc))) {
+                    ok = false;
+                    break;
+                }
+                if (kt > w.kt0 && __any_sync(0xffffffffu, move)) {
+                    tc_fence_after();
+                    for (int v = 0; v < 2 * vblocks; ++v) {
+                        uint32_t o[32];
+                        tmem_ld_x32(tmem + tlane + v * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * back);
+                        tmem_st_x32(tmem + tlane + v * 32, o);
+                    }
+                    tmem_st_wait();
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    st_shared_v4(p_row + ((j ^ (row & 7)) << 4), p[4 * j], p[4 * j + 1],
+                                 p[4 * j + 2], p[4 * j + 3]);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(p_full);
+            }
+            if (!ok) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_full, (g - 1) & 1, wc))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            s_sum[half * 64 + row] = l;
+            named_bar_sync(3 + (warp & 1), 64);
+            if (*wc.abort_flag) {
+                ok = false;
+                break;
+            }
+            l += s_sum[(half ^ 1) * 64 + row];
+            const bool whole = w.kt0 == 0 && w.kt1 == w.r.tiles;
+            const uint32_t valid = __ballot_sync(0xffffffffu, rr < rows_all);
+            const int64_t row0 = w.r.first * a.num_heads + rr - lane;  // of this warp's 32
+            if (whole) {
+                const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+                for (int v = 0; v < vblocks; ++v) {
+                    const int col = (half * vblocks + v) * 64;
+                    if (col >= R) break;
+                    uint32_t x0[32], x1[32], p[32];
+                    tmem_ld_x32(tmem + tlane + v * 64, x0);
+                    tmem_ld_x32(tmem + tlane + v * 64 + 32, x1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        p[k] = pack_bf16x2(__uint_as_float(x0[2 * k]) * inv,
+                                           __uint_as_float(x0[2 * k + 1]) * inv);
+                        p[16 + k] = pack_bf16x2(__uint_as_float(x1[2 * k]) * inv,
+                                                __uint_as_float(x1[2 * k + 1]) * inv);
+                    }
+                    warp_store_rows_32x64(stage, p, a.out + row0 * R + col, R, valid, lane);
+                }
+                if (half == 0 && rr < rows_all && a.lse != nullptr)
+                    a.lse[row0 + lane] = l != 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+            } else {
+                const int64_t slot = 2 * pair + (w.kt0 > 0 ? 0 : 1);
+                const int64_t at = slot * ws.rows + rank * 64 + (warp & 1) * 32;
+                float* part = reinterpret_cast<float*>(a.workspace + ws.parts) + at * R;
+                for (int v = 0; v < 2 * vblocks; ++v) {
+                    const int col = half * vblocks * 64 + v * 32;
+                    if (col >= R) break;
+                    uint32_t x[32];
+                    tmem_ld_x32(tmem + tlane + v * 32, x);
+                    tmem_ld_wait();
+                    warp_store_rows_32x64(stage, x, reinterpret_cast<uint16_t*>(part + col),
+                                          2 * static_cast<int64_t>(R), valid, lane);
+                }
+                if (half == 0 && rr < rows_all)
+                    reinterpret_cast<float2*>(a.workspace + ws.stats)[at + lane] = make_float2(m, l);
+                if (w.kt0 == 0) {
+                    const int64_t end = w.base + (w.item + 1) * w.r.tiles;
+                    left_first = w.r.first * a.num_heads + w.item * 128;
+                    left_rows = static_cast<int32_t>(min(rows_all - w.item * 128,
+                                                         static_cast<int64_t>(128)));
+                    left_parts = static_cast<int32_t>((end * sharing - 1) / bars->units - pair) + 1;
                 }
             }
-            for (int e = 0; e < 8; ++e) s = fmaf(q[p][e], k[p][e], s);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(o_empty);
         }
-        for (int sh = 16; sh >= 1; sh >>= 1) s += __shfl_xor_sync(0xffffffffu, s, sh);
-        s *= a.scale;
-        const float m_new = fmaxf(m, s);
-        const float f = m == -INFINITY ? 0.0f : expf(m - m_new), w = expf(s - m_new);
-        l = l * f + w;
-        m = m_new;
-        for (int p = 0; p < kPieces; ++p)
-            for (int e = 0; e < 8; ++e) o[p][e] = o[p][e] * f + w * k[p][e];
+        if (!ok) named_bar_arrive(3 + (warp & 1), 64);  // releases the partner warp
+        if (leader && threadIdx.x == 0) {
+            TreeItem* items = reinterpret_cast<TreeItem*>(a.workspace + ws.items);
+            items[pair] = TreeItem{left_first, ok ? left_rows : 0, left_parts};
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------- MMA issuer (even CTA) ----------------
+        if (leader && lane == 0) {
+            const uint32_t id_s = idesc_bf16(128, kKeys, false, false);
+            const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
+            const uint64_t p_desc = sdesc_sw128(smem_u32(sP), 16, 1024);
+            const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kValueBytes, 1024);
+            uint32_t g = 0, item = 0;
+            bool first = false;   // the tile whose values come next starts its item
+            // O (+)= P V of tile g - 1, the last whose scores were issued
+            const auto values = [&]() -> bool {
+                const uint32_t ph = (g - 1) & 1;
+                if (!mbar_wait_cluster(&bars->p_full, ph, wc)) return false;
+                if (first && item > 1 && !mbar_wait(&bars->o_empty, item & 1, wc)) return false;
+                tc_fence_after();
+                for (int vg = 0; vg < vgroups; ++vg) {
+                    if (!mbar_wait_cluster(&bars->v_full[vg], ph, wc)) return false;
+                    tc_fence_after();
+                    const uint32_t id = idesc_bf16(128, 2 * vg + 1 < vblocks ? 256 : 128, false, true);
+                    const uint64_t vd = desc_add_bytes(v_desc, vg * 2 * kValueBytes);
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 32 bytes of P, 2048 of V
+                        mma_bf16_pair(tmem + vg * 128,
+                                      desc_add_bytes(p_desc, (k / 4) * kBlockBytes + (k % 4) * 32),
+                                      vd + 128 * k, id, !first || k > 0 ? 1u : 0u);
+                    mma_commit_pair(&bars->v_empty[vg], 3);
+                }
+                mma_commit_pair(&bars->o_full, 3);
+                first = false;
+                return true;
+            };
+            bool ok = true;
+            while (ok && w.next(a)) {
+                if (g > 0 && !values()) break;
+                ++item;
+                if (!mbar_wait(&bars->q_full, (item - 1) & 1, wc)) break;
+                for (int64_t kt = w.kt0; kt < w.kt1; ++kt) {
+                    const uint32_t d = tmem + kScoreCol + (g & 1) * 64;
+                    for (int kb = 0; kb < kblocks; ++kb) {
+                        ok = SRC == kTma ? mbar_wait(&bars->k_full[kb], g & 1, wc)
+                                         : mbar_wait_cluster(&bars->k_full[kb], g & 1, wc);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t qd = desc_add_bytes(q_desc, kb * kBlockBytes);
+                        const uint64_t kd = desc_add_bytes(k_desc, kb * kBlockBytes);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_pair(d, qd + 2 * k, kd + 2 * k, id_s, (kb | k) != 0 ? 1u : 0u);
+                        mma_commit_pair(&bars->k_empty[kb], 3);
+                    }
+                    if (!ok) break;
+                    mma_commit_pair(&bars->s_full[g & 1], 3);
+                    if (kt + 1 == w.kt1) mma_commit_pair(&bars->q_empty, 3);
+                    if (kt > w.kt0 && !values()) {
+                        ok = false;
+                        break;
+                    }
+                    if (kt == w.kt0) first = true;
+                    ++g;
+                }
+            }
+            if (ok && g > 0) values();
+            mma_commit_pair(&bars->mma_done, 1);
+            mbar_wait(&bars->mma_done, 0, wc, false);
+        }
+    } else if (warp < kValueWarp) {
+        // ---------------- keys: this CTA's 64 of each tile, all columns ----------------
+        const uint32_t k_full = mapa_shared(smem_u32(&bars->k_full[0]), 0);
+        uint32_t g = 0;
+        bool ok = true;
+        if constexpr (SRC == kTma) {
+            const int boxes = 64 / box;
+            uint32_t issued[kBlocks] = {};
+            while (warp == kKeyWarp && ok && w.next(a)) {
+                for (int64_t kt = w.kt0; ok && kt < w.kt1; ++kt, ++g) {
+                    const int64_t pos = kt * kKeys + rank * 64 + lane * box;
+                    int32_t page = -1, slot = 0;
+                    if (lane < boxes) {
+                        page = page_of(a, w.b, pos, w.r.kv);
+                        slot = static_cast<int32_t>(pos % a.page_size);
+                    }
+                    for (int kb = 0; kb < kblocks; ++kb) {
+                        const int go = lane == 0 ? mbar_wait(&bars->k_empty[kb], (g & 1) ^ 1, wc) : 1;
+                        ok = __shfl_sync(0xffffffffu, go, 0);
+                        if (!ok) break;
+                        if (leader && lane == 0)
+                            mbar_arrive_expect_tx(&bars->k_full[kb], 2 * kBlockBytes);
+                        if (lane < boxes)
+                            tma_load_3d_pair(sK + kb * kBlockBytes + lane * box * 128, &tm_c,
+                                             k_full + kb * 8, kb * 64, slot, page);
+                        issued[kb] = g + 1;
+                    }
+                }
+            }
+            if (!ok && lane == 0) {  // let the loads in flight land before the CTA retires
+                if (leader)
+                    for (int kb = 0; kb < kBlocks; ++kb)
+                        if (issued[kb] > 0)
+                            mbar_wait(&bars->k_full[kb], (issued[kb] - 1) & 1, wc, false);
+                if (!leader) spin_ns(50000);
+            }
+        } else {
+            const int t = threadIdx.x - kKeyWarp * 32, key = t >> 1, side = t & 1;
+            while (ok && w.next(a)) {
+                for (int64_t kt = w.kt0; ok && kt < w.kt1; ++kt, ++g) {
+                    const int64_t slot =
+                        slot_of(a, w.b, kt * kKeys + rank * 64 + key, w.r.kv);
+                    for (int kb = 0; kb < kblocks; ++kb) {
+                        if (t == 0) bars->k_go = mbar_wait(&bars->k_empty[kb], (g & 1) ^ 1, wc);
+                        named_bar_sync(2, 128);
+                        ok = bars->k_go;
+                        if (!ok) break;
+                        uint4 x[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            x[j] = row_piece<SRC>(a, slot, kb * 64 + side * 32 + j * 8);
+                        const uint32_t dst = smem_u32(sK + kb * kBlockBytes) + key * 128;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            st_shared_v4(dst + (((side * 4 + j) ^ (key & 7)) << 4), x[j].x, x[j].y,
+                                         x[j].z, x[j].w);
+                        fence_proxy_async_smem();
+                        named_bar_sync(2, 128);
+                        if (t == 0) mbar_arrive_cluster(k_full + kb * 8);
+                    }
+                }
+            }
+        }
+    } else if (warp < kQueryWarp) {
+        // ---------------- values: all 128 keys of each tile, this CTA's columns ----------------
+        const uint32_t v_full = mapa_shared(smem_u32(&bars->v_full[0]), 0);
+        const int t = threadIdx.x - kValueWarp * 32;
+        const int boxes = SRC == kTma ? kKeys / box : 1;
+        uint32_t g = 0, issued[2] = {};
+        bool ok = true;
+        while (ok && w.next(a)) {
+            for (int64_t kt = w.kt0; ok && kt < w.kt1; ++kt, ++g) {
+                if (SRC == kTma && !w.partial(kt)) {
+                    if (warp != kValueWarp) continue;
+                    const int blk = lane / boxes, i = lane % boxes;
+                    const int64_t pos = kt * kKeys + i * box;
+                    int32_t page = -1, slot = 0;
+                    if (blk < 2) {
+                        page = page_of(a, w.b, pos, w.r.kv);
+                        slot = static_cast<int32_t>(pos % a.page_size);
+                    }
+                    for (int vg = 0; vg < vgroups; ++vg) {
+                        const int go = lane == 0 ? mbar_wait(&bars->v_empty[vg], (g & 1) ^ 1, wc) : 1;
+                        ok = __shfl_sync(0xffffffffu, go, 0);
+                        if (!ok) break;
+                        const int blocks = min(2, vblocks - 2 * vg);
+                        if (lane == 0) {
+                            if (leader)
+                                mbar_arrive_expect_tx(&bars->v_full[vg], 2 * blocks * kValueBytes);
+                            else
+                                mbar_arrive_remote(v_full + vg * 8);
+                        }
+                        if (blk < blocks) {
+                            const int v = 2 * vg + blk;
+                            tma_load_3d_pair(sV + v * kValueBytes + i * box * 128, &tm_c,
+                                             v_full + vg * 8,
+                                             (static_cast<int>(rank) * vblocks + v) * 64, slot, page);
+                        }
+                        issued[vg] = g + 1;
+                    }
+                    if (!ok) {  // releases the other value warps from a later tile
+                        if (lane == 0) bars->v_go = 0;
+                        __syncwarp();
+                        named_bar_arrive(1, 128);
+                    }
+                } else {
+                    // Rows brought by loads: quantised ones, pages that no box divides, and
+                    // tiles with drafts, where a row that some query does not attend must not
+                    // turn its zero weight into NaN: infinities and NaN become zero.  (A query
+                    // that does attend such a draft has NaN or infinity among its scores.)
+                    const int64_t pos = kt * kKeys + t;
+                    const int64_t slot = slot_of(a, w.b, pos, w.r.kv);
+                    const bool clean = pos >= w.r.len;
+                    for (int vg = 0; vg < vgroups; ++vg) {
+                        if (t == 0) bars->v_go = mbar_wait(&bars->v_empty[vg], (g & 1) ^ 1, wc);
+                        named_bar_sync(1, 128);
+                        ok = bars->v_go;
+                        if (!ok) break;
+                        for (int v = 2 * vg; v < min(2 * vg + 2, vblocks); ++v) {
+                            const int col = (static_cast<int>(rank) * vblocks + v) * 64;
+                            uint4 x[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                x[j] = row_piece<SRC>(a, slot, col + j * 8);
+                            const uint32_t dst = smem_u32(sV + v * kValueBytes) + t * 128;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                if (clean) x[j] = finite8(x[j]);
+                                st_shared_v4(dst + ((j ^ (t & 7)) << 4), x[j].x, x[j].y, x[j].z,
+                                             x[j].w);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        named_bar_sync(1, 128);
+                        if (t == 0) mbar_arrive_cluster(v_full + vg * 8);
+                    }
+                }
+            }
+        }
+        if (SRC == kTma && !ok && t == 0) {
+            if (leader)
+                for (int vg = 0; vg < 2; ++vg)
+                    if (issued[vg] > 0)
+                        mbar_wait(&bars->v_full[vg], (issued[vg] - 1) & 1, wc, false);
+            if (!leader) spin_ns(50000);
+        }
+    } else {
+        // ---------------- queries: this CTA's 64 rows of each item ----------------
+        const uint32_t q_full = mapa_shared(smem_u32(&bars->q_full), 0);
+        uint32_t item = 0;
+        bool ok = true;
+        while (ok && w.next(a)) {
+            const int go = lane == 0 ? mbar_wait(&bars->q_empty, (item & 1) ^ 1, wc) : 1;
+            ok = __shfl_sync(0xffffffffu, go, 0);
+            if (!ok) break;
+            const int64_t row = w.r.first * a.num_heads + w.item * 128 + rank * 64;
+            if (leader && lane == 0)
+                mbar_arrive_expect_tx(&bars->q_full, 2 * kblocks * kBlockBytes);
+            if (lane < kblocks)
+                tma_load_2d_pair(sQ + lane * kBlockBytes, &tm_q, q_full, lane * 64,
+                                 static_cast<int32_t>(row));
+            ++item;
+        }
+        if (!ok && lane == 0) {
+            if (leader && item > 0) mbar_wait(&bars->q_full, (item - 1) & 1, wc, false);
+            if (!leader) spin_ns(50000);
+        }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    for (int p = 0; p < kPieces; ++p) {
-        const int c = (lane + 32 * p) * 8;
-        if (c >= rank) continue;
-        st_v4(a.out + row * rank + c,
-              make_uint4(pack_bf16x2(o[p][0] * inv, o[p][1] * inv), pack_bf16x2(o[p][2] * inv, o[p][3] * inv),
-                         pack_bf16x2(o[p][4] * inv, o[p][5] * inv), pack_bf16x2(o[p][6] * inv, o[p][7] * inv)));
+
+    griddep_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+constexpr int kJoinThreads = 256;
+
+// Joins the parts of the items that several pairs share: with M the largest of the parts'
+// maxima, out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same
+// order.  A block takes rows one after the other; groups of R / 4 threads take a share of
+// the parts each, 16 bytes a thread, and meet in shared memory.
+__global__ void __launch_bounds__(kJoinThreads)
+    tree_join_kernel(const TreeAttentionArgs a, const TreeWorkspace ws, const int pairs) {
+    __shared__ TreeItem items[kTreeMaxPairs];
+    __shared__ float weight[kTreeMaxPairs];
+    __shared__ float4 sums[kJoinThreads];
+    griddep_wait();
+    const TreeItem* held = reinterpret_cast<const TreeItem*>(a.workspace + ws.items);
+    for (int p = threadIdx.x; p < pairs; p += kJoinThreads) items[p] = held[p];
+    __syncthreads();
+    const int R = a.kv_lora_rank, quads = R / 4;
+    const int groups = kJoinThreads / quads;
+    const int quad = threadIdx.x % quads, grp = threadIdx.x / quads;
+    const float2* stats = reinterpret_cast<const float2*>(a.workspace + ws.stats);
+    const float4* parts = reinterpret_cast<const float4*>(a.workspace + ws.parts);
+    int before = 0;
+    for (int p = 0; p < pairs; ++p) {
+        const TreeItem it = items[p];
+        // rows are dealt to the blocks across all items
+        int row = (static_cast<int>(blockIdx.x) - before) % static_cast<int>(gridDim.x);
+        if (row < 0) row += gridDim.x;
+        before = (before + it.rows) % static_cast<int>(gridDim.x);
+        for (; row < it.rows; row += gridDim.x) {
+            // part k of the item: the pair's second slot, then the first slots behind it
+            const auto slot = [&](int k) -> int64_t {
+                return (static_cast<int64_t>(2) * (p + k) + (k == 0 ? 1 : 0)) * ws.rows + row;
+            };
+            if (threadIdx.x < 32) {
+                float top = -INFINITY;
+                for (int k = threadIdx.x; k < it.parts; k += 32) top = fmaxf(top, stats[slot(k)].x);
+#pragma unroll
+                for (int sh = 16; sh >= 1; sh >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+                float total = 0.0f;
+                for (int k = threadIdx.x; k < it.parts; k += 32) {
+                    const float2 s = stats[slot(k)];
+                    const float f = s.x == -INFINITY ? 0.0f : exp2f(s.x - top);
+                    weight[k] = f;
+                    total += f * s.y;
+                }
+#pragma unroll
+                for (int sh = 16; sh >= 1; sh >>= 1)
+                    total += __shfl_xor_sync(0xffffffffu, total, sh);
+                __syncwarp();
+                const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+                for (int k = threadIdx.x; k < it.parts; k += 32) weight[k] *= inv;
+                if (threadIdx.x == 0 && a.lse != nullptr)
+                    a.lse[it.first + row] = total != 0.0f ? top * kLn2 + logf(total) : -INFINITY;
+            }
+            __syncthreads();
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (grp < groups) {
+#pragma unroll 4
+                for (int k = grp; k < it.parts; k += groups) {
+                    const float f = weight[k];
+                    const float4 v = parts[slot(k) * quads + quad];
+                    o.x = fmaf(f, v.x, o.x);
+                    o.y = fmaf(f, v.y, o.y);
+                    o.z = fmaf(f, v.z, o.z);
+                    o.w = fmaf(f, v.w, o.w);
+                }
+            }
+            sums[threadIdx.x] = o;
+            __syncthreads();
+            if (grp == 0) {
+                for (int i = 1; i < groups; ++i) {
+                    const float4 v = sums[i * quads + quad];
+                    o.x += v.x;
+                    o.y += v.y;
+                    o.z += v.z;
+                    o.w += v.w;
+                }
+                *reinterpret_cast<uint2*>(a.out + (it.first + row) * R + quad * 4) =
+                    make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+            }
+            __syncthreads();
+        }
     }
-    if (lane == 0 && a.lse != nullptr) a.lse[row] = l > 0.0f ? m + logf(l) : -INFINITY;
+}
+
+template <Source SRC>
+cudaError_t launch_source(const CUtensorMap& tm_q, const CUtensorMap& tm_c,
+                          const TreeAttentionArgs& args, const TreeWorkspace& ws, int box,
+                          int pairs, cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<SRC>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kSmemBytes));
+    if (e != cudaSuccess) return e;
+    tree_attention_kernel<SRC><<<static_cast<unsigned>(2 * pairs), kThreads, kSmemBytes, stream>>>(
+        tm_q, tm_c, args, ws, box);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tree_attention(TreeAttentionArgs args, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    const int64_t rows = static_cast<int64_t>(args.total_rows) * args.num_heads;
-    tree_attention_kernel<<<static_cast<unsigned>((rows + 3) / 4), kThreads, 0, stream>>>(args);
-    return cudaGetLastError();
+cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_c,
+                                  TreeAttentionArgs args, int box, int num_sms,
+                                  cudaStream_t stream) {
+    const TreeWorkspace ws = tree_workspace(args.total_rows, args.num_heads, args.kv_lora_rank);
+    const int pairs = num_sms / 2 < kTreeMaxPairs ? num_sms / 2 : kTreeMaxPairs;
+    const cudaError_t e =
+        args.qcache_layer != nullptr
+            ? launch_source<kCodes>(tm_q, tm_c, args, ws, box, pairs, stream)
+        : box >= 8 ? launch_source<kTma>(tm_q, tm_c, args, ws, box, pairs, stream)
+                   : launch_source<kRows>(tm_q, tm_c, args, ws, box, pairs, stream);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(tree_join_kernel, static_cast<unsigned>(num_sms) * 2, kJoinThreads, 0,
+                            stream, args, ws, pairs);
 }
 
 }  // namespace pkm
