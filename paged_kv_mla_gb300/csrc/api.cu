@@ -941,21 +941,26 @@ pkm_status tree_attention(TreeAttentionArgs a, const void* q, const uint32_t* in
     if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
     // Query rows and, where the pages are divided by boxes of at least 8 slots (whole swizzle
     // atoms), the cache come by TMA; other pages and quantised rows are loaded row by row.
-    int box = 64;
-    while (box > 1 && a.page_size % box != 0) box /= 2;
-    alignas(64) CUtensorMap tm_q, tm_c;
+    // A box holds as many slots of one page as a tile's 64 keys or 128 values and the page
+    // size allow.
+    int vbox = 128;
+    while (vbox > 1 && a.page_size % vbox != 0) vbox /= 2;
+    const int box = vbox < 64 ? vbox : 64;
+    alignas(64) CUtensorMap tm_q, tm_c, tm_v;
     if (!encode_2d(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, a.cols,
                    static_cast<uint64_t>(total_rows) * num_heads,
                    static_cast<uint64_t>(a.cols) * 2, 64, 64))
         return encode_failed();
     if (a.qcache_layer != nullptr || box < 8)
-        tm_c = tm_q;
+        tm_c = tm_v = tm_q;
     else if (!encode_cache_pages(&tm_c, a.cache_layer, a.cols, a.page_size, a.num_pages,
-                                 a.slot_stride, a.page_stride, static_cast<uint32_t>(box)))
+                                 a.slot_stride, a.page_stride, static_cast<uint32_t>(box)) ||
+             !encode_cache_pages(&tm_v, a.cache_layer, a.cols, a.page_size, a.num_pages,
+                                 a.slot_stride, a.page_stride, static_cast<uint32_t>(vbox)))
         return encode_failed();
     if (const cudaError_t e = debug_validate(input_row_offsets, batch, dev_status, stream))
         return cuda_status(e);
-    return cuda_status(pkm::launch_tree_attention(tm_q, tm_c, a, box, sms,
+    return cuda_status(pkm::launch_tree_attention(tm_q, tm_c, tm_v, a, box, vbox, sms,
                                                   static_cast<cudaStream_t>(stream)));
 }
 

@@ -215,12 +215,9 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
     return ok != 0;
 }
 
-// mbar_wait with acquire at cluster scope, for a barrier whose completion publishes ordinary
-// (generic-proxy) shared-memory writes made by threads of the other CTA of the pair.  Same
-// limits and abort behaviour as mbar_wait.
-static __device__ __noinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                      const WaitCtl& w, bool obey_abort = true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+// Slow path of the cluster-scope waits (mbar_wait_spin with the cluster-scope test).
+__device__ __forceinline__ bool mbar_wait_cluster_spin(uint64_t* bar, uint32_t parity,
+                                                       const WaitCtl& w, bool obey_abort) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait_cluster(bar, parity)) return true;
@@ -233,6 +230,22 @@ static __device__ __noinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t pa
             }
         }
     }
+}
+
+// mbar_wait with acquire at cluster scope, for a barrier whose completion publishes ordinary
+// (generic-proxy) shared-memory writes made by threads of the other CTA of the pair.  Same
+// limits and abort behaviour as mbar_wait.
+static __device__ __noinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                      const WaitCtl& w, bool obey_abort = true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    return mbar_wait_cluster_spin(bar, parity, w, obey_abort);
+}
+
+// mbar_wait_cluster inlined (see mbar_wait_inl).
+__device__ __forceinline__ bool mbar_wait_cluster_inl(uint64_t* bar, uint32_t parity,
+                                                      const WaitCtl& w, bool obey_abort = true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    return mbar_wait_cluster_spin(bar, parity, w, obey_abort);
 }
 
 // All threads of every CTA in the cluster (release / acquire).
@@ -283,6 +296,14 @@ __device__ __forceinline__ void bulk_load_1d(void* dst, const void* src, uint32_
         ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes),
         "r"(smem_u32(bar))
         : "memory");
+}
+
+// Fetches `bytes` contiguous bytes (16-byte aligned, a multiple of 16) into L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                     reinterpret_cast<uint64_t>(src)),
+                 "r"(bytes)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -341,7 +362,7 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
         : "memory");
 }
 
-// The 2-D and 3-D pair loads without an L2 policy.
+// The 2-D pair load without an L2 policy.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map,
                                                  uint32_t bar_cluster, int32_t c0, int32_t c1) {
     asm volatile(
@@ -351,12 +372,15 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
-                                                 uint32_t bar_cluster, int32_t c0, int32_t c1,
-                                                 int32_t c2) {
+// The 3-D load issued by one elected lane of a warp whose lanes run together.
+__device__ __forceinline__ void tma_load_3d_pair_elect(void* dst, const CUtensorMap* map,
+                                                       uint32_t bar_cluster, int32_t c0,
+                                                       int32_t c1, int32_t c2) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
@@ -785,6 +809,32 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, u
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The same operations for a warp that runs its issue loop with all lanes together: one elected
+// lane issues.  Operands that the compiler sees to be the same in every lane stay in uniform
+// registers, where the instruction wants them; inside a branch taken by one lane each is moved
+// there again for every MMA, and the issue, not the tensor cores, bounds MMAs of N <= 128.
+__device__ __forceinline__ void mma_bf16_pair_elect(uint32_t d_tmem, uint64_t adesc,
+                                                    uint64_t bdesc, uint32_t idesc,
+                                                    uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar, uint16_t cta_mask) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+        ".multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "h"(cta_mask)
         : "memory");
 }
 

@@ -221,9 +221,9 @@ cudaError_t launch_kv_matmul_fp8(const CUtensorMap& tm_q, const CUtensorMap& tm_
 cudaError_t launch_cache_write(CacheWriteArgs args, int num_sms, cudaStream_t stream);
 cudaError_t launch_rope_heads(RopeHeadsArgs args, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_compact(CompactArgs args, cudaStream_t stream);
-cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_cache,
-                                  TreeAttentionArgs args, int box, int num_sms,
-                                  cudaStream_t stream);
+cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_keys,
+                                  const CUtensorMap& tm_values, TreeAttentionArgs args, int box,
+                                  int vbox, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_timeout_check(int32_t* status, uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t launch_validate_offsets(const uint32_t* offsets, int32_t batch, int32_t* status,
                                     cudaStream_t stream);

@@ -23,8 +23,8 @@
 // it did not start.  Such parts leave unnormalised fp32 sums, maxima and totals in the
 // workspace and a second kernel joins them; whole items are written directly.
 //
-// Roles of a CTA (14 warps): 0-3 softmax and epilogue, 4 MMA issue (even CTA), 5-8 keys,
-// 9-12 values, 13 queries.  Scores are kept in base 2; the running maximum moves only when
+// Roles of a CTA (16 warps): 0-3 softmax and epilogue, 4 MMA issue (even CTA), 5 queries, 6
+// a relay, 8-11 keys, 12-15 values; the softmax warps take over registers of warps 4-7.  Scores are kept in base 2; the running maximum moves only when
 // a row's new maximum exceeds it by 2^8, since any reference works as long as nothing
 // overflows, so the accumulator is hardly ever rescaled.
 #include <cuda_fp16.h>
@@ -35,11 +35,14 @@
 namespace pkm {
 namespace {
 
-constexpr int kSoftWarps = 4, kMmaWarp = 4, kKeyWarp = 5, kValueWarp = 9, kQueryWarp = 13;
-constexpr int kThreads = 14 * 32;
+constexpr int kSoftWarps = 4, kMmaWarp = 4, kQueryWarp = 5, kRelayWarp = 6, kKeyWarp = 8, kValueWarp = 12;
+constexpr int kThreads = 16 * 32;
+constexpr int kSoftRegs = 192, kIssueRegs = 64;  // with 128 for each loader: 4 x 128 in all
 constexpr int kKeys = 128;          // keys of a tile (64 loaded by each CTA as keys)
 constexpr int kBlocks = 9;          // 64-column blocks of a latent row
 constexpr int kBlockBytes = 64 * 128;
+constexpr int kGroup = 3;           // key blocks that are waited for and released together
+constexpr int kKeyGroups = kBlocks / kGroup;
 constexpr int kValueBlocks = 4;     // 64-column value blocks a CTA loads
 constexpr int kValueBytes = kKeys * 128;
 constexpr uint32_t kTmemCols = 512;
@@ -50,22 +53,23 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 enum Source { kTma, kRows, kCodes };  // pages by TMA, bf16 rows by loads, quantised rows
 
 struct Bars {
-    uint64_t k_full[kBlocks];   // even CTA: a 64-column block of both CTAs' keys is there
-    uint64_t k_empty[kBlocks];  // both: its MMAs are done
-    uint64_t v_full[2];         // even CTA: two value blocks of both CTAs are there
-    uint64_t v_empty[2];        // both
+    uint64_t k_full[kKeyGroups];   // even CTA: a group of blocks of both CTAs' keys is there
+    uint64_t k_empty[kKeyGroups];  // both: its MMAs are done
+    uint64_t v_full[kValueBlocks];  // even CTA: a value block of both CTAs is there
+    uint64_t v_empty[2];        // both: two value blocks are free
     uint64_t q_full, q_empty;   // the item's query rows
     uint64_t s_full[2];         // both: a score tile is complete
     uint64_t p_full;            // even CTA: both CTAs' weights are written
+    uint64_t p_ready;           // even CTA: the same, passed on within the CTA
     uint64_t o_full;            // both: the tile's weights are used up and O is current
     uint64_t o_empty;           // even CTA: both CTAs' epilogues have read O
     uint64_t mma_done;
     int64_t units;              // tiles of all items
-    int64_t start_unit;         // first tile of the request that holds this pair's first
-    int32_t start_request;
+    int64_t first_unit;         // this pair's share begins here
+    int32_t share;              // and has so many tiles
+    int32_t request, item, tile;  // its first tile
     uint32_t tmem_base;
     int abort_flag;
-    int k_go, v_go;             // the leading key / value warp's verdict on a wait
 };
 
 constexpr size_t kOffQ = 0;
@@ -78,69 +82,80 @@ constexpr size_t kOffBars = kOffSum + 128 * sizeof(float);
 constexpr size_t kSmemBytes = kOffBars + sizeof(Bars) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103a CTA");
 
+// a / b; the 64-bit division is a long routine, and the operands are hardly ever that large.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // One request as the schedule sees it.
 struct Request {
     int64_t first;   // its first row
     int32_t n;       // its new tokens
     int64_t len;     // cached tokens before them
     int64_t kv;      // positions that exist: len + n, cut at the page-table row
-    int64_t tiles;   // 128-key tiles
-    int64_t items;   // 128-row items
+    int32_t tiles;   // 128-key tiles
+    int32_t items;   // 128-row items
 
     __device__ __forceinline__ void load(const TreeAttentionArgs& a, int b) {
-        const int64_t lo = min(static_cast<int64_t>(__ldg(a.row_offsets + b)),
-                               static_cast<int64_t>(a.total_rows));
-        const int64_t hi = min(static_cast<int64_t>(__ldg(a.row_offsets + b + 1)),
-                               static_cast<int64_t>(a.total_rows));
+        const int64_t rows = a.total_rows;
+        const int64_t lo = min(static_cast<int64_t>(__ldg(a.row_offsets + b)), rows);
+        const int64_t hi = min(static_cast<int64_t>(__ldg(a.row_offsets + b + 1)), rows);
         first = lo;
         n = hi > lo ? static_cast<int32_t>(hi - lo) : 0;
         len = __ldg(a.cache_lengths + b);
         kv = min(len + n, static_cast<int64_t>(a.max_pages) * a.page_size);
-        tiles = (kv + kKeys - 1) / kKeys;
-        items = (static_cast<int64_t>(n) * a.num_heads + 127) / 128;
+        tiles = static_cast<int32_t>((kv + kKeys - 1) / kKeys);
+        items = static_cast<int32_t>((static_cast<int64_t>(n) * a.num_heads + 127) / 128);
     }
-    __device__ __forceinline__ int64_t units() const { return n > 0 ? tiles * items : 0; }
+    __device__ __forceinline__ int64_t units() const {
+        return n > 0 ? static_cast<int64_t>(tiles) * items : 0;
+    }
 };
 
-// A pair's share [u, end) of the tiles of all items, walked item by item.  After next()
-// returned true, the part is tiles [kt0, kt1) of item `item` of request r.
+// A pair's share of the tiles of all items, walked item by item.  After next() returned
+// true, the part is tiles [kt0, kt1) of item `item` of request r.
 struct Walk {
-    int64_t u, end, base;  // base: first unit of the request
-    int b, batch;
+    int64_t u;       // first unit of the part
+    int32_t left;    // tiles of the share behind the part
+    int b;
     Request r;
-    int64_t item, kt0, kt1;
+    int32_t item, kt0, kt1;
 
-    __device__ __forceinline__ Walk(const TreeAttentionArgs& a, const Bars* bars, int64_t pair,
-                                    int64_t pairs) {
-        u = min(pair, pairs) * bars->units / max(pairs, static_cast<int64_t>(1));
-        end = min(pair + 1, pairs) * bars->units / max(pairs, static_cast<int64_t>(1));
-        base = bars->start_unit;
-        b = bars->start_request;
-        batch = a.batch;
-        if (u < end) r.load(a, b);
+    __device__ __forceinline__ Walk(const TreeAttentionArgs& a, const Bars* bars) {
+        left = bars->share;
+        b = bars->request;
+        item = bars->item;
+        kt0 = kt1 = bars->tile;
+        u = bars->first_unit;
+        if (left > 0) r.load(a, b);
     }
     __device__ __forceinline__ bool next(const TreeAttentionArgs& a) {
-        if (u >= end) return false;
-        while (u >= base + r.units()) {  // u < units: a request further on holds it
-            base += r.units();
-            r.load(a, ++b);
-        }
-        item = (u - base) / r.tiles;
-        kt0 = (u - base) % r.tiles;
-        kt1 = min(r.tiles, kt0 + (end - u));
+        if (left <= 0) return false;
         u += kt1 - kt0;
+        if (kt1 == r.tiles) {
+            kt1 = 0;
+            if (++item == r.items) {
+                item = 0;
+                do r.load(a, ++b);  // tiles are left: a request further on has them
+                while (r.units() == 0);
+            }
+        }
+        kt0 = kt1;
+        kt1 = min(r.tiles, kt0 + left);
+        left -= kt1 - kt0;
         return true;
     }
-    // First tile whose keys are not all cached tokens that every row attends.
-    __device__ __forceinline__ bool partial(int64_t kt) const {
-        return (kt + 1) * kKeys > min(r.len, r.kv);
+    // The first tiles of an item hold cached tokens alone, which every row attends.
+    __device__ __forceinline__ int32_t cached_tiles() const {
+        return static_cast<int32_t>(min(r.len, r.kv) / kKeys);
     }
 };
 
-// Counts the tiles of all requests and finds the request of the pair's first one; every
-// thread sums a run of requests.  `scratch`: 16 int64 of shared memory.
+// Counts the tiles of all requests and cuts out the pair's share; every thread sums a run of
+// requests.  `scratch`: 16 int64 of shared memory.
 __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int64_t* scratch,
-                                     int64_t pair, int64_t pairs, bool report_range) {
+                                     int64_t pair, int64_t pairs) {
     const int per = (a.batch + kThreads - 1) / kThreads;
     const int b0 = min(static_cast<int>(threadIdx.x) * per, a.batch), b1 = min(b0 + per, a.batch);
     int64_t sum = 0;
@@ -148,7 +163,7 @@ __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int
     for (int b = b0; b < b1; ++b) {
         r.load(a, b);
         sum += r.units();
-        if (report_range && r.n > 0 && r.kv < r.len + r.n) report(a.status, PKM_ERR_OUT_OF_RANGE);
+        if (r.n > 0 && r.kv < r.len + r.n) report(a.status, PKM_ERR_OUT_OF_RANGE);
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t incl = sum;
@@ -158,49 +173,51 @@ __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int
         if (lane >= sh) incl += o;
     }
     if (lane == 31) scratch[warp] = incl;
+    if (threadIdx.x == 0) bars->share = 0;
     __syncthreads();
     int64_t before = 0, total = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    pairs = min(pairs, total);  // no pair without a tile lies between two that share an item
-    const int64_t u = pair < pairs ? total * pair / pairs : total;
-    int64_t at = before + incl - sum;
     if (threadIdx.x == 0) bars->units = total;
-    if (u < total && at <= u && u < at + sum)
+    pairs = min(pairs, total);  // no pair without a tile lies between two that share an item
+    if (pair >= pairs) return;
+    const int64_t u = quotient(total * pair, pairs);
+    int64_t at = before + incl - sum;
+    if (at <= u && u < at + sum)
         for (int b = b0; b < b1; ++b) {
             r.load(a, b);
             if (u < at + r.units()) {
-                bars->start_request = b;
-                bars->start_unit = at;
+                bars->first_unit = u;
+                bars->share = static_cast<int32_t>(quotient(total * (pair + 1), pairs) - u);
+                bars->request = b;
+                bars->item = static_cast<int32_t>(quotient(u - at, r.tiles));
+                bars->tile = static_cast<int32_t>((u - at) - static_cast<int64_t>(bars->item) * r.tiles);
                 break;
             }
             at += r.units();
         }
 }
 
-// Page id of position pos of request b: -1 (loads as zeros) at or past kv and for ids that the
-// cache does not have, which are reported.
-__device__ __forceinline__ int32_t page_of(const TreeAttentionArgs& a, int b, int64_t pos,
-                                           int64_t kv) {
-    if (pos >= kv) return -1;
-    const uint32_t page =
-        __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + pos / a.page_size);
-    if (page >= static_cast<uint32_t>(a.num_pages)) {
-        report(a.status, PKM_ERR_OUT_OF_RANGE);
-        return -1;
+// Page and slot of position pos of request b; page -1 (loads as zeros) at or past kv and for
+// ids that the cache does not have, which are reported.
+struct Place {
+    int32_t page, slot;
+    __device__ __forceinline__ Place(const TreeAttentionArgs& a, int b, int64_t pos, int64_t kv)
+        : page(-1), slot(0) {
+        if (pos >= kv) return;
+        const int64_t lp = quotient(pos, a.page_size);
+        slot = static_cast<int32_t>(pos - lp * a.page_size);
+        const uint32_t id = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
+        if (id < static_cast<uint32_t>(a.num_pages)) page = static_cast<int32_t>(id);
+        else report(a.status, PKM_ERR_OUT_OF_RANGE);
     }
-    return static_cast<int32_t>(page);
-}
-
-// Offset of a position's slot in the layer, -1 where page_of has none.
-__device__ __forceinline__ int64_t slot_of(const TreeAttentionArgs& a, int b, int64_t pos,
-                                           int64_t kv) {
-    const int32_t page = page_of(a, b, pos, kv);
-    if (page < 0) return -1;
-    return page * a.page_stride + (pos % a.page_size) * a.slot_stride;
-}
+    // Offset of the slot in the layer, or -1.
+    __device__ __forceinline__ int64_t offset(const TreeAttentionArgs& a) const {
+        return page < 0 ? -1 : page * a.page_stride + slot * a.slot_stride;
+    }
+};
 
 // Infinities and NaN of a packed pair of bf16 become zero.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
@@ -230,23 +247,50 @@ __device__ __forceinline__ uint2 dequant4(uint32_t codes, float scale) {
     return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// Eight columns c .. c+7 of a latent row as bf16; zeros past the row's columns.
+// Sixteen columns c .. c+15 of a latent row, as they lie in the cache: two pieces of eight
+// bf16 values, or sixteen codes and their scale.  Past the row's columns and for rows that do
+// not exist (offset -1): zeros.
 template <Source SRC>
-__device__ __forceinline__ uint4 row_piece(const TreeAttentionArgs& a, int64_t slot, int c) {
-    if (slot < 0 || c >= a.cols) return make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (SRC == kCodes) {
-        const uint8_t* p = a.qcache_layer + slot;
-        const int R = a.kv_lora_rank;
-        if (c >= R) return ld_nc_v4(p + R + 2 * (c - R));
-        const uint2 q = *reinterpret_cast<const uint2*>(p + c);
-        const float scale =
-            *reinterpret_cast<const float*>(p + R + 2 * (a.cols - R) + 4 * (c / 128));
-        const uint2 lo = dequant4(q.x, scale), hi = dequant4(q.y, scale);
-        return make_uint4(lo.x, lo.y, hi.x, hi.y);
-    } else {
-        return ld_nc_v4(a.cache_layer + slot + c);
+struct Piece {
+    uint4 lo, hi;
+
+    __device__ __forceinline__ void load(const TreeAttentionArgs& a, int64_t row, int c) {
+        lo = hi = make_uint4(0u, 0u, 0u, 0u);
+        if (row < 0 || c >= a.cols) return;
+        if constexpr (SRC == kCodes) {
+            const uint8_t* p = a.qcache_layer + row;
+            const int R = a.kv_lora_rank;
+            if (c < R) {
+                lo = ld_nc_v4(p + c);
+                hi.x = __ldg(reinterpret_cast<const uint32_t*>(
+                    p + R + 2 * (a.cols - R) + 4 * (c / 128)));
+            } else {
+                lo = ld_nc_v4(p + R + 2 * (c - R));
+                if (c + 8 < a.cols) hi = ld_nc_v4(p + R + 2 * (c - R) + 16);
+            }
+        } else {
+            lo = ld_nc_v4(a.cache_layer + row + c);
+            if (c + 8 < a.cols) hi = ld_nc_v4(a.cache_layer + row + c + 8);
+        }
     }
-}
+    // Writes the columns as bf16 to a swizzled 128-byte row, 16-byte chunks ch and ch + 1.
+    __device__ __forceinline__ void store(const TreeAttentionArgs& a, int c, uint32_t row,
+                                          int key, int ch, bool clean) {
+        if (SRC == kCodes && c < a.kv_lora_rank) {
+            const float scale = __uint_as_float(hi.x);
+            const uint2 d0 = dequant4(lo.x, scale), d1 = dequant4(lo.y, scale);
+            const uint2 d2 = dequant4(lo.z, scale), d3 = dequant4(lo.w, scale);
+            lo = make_uint4(d0.x, d0.y, d1.x, d1.y);
+            hi = make_uint4(d2.x, d2.y, d3.x, d3.y);
+        }
+        if (clean) {
+            lo = finite8(lo);
+            hi = finite8(hi);
+        }
+        st_shared_v4(row + ((ch ^ (key & 7)) << 4), lo.x, lo.y, lo.z, lo.w);
+        st_shared_v4(row + (((ch + 1) ^ (key & 7)) << 4), hi.x, hi.y, hi.z, hi.w);
+    }
+};
 
 // Bits k of the 64 keys c0 .. c0+63 that token i of the request may attend.
 __device__ __forceinline__ uint64_t attended(const TreeAttentionArgs& a, const Request& r,
@@ -282,8 +326,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
 template <Source SRC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
-                          const __grid_constant__ CUtensorMap tm_c, const TreeAttentionArgs a,
-                          const TreeWorkspace ws, const int box) {
+                          const __grid_constant__ CUtensorMap tm_c,
+                          const __grid_constant__ CUtensorMap tm_v, const TreeAttentionArgs a,
+                          const TreeWorkspace ws, const int box, const int vbox) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -295,29 +340,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float* s_sum = reinterpret_cast<float*>(smem + kOffSum);
     Bars* bars = reinterpret_cast<Bars*>(smem + kOffBars);
 
-    const int warp = threadIdx.x >> 5;
+    // Values that are the same in every lane pass through a shuffle, from which the compiler
+    // sees that they are: branches and addresses made of them then use uniform registers,
+    // where MMAs and TMA loads take their operands.  With operands that have to be moved there
+    // one by one, an MMA took 75 to 165 cycles to issue instead of 32 to execute.
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t rank = __shfl_sync(0xffffffffu, cluster_ctarank(), 0);
     const bool leader = rank == 0;
     const int64_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     const int R = a.kv_lora_rank;
     const int kblocks = (a.cols + 63) / 64;
+    const int kgroups = (kblocks + kGroup - 1) / kGroup;
     const int vblocks = (R + 127) / 128;        // value blocks of each CTA
     const int vgroups = (vblocks + 1) / 2;      // groups of two blocks, one MMA width each
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kBlocks; ++i) {
-            mbar_init(&bars->k_full[i], SRC == kTma ? 1 : 2);
+        for (int i = 0; i < kKeyGroups; ++i) {
+            // by TMA one arrival, with the bytes; else one for each block and CTA
+            const int blocks = max(min(kblocks - kGroup * i, kGroup), 1);
+            mbar_init(&bars->k_full[i], SRC == kTma ? 1 : 2 * blocks);
             mbar_init(&bars->k_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->v_full[i], 2);
             mbar_init(&bars->v_empty[i], 1);
             mbar_init(&bars->s_full[i], 1);
         }
+        for (int i = 0; i < kValueBlocks; ++i) mbar_init(&bars->v_full[i], 2);
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->p_full, 2 * kSoftWarps);
+        mbar_init(&bars->p_ready, 1);
         mbar_init(&bars->o_full, 1);
         mbar_init(&bars->o_empty, 2 * kSoftWarps);
         mbar_init(&bars->mma_done, 1);
@@ -328,18 +381,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_alloc_pair(&bars->tmem_base, kTmemCols);
         tmem_relinquish_pair();
     }
-    plan(a, bars, reinterpret_cast<int64_t*>(s_max), pair, pairs, blockIdx.x == 0);
+    plan(a, bars, reinterpret_cast<int64_t*>(s_max), pair, pairs);
+    griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
-    const uint32_t tmem = bars->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const WaitCtl wc{&bars->abort_flag, a.status, a.timeout_ns};
     const int64_t sharing = min(pairs, bars->units);  // pairs with a share
-    Walk w(a, bars, pair, sharing);
 
     if (warp < kSoftWarps) {
         // ---------------- softmax and epilogue: row = lane of the CTA's 64 ----------------
+        warpgroup_reg_alloc<kSoftRegs>();
+        Walk w(a, bars);
         const int half = warp >> 1;                   // which 64 keys, which half of O's columns
         const int row = (warp & 1) * 32 + lane;       // of this CTA's 64
         const float scale2 = a.scale * kLog2e;
@@ -354,12 +409,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && w.next(a)) {
             const int64_t rows_all = static_cast<int64_t>(w.r.n) * a.num_heads;
-            const int64_t rr = w.item * 128 + rank * 64 + row;
+            const int64_t rr = static_cast<int64_t>(w.item) * 128 + rank * 64 + row;
             const int32_t token =
-                static_cast<int32_t>(min(rr / a.num_heads, static_cast<int64_t>(w.r.n - 1)));
+                min(static_cast<int32_t>(quotient(rr, a.num_heads)), w.r.n - 1);
             float m = -INFINITY, l = 0.0f;
-            for (int64_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[g & 1], (g >> 1) & 1, wc))) {
+            for (int32_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
+                if (!__all_sync(0xffffffffu, mbar_wait_inl(&bars->s_full[g & 1], (g >> 1) & 1, wc))) {
                     ok = false;
                     break;
                 }
@@ -368,9 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_ld_x32(tmem + tlane + kScoreCol + (g & 1) * 64, x0);
                 tmem_ld_x32(tmem + tlane + kScoreCol + (g & 1) * 64 + 32, x1);
                 uint32_t lo = ~0u, hi = ~0u;
-                const bool partial = w.partial(kt);
+                const bool partial = kt >= w.cached_tiles();
                 if (partial) {
-                    const uint64_t bits = attended(a, w.r, token, kt * kKeys + half * 64);
+                    const uint64_t bits = attended(a, w.r, token, static_cast<int64_t>(kt) * kKeys + half * 64);
                     lo = static_cast<uint32_t>(bits);
                     hi = static_cast<uint32_t>(bits >> 32);
                 }
@@ -424,9 +479,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     p[k] = pack_bf16x2(e0, e1);
                 }
                 l = l * back + (sum0 + sum1);
+                // the weights are finished before the wait, not after it
+#pragma unroll
+                for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(p[k]));
                 // the previous tile's weights are used up, and O holds it
                 if (g > 0 &&
-                    !__all_sync(0xffffffffu, mbar_wait(&bars->o_full, (g - 1) & 1, wc))) {
+                    !__all_sync(0xffffffffu, mbar_wait_inl(&bars->o_full, (g - 1) & 1, wc))) {
                     ok = false;
                     break;
                 }
@@ -453,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_cluster(p_full);
             }
             if (!ok) break;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_full, (g - 1) & 1, wc))) {
+            if (!__all_sync(0xffffffffu, mbar_wait_inl(&bars->o_full, (g - 1) & 1, wc))) {
                 ok = false;
                 break;
             }
@@ -504,10 +562,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (half == 0 && rr < rows_all)
                     reinterpret_cast<float2*>(a.workspace + ws.stats)[at + lane] = make_float2(m, l);
                 if (w.kt0 == 0) {
-                    const int64_t end = w.base + (w.item + 1) * w.r.tiles;
-                    left_first = w.r.first * a.num_heads + w.item * 128;
-                    left_rows = static_cast<int32_t>(min(rows_all - w.item * 128,
-                                                         static_cast<int64_t>(128)));
+                    const int64_t end = w.u + w.r.tiles;
+                    left_first = row0 - rank * 64 - (warp & 1) * 32;
+                    left_rows = static_cast<int32_t>(
+                        min(rows_all - static_cast<int64_t>(w.item) * 128, static_cast<int64_t>(128)));
                     left_parts = static_cast<int32_t>((end * sharing - 1) / bars->units - pair) + 1;
                 }
             }
@@ -520,228 +578,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             TreeItem* items = reinterpret_cast<TreeItem*>(a.workspace + ws.items);
             items[pair] = TreeItem{left_first, ok ? left_rows : 0, left_parts};
         }
-    } else if (warp == kMmaWarp) {
-        // ---------------- MMA issuer (even CTA) ----------------
-        if (leader && lane == 0) {
+    } else if (warp < kKeyWarp) {
+      warpgroup_reg_dealloc<kIssueRegs>();
+      if (warp == kMmaWarp) {
+        // ---------------- MMA issuer (even CTA), all lanes together ----------------
+        if (leader) {
+            Walk w(a, bars);
+            // Waits that keep the loop's control flow uniform: a lane that gives up (as
+            // mbar_wait does) leaves the loop like the others, and the warp looks at `failed`
+            // once a tile.  What it issues until then is not used.
+            uint64_t t0 = globaltimer_ns();
+            bool failed = false;
+            const auto give_up = [&]() {
+                if (*wc.abort_flag) return true;
+                if (globaltimer_ns() - t0 <= a.timeout_ns) return false;
+                report(a.status, PKM_ERR_TIMEOUT);
+                *wc.abort_flag = 1;
+                return true;
+            };
+            const auto wait = [&](uint64_t* bar, uint32_t parity) {
+                uint32_t n = 0;
+                while (!mbar_try_wait(bar, parity))
+                    if ((++n & 127u) == 0 && (failed || give_up())) {
+                        failed = true;
+                        break;
+                    }
+            };
+            const auto wait_cluster = [&](uint64_t* bar, uint32_t parity) {
+                uint32_t n = 0;
+                while (!mbar_try_wait_cluster(bar, parity))
+                    if ((++n & 127u) == 0 && (failed || give_up())) {
+                        failed = true;
+                        break;
+                    }
+            };
             const uint32_t id_s = idesc_bf16(128, kKeys, false, false);
             const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
             const uint64_t p_desc = sdesc_sw128(smem_u32(sP), 16, 1024);
             const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kValueBytes, 1024);
             uint32_t g = 0, item = 0;
-            bool first = false;   // the tile whose values come next starts its item
+            bool first = false;     // the tile whose values come next starts its item
+            bool by_loads = false;  // and its values were written by threads
             // O (+)= P V of tile g - 1, the last whose scores were issued
-            const auto values = [&]() -> bool {
+            const auto values = [&]() {
                 const uint32_t ph = (g - 1) & 1;
-                if (!mbar_wait_cluster(&bars->p_full, ph, wc)) return false;
-                if (first && item > 1 && !mbar_wait(&bars->o_empty, item & 1, wc)) return false;
+                wait(&bars->p_ready, ph);
+                if (first && item > 1) wait(&bars->o_empty, item & 1);
                 tc_fence_after();
+                const uint32_t keep = first ? 0u : 1u;
                 for (int vg = 0; vg < vgroups; ++vg) {
-                    if (!mbar_wait_cluster(&bars->v_full[vg], ph, wc)) return false;
+                    const bool two = 2 * vg + 1 < vblocks;
+                    if (by_loads) {
+                        wait_cluster(&bars->v_full[2 * vg], ph);
+                        if (two) wait_cluster(&bars->v_full[2 * vg + 1], ph);
+                    } else {
+                        wait(&bars->v_full[2 * vg], ph);
+                        if (two) wait(&bars->v_full[2 * vg + 1], ph);
+                    }
                     tc_fence_after();
-                    const uint32_t id = idesc_bf16(128, 2 * vg + 1 < vblocks ? 256 : 128, false, true);
+                    const uint32_t id = idesc_bf16(128, two ? 256 : 128, false, true);
                     const uint64_t vd = desc_add_bytes(v_desc, vg * 2 * kValueBytes);
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 32 bytes of P, 2048 of V
-                        mma_bf16_pair(tmem + vg * 128,
-                                      desc_add_bytes(p_desc, (k / 4) * kBlockBytes + (k % 4) * 32),
-                                      vd + 128 * k, id, !first || k > 0 ? 1u : 0u);
-                    mma_commit_pair(&bars->v_empty[vg], 3);
+                        mma_bf16_pair_elect(
+                            tmem + vg * 128,
+                            desc_add_bytes(p_desc, (k / 4) * kBlockBytes + (k % 4) * 32),
+                            vd + 128 * k, id, k > 0 ? 1u : keep);
+                    mma_commit_pair_elect(&bars->v_empty[vg], 3);
                 }
-                mma_commit_pair(&bars->o_full, 3);
+                mma_commit_pair_elect(&bars->o_full, 3);
                 first = false;
-                return true;
             };
-            bool ok = true;
-            while (ok && w.next(a)) {
-                if (g > 0 && !values()) break;
+            while (__any_sync(0xffffffffu, w.next(a))) {
+                const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
+                const int cached = __shfl_sync(0xffffffffu, w.cached_tiles() - w.kt0, 0);
+                if (g > 0) values();
                 ++item;
-                if (!mbar_wait(&bars->q_full, (item - 1) & 1, wc)) break;
-                for (int64_t kt = w.kt0; kt < w.kt1; ++kt) {
+                wait(&bars->q_full, (item - 1) & 1);
+                for (int t = 0; t < tiles; ++t) {
                     const uint32_t d = tmem + kScoreCol + (g & 1) * 64;
-                    for (int kb = 0; kb < kblocks; ++kb) {
-                        ok = SRC == kTma ? mbar_wait(&bars->k_full[kb], g & 1, wc)
-                                         : mbar_wait_cluster(&bars->k_full[kb], g & 1, wc);
-                        if (!ok) break;
+                    for (int kg = 0; kg < kgroups; ++kg) {
+                        if (SRC == kTma) wait(&bars->k_full[kg], g & 1);
+                        else wait_cluster(&bars->k_full[kg], g & 1);
                         tc_fence_after();
-                        const uint64_t qd = desc_add_bytes(q_desc, kb * kBlockBytes);
-                        const uint64_t kd = desc_add_bytes(k_desc, kb * kBlockBytes);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16_pair(d, qd + 2 * k, kd + 2 * k, id_s, (kb | k) != 0 ? 1u : 0u);
-                        mma_commit_pair(&bars->k_empty[kb], 3);
+                        for (int i = 0; i < kGroup; ++i) {
+                            if (kg * kGroup + i >= kblocks) break;
+                            const uint64_t qd = desc_add_bytes(q_desc, (kg * kGroup + i) * kBlockBytes);
+                            const uint64_t kd = desc_add_bytes(k_desc, (kg * kGroup + i) * kBlockBytes);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16_pair_elect(d, qd + 2 * k, kd + 2 * k, id_s,
+                                                    (kg | i | k) != 0 ? 1u : 0u);
+                        }
+                        mma_commit_pair_elect(&bars->k_empty[kg], 3);
                     }
-                    if (!ok) break;
-                    mma_commit_pair(&bars->s_full[g & 1], 3);
-                    if (kt + 1 == w.kt1) mma_commit_pair(&bars->q_empty, 3);
-                    if (kt > w.kt0 && !values()) {
-                        ok = false;
-                        break;
-                    }
-                    if (kt == w.kt0) first = true;
+                    mma_commit_pair_elect(&bars->s_full[g & 1], 3);
+                    if (t + 1 == tiles) mma_commit_pair_elect(&bars->q_empty, 3);
+                    if (t > 0) values();
+                    else first = true;
+                    by_loads = SRC != kTma || t >= cached;
                     ++g;
+                    t0 = globaltimer_ns();
+                    if (__any_sync(0xffffffffu, failed)) break;
                 }
+                if (__any_sync(0xffffffffu, failed)) break;
             }
-            if (ok && g > 0) values();
-            mma_commit_pair(&bars->mma_done, 1);
-            mbar_wait(&bars->mma_done, 0, wc, false);
+            if (g > 0 && !__any_sync(0xffffffffu, failed)) values();
+            mma_commit_pair_elect(&bars->mma_done, 1);
+            mbar_wait_inl(&bars->mma_done, 0, wc, false);
         }
-    } else if (warp < kValueWarp) {
-        // ---------------- keys: this CTA's 64 of each tile, all columns ----------------
-        const uint32_t k_full = mapa_shared(smem_u32(&bars->k_full[0]), 0);
-        uint32_t g = 0;
-        bool ok = true;
-        if constexpr (SRC == kTma) {
-            const int boxes = 64 / box;
-            uint32_t issued[kBlocks] = {};
-            while (warp == kKeyWarp && ok && w.next(a)) {
-                for (int64_t kt = w.kt0; ok && kt < w.kt1; ++kt, ++g) {
-                    const int64_t pos = kt * kKeys + rank * 64 + lane * box;
-                    int32_t page = -1, slot = 0;
-                    if (lane < boxes) {
-                        page = page_of(a, w.b, pos, w.r.kv);
-                        slot = static_cast<int32_t>(pos % a.page_size);
-                    }
-                    for (int kb = 0; kb < kblocks; ++kb) {
-                        const int go = lane == 0 ? mbar_wait(&bars->k_empty[kb], (g & 1) ^ 1, wc) : 1;
-                        ok = __shfl_sync(0xffffffffu, go, 0);
-                        if (!ok) break;
-                        if (leader && lane == 0)
-                            mbar_arrive_expect_tx(&bars->k_full[kb], 2 * kBlockBytes);
-                        if (lane < boxes)
-                            tma_load_3d_pair(sK + kb * kBlockBytes + lane * box * 128, &tm_c,
-                                             k_full + kb * 8, kb * 64, slot, page);
-                        issued[kb] = g + 1;
-                    }
-                }
+      } else if (warp == kRelayWarp) {
+        // The weights of both CTAs are waited for here, at cluster scope: a satisfied wait of
+        // that scope takes several hundred cycles, which the MMA warp does not have.
+        if (leader)
+            for (int g = 0; g < bars->share; ++g) {
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster_inl(&bars->p_full, g & 1, wc))) break;
+                if (lane == 0) mbar_arrive(&bars->p_ready);
             }
-            if (!ok && lane == 0) {  // let the loads in flight land before the CTA retires
-                if (leader)
-                    for (int kb = 0; kb < kBlocks; ++kb)
-                        if (issued[kb] > 0)
-                            mbar_wait(&bars->k_full[kb], (issued[kb] - 1) & 1, wc, false);
-                if (!leader) spin_ns(50000);
-            }
-        } else {
-            const int t = threadIdx.x - kKeyWarp * 32, key = t >> 1, side = t & 1;
-            while (ok && w.next(a)) {
-                for (int64_t kt = w.kt0; ok && kt < w.kt1; ++kt, ++g) {
-                    const int64_t slot =
-                        slot_of(a, w.b, kt * kKeys + rank * 64 + key, w.r.kv);
-                    for (int kb = 0; kb < kblocks; ++kb) {
-                        if (t == 0) bars->k_go = mbar_wait(&bars->k_empty[kb], (g & 1) ^ 1, wc);
-                        named_bar_sync(2, 128);
-                        ok = bars->k_go;
-                        if (!ok) break;
-                        uint4 x[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            x[j] = row_piece<SRC>(a, slot, kb * 64 + side * 32 + j * 8);
-                        const uint32_t dst = smem_u32(sK + kb * kBlockBytes) + key * 128;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            st_shared_v4(dst + (((side * 4 + j) ^ (key & 7)) << 4), x[j].x, x[j].y,
-                                         x[j].z, x[j].w);
-                        fence_proxy_async_smem();
-                        named_bar_sync(2, 128);
-                        if (t == 0) mbar_arrive_cluster(k_full + kb * 8);
-                    }
-                }
-            }
-        }
-    } else if (warp < kQueryWarp) {
-        // ---------------- values: all 128 keys of each tile, this CTA's columns ----------------
-        const uint32_t v_full = mapa_shared(smem_u32(&bars->v_full[0]), 0);
-        const int t = threadIdx.x - kValueWarp * 32;
-        const int boxes = SRC == kTma ? kKeys / box : 1;
-        uint32_t g = 0, issued[2] = {};
-        bool ok = true;
-        while (ok && w.next(a)) {
-            for (int64_t kt = w.kt0; ok && kt < w.kt1; ++kt, ++g) {
-                if (SRC == kTma && !w.partial(kt)) {
-                    if (warp != kValueWarp) continue;
-                    const int blk = lane / boxes, i = lane % boxes;
-                    const int64_t pos = kt * kKeys + i * box;
-                    int32_t page = -1, slot = 0;
-                    if (blk < 2) {
-                        page = page_of(a, w.b, pos, w.r.kv);
-                        slot = static_cast<int32_t>(pos % a.page_size);
-                    }
-                    for (int vg = 0; vg < vgroups; ++vg) {
-                        const int go = lane == 0 ? mbar_wait(&bars->v_empty[vg], (g & 1) ^ 1, wc) : 1;
-                        ok = __shfl_sync(0xffffffffu, go, 0);
-                        if (!ok) break;
-                        const int blocks = min(2, vblocks - 2 * vg);
-                        if (lane == 0) {
-                            if (leader)
-                                mbar_arrive_expect_tx(&bars->v_full[vg], 2 * blocks * kValueBytes);
-                            else
-                                mbar_arrive_remote(v_full + vg * 8);
-                        }
-                        if (blk < blocks) {
-                            const int v = 2 * vg + blk;
-                            tma_load_3d_pair(sV + v * kValueBytes + i * box * 128, &tm_c,
-                                             v_full + vg * 8,
-                                             (static_cast<int>(rank) * vblocks + v) * 64, slot, page);
-                        }
-                        issued[vg] = g + 1;
-                    }
-                    if (!ok) {  // releases the other value warps from a later tile
-                        if (lane == 0) bars->v_go = 0;
-                        __syncwarp();
-                        named_bar_arrive(1, 128);
-                    }
-                } else {
-                    // Rows brought by loads: quantised ones, pages that no box divides, and
-                    // tiles with drafts, where a row that some query does not attend must not
-                    // turn its zero weight into NaN: infinities and NaN become zero.  (A query
-                    // that does attend such a draft has NaN or infinity among its scores.)
-                    const int64_t pos = kt * kKeys + t;
-                    const int64_t slot = slot_of(a, w.b, pos, w.r.kv);
-                    const bool clean = pos >= w.r.len;
-                    for (int vg = 0; vg < vgroups; ++vg) {
-                        if (t == 0) bars->v_go = mbar_wait(&bars->v_empty[vg], (g & 1) ^ 1, wc);
-                        named_bar_sync(1, 128);
-                        ok = bars->v_go;
-                        if (!ok) break;
-                        for (int v = 2 * vg; v < min(2 * vg + 2, vblocks); ++v) {
-                            const int col = (static_cast<int>(rank) * vblocks + v) * 64;
-                            uint4 x[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                x[j] = row_piece<SRC>(a, slot, col + j * 8);
-                            const uint32_t dst = smem_u32(sV + v * kValueBytes) + t * 128;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                if (clean) x[j] = finite8(x[j]);
-                                st_shared_v4(dst + ((j ^ (t & 7)) << 4), x[j].x, x[j].y, x[j].z,
-                                             x[j].w);
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        named_bar_sync(1, 128);
-                        if (t == 0) mbar_arrive_cluster(v_full + vg * 8);
-                    }
-                }
-            }
-        }
-        if (SRC == kTma && !ok && t == 0) {
-            if (leader)
-                for (int vg = 0; vg < 2; ++vg)
-                    if (issued[vg] > 0)
-                        mbar_wait(&bars->v_full[vg], (issued[vg] - 1) & 1, wc, false);
-            if (!leader) spin_ns(50000);
-        }
-    } else {
+      } else if (warp == kQueryWarp) {
         // ---------------- queries: this CTA's 64 rows of each item ----------------
+        Walk w(a, bars);
         const uint32_t q_full = mapa_shared(smem_u32(&bars->q_full), 0);
         uint32_t item = 0;
         bool ok = true;
         while (ok && w.next(a)) {
-            const int go = lane == 0 ? mbar_wait(&bars->q_empty, (item & 1) ^ 1, wc) : 1;
+            const int go = lane == 0 ? mbar_wait_inl(&bars->q_empty, (item & 1) ^ 1, wc) : 1;
             ok = __shfl_sync(0xffffffffu, go, 0);
             if (!ok) break;
-            const int64_t row = w.r.first * a.num_heads + w.item * 128 + rank * 64;
+            const int64_t row = w.r.first * a.num_heads + static_cast<int64_t>(w.item) * 128 + rank * 64;
             if (leader && lane == 0)
                 mbar_arrive_expect_tx(&bars->q_full, 2 * kblocks * kBlockBytes);
             if (lane < kblocks)
@@ -749,13 +715,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                  static_cast<int32_t>(row));
             ++item;
         }
-        if (!ok && lane == 0) {
-            if (leader && item > 0) mbar_wait(&bars->q_full, (item - 1) & 1, wc, false);
+        if (!ok && lane == 0) {  // let the loads in flight land before the CTA retires
+            if (leader && item > 0) mbar_wait_inl(&bars->q_full, (item - 1) & 1, wc, false);
+            if (!leader) spin_ns(50000);
+        }
+      }
+    } else {
+        // ---------------- keys and values ----------------
+        // Keys: this CTA's 64 of each tile, all columns; warp i brings group i by TMA, or
+        // blocks i, i + 4, ... by loads.  Values: all 128 keys, this CTA's columns, block i.
+        Walk w(a, bars);
+        const bool keys = warp < kValueWarp;
+        const int i = (warp - kKeyWarp) & 3;
+        const int blocks = keys ? kblocks : min(vblocks, i + 1);
+        const int rows = keys ? 64 : kKeys;
+        const int slots = keys ? box : vbox;       // of one page in a TMA box
+        const int boxes = SRC == kTma ? rows / slots : 1;
+        const uint32_t bytes = static_cast<uint32_t>(rows) * 128;
+        uint8_t* base = keys ? sK : sV;
+        uint64_t* full = keys ? bars->k_full : bars->v_full;
+        uint64_t* empty = keys ? bars->k_empty : bars->v_empty;
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+        const int col0 = keys ? 0 : static_cast<int>(rank) * vblocks * 64;
+        const CUtensorMap* map = keys ? &tm_c : &tm_v;
+        // by TMA a key warp brings a whole group
+        const int from = keys ? i * kGroup : i;
+        const int to = keys ? min(kblocks, from + kGroup) : blocks;
+        uint32_t g = 0, issued = 0;                // issued: tiles brought by TMA
+        bool ok = true;
+        while (ok && __any_sync(0xffffffffu, w.next(a))) {
+            const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
+            const int cached = __shfl_sync(0xffffffffu, w.cached_tiles() - w.kt0, 0);
+            for (int t = 0; ok && t < tiles; ++t, ++g) {
+                const int32_t kt = w.kt0 + t;
+                const int64_t pos0 = static_cast<int64_t>(kt) * kKeys + (keys ? rank * 64 : 0u);
+                // Drafts that some query does not attend must not turn its zero weights into
+                // NaN: as values their infinities and NaN become zero, which takes a pass
+                // through registers.  (A query that attends such a draft has it in its scores.)
+                if (SRC == kTma && (keys || t < cached)) {
+                    if (from >= to) continue;
+                    const Place at(a, w.b, lane < boxes ? pos0 + lane * slots : w.r.kv, w.r.kv);
+                    ok = __all_sync(0xffffffffu, mbar_wait_inl(&empty[keys ? i : i >> 1],
+                                                               (g & 1) ^ 1, wc));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (leader) mbar_arrive_expect_tx(&full[i], 2 * (to - from) * bytes);
+                        else if (!keys) mbar_arrive_remote(full0 + i * 8);
+                    }
+                    for (int blk = from; blk < to; ++blk)
+                        for (int x = 0; x < boxes; ++x)
+                            tma_load_3d_pair_elect(base + blk * bytes + x * slots * 128, map,
+                                                   full0 + i * 8, col0 + blk * 64,
+                                                   __shfl_sync(0xffffffffu, at.slot, x),
+                                                   __shfl_sync(0xffffffffu, at.page, x));
+                    issued = g + 1;
+                    continue;
+                }
+                // By loads: four lanes take a row's 64 columns, 16 each; eight rows at a time.
+                const int sub = lane >> 2, part = lane & 3;
+                for (int blk = i; blk < blocks; blk += 4) {
+                    const int c = col0 + blk * 64 + part * 16;
+                    const int64_t mine[2] = {
+                        Place(a, w.b, pos0 + lane, w.r.kv).offset(a),
+                        Place(a, w.b, pos0 + 32 + lane, w.r.kv).offset(a)};
+                    const int64_t more[2] = {
+                        keys ? -1 : Place(a, w.b, pos0 + 64 + lane, w.r.kv).offset(a),
+                        keys ? -1 : Place(a, w.b, pos0 + 96 + lane, w.r.kv).offset(a)};
+                    bool waited = false;
+                    for (int r0 = 0; r0 < rows; r0 += 64) {
+                        Piece<SRC> x[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int64_t from = r0 == 0 ? mine[k >> 2] : more[k >> 2];
+                            x[k].load(a, __shfl_sync(0xffffffffu, from, (k & 3) * 8 + sub), c);
+                        }
+                        if (!waited) {
+                            const int go = lane == 0 ? mbar_wait_inl(&empty[keys ? blk / kGroup : blk >> 1],
+                                                                     (g & 1) ^ 1, wc)
+                                                     : 1;
+                            ok = __shfl_sync(0xffffffffu, go, 0);
+                            if (!ok) break;
+                            waited = true;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int key = r0 + k * 8 + sub;
+                            x[k].store(a, c, smem_u32(base + blk * bytes) + key * 128, key, part * 2,
+                                       !keys && pos0 + key >= w.r.len);
+                        }
+                    }
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(full0 + (keys ? blk / kGroup : blk) * 8);
+                }
+            }
+        }
+        if (!ok && issued > 0 && lane == 0) {  // let the loads in flight land
+            if (leader) mbar_wait_inl(&full[i], (issued - 1) & 1, wc, false);
             if (!leader) spin_ns(50000);
         }
     }
 
-    griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -772,25 +833,33 @@ constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const TreeAttentionArgs a, const TreeWorkspace ws, const int pairs) {
     __shared__ TreeItem items[kTreeMaxPairs];
+    __shared__ int ends[kTreeMaxPairs];  // rows of all items up to and including this one
+    __shared__ int which;
     __shared__ float weight[kTreeMaxPairs];
     __shared__ float4 sums[kJoinThreads];
     griddep_wait();
     const TreeItem* held = reinterpret_cast<const TreeItem*>(a.workspace + ws.items);
     for (int p = threadIdx.x; p < pairs; p += kJoinThreads) items[p] = held[p];
     __syncthreads();
+    int end = 0;
+    if (threadIdx.x < pairs) {
+        for (int p = 0; p <= static_cast<int>(threadIdx.x); ++p) end += items[p].rows;
+        ends[threadIdx.x] = end;
+    }
+    __syncthreads();
+    const int total_rows = ends[pairs - 1];
     const int R = a.kv_lora_rank, quads = R / 4;
     const int groups = kJoinThreads / quads;
     const int quad = threadIdx.x % quads, grp = threadIdx.x / quads;
     const float2* stats = reinterpret_cast<const float2*>(a.workspace + ws.stats);
     const float4* parts = reinterpret_cast<const float4*>(a.workspace + ws.parts);
-    int before = 0;
-    for (int p = 0; p < pairs; ++p) {
-        const TreeItem it = items[p];
-        // rows are dealt to the blocks across all items
-        int row = (static_cast<int>(blockIdx.x) - before) % static_cast<int>(gridDim.x);
-        if (row < 0) row += gridDim.x;
-        before = (before + it.rows) % static_cast<int>(gridDim.x);
-        for (; row < it.rows; row += gridDim.x) {
+    for (int f = blockIdx.x; f < total_rows; f += gridDim.x) {
+            if (threadIdx.x < pairs && f < end && f >= end - items[threadIdx.x].rows)
+                which = threadIdx.x;
+            __syncthreads();
+            const int p = which;
+            const TreeItem it = items[p];
+            const int row = f - (ends[p] - it.rows);
             // part k of the item: the pair's second slot, then the first slots behind it
             const auto slot = [&](int k) -> int64_t {
                 return (static_cast<int64_t>(2) * (p + k) + (k == 0 ? 1 : 0)) * ws.rows + row;
@@ -844,35 +913,35 @@ __global__ void __launch_bounds__(kJoinThreads)
                     make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
             }
             __syncthreads();
-        }
     }
 }
 
 template <Source SRC>
 cudaError_t launch_source(const CUtensorMap& tm_q, const CUtensorMap& tm_c,
-                          const TreeAttentionArgs& args, const TreeWorkspace& ws, int box,
-                          int pairs, cudaStream_t stream) {
+                          const CUtensorMap& tm_v, const TreeAttentionArgs& args,
+                          const TreeWorkspace& ws, int box, int vbox, int pairs,
+                          cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<SRC>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
     tree_attention_kernel<SRC><<<static_cast<unsigned>(2 * pairs), kThreads, kSmemBytes, stream>>>(
-        tm_q, tm_c, args, ws, box);
+        tm_q, tm_c, tm_v, args, ws, box, vbox);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_c,
-                                  TreeAttentionArgs args, int box, int num_sms,
-                                  cudaStream_t stream) {
+                                  const CUtensorMap& tm_v, TreeAttentionArgs args, int box,
+                                  int vbox, int num_sms, cudaStream_t stream) {
     const TreeWorkspace ws = tree_workspace(args.total_rows, args.num_heads, args.kv_lora_rank);
     const int pairs = num_sms / 2 < kTreeMaxPairs ? num_sms / 2 : kTreeMaxPairs;
     const cudaError_t e =
         args.qcache_layer != nullptr
-            ? launch_source<kCodes>(tm_q, tm_c, args, ws, box, pairs, stream)
-        : box >= 8 ? launch_source<kTma>(tm_q, tm_c, args, ws, box, pairs, stream)
-                   : launch_source<kRows>(tm_q, tm_c, args, ws, box, pairs, stream);
+            ? launch_source<kCodes>(tm_q, tm_c, tm_v, args, ws, box, vbox, pairs, stream)
+        : box >= 8 ? launch_source<kTma>(tm_q, tm_c, tm_v, args, ws, box, vbox, pairs, stream)
+                   : launch_source<kRows>(tm_q, tm_c, tm_v, args, ws, box, vbox, pairs, stream);
     if (e != cudaSuccess) return e;
     return launch_dependent(tree_join_kernel, static_cast<unsigned>(num_sms) * 2, kJoinThreads, 0,
                             stream, args, ws, pairs);
