@@ -132,21 +132,26 @@ bool encode_cache_gather(CUtensorMap* map, const void* layer, int32_t page_size,
            CUDA_SUCCESS;
 }
 
-// One layer of the paged latent cache as a 3-D tensor {column, slot, page}, boxes of
-// {64, box_slots, 1}: 64 columns of consecutive slots of one page, 128-byte swizzled, zeros
-// past the row's columns and for pages that do not exist.
+// One layer of the paged latent cache for boxes of box_slots consecutive slots of one page,
+// 128-byte swizzled, zeros for pages that do not exist.  Boxes of several 64-column blocks of
+// a row: a 4-D tensor {64 columns of a block, slot, page, block}, each block of a box a
+// [box_slots x 64] tile of its own.  Boxes of one block: {column, slot, page, 1}, zeros past
+// the row's last column.
 bool encode_cache_pages(CUtensorMap* map, const void* layer, int32_t cols, int32_t page_size,
                         int32_t num_pages, int64_t slot_stride, int64_t page_stride,
-                        uint32_t box_slots) {
+                        uint32_t box_slots, uint32_t box_blocks) {
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(page_size),
-                                static_cast<cuuint64_t>(num_pages)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(slot_stride) * 2,
-                                   static_cast<cuuint64_t>(page_stride) * 2};
-    const cuuint32_t box[3] = {64, box_slots, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(layer), dims, strides,
+    const bool whole = box_blocks > 1;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(whole ? 64 : cols),
+                                static_cast<cuuint64_t>(page_size),
+                                static_cast<cuuint64_t>(num_pages),
+                                static_cast<cuuint64_t>(whole ? cols / 64 : 1)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot_stride) * 2,
+                                   static_cast<cuuint64_t>(page_stride) * 2, 128};
+    const cuuint32_t box[4] = {64, box_slots, 1, box_blocks};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(layer), dims, strides,
               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
@@ -946,21 +951,30 @@ pkm_status tree_attention(TreeAttentionArgs a, const void* q, const uint32_t* in
     int vbox = 128;
     while (vbox > 1 && a.page_size % vbox != 0) vbox /= 2;
     const int box = vbox < 64 ? vbox : 64;
-    alignas(64) CUtensorMap tm_q, tm_c, tm_v;
+    // and, where that is all of them and the row has only whole blocks, several blocks
+    const bool whole = a.cols % 64 == 0;
+    const bool key_groups = whole && box == 64, value_groups = whole && vbox == 128;
+    const auto encode_pages = [&](CUtensorMap* map, int slots, int blocks) {
+        return encode_cache_pages(map, a.cache_layer, a.cols, a.page_size, a.num_pages,
+                                  a.slot_stride, a.page_stride, static_cast<uint32_t>(slots),
+                                  static_cast<uint32_t>(blocks));
+    };
+    alignas(64) CUtensorMap tm_q, tm_k0, tm_k1, tm_v;
     if (!encode_2d(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, a.cols,
                    static_cast<uint64_t>(total_rows) * num_heads,
                    static_cast<uint64_t>(a.cols) * 2, 64, 64))
         return encode_failed();
     if (a.qcache_layer != nullptr || box < 8)
-        tm_c = tm_v = tm_q;
-    else if (!encode_cache_pages(&tm_c, a.cache_layer, a.cols, a.page_size, a.num_pages,
-                                 a.slot_stride, a.page_stride, static_cast<uint32_t>(box)) ||
-             !encode_cache_pages(&tm_v, a.cache_layer, a.cols, a.page_size, a.num_pages,
-                                 a.slot_stride, a.page_stride, static_cast<uint32_t>(vbox)))
+        tm_k0 = tm_k1 = tm_v = tm_q;
+    else if (!encode_pages(&tm_k0, box, key_groups ? pkm::kTreeKeyBlocks : 1) ||
+             !encode_pages(&tm_k1, box, key_groups ? pkm::kTreeLastKeyBlocks : 1) ||
+             !encode_pages(&tm_v, vbox, value_groups ? pkm::kTreeValueBlocks : 1))
         return encode_failed();
+    const pkm::TreeBoxes boxes{box, vbox, key_groups ? pkm::kTreeKeyBlocks : 1,
+                               value_groups ? pkm::kTreeValueBlocks : 1};
     if (const cudaError_t e = debug_validate(input_row_offsets, batch, dev_status, stream))
         return cuda_status(e);
-    return cuda_status(pkm::launch_tree_attention(tm_q, tm_c, tm_v, a, box, vbox, sms,
+    return cuda_status(pkm::launch_tree_attention(tm_q, tm_k0, tm_k1, tm_v, a, boxes, sms,
                                                   static_cast<cudaStream_t>(stream)));
 }
 

@@ -372,16 +372,17 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         : "memory");
 }
 
-// The 3-D load issued by one elected lane of a warp whose lanes run together.
-__device__ __forceinline__ void tma_load_3d_pair_elect(void* dst, const CUtensorMap* map,
+// The 4-D load issued by one elected lane of a warp whose lanes run together.
+__device__ __forceinline__ void tma_load_4d_pair_elect(void* dst, const CUtensorMap* map,
                                                        uint32_t bar_cluster, int32_t c0,
-                                                       int32_t c1, int32_t c2) {
+                                                       int32_t c1, int32_t c2, int32_t c3) {
     asm volatile(
         "{\n\t.reg .pred e;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2),
+        "r"(c3)
         : "memory");
 }
 
@@ -825,6 +826,20 @@ __device__ __forceinline__ void mma_bf16_pair_elect(uint32_t d_tmem, uint64_t ad
         "setp.ne.b32 p, %4, 0;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// A in tensor memory: packed bf16 pairs, K along the columns; with M = 128 row r of a CTA's 64
+// lies in lanes r and r + 64, since each half of the lanes computes its half of the columns.
+__device__ __forceinline__ void mma_bf16_pair_ts_elect(uint32_t d_tmem, uint32_t a_tmem,
+                                                       uint64_t bdesc, uint32_t idesc,
+                                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 

@@ -154,13 +154,18 @@ struct KvFp8Extra {
 // request) leave for the kernel that joins their parts.  A pair starts at most one item that
 // it does not finish and finishes at most one that it did not start, so it has two slots.
 constexpr int kTreeMaxPairs = 80;
+// 64-column blocks of the TMA boxes: of a row's first keys, its other keys, its values
+constexpr int kTreeKeyBlocks = 4, kTreeLastKeyBlocks = 5, kTreeValueBlocks = 2;
+struct TreeBoxes {      // slots of one page and 64-column blocks of the TMA boxes
+    int32_t key_slots, value_slots, key_blocks, value_blocks;
+};
 struct TreeItem {       // an item that a pair starts and leaves unfinished (rows = 0: none)
     int64_t first;      // first of its rows (token, head)
     int32_t rows, parts;
 };
 struct TreeWorkspace {
     int32_t rows;       // rows a slot holds
-    size_t parts;       // fp32 [2 * kTreeMaxPairs, rows, R], unnormalised
+    size_t parts;       // fp32 [2 * kTreeMaxPairs, R / 4, rows, 4], unnormalised
     size_t stats;       // fp32 [2 * kTreeMaxPairs, rows, 2]: maximum (base 2) and sum
     size_t items;       // TreeItem [kTreeMaxPairs]
     size_t bytes;
@@ -221,9 +226,10 @@ cudaError_t launch_kv_matmul_fp8(const CUtensorMap& tm_q, const CUtensorMap& tm_
 cudaError_t launch_cache_write(CacheWriteArgs args, int num_sms, cudaStream_t stream);
 cudaError_t launch_rope_heads(RopeHeadsArgs args, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_compact(CompactArgs args, cudaStream_t stream);
-cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_keys,
-                                  const CUtensorMap& tm_values, TreeAttentionArgs args, int box,
-                                  int vbox, int num_sms, cudaStream_t stream);
+cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_first_keys,
+                                  const CUtensorMap& tm_last_keys,
+                                  const CUtensorMap& tm_values, TreeAttentionArgs args,
+                                  TreeBoxes boxes, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_timeout_check(int32_t* status, uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t launch_validate_offsets(const uint32_t* offsets, int32_t batch, int32_t* status,
                                     cudaStream_t stream);

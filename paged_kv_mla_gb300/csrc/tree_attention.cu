@@ -23,10 +23,15 @@
 // it did not start.  Such parts leave unnormalised fp32 sums, maxima and totals in the
 // workspace and a second kernel joins them; whole items are written directly.
 //
-// Roles of a CTA (16 warps): 0-3 softmax and epilogue, 4 MMA issue (even CTA), 5 queries, 6
-// a relay, 8-11 keys, 12-15 values; the softmax warps take over registers of warps 4-7.  Scores are kept in base 2; the running maximum moves only when
+// Roles of a CTA (16 warps): 0-3 softmax and epilogue, 4 MMA issue (even CTA), 5 queries,
+// 8-11 keys, 12-15 values; the softmax warps take over registers of warps 4-7.  Scores are kept in base 2; the running maximum moves only when
 // a row's new maximum exceeds it by 2^8, since any reference works as long as nothing
 // overflows, so the accumulator is hardly ever rescaled.
+//
+// What threads write for the MMAs (weights, rows brought by loads) each CTA's tensor core
+// reads from its own shared memory.  The writer's fence.proxy.async completes before its
+// arrival at the even CTA's barrier, so an arrival of default scope is enough; one with
+// cluster-scope release took 1430 cycles of every tile.
 #include <cuda_fp16.h>
 
 #include "pkm_device.cuh"
@@ -35,18 +40,19 @@
 namespace pkm {
 namespace {
 
-constexpr int kSoftWarps = 4, kMmaWarp = 4, kQueryWarp = 5, kRelayWarp = 6, kKeyWarp = 8, kValueWarp = 12;
+constexpr int kSoftWarps = 4, kMmaWarp = 4, kQueryWarp = 5, kKeyWarp = 8, kValueWarp = 12;
 constexpr int kThreads = 16 * 32;
 constexpr int kSoftRegs = 192, kIssueRegs = 64;  // with 128 for each loader: 4 x 128 in all
 constexpr int kKeys = 128;          // keys of a tile (64 loaded by each CTA as keys)
 constexpr int kBlocks = 9;          // 64-column blocks of a latent row
 constexpr int kBlockBytes = 64 * 128;
-constexpr int kGroup = 3;           // key blocks that are waited for and released together
-constexpr int kKeyGroups = kBlocks / kGroup;
-constexpr int kValueBlocks = 4;     // 64-column value blocks a CTA loads
-constexpr int kValueBytes = kKeys * 128;
+constexpr int kKeyGroups = 2;       // key blocks waited for and released together: 0-3, 4-8
+constexpr int kQueryBlocks = kTreeKeyBlocks;  // query blocks kept in tensor memory, the others in shared
+constexpr int kValueBytes = kKeys * 128;  // one of a CTA's up to four 64-column value blocks
+constexpr int kValueRing = 3;       // groups of two value blocks in flight
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScoreCol = 256; // TMEM column of the first score tile
+constexpr uint32_t kQueryCol = 384; // TMEM column of the queries, 32 a block
 constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
@@ -55,12 +61,11 @@ enum Source { kTma, kRows, kCodes };  // pages by TMA, bf16 rows by loads, quant
 struct Bars {
     uint64_t k_full[kKeyGroups];   // even CTA: a group of blocks of both CTAs' keys is there
     uint64_t k_empty[kKeyGroups];  // both: its MMAs are done
-    uint64_t v_full[kValueBlocks];  // even CTA: a value block of both CTAs is there
-    uint64_t v_empty[2];        // both: two value blocks are free
+    uint64_t v_full[kValueRing];   // even CTA: a group of both CTAs' value blocks is there
+    uint64_t v_empty[kValueRing];  // both: its MMAs are done
     uint64_t q_full, q_empty;   // the item's query rows
     uint64_t s_full[2];         // both: a score tile is complete
     uint64_t p_full;            // even CTA: both CTAs' weights are written
-    uint64_t p_ready;           // even CTA: the same, passed on within the CTA
     uint64_t o_full;            // both: the tile's weights are used up and O is current
     uint64_t o_empty;           // even CTA: both CTAs' epilogues have read O
     uint64_t mma_done;
@@ -73,9 +78,9 @@ struct Bars {
 };
 
 constexpr size_t kOffQ = 0;
-constexpr size_t kOffK = kOffQ + size_t(kBlocks) * kBlockBytes;
+constexpr size_t kOffK = kOffQ + size_t(kBlocks - kQueryBlocks) * kBlockBytes;
 constexpr size_t kOffV = kOffK + size_t(kBlocks) * kBlockBytes;
-constexpr size_t kOffP = kOffV + size_t(kValueBlocks) * kValueBytes;
+constexpr size_t kOffP = kOffV + size_t(kValueRing) * 2 * kValueBytes;
 constexpr size_t kOffMax = kOffP + 2 * size_t(kBlockBytes);
 constexpr size_t kOffSum = kOffMax + 2 * 128 * sizeof(float);
 constexpr size_t kOffBars = kOffSum + 128 * sizeof(float);
@@ -323,12 +328,18 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// Waits with all lanes of a warp; the verdict is the same in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
+    return __all_sync(0xffffffffu, mbar_wait_inl(bar, parity, wc));
+}
+
 template <Source SRC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
-                          const __grid_constant__ CUtensorMap tm_c,
+                          const __grid_constant__ CUtensorMap tm_k0,
+                          const __grid_constant__ CUtensorMap tm_k1,
                           const __grid_constant__ CUtensorMap tm_v, const TreeAttentionArgs a,
-                          const TreeWorkspace ws, const int box, const int vbox) {
+                          const TreeWorkspace ws, const TreeBoxes tb) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -351,31 +362,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int64_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     const int R = a.kv_lora_rank;
     const int kblocks = (a.cols + 63) / 64;
-    const int kgroups = (kblocks + kGroup - 1) / kGroup;
     const int vblocks = (R + 127) / 128;        // value blocks of each CTA
     const int vgroups = (vblocks + 1) / 2;      // groups of two blocks, one MMA width each
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kKeyGroups; ++i) {
-            // by TMA one arrival, with the bytes; else one for each block and CTA
-            const int blocks = max(min(kblocks - kGroup * i, kGroup), 1);
-            mbar_init(&bars->k_full[i], SRC == kTma ? 1 : 2 * blocks);
+            // one box: one arrival, with the bytes; boxes of a block: one each; by loads: one
+            // for each block and CTA
+            const int blocks = max(i == 0 ? min(kblocks, kQueryBlocks) : kblocks - kQueryBlocks, 1);
+            mbar_init(&bars->k_full[i], SRC != kTma ? 2 * blocks : tb.key_blocks > 1 ? 1 : blocks);
             mbar_init(&bars->k_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kValueRing; ++i) {
+            mbar_init(&bars->v_full[i], 4);  // two blocks, two CTAs
             mbar_init(&bars->v_empty[i], 1);
-            mbar_init(&bars->s_full[i], 1);
         }
-        for (int i = 0; i < kValueBlocks; ++i) mbar_init(&bars->v_full[i], 2);
-        mbar_init(&bars->q_full, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bars->s_full[i], 1);
+        mbar_init(&bars->q_full, 1 + 2 * 4);  // the TMA bytes, and four value warps of each CTA
         mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->p_full, 2 * kSoftWarps);
-        mbar_init(&bars->p_ready, 1);
         mbar_init(&bars->o_full, 1);
         mbar_init(&bars->o_empty, 2 * kSoftWarps);
         mbar_init(&bars->mma_done, 1);
         bars->abort_flag = 0;
         fence_mbar_init();
+    }
+    if (warp == kQueryWarp && lane == 0) {
+        tma_prefetch_map(&tm_q);
+        tma_prefetch_map(&tm_k0);
+        tma_prefetch_map(&tm_k1);
+        tma_prefetch_map(&tm_v);
     }
     if (warp == kMmaWarp) {
         tmem_alloc_pair(&bars->tmem_base, kTmemCols);
@@ -414,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 min(static_cast<int32_t>(quotient(rr, a.num_heads)), w.r.n - 1);
             float m = -INFINITY, l = 0.0f;
             for (int32_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
-                if (!__all_sync(0xffffffffu, mbar_wait_inl(&bars->s_full[g & 1], (g >> 1) & 1, wc))) {
+                if (!warp_wait(&bars->s_full[g & 1], (g >> 1) & 1, wc)) {
                     ok = false;
                     break;
                 }
@@ -484,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(p[k]));
                 // the previous tile's weights are used up, and O holds it
                 if (g > 0 &&
-                    !__all_sync(0xffffffffu, mbar_wait_inl(&bars->o_full, (g - 1) & 1, wc))) {
+                    !warp_wait(&bars->o_full, (g - 1) & 1, wc)) {
                     ok = false;
                     break;
                 }
@@ -508,10 +524,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(p_full);
+                if (lane == 0) mbar_arrive_remote(p_full);
             }
             if (!ok) break;
-            if (!__all_sync(0xffffffffu, mbar_wait_inl(&bars->o_full, (g - 1) & 1, wc))) {
+            if (!warp_wait(&bars->o_full, (g - 1) & 1, wc)) {
                 ok = false;
                 break;
             }
@@ -528,12 +544,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t row0 = w.r.first * a.num_heads + rr - lane;  // of this warp's 32
             if (whole) {
                 const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+                uint32_t x0[32], x1[32], p[32];
+                tmem_ld_x32(tmem + tlane, x0);
+                tmem_ld_x32(tmem + tlane + 32, x1);
                 for (int v = 0; v < vblocks; ++v) {
                     const int col = (half * vblocks + v) * 64;
                     if (col >= R) break;
-                    uint32_t x0[32], x1[32], p[32];
-                    tmem_ld_x32(tmem + tlane + v * 64, x0);
-                    tmem_ld_x32(tmem + tlane + v * 64 + 32, x1);
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -542,25 +558,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         p[16 + k] = pack_bf16x2(__uint_as_float(x1[2 * k]) * inv,
                                                 __uint_as_float(x1[2 * k + 1]) * inv);
                     }
+                    if (v + 1 < vblocks) {  // in flight while this block is stored
+                        tmem_ld_x32(tmem + tlane + (v + 1) * 64, x0);
+                        tmem_ld_x32(tmem + tlane + (v + 1) * 64 + 32, x1);
+                    }
                     warp_store_rows_32x64(stage, p, a.out + row0 * R + col, R, valid, lane);
                 }
+                tmem_ld_wait();
                 if (half == 0 && rr < rows_all && a.lse != nullptr)
                     a.lse[row0 + lane] = l != 0.0f ? m * kLn2 + logf(l) : -INFINITY;
             } else {
                 const int64_t slot = 2 * pair + (w.kt0 > 0 ? 0 : 1);
-                const int64_t at = slot * ws.rows + rank * 64 + (warp & 1) * 32;
-                float* part = reinterpret_cast<float*>(a.workspace + ws.parts) + at * R;
+                // four columns of consecutive rows side by side: whole lines, without staging
+                const int at = rank * 64 + row;
+                float4* part = reinterpret_cast<float4*>(a.workspace + ws.parts) +
+                               (slot * (R / 4) + half * vblocks * 16) * ws.rows + at;
                 for (int v = 0; v < 2 * vblocks; ++v) {
-                    const int col = half * vblocks * 64 + v * 32;
-                    if (col >= R) break;
+                    if (half * vblocks * 64 + v * 32 >= R) break;
                     uint32_t x[32];
                     tmem_ld_x32(tmem + tlane + v * 32, x);
                     tmem_ld_wait();
-                    warp_store_rows_32x64(stage, x, reinterpret_cast<uint16_t*>(part + col),
-                                          2 * static_cast<int64_t>(R), valid, lane);
+                    if (rr < rows_all)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            st_v4(part + static_cast<int64_t>(v * 8 + k) * ws.rows,
+                                  make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
                 }
                 if (half == 0 && rr < rows_all)
-                    reinterpret_cast<float2*>(a.workspace + ws.stats)[at + lane] = make_float2(m, l);
+                    reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + at] =
+                        make_float2(m, l);
                 if (w.kt0 == 0) {
                     const int64_t end = w.u + w.r.tiles;
                     left_first = row0 - rank * 64 - (warp & 1) * 32;
@@ -587,27 +613,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // Waits that keep the loop's control flow uniform: a lane that gives up (as
             // mbar_wait does) leaves the loop like the others, and the warp looks at `failed`
             // once a tile.  What it issues until then is not used.
-            uint64_t t0 = globaltimer_ns();
             bool failed = false;
-            const auto give_up = [&]() {
+            const auto give_up = [&](uint64_t& since) {
                 if (*wc.abort_flag) return true;
-                if (globaltimer_ns() - t0 <= a.timeout_ns) return false;
+                const uint64_t now = globaltimer_ns();
+                if (since == 0) since = now;
+                if (now - since <= a.timeout_ns) return false;
                 report(a.status, PKM_ERR_TIMEOUT);
                 *wc.abort_flag = 1;
                 return true;
             };
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
                 uint32_t n = 0;
+                uint64_t since = 0;
                 while (!mbar_try_wait(bar, parity))
-                    if ((++n & 127u) == 0 && (failed || give_up())) {
-                        failed = true;
-                        break;
-                    }
-            };
-            const auto wait_cluster = [&](uint64_t* bar, uint32_t parity) {
-                uint32_t n = 0;
-                while (!mbar_try_wait_cluster(bar, parity))
-                    if ((++n & 127u) == 0 && (failed || give_up())) {
+                    if ((++n & 127u) == 0 && (failed || give_up(since))) {
                         failed = true;
                         break;
                     }
@@ -618,101 +638,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t p_desc = sdesc_sw128(smem_u32(sP), 16, 1024);
             const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kValueBytes, 1024);
             uint32_t g = 0, item = 0;
-            bool first = false;     // the tile whose values come next starts its item
-            bool by_loads = false;  // and its values were written by threads
-            // O (+)= P V of tile g - 1, the last whose scores were issued
-            const auto values = [&]() {
-                const uint32_t ph = (g - 1) & 1;
-                wait(&bars->p_ready, ph);
+            bool first = false;   // the tile whose values come next starts its item
+            RingPos vring;
+            // O (+)= P V of a tile; `first`: of its item
+            const auto values = [&](uint32_t tile, bool first) {
+                const uint32_t ph = tile & 1;
+                wait(&bars->p_full, ph);
                 if (first && item > 1) wait(&bars->o_empty, item & 1);
                 tc_fence_after();
                 const uint32_t keep = first ? 0u : 1u;
+#pragma unroll 1
                 for (int vg = 0; vg < vgroups; ++vg) {
-                    const bool two = 2 * vg + 1 < vblocks;
-                    if (by_loads) {
-                        wait_cluster(&bars->v_full[2 * vg], ph);
-                        if (two) wait_cluster(&bars->v_full[2 * vg + 1], ph);
-                    } else {
-                        wait(&bars->v_full[2 * vg], ph);
-                        if (two) wait(&bars->v_full[2 * vg + 1], ph);
-                    }
+                    const uint32_t v = vring.stage;
+                    wait(&bars->v_full[v], vring.phase);
                     tc_fence_after();
-                    const uint32_t id = idesc_bf16(128, two ? 256 : 128, false, true);
-                    const uint64_t vd = desc_add_bytes(v_desc, vg * 2 * kValueBytes);
+                    const uint32_t id = idesc_bf16(128, 2 * vg + 1 < vblocks ? 256 : 128, false, true);
+                    const uint64_t vd = desc_add_bytes(v_desc, v * 2 * kValueBytes);
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {  // 64 keys: one block of P
+                        const uint64_t pd = desc_add_bytes(p_desc, h * kBlockBytes);
+                        const uint64_t vh = desc_add_bytes(vd, h * 64 * 128);
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 32 bytes of P, 2048 of V
-                        mma_bf16_pair_elect(
-                            tmem + vg * 128,
-                            desc_add_bytes(p_desc, (k / 4) * kBlockBytes + (k % 4) * 32),
-                            vd + 128 * k, id, k > 0 ? 1u : keep);
-                    mma_commit_pair_elect(&bars->v_empty[vg], 3);
+                        for (int k = 0; k < 4; ++k)  // 16 keys: 32 bytes of P, 2048 of V
+                            mma_bf16_pair_elect(tmem + vg * 128, pd + 2 * k, vh + 128 * k, id,
+                                                (h | k) != 0 ? 1u : keep);
+                    }
+                    mma_commit_pair_elect(&bars->v_empty[v], 3);
+                    vring.next(kValueRing);
                 }
                 mma_commit_pair_elect(&bars->o_full, 3);
-                first = false;
             };
-            while (__any_sync(0xffffffffu, w.next(a))) {
-                const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
-                const int cached = __shfl_sync(0xffffffffu, w.cached_tiles() - w.kt0, 0);
-                if (g > 0) values();
-                ++item;
-                wait(&bars->q_full, (item - 1) & 1);
-                for (int t = 0; t < tiles; ++t) {
+            int tiles = 0, t = 0;
+            while (true) {
+                const bool next_item = t == tiles;
+                if (!next_item) {
                     const uint32_t d = tmem + kScoreCol + (g & 1) * 64;
-                    for (int kg = 0; kg < kgroups; ++kg) {
-                        if (SRC == kTma) wait(&bars->k_full[kg], g & 1);
-                        else wait_cluster(&bars->k_full[kg], g & 1);
-                        tc_fence_after();
+                    // Rolled loops without branches: unrolled or with the choice of the A operand
+                    // inside, the same MMAs took 10 to 65 % longer to issue.
+                    wait(&bars->k_full[0], g & 1);
+                    tc_fence_after();
+                    const int first_blocks = min(kblocks, kQueryBlocks);
+#pragma unroll 1
+                    for (int kb = 0; kb < first_blocks; ++kb) {
+                        const uint64_t kd = desc_add_bytes(k_desc, kb * kBlockBytes);
+                        const uint32_t qt = tmem + kQueryCol + kb * 32;
 #pragma unroll
-                        for (int i = 0; i < kGroup; ++i) {
-                            if (kg * kGroup + i >= kblocks) break;
-                            const uint64_t qd = desc_add_bytes(q_desc, (kg * kGroup + i) * kBlockBytes);
-                            const uint64_t kd = desc_add_bytes(k_desc, (kg * kGroup + i) * kBlockBytes);
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_pair_ts_elect(d, qt + k * 8, kd + 2 * k, id_s,
+                                                   (kb | k) != 0 ? 1u : 0u);
+                    }
+                    mma_commit_pair_elect(&bars->k_empty[0], 3);
+                    if (kblocks > kQueryBlocks) {
+                        wait(&bars->k_full[1], g & 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int kb = kQueryBlocks; kb < kblocks; ++kb) {
+                            const uint64_t kd = desc_add_bytes(k_desc, kb * kBlockBytes);
+                            const uint64_t qd = desc_add_bytes(q_desc, (kb - kQueryBlocks) * kBlockBytes);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_bf16_pair_elect(d, qd + 2 * k, kd + 2 * k, id_s,
-                                                    (kg | i | k) != 0 ? 1u : 0u);
+                                mma_bf16_pair_elect(d, qd + 2 * k, kd + 2 * k, id_s, 1u);
                         }
-                        mma_commit_pair_elect(&bars->k_empty[kg], 3);
+                        mma_commit_pair_elect(&bars->k_empty[1], 3);
                     }
                     mma_commit_pair_elect(&bars->s_full[g & 1], 3);
                     if (t + 1 == tiles) mma_commit_pair_elect(&bars->q_empty, 3);
-                    if (t > 0) values();
-                    else first = true;
-                    by_loads = SRC != kTma || t >= cached;
                     ++g;
-                    t0 = globaltimer_ns();
-                    if (__any_sync(0xffffffffu, failed)) break;
+                    ++t;
                 }
+                // The values of the tile before, behind this tile's scores; those of an item's
+                // last tile before the next item's queries are waited for.
+                if (next_item ? g > 0 : t > 1) {
+                    values(next_item ? g - 1 : g - 2, first);
+                    first = false;
+                }
+                if (!next_item && t == 1) first = true;
                 if (__any_sync(0xffffffffu, failed)) break;
+                if (next_item) {
+                    if (!__any_sync(0xffffffffu, w.next(a))) break;
+                    tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
+                    t = 0;
+                    ++item;
+                    wait(&bars->q_full, (item - 1) & 1);
+                }
             }
-            if (g > 0 && !__any_sync(0xffffffffu, failed)) values();
             mma_commit_pair_elect(&bars->mma_done, 1);
             mbar_wait_inl(&bars->mma_done, 0, wc, false);
         }
-      } else if (warp == kRelayWarp) {
-        // The weights of both CTAs are waited for here, at cluster scope: a satisfied wait of
-        // that scope takes several hundred cycles, which the MMA warp does not have.
-        if (leader)
-            for (int g = 0; g < bars->share; ++g) {
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster_inl(&bars->p_full, g & 1, wc))) break;
-                if (lane == 0) mbar_arrive(&bars->p_ready);
-            }
       } else if (warp == kQueryWarp) {
-        // ---------------- queries: this CTA's 64 rows of each item ----------------
+        // ---------------- queries: this CTA's 64 rows of each item, the later blocks --------
         Walk w(a, bars);
         const uint32_t q_full = mapa_shared(smem_u32(&bars->q_full), 0);
         uint32_t item = 0;
         bool ok = true;
         while (ok && w.next(a)) {
-            const int go = lane == 0 ? mbar_wait_inl(&bars->q_empty, (item & 1) ^ 1, wc) : 1;
-            ok = __shfl_sync(0xffffffffu, go, 0);
+            ok = warp_wait(&bars->q_empty, (item & 1) ^ 1, wc);
             if (!ok) break;
             const int64_t row = w.r.first * a.num_heads + static_cast<int64_t>(w.item) * 128 + rank * 64;
+            const int blocks = max(kblocks - kQueryBlocks, 0);
             if (leader && lane == 0)
-                mbar_arrive_expect_tx(&bars->q_full, 2 * kblocks * kBlockBytes);
-            if (lane < kblocks)
-                tma_load_2d_pair(sQ + lane * kBlockBytes, &tm_q, q_full, lane * 64,
-                                 static_cast<int32_t>(row));
+                mbar_arrive_expect_tx(&bars->q_full, 2 * blocks * kBlockBytes);
+            if (lane < blocks)
+                tma_load_2d_pair(sQ + lane * kBlockBytes, &tm_q, q_full,
+                                 (kQueryBlocks + lane) * 64, static_cast<int32_t>(row));
             ++item;
         }
         if (!ok && lane == 0) {  // let the loads in flight land before the CTA retires
@@ -727,53 +755,119 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Walk w(a, bars);
         const bool keys = warp < kValueWarp;
         const int i = (warp - kKeyWarp) & 3;
-        const int blocks = keys ? kblocks : min(vblocks, i + 1);
         const int rows = keys ? 64 : kKeys;
-        const int slots = keys ? box : vbox;       // of one page in a TMA box
+        const int slots = keys ? tb.key_slots : tb.value_slots;
+        const int wide = SRC != kTma ? 1 : keys ? tb.key_blocks : tb.value_blocks;
         const int boxes = SRC == kTma ? rows / slots : 1;
         const uint32_t bytes = static_cast<uint32_t>(rows) * 128;
-        uint8_t* base = keys ? sK : sV;
         uint64_t* full = keys ? bars->k_full : bars->v_full;
         uint64_t* empty = keys ? bars->k_empty : bars->v_empty;
         const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+        const uint32_t q_full = mapa_shared(smem_u32(&bars->q_full), 0);
         const int col0 = keys ? 0 : static_cast<int>(rank) * vblocks * 64;
-        const CUtensorMap* map = keys ? &tm_c : &tm_v;
-        // by TMA a key warp brings a whole group
-        const int from = keys ? i * kGroup : i;
-        const int to = keys ? min(kblocks, from + kGroup) : blocks;
-        uint32_t g = 0, issued = 0;                // issued: tiles brought by TMA
+        const CUtensorMap* map = !keys ? &tm_v : i == 0 ? &tm_k0 : &tm_k1;
+        // Key warp i brings blocks i, i + 4 and i + 8, or, by boxes of whole groups, group i;
+        // value warp i brings block i, half of group i / 2 (a block past the CTA's last is
+        // only signalled), or the even one both.
+        const bool idle = keys ? wide > 1 && (i > 1 || (i == 1 && kblocks <= kQueryBlocks))
+                               : i >= 2 * vgroups;
+        RingPos ring;                              // values: the group's place
+        if (!keys && i >= 2) ring.next(kValueRing);
+        uint32_t g = 0, issued = 0, item = 0;      // issued: tiles brought by TMA
+        uint32_t last_group = 0, last_phase = 0;
         bool ok = true;
         while (ok && __any_sync(0xffffffffu, w.next(a))) {
             const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
             const int cached = __shfl_sync(0xffffffffu, w.cached_tiles() - w.kt0, 0);
-            for (int t = 0; ok && t < tiles; ++t, ++g) {
+            if (!keys) {
+                // the first query blocks go to tensor memory: lanes 32 i .. 32 i + 31
+                ok = warp_wait(&bars->q_empty, (item & 1) ^ 1, wc);
+                if (!ok) break;
+                tc_fence_after();
+                const int64_t row = w.r.first * a.num_heads + static_cast<int64_t>(w.item) * 128 +
+                                    rank * 64 + (i & 1) * 32 + lane;
+                const uint16_t* q = a.q + row * a.cols;
+                const bool have = row < static_cast<int64_t>(a.total_rows) * a.num_heads;
+                for (int kb = 0; kb < min(kblocks, kQueryBlocks); ++kb) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int c = kb * 64 + k * 8;
+                        const uint4 v = have && c < a.cols ? ld_nc_v4(q + c) : make_uint4(0u, 0u, 0u, 0u);
+                        x[4 * k] = v.x;
+                        x[4 * k + 1] = v.y;
+                        x[4 * k + 2] = v.z;
+                        x[4 * k + 3] = v.w;
+                    }
+                    tmem_st_x32(tmem + (static_cast<uint32_t>(i * 32) << 16) + kQueryCol + kb * 32, x);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(q_full);
+                ++item;
+            }
+            for (int t = 0; ok && !idle && t < tiles; ++t, ++g) {
                 const int32_t kt = w.kt0 + t;
                 const int64_t pos0 = static_cast<int64_t>(kt) * kKeys + (keys ? rank * 64 : 0u);
                 // Drafts that some query does not attend must not turn its zero weights into
                 // NaN: as values their infinities and NaN become zero, which takes a pass
                 // through registers.  (A query that attends such a draft has it in its scores.)
+                const uint32_t slot = ring.stage;              // of the value group
+                const uint32_t phase = keys ? g & 1 : ring.phase;
+                uint8_t* dst = keys ? sK : sV + slot * 2 * kValueBytes + (i & 1) * kValueBytes;
+                if (!keys)
+                    for (int v = 0; v < vgroups; ++v) ring.next(kValueRing);
                 if (SRC == kTma && (keys || t < cached)) {
-                    if (from >= to) continue;
                     const Place at(a, w.b, lane < boxes ? pos0 + lane * slots : w.r.kv, w.r.kv);
-                    ok = __all_sync(0xffffffffu, mbar_wait_inl(&empty[keys ? i : i >> 1],
-                                                               (g & 1) ^ 1, wc));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        if (leader) mbar_arrive_expect_tx(&full[i], 2 * (to - from) * bytes);
-                        else if (!keys) mbar_arrive_remote(full0 + i * 8);
+                    // A box brings a whole group, or one block: a load takes the TMA unit about
+                    // 130 cycles and 0.8 for each of its 128-byte rows, so few wide ones are
+                    // better.
+                    if (wide > 1) {
+                        const uint32_t group = keys ? i : slot;
+                        const int brings = keys ? (i == 0 ? kTreeKeyBlocks : kTreeLastKeyBlocks)
+                                                : (i & 1) ? 0 : kTreeValueBlocks;
+                        const int blk = keys ? i * kTreeKeyBlocks : i;
+                        ok = warp_wait(&empty[group], phase ^ 1, wc);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            if (leader) mbar_arrive_expect_tx(&full[group], 2 * brings * bytes);
+                            else if (!keys) mbar_arrive_remote(full0 + group * 8);
+                        }
+                        if (brings > 0)
+                            tma_load_4d_pair_elect(dst + (keys ? blk * bytes : 0), map,
+                                                   full0 + group * 8, 0,
+                                                   __shfl_sync(0xffffffffu, at.slot, 0),
+                                                   __shfl_sync(0xffffffffu, at.page, 0),
+                                                   col0 / 64 + blk);
+                        last_group = group;
+                    } else {
+                        for (int blk = i; blk < (keys ? kblocks : i + 1); blk += 4) {
+                            const uint32_t group = !keys ? slot : blk < kQueryBlocks ? 0 : 1;
+                            const bool brings = keys || blk < vblocks;
+                            ok = warp_wait(&empty[group], phase ^ 1, wc);
+                            if (!ok) break;
+                            if (lane == 0) {
+                                if (leader) mbar_arrive_expect_tx(&full[group], brings ? 2 * bytes : 0);
+                                else if (!keys) mbar_arrive_remote(full0 + group * 8);
+                            }
+                            for (int x = 0; brings && x < boxes; ++x)
+                                tma_load_4d_pair_elect(dst + (keys ? blk * bytes : 0) + x * slots * 128,
+                                                       map, full0 + group * 8, col0 + blk * 64,
+                                                       __shfl_sync(0xffffffffu, at.slot, x),
+                                                       __shfl_sync(0xffffffffu, at.page, x), 0);
+                            last_group = group;
+                        }
+                        if (!ok) break;
                     }
-                    for (int blk = from; blk < to; ++blk)
-                        for (int x = 0; x < boxes; ++x)
-                            tma_load_3d_pair_elect(base + blk * bytes + x * slots * 128, map,
-                                                   full0 + i * 8, col0 + blk * 64,
-                                                   __shfl_sync(0xffffffffu, at.slot, x),
-                                                   __shfl_sync(0xffffffffu, at.page, x));
                     issued = g + 1;
+                    last_phase = phase;
                     continue;
                 }
                 // By loads: four lanes take a row's 64 columns, 16 each; eight rows at a time.
                 const int sub = lane >> 2, part = lane & 3;
-                for (int blk = i; blk < blocks; blk += 4) {
+                for (int blk = i; blk < (keys ? kblocks : i + 1); blk += 4) {
+                    const uint32_t group = !keys ? slot : blk < kQueryBlocks ? 0 : 1;
                     const int c = col0 + blk * 64 + part * 16;
                     const int64_t mine[2] = {
                         Place(a, w.b, pos0 + lane, w.r.kv).offset(a),
@@ -790,29 +884,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             x[k].load(a, __shfl_sync(0xffffffffu, from, (k & 3) * 8 + sub), c);
                         }
                         if (!waited) {
-                            const int go = lane == 0 ? mbar_wait_inl(&empty[keys ? blk / kGroup : blk >> 1],
-                                                                     (g & 1) ^ 1, wc)
-                                                     : 1;
-                            ok = __shfl_sync(0xffffffffu, go, 0);
+                            ok = warp_wait(&empty[group], phase ^ 1, wc);
                             if (!ok) break;
                             waited = true;
                         }
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int key = r0 + k * 8 + sub;
-                            x[k].store(a, c, smem_u32(base + blk * bytes) + key * 128, key, part * 2,
+                            x[k].store(a, c, smem_u32(dst + (keys ? blk * bytes : 0)) + key * 128, key, part * 2,
                                        !keys && pos0 + key >= w.r.len);
                         }
                     }
                     if (!ok) break;
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(full0 + (keys ? blk / kGroup : blk) * 8);
+                    if (lane == 0) mbar_arrive_remote(full0 + group * 8);
                 }
             }
         }
         if (!ok && issued > 0 && lane == 0) {  // let the loads in flight land
-            if (leader) mbar_wait_inl(&full[i], (issued - 1) & 1, wc, false);
+            if (leader) mbar_wait_inl(&full[last_group], last_phase, wc, false);
             if (!leader) spin_ns(50000);
         }
     }
@@ -824,126 +915,148 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
 
 // Joins the parts of the items that several pairs share: with M the largest of the parts'
-// maxima, out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same
-// order.  A block takes rows one after the other; groups of R / 4 threads take a share of
-// the parts each, 16 bytes a thread, and meet in shared memory.
+// maxima, out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k.  A lane has a row and 32 of its
+// columns; the parts of a task are dealt to 2, 4 or 8 warps, which meet in shared memory, always
+// in the same order, and then each finish a share of the columns.
 __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const TreeAttentionArgs a, const TreeWorkspace ws, const int pairs) {
     __shared__ TreeItem items[kTreeMaxPairs];
-    __shared__ int ends[kTreeMaxPairs];  // rows of all items up to and including this one
+    __shared__ int tasks_at[kTreeMaxPairs];
     __shared__ int which;
-    __shared__ float weight[kTreeMaxPairs];
-    __shared__ float4 sums[kJoinThreads];
+    __shared__ float sums[kJoinWarps][32][32], tops[kJoinWarps][32], totals[kJoinWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int R = a.kv_lora_rank, col_groups = R / 32;
+    const auto split = [](int parts) { return parts <= 2 ? 2 : parts <= 4 ? 4 : 8; };
+    const auto tasks_of = [&](const TreeItem& it) {
+        const int wide = kJoinWarps / split(it.parts);  // column groups a block takes at once
+        return (it.rows + 31) / 32 * ((col_groups + wide - 1) / wide);
+    };
     griddep_wait();
-    const TreeItem* held = reinterpret_cast<const TreeItem*>(a.workspace + ws.items);
-    for (int p = threadIdx.x; p < pairs; p += kJoinThreads) items[p] = held[p];
+    if (threadIdx.x < pairs)
+        items[threadIdx.x] = reinterpret_cast<const TreeItem*>(a.workspace + ws.items)[threadIdx.x];
     __syncthreads();
-    int end = 0;
-    if (threadIdx.x < pairs) {
-        for (int p = 0; p <= static_cast<int>(threadIdx.x); ++p) end += items[p].rows;
-        ends[threadIdx.x] = end;
+    if (threadIdx.x < pairs) tasks_at[threadIdx.x] = tasks_of(items[threadIdx.x]);
+    __syncthreads();
+    int begin = 0, end = 0, tasks = 0;  // tasks of the item of this thread's index; of all
+    for (int p = 0; p < pairs; ++p) {
+        if (p == static_cast<int>(threadIdx.x)) {
+            begin = tasks;
+            end = tasks + tasks_at[p];
+        }
+        tasks += tasks_at[p];
     }
-    __syncthreads();
-    const int total_rows = ends[pairs - 1];
-    const int R = a.kv_lora_rank, quads = R / 4;
-    const int groups = kJoinThreads / quads;
-    const int quad = threadIdx.x % quads, grp = threadIdx.x / quads;
+    __shared__ int first_task;
     const float2* stats = reinterpret_cast<const float2*>(a.workspace + ws.stats);
     const float4* parts = reinterpret_cast<const float4*>(a.workspace + ws.parts);
-    for (int f = blockIdx.x; f < total_rows; f += gridDim.x) {
-            if (threadIdx.x < pairs && f < end && f >= end - items[threadIdx.x].rows)
-                which = threadIdx.x;
-            __syncthreads();
-            const int p = which;
-            const TreeItem it = items[p];
-            const int row = f - (ends[p] - it.rows);
-            // part k of the item: the pair's second slot, then the first slots behind it
-            const auto slot = [&](int k) -> int64_t {
-                return (static_cast<int64_t>(2) * (p + k) + (k == 0 ? 1 : 0)) * ws.rows + row;
-            };
-            if (threadIdx.x < 32) {
-                float top = -INFINITY;
-                for (int k = threadIdx.x; k < it.parts; k += 32) top = fmaxf(top, stats[slot(k)].x);
+    for (int f = blockIdx.x; f < tasks; f += gridDim.x) {
+        if (begin <= f && f < end) {
+            which = threadIdx.x;
+            first_task = begin;
+        }
+        __syncthreads();
+        const int p = which;
+        const TreeItem it = items[p];
+        const int task = f - first_task;
+        const int row_groups = (it.rows + 31) / 32;
+        const int ways = split(it.parts);
+        const int way = warp & (ways - 1);
+        const int cg = task / row_groups * (kJoinWarps / ways) + warp / ways;
+        const int row = task % row_groups * 32 + lane;
+        const bool live = row < it.rows && cg < col_groups;
+        float top = -INFINITY, total = 0.0f;
+        float o[32] = {};
+        if (live)
+            for (int k = way; k < it.parts; k += ways) {
+                // part k: the pair's second slot, then the first slots of the pairs behind it
+                const int64_t slot = 2 * static_cast<int64_t>(p + k) + (k == 0 ? 1 : 0);
+                const float4* from = parts + (slot * (R / 4) + cg * 8) * ws.rows + row;
+                const float2 s = stats[slot * ws.rows + row];
+                float4 v[8];
 #pragma unroll
-                for (int sh = 16; sh >= 1; sh >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
-                float total = 0.0f;
-                for (int k = threadIdx.x; k < it.parts; k += 32) {
-                    const float2 s = stats[slot(k)];
-                    const float f = s.x == -INFINITY ? 0.0f : exp2f(s.x - top);
-                    weight[k] = f;
-                    total += f * s.y;
-                }
+                for (int i = 0; i < 8; ++i) v[i] = __ldcg(from + static_cast<int64_t>(i) * ws.rows);
+                const float m = fmaxf(top, s.x);
+                const float f0 = top == -INFINITY ? 0.0f : exp2f(top - m);
+                const float f1 = s.x == -INFINITY ? 0.0f : exp2f(s.x - m);
+                top = m;
+                total = total * f0 + s.y * f1;
 #pragma unroll
-                for (int sh = 16; sh >= 1; sh >>= 1)
-                    total += __shfl_xor_sync(0xffffffffu, total, sh);
-                __syncwarp();
-                const float inv = total != 0.0f ? 1.0f / total : 0.0f;
-                for (int k = threadIdx.x; k < it.parts; k += 32) weight[k] *= inv;
-                if (threadIdx.x == 0 && a.lse != nullptr)
-                    a.lse[it.first + row] = total != 0.0f ? top * kLn2 + logf(total) : -INFINITY;
-            }
-            __syncthreads();
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (grp < groups) {
-#pragma unroll 4
-                for (int k = grp; k < it.parts; k += groups) {
-                    const float f = weight[k];
-                    const float4 v = parts[slot(k) * quads + quad];
-                    o.x = fmaf(f, v.x, o.x);
-                    o.y = fmaf(f, v.y, o.y);
-                    o.z = fmaf(f, v.z, o.z);
-                    o.w = fmaf(f, v.w, o.w);
+                for (int i = 0; i < 8; ++i) {
+                    o[4 * i] = o[4 * i] * f0 + v[i].x * f1;
+                    o[4 * i + 1] = o[4 * i + 1] * f0 + v[i].y * f1;
+                    o[4 * i + 2] = o[4 * i + 2] * f0 + v[i].z * f1;
+                    o[4 * i + 3] = o[4 * i + 3] * f0 + v[i].w * f1;
                 }
             }
-            sums[threadIdx.x] = o;
-            __syncthreads();
-            if (grp == 0) {
-                for (int i = 1; i < groups; ++i) {
-                    const float4 v = sums[i * quads + quad];
-                    o.x += v.x;
-                    o.y += v.y;
-                    o.z += v.z;
-                    o.w += v.w;
+        tops[warp][lane] = top;
+        totals[warp][lane] = total;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sums[warp][i][lane] = o[i];
+        __syncthreads();
+        if (live) {
+            const int w0 = warp - way;
+            float m = -INFINITY;
+            for (int k = 0; k < ways; ++k) m = fmaxf(m, tops[w0 + k][lane]);
+            float f[kJoinWarps], sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) {
+                f[k] = 0.0f;
+                if (k < ways) {
+                    const float t = tops[w0 + k][lane];
+                    f[k] = t == -INFINITY ? 0.0f : exp2f(t - m);
+                    sum += totals[w0 + k][lane] * f[k];
                 }
-                *reinterpret_cast<uint2*>(a.out + (it.first + row) * R + quad * 4) =
-                    make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
             }
-            __syncthreads();
+            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+            const int each = 32 / ways;  // columns
+            uint16_t* out = a.out + (it.first + row) * R + cg * 32 + way * each;
+            for (int c = 0; c < each; c += 4) {
+                float x[4] = {};
+#pragma unroll
+                for (int k = 0; k < kJoinWarps; ++k)
+                    if (k < ways)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] += sums[w0 + k][way * each + c + e][lane] * f[k];
+                *reinterpret_cast<uint2*>(out + c) = make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv),
+                                                                pack_bf16x2(x[2] * inv, x[3] * inv));
+            }
+            if (a.lse != nullptr && cg == 0 && way == 0)
+                a.lse[it.first + row] = sum != 0.0f ? m * kLn2 + logf(sum) : -INFINITY;
+        }
+        __syncthreads();
     }
 }
 
 template <Source SRC>
-cudaError_t launch_source(const CUtensorMap& tm_q, const CUtensorMap& tm_c,
+cudaError_t launch_source(const CUtensorMap& tm_q, const CUtensorMap& tm_k0, const CUtensorMap& tm_k1,
                           const CUtensorMap& tm_v, const TreeAttentionArgs& args,
-                          const TreeWorkspace& ws, int box, int vbox, int pairs,
+                          const TreeWorkspace& ws, const TreeBoxes& boxes, int pairs,
                           cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<SRC>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
     tree_attention_kernel<SRC><<<static_cast<unsigned>(2 * pairs), kThreads, kSmemBytes, stream>>>(
-        tm_q, tm_c, tm_v, args, ws, box, vbox);
+        tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_c,
-                                  const CUtensorMap& tm_v, TreeAttentionArgs args, int box,
-                                  int vbox, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k0, const CUtensorMap& tm_k1,
+                                  const CUtensorMap& tm_v, TreeAttentionArgs args, TreeBoxes boxes,
+                                  int num_sms, cudaStream_t stream) {
     const TreeWorkspace ws = tree_workspace(args.total_rows, args.num_heads, args.kv_lora_rank);
     const int pairs = num_sms / 2 < kTreeMaxPairs ? num_sms / 2 : kTreeMaxPairs;
     const cudaError_t e =
         args.qcache_layer != nullptr
-            ? launch_source<kCodes>(tm_q, tm_c, tm_v, args, ws, box, vbox, pairs, stream)
-        : box >= 8 ? launch_source<kTma>(tm_q, tm_c, tm_v, args, ws, box, vbox, pairs, stream)
-                   : launch_source<kRows>(tm_q, tm_c, tm_v, args, ws, box, vbox, pairs, stream);
+            ? launch_source<kCodes>(tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes, pairs, stream)
+        : boxes.key_slots >= 8 ? launch_source<kTma>(tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes, pairs, stream)
+                   : launch_source<kRows>(tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes, pairs, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(tree_join_kernel, static_cast<unsigned>(num_sms) * 2, kJoinThreads, 0,
+    return launch_dependent(tree_join_kernel, static_cast<unsigned>(num_sms) * 4, kJoinThreads, 0,
                             stream, args, ws, pairs);
 }
 
