@@ -333,6 +333,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, mbar_wait_inl(bar, parity, wc));
 }
 
+// The wait of the issuing warps: a bare loop, limited by its tries (one suspends the thread for
+// about 4 us when the phase is not complete), false when they run out.  Their issue loops are
+// fast only while the compiler sees that the warp stays together: with mbar_wait's exits in
+// the loop, the scores' MMAs took 50 cycles each instead of 30 and a tile 4350 instead of 2400.
+__device__ __forceinline__ bool plain_wait(uint64_t* bar, uint32_t parity, uint32_t tries) {
+    uint32_t n = 0;
+    for (; n < tries && !mbar_try_wait(bar, parity); ++n) {
+    }
+    return n < tries;
+}
+
+// Records a wait that ran out and ends the CTA's other waits.
+__device__ __forceinline__ void gave_up(const WaitCtl& wc) {
+    report(wc.status, PKM_ERR_TIMEOUT);
+    *wc.abort_flag = 1;
+}
+
 template <Source SRC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -405,7 +422,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const WaitCtl wc{&bars->abort_flag, a.status, a.timeout_ns};
+    // between 10 ms and 4 s for the default limit of a second
+    const uint32_t tries = static_cast<uint32_t>(min(a.timeout_ns / 1000, uint64_t{1} << 30));
     const int64_t sharing = min(pairs, bars->units);  // pairs with a share
+    const auto issue_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool ok = __all_sync(0xffffffffu, plain_wait(bar, parity, tries));
+        if (!ok) gave_up(wc);
+        return ok;
+    };
 
     if (warp < kSoftWarps) {
         // ---------------- softmax and epilogue: row = lane of the CTA's 64 ----------------
@@ -610,27 +634,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------- MMA issuer (even CTA), all lanes together ----------------
         if (leader) {
             Walk w(a, bars);
-            // Waits that keep the loop's control flow uniform: a lane that gives up (as
-            // mbar_wait does) leaves the loop like the others, and the warp looks at `failed`
-            // once a tile.  What it issues until then is not used.
+            // A wait that runs out is looked at once a tile; what is issued until then is not used.
             bool failed = false;
-            const auto give_up = [&](uint64_t& since) {
-                if (*wc.abort_flag) return true;
-                const uint64_t now = globaltimer_ns();
-                if (since == 0) since = now;
-                if (now - since <= a.timeout_ns) return false;
-                report(a.status, PKM_ERR_TIMEOUT);
-                *wc.abort_flag = 1;
-                return true;
-            };
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                uint32_t n = 0;
-                uint64_t since = 0;
-                while (!mbar_try_wait(bar, parity))
-                    if ((++n & 127u) == 0 && (failed || give_up(since))) {
-                        failed = true;
-                        break;
-                    }
+                failed |= !plain_wait(bar, parity, tries);
             };
             const uint32_t id_s = idesc_bf16(128, kKeys, false, false);
             const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
@@ -713,7 +720,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     first = false;
                 }
                 if (!next_item && t == 1) first = true;
-                if (__any_sync(0xffffffffu, failed)) break;
+                if (__any_sync(0xffffffffu, failed)) {
+                    gave_up(wc);
+                    break;
+                }
                 if (next_item) {
                     if (!__any_sync(0xffffffffu, w.next(a))) break;
                     tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
@@ -732,7 +742,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t item = 0;
         bool ok = true;
         while (ok && w.next(a)) {
-            ok = warp_wait(&bars->q_empty, (item & 1) ^ 1, wc);
+            ok = issue_wait(&bars->q_empty, (item & 1) ^ 1);
             if (!ok) break;
             const int64_t row = w.r.first * a.num_heads + static_cast<int64_t>(w.item) * 128 + rank * 64;
             const int blocks = max(kblocks - kQueryBlocks, 0);
@@ -781,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int cached = __shfl_sync(0xffffffffu, w.cached_tiles() - w.kt0, 0);
             if (!keys) {
                 // the first query blocks go to tensor memory: lanes 32 i .. 32 i + 31
-                ok = warp_wait(&bars->q_empty, (item & 1) ^ 1, wc);
+                ok = issue_wait(&bars->q_empty, (item & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
                 const int64_t row = w.r.first * a.num_heads + static_cast<int64_t>(w.item) * 128 +
@@ -828,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int brings = keys ? (i == 0 ? kTreeKeyBlocks : kTreeLastKeyBlocks)
                                                 : (i & 1) ? 0 : kTreeValueBlocks;
                         const int blk = keys ? i * kTreeKeyBlocks : i;
-                        ok = warp_wait(&empty[group], phase ^ 1, wc);
+                        ok = issue_wait(&empty[group], phase ^ 1);
                         if (!ok) break;
                         if (lane == 0) {
                             if (leader) mbar_arrive_expect_tx(&full[group], 2 * brings * bytes);
@@ -845,7 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int blk = i; blk < (keys ? kblocks : i + 1); blk += 4) {
                             const uint32_t group = !keys ? slot : blk < kQueryBlocks ? 0 : 1;
                             const bool brings = keys || blk < vblocks;
-                            ok = warp_wait(&empty[group], phase ^ 1, wc);
+                            ok = issue_wait(&empty[group], phase ^ 1);
                             if (!ok) break;
                             if (lane == 0) {
                                 if (leader) mbar_arrive_expect_tx(&full[group], brings ? 2 * bytes : 0);
@@ -884,7 +894,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             x[k].load(a, __shfl_sync(0xffffffffu, from, (k & 3) * 8 + sub), c);
                         }
                         if (!waited) {
-                            ok = warp_wait(&empty[group], phase ^ 1, wc);
+                            ok = issue_wait(&empty[group], phase ^ 1);
                             if (!ok) break;
                             waited = true;
                         }
