@@ -215,9 +215,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
     return ok != 0;
 }
 
-// Slow path of the cluster-scope waits (mbar_wait_spin with the cluster-scope test).
-__device__ __forceinline__ bool mbar_wait_cluster_spin(uint64_t* bar, uint32_t parity,
-                                                       const WaitCtl& w, bool obey_abort) {
+// mbar_wait with acquire at cluster scope, for a barrier whose completion publishes ordinary
+// (generic-proxy) shared-memory writes made by threads of the other CTA of the pair.  Same
+// limits and abort behaviour as mbar_wait.
+static __device__ __noinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                      const WaitCtl& w, bool obey_abort = true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait_cluster(bar, parity)) return true;
@@ -230,22 +233,6 @@ __device__ __forceinline__ bool mbar_wait_cluster_spin(uint64_t* bar, uint32_t p
             }
         }
     }
-}
-
-// mbar_wait with acquire at cluster scope, for a barrier whose completion publishes ordinary
-// (generic-proxy) shared-memory writes made by threads of the other CTA of the pair.  Same
-// limits and abort behaviour as mbar_wait.
-static __device__ __noinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                      const WaitCtl& w, bool obey_abort = true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    return mbar_wait_cluster_spin(bar, parity, w, obey_abort);
-}
-
-// mbar_wait_cluster inlined (see mbar_wait_inl).
-__device__ __forceinline__ bool mbar_wait_cluster_inl(uint64_t* bar, uint32_t parity,
-                                                      const WaitCtl& w, bool obey_abort = true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    return mbar_wait_cluster_spin(bar, parity, w, obey_abort);
 }
 
 // All threads of every CTA in the cluster (release / acquire).
@@ -298,12 +285,9 @@ __device__ __forceinline__ void bulk_load_1d(void* dst, const void* src, uint32_
         : "memory");
 }
 
-// Fetches `bytes` contiguous bytes (16-byte aligned, a multiple of 16) into L2.
-__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                     reinterpret_cast<uint64_t>(src)),
-                 "r"(bytes)
-                 : "memory");
+// Fetches the 128-byte line at p into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -382,6 +366,20 @@ __device__ __forceinline__ void tma_load_4d_pair_elect(void* dst, const CUtensor
         "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         ".cta_group::2 [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2),
+        "r"(c3)
+        : "memory");
+}
+
+// The same into this CTA alone, completing on its own mbarrier.
+__device__ __forceinline__ void tma_load_4d_elect(void* dst, const CUtensorMap* map,
+                                                  uint64_t* bar, int32_t c0, int32_t c1,
+                                                  int32_t c2, int32_t c3) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
         "r"(c3)
         : "memory");
 }

@@ -40,7 +40,7 @@
 namespace pkm {
 namespace {
 
-constexpr int kSoftWarps = 4, kMmaWarp = 4, kQueryWarp = 5, kKeyWarp = 8, kValueWarp = 12;
+constexpr int kSoftWarps = 4, kMmaWarp = 4, kQueryWarp = 5, kFetchWarp = 6, kKeyWarp = 8, kValueWarp = 12;
 constexpr int kThreads = 16 * 32;
 constexpr int kSoftRegs = 192, kIssueRegs = 64;  // with 128 for each loader: 4 x 128 in all
 constexpr int kKeys = 128;          // keys of a tile (64 loaded by each CTA as keys)
@@ -53,39 +53,11 @@ constexpr int kValueRing = 3;       // groups of two value blocks in flight
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScoreCol = 256; // TMEM column of the first score tile
 constexpr uint32_t kQueryCol = 384; // TMEM column of the queries, 32 a block
+constexpr uint64_t kDrainNs = 1000000;  // a role that gave up leaves its loads time to land
 constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 enum Source { kTma, kRows, kCodes };  // pages by TMA, bf16 rows by loads, quantised rows
-
-struct Bars {
-    uint64_t k_full[kKeyGroups];   // even CTA: a group of blocks of both CTAs' keys is there
-    uint64_t k_empty[kKeyGroups];  // both: its MMAs are done
-    uint64_t v_full[kValueRing];   // even CTA: a group of both CTAs' value blocks is there
-    uint64_t v_empty[kValueRing];  // both: its MMAs are done
-    uint64_t q_full, q_empty;   // the item's query rows
-    uint64_t s_full[2];         // both: a score tile is complete
-    uint64_t p_full;            // even CTA: both CTAs' weights are written
-    uint64_t o_full;            // both: the tile's weights are used up and O is current
-    uint64_t o_empty;           // even CTA: both CTAs' epilogues have read O
-    uint64_t mma_done;
-    int64_t units;              // tiles of all items
-    int64_t first_unit;         // this pair's share begins here
-    int32_t share;              // and has so many tiles
-    int32_t request, item, tile;  // its first tile
-    uint32_t tmem_base;
-    int abort_flag;
-};
-
-constexpr size_t kOffQ = 0;
-constexpr size_t kOffK = kOffQ + size_t(kBlocks - kQueryBlocks) * kBlockBytes;
-constexpr size_t kOffV = kOffK + size_t(kBlocks) * kBlockBytes;
-constexpr size_t kOffP = kOffV + size_t(kValueRing) * 2 * kValueBytes;
-constexpr size_t kOffMax = kOffP + 2 * size_t(kBlockBytes);
-constexpr size_t kOffSum = kOffMax + 2 * 128 * sizeof(float);
-constexpr size_t kOffBars = kOffSum + 128 * sizeof(float);
-constexpr size_t kSmemBytes = kOffBars + sizeof(Bars) + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103a CTA");
 
 // a / b; the 64-bit division is a long routine, and the operands are hardly ever that large.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -118,6 +90,38 @@ struct Request {
     }
 };
 
+struct Bars {
+    uint64_t k_full[kKeyGroups];   // even CTA: a group of blocks of both CTAs' keys is there
+    uint64_t k_empty[kKeyGroups];  // both: its MMAs are done
+    uint64_t v_full[kValueRing];   // even CTA: a group of both CTAs' value blocks is there
+    uint64_t v_empty[kValueRing];  // both: its MMAs are done
+    uint64_t v_own[kValueRing];    // both: values that the CTA looks through first are there
+    uint64_t q_full, q_empty;   // the item's query rows
+    uint64_t s_full[2];         // both: a score tile is complete
+    uint64_t p_full;            // even CTA: both CTAs' weights are written
+    uint64_t o_full;            // both: the tile's weights are used up and O is current
+    uint64_t o_empty;           // even CTA: both CTAs' epilogues have read O
+    uint64_t mma_done;
+    int64_t units;              // tiles of all items
+    int64_t first_unit;         // this pair's share begins here
+    int32_t share;              // and has so many tiles
+    int32_t request, item, tile;  // its first tile
+    Request first;
+    int32_t progress;           // tiles whose keys have been asked for
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+constexpr size_t kOffQ = 0;
+constexpr size_t kOffK = kOffQ + size_t(kBlocks - kQueryBlocks) * kBlockBytes;
+constexpr size_t kOffV = kOffK + size_t(kBlocks) * kBlockBytes;
+constexpr size_t kOffP = kOffV + size_t(kValueRing) * 2 * kValueBytes;
+constexpr size_t kOffMax = kOffP + 2 * size_t(kBlockBytes);
+constexpr size_t kOffSum = kOffMax + 2 * 128 * sizeof(float);
+constexpr size_t kOffBars = kOffSum + 128 * sizeof(float);
+constexpr size_t kSmemBytes = kOffBars + sizeof(Bars) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103a CTA");
+
 // A pair's share of the tiles of all items, walked item by item.  After next() returned
 // true, the part is tiles [kt0, kt1) of item `item` of request r.
 struct Walk {
@@ -127,13 +131,13 @@ struct Walk {
     Request r;
     int32_t item, kt0, kt1;
 
-    __device__ __forceinline__ Walk(const TreeAttentionArgs& a, const Bars* bars) {
+    __device__ __forceinline__ explicit Walk(const Bars* bars) {
         left = bars->share;
         b = bars->request;
         item = bars->item;
         kt0 = kt1 = bars->tile;
         u = bars->first_unit;
-        if (left > 0) r.load(a, b);
+        r = bars->first;
     }
     __device__ __forceinline__ bool next(const TreeAttentionArgs& a) {
         if (left <= 0) return false;
@@ -178,7 +182,7 @@ __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int
         if (lane >= sh) incl += o;
     }
     if (lane == 31) scratch[warp] = incl;
-    if (threadIdx.x == 0) bars->share = 0;
+    if (threadIdx.x == 0) bars->share = bars->progress = 0;
     __syncthreads();
     int64_t before = 0, total = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
@@ -197,6 +201,7 @@ __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int
                 bars->first_unit = u;
                 bars->share = static_cast<int32_t>(quotient(total * (pair + 1), pairs) - u);
                 bars->request = b;
+                bars->first = r;
                 bars->item = static_cast<int32_t>(quotient(u - at, r.tiles));
                 bars->tile = static_cast<int32_t>((u - at) - static_cast<int64_t>(bars->item) * r.tiles);
                 break;
@@ -393,6 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kValueRing; ++i) {
             mbar_init(&bars->v_full[i], 4);  // two blocks, two CTAs
             mbar_init(&bars->v_empty[i], 1);
+            mbar_init(&bars->v_own[i], tb.value_blocks > 1 ? 1 : 2);  // warps that load
         }
         for (int i = 0; i < 2; ++i) mbar_init(&bars->s_full[i], 1);
         mbar_init(&bars->q_full, 1 + 2 * 4);  // the TMA bytes, and four value warps of each CTA
@@ -434,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp < kSoftWarps) {
         // ---------------- softmax and epilogue: row = lane of the CTA's 64 ----------------
         warpgroup_reg_alloc<kSoftRegs>();
-        Walk w(a, bars);
+        Walk w(bars);
         const int half = warp >> 1;                   // which 64 keys, which half of O's columns
         const int row = (warp & 1) * 32 + lane;       // of this CTA's 64
         const float scale2 = a.scale * kLog2e;
@@ -597,16 +603,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int at = rank * 64 + row;
                 float4* part = reinterpret_cast<float4*>(a.workspace + ws.parts) +
                                (slot * (R / 4) + half * vblocks * 16) * ws.rows + at;
-                for (int v = 0; v < 2 * vblocks; ++v) {
-                    if (half * vblocks * 64 + v * 32 >= R) break;
-                    uint32_t x[32];
-                    tmem_ld_x32(tmem + tlane + v * 32, x);
-                    tmem_ld_wait();
-                    if (rr < rows_all)
+                const auto put = [&](int v, const uint32_t(&x)[32]) {
+                    if (rr >= rows_all) return;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            st_v4(part + static_cast<int64_t>(v * 8 + k) * ws.rows,
-                                  make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
+                    for (int k = 0; k < 8; ++k)
+                        st_v4(part + static_cast<int64_t>(v * 8 + k) * ws.rows,
+                              make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
+                };
+                for (int v = 0; v < 2 * vblocks; v += 2) {  // 64 columns, whole within R
+                    if (half * vblocks * 64 + v * 32 >= R) break;
+                    uint32_t x0[32], x1[32];
+                    tmem_ld_x32(tmem + tlane + v * 32, x0);
+                    tmem_ld_x32(tmem + tlane + v * 32 + 32, x1);
+                    tmem_ld_wait();
+                    put(v, x0);
+                    put(v + 1, x1);
                 }
                 if (half == 0 && rr < rows_all)
                     reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + at] =
@@ -633,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (warp == kMmaWarp) {
         // ---------------- MMA issuer (even CTA), all lanes together ----------------
         if (leader) {
-            Walk w(a, bars);
+            Walk w(bars);
             // A wait that runs out is looked at once a tile; what is issued until then is not used.
             bool failed = false;
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -735,9 +746,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mma_commit_pair_elect(&bars->mma_done, 1);
             mbar_wait_inl(&bars->mma_done, 0, wc, false);
         }
+      } else if (warp == kFetchWarp) {
+        // Asks for the keys of the tile after the next to be brought into L2: the loads
+        // proper are issued when their shared memory is free, too late to wait for DRAM.
+        Walk w(bars);
+        volatile int32_t* progress = &bars->progress;
+        const int bytes = SRC == kCodes ? R + 2 * (a.cols - R) + 4 * (R / 128) : 2 * a.cols;
+        int g = 0;
+        while (w.next(a))
+            for (int32_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
+                for (uint32_t n = 0; g - 2 > *progress && n < tries; ++n) __nanosleep(200);
+                for (int x = 0; x < 2; ++x) {
+                    const int64_t pos = static_cast<int64_t>(kt) * kKeys + rank * 64 + x * 32 + lane;
+                    const int64_t row = Place(a, w.b, pos, w.r.kv).offset(a);
+                    if (row < 0) continue;
+                    const uint8_t* from = SRC == kCodes
+                                              ? a.qcache_layer + row
+                                              : reinterpret_cast<const uint8_t*>(a.cache_layer + row);
+                    for (int c = 0; c < bytes; c += 128) prefetch_l2(from + c);
+                    prefetch_l2(from + bytes - 1);
+                }
+            }
       } else if (warp == kQueryWarp) {
         // ---------------- queries: this CTA's 64 rows of each item, the later blocks --------
-        Walk w(a, bars);
+        Walk w(bars);
         const uint32_t q_full = mapa_shared(smem_u32(&bars->q_full), 0);
         uint32_t item = 0;
         bool ok = true;
@@ -753,168 +785,255 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                  (kQueryBlocks + lane) * 64, static_cast<int32_t>(row));
             ++item;
         }
-        if (!ok && lane == 0) {  // let the loads in flight land before the CTA retires
-            if (leader && item > 0) mbar_wait_inl(&bars->q_full, (item - 1) & 1, wc, false);
-            if (!leader) spin_ns(50000);
-        }
+        if (!ok) spin_ns(kDrainNs);
       }
     } else {
         // ---------------- keys and values ----------------
-        // Keys: this CTA's 64 of each tile, all columns; warp i brings group i by TMA, or
-        // blocks i, i + 4, ... by loads.  Values: all 128 keys, this CTA's columns, block i.
-        Walk w(a, bars);
+        // Keys: this CTA's 64 of each tile, all columns, warp i bringing blocks i, i + 4 and
+        // i + 8, or by boxes of whole groups group i.  Values: all 128 keys, this CTA's
+        // columns, warp i bringing block i of its group i / 2 (past the CTA's last block it
+        // only signals), or by boxes of both blocks the even warp.
         const bool keys = warp < kValueWarp;
         const int i = (warp - kKeyWarp) & 3;
-        const int rows = keys ? 64 : kKeys;
-        const int slots = keys ? tb.key_slots : tb.value_slots;
-        const int wide = SRC != kTma ? 1 : keys ? tb.key_blocks : tb.value_blocks;
-        const int boxes = SRC == kTma ? rows / slots : 1;
-        const uint32_t bytes = static_cast<uint32_t>(rows) * 128;
-        uint64_t* full = keys ? bars->k_full : bars->v_full;
-        uint64_t* empty = keys ? bars->k_empty : bars->v_empty;
-        const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+        const uint32_t k_full = mapa_shared(smem_u32(bars->k_full), 0);
+        const uint32_t v_full = mapa_shared(smem_u32(bars->v_full), 0);
         const uint32_t q_full = mapa_shared(smem_u32(&bars->q_full), 0);
-        const int col0 = keys ? 0 : static_cast<int>(rank) * vblocks * 64;
-        const CUtensorMap* map = !keys ? &tm_v : i == 0 ? &tm_k0 : &tm_k1;
-        // Key warp i brings blocks i, i + 4 and i + 8, or, by boxes of whole groups, group i;
-        // value warp i brings block i, half of group i / 2 (a block past the CTA's last is
-        // only signalled), or the even one both.
-        const bool idle = keys ? wide > 1 && (i > 1 || (i == 1 && kblocks <= kQueryBlocks))
-                               : i >= 2 * vgroups;
-        RingPos ring;                              // values: the group's place
-        if (!keys && i >= 2) ring.next(kValueRing);
-        uint32_t g = 0, issued = 0, item = 0;      // issued: tiles brought by TMA
-        uint32_t last_group = 0, last_phase = 0;
+        const int col0 = static_cast<int>(rank) * vblocks * 64;  // first value column
+        uint32_t g = 0, item = 0;
         bool ok = true;
-        while (ok && __any_sync(0xffffffffu, w.next(a))) {
-            const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
-            const int cached = __shfl_sync(0xffffffffu, w.cached_tiles() - w.kt0, 0);
-            if (!keys) {
-                // the first query blocks go to tensor memory: lanes 32 i .. 32 i + 31
-                ok = issue_wait(&bars->q_empty, (item & 1) ^ 1);
-                if (!ok) break;
-                tc_fence_after();
-                const int64_t row = w.r.first * a.num_heads + static_cast<int64_t>(w.item) * 128 +
-                                    rank * 64 + (i & 1) * 32 + lane;
-                const uint16_t* q = a.q + row * a.cols;
-                const bool have = row < static_cast<int64_t>(a.total_rows) * a.num_heads;
-                for (int kb = 0; kb < min(kblocks, kQueryBlocks); ++kb) {
-                    uint32_t x[32];
+        // The first query blocks of an item go to tensor memory: lanes 32 i .. 32 i + 31 by key
+        // warp i, behind the keys of the item's first tile.
+        const auto queries = [&](const Walk& w) -> bool {
+            const int64_t row = w.r.first * a.num_heads + static_cast<int64_t>(w.item) * 128 +
+                                rank * 64 + (i & 1) * 32 + lane;
+            const uint16_t* q = a.q + row * a.cols;
+            const bool have = row < static_cast<int64_t>(a.total_rows) * a.num_heads;
+            const uint32_t to = tmem + (static_cast<uint32_t>(i * 32) << 16) + kQueryCol;
+            bool waited = false;
+#pragma unroll 1
+            for (int kb = 0; kb < kQueryBlocks; kb += 2) {
+                uint32_t x[2][32];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int c = kb * 64 + k * 8;
-                        const uint4 v = have && c < a.cols ? ld_nc_v4(q + c) : make_uint4(0u, 0u, 0u, 0u);
-                        x[4 * k] = v.x;
-                        x[4 * k + 1] = v.y;
-                        x[4 * k + 2] = v.z;
-                        x[4 * k + 3] = v.w;
-                    }
-                    tmem_st_x32(tmem + (static_cast<uint32_t>(i * 32) << 16) + kQueryCol + kb * 32, x);
+                for (int k = 0; k < 16; ++k) {
+                    const int c = kb * 64 + k * 8;
+                    const uint4 v = have && c < a.cols ? ld_nc_v4(q + c) : make_uint4(0u, 0u, 0u, 0u);
+                    x[k >> 3][4 * (k & 7)] = v.x;
+                    x[k >> 3][4 * (k & 7) + 1] = v.y;
+                    x[k >> 3][4 * (k & 7) + 2] = v.z;
+                    x[k >> 3][4 * (k & 7) + 3] = v.w;
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(q_full);
-                ++item;
+                if (!waited && !issue_wait(&bars->q_empty, (item & 1) ^ 1)) return false;
+                if (!waited) tc_fence_after();
+                waited = true;
+                tmem_st_x32(to + kb * 32, x[0]);
+                tmem_st_x32(to + kb * 32 + 32, x[1]);
             }
-            for (int t = 0; ok && !idle && t < tiles; ++t, ++g) {
-                const int32_t kt = w.kt0 + t;
-                const int64_t pos0 = static_cast<int64_t>(kt) * kKeys + (keys ? rank * 64 : 0u);
-                // Drafts that some query does not attend must not turn its zero weights into
-                // NaN: as values their infinities and NaN become zero, which takes a pass
-                // through registers.  (A query that attends such a draft has it in its scores.)
-                const uint32_t slot = ring.stage;              // of the value group
-                const uint32_t phase = keys ? g & 1 : ring.phase;
-                uint8_t* dst = keys ? sK : sV + slot * 2 * kValueBytes + (i & 1) * kValueBytes;
-                if (!keys)
-                    for (int v = 0; v < vgroups; ++v) ring.next(kValueRing);
-                if (SRC == kTma && (keys || t < cached)) {
-                    const Place at(a, w.b, lane < boxes ? pos0 + lane * slots : w.r.kv, w.r.kv);
-                    // A box brings a whole group, or one block: a load takes the TMA unit about
-                    // 130 cycles and 0.8 for each of its 128-byte rows, so few wide ones are
-                    // better.
-                    if (wide > 1) {
-                        const uint32_t group = keys ? i : slot;
-                        const int brings = keys ? (i == 0 ? kTreeKeyBlocks : kTreeLastKeyBlocks)
-                                                : (i & 1) ? 0 : kTreeValueBlocks;
-                        const int blk = keys ? i * kTreeKeyBlocks : i;
-                        ok = issue_wait(&empty[group], phase ^ 1);
-                        if (!ok) break;
-                        if (lane == 0) {
-                            if (leader) mbar_arrive_expect_tx(&full[group], 2 * brings * bytes);
-                            else if (!keys) mbar_arrive_remote(full0 + group * 8);
-                        }
-                        if (brings > 0)
-                            tma_load_4d_pair_elect(dst + (keys ? blk * bytes : 0), map,
-                                                   full0 + group * 8, 0,
-                                                   __shfl_sync(0xffffffffu, at.slot, 0),
-                                                   __shfl_sync(0xffffffffu, at.page, 0),
-                                                   col0 / 64 + blk);
-                        last_group = group;
-                    } else {
-                        for (int blk = i; blk < (keys ? kblocks : i + 1); blk += 4) {
-                            const uint32_t group = !keys ? slot : blk < kQueryBlocks ? 0 : 1;
-                            const bool brings = keys || blk < vblocks;
-                            ok = issue_wait(&empty[group], phase ^ 1);
-                            if (!ok) break;
-                            if (lane == 0) {
-                                if (leader) mbar_arrive_expect_tx(&full[group], brings ? 2 * bytes : 0);
-                                else if (!keys) mbar_arrive_remote(full0 + group * 8);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(q_full);
+            ++item;
+            return true;
+        };
+        Walk w(bars);
+        if constexpr (SRC == kTma) {
+            // A box brings a whole group, or one block: a load takes the TMA unit about 130
+            // cycles and 0.8 for each of its 128-byte rows, so few wide ones are better.
+            const bool wide = keys ? tb.key_blocks > 1 : tb.value_blocks > 1;
+            const int slots = keys ? tb.key_slots : tb.value_slots;
+            const int boxes = (keys ? 64 : kKeys) / slots;
+            const uint32_t block = keys ? kBlockBytes : kValueBytes;
+            if (keys) {
+                const bool idle = wide && (i > 1 || (i == 1 && kblocks <= kQueryBlocks));
+                const CUtensorMap* map = wide && i == 1 ? &tm_k1 : &tm_k0;
+                const int step = wide ? kBlocks : 4;  // blocks between those of this warp
+                const int brings = !wide ? 1 : i == 0 ? kTreeKeyBlocks : kTreeLastKeyBlocks;
+                while (ok && __any_sync(0xffffffffu, w.next(a))) {
+                    const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
+                    for (int t = 0; t < tiles; ++t) {
+                        if (!idle) {
+                            const int64_t pos0 = static_cast<int64_t>(w.kt0 + t) * kKeys + rank * 64;
+                            const Place at(a, w.b, lane < boxes ? pos0 + lane * slots : w.r.kv, w.r.kv);
+                            for (int blk = wide ? i * kTreeKeyBlocks : i; blk < kblocks; blk += step) {
+                                const uint32_t group = blk < kQueryBlocks ? 0 : 1;
+                                ok = issue_wait(&bars->k_empty[group], (g & 1) ^ 1);
+                                if (!ok) break;
+                                if (leader && lane == 0)
+                                    mbar_arrive_expect_tx(&bars->k_full[group], 2 * brings * block);
+                                for (int x = 0; x < boxes; ++x)
+                                    tma_load_4d_pair_elect(
+                                        sK + blk * block + x * slots * 128, map, k_full + group * 8,
+                                        wide ? 0 : blk * 64, __shfl_sync(0xffffffffu, at.slot, x),
+                                        __shfl_sync(0xffffffffu, at.page, x), wide ? blk : 0);
                             }
-                            for (int x = 0; brings && x < boxes; ++x)
-                                tma_load_4d_pair_elect(dst + (keys ? blk * bytes : 0) + x * slots * 128,
-                                                       map, full0 + group * 8, col0 + blk * 64,
-                                                       __shfl_sync(0xffffffffu, at.slot, x),
-                                                       __shfl_sync(0xffffffffu, at.page, x), 0);
-                            last_group = group;
-                        }
-                        if (!ok) break;
-                    }
-                    issued = g + 1;
-                    last_phase = phase;
-                    continue;
-                }
-                // By loads: four lanes take a row's 64 columns, 16 each; eight rows at a time.
-                const int sub = lane >> 2, part = lane & 3;
-                for (int blk = i; blk < (keys ? kblocks : i + 1); blk += 4) {
-                    const uint32_t group = !keys ? slot : blk < kQueryBlocks ? 0 : 1;
-                    const int c = col0 + blk * 64 + part * 16;
-                    const int64_t mine[2] = {
-                        Place(a, w.b, pos0 + lane, w.r.kv).offset(a),
-                        Place(a, w.b, pos0 + 32 + lane, w.r.kv).offset(a)};
-                    const int64_t more[2] = {
-                        keys ? -1 : Place(a, w.b, pos0 + 64 + lane, w.r.kv).offset(a),
-                        keys ? -1 : Place(a, w.b, pos0 + 96 + lane, w.r.kv).offset(a)};
-                    bool waited = false;
-                    for (int r0 = 0; r0 < rows; r0 += 64) {
-                        Piece<SRC> x[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int64_t from = r0 == 0 ? mine[k >> 2] : more[k >> 2];
-                            x[k].load(a, __shfl_sync(0xffffffffu, from, (k & 3) * 8 + sub), c);
-                        }
-                        if (!waited) {
-                            ok = issue_wait(&empty[group], phase ^ 1);
                             if (!ok) break;
-                            waited = true;
+                            ++g;
+                            if (i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
                         }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int key = r0 + k * 8 + sub;
-                            x[k].store(a, c, smem_u32(dst + (keys ? blk * bytes : 0)) + key * 128, key, part * 2,
-                                       !keys && pos0 + key >= w.r.len);
+                        if (t == 0) ok = queries(w);
+                        if (!ok || idle) break;
+                    }
+                }
+                if (!ok && lane == 0) bars->progress = INT32_MAX;
+            } else {
+                RingPos ring;            // place of the tile's first group
+                uint32_t own_phase = 0;  // bit s: phase of v_own[s], which both groups use in turn
+                const int brings = wide ? ((i & 1) ? 0 : kTreeValueBlocks) : i < vblocks ? 1 : 0;
+                while (ok && i < 2 * vgroups && __any_sync(0xffffffffu, w.next(a))) {
+                    const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
+                    const int cached = __shfl_sync(0xffffffffu, w.cached_tiles() - w.kt0, 0);
+                    for (int t = 0; t < tiles; ++t) {
+                        const int64_t pos0 = static_cast<int64_t>(w.kt0 + t) * kKeys;
+                        const Place at(a, w.b, lane < boxes ? pos0 + lane * slots : w.r.kv, w.r.kv);
+                        RingPos mine = ring;
+                        if (i >= 2) mine.next(kValueRing);
+                        const uint32_t s = mine.stage;
+                        uint8_t* dst = sV + s * 2 * kValueBytes + (i & 1) * kValueBytes;
+                        ok = issue_wait(&bars->v_empty[s], mine.phase ^ 1);
+                        if (!ok) break;
+                        if (t < cached) {
+                            if (lane == 0) {
+                                if (leader) mbar_arrive_expect_tx(&bars->v_full[s], 2 * brings * block);
+                                else mbar_arrive_remote(v_full + s * 8);
+                            }
+                            for (int x = 0; brings > 0 && x < boxes; ++x)
+                                tma_load_4d_pair_elect(
+                                    dst + x * slots * 128, &tm_v, v_full + s * 8,
+                                    wide ? 0 : col0 + i * 64, __shfl_sync(0xffffffffu, at.slot, x),
+                                    __shfl_sync(0xffffffffu, at.page, x), wide ? col0 / 64 + i : 0);
+                        } else {
+                            // Drafts, which not every query attends, and rows past the last: a
+                            // zero weight must not meet an infinity or NaN.  The CTA loads them
+                            // for itself and makes those zero before it passes the block on.
+                            // (A query that attends such a draft has it in its scores.)
+                            if (lane == 0 && (brings > 0 || !wide))
+                                mbar_arrive_expect_tx(&bars->v_own[s], brings * block);
+                            for (int x = 0; brings > 0 && x < boxes; ++x)
+                                tma_load_4d_elect(
+                                    dst + x * slots * 128, &tm_v, &bars->v_own[s],
+                                    wide ? 0 : col0 + i * 64, __shfl_sync(0xffffffffu, at.slot, x),
+                                    __shfl_sync(0xffffffffu, at.page, x), wide ? col0 / 64 + i : 0);
+                            ok = issue_wait(&bars->v_own[s], (own_phase >> s) & 1);
+                            if (!ok) break;
+                            const int drafts = static_cast<int>(
+                                max(min(w.r.len, w.r.kv) - pos0, static_cast<int64_t>(0)));
+                            const uint32_t from = smem_u32(dst) + (lane & 7) * 16;
+                            for (int r = drafts + (lane >> 3); r < kKeys; r += 4) {
+                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                                if (pos0 + r < w.r.kv) v = finite8(ld_shared_v4(from + r * 128));
+                                st_shared_v4(from + r * 128, v.x, v.y, v.z, v.w);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_remote(v_full + s * 8);
+                        }
+                        for (int v = 0; v < vgroups; ++v) {
+                            if (t >= cached) own_phase ^= 1u << ring.stage;
+                            ring.next(kValueRing);
                         }
                     }
-                    if (!ok) break;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(full0 + group * 8);
                 }
             }
-        }
-        if (!ok && issued > 0 && lane == 0) {  // let the loads in flight land
-            if (leader) mbar_wait_inl(&full[last_group], last_phase, wc, false);
-            if (!leader) spin_ns(50000);
+            if (!ok) spin_ns(kDrainNs);
+        } else {
+            // By loads, 32 rows of a block a step: four lanes take a row's 64 columns, 16 each,
+            // eight rows at a time.  Two steps are in flight: while one is converted and
+            // stored, the next one's rows are on their way.
+            const int per_block = keys ? 2 : 4;
+            RingPos ring;
+            if (!keys && i >= 2) ring.next(kValueRing);
+            const int sub = lane >> 2, part = lane & 3;
+            Walk ahead(bars);
+            int tiles = 0, t = 0, blk = i, step = 0;              // the step to be stored
+            int a_tiles = 0, a_t = 0, a_blk = i, a_step = 0;      // the step to be loaded
+            bool a_more = true;
+            int64_t rows[4];       // offsets of rows lane, 32 + lane, ... of the loaded tile
+            Piece<SRC> x[2][4];
+            const int blocks = keys ? kblocks : i + 1;
+            const bool any = keys ? i < kblocks : i < 2 * vgroups;
+            const auto load = [&](Piece<SRC>(&p)[4]) {
+                if (a_t == a_tiles) {
+                    a_more = a_more && __any_sync(0xffffffffu, ahead.next(a));
+                    if (!a_more) return;
+                    a_tiles = ahead.kt1 - ahead.kt0;
+                    a_t = 0;
+                }
+                if (a_blk == i && a_step == 0) {
+                    const int64_t pos0 =
+                        static_cast<int64_t>(ahead.kt0 + a_t) * kKeys + (keys ? rank * 64 : 0u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < per_block)
+                            rows[k] = Place(a, ahead.b, pos0 + k * 32 + lane, ahead.r.kv).offset(a);
+                }
+                const int64_t mine = a_step == 0 ? rows[0] : a_step == 1 ? rows[1]
+                                     : a_step == 2 ? rows[2] : rows[3];
+                const int c = (keys ? 0 : col0) + a_blk * 64 + part * 16;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    p[k].load(a, __shfl_sync(0xffffffffu, mine, k * 8 + sub), c);
+                if (++a_step == per_block) {
+                    a_step = 0;
+                    a_blk += 4;
+                    if (a_blk >= blocks) {
+                        a_blk = i;
+                        ++a_t;
+                    }
+                }
+            };
+            const auto store = [&](Piece<SRC>(&p)[4]) {
+                const uint32_t group = !keys ? ring.stage : blk < kQueryBlocks ? 0 : 1;
+                uint64_t* empty = keys ? &bars->k_empty[group] : &bars->v_empty[group];
+                if (step == 0) {
+                    ok = issue_wait(empty, keys ? (g & 1) ^ 1 : ring.phase ^ 1);
+                    if (!ok) return;
+                }
+                const int64_t pos0 = static_cast<int64_t>(w.kt0 + t) * kKeys + (keys ? rank * 64 : 0u);
+                uint8_t* dst = keys ? sK + blk * kBlockBytes
+                                    : sV + group * 2 * kValueBytes + (i & 1) * kValueBytes;
+                const int c = (keys ? 0 : col0) + blk * 64 + part * 16;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int key = step * 32 + k * 8 + sub;
+                    // as in the loads by TMA, drafts' infinities and NaN are no values
+                    p[k].store(a, c, smem_u32(dst) + key * 128, key, part * 2,
+                               !keys && pos0 + key >= w.r.len);
+                }
+                if (++step < per_block) return;
+                step = 0;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote((keys ? k_full : v_full) + group * 8);
+                blk += 4;
+                if (blk < blocks) return;
+                blk = i;
+                if (keys && t == 0) ok = queries(w);
+                ++t;
+                ++g;
+                if (keys && i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
+                for (int v = 0; v < vgroups; ++v) ring.next(kValueRing);
+            };
+            if (any) {
+                load(x[0]);
+                load(x[1]);
+                while (ok) {
+                    if (t == tiles) {
+                        if (!__any_sync(0xffffffffu, w.next(a))) break;
+                        tiles = w.kt1 - w.kt0;
+                        t = 0;
+                    }
+                    // an even number of steps a tile: the buffers keep their turn
+                    store(x[0]);
+                    if (!ok) break;
+                    load(x[0]);
+                    store(x[1]);
+                    if (!ok) break;
+                    load(x[1]);
+                }
+            } else if (keys) {  // fewer blocks than warps: the queries alone
+                while (ok && __any_sync(0xffffffffu, w.next(a))) ok = queries(w);
+            }
+            if (!ok && lane == 0) bars->progress = INT32_MAX;
         }
     }
 

@@ -269,3 +269,13 @@ def test_cache_beyond_32_bit_offsets():
     out, lse, status = g.results()
     assert status == 0
     assert_tree_close(p, out, lse)
+
+
+@pytest.mark.parametrize("page", [128, 256, 64])
+def test_drafts_over_tiles_of_many_items(page):
+    """Several 128-row items per pair of CTAs whose drafts lie in one or two key tiles, pages
+    of whole tiles: the value buffers change their use from item to item."""
+    gen = np.random.default_rng(page)
+    ctx = [int(x) for x in gen.integers(0, 400, 40)]
+    new = [int(x) for x in gen.integers(1, 65, 40)]
+    check(make_tree(620 + page, ctx, new, 24, 512, 64, page=page))
