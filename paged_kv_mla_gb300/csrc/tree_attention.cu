@@ -43,6 +43,7 @@ namespace {
 constexpr int kSoftWarps = 4, kMmaWarp = 4, kQueryWarp = 5, kFetchWarp = 6, kKeyWarp = 8, kValueWarp = 12;
 constexpr int kThreads = 16 * 32;
 constexpr int kSoftRegs = 192, kIssueRegs = 64;  // with 128 for each loader: 4 x 128 in all
+constexpr int kItemCost = 4;        // an item's start and end, in tiles (7 us against 1.6 us)
 constexpr int kKeys = 128;          // keys of a tile (64 loaded by each CTA as keys)
 constexpr int kBlocks = 9;          // 64-column blocks of a latent row
 constexpr int kBlockBytes = 64 * 128;
@@ -85,8 +86,9 @@ struct Request {
         tiles = static_cast<int32_t>((kv + kKeys - 1) / kKeys);
         items = static_cast<int32_t>((static_cast<int64_t>(n) * a.num_heads + 127) / 128);
     }
+    __device__ __forceinline__ int32_t item_units() const { return tiles + kItemCost; }
     __device__ __forceinline__ int64_t units() const {
-        return n > 0 ? static_cast<int64_t>(tiles) * items : 0;
+        return n > 0 ? static_cast<int64_t>(item_units()) * items : 0;
     }
 };
 
@@ -102,11 +104,11 @@ struct Bars {
     uint64_t o_full;            // both: the tile's weights are used up and O is current
     uint64_t o_empty;           // even CTA: both CTAs' epilogues have read O
     uint64_t mma_done;
-    int64_t units;              // tiles of all items
+    int64_t units;              // units of all items
     int64_t first_unit;         // this pair's share begins here
-    int32_t share;              // and has so many tiles
-    int32_t request, item, tile;  // its first tile
-    Request first;
+    int32_t share;              // and has so many units
+    int32_t request, item, unit;  // its first unit
+    Request first;              // the request of that
     int32_t progress;           // tiles whose keys have been asked for
     uint32_t tmem_base;
     int abort_flag;
@@ -122,11 +124,13 @@ constexpr size_t kOffBars = kOffSum + 128 * sizeof(float);
 constexpr size_t kSmemBytes = kOffBars + sizeof(Bars) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103a CTA");
 
-// A pair's share of the tiles of all items, walked item by item.  After next() returned
-// true, the part is tiles [kt0, kt1) of item `item` of request r.
+// A pair's share of the units of all items, walked item by item.  An item has a unit for each
+// of its tiles, behind kItemCost units that stand for its start and end.  After next()
+// returned true, the part is tiles [kt0, kt1) of item `item` of request r.
 struct Walk {
-    int64_t u;       // first unit of the part
-    int32_t left;    // tiles of the share behind the part
+    int64_t u;       // first unit behind the part
+    int32_t left;    // units of the share behind the part
+    int32_t at;      // unit of the item behind the part
     int b;
     Request r;
     int32_t item, kt0, kt1;
@@ -135,24 +139,28 @@ struct Walk {
         left = bars->share;
         b = bars->request;
         item = bars->item;
-        kt0 = kt1 = bars->tile;
+        at = bars->unit;
         u = bars->first_unit;
         r = bars->first;
     }
     __device__ __forceinline__ bool next(const TreeAttentionArgs& a) {
-        if (left <= 0) return false;
-        u += kt1 - kt0;
-        if (kt1 == r.tiles) {
-            kt1 = 0;
-            if (++item == r.items) {
-                item = 0;
-                do r.load(a, ++b);  // tiles are left: a request further on has them
-                while (r.units() == 0);
+        do {
+            if (left <= 0) return false;
+            if (at == r.item_units()) {
+                at = 0;
+                if (++item == r.items) {
+                    item = 0;
+                    do r.load(a, ++b);  // units are left: a request further on has them
+                    while (r.units() == 0);
+                }
             }
-        }
-        kt0 = kt1;
-        kt1 = min(r.tiles, kt0 + left);
-        left -= kt1 - kt0;
+            const int32_t take = min(r.item_units() - at, left);
+            kt0 = max(at - kItemCost, 0);
+            at += take;
+            kt1 = max(at - kItemCost, 0);
+            u += take;
+            left -= take;
+        } while (kt1 == kt0);  // a share can end within an item's first units
         return true;
     }
     // The first tiles of an item hold cached tokens alone, which every row attends.
@@ -161,7 +169,7 @@ struct Walk {
     }
 };
 
-// Counts the tiles of all requests and cuts out the pair's share; every thread sums a run of
+// Counts the units of all requests and cuts out the pair's share; every thread sums a run of
 // requests.  `scratch`: 16 int64 of shared memory.
 __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int64_t* scratch,
                                      int64_t pair, int64_t pairs) {
@@ -190,7 +198,7 @@ __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int
         total += scratch[w];
     }
     if (threadIdx.x == 0) bars->units = total;
-    pairs = min(pairs, total);  // no pair without a tile lies between two that share an item
+    pairs = min(pairs, total);  // no pair without a unit lies between two that share an item
     if (pair >= pairs) return;
     const int64_t u = quotient(total * pair, pairs);
     int64_t at = before + incl - sum;
@@ -202,8 +210,9 @@ __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int
                 bars->share = static_cast<int32_t>(quotient(total * (pair + 1), pairs) - u);
                 bars->request = b;
                 bars->first = r;
-                bars->item = static_cast<int32_t>(quotient(u - at, r.tiles));
-                bars->tile = static_cast<int32_t>((u - at) - static_cast<int64_t>(bars->item) * r.tiles);
+                const int32_t item = static_cast<int32_t>(quotient(u - at, r.item_units()));
+                bars->item = item;
+                bars->unit = static_cast<int32_t>((u - at) - static_cast<int64_t>(item) * r.item_units());
                 break;
             }
             at += r.units();
@@ -257,48 +266,66 @@ __device__ __forceinline__ uint2 dequant4(uint32_t codes, float scale) {
     return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// Sixteen columns c .. c+15 of a latent row, as they lie in the cache: two pieces of eight
-// bf16 values, or sixteen codes and their scale.  Past the row's columns and for rows that do
-// not exist (offset -1): zeros.
+// Sixteen columns c .. c+15 of a latent row on their way from the cache to a swizzled 128-byte
+// row in shared memory (16-byte chunks ch and ch + 1).  Past the row's columns and for rows
+// that do not exist (offset -1): zeros.
+__device__ __forceinline__ void store_piece(uint4 lo, uint4 hi, uint32_t row, int key, int ch,
+                                            bool clean) {
+    if (clean) {
+        lo = finite8(lo);
+        hi = finite8(hi);
+    }
+    st_shared_v4(row + ((ch ^ (key & 7)) << 4), lo.x, lo.y, lo.z, lo.w);
+    st_shared_v4(row + (((ch + 1) ^ (key & 7)) << 4), hi.x, hi.y, hi.z, hi.w);
+}
+
 template <Source SRC>
-struct Piece {
+struct Piece {  // bf16 columns
+    static constexpr int kCount = 2;  // pieces a step (8 rows each)
     uint4 lo, hi;
 
     __device__ __forceinline__ void load(const TreeAttentionArgs& a, int64_t row, int c) {
         lo = hi = make_uint4(0u, 0u, 0u, 0u);
         if (row < 0 || c >= a.cols) return;
-        if constexpr (SRC == kCodes) {
-            const uint8_t* p = a.qcache_layer + row;
-            const int R = a.kv_lora_rank;
-            if (c < R) {
-                lo = ld_nc_v4(p + c);
-                hi.x = __ldg(reinterpret_cast<const uint32_t*>(
-                    p + R + 2 * (a.cols - R) + 4 * (c / 128)));
-            } else {
-                lo = ld_nc_v4(p + R + 2 * (c - R));
-                if (c + 8 < a.cols) hi = ld_nc_v4(p + R + 2 * (c - R) + 16);
-            }
-        } else {
-            lo = ld_nc_v4(a.cache_layer + row + c);
-            if (c + 8 < a.cols) hi = ld_nc_v4(a.cache_layer + row + c + 8);
-        }
+        lo = ld_nc_v4(a.cache_layer + row + c);
+        if (c + 8 < a.cols) hi = ld_nc_v4(a.cache_layer + row + c + 8);
     }
-    // Writes the columns as bf16 to a swizzled 128-byte row, 16-byte chunks ch and ch + 1.
-    __device__ __forceinline__ void store(const TreeAttentionArgs& a, int c, uint32_t row,
+    __device__ __forceinline__ void store(const TreeAttentionArgs&, int64_t, int, uint32_t row,
                                           int key, int ch, bool clean) {
-        if (SRC == kCodes && c < a.kv_lora_rank) {
-            const float scale = __uint_as_float(hi.x);
-            const uint2 d0 = dequant4(lo.x, scale), d1 = dequant4(lo.y, scale);
-            const uint2 d2 = dequant4(lo.z, scale), d3 = dequant4(lo.w, scale);
-            lo = make_uint4(d0.x, d0.y, d1.x, d1.y);
-            hi = make_uint4(d2.x, d2.y, d3.x, d3.y);
+        store_piece(lo, hi, row, key, ch, clean);
+    }
+};
+
+template <>
+struct Piece<kCodes> {  // codes and their scale; the rope columns, bf16, are loaded when stored
+    static constexpr int kCount = 4;
+    uint4 codes;
+    float scale;
+
+    __device__ __forceinline__ void load(const TreeAttentionArgs& a, int64_t row, int c) {
+        codes = make_uint4(0u, 0u, 0u, 0u);
+        scale = 0.0f;
+        const int R = a.kv_lora_rank;
+        if (row < 0 || c >= R) return;
+        const uint8_t* p = a.qcache_layer + row;
+        codes = ld_nc_v4(p + c);
+        scale = __ldg(reinterpret_cast<const float*>(p + R + 2 * (a.cols - R) + 4 * (c / 128)));
+    }
+    __device__ __forceinline__ void store(const TreeAttentionArgs& a, int64_t from, int c,
+                                          uint32_t row, int key, int ch, bool clean) {
+        const int R = a.kv_lora_rank;
+        if (c < R) {
+            const uint2 d0 = dequant4(codes.x, scale), d1 = dequant4(codes.y, scale);
+            const uint2 d2 = dequant4(codes.z, scale), d3 = dequant4(codes.w, scale);
+            store_piece(make_uint4(d0.x, d0.y, d1.x, d1.y), make_uint4(d2.x, d2.y, d3.x, d3.y),
+                        row, key, ch, clean);
+            return;
         }
-        if (clean) {
-            lo = finite8(lo);
-            hi = finite8(hi);
-        }
-        st_shared_v4(row + ((ch ^ (key & 7)) << 4), lo.x, lo.y, lo.z, lo.w);
-        st_shared_v4(row + (((ch + 1) ^ (key & 7)) << 4), hi.x, hi.y, hi.z, hi.w);
+        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+        const uint8_t* p = a.qcache_layer + from + R + 2 * (c - R);
+        if (from >= 0 && c < a.cols) lo = ld_nc_v4(p);
+        if (from >= 0 && c + 8 < a.cols) hi = ld_nc_v4(p + 16);
+        store_piece(lo, hi, row, key, ch, clean);
     }
 };
 
@@ -420,11 +447,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_alloc_pair(&bars->tmem_base, kTmemCols);
         tmem_relinquish_pair();
     }
+    __syncwarp();
+    cluster_arrive();  // the barriers are set up; the peer may signal them behind cluster_wait
+    griddep_wait();    // launched while the work before it may still run; reads nothing before
     plan(a, bars, reinterpret_cast<int64_t*>(s_max), pair, pairs);
     griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();
+    cluster_wait();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const WaitCtl wc{&bars->abort_flag, a.status, a.timeout_ns};
@@ -623,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + at] =
                         make_float2(m, l);
                 if (w.kt0 == 0) {
-                    const int64_t end = w.u + w.r.tiles;
+                    const int64_t end = w.u + (w.r.tiles - w.kt1);
                     left_first = row0 - rank * 64 - (warp & 1) * 32;
                     left_rows = static_cast<int32_t>(
                         min(rows_all - static_cast<int64_t>(w.item) * 128, static_cast<int64_t>(128)));
@@ -802,31 +832,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t g = 0, item = 0;
         bool ok = true;
         // The first query blocks of an item go to tensor memory: lanes 32 i .. 32 i + 31 by key
-        // warp i, behind the keys of the item's first tile.
-        const auto queries = [&](const Walk& w) -> bool {
+        // warp i, behind the keys of the item's first tile; the first of them are fetched
+        // before those keys are asked for.
+        constexpr int kAtOnce = SRC == kTma ? 2 : 1;  // blocks in flight
+        const auto fetch = [&](const Walk& w, int kb, uint32_t(&x)[kAtOnce][32]) {
             const int64_t row = w.r.first * a.num_heads + static_cast<int64_t>(w.item) * 128 +
                                 rank * 64 + (i & 1) * 32 + lane;
             const uint16_t* q = a.q + row * a.cols;
             const bool have = row < static_cast<int64_t>(a.total_rows) * a.num_heads;
-            const uint32_t to = tmem + (static_cast<uint32_t>(i * 32) << 16) + kQueryCol;
-            bool waited = false;
-#pragma unroll 1
-            for (int kb = 0; kb < kQueryBlocks; kb += 2) {
-                uint32_t x[2][32];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int c = kb * 64 + k * 8;
-                    const uint4 v = have && c < a.cols ? ld_nc_v4(q + c) : make_uint4(0u, 0u, 0u, 0u);
-                    x[k >> 3][4 * (k & 7)] = v.x;
-                    x[k >> 3][4 * (k & 7) + 1] = v.y;
-                    x[k >> 3][4 * (k & 7) + 2] = v.z;
-                    x[k >> 3][4 * (k & 7) + 3] = v.w;
-                }
-                if (!waited && !issue_wait(&bars->q_empty, (item & 1) ^ 1)) return false;
-                if (!waited) tc_fence_after();
-                waited = true;
-                tmem_st_x32(to + kb * 32, x[0]);
-                tmem_st_x32(to + kb * 32 + 32, x[1]);
+            for (int k = 0; k < 8 * kAtOnce; ++k) {
+                const int c = kb * 64 + k * 8;
+                const uint4 v = have && c < a.cols ? ld_nc_v4(q + c) : make_uint4(0u, 0u, 0u, 0u);
+                x[k >> 3][4 * (k & 7)] = v.x;
+                x[k >> 3][4 * (k & 7) + 1] = v.y;
+                x[k >> 3][4 * (k & 7) + 2] = v.z;
+                x[k >> 3][4 * (k & 7) + 3] = v.w;
+            }
+        };
+        const auto queries = [&](const Walk& w, uint32_t(&x)[kAtOnce][32]) -> bool {
+            if (!issue_wait(&bars->q_empty, (item & 1) ^ 1)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int kb = 0; kb < kQueryBlocks; kb += kAtOnce) {
+                if (kb > 0) fetch(w, kb, x);
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    tmem_st_x32(tmem + (static_cast<uint32_t>(i * 32) << 16) + kQueryCol + (kb + k) * 32,
+                                x[k]);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -850,6 +883,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int brings = !wide ? 1 : i == 0 ? kTreeKeyBlocks : kTreeLastKeyBlocks;
                 while (ok && __any_sync(0xffffffffu, w.next(a))) {
                     const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
+                    uint32_t q[kAtOnce][32];
+                    fetch(w, 0, q);
                     for (int t = 0; t < tiles; ++t) {
                         if (!idle) {
                             const int64_t pos0 = static_cast<int64_t>(w.kt0 + t) * kKeys + rank * 64;
@@ -870,7 +905,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             ++g;
                             if (i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
                         }
-                        if (t == 0) ok = queries(w);
+                        if (t == 0) ok = queries(w, q);
                         if (!ok || idle) break;
                     }
                 }
@@ -936,10 +971,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok) spin_ns(kDrainNs);
         } else {
-            // By loads, 32 rows of a block a step: four lanes take a row's 64 columns, 16 each,
-            // eight rows at a time.  Two steps are in flight: while one is converted and
+            // By loads, a few rows of a block a step: four lanes take a row's 64 columns, 16
+            // each, eight rows at a time.  Two steps are in flight: while one is converted and
             // stored, the next one's rows are on their way.
-            const int per_block = keys ? 2 : 4;
+            constexpr int kPieces = Piece<SRC>::kCount, kRowsAtOnce = 8 * kPieces;
+            const int per_block = (keys ? 64 : kKeys) / kRowsAtOnce;
             RingPos ring;
             if (!keys && i >= 2) ring.next(kValueRing);
             const int sub = lane >> 2, part = lane & 3;
@@ -948,10 +984,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int a_tiles = 0, a_t = 0, a_blk = i, a_step = 0;      // the step to be loaded
             bool a_more = true;
             int64_t rows[4];       // offsets of rows lane, 32 + lane, ... of the loaded tile
-            Piece<SRC> x[2][4];
+            Piece<SRC> x[2][kPieces];
+            int64_t from[2];       // the step's row offsets, one in each of its lanes
             const int blocks = keys ? kblocks : i + 1;
             const bool any = keys ? i < kblocks : i < 2 * vgroups;
-            const auto load = [&](Piece<SRC>(&p)[4]) {
+            const auto load = [&](Piece<SRC>(&p)[kPieces], int64_t& mine) {
                 if (a_t == a_tiles) {
                     a_more = a_more && __any_sync(0xffffffffu, ahead.next(a));
                     if (!a_more) return;
@@ -963,15 +1000,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         static_cast<int64_t>(ahead.kt0 + a_t) * kKeys + (keys ? rank * 64 : 0u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (k < per_block)
+                        if (k < (keys ? 2 : 4))
                             rows[k] = Place(a, ahead.b, pos0 + k * 32 + lane, ahead.r.kv).offset(a);
                 }
-                const int64_t mine = a_step == 0 ? rows[0] : a_step == 1 ? rows[1]
-                                     : a_step == 2 ? rows[2] : rows[3];
+                const int r0 = a_step * kRowsAtOnce;
+                mine = r0 < 32 ? rows[0] : r0 < 64 ? rows[1] : r0 < 96 ? rows[2] : rows[3];
                 const int c = (keys ? 0 : col0) + a_blk * 64 + part * 16;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    p[k].load(a, __shfl_sync(0xffffffffu, mine, k * 8 + sub), c);
+                for (int k = 0; k < kPieces; ++k)
+                    p[k].load(a, __shfl_sync(0xffffffffu, mine, (r0 & 31) + k * 8 + sub), c);
                 if (++a_step == per_block) {
                     a_step = 0;
                     a_blk += 4;
@@ -981,7 +1018,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            const auto store = [&](Piece<SRC>(&p)[4]) {
+            const auto all_queries = [&](const Walk& w) {
+                uint32_t q[kAtOnce][32];
+                fetch(w, 0, q);
+                return queries(w, q);
+            };
+            const auto store = [&](Piece<SRC>(&p)[kPieces], int64_t mine) {
                 const uint32_t group = !keys ? ring.stage : blk < kQueryBlocks ? 0 : 1;
                 uint64_t* empty = keys ? &bars->k_empty[group] : &bars->v_empty[group];
                 if (step == 0) {
@@ -992,11 +1034,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint8_t* dst = keys ? sK + blk * kBlockBytes
                                     : sV + group * 2 * kValueBytes + (i & 1) * kValueBytes;
                 const int c = (keys ? 0 : col0) + blk * 64 + part * 16;
+                const int r0 = step * kRowsAtOnce;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int key = step * 32 + k * 8 + sub;
+                for (int k = 0; k < kPieces; ++k) {
+                    const int key = r0 + k * 8 + sub;
                     // as in the loads by TMA, drafts' infinities and NaN are no values
-                    p[k].store(a, c, smem_u32(dst) + key * 128, key, part * 2,
+                    p[k].store(a, __shfl_sync(0xffffffffu, mine, key & 31), c,
+                               smem_u32(dst) + key * 128, key, part * 2,
                                !keys && pos0 + key >= w.r.len);
                 }
                 if (++step < per_block) return;
@@ -1007,15 +1051,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 blk += 4;
                 if (blk < blocks) return;
                 blk = i;
-                if (keys && t == 0) ok = queries(w);
+                if (keys && t == 0) ok = all_queries(w);
                 ++t;
                 ++g;
                 if (keys && i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
                 for (int v = 0; v < vgroups; ++v) ring.next(kValueRing);
             };
             if (any) {
-                load(x[0]);
-                load(x[1]);
+                load(x[0], from[0]);
+                load(x[1], from[1]);
                 while (ok) {
                     if (t == tiles) {
                         if (!__any_sync(0xffffffffu, w.next(a))) break;
@@ -1023,15 +1067,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         t = 0;
                     }
                     // an even number of steps a tile: the buffers keep their turn
-                    store(x[0]);
+                    store(x[0], from[0]);
                     if (!ok) break;
-                    load(x[0]);
-                    store(x[1]);
+                    load(x[0], from[0]);
+                    store(x[1], from[1]);
                     if (!ok) break;
-                    load(x[1]);
+                    load(x[1], from[1]);
                 }
             } else if (keys) {  // fewer blocks than warps: the queries alone
-                while (ok && __any_sync(0xffffffffu, w.next(a))) ok = queries(w);
+                while (ok && __any_sync(0xffffffffu, w.next(a))) ok = all_queries(w);
             }
             if (!ok && lane == 0) bars->progress = INT32_MAX;
         }
@@ -1053,8 +1097,7 @@ constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
 __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const TreeAttentionArgs a, const TreeWorkspace ws, const int pairs) {
     __shared__ TreeItem items[kTreeMaxPairs];
-    __shared__ int tasks_at[kTreeMaxPairs];
-    __shared__ int which;
+    __shared__ int begins[kTreeMaxPairs + 1];  // first task of every item, and their number
     __shared__ float sums[kJoinWarps][32][32], tops[kJoinWarps][32], totals[kJoinWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int R = a.kv_lora_rank, col_groups = R / 32;
@@ -1063,32 +1106,49 @@ __global__ void __launch_bounds__(kJoinThreads)
         const int wide = kJoinWarps / split(it.parts);  // column groups a block takes at once
         return (it.rows + 31) / 32 * ((col_groups + wide - 1) / wide);
     };
+    griddep_launch_dependents();
     griddep_wait();
-    if (threadIdx.x < pairs)
-        items[threadIdx.x] = reinterpret_cast<const TreeItem*>(a.workspace + ws.items)[threadIdx.x];
-    __syncthreads();
-    if (threadIdx.x < pairs) tasks_at[threadIdx.x] = tasks_of(items[threadIdx.x]);
-    __syncthreads();
-    int begin = 0, end = 0, tasks = 0;  // tasks of the item of this thread's index; of all
-    for (int p = 0; p < pairs; ++p) {
-        if (p == static_cast<int>(threadIdx.x)) {
-            begin = tasks;
-            end = tasks + tasks_at[p];
+    if (warp == 0) {
+        constexpr int kEach = (kTreeMaxPairs + 31) / 32;
+        int n[kEach], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int p = lane * kEach + k;
+            n[k] = 0;
+            if (p < pairs) {
+                const TreeItem it = reinterpret_cast<const TreeItem*>(a.workspace + ws.items)[p];
+                items[p] = it;
+                n[k] = it.rows > 0 ? tasks_of(it) : 0;
+            }
+            sum += n[k];
         }
-        tasks += tasks_at[p];
+        int incl = sum;
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, sh);
+            if (lane >= sh) incl += o;
+        }
+        int at = incl - sum;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int p = lane * kEach + k;
+            if (p <= pairs) begins[p] = at;
+            at += n[k];
+        }
     }
-    __shared__ int first_task;
+    __syncthreads();
+    const int tasks = begins[pairs];
     const float2* stats = reinterpret_cast<const float2*>(a.workspace + ws.stats);
     const float4* parts = reinterpret_cast<const float4*>(a.workspace + ws.parts);
     for (int f = blockIdx.x; f < tasks; f += gridDim.x) {
-        if (begin <= f && f < end) {
-            which = threadIdx.x;
-            first_task = begin;
+        int p = 0, behind = pairs;  // the last item whose first task is at or before f
+        while (behind - p > 1) {
+            const int mid = (p + behind) / 2;
+            if (begins[mid] <= f) p = mid;
+            else behind = mid;
         }
-        __syncthreads();
-        const int p = which;
         const TreeItem it = items[p];
-        const int task = f - first_task;
+        const int task = f - begins[p];
         const int row_groups = (it.rows + 31) / 32;
         const int ways = split(it.parts);
         const int way = warp & (ways - 1);
@@ -1167,9 +1227,8 @@ cudaError_t launch_source(const CUtensorMap& tm_q, const CUtensorMap& tm_k0, con
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
-    tree_attention_kernel<SRC><<<static_cast<unsigned>(2 * pairs), kThreads, kSmemBytes, stream>>>(
-        tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes);
-    return cudaGetLastError();
+    return launch_dependent(tree_attention_kernel<SRC>, static_cast<unsigned>(2 * pairs), kThreads,
+                            kSmemBytes, stream, tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes);
 }
 
 }  // namespace
