@@ -490,6 +490,33 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
     return v;
 }
 
+// ld_nc_v4 where `have`, else zeros, as one predicated load: behind a branch the compiler moves
+// the loaded value into place, and the move waits for it.
+__device__ __forceinline__ uint4 ld_nc_v4_if(const void* p, bool have) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"(static_cast<int>(have)));
+    return v;
+}
+
+// The same for one 32-bit word.
+__device__ __forceinline__ uint32_t ld_nc_u32_if(const void* p, bool have) {
+    uint32_t v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "mov.b32 %0, 0;\n\t"
+        "@q ld.global.nc.u32 %0, [%1];\n\t}"
+        : "=&r"(v)
+        : "l"(p), "r"(static_cast<int>(have)));
+    return v;
+}
+
 __device__ __forceinline__ void st_v4(void* p, uint4 v) {
     asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y),
                  "r"(v.z), "r"(v.w)

@@ -249,50 +249,72 @@ __device__ __forceinline__ uint4 finite8(uint4 v) {
     return make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
 }
 
-// Four e4m3 codes times a scale, each product rounded to fp32 and then to bf16.
+// Four e4m3 codes times a scale, each product rounded to fp32 and then to bf16.  The halves that
+// the codes unpack to are widened by the mixed-precision add of -0, which keeps a zero's sign
+// and leaves the conversion unit to the unpacking.
 __device__ __forceinline__ uint2 dequant4(uint32_t codes, float scale) {
-    uint32_t h0, h1;
-    asm("{\n\t.reg .b16 l, h;\n\t"
-        "mov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(h0), "=r"(h1)
+    float f0, f1, f2, f3;
+    asm("{\n\t.reg .b16 l, h, a, b, c, d;\n\t.reg .b32 lo, hi;\n\t"
+        "mov.b32 {l, h}, %4;\n\t"
+        "cvt.rn.f16x2.e4m3x2 lo, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 hi, h;\n\t"
+        "mov.b32 {a, b}, lo;\n\t"
+        "mov.b32 {c, d}, hi;\n\t"
+        "add.rn.f32.f16 %0, a, 0f80000000;\n\t"
+        "add.rn.f32.f16 %1, b, 0f80000000;\n\t"
+        "add.rn.f32.f16 %2, c, 0f80000000;\n\t"
+        "add.rn.f32.f16 %3, d, 0f80000000;\n\t}"
+        : "=f"(f0), "=f"(f1), "=f"(f2), "=f"(f3)
         : "r"(codes));
-    const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&h0));
-    const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&h1));
     float a, b, c, d;
-    mul2(a, b, f0.x, f0.y, scale, scale);
-    mul2(c, d, f1.x, f1.y, scale, scale);
+    mul2(a, b, f0, f1, scale, scale);
+    mul2(c, d, f2, f3, scale, scale);
     return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// Sixteen columns c .. c+15 of a latent row on their way from the cache to a swizzled 128-byte
-// row in shared memory (16-byte chunks ch and ch + 1).  Past the row's columns and for rows
-// that do not exist (offset -1): zeros.
-__device__ __forceinline__ void store_piece(uint4 lo, uint4 hi, uint32_t row, int key, int ch,
-                                            bool clean) {
-    if (clean) {
-        lo = finite8(lo);
-        hi = finite8(hi);
-    }
-    st_shared_v4(row + ((ch ^ (key & 7)) << 4), lo.x, lo.y, lo.z, lo.w);
-    st_shared_v4(row + (((ch + 1) ^ (key & 7)) << 4), hi.x, hi.y, hi.z, hi.w);
-}
+// Slot offsets of positions pos0 + 32 k + lane, k < n <= 4: Place::offset of each, with all page
+// ids on their way at once.
+struct Slots {
+    uint32_t id[4];
+    int32_t slot[4];
 
+    __device__ __forceinline__ void fetch(const TreeAttentionArgs& a, int b, int64_t pos0,
+                                          int64_t kv, int n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t pos = pos0 + k * 32;
+            const bool have = k < n && pos < kv;
+            const int64_t lp = quotient(pos, a.page_size);
+            slot[k] = have ? static_cast<int32_t>(pos - lp * a.page_size) : -1;
+            id[k] = ld_nc_u32_if(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp, have);
+        }
+    }
+    __device__ __forceinline__ void offsets(const TreeAttentionArgs& a, int64_t (&rows)[4]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const bool have = slot[k] >= 0 && id[k] < static_cast<uint32_t>(a.num_pages);
+            rows[k] = have ? id[k] * a.page_stride + slot[k] * a.slot_stride : -1;
+            if (!have && slot[k] >= 0) report(a.status, PKM_ERR_OUT_OF_RANGE);
+        }
+    }
+};
+
+// Sixteen columns c .. c+15 of a latent row on their way from the cache to shared memory.  Past
+// the row's columns and for rows that do not exist (offset -1): zeros.
 template <Source SRC>
 struct Piece {  // bf16 columns
     static constexpr int kCount = 2;  // pieces a step (8 rows each)
     uint4 lo, hi;
 
     __device__ __forceinline__ void load(const TreeAttentionArgs& a, int64_t row, int c) {
-        lo = hi = make_uint4(0u, 0u, 0u, 0u);
-        if (row < 0 || c >= a.cols) return;
-        lo = ld_nc_v4(a.cache_layer + row + c);
-        if (c + 8 < a.cols) hi = ld_nc_v4(a.cache_layer + row + c + 8);
+        const uint16_t* p = a.cache_layer + row + c;
+        lo = ld_nc_v4_if(p, row >= 0 && c < a.cols);
+        hi = ld_nc_v4_if(p + 8, row >= 0 && c + 8 < a.cols);
     }
-    __device__ __forceinline__ void store(const TreeAttentionArgs&, int64_t, int, uint32_t row,
-                                          int key, int ch, bool clean) {
-        store_piece(lo, hi, row, key, ch, clean);
+    __device__ __forceinline__ void columns(const TreeAttentionArgs&, int64_t, int, uint4& l,
+                                            uint4& h) const {
+        l = lo;
+        h = hi;
     }
 };
 
@@ -303,29 +325,25 @@ struct Piece<kCodes> {  // codes and their scale; the rope columns, bf16, are lo
     float scale;
 
     __device__ __forceinline__ void load(const TreeAttentionArgs& a, int64_t row, int c) {
-        codes = make_uint4(0u, 0u, 0u, 0u);
-        scale = 0.0f;
         const int R = a.kv_lora_rank;
-        if (row < 0 || c >= R) return;
         const uint8_t* p = a.qcache_layer + row;
-        codes = ld_nc_v4(p + c);
-        scale = __ldg(reinterpret_cast<const float*>(p + R + 2 * (a.cols - R) + 4 * (c / 128)));
+        const bool have = row >= 0 && c < R;
+        codes = ld_nc_v4_if(p + c, have);
+        scale = __uint_as_float(ld_nc_u32_if(p + R + 2 * (a.cols - R) + 4 * (c / 128), have));
     }
-    __device__ __forceinline__ void store(const TreeAttentionArgs& a, int64_t from, int c,
-                                          uint32_t row, int key, int ch, bool clean) {
+    __device__ __forceinline__ void columns(const TreeAttentionArgs& a, int64_t row, int c,
+                                            uint4& l, uint4& h) const {
         const int R = a.kv_lora_rank;
-        if (c < R) {
+        if (c < R) {  // the same in all lanes: blocks of 64 columns are codes or rope columns
             const uint2 d0 = dequant4(codes.x, scale), d1 = dequant4(codes.y, scale);
             const uint2 d2 = dequant4(codes.z, scale), d3 = dequant4(codes.w, scale);
-            store_piece(make_uint4(d0.x, d0.y, d1.x, d1.y), make_uint4(d2.x, d2.y, d3.x, d3.y),
-                        row, key, ch, clean);
+            l = make_uint4(d0.x, d0.y, d1.x, d1.y);
+            h = make_uint4(d2.x, d2.y, d3.x, d3.y);
             return;
         }
-        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-        const uint8_t* p = a.qcache_layer + from + R + 2 * (c - R);
-        if (from >= 0 && c < a.cols) lo = ld_nc_v4(p);
-        if (from >= 0 && c + 8 < a.cols) hi = ld_nc_v4(p + 16);
-        store_piece(lo, hi, row, key, ch, clean);
+        const uint8_t* p = a.qcache_layer + row + R + 2 * (c - R);
+        l = ld_nc_v4_if(p, row >= 0 && c < a.cols);
+        h = ld_nc_v4_if(p + 16, row >= 0 && c + 8 < a.cols);
     }
 };
 
@@ -843,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 8 * kAtOnce; ++k) {
                 const int c = kb * 64 + k * 8;
-                const uint4 v = have && c < a.cols ? ld_nc_v4(q + c) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 v = ld_nc_v4_if(q + c, have && c < a.cols);
                 x[k >> 3][4 * (k & 7)] = v.x;
                 x[k >> 3][4 * (k & 7) + 1] = v.y;
                 x[k >> 3][4 * (k & 7) + 2] = v.z;
@@ -984,6 +1002,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int a_tiles = 0, a_t = 0, a_blk = i, a_step = 0;      // the step to be loaded
             bool a_more = true;
             int64_t rows[4];       // offsets of rows lane, 32 + lane, ... of the loaded tile
+            Slots slots;
             Piece<SRC> x[2][kPieces];
             int64_t from[2];       // the step's row offsets, one in each of its lanes
             const int blocks = keys ? kblocks : i + 1;
@@ -996,12 +1015,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     a_t = 0;
                 }
                 if (a_blk == i && a_step == 0) {
-                    const int64_t pos0 =
-                        static_cast<int64_t>(ahead.kt0 + a_t) * kKeys + (keys ? rank * 64 : 0u);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < (keys ? 2 : 4))
-                            rows[k] = Place(a, ahead.b, pos0 + k * 32 + lane, ahead.r.kv).offset(a);
+                    const int64_t pos0 = static_cast<int64_t>(ahead.kt0 + a_t) * kKeys +
+                                         (keys ? rank * 64 : 0u) + lane;
+                    if (a_t == 0) slots.fetch(a, ahead.b, pos0, ahead.r.kv, keys ? 2 : 4);
+                    slots.offsets(a, rows);
+                    // the next tile's page ids, while this one is loaded
+                    slots.fetch(a, ahead.b, pos0 + kKeys, ahead.r.kv, keys ? 2 : 4);
                 }
                 const int r0 = a_step * kRowsAtOnce;
                 mine = r0 < 32 ? rows[0] : r0 < 64 ? rows[1] : r0 < 96 ? rows[2] : rows[3];
@@ -1030,18 +1049,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = issue_wait(empty, keys ? (g & 1) ^ 1 : ring.phase ^ 1);
                     if (!ok) return;
                 }
-                const int64_t pos0 = static_cast<int64_t>(w.kt0 + t) * kKeys + (keys ? rank * 64 : 0u);
-                uint8_t* dst = keys ? sK + blk * kBlockBytes
-                                    : sV + group * 2 * kValueBytes + (i & 1) * kValueBytes;
+                const uint32_t dst = smem_u32(keys ? sK + blk * kBlockBytes
+                                                   : sV + group * 2 * kValueBytes + (i & 1) * kValueBytes);
                 const int c = (keys ? 0 : col0) + blk * 64 + part * 16;
                 const int r0 = step * kRowsAtOnce;
+                uint4 lo[kPieces], hi[kPieces];
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k)
+                    p[k].columns(a, SRC == kCodes ? __shfl_sync(0xffffffffu, mine, ((r0 & 31) + k * 8 + sub)) : 0,
+                                 c, lo[k], hi[k]);
+                if (!keys && w.kt0 + t >= w.cached_tiles()) {
+                    // as in the loads by TMA, drafts' infinities and NaN are no values
+#pragma unroll
+                    for (int k = 0; k < kPieces; ++k) {
+                        const int64_t pos =
+                            static_cast<int64_t>(w.kt0 + t) * kKeys + r0 + k * 8 + sub;
+                        if (pos < w.r.len) continue;
+                        lo[k] = finite8(lo[k]);
+                        hi[k] = finite8(hi[k]);
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < kPieces; ++k) {
                     const int key = r0 + k * 8 + sub;
-                    // as in the loads by TMA, drafts' infinities and NaN are no values
-                    p[k].store(a, __shfl_sync(0xffffffffu, mine, key & 31), c,
-                               smem_u32(dst) + key * 128, key, part * 2,
-                               !keys && pos0 + key >= w.r.len);
+                    const uint32_t row = dst + key * 128;
+                    st_shared_v4(row + (((2 * part) ^ (key & 7)) << 4), lo[k].x, lo[k].y, lo[k].z, lo[k].w);
+                    st_shared_v4(row + (((2 * part + 1) ^ (key & 7)) << 4), hi[k].x, hi[k].y, hi[k].z, hi[k].w);
                 }
                 if (++step < per_block) return;
                 step = 0;
@@ -1089,22 +1122,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
+constexpr int kFewParts = 2;
 
 // Joins the parts of the items that several pairs share: with M the largest of the parts'
-// maxima, out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k.  A lane has a row and 32 of its
-// columns; the parts of a task are dealt to 2, 4 or 8 warps, which meet in shared memory, always
-// in the same order, and then each finish a share of the columns.
-__global__ void __launch_bounds__(kJoinThreads)
+// maxima, out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same order.
+// A lane has a row and 16 (few parts) or 32 of its columns.  Few parts, as of a batch whose
+// items are cut once or twice, are one warp's task each, all their loads in flight at once;
+// many parts, as of few long histories, are dealt to the warps of a block, which meet in
+// shared memory and then each finish a share of the columns.
+__global__ void __launch_bounds__(kJoinThreads, 3)
     tree_join_kernel(const TreeAttentionArgs a, const TreeWorkspace ws, const int pairs) {
     __shared__ TreeItem items[kTreeMaxPairs];
     __shared__ int begins[kTreeMaxPairs + 1];  // first task of every item, and their number
     __shared__ float sums[kJoinWarps][32][32], tops[kJoinWarps][32], totals[kJoinWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int R = a.kv_lora_rank, col_groups = R / 32;
-    const auto split = [](int parts) { return parts <= 2 ? 2 : parts <= 4 ? 4 : 8; };
+    const int R = a.kv_lora_rank;
+    // tasks of a block: 16 columns a warp, or 32 columns for all warps
     const auto tasks_of = [&](const TreeItem& it) {
-        const int wide = kJoinWarps / split(it.parts);  // column groups a block takes at once
-        return (it.rows + 31) / 32 * ((col_groups + wide - 1) / wide);
+        const int groups = it.parts <= kFewParts ? (R / 16 + kJoinWarps - 1) / kJoinWarps : R / 32;
+        return (it.rows + 31) / 32 * groups;
     };
     griddep_launch_dependents();
     griddep_wait();
@@ -1150,19 +1186,63 @@ __global__ void __launch_bounds__(kJoinThreads)
         const TreeItem it = items[p];
         const int task = f - begins[p];
         const int row_groups = (it.rows + 31) / 32;
-        const int ways = split(it.parts);
-        const int way = warp & (ways - 1);
-        const int cg = task / row_groups * (kJoinWarps / ways) + warp / ways;
         const int row = task % row_groups * 32 + lane;
-        const bool live = row < it.rows && cg < col_groups;
+        // part k of the item: the pair's second slot, then the first slots of the pairs behind
+        const auto slot = [&](int k) -> int64_t {
+            return 2 * static_cast<int64_t>(p + k) + (k == 0 ? 1 : 0);
+        };
+        if (it.parts <= kFewParts) {
+            const int cg = task / row_groups * kJoinWarps + warp;
+            if (row >= it.rows || cg >= R / 16) continue;
+            float4 v[kFewParts][4];
+            float2 s[kFewParts];
+#pragma unroll
+            for (int k = 0; k < kFewParts; ++k) {
+                s[k] = make_float2(-INFINITY, 0.0f);
+                if (k >= it.parts) continue;
+                s[k] = __ldcg(stats + slot(k) * ws.rows + row);
+                const float4* from = parts + (slot(k) * (R / 4) + cg * 4) * ws.rows + row;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[k][i] = __ldcg(from + static_cast<int64_t>(i) * ws.rows);
+            }
+            float top = -INFINITY, total = 0.0f;
+            float o[16] = {};
+#pragma unroll
+            for (int k = 0; k < kFewParts; ++k) top = fmaxf(top, s[k].x);
+#pragma unroll
+            for (int k = 0; k < kFewParts; ++k) {
+                if (k >= it.parts) continue;
+                const float w = s[k].x == -INFINITY ? 0.0f : exp2f(s[k].x - top);
+                total = fmaf(s[k].y, w, total);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[4 * i] = fmaf(v[k][i].x, w, o[4 * i]);
+                    o[4 * i + 1] = fmaf(v[k][i].y, w, o[4 * i + 1]);
+                    o[4 * i + 2] = fmaf(v[k][i].z, w, o[4 * i + 2]);
+                    o[4 * i + 3] = fmaf(v[k][i].w, w, o[4 * i + 3]);
+                }
+            }
+            const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+            uint16_t* out = a.out + (it.first + row) * R + cg * 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                st_v4(out + 8 * i, make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                              pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                              pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                              pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv)));
+            if (a.lse != nullptr && cg == 0)
+                a.lse[it.first + row] = total != 0.0f ? top * kLn2 + logf(total) : -INFINITY;
+            continue;
+        }
+        const int cg = task / row_groups;
+        const bool live = row < it.rows;
         float top = -INFINITY, total = 0.0f;
         float o[32] = {};
         if (live)
-            for (int k = way; k < it.parts; k += ways) {
-                // part k: the pair's second slot, then the first slots of the pairs behind it
-                const int64_t slot = 2 * static_cast<int64_t>(p + k) + (k == 0 ? 1 : 0);
-                const float4* from = parts + (slot * (R / 4) + cg * 8) * ws.rows + row;
-                const float2 s = stats[slot * ws.rows + row];
+#pragma unroll 2
+            for (int k = warp; k < it.parts; k += kJoinWarps) {
+                const float4* from = parts + (slot(k) * (R / 4) + cg * 8) * ws.rows + row;
+                const float2 s = __ldcg(stats + slot(k) * ws.rows + row);
                 float4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = __ldcg(from + static_cast<int64_t>(i) * ws.rows);
@@ -1185,33 +1265,22 @@ __global__ void __launch_bounds__(kJoinThreads)
         for (int i = 0; i < 32; ++i) sums[warp][i][lane] = o[i];
         __syncthreads();
         if (live) {
-            const int w0 = warp - way;
             float m = -INFINITY;
-            for (int k = 0; k < ways; ++k) m = fmaxf(m, tops[w0 + k][lane]);
-            float f[kJoinWarps], sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) m = fmaxf(m, tops[k][lane]);
+            float x[4] = {}, sum = 0.0f;  // four columns a warp
 #pragma unroll
             for (int k = 0; k < kJoinWarps; ++k) {
-                f[k] = 0.0f;
-                if (k < ways) {
-                    const float t = tops[w0 + k][lane];
-                    f[k] = t == -INFINITY ? 0.0f : exp2f(t - m);
-                    sum += totals[w0 + k][lane] * f[k];
-                }
+                const float t = tops[k][lane];
+                const float w = t == -INFINITY ? 0.0f : exp2f(t - m);
+                sum = fmaf(totals[k][lane], w, sum);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = fmaf(sums[k][warp * 4 + e][lane], w, x[e]);
             }
             const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-            const int each = 32 / ways;  // columns
-            uint16_t* out = a.out + (it.first + row) * R + cg * 32 + way * each;
-            for (int c = 0; c < each; c += 4) {
-                float x[4] = {};
-#pragma unroll
-                for (int k = 0; k < kJoinWarps; ++k)
-                    if (k < ways)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] += sums[w0 + k][way * each + c + e][lane] * f[k];
-                *reinterpret_cast<uint2*>(out + c) = make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv),
-                                                                pack_bf16x2(x[2] * inv, x[3] * inv));
-            }
-            if (a.lse != nullptr && cg == 0 && way == 0)
+            *reinterpret_cast<uint2*>(a.out + (it.first + row) * R + cg * 32 + warp * 4) =
+                make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+            if (a.lse != nullptr && cg == 0 && warp == 0)
                 a.lse[it.first + row] = sum != 0.0f ? m * kLn2 + logf(sum) : -INFINITY;
         }
         __syncthreads();
