@@ -951,6 +951,11 @@ pkm_status tree_attention(TreeAttentionArgs a, const void* q, const uint32_t* in
     int vbox = 128;
     while (vbox > 1 && a.page_size % vbox != 0) vbox /= 2;
     const int box = vbox < 64 ? vbox : 64;
+    // loads keep a row as a 32-bit count of 16-byte units inside the layer
+    const int64_t span = a.num_pages * a.page_stride + a.page_size * a.slot_stride;
+    if ((a.qcache_layer != nullptr && span / 16 >= UINT32_MAX - 1) ||
+        (a.qcache_layer == nullptr && box < 8 && span / 8 >= UINT32_MAX - 1))
+        return PKM_ERR_UNSUPPORTED;
     // and, where that is all of them and the row has only whole blocks, several blocks
     const bool whole = a.cols % 64 == 0;
     const bool key_groups = whole && box == 64, value_groups = whole && vbox == 128;

@@ -272,78 +272,74 @@ __device__ __forceinline__ uint2 dequant4(uint32_t codes, float scale) {
     return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// Slot offsets of positions pos0 + 32 k + lane, k < n <= 4: Place::offset of each, with all page
-// ids on their way at once.
-struct Slots {
-    uint32_t id[4];
-    int32_t slot[4];
+// Rows pos0 + 32 k, k < N (pos0 differs from lane to lane): page ids first, all on their way at
+// once, then the slots in 16-byte units of the layer (kNoRow where Place has none).
+constexpr uint32_t kNoRow = 0xffffffffu;
+template <int N>
+struct Rows {
+    uint32_t id[N], unit[N];
 
-    __device__ __forceinline__ void fetch(const TreeAttentionArgs& a, int b, int64_t pos0,
-                                          int64_t kv, int n) {
+    __device__ __forceinline__ void fetch(const TreeAttentionArgs& a, int b, int64_t pos0, int64_t kv) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < N; ++k) {
             const int64_t pos = pos0 + k * 32;
-            const bool have = k < n && pos < kv;
             const int64_t lp = quotient(pos, a.page_size);
-            slot[k] = have ? static_cast<int32_t>(pos - lp * a.page_size) : -1;
-            id[k] = ld_nc_u32_if(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp, have);
+            id[k] = ld_nc_u32_if(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp, pos < kv);
         }
     }
-    __device__ __forceinline__ void offsets(const TreeAttentionArgs& a, int64_t (&rows)[4]) const {
+    // `per`: elements or bytes of a unit
+    __device__ __forceinline__ void resolve(const TreeAttentionArgs& a, int64_t pos0, int64_t kv, int per) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const bool have = slot[k] >= 0 && id[k] < static_cast<uint32_t>(a.num_pages);
-            rows[k] = have ? id[k] * a.page_stride + slot[k] * a.slot_stride : -1;
-            if (!have && slot[k] >= 0) report(a.status, PKM_ERR_OUT_OF_RANGE);
+        for (int k = 0; k < N; ++k) {
+            const int64_t pos = pos0 + k * 32;
+            const int64_t slot = pos - quotient(pos, a.page_size) * a.page_size;
+            const bool have = pos < kv && id[k] < static_cast<uint32_t>(a.num_pages);
+            unit[k] = have ? static_cast<uint32_t>((id[k] * a.page_stride + slot * a.slot_stride) / per)
+                           : kNoRow;
+            if (!have && pos < kv) report(a.status, PKM_ERR_OUT_OF_RANGE);
         }
     }
 };
 
-// Sixteen columns c .. c+15 of a latent row on their way from the cache to shared memory.  Past
-// the row's columns and for rows that do not exist (offset -1): zeros.
+// A lane's columns of a latent row on their way from the cache to shared memory: 16 from c on,
+// or, where the block is `narrow`, 8.  Past the row's columns and without a row: zeros.
 template <Source SRC>
 struct Piece {  // bf16 columns
-    static constexpr int kCount = 2;  // pieces a step (8 rows each)
+    static constexpr int kCount = 2, kPer = 8;  // pieces a step (8 rows each), elements a unit
     uint4 lo, hi;
 
-    __device__ __forceinline__ void load(const TreeAttentionArgs& a, int64_t row, int c) {
-        const uint16_t* p = a.cache_layer + row + c;
-        lo = ld_nc_v4_if(p, row >= 0 && c < a.cols);
-        hi = ld_nc_v4_if(p + 8, row >= 0 && c + 8 < a.cols);
+    __device__ __forceinline__ void load(const TreeAttentionArgs& a, uint32_t unit, int c, bool) {
+        const uint16_t* p = a.cache_layer + static_cast<int64_t>(unit) * kPer + c;
+        lo = ld_nc_v4_if(p, unit != kNoRow && c < a.cols);
+        hi = ld_nc_v4_if(p + 8, unit != kNoRow && c + 8 < a.cols);
     }
-    __device__ __forceinline__ void columns(const TreeAttentionArgs&, int64_t, int, uint4& l,
-                                            uint4& h) const {
+    __device__ __forceinline__ void columns(bool, uint4& l, uint4& h) const {
         l = lo;
         h = hi;
     }
 };
 
 template <>
-struct Piece<kCodes> {  // codes and their scale; the rope columns, bf16, are loaded when stored
-    static constexpr int kCount = 4;
+struct Piece<kCodes> {  // 16 codes and their scale, or (narrow) 8 rope columns
+    static constexpr int kCount = 4, kPer = 16;
     uint4 codes;
-    float scale;
+    uint32_t scale;
 
-    __device__ __forceinline__ void load(const TreeAttentionArgs& a, int64_t row, int c) {
+    __device__ __forceinline__ void load(const TreeAttentionArgs& a, uint32_t unit, int c, bool narrow) {
         const int R = a.kv_lora_rank;
-        const uint8_t* p = a.qcache_layer + row;
-        const bool have = row >= 0 && c < R;
-        codes = ld_nc_v4_if(p + c, have);
-        scale = __uint_as_float(ld_nc_u32_if(p + R + 2 * (a.cols - R) + 4 * (c / 128), have));
+        const uint8_t* p = a.qcache_layer + static_cast<int64_t>(unit) * kPer;
+        const bool have = unit != kNoRow && c < a.cols;
+        codes = ld_nc_v4_if(p + (narrow ? R + 2 * (c - R) : c), have);
+        scale = ld_nc_u32_if(p + R + 2 * (a.cols - R) + 4 * (c / 128), have && !narrow);
     }
-    __device__ __forceinline__ void columns(const TreeAttentionArgs& a, int64_t row, int c,
-                                            uint4& l, uint4& h) const {
-        const int R = a.kv_lora_rank;
-        if (c < R) {  // the same in all lanes: blocks of 64 columns are codes or rope columns
-            const uint2 d0 = dequant4(codes.x, scale), d1 = dequant4(codes.y, scale);
-            const uint2 d2 = dequant4(codes.z, scale), d3 = dequant4(codes.w, scale);
-            l = make_uint4(d0.x, d0.y, d1.x, d1.y);
-            h = make_uint4(d2.x, d2.y, d3.x, d3.y);
-            return;
-        }
-        const uint8_t* p = a.qcache_layer + row + R + 2 * (c - R);
-        l = ld_nc_v4_if(p, row >= 0 && c < a.cols);
-        h = ld_nc_v4_if(p + 16, row >= 0 && c + 8 < a.cols);
+    __device__ __forceinline__ void columns(bool narrow, uint4& l, uint4& h) const {
+        l = codes;
+        if (narrow) return;
+        const float f = __uint_as_float(scale);
+        const uint2 d0 = dequant4(codes.x, f), d1 = dequant4(codes.y, f);
+        const uint2 d2 = dequant4(codes.z, f), d3 = dequant4(codes.w, f);
+        l = make_uint4(d0.x, d0.y, d1.x, d1.y);
+        h = make_uint4(d2.x, d2.y, d3.x, d3.y);
     }
 };
 
@@ -398,6 +394,138 @@ __device__ __forceinline__ bool plain_wait(uint64_t* bar, uint32_t parity, uint3
 __device__ __forceinline__ void gave_up(const WaitCtl& wc) {
     report(wc.status, PKM_ERR_TIMEOUT);
     *wc.abort_flag = 1;
+}
+
+// Key (KEYS) or value warp i of a CTA whose rows come by loads: blocks i, i + 4 and i + 8 of the
+// keys, or block i of the values.  Four lanes take a row's columns, eight rows at a time; two
+// steps of a few rows are in flight: while one is converted and stored, the next one's rows are
+// on their way.  `queries(w)` runs once an item, behind its first tile.
+template <Source SRC, bool KEYS, typename Queries>
+__device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars, uint8_t* smem,
+                                         uint32_t rank, int i, int kblocks, int vgroups, int col0,
+                                         uint32_t full, uint32_t tries, const WaitCtl& wc,
+                                         const Queries& queries) {
+    constexpr int kPieces = Piece<SRC>::kCount, kRowsAtOnce = 8 * kPieces;
+    constexpr int kRows32 = KEYS ? 2 : 4;  // groups of 32 rows
+    constexpr int kPerBlock = kRows32 * 32 / kRowsAtOnce;
+    const int lane = threadIdx.x & 31, sub = lane >> 2, part = lane & 3;
+    const int blocks = KEYS ? (kblocks - i + 3) / 4 : 1;  // of this warp
+    const bool any = KEYS ? i < kblocks : i < 2 * vgroups;
+    // a quantised row's rope columns lie as bf16 values: half a block a step
+    const auto narrow = [&](int blk) { return SRC == kCodes && KEYS && blk * 64 >= a.kv_lora_rank; };
+    const auto steps_of = [&](int blk) { return narrow(blk) ? 2 * kPerBlock : kPerBlock; };
+    RingPos ring;
+    if (!KEYS && i >= 2) ring.next(kValueRing);
+    uint32_t g = 0;
+    bool ok = true;
+    Walk w(bars);
+    while (ok && __any_sync(0xffffffffu, w.next(a))) {
+        const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
+        if (!any) {  // fewer blocks than warps
+            ok = queries(w);
+            continue;
+        }
+        int64_t pos0 = static_cast<int64_t>(w.kt0) * kKeys + (KEYS ? rank * 64 : 0u) + lane;
+        Rows<kRows32> rows;
+        rows.fetch(a, w.b, pos0, w.r.kv);
+        int l_t = 0, l_n = 0, l_step = 0;  // the step to be loaded: tile, block of the warp, step
+        int s_t = 0, s_n = 0, s_step = 0;  // the step to be stored
+        Piece<SRC> x[2][kPieces];
+        const auto load = [&](Piece<SRC>(&p)[kPieces]) {
+            if (l_t == tiles) return;
+            if (l_n == 0 && l_step == 0) {
+                rows.resolve(a, pos0, w.r.kv, Piece<SRC>::kPer);
+                pos0 += kKeys;
+                rows.fetch(a, w.b, pos0, w.r.kv);  // for the next tile
+            }
+            const int blk = i + 4 * l_n;
+            const bool thin = narrow(blk);
+            const int r0 = (thin ? l_step % kPerBlock : l_step) * kRowsAtOnce;
+            const int c = (KEYS ? 0 : col0) + blk * 64 +
+                          (thin ? l_step / kPerBlock * 32 + part * 8 : part * 16);
+            uint32_t unit = rows.unit[0];
+#pragma unroll
+            for (int k = 1; k < kRows32; ++k)
+                if (r0 >= 32 * k) unit = rows.unit[k];
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+                p[k].load(a, __shfl_sync(0xffffffffu, unit, (r0 & 31) + k * 8 + sub), c, thin);
+            if (++l_step == steps_of(blk)) {
+                l_step = 0;
+                if (++l_n == blocks) {
+                    l_n = 0;
+                    ++l_t;
+                }
+            }
+        };
+        const auto store = [&](Piece<SRC>(&p)[kPieces]) {
+            const int blk = i + 4 * s_n;
+            const uint32_t group = !KEYS ? ring.stage : blk < kQueryBlocks ? 0 : 1;
+            if (s_step == 0) {
+                ok = __all_sync(0xffffffffu,
+                                plain_wait(KEYS ? &bars->k_empty[group] : &bars->v_empty[group],
+                                           KEYS ? (g & 1) ^ 1 : ring.phase ^ 1, tries));
+                if (!ok) {
+                    gave_up(wc);
+                    return;
+                }
+            }
+            const bool thin = narrow(blk);
+            const int r0 = (thin ? s_step % kPerBlock : s_step) * kRowsAtOnce;
+            const int chunk = thin ? s_step / kPerBlock * 4 + part : part * 2;
+            const uint32_t dst =
+                smem_u32(smem) + (KEYS ? kOffK + blk * kBlockBytes
+                                       : kOffV + group * 2 * kValueBytes + (i & 1) * kValueBytes);
+            uint4 lo[kPieces], hi[kPieces];
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) p[k].columns(thin, lo[k], hi[k]);
+            if (!KEYS && w.kt0 + s_t >= w.cached_tiles()) {
+                // as in the loads by TMA, drafts' infinities and NaN are no values
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) {
+                    if (static_cast<int64_t>(w.kt0 + s_t) * kKeys + r0 + k * 8 + sub < w.r.len) continue;
+                    lo[k] = finite8(lo[k]);
+                    hi[k] = finite8(hi[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int key = r0 + k * 8 + sub;
+                const uint32_t row = dst + key * 128;
+                st_shared_v4(row + ((chunk ^ (key & 7)) << 4), lo[k].x, lo[k].y, lo[k].z, lo[k].w);
+                if (!thin)
+                    st_shared_v4(row + (((chunk + 1) ^ (key & 7)) << 4), hi[k].x, hi[k].y, hi[k].z,
+                                 hi[k].w);
+            }
+            if (++s_step < steps_of(blk)) return;
+            s_step = 0;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(full + group * 8);
+            if (++s_n < blocks) return;
+            s_n = 0;
+            ++s_t;
+            ++g;
+            if (KEYS && i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
+            for (int v = 0; v < vgroups; ++v) ring.next(kValueRing);
+        };
+        load(x[0]);
+        load(x[1]);
+        bool asked = false;
+        while (ok && s_t < tiles) {  // an even number of steps a tile
+            store(x[0]);
+            if (!ok) break;
+            load(x[0]);
+            store(x[1]);
+            if (!ok) break;
+            load(x[1]);
+            if (!asked && s_t > 0) {
+                ok = queries(w);
+                asked = true;
+            }
+        }
+    }
+    if (KEYS && !ok && lane == 0) bars->progress = INT32_MAX;
 }
 
 template <Source SRC>
@@ -989,128 +1117,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok) spin_ns(kDrainNs);
         } else {
-            // By loads, a few rows of a block a step: four lanes take a row's 64 columns, 16
-            // each, eight rows at a time.  Two steps are in flight: while one is converted and
-            // stored, the next one's rows are on their way.
-            constexpr int kPieces = Piece<SRC>::kCount, kRowsAtOnce = 8 * kPieces;
-            const int per_block = (keys ? 64 : kKeys) / kRowsAtOnce;
-            RingPos ring;
-            if (!keys && i >= 2) ring.next(kValueRing);
-            const int sub = lane >> 2, part = lane & 3;
-            Walk ahead(bars);
-            int tiles = 0, t = 0, blk = i, step = 0;              // the step to be stored
-            int a_tiles = 0, a_t = 0, a_blk = i, a_step = 0;      // the step to be loaded
-            bool a_more = true;
-            int64_t rows[4];       // offsets of rows lane, 32 + lane, ... of the loaded tile
-            Slots slots;
-            Piece<SRC> x[2][kPieces];
-            int64_t from[2];       // the step's row offsets, one in each of its lanes
-            const int blocks = keys ? kblocks : i + 1;
-            const bool any = keys ? i < kblocks : i < 2 * vgroups;
-            const auto load = [&](Piece<SRC>(&p)[kPieces], int64_t& mine) {
-                if (a_t == a_tiles) {
-                    a_more = a_more && __any_sync(0xffffffffu, ahead.next(a));
-                    if (!a_more) return;
-                    a_tiles = ahead.kt1 - ahead.kt0;
-                    a_t = 0;
-                }
-                if (a_blk == i && a_step == 0) {
-                    const int64_t pos0 = static_cast<int64_t>(ahead.kt0 + a_t) * kKeys +
-                                         (keys ? rank * 64 : 0u) + lane;
-                    if (a_t == 0) slots.fetch(a, ahead.b, pos0, ahead.r.kv, keys ? 2 : 4);
-                    slots.offsets(a, rows);
-                    // the next tile's page ids, while this one is loaded
-                    slots.fetch(a, ahead.b, pos0 + kKeys, ahead.r.kv, keys ? 2 : 4);
-                }
-                const int r0 = a_step * kRowsAtOnce;
-                mine = r0 < 32 ? rows[0] : r0 < 64 ? rows[1] : r0 < 96 ? rows[2] : rows[3];
-                const int c = (keys ? 0 : col0) + a_blk * 64 + part * 16;
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k)
-                    p[k].load(a, __shfl_sync(0xffffffffu, mine, (r0 & 31) + k * 8 + sub), c);
-                if (++a_step == per_block) {
-                    a_step = 0;
-                    a_blk += 4;
-                    if (a_blk >= blocks) {
-                        a_blk = i;
-                        ++a_t;
-                    }
-                }
-            };
-            const auto all_queries = [&](const Walk& w) {
+            // By loads, a few rows of a block a step: four lanes take a row's columns, eight rows
+            // at a time.  Two steps are in flight: while one is converted and stored, the next
+            // one's rows are on their way.
+            if (keys) by_loads<SRC, true>(a, bars, smem, rank, i, kblocks, vgroups, col0, k_full, tries, wc, [&](const Walk& w) {
                 uint32_t q[kAtOnce][32];
                 fetch(w, 0, q);
                 return queries(w, q);
-            };
-            const auto store = [&](Piece<SRC>(&p)[kPieces], int64_t mine) {
-                const uint32_t group = !keys ? ring.stage : blk < kQueryBlocks ? 0 : 1;
-                uint64_t* empty = keys ? &bars->k_empty[group] : &bars->v_empty[group];
-                if (step == 0) {
-                    ok = issue_wait(empty, keys ? (g & 1) ^ 1 : ring.phase ^ 1);
-                    if (!ok) return;
-                }
-                const uint32_t dst = smem_u32(keys ? sK + blk * kBlockBytes
-                                                   : sV + group * 2 * kValueBytes + (i & 1) * kValueBytes);
-                const int c = (keys ? 0 : col0) + blk * 64 + part * 16;
-                const int r0 = step * kRowsAtOnce;
-                uint4 lo[kPieces], hi[kPieces];
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k)
-                    p[k].columns(a, SRC == kCodes ? __shfl_sync(0xffffffffu, mine, ((r0 & 31) + k * 8 + sub)) : 0,
-                                 c, lo[k], hi[k]);
-                if (!keys && w.kt0 + t >= w.cached_tiles()) {
-                    // as in the loads by TMA, drafts' infinities and NaN are no values
-#pragma unroll
-                    for (int k = 0; k < kPieces; ++k) {
-                        const int64_t pos =
-                            static_cast<int64_t>(w.kt0 + t) * kKeys + r0 + k * 8 + sub;
-                        if (pos < w.r.len) continue;
-                        lo[k] = finite8(lo[k]);
-                        hi[k] = finite8(hi[k]);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k) {
-                    const int key = r0 + k * 8 + sub;
-                    const uint32_t row = dst + key * 128;
-                    st_shared_v4(row + (((2 * part) ^ (key & 7)) << 4), lo[k].x, lo[k].y, lo[k].z, lo[k].w);
-                    st_shared_v4(row + (((2 * part + 1) ^ (key & 7)) << 4), hi[k].x, hi[k].y, hi[k].z, hi[k].w);
-                }
-                if (++step < per_block) return;
-                step = 0;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote((keys ? k_full : v_full) + group * 8);
-                blk += 4;
-                if (blk < blocks) return;
-                blk = i;
-                if (keys && t == 0) ok = all_queries(w);
-                ++t;
-                ++g;
-                if (keys && i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
-                for (int v = 0; v < vgroups; ++v) ring.next(kValueRing);
-            };
-            if (any) {
-                load(x[0], from[0]);
-                load(x[1], from[1]);
-                while (ok) {
-                    if (t == tiles) {
-                        if (!__any_sync(0xffffffffu, w.next(a))) break;
-                        tiles = w.kt1 - w.kt0;
-                        t = 0;
-                    }
-                    // an even number of steps a tile: the buffers keep their turn
-                    store(x[0], from[0]);
-                    if (!ok) break;
-                    load(x[0], from[0]);
-                    store(x[1], from[1]);
-                    if (!ok) break;
-                    load(x[1], from[1]);
-                }
-            } else if (keys) {  // fewer blocks than warps: the queries alone
-                while (ok && __any_sync(0xffffffffu, w.next(a))) ok = all_queries(w);
-            }
-            if (!ok && lane == 0) bars->progress = INT32_MAX;
+            });
+            else by_loads<SRC, false>(a, bars, smem, rank, i, kblocks, vgroups, col0, v_full, tries, wc, [](const Walk&) { return true; });
         }
     }
 
