@@ -272,44 +272,69 @@ __device__ __forceinline__ uint2 dequant4(uint32_t codes, float scale) {
     return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// Rows pos0 + 32 k, k < N (pos0 differs from lane to lane): page ids first, all on their way at
-// once, then the slots in 16-byte units of the layer (kNoRow where Place has none).
+// Rows pos0 + 32 k, k < N (pos0 differs from lane to lane), moved on a tile at a time: page ids
+// first, all on their way at once, then the slots in 16-byte units of the layer (kNoRow where
+// Place has none).
 constexpr uint32_t kNoRow = 0xffffffffu;
 template <int N>
 struct Rows {
+    int64_t pos;        // of k = 0
+    int32_t page[N], slot[N];
     uint32_t id[N], unit[N];
 
-    __device__ __forceinline__ void fetch(const TreeAttentionArgs& a, int b, int64_t pos0, int64_t kv) {
+    __device__ __forceinline__ void start(const TreeAttentionArgs& a, int64_t pos0) {
+        pos = pos0;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int64_t pos = pos0 + k * 32;
-            const int64_t lp = quotient(pos, a.page_size);
-            id[k] = ld_nc_u32_if(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp, pos < kv);
-        }
+        for (int k = 0; k < N; ++k) locate(a, k);
     }
-    // `per`: elements or bytes of a unit
-    __device__ __forceinline__ void resolve(const TreeAttentionArgs& a, int64_t pos0, int64_t kv, int per) {
+    __device__ __forceinline__ void locate(const TreeAttentionArgs& a, int k) {
+        const int64_t lp = quotient(pos + k * 32, a.page_size);
+        page[k] = static_cast<int32_t>(lp);
+        slot[k] = static_cast<int32_t>(pos + k * 32 - lp * a.page_size);
+    }
+    __device__ __forceinline__ void fetch(const TreeAttentionArgs& a, int b, int64_t kv) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            id[k] = ld_nc_u32_if(a.page_table + static_cast<int64_t>(b) * a.max_pages + page[k],
+                                 pos + k * 32 < kv);
+    }
+    // Units of the rows fetched, then on to the next tile's.  `unit_shift`: log2 of the elements
+    // or bytes of a unit.
+    __device__ __forceinline__ void resolve(const TreeAttentionArgs& a, int64_t kv, int unit_shift) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const int64_t pos = pos0 + k * 32;
-            const int64_t slot = pos - quotient(pos, a.page_size) * a.page_size;
-            const bool have = pos < kv && id[k] < static_cast<uint32_t>(a.num_pages);
-            unit[k] = have ? static_cast<uint32_t>((id[k] * a.page_stride + slot * a.slot_stride) / per)
+            const bool exists = pos + k * 32 < kv;
+            const bool have = exists && id[k] < static_cast<uint32_t>(a.num_pages);
+            unit[k] = have ? static_cast<uint32_t>((id[k] * a.page_stride + slot[k] * a.slot_stride) >>
+                                                   unit_shift)
                            : kNoRow;
-            if (!have && pos < kv) report(a.status, PKM_ERR_OUT_OF_RANGE);
+            if (exists && !have) report(a.status, PKM_ERR_OUT_OF_RANGE);
+        }
+        pos += kKeys;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (a.page_size < 32) {
+                locate(a, k);
+                continue;
+            }
+            slot[k] += kKeys;
+            while (slot[k] >= a.page_size) {
+                slot[k] -= a.page_size;
+                ++page[k];
+            }
         }
     }
 };
 
 // A lane's columns of a latent row on their way from the cache to shared memory: 16 from c on,
-// or, where the block is `narrow`, 8.  Past the row's columns and without a row: zeros.
+// or, where the step is `thin`, 8.  Past the row's columns and without a row: zeros.
 template <Source SRC>
 struct Piece {  // bf16 columns
-    static constexpr int kCount = 2, kPer = 8;  // pieces a step (8 rows each), elements a unit
+    static constexpr int kCount = 2, kShift = 3;  // pieces a step (8 rows each), elements a unit
     uint4 lo, hi;
 
     __device__ __forceinline__ void load(const TreeAttentionArgs& a, uint32_t unit, int c, bool) {
-        const uint16_t* p = a.cache_layer + static_cast<int64_t>(unit) * kPer + c;
+        const uint16_t* p = a.cache_layer + (static_cast<int64_t>(unit) << kShift) + c;
         lo = ld_nc_v4_if(p, unit != kNoRow && c < a.cols);
         hi = ld_nc_v4_if(p + 8, unit != kNoRow && c + 8 < a.cols);
     }
@@ -320,21 +345,21 @@ struct Piece {  // bf16 columns
 };
 
 template <>
-struct Piece<kCodes> {  // 16 codes and their scale, or (narrow) 8 rope columns
-    static constexpr int kCount = 4, kPer = 16;
+struct Piece<kCodes> {  // 16 codes and their scale, or (thin) 8 rope columns
+    static constexpr int kCount = 4, kShift = 4;
     uint4 codes;
     uint32_t scale;
 
-    __device__ __forceinline__ void load(const TreeAttentionArgs& a, uint32_t unit, int c, bool narrow) {
+    __device__ __forceinline__ void load(const TreeAttentionArgs& a, uint32_t unit, int c, bool thin) {
         const int R = a.kv_lora_rank;
-        const uint8_t* p = a.qcache_layer + static_cast<int64_t>(unit) * kPer;
+        const uint8_t* p = a.qcache_layer + (static_cast<int64_t>(unit) << kShift);
         const bool have = unit != kNoRow && c < a.cols;
-        codes = ld_nc_v4_if(p + (narrow ? R + 2 * (c - R) : c), have);
-        scale = ld_nc_u32_if(p + R + 2 * (a.cols - R) + 4 * (c / 128), have && !narrow);
+        codes = ld_nc_v4_if(p + (thin ? R + 2 * (c - R) : c), have);
+        scale = ld_nc_u32_if(p + R + 2 * (a.cols - R) + 4 * (c / 128), have && !thin);
     }
-    __device__ __forceinline__ void columns(bool narrow, uint4& l, uint4& h) const {
+    __device__ __forceinline__ void columns(bool thin, uint4& l, uint4& h) const {
         l = codes;
-        if (narrow) return;
+        if (thin) return;
         const float f = __uint_as_float(scale);
         const uint2 d0 = dequant4(codes.x, f), d1 = dequant4(codes.y, f);
         const uint2 d2 = dequant4(codes.z, f), d3 = dequant4(codes.w, f);
@@ -396,136 +421,138 @@ __device__ __forceinline__ void gave_up(const WaitCtl& wc) {
     *wc.abort_flag = 1;
 }
 
-// Key (KEYS) or value warp i of a CTA whose rows come by loads: blocks i, i + 4 and i + 8 of the
-// keys, or block i of the values.  Four lanes take a row's columns, eight rows at a time; two
-// steps of a few rows are in flight: while one is converted and stored, the next one's rows are
-// on their way.  `queries(w)` runs once an item, behind its first tile.
-template <Source SRC, bool KEYS, typename Queries>
+// Key or value warp i of a CTA whose rows come by loads: blocks i, i + 4 and i + 8 of the keys,
+// or block i of the values.  Four lanes take a row's columns, eight rows at a time; two steps of
+// a few rows are in flight: while one is converted and stored, the next one's rows are on their
+// way.  A quantised row's rope columns lie as bf16 values; of their blocks every key warp brings
+// 16 rows in two thin steps.  `queries(w)` runs once an item, right behind its first tile, whose
+// scores wait for it and free the keys' place for the second.
+// One copy of this code serves keys and values: two of them, with the loads and stores unrolled
+// further, left the warps waiting for instructions for a third of their time.
+template <Source SRC, typename Queries>
 __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars, uint8_t* smem,
-                                         uint32_t rank, int i, int kblocks, int vgroups, int col0,
-                                         uint32_t full, uint32_t tries, const WaitCtl& wc,
-                                         const Queries& queries) {
+                                         uint32_t rank, const bool keys, int i, int kblocks,
+                                         int vgroups, int col0, uint32_t full, uint32_t tries,
+                                         const WaitCtl& wc, const Queries& queries) {
     constexpr int kPieces = Piece<SRC>::kCount, kRowsAtOnce = 8 * kPieces;
-    constexpr int kRows32 = KEYS ? 2 : 4;  // groups of 32 rows
-    constexpr int kPerBlock = kRows32 * 32 / kRowsAtOnce;
     const int lane = threadIdx.x & 31, sub = lane >> 2, part = lane & 3;
-    const int blocks = KEYS ? (kblocks - i + 3) / 4 : 1;  // of this warp
-    const bool any = KEYS ? i < kblocks : i < 2 * vgroups;
-    // a quantised row's rope columns lie as bf16 values: half a block a step
-    const auto narrow = [&](int blk) { return SRC == kCodes && KEYS && blk * 64 >= a.kv_lora_rank; };
-    const auto steps_of = [&](int blk) { return narrow(blk) ? 2 * kPerBlock : kPerBlock; };
+    const int per_block = (keys ? 64 : kKeys) / kRowsAtOnce;  // steps, an even number
+    const int wide_blocks = SRC == kCodes && keys ? a.kv_lora_rank / 64 : kblocks;
+    const int mine = !keys ? 1 : i < wide_blocks ? (wide_blocks - i + 3) / 4 : 0;
+    const int wide_steps = mine * per_block;
+    const int steps = !keys ? (i < 2 * vgroups ? wide_steps : 0) : wide_steps + 2 * (kblocks - wide_blocks);
+    uint64_t* empty = keys ? bars->k_empty : bars->v_empty;
     RingPos ring;
-    if (!KEYS && i >= 2) ring.next(kValueRing);
+    if (!keys && i >= 2) ring.next(kValueRing);
     uint32_t g = 0;
     bool ok = true;
     Walk w(bars);
     while (ok && __any_sync(0xffffffffu, w.next(a))) {
         const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
-        if (!any) {  // fewer blocks than warps
-            ok = queries(w);
+        if (steps == 0) {  // fewer blocks than warps
+            if (keys) ok = queries(w);
             continue;
         }
-        int64_t pos0 = static_cast<int64_t>(w.kt0) * kKeys + (KEYS ? rank * 64 : 0u) + lane;
-        Rows<kRows32> rows;
-        rows.fetch(a, w.b, pos0, w.r.kv);
-        int l_t = 0, l_n = 0, l_step = 0;  // the step to be loaded: tile, block of the warp, step
-        int s_t = 0, s_n = 0, s_step = 0;  // the step to be stored
+        Rows<4> rows;  // keys: two groups of 32
+        rows.start(a, static_cast<int64_t>(w.kt0) * kKeys + (keys ? rank * 64 : 0u) + lane);
+        const int64_t kv = w.r.kv;
+        rows.fetch(a, w.b, kv);
+        int l_t = 0, l_step = 0, l_blk = i, l_in = 0;  // the step to be loaded
+        int s_t = 0, s_step = 0, s_blk = i, s_in = 0;  // the step to be stored
+        // block and step in it of the next step of a tile
+        const auto move = [&](int& t, int& step, int& blk, int& in) {
+            ++step;
+            ++in;
+            if (step == steps) {
+                step = 0;
+                ++t;
+                blk = wide_steps > 0 ? i : wide_blocks;
+                in = 0;
+            } else if (step <= wide_steps ? in == per_block : in == 2) {
+                in = 0;
+                blk = step < wide_steps ? blk + 4 : step == wide_steps ? wide_blocks : blk + 1;
+            }
+        };
+        if (wide_steps == 0) l_blk = s_blk = wide_blocks;
         Piece<SRC> x[2][kPieces];
         const auto load = [&](Piece<SRC>(&p)[kPieces]) {
             if (l_t == tiles) return;
-            if (l_n == 0 && l_step == 0) {
-                rows.resolve(a, pos0, w.r.kv, Piece<SRC>::kPer);
-                pos0 += kKeys;
-                rows.fetch(a, w.b, pos0, w.r.kv);  // for the next tile
+            if (l_step == 0) {
+                rows.resolve(a, kv, Piece<SRC>::kShift);
+                rows.fetch(a, w.b, kv);  // for the next tile
             }
-            const int blk = i + 4 * l_n;
-            const bool thin = narrow(blk);
-            const int r0 = (thin ? l_step % kPerBlock : l_step) * kRowsAtOnce;
-            const int c = (KEYS ? 0 : col0) + blk * 64 +
-                          (thin ? l_step / kPerBlock * 32 + part * 8 : part * 16);
-            uint32_t unit = rows.unit[0];
+            const bool thin = l_step >= wide_steps;
+            const int r0 = thin ? 16 * i : l_in * kRowsAtOnce;
+            const int c = (keys ? 0 : col0) + l_blk * 64 + (thin ? l_in * 32 + part * 8 : part * 16);
+            const uint32_t unit = r0 < 32   ? rows.unit[0]
+                                  : r0 < 64 ? rows.unit[1]
+                                  : r0 < 96 ? rows.unit[2]
+                                            : rows.unit[3];
 #pragma unroll
-            for (int k = 1; k < kRows32; ++k)
-                if (r0 >= 32 * k) unit = rows.unit[k];
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k)
-                p[k].load(a, __shfl_sync(0xffffffffu, unit, (r0 & 31) + k * 8 + sub), c, thin);
-            if (++l_step == steps_of(blk)) {
-                l_step = 0;
-                if (++l_n == blocks) {
-                    l_n = 0;
-                    ++l_t;
-                }
+            for (int k = 0; k < kPieces; ++k) {
+                const uint32_t u = __shfl_sync(0xffffffffu, unit, ((r0 & 31) + k * 8 + sub) & 31);
+                p[k].load(a, thin && k >= 2 ? kNoRow : u, c, thin);
             }
+            move(l_t, l_step, l_blk, l_in);
         };
         const auto store = [&](Piece<SRC>(&p)[kPieces]) {
-            const int blk = i + 4 * s_n;
-            const uint32_t group = !KEYS ? ring.stage : blk < kQueryBlocks ? 0 : 1;
-            if (s_step == 0) {
+            const bool thin = s_step >= wide_steps;
+            const uint32_t group = !keys ? ring.stage : s_blk < kQueryBlocks ? 0 : 1;
+            if (s_in == 0) {
                 ok = __all_sync(0xffffffffu,
-                                plain_wait(KEYS ? &bars->k_empty[group] : &bars->v_empty[group],
-                                           KEYS ? (g & 1) ^ 1 : ring.phase ^ 1, tries));
+                                plain_wait(&empty[group], (keys ? g & 1 : ring.phase) ^ 1, tries));
                 if (!ok) {
                     gave_up(wc);
                     return;
                 }
             }
-            const bool thin = narrow(blk);
-            const int r0 = (thin ? s_step % kPerBlock : s_step) * kRowsAtOnce;
-            const int chunk = thin ? s_step / kPerBlock * 4 + part : part * 2;
+            const int r0 = thin ? 16 * i : s_in * kRowsAtOnce;
+            // 16-byte chunk c of row r lies at chunk c ^ (r & 7), and the rows here are sub + 8 n
             const uint32_t dst =
-                smem_u32(smem) + (KEYS ? kOffK + blk * kBlockBytes
-                                       : kOffV + group * 2 * kValueBytes + (i & 1) * kValueBytes);
-            uint4 lo[kPieces], hi[kPieces];
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k) p[k].columns(thin, lo[k], hi[k]);
-            if (!KEYS && w.kt0 + s_t >= w.cached_tiles()) {
-                // as in the loads by TMA, drafts' infinities and NaN are no values
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k) {
-                    if (static_cast<int64_t>(w.kt0 + s_t) * kKeys + r0 + k * 8 + sub < w.r.len) continue;
-                    lo[k] = finite8(lo[k]);
-                    hi[k] = finite8(hi[k]);
-                }
-            }
+                smem_u32(smem) + sub * 128 + r0 * 128 +
+                (keys ? kOffK + s_blk * kBlockBytes
+                      : kOffV + group * 2 * kValueBytes + (i & 1) * kValueBytes);
+            const uint32_t c0 = ((thin ? s_in * 4 + part : part * 2) ^ sub) << 4;
+            const uint32_t c1 = ((part * 2 + 1) ^ sub) << 4;
+            const bool drafts = !keys && w.kt0 + s_t >= w.cached_tiles();
 #pragma unroll
             for (int k = 0; k < kPieces; ++k) {
-                const int key = r0 + k * 8 + sub;
-                const uint32_t row = dst + key * 128;
-                st_shared_v4(row + ((chunk ^ (key & 7)) << 4), lo[k].x, lo[k].y, lo[k].z, lo[k].w);
-                if (!thin)
-                    st_shared_v4(row + (((chunk + 1) ^ (key & 7)) << 4), hi[k].x, hi[k].y, hi[k].z,
-                                 hi[k].w);
+                uint4 lo, hi;
+                p[k].columns(thin, lo, hi);
+                if (drafts) {
+                    // as in the loads by TMA, drafts' infinities and NaN are no values
+                    if (static_cast<int64_t>(w.kt0 + s_t) * kKeys + r0 + k * 8 + sub >= w.r.len) {
+                        lo = finite8(lo);
+                        hi = finite8(hi);
+                    }
+                }
+                if (!thin || k < 2) st_shared_v4(dst + k * 1024 + c0, lo.x, lo.y, lo.z, lo.w);
+                if (!thin) st_shared_v4(dst + k * 1024 + c1, hi.x, hi.y, hi.z, hi.w);
             }
-            if (++s_step < steps_of(blk)) return;
-            s_step = 0;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(full + group * 8);
-            if (++s_n < blocks) return;
-            s_n = 0;
-            ++s_t;
+            if (s_in == (thin ? 1 : per_block - 1)) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(full + group * 8);
+            }
+            move(s_t, s_step, s_blk, s_in);
+            if (s_step > 0) return;
             ++g;
-            if (KEYS && i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
+            if (keys && i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
             for (int v = 0; v < vgroups; ++v) ring.next(kValueRing);
         };
-        load(x[0]);
-        load(x[1]);
-        bool asked = false;
-        while (ok && s_t < tiles) {  // an even number of steps a tile
-            store(x[0]);
+        const int pairs = tiles * (steps / 2);
+#pragma unroll 1
+        for (int n = -1; ok && n < pairs; ++n) {  // first two loads without stores
+            if (n >= 0) store(x[0]);
             if (!ok) break;
             load(x[0]);
-            store(x[1]);
+            if (n >= 0) store(x[1]);
             if (!ok) break;
             load(x[1]);
-            if (!asked && s_t > 0) {
-                ok = queries(w);
-                asked = true;
-            }
+            if (keys && n == steps / 2 - 1) ok = queries(w);
         }
     }
-    if (KEYS && !ok && lane == 0) bars->progress = INT32_MAX;
+    if (keys && !ok && lane == 0) bars->progress = INT32_MAX;
 }
 
 template <Source SRC>
@@ -563,9 +590,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kKeyGroups; ++i) {
             // one box: one arrival, with the bytes; boxes of a block: one each; by loads: one
-            // for each block and CTA
-            const int blocks = max(i == 0 ? min(kblocks, kQueryBlocks) : kblocks - kQueryBlocks, 1);
-            mbar_init(&bars->k_full[i], SRC != kTma ? 2 * blocks : tb.key_blocks > 1 ? 1 : blocks);
+            // for each block and CTA, four for a block of rope columns
+            const int from = i == 0 ? 0 : kQueryBlocks, to = i == 0 ? min(kblocks, kQueryBlocks) : kblocks;
+            const int blocks = max(to - from, 1);
+            const int thin = SRC == kCodes ? max(to - max(from, R / 64), 0) : 0;
+            mbar_init(&bars->k_full[i], SRC != kTma          ? 2 * (blocks + 3 * thin)
+                                        : tb.key_blocks > 1 ? 1
+                                                            : blocks);
             mbar_init(&bars->k_empty[i], 1);
         }
         for (int i = 0; i < kValueRing; ++i) {
@@ -1117,15 +1148,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok) spin_ns(kDrainNs);
         } else {
-            // By loads, a few rows of a block a step: four lanes take a row's columns, eight rows
-            // at a time.  Two steps are in flight: while one is converted and stored, the next
-            // one's rows are on their way.
-            if (keys) by_loads<SRC, true>(a, bars, smem, rank, i, kblocks, vgroups, col0, k_full, tries, wc, [&](const Walk& w) {
-                uint32_t q[kAtOnce][32];
-                fetch(w, 0, q);
-                return queries(w, q);
-            });
-            else by_loads<SRC, false>(a, bars, smem, rank, i, kblocks, vgroups, col0, v_full, tries, wc, [](const Walk&) { return true; });
+            by_loads<SRC>(a, bars, smem, rank, keys, i, kblocks, vgroups, col0, keys ? k_full : v_full,
+                          tries, wc, [&](const Walk& w) {
+                              uint32_t q[kAtOnce][32];
+                              fetch(w, 0, q);
+                              return queries(w, q);
+                          });
         }
     }
 
