@@ -174,16 +174,50 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
+def _current_stream() -> int:
+    """torch.cuda.current_stream().cuda_stream, without building the stream object: that takes
+    a quarter of a small call's time on the host."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+if not (hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice")):
+    def _current_stream() -> int:  # noqa: F811
+        return torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
+class _Descriptor:
+    """Keeps the C struct of a cache descriptor from call to call, as long as no field is
+    assigned; the tensors' addresses and the table's width are read anew for every call."""
+
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_c", None)
+        self.__dict__[name] = value
+
+    def __getstate__(self):  # copies and pickles make their own
+        return {k: v for k, v in self.__dict__.items() if k != "_c"}
+
+    def c_struct(self):
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = self.__dict__["_c"] = self._new_struct()
+        else:
+            c.data = self.data.data_ptr()
+            c.page_table = self.page_table.data_ptr()
+            c.max_pages_per_seq = self.page_table.shape[-1]
+            c.cache_lengths = _ptr(self.cache_lengths)
+        return c
+
+
 @dataclass
-class PagedCache:
+class PagedCache(_Descriptor):
     """A paged cache (all layers) described by element strides; see pkm_paged_cache.
 
     data: bf16 storage (any shape; only its base pointer is used).
@@ -202,7 +236,7 @@ class PagedCache:
     kv_stride: int = 0
     cache_lengths: Optional[torch.Tensor] = None
 
-    def c_struct(self) -> _CCache:
+    def _new_struct(self) -> _CCache:
         return _CCache(self.data.data_ptr(), int(self.layer_stride), int(self.page_stride),
                        int(self.slot_stride), int(self.kv_stride), int(self.num_layers),
                        int(self.num_pages), int(self.page_size), int(self.row_elems),
@@ -211,7 +245,7 @@ class PagedCache:
 
 
 @dataclass
-class QuantCache:
+class QuantCache(_Descriptor):
     """A quantised paged latent cache described by byte strides; see pkm_quant_cache.
 
     data: storage of the slots (any dtype and shape; only its base pointer is used).  A slot
@@ -229,7 +263,7 @@ class QuantCache:
     rope_dim: int
     cache_lengths: Optional[torch.Tensor] = None
 
-    def c_struct(self) -> _CQuantCache:
+    def _new_struct(self) -> _CQuantCache:
         return _CQuantCache(self.data.data_ptr(), int(self.layer_stride), int(self.page_stride),
                             int(self.slot_stride), int(self.num_layers), int(self.num_pages),
                             int(self.page_size), int(self.kv_lora_rank), int(self.rope_dim),

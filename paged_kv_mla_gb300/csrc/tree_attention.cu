@@ -34,6 +34,8 @@
 // cluster-scope release took 1430 cycles of every tile.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "pkm_device.cuh"
 #include "pkm_internal.h"
 
@@ -1335,10 +1337,20 @@ cudaError_t launch_source(const CUtensorMap& tm_q, const CUtensorMap& tm_k0, con
                           const CUtensorMap& tm_v, const TreeAttentionArgs& args,
                           const TreeWorkspace& ws, const TreeBoxes& boxes, int pairs,
                           cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<SRC>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kSmemBytes));
+    // once a device: the attribute stays (every thread sets the same value)
+    static std::atomic<uint64_t> set[2] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 128;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (!known || !(set[dev >> 6].load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(tree_attention_kernel<SRC>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kSmemBytes));
+        if (e != cudaSuccess) return e;
+        if (known) set[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
+    }
     return launch_dependent(tree_attention_kernel<SRC>, static_cast<unsigned>(2 * pairs), kThreads,
                             kSmemBytes, stream, tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes);
 }
