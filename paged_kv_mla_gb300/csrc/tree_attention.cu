@@ -274,97 +274,79 @@ __device__ __forceinline__ uint2 dequant4(uint32_t codes, float scale) {
     return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// Rows pos0 + 32 k, k < N (pos0 differs from lane to lane), moved on a tile at a time: page ids
-// first, all on their way at once, then the slots in 16-byte units of the layer (kNoRow where
-// Place has none).
+// A row of each tile (a lane's own), moved on a tile at a time: its page id first, on its way
+// while other work is done, then its place in 16-byte units of the layer (kNoRow past the last
+// row and for ids that the cache does not have, which are reported).
 constexpr uint32_t kNoRow = 0xffffffffu;
-template <int N>
-struct Rows {
-    int64_t pos;        // of k = 0
-    int32_t page[N], slot[N];
-    uint32_t id[N], unit[N];
+struct Row {
+    int32_t left;  // rows from it to the last
+    int32_t page, slot;
+    uint32_t id, unit;
 
-    __device__ __forceinline__ void start(const TreeAttentionArgs& a, int64_t pos0) {
-        pos = pos0;
-#pragma unroll
-        for (int k = 0; k < N; ++k) locate(a, k);
+    __device__ __forceinline__ void start(const TreeAttentionArgs& a, int64_t pos, int64_t end) {
+        left = static_cast<int32_t>(end - pos);
+        const int64_t lp = quotient(pos, a.page_size);
+        page = static_cast<int32_t>(lp);
+        slot = static_cast<int32_t>(pos - lp * a.page_size);
     }
-    __device__ __forceinline__ void locate(const TreeAttentionArgs& a, int k) {
-        const int64_t lp = quotient(pos + k * 32, a.page_size);
-        page[k] = static_cast<int32_t>(lp);
-        slot[k] = static_cast<int32_t>(pos + k * 32 - lp * a.page_size);
-    }
-    __device__ __forceinline__ void fetch(const TreeAttentionArgs& a, int b, int64_t kv) {
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            id[k] = ld_nc_u32_if(a.page_table + static_cast<int64_t>(b) * a.max_pages + page[k],
-                                 pos + k * 32 < kv);
-    }
-    // Units of the rows fetched, then on to the next tile's.  `unit_shift`: log2 of the elements
-    // or bytes of a unit.
-    __device__ __forceinline__ void resolve(const TreeAttentionArgs& a, int64_t kv, int unit_shift) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const bool exists = pos + k * 32 < kv;
-            const bool have = exists && id[k] < static_cast<uint32_t>(a.num_pages);
-            unit[k] = have ? static_cast<uint32_t>((id[k] * a.page_stride + slot[k] * a.slot_stride) >>
-                                                   unit_shift)
-                           : kNoRow;
-            if (exists && !have) report(a.status, PKM_ERR_OUT_OF_RANGE);
-        }
-        pos += kKeys;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            if (a.page_size < 32) {
-                locate(a, k);
-                continue;
-            }
-            slot[k] += kKeys;
-            while (slot[k] >= a.page_size) {
-                slot[k] -= a.page_size;
-                ++page[k];
-            }
-        }
+    __device__ __forceinline__ void fetch(const uint32_t* table) {
+        id = ld_nc_u32_if(table + page, left > 0);
     }
 };
 
-// A lane's columns of a latent row on their way from the cache to shared memory: 16 from c on,
-// or, where the step is `thin`, 8.  Past the row's columns and without a row: zeros.
-template <Source SRC>
-struct Piece {  // bf16 columns
-    static constexpr int kCount = 2, kShift = 3;  // pieces a step (8 rows each), elements a unit
+// How rows lie in the layer: all in 16-byte units, whose number fits 32 bits.
+struct Layout {
+    uint32_t pages, page_units, slot_units;
+    int32_t page_size, tile_pages, tile_slots;  // a tile is so many pages and slots
+
+    __device__ __forceinline__ Layout(const TreeAttentionArgs& a, int unit_shift)
+        : pages(static_cast<uint32_t>(a.num_pages)),
+          page_units(static_cast<uint32_t>(a.page_stride >> unit_shift)),
+          slot_units(static_cast<uint32_t>(a.slot_stride >> unit_shift)),
+          page_size(a.page_size),
+          tile_pages(kKeys / a.page_size),
+          tile_slots(kKeys % a.page_size) {}
+    // The place of the row whose id was fetched, then on to the next tile's.
+    __device__ __forceinline__ void resolve(const TreeAttentionArgs& a, Row& r) const {
+        const bool have = r.left > 0 && r.id < pages;
+        r.unit = have ? r.id * page_units + r.slot * slot_units : kNoRow;
+        if (r.left > 0 && !have) report(a.status, PKM_ERR_OUT_OF_RANGE);
+        r.left -= kKeys;
+        r.page += tile_pages;
+        r.slot += tile_slots;
+        const bool over = r.slot >= page_size;
+        r.page += over ? 1 : 0;
+        r.slot -= over ? page_size : 0;
+    }
+};
+
+// 16 columns of a latent row on their way from the cache to shared memory: bf16, or (lo and
+// scale) e4m3 codes.
+struct Piece {
     uint4 lo, hi;
-
-    __device__ __forceinline__ void load(const TreeAttentionArgs& a, uint32_t unit, int c, bool) {
-        const uint16_t* p = a.cache_layer + (static_cast<int64_t>(unit) << kShift) + c;
-        lo = ld_nc_v4_if(p, unit != kNoRow && c < a.cols);
-        hi = ld_nc_v4_if(p + 8, unit != kNoRow && c + 8 < a.cols);
-    }
-    __device__ __forceinline__ void columns(bool, uint4& l, uint4& h) const {
-        l = lo;
-        h = hi;
-    }
-};
-
-template <>
-struct Piece<kCodes> {  // 16 codes and their scale, or (thin) 8 rope columns
-    static constexpr int kCount = 4, kShift = 4;
-    uint4 codes;
     uint32_t scale;
 
-    __device__ __forceinline__ void load(const TreeAttentionArgs& a, uint32_t unit, int c, bool thin) {
-        const int R = a.kv_lora_rank;
-        const uint8_t* p = a.qcache_layer + (static_cast<int64_t>(unit) << kShift);
-        const bool have = unit != kNoRow && c < a.cols;
-        codes = ld_nc_v4_if(p + (thin ? R + 2 * (c - R) : c), have);
-        scale = ld_nc_u32_if(p + R + 2 * (a.cols - R) + 4 * (c / 128), have && !thin);
+    // `hi`: the upper 8 columns exist
+    __device__ __forceinline__ void load_bf16(const uint8_t* from, uint32_t unit, bool upper) {
+        const uint8_t* p = from + static_cast<uint64_t>(unit) * 16;
+        lo = ld_nc_v4_if(p, unit != kNoRow);
+        hi = ld_nc_v4_if(p + 16, unit != kNoRow && upper);
     }
-    __device__ __forceinline__ void columns(bool thin, uint4& l, uint4& h) const {
-        l = codes;
-        if (thin) return;
+    __device__ __forceinline__ void load_codes(const uint8_t* from, const uint8_t* scales, uint32_t unit) {
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.u32 q, %7, 0xffffffff;\n\t"
+            "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\tmov.b32 %4, 0;\n\t"
+            "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%5];\n\t"
+            "@q ld.global.nc.u32 %4, [%6];\n\t}"
+            : "=&r"(lo.x), "=&r"(lo.y), "=&r"(lo.z), "=&r"(lo.w), "=&r"(scale)
+            : "l"(from + static_cast<uint64_t>(unit) * 16), "l"(scales + static_cast<uint64_t>(unit) * 16),
+              "r"(unit));
+    }
+    __device__ __forceinline__ void dequant(uint4& l, uint4& h) const {
         const float f = __uint_as_float(scale);
-        const uint2 d0 = dequant4(codes.x, f), d1 = dequant4(codes.y, f);
-        const uint2 d2 = dequant4(codes.z, f), d3 = dequant4(codes.w, f);
+        const uint2 d0 = dequant4(lo.x, f), d1 = dequant4(lo.y, f);
+        const uint2 d2 = dequant4(lo.z, f), d3 = dequant4(lo.w, f);
         l = make_uint4(d0.x, d0.y, d1.x, d1.y);
         h = make_uint4(d2.x, d2.y, d3.x, d3.y);
     }
@@ -395,6 +377,19 @@ __device__ __forceinline__ uint64_t attended(const TreeAttentionArgs& a, const R
     return exist & bits;
 }
 
+// The value blocks of a group, four at most, of which each CTA has the first or second half.
+struct ValueBlocks {
+    int first, each;
+    __device__ __forceinline__ ValueBlocks(const TreeAttentionArgs& a, int group)
+        : first(4 * group), each((min(max(a.kv_lora_rank / 64 - 4 * group, 0), 4) + 1) / 2) {}
+    __device__ __forceinline__ int block(int rank, int n) const { return first + rank * each + n; }
+};
+
+// Block n of a CTA's value blocks.
+__device__ __forceinline__ int value_block(const TreeAttentionArgs& a, int rank, int n) {
+    return ValueBlocks(a, n >> 1).block(rank, n & 1);
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -423,138 +418,173 @@ __device__ __forceinline__ void gave_up(const WaitCtl& wc) {
     *wc.abort_flag = 1;
 }
 
-// Key or value warp i of a CTA whose rows come by loads: blocks i, i + 4 and i + 8 of the keys,
-// or block i of the values.  Four lanes take a row's columns, eight rows at a time; two steps of
-// a few rows are in flight: while one is converted and stored, the next one's rows are on their
-// way.  A quantised row's rope columns lie as bf16 values; of their blocks every key warp brings
-// 16 rows in two thin steps.  `queries(w)` runs once an item, right behind its first tile, whose
-// scores wait for it and free the keys' place for the second.
-// One copy of this code serves keys and values: two of them, with the loads and stores unrolled
-// further, left the warps waiting for instructions for a third of their time.
+// Warp i of the eight that bring the rows of a CTA by loads, as keys and as values in one go: the
+// tile's columns come in two sets of four blocks (the ninth block with the second), and of each
+// set a warp brings
+//   - 32 of the CTA's own 64 keys of a block, which are stored as keys and, where the block is one
+//     of the CTA's value blocks too, as values;
+//   - 16 of the other CTA's 64 keys of a value block;
+//   - of the ninth block 8 of its 32 keys.
+// A value is converted once in the CTA that has it as key and once more where the other CTA has it
+// as value.  Four lanes take a row's 64 columns.  As soon as a piece is stored the next set's is
+// asked for, so a whole set (6 KB a warp) is on its way all the time.  `queries(w)` runs once an
+// item, right behind its first set, whose scores wait for it.
+//
+// One copy of the code serves all warps and both sets.  An earlier form, in which four warps brought
+// keys and four brought all values, converted 1.9 times as much in 3.5 times as many steps.
 template <Source SRC, typename Queries>
 __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars, uint8_t* smem,
-                                         uint32_t rank, const bool keys, int i, int kblocks,
-                                         int vgroups, int col0, uint32_t full, uint32_t tries,
-                                         const WaitCtl& wc, const Queries& queries) {
-    constexpr int kPieces = Piece<SRC>::kCount, kRowsAtOnce = 8 * kPieces;
+                                         uint32_t rank, int i, int kblocks, int vgroups,
+                                         uint32_t k_full, uint32_t tries, const WaitCtl& wc,
+                                         const Queries& queries) {
     const int lane = threadIdx.x & 31, sub = lane >> 2, part = lane & 3;
-    const int per_block = (keys ? 64 : kKeys) / kRowsAtOnce;  // steps, an even number
-    const int wide_blocks = SRC == kCodes && keys ? a.kv_lora_rank / 64 : kblocks;
-    const int mine = !keys ? 1 : i < wide_blocks ? (wide_blocks - i + 3) / 4 : 0;
-    const int wide_steps = mine * per_block;
-    const int steps = !keys ? (i < 2 * vgroups ? wide_steps : 0) : wide_steps + 2 * (kblocks - wide_blocks);
-    uint64_t* empty = keys ? bars->k_empty : bars->v_empty;
+    const int R = a.kv_lora_rank, slot = i & 3, half = i & 1;
+    const int sets = kblocks > kQueryBlocks ? 2 : 1;
+    const int own0 = rank * 64 + (i >> 2) * 32;           // the tile's rows that it brings as keys
+    const int other0 = (rank ^ 1) * 64 + (i >> 1) * 16;   // and as values alone
+    const int ninth = slot * 8 + (lane >> 3);             // of its 32 rows, and 4 further on
+    const int ninth_c = 8 * 64 + (lane & 7) * 8;
+    // 16-byte chunk c of row r lies at chunk c ^ (r & 7), and the rows here are sub + 8 n
+    const uint32_t c0 = sub * 128 + (((part * 2) ^ sub) << 4), c1 = sub * 128 + (((part * 2 + 1) ^ sub) << 4);
+    const uint32_t keys_at = smem_u32(smem) + kOffK + (i >> 2) * 32 * 128;
+    const uint32_t values_at = smem_u32(smem) + kOffV;
+    const Layout layout(a, SRC == kCodes ? 4 : 3);
+    const uint8_t* layer = SRC == kCodes ? a.qcache_layer : reinterpret_cast<const uint8_t*>(a.cache_layer);
+    // bytes of a row before column c
+    const auto before = [&](int c) { return SRC == kCodes && c < R ? c : 2 * c - (SRC == kCodes ? R : 0); };
+    Piece own[4], other[2];
+    uint4 last[2];
+    Row k{}, v{};
     RingPos ring;
-    if (!keys && i >= 2) ring.next(kValueRing);
     uint32_t g = 0;
     bool ok = true;
     Walk w(bars);
-    while (ok && __any_sync(0xffffffffu, w.next(a))) {
-        const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
-        if (steps == 0) {  // fewer blocks than warps
-            if (keys) ok = queries(w);
-            continue;
+    const auto load = [&](int set) {
+        const ValueBlocks vb(a, set);
+        const int b0 = set * 4 + slot, b1 = vb.block(rank, half);
+        const int col0 = b0 * 64 + part * 16, col1 = b1 * 64 + part * 16;
+        const uint8_t *from0 = layer + before(col0), *from1 = layer + before(col1);
+        const uint8_t* scales = layer + 2 * a.cols - R;
+        if (SRC == kCodes && b0 * 64 < R) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                own[n].load_codes(from0, scales + b0 / 2 * 4, __shfl_sync(0xffffffffu, k.unit, n * 8 + sub));
+        } else {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const uint32_t unit = __shfl_sync(0xffffffffu, k.unit, n * 8 + sub);
+                own[n].load_bf16(from0, col0 < a.cols ? unit : kNoRow, col0 + 8 < a.cols);
+            }
         }
-        Rows<4> rows;  // keys: two groups of 32
-        rows.start(a, static_cast<int64_t>(w.kt0) * kKeys + (keys ? rank * 64 : 0u) + lane);
-        const int64_t kv = w.r.kv;
-        rows.fetch(a, w.b, kv);
-        int l_t = 0, l_step = 0, l_blk = i, l_in = 0;  // the step to be loaded
-        int s_t = 0, s_step = 0, s_blk = i, s_in = 0;  // the step to be stored
-        // block and step in it of the next step of a tile
-        const auto move = [&](int& t, int& step, int& blk, int& in) {
-            ++step;
-            ++in;
-            if (step == steps) {
-                step = 0;
-                ++t;
-                blk = wide_steps > 0 ? i : wide_blocks;
-                in = 0;
-            } else if (step <= wide_steps ? in == per_block : in == 2) {
-                in = 0;
-                blk = step < wide_steps ? blk + 4 : step == wide_steps ? wide_blocks : blk + 1;
-            }
-        };
-        if (wide_steps == 0) l_blk = s_blk = wide_blocks;
-        Piece<SRC> x[2][kPieces];
-        const auto load = [&](Piece<SRC>(&p)[kPieces]) {
-            if (l_t == tiles) return;
-            if (l_step == 0) {
-                rows.resolve(a, kv, Piece<SRC>::kShift);
-                rows.fetch(a, w.b, kv);  // for the next tile
-            }
-            const bool thin = l_step >= wide_steps;
-            const int r0 = thin ? 16 * i : l_in * kRowsAtOnce;
-            const int c = (keys ? 0 : col0) + l_blk * 64 + (thin ? l_in * 32 + part * 8 : part * 16);
-            const uint32_t unit = r0 < 32   ? rows.unit[0]
-                                  : r0 < 64 ? rows.unit[1]
-                                  : r0 < 96 ? rows.unit[2]
-                                            : rows.unit[3];
+        if (half < vb.each) {
 #pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-                const uint32_t u = __shfl_sync(0xffffffffu, unit, ((r0 & 31) + k * 8 + sub) & 31);
-                p[k].load(a, thin && k >= 2 ? kNoRow : u, c, thin);
+            for (int n = 0; n < 2; ++n) {
+                const uint32_t unit = __shfl_sync(0xffffffffu, v.unit, n * 8 + sub);
+                if (SRC == kCodes) other[n].load_codes(from1, scales + b1 / 2 * 4, unit);
+                else other[n].load_bf16(from1, col1 < a.cols ? unit : kNoRow, col1 + 8 < a.cols);
             }
-            move(l_t, l_step, l_blk, l_in);
-        };
-        const auto store = [&](Piece<SRC>(&p)[kPieces]) {
-            const bool thin = s_step >= wide_steps;
-            const uint32_t group = !keys ? ring.stage : s_blk < kQueryBlocks ? 0 : 1;
-            if (s_in == 0) {
-                ok = __all_sync(0xffffffffu,
-                                plain_wait(&empty[group], (keys ? g & 1 : ring.phase) ^ 1, tries));
-                if (!ok) {
-                    gave_up(wc);
-                    return;
-                }
-            }
-            const int r0 = thin ? 16 * i : s_in * kRowsAtOnce;
-            // 16-byte chunk c of row r lies at chunk c ^ (r & 7), and the rows here are sub + 8 n
-            const uint32_t dst =
-                smem_u32(smem) + sub * 128 + r0 * 128 +
-                (keys ? kOffK + s_blk * kBlockBytes
-                      : kOffV + group * 2 * kValueBytes + (i & 1) * kValueBytes);
-            const uint32_t c0 = ((thin ? s_in * 4 + part : part * 2) ^ sub) << 4;
-            const uint32_t c1 = ((part * 2 + 1) ^ sub) << 4;
-            const bool drafts = !keys && w.kt0 + s_t >= w.cached_tiles();
+        }
+        if (set == 0 || kblocks < kBlocks) return;
 #pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-                uint4 lo, hi;
-                p[k].columns(thin, lo, hi);
-                if (drafts) {
-                    // as in the loads by TMA, drafts' infinities and NaN are no values
-                    if (static_cast<int64_t>(w.kt0 + s_t) * kKeys + r0 + k * 8 + sub >= w.r.len) {
-                        lo = finite8(lo);
-                        hi = finite8(hi);
-                    }
-                }
-                if (!thin || k < 2) st_shared_v4(dst + k * 1024 + c0, lo.x, lo.y, lo.z, lo.w);
-                if (!thin) st_shared_v4(dst + k * 1024 + c1, hi.x, hi.y, hi.z, hi.w);
-            }
-            if (s_in == (thin ? 1 : per_block - 1)) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(full + group * 8);
-            }
-            move(s_t, s_step, s_blk, s_in);
-            if (s_step > 0) return;
-            ++g;
-            if (keys && i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
-            for (int v = 0; v < vgroups; ++v) ring.next(kValueRing);
+        for (int n = 0; n < 2; ++n) {
+            const uint32_t unit = __shfl_sync(0xffffffffu, k.unit, ninth + 4 * n);
+            last[n] = ld_nc_v4_if(layer + before(ninth_c) + static_cast<uint64_t>(unit) * 16,
+                                  unit != kNoRow && ninth_c < a.cols);
+        }
+    };
+    while (ok && __any_sync(0xffffffffu, w.next(a))) {
+        const int steps = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0) * sets;
+        const int64_t pos0 = static_cast<int64_t>(w.kt0) * kKeys;
+        const int64_t end = min(w.r.kv, static_cast<int64_t>(w.kt1) * kKeys);
+        const uint32_t* table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
+        // of the tile at hand rows behind the cached ones, as far as 32 bits say
+        int cached = __shfl_sync(
+            0xffffffffu,
+            static_cast<int>(min(w.r.len - pos0, static_cast<int64_t>(INT32_MAX))), 0);
+        k.start(a, pos0 + own0 + lane, end);
+        v.start(a, pos0 + other0 + (lane & 15), end);
+        const auto rows = [&] {  // of the next tile, and the ids of the one behind it
+            layout.resolve(a, k);
+            layout.resolve(a, v);
+            k.fetch(table);
+            v.fetch(table);
         };
-        const int pairs = tiles * (steps / 2);
+        k.fetch(table);
+        v.fetch(table);
+        rows();
+        load(0);
+        int set = 0;
 #pragma unroll 1
-        for (int n = -1; ok && n < pairs; ++n) {  // first two loads without stores
-            if (n >= 0) store(x[0]);
+        for (int step = 0; step < steps; ++step) {
+            const int block = set * 4 + slot;
+            const ValueBlocks vb(a, set);
+            const int mine = slot - static_cast<int>(rank) * vb.each;  // value block among the CTA's
+            ok = plain_wait(&bars->k_empty[set], (g & 1) ^ 1, tries);
+            if (vb.each > 0) ok = ok && plain_wait(&bars->v_empty[ring.stage], ring.phase ^ 1, tries);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                gave_up(wc);
+                break;
+            }
+            const int next = set + 1 == sets ? 0 : set + 1;
+            if (next == 0) rows();
+            const uint32_t values = values_at + ring.stage * 2 * kValueBytes;
+            const bool codes = SRC == kCodes && block * 64 < R;
+            // a tile's part behind the cached tokens: drafts' infinities and NaN are no values, as
+            // in the loads by TMA
+            const auto put = [&](uint32_t at0, uint32_t at1, uint4 lo, uint4 hi, int row) {
+                if (cached < kKeys && row >= cached) {
+                    lo = finite8(lo);
+                    hi = finite8(hi);
+                }
+                st_shared_v4(at0, lo.x, lo.y, lo.z, lo.w);
+                st_shared_v4(at1, hi.x, hi.y, hi.z, hi.w);
+            };
+            if (block < kblocks) {
+                const uint32_t k0 = keys_at + block * kBlockBytes + c0, k1 = k0 + c1 - c0;
+                const uint32_t v0 = values + mine * kValueBytes + own0 * 128 + c0, v1 = v0 + c1 - c0;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    uint4 lo = own[n].lo, hi = own[n].hi;
+                    if (codes) own[n].dequant(lo, hi);
+                    st_shared_v4(k0 + n * 1024, lo.x, lo.y, lo.z, lo.w);
+                    st_shared_v4(k1 + n * 1024, hi.x, hi.y, hi.z, hi.w);
+                    if (mine >= 0 && mine < vb.each)
+                        put(v0 + n * 1024, v1 + n * 1024, lo, hi, own0 + n * 8 + sub);
+                }
+            }
+            if (half < vb.each) {
+                const uint32_t v0 = values + half * kValueBytes + other0 * 128 + c0, v1 = v0 + c1 - c0;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    uint4 lo = other[n].lo, hi = other[n].hi;
+                    if (SRC == kCodes) other[n].dequant(lo, hi);
+                    put(v0 + n * 1024, v1 + n * 1024, lo, hi, other0 + n * 8 + sub);
+                }
+            }
+            if (set == 1 && kblocks == kBlocks) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int r = ninth + 4 * n;
+                    st_shared_v4(keys_at + 8 * kBlockBytes + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                                 last[n].x, last[n].y, last[n].z, last[n].w);
+                }
+            }
+            load(next);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(k_full + set * 8);
+            if (vb.each > 0) ring.next(kValueRing);
+            if (step == 0) ok = queries(w);
             if (!ok) break;
-            load(x[0]);
-            if (n >= 0) store(x[1]);
-            if (!ok) break;
-            load(x[1]);
-            if (keys && n == steps / 2 - 1) ok = queries(w);
+            set = next;
+            if (set > 0) continue;
+            cached -= kKeys;
+            ++g;
+            if (i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
         }
     }
-    if (keys && !ok && lane == 0) bars->progress = INT32_MAX;
+    if (!ok && lane == 0) bars->progress = INT32_MAX;
 }
 
 template <Source SRC>
@@ -591,14 +621,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kKeyGroups; ++i) {
-            // one box: one arrival, with the bytes; boxes of a block: one each; by loads: one
-            // for each block and CTA, four for a block of rope columns
+            // one box: one arrival, with the bytes; boxes of a block: one each; by loads: eight
+            // warps of each CTA
             const int from = i == 0 ? 0 : kQueryBlocks, to = i == 0 ? min(kblocks, kQueryBlocks) : kblocks;
             const int blocks = max(to - from, 1);
-            const int thin = SRC == kCodes ? max(to - max(from, R / 64), 0) : 0;
-            mbar_init(&bars->k_full[i], SRC != kTma          ? 2 * (blocks + 3 * thin)
-                                        : tb.key_blocks > 1 ? 1
-                                                            : blocks);
+            mbar_init(&bars->k_full[i], SRC != kTma ? 16 : tb.key_blocks > 1 ? 1 : blocks);
             mbar_init(&bars->k_empty[i], 1);
         }
         for (int i = 0; i < kValueRing; ++i) {
@@ -607,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&bars->v_own[i], tb.value_blocks > 1 ? 1 : 2);  // warps that load
         }
         for (int i = 0; i < 2; ++i) mbar_init(&bars->s_full[i], 1);
-        mbar_init(&bars->q_full, 1 + 2 * 4);  // the TMA bytes, and four value warps of each CTA
+        mbar_init(&bars->q_full, 1 + 2 * (SRC == kTma ? 4 : 8));  // the TMA bytes, and warps of each CTA
         mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->p_full, 2 * kSoftWarps);
         mbar_init(&bars->o_full, 1);
@@ -787,7 +814,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_ld_x32(tmem + tlane, x0);
                 tmem_ld_x32(tmem + tlane + 32, x1);
                 for (int v = 0; v < vblocks; ++v) {
-                    const int col = (half * vblocks + v) * 64;
+                    const int col = value_block(a, half, v) * 64;
                     if (col >= R) break;
                     tmem_ld_wait();
 #pragma unroll
@@ -811,22 +838,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // four columns of consecutive rows side by side: whole lines, without staging
                 const int at = rank * 64 + row;
                 float4* part = reinterpret_cast<float4*>(a.workspace + ws.parts) +
-                               (slot * (R / 4) + half * vblocks * 16) * ws.rows + at;
-                const auto put = [&](int v, const uint32_t(&x)[32]) {
+                               slot * (R / 4) * ws.rows + at;
+                const auto put = [&](int quads, const uint32_t(&x)[32]) {
                     if (rr >= rows_all) return;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        st_v4(part + static_cast<int64_t>(v * 8 + k) * ws.rows,
+                        st_v4(part + static_cast<int64_t>(quads + k) * ws.rows,
                               make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
                 };
-                for (int v = 0; v < 2 * vblocks; v += 2) {  // 64 columns, whole within R
-                    if (half * vblocks * 64 + v * 32 >= R) break;
+                for (int v = 0; v < vblocks; ++v) {  // 64 columns, whole within R
+                    const int block = value_block(a, half, v);
+                    if (block * 64 >= R) break;
                     uint32_t x0[32], x1[32];
-                    tmem_ld_x32(tmem + tlane + v * 32, x0);
-                    tmem_ld_x32(tmem + tlane + v * 32 + 32, x1);
+                    tmem_ld_x32(tmem + tlane + v * 64, x0);
+                    tmem_ld_x32(tmem + tlane + v * 64 + 32, x1);
                     tmem_ld_wait();
-                    put(v, x0);
-                    put(v + 1, x1);
+                    put(block * 16, x0);
+                    put(block * 16 + 8, x1);
                 }
                 if (half == 0 && rr < rows_all)
                     reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + at] =
@@ -877,8 +905,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int vg = 0; vg < vgroups; ++vg) {
                     const uint32_t v = vring.stage;
-                    wait(&bars->v_full[v], vring.phase);
-                    tc_fence_after();
+                    if (SRC == kTma) {  // by loads they are there with the tile's keys
+                        wait(&bars->v_full[v], vring.phase);
+                        tc_fence_after();
+                    }
                     const uint32_t id = idesc_bf16(128, 2 * vg + 1 < vblocks ? 256 : 128, false, true);
                     const uint64_t vd = desc_add_bytes(v_desc, v * 2 * kValueBytes);
 #pragma unroll 1
@@ -902,6 +932,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint32_t d = tmem + kScoreCol + (g & 1) * 64;
                     // Rolled loops without branches: unrolled or with the choice of the A operand
                     // inside, the same MMAs took 10 to 65 % longer to issue.
+                    if (SRC != kTma && t > 0) {
+                        values(g - 1, first);
+                        first = false;
+                    }
                     wait(&bars->k_full[0], g & 1);
                     tc_fence_after();
                     const int first_blocks = min(kblocks, kQueryBlocks);
@@ -933,9 +967,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ++g;
                     ++t;
                 }
-                // The values of the tile before, behind this tile's scores; those of an item's
-                // last tile before the next item's queries are waited for.
-                if (next_item ? g > 0 : t > 1) {
+                // The values of the tile before, behind this tile's scores (by loads before them:
+                // those loads take longer than the weights, and need the values' place); those
+                // of an item's last tile before the next item's queries are waited for.
+                if (next_item ? g > 0 : SRC == kTma && t > 1) {
                     values(next_item ? g - 1 : g - 2, first);
                     first = false;
                 }
@@ -964,7 +999,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int g = 0;
         while (w.next(a))
             for (int32_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
-                for (uint32_t n = 0; g - 2 > *progress && n < tries; ++n) __nanosleep(200);
+                for (uint32_t n = 0; g - 2 > *progress && n < tries; ++n) __nanosleep(500);
                 for (int x = 0; x < 2; ++x) {
                     const int64_t pos = static_cast<int64_t>(kt) * kKeys + rank * 64 + x * 32 + lane;
                     const int64_t row = Place(a, w.b, pos, w.r.kv).offset(a);
@@ -1003,17 +1038,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // columns, warp i bringing block i of its group i / 2 (past the CTA's last block it
         // only signals), or by boxes of both blocks the even warp.
         const bool keys = warp < kValueWarp;
-        const int i = (warp - kKeyWarp) & 3;
+        const int i = warp & 3;
         const uint32_t k_full = mapa_shared(smem_u32(bars->k_full), 0);
         const uint32_t v_full = mapa_shared(smem_u32(bars->v_full), 0);
         const uint32_t q_full = mapa_shared(smem_u32(&bars->q_full), 0);
-        const int col0 = static_cast<int>(rank) * vblocks * 64;  // first value column
         uint32_t g = 0, item = 0;
         bool ok = true;
         // The first query blocks of an item go to tensor memory: lanes 32 i .. 32 i + 31 by key
-        // warp i, behind the keys of the item's first tile; the first of them are fetched
-        // before those keys are asked for.
+        // warp i (by loads each of the two warps i half of the blocks), behind the keys of the
+        // item's first tile; the first of them are fetched before those keys are asked for.
         constexpr int kAtOnce = SRC == kTma ? 2 : 1;  // blocks in flight
+        const int first_kb = SRC == kTma || keys ? 0 : kQueryBlocks / 2;
+        const int last_kb = SRC == kTma || !keys ? kQueryBlocks : kQueryBlocks / 2;
         const auto fetch = [&](const Walk& w, int kb, uint32_t(&x)[kAtOnce][32]) {
             const int64_t row = w.r.first * a.num_heads + static_cast<int64_t>(w.item) * 128 +
                                 rank * 64 + (i & 1) * 32 + lane;
@@ -1033,8 +1069,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!issue_wait(&bars->q_empty, (item & 1) ^ 1)) return false;
             tc_fence_after();
 #pragma unroll 1
-            for (int kb = 0; kb < kQueryBlocks; kb += kAtOnce) {
-                if (kb > 0) fetch(w, kb, x);
+            for (int kb = first_kb; kb < last_kb; kb += kAtOnce) {
+                if (kb > first_kb) fetch(w, kb, x);
 #pragma unroll
                 for (int k = 0; k < kAtOnce; ++k)
                     tmem_st_x32(tmem + (static_cast<uint32_t>(i * 32) << 16) + kQueryCol + (kb + k) * 32,
@@ -1092,6 +1128,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else {
                 RingPos ring;            // place of the tile's first group
                 uint32_t own_phase = 0;  // bit s: phase of v_own[s], which both groups use in turn
+                const int first_block = value_block(a, rank, i);
                 const int brings = wide ? ((i & 1) ? 0 : kTreeValueBlocks) : i < vblocks ? 1 : 0;
                 while (ok && i < 2 * vgroups && __any_sync(0xffffffffu, w.next(a))) {
                     const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
@@ -1113,8 +1150,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             for (int x = 0; brings > 0 && x < boxes; ++x)
                                 tma_load_4d_pair_elect(
                                     dst + x * slots * 128, &tm_v, v_full + s * 8,
-                                    wide ? 0 : col0 + i * 64, __shfl_sync(0xffffffffu, at.slot, x),
-                                    __shfl_sync(0xffffffffu, at.page, x), wide ? col0 / 64 + i : 0);
+                                    wide ? 0 : first_block * 64, __shfl_sync(0xffffffffu, at.slot, x),
+                                    __shfl_sync(0xffffffffu, at.page, x), wide ? first_block : 0);
                         } else {
                             // Drafts, which not every query attends, and rows past the last: a
                             // zero weight must not meet an infinity or NaN.  The CTA loads them
@@ -1125,8 +1162,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             for (int x = 0; brings > 0 && x < boxes; ++x)
                                 tma_load_4d_elect(
                                     dst + x * slots * 128, &tm_v, &bars->v_own[s],
-                                    wide ? 0 : col0 + i * 64, __shfl_sync(0xffffffffu, at.slot, x),
-                                    __shfl_sync(0xffffffffu, at.page, x), wide ? col0 / 64 + i : 0);
+                                    wide ? 0 : first_block * 64, __shfl_sync(0xffffffffu, at.slot, x),
+                                    __shfl_sync(0xffffffffu, at.page, x), wide ? first_block : 0);
                             ok = issue_wait(&bars->v_own[s], (own_phase >> s) & 1);
                             if (!ok) break;
                             const int drafts = static_cast<int>(
@@ -1150,10 +1187,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok) spin_ns(kDrainNs);
         } else {
-            by_loads<SRC>(a, bars, smem, rank, keys, i, kblocks, vgroups, col0, keys ? k_full : v_full,
-                          tries, wc, [&](const Walk& w) {
+            by_loads<SRC>(a, bars, smem, rank, warp - kKeyWarp, kblocks, vgroups, k_full, tries, wc,
+                          [&](const Walk& w) {
                               uint32_t q[kAtOnce][32];
-                              fetch(w, 0, q);
+                              fetch(w, first_kb, q);
                               return queries(w, q);
                           });
         }
