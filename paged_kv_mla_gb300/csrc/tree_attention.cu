@@ -60,7 +60,9 @@ constexpr uint64_t kDrainNs = 1000000;  // a role that gave up leaves its loads 
 constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
-enum Source { kTma, kRows, kCodes };  // pages by TMA, bf16 rows by loads, quantised rows
+// Pages by TMA, bf16 rows by loads, quantised rows whose codes fill both sets of blocks (a rank of
+// 512) and others, whose rope columns lie among them.
+enum Source { kTma, kRows, kCodes, kCodesNarrow };
 
 // a / b; the 64-bit division is a long routine, and the operands are hardly ever that large.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -320,33 +322,23 @@ struct Layout {
     }
 };
 
-// 16 columns of a latent row on their way from the cache to shared memory: bf16, or (lo and
-// scale) e4m3 codes.
+// 16 columns of a latent row on their way from the cache to shared memory: bf16, or (in lo) e4m3
+// codes.
 struct Piece {
     uint4 lo, hi;
-    uint32_t scale;
 
-    // `hi`: the upper 8 columns exist
+    // `upper`: the upper 8 columns exist
     __device__ __forceinline__ void load_bf16(const uint8_t* from, uint32_t unit, bool upper) {
         const uint8_t* p = from + static_cast<uint64_t>(unit) * 16;
         lo = ld_nc_v4_if(p, unit != kNoRow);
         hi = ld_nc_v4_if(p + 16, unit != kNoRow && upper);
     }
-    __device__ __forceinline__ void load_codes(const uint8_t* from, const uint8_t* scales, uint32_t unit) {
-        asm volatile(
-            "{\n\t.reg .pred q;\n\t"
-            "setp.ne.u32 q, %7, 0xffffffff;\n\t"
-            "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\tmov.b32 %4, 0;\n\t"
-            "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%5];\n\t"
-            "@q ld.global.nc.u32 %4, [%6];\n\t}"
-            : "=&r"(lo.x), "=&r"(lo.y), "=&r"(lo.z), "=&r"(lo.w), "=&r"(scale)
-            : "l"(from + static_cast<uint64_t>(unit) * 16), "l"(scales + static_cast<uint64_t>(unit) * 16),
-              "r"(unit));
+    __device__ __forceinline__ void load_codes(const uint8_t* from, uint32_t unit) {
+        lo = ld_nc_v4_if(from + static_cast<uint64_t>(unit) * 16, unit != kNoRow);
     }
-    __device__ __forceinline__ void dequant(uint4& l, uint4& h) const {
-        const float f = __uint_as_float(scale);
-        const uint2 d0 = dequant4(lo.x, f), d1 = dequant4(lo.y, f);
-        const uint2 d2 = dequant4(lo.z, f), d3 = dequant4(lo.w, f);
+    __device__ __forceinline__ void dequant(float scale, uint4& l, uint4& h) const {
+        const uint2 d0 = dequant4(lo.x, scale), d1 = dequant4(lo.y, scale);
+        const uint2 d2 = dequant4(lo.z, scale), d3 = dequant4(lo.w, scale);
         l = make_uint4(d0.x, d0.y, d1.x, d1.y);
         h = make_uint4(d2.x, d2.y, d3.x, d3.y);
     }
@@ -377,18 +369,8 @@ __device__ __forceinline__ uint64_t attended(const TreeAttentionArgs& a, const R
     return exist & bits;
 }
 
-// The value blocks of a group, four at most, of which each CTA has the first or second half.
-struct ValueBlocks {
-    int first, each;
-    __device__ __forceinline__ ValueBlocks(const TreeAttentionArgs& a, int group)
-        : first(4 * group), each((min(max(a.kv_lora_rank / 64 - 4 * group, 0), 4) + 1) / 2) {}
-    __device__ __forceinline__ int block(int rank, int n) const { return first + rank * each + n; }
-};
-
-// Block n of a CTA's value blocks.
-__device__ __forceinline__ int value_block(const TreeAttentionArgs& a, int rank, int n) {
-    return ValueBlocks(a, n >> 1).block(rank, n & 1);
-}
+// Block n of a CTA's value blocks: of every four blocks the even CTA has the first two.
+__device__ __forceinline__ int value_block(int rank, int n) { return 4 * (n >> 1) + 2 * rank + (n & 1); }
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -421,106 +403,106 @@ __device__ __forceinline__ void gave_up(const WaitCtl& wc) {
 // Warp i of the eight that bring the rows of a CTA by loads, as keys and as values in one go: the
 // tile's columns come in two sets of four blocks (the ninth block with the second), and of each
 // set a warp brings
-//   - 32 of the CTA's own 64 keys of a block, which are stored as keys and, where the block is one
-//     of the CTA's value blocks too, as values;
-//   - 16 of the other CTA's 64 keys of a value block;
-//   - of the ninth block 8 of its 32 keys.
-// A value is converted once in the CTA that has it as key and once more where the other CTA has it
-// as value.  Four lanes take a row's 64 columns.  As soon as a piece is stored the next set's is
-// asked for, so a whole set (6 KB a warp) is on its way all the time.  `queries(w)` runs once an
-// item, right behind its first set, whose scores wait for it.
+//   - of one of its two pairs of blocks 16 of the CTA's own 64 keys; the pair that the CTA has as
+//     values is stored a second time as those;
+//   - of that pair 8 of the other CTA's 64 keys, as values;
+//   - of the ninth block 8 of its 16 keys.
+// Eight lanes take a row's 128 columns; lane l keeps row l of its own 16 or of the other 8, that
+// is, finds its page and loads its scale.  When a set is stored the next one is asked for.
 //
-// One copy of the code serves all warps and both sets.  An earlier form, in which four warps brought
-// keys and four brought all values, converted 1.9 times as much in 3.5 times as many steps.
+// One copy of the code serves all warps and both sets, with few branches: the warps wait for
+// instructions more than for loads.  A form in which four warps brought all keys and four all
+// values converted 1.9 times as much (182 us instead of 134 for chains over the quantised cache);
+// with a scale of its own for every piece and 64 columns of a row at a time it took 134 us.
 template <Source SRC, typename Queries>
 __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars, uint8_t* smem,
                                          uint32_t rank, int i, int kblocks, int vgroups,
                                          uint32_t k_full, uint32_t tries, const WaitCtl& wc,
                                          const Queries& queries) {
-    const int lane = threadIdx.x & 31, sub = lane >> 2, part = lane & 3;
-    const int R = a.kv_lora_rank, slot = i & 3, half = i & 1;
+    constexpr bool kQuant = SRC == kCodes || SRC == kCodesNarrow;
+    const int lane = threadIdx.x & 31;
+    // a lane's row of each four and its 16 columns of the pair: lanes that store together have
+    // two rows' same columns, whose 16-byte chunks lie in different banks
+    const int sub = (lane >> 2 & 1) | (lane >> 4 << 1), part = (lane & 3) | (lane >> 3 & 1) << 2;
+    const int R = a.kv_lora_rank, pair = i & 1;
     const int sets = kblocks > kQueryBlocks ? 2 : 1;
-    const int own0 = rank * 64 + (i >> 2) * 32;           // the tile's rows that it brings as keys
-    const int other0 = (rank ^ 1) * 64 + (i >> 1) * 16;   // and as values alone
-    const int ninth = slot * 8 + (lane >> 3);             // of its 32 rows, and 4 further on
+    const int own0 = rank * 64 + (i >> 1) * 16;  // the tile's rows that it brings as keys
+    const int other0 = (rank ^ 1) * 64 + i * 8;  // and as values alone
+    const int ninth = pair * 8 + (lane >> 3);    // of its 16 rows, and 4 further on
     const int ninth_c = 8 * 64 + (lane & 7) * 8;
-    // 16-byte chunk c of row r lies at chunk c ^ (r & 7), and the rows here are sub + 8 n
-    const uint32_t c0 = sub * 128 + (((part * 2) ^ sub) << 4), c1 = sub * 128 + (((part * 2 + 1) ^ sub) << 4);
-    const uint32_t keys_at = smem_u32(smem) + kOffK + (i >> 2) * 32 * 128;
+    // Chunk c of row r lies at chunk c ^ (r & 7), and the rows here are sub + 4 n.
+    const uint32_t at = (part >> 2) * kBlockBytes + sub * 128 + ((((part & 3) * 2) ^ sub) << 4);
+    const uint32_t at2 = (part >> 2) * kValueBytes + at - (part >> 2) * kBlockBytes;
+    const uint32_t keys_at = smem_u32(smem) + kOffK + (i >> 1) * 16 * 128;
     const uint32_t values_at = smem_u32(smem) + kOffV;
-    const Layout layout(a, SRC == kCodes ? 4 : 3);
-    const uint8_t* layer = SRC == kCodes ? a.qcache_layer : reinterpret_cast<const uint8_t*>(a.cache_layer);
-    // bytes of a row before column c
-    const auto before = [&](int c) { return SRC == kCodes && c < R ? c : 2 * c - (SRC == kCodes ? R : 0); };
+    const Layout layout(a, kQuant ? 4 : 3);
+    const uint8_t* layer = kQuant ? a.qcache_layer : reinterpret_cast<const uint8_t*>(a.cache_layer);
+    // bytes of a row before column c, which `codes` says are codes
+    const auto before = [&](int c, bool codes) { return codes ? c : 2 * c - (kQuant ? R : 0); };
+    const auto are_codes = [&](int set, int pair) {
+        return SRC == kCodes || (SRC == kCodesNarrow && set * 256 + pair * 128 < R);
+    };
     Piece own[4], other[2];
     uint4 last[2];
-    Row k{}, v{};
+    uint32_t scale = 0;
+    Row row{};
     RingPos ring;
     uint32_t g = 0;
     bool ok = true;
     Walk w(bars);
     const auto load = [&](int set) {
-        const ValueBlocks vb(a, set);
-        const int b0 = set * 4 + slot, b1 = vb.block(rank, half);
-        const int col0 = b0 * 64 + part * 16, col1 = b1 * 64 + part * 16;
-        const uint8_t *from0 = layer + before(col0), *from1 = layer + before(col1);
-        const uint8_t* scales = layer + 2 * a.cols - R;
-        if (SRC == kCodes && b0 * 64 < R) {
+        uint32_t u[6], u9[2];
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-                own[n].load_codes(from0, scales + b0 / 2 * 4, __shfl_sync(0xffffffffu, k.unit, n * 8 + sub));
-        } else {
+        for (int n = 0; n < 6; ++n) u[n] = __shfl_sync(0xffffffffu, row.unit, n * 4 + sub);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const uint32_t unit = __shfl_sync(0xffffffffu, k.unit, n * 8 + sub);
-                own[n].load_bf16(from0, col0 < a.cols ? unit : kNoRow, col0 + 8 < a.cols);
-            }
+        for (int n = 0; n < 2; ++n) u9[n] = __shfl_sync(0xffffffffu, row.unit, ninth + 4 * n);
+        const int col0 = set * 256 + pair * 128 + part * 16;
+        const int col1 = set * 256 + static_cast<int>(rank) * 128 + part * 16;
+        if (kQuant) {  // the lane's row's
+            const int scaled = set * 2 + (lane < 16 ? pair : static_cast<int>(rank));
+            scale = ld_nc_u32_if(layer + 2 * a.cols - R + scaled * 4 + static_cast<uint64_t>(row.unit) * 16,
+                                 row.unit != kNoRow && scaled * 128 < R);
         }
-        if (half < vb.each) {
+        const bool codes0 = are_codes(set, pair), codes1 = are_codes(set, rank);
+        const uint8_t *from0 = layer + before(col0, codes0), *from1 = layer + before(col1, codes1);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const uint32_t unit = __shfl_sync(0xffffffffu, v.unit, n * 8 + sub);
-                if (SRC == kCodes) other[n].load_codes(from1, scales + b1 / 2 * 4, unit);
-                else other[n].load_bf16(from1, col1 < a.cols ? unit : kNoRow, col1 + 8 < a.cols);
-            }
+        for (int n = 0; n < 4; ++n) {
+            if (codes0) own[n].load_codes(from0, u[n]);
+            else own[n].load_bf16(from0, col0 < a.cols ? u[n] : kNoRow, col0 + 8 < a.cols);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            if (codes1) other[n].load_codes(from1, u[4 + n]);
+            else other[n].load_bf16(from1, col1 < a.cols ? u[4 + n] : kNoRow, col1 + 8 < a.cols);
         }
         if (set == 0 || kblocks < kBlocks) return;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const uint32_t unit = __shfl_sync(0xffffffffu, k.unit, ninth + 4 * n);
-            last[n] = ld_nc_v4_if(layer + before(ninth_c) + static_cast<uint64_t>(unit) * 16,
-                                  unit != kNoRow && ninth_c < a.cols);
-        }
+        for (int n = 0; n < 2; ++n)
+            last[n] = ld_nc_v4_if(layer + before(ninth_c, false) + static_cast<uint64_t>(u9[n]) * 16,
+                                  u9[n] != kNoRow && ninth_c < a.cols);
     };
     while (ok && __any_sync(0xffffffffu, w.next(a))) {
         const int steps = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0) * sets;
         const int64_t pos0 = static_cast<int64_t>(w.kt0) * kKeys;
         const int64_t end = min(w.r.kv, static_cast<int64_t>(w.kt1) * kKeys);
         const uint32_t* table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
-        // of the tile at hand rows behind the cached ones, as far as 32 bits say
+        // rows of the tile at hand and behind it that are cached ones, as far as 32 bits say
         int cached = __shfl_sync(
             0xffffffffu,
             static_cast<int>(min(w.r.len - pos0, static_cast<int64_t>(INT32_MAX))), 0);
-        k.start(a, pos0 + own0 + lane, end);
-        v.start(a, pos0 + other0 + (lane & 15), end);
-        const auto rows = [&] {  // of the next tile, and the ids of the one behind it
-            layout.resolve(a, k);
-            layout.resolve(a, v);
-            k.fetch(table);
-            v.fetch(table);
+        row.start(a, pos0 + (lane < 16 ? own0 + lane : lane < 24 ? other0 + lane - 16 : 0), end);
+        const auto rows = [&] {  // of the next tile, and the id of the one behind it
+            layout.resolve(a, row);
+            row.fetch(table);
         };
-        k.fetch(table);
-        v.fetch(table);
+        row.fetch(table);
         rows();
         load(0);
         int set = 0;
 #pragma unroll 1
         for (int step = 0; step < steps; ++step) {
-            const int block = set * 4 + slot;
-            const ValueBlocks vb(a, set);
-            const int mine = slot - static_cast<int>(rank) * vb.each;  // value block among the CTA's
             ok = plain_wait(&bars->k_empty[set], (g & 1) ^ 1, tries);
-            if (vb.each > 0) ok = ok && plain_wait(&bars->v_empty[ring.stage], ring.phase ^ 1, tries);
+            if (set < vgroups) ok = ok && plain_wait(&bars->v_empty[ring.stage], ring.phase ^ 1, tries);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
                 gave_up(wc);
@@ -528,38 +510,40 @@ __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars,
             }
             const int next = set + 1 == sets ? 0 : set + 1;
             if (next == 0) rows();
-            const uint32_t values = values_at + ring.stage * 2 * kValueBytes;
-            const bool codes = SRC == kCodes && block * 64 < R;
-            // a tile's part behind the cached tokens: drafts' infinities and NaN are no values, as
-            // in the loads by TMA
-            const auto put = [&](uint32_t at0, uint32_t at1, uint4 lo, uint4 hi, int row) {
-                if (cached < kKeys && row >= cached) {
+            float f[6];
+#pragma unroll
+            for (int n = 0; n < 6; ++n)
+                f[n] = kQuant ? __uint_as_float(__shfl_sync(0xffffffffu, scale, n * 4 + sub)) : 0.0f;
+            const uint32_t k0 = keys_at + (set * 4 + pair * 2) * kBlockBytes + at;
+            const uint32_t values = values_at + ring.stage * 2 * kValueBytes + at2;
+            const auto put = [&](uint32_t to, int n, const uint4& lo, const uint4& hi) {
+                const uint32_t p = (to + n * 512) ^ ((n & 1) << 6);
+                st_shared_v4(p, lo.x, lo.y, lo.z, lo.w);
+                st_shared_v4(p ^ 16, hi.x, hi.y, hi.z, hi.w);
+            };
+            // drafts' infinities and NaN are no values, as in the loads by TMA
+            const auto put_value = [&](uint32_t to, int n, uint4 lo, uint4 hi, int r) {
+                if (cached < kKeys && r >= cached) {
                     lo = finite8(lo);
                     hi = finite8(hi);
                 }
-                st_shared_v4(at0, lo.x, lo.y, lo.z, lo.w);
-                st_shared_v4(at1, hi.x, hi.y, hi.z, hi.w);
+                put(to, n, lo, hi);
             };
-            if (block < kblocks) {
-                const uint32_t k0 = keys_at + block * kBlockBytes + c0, k1 = k0 + c1 - c0;
-                const uint32_t v0 = values + mine * kValueBytes + own0 * 128 + c0, v1 = v0 + c1 - c0;
+            const bool codes0 = are_codes(set, pair), codes1 = are_codes(set, rank);
+            const bool both = set < vgroups && pair == static_cast<int>(rank);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    uint4 lo = own[n].lo, hi = own[n].hi;
-                    if (codes) own[n].dequant(lo, hi);
-                    st_shared_v4(k0 + n * 1024, lo.x, lo.y, lo.z, lo.w);
-                    st_shared_v4(k1 + n * 1024, hi.x, hi.y, hi.z, hi.w);
-                    if (mine >= 0 && mine < vb.each)
-                        put(v0 + n * 1024, v1 + n * 1024, lo, hi, own0 + n * 8 + sub);
-                }
+            for (int n = 0; n < 4; ++n) {
+                uint4 lo = own[n].lo, hi = own[n].hi;
+                if (codes0) own[n].dequant(f[n], lo, hi);
+                put(k0, n, lo, hi);
+                if (both) put_value(values + own0 * 128, n, lo, hi, own0 + n * 4 + sub);
             }
-            if (half < vb.each) {
-                const uint32_t v0 = values + half * kValueBytes + other0 * 128 + c0, v1 = v0 + c1 - c0;
+            if (set < vgroups) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     uint4 lo = other[n].lo, hi = other[n].hi;
-                    if (SRC == kCodes) other[n].dequant(lo, hi);
-                    put(v0 + n * 1024, v1 + n * 1024, lo, hi, other0 + n * 8 + sub);
+                    if (codes1) other[n].dequant(f[4 + n], lo, hi);
+                    put_value(values + other0 * 128, n, lo, hi, other0 + n * 4 + sub);
                 }
             }
             if (set == 1 && kblocks == kBlocks) {
@@ -574,7 +558,7 @@ __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars,
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(k_full + set * 8);
-            if (vb.each > 0) ring.next(kValueRing);
+            if (set < vgroups) ring.next(kValueRing);
             if (step == 0) ok = queries(w);
             if (!ok) break;
             set = next;
@@ -616,8 +600,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int64_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     const int R = a.kv_lora_rank;
     const int kblocks = (a.cols + 63) / 64;
-    const int vblocks = (R + 127) / 128;        // value blocks of each CTA
-    const int vgroups = (vblocks + 1) / 2;      // groups of two blocks, one MMA width each
+    const int vgroups = (R + 255) / 256;        // groups of two value blocks of each CTA
+    const int vblocks = 2 * vgroups;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kKeyGroups; ++i) {
@@ -814,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_ld_x32(tmem + tlane, x0);
                 tmem_ld_x32(tmem + tlane + 32, x1);
                 for (int v = 0; v < vblocks; ++v) {
-                    const int col = value_block(a, half, v) * 64;
+                    const int col = value_block(half, v) * 64;
                     if (col >= R) break;
                     tmem_ld_wait();
 #pragma unroll
@@ -847,7 +831,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
                 };
                 for (int v = 0; v < vblocks; ++v) {  // 64 columns, whole within R
-                    const int block = value_block(a, half, v);
+                    const int block = value_block(half, v);
                     if (block * 64 >= R) break;
                     uint32_t x0[32], x1[32];
                     tmem_ld_x32(tmem + tlane + v * 64, x0);
@@ -888,6 +872,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 failed |= !plain_wait(bar, parity, tries);
             };
             const uint32_t id_s = idesc_bf16(128, kKeys, false, false);
+            const uint32_t id_o = idesc_bf16(128, 256, false, true);
             const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
             const uint64_t p_desc = sdesc_sw128(smem_u32(sP), 16, 1024);
@@ -909,15 +894,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         wait(&bars->v_full[v], vring.phase);
                         tc_fence_after();
                     }
-                    const uint32_t id = idesc_bf16(128, 2 * vg + 1 < vblocks ? 256 : 128, false, true);
-                    const uint64_t vd = desc_add_bytes(v_desc, v * 2 * kValueBytes);
+                                        const uint64_t vd = desc_add_bytes(v_desc, v * 2 * kValueBytes);
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {  // 64 keys: one block of P
                         const uint64_t pd = desc_add_bytes(p_desc, h * kBlockBytes);
                         const uint64_t vh = desc_add_bytes(vd, h * 64 * 128);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)  // 16 keys: 32 bytes of P, 2048 of V
-                            mma_bf16_pair_elect(tmem + vg * 128, pd + 2 * k, vh + 128 * k, id,
+                            mma_bf16_pair_elect(tmem + vg * 128, pd + 2 * k, vh + 128 * k, id_o,
                                                 (h | k) != 0 ? 1u : keep);
                     }
                     mma_commit_pair_elect(&bars->v_empty[v], 3);
@@ -995,7 +979,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // proper are issued when their shared memory is free, too late to wait for DRAM.
         Walk w(bars);
         volatile int32_t* progress = &bars->progress;
-        const int bytes = SRC == kCodes ? R + 2 * (a.cols - R) + 4 * (R / 128) : 2 * a.cols;
+        const int bytes = SRC >= kCodes ? R + 2 * (a.cols - R) + 4 * (R / 128) : 2 * a.cols;
         int g = 0;
         while (w.next(a))
             for (int32_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
@@ -1004,7 +988,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int64_t pos = static_cast<int64_t>(kt) * kKeys + rank * 64 + x * 32 + lane;
                     const int64_t row = Place(a, w.b, pos, w.r.kv).offset(a);
                     if (row < 0) continue;
-                    const uint8_t* from = SRC == kCodes
+                    const uint8_t* from = SRC >= kCodes
                                               ? a.qcache_layer + row
                                               : reinterpret_cast<const uint8_t*>(a.cache_layer + row);
                     for (int c = 0; c < bytes; c += 128) prefetch_l2(from + c);
@@ -1128,8 +1112,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else {
                 RingPos ring;            // place of the tile's first group
                 uint32_t own_phase = 0;  // bit s: phase of v_own[s], which both groups use in turn
-                const int first_block = value_block(a, rank, i);
-                const int brings = wide ? ((i & 1) ? 0 : kTreeValueBlocks) : i < vblocks ? 1 : 0;
+                const int first_block = value_block(rank, i);
+                const int brings = wide ? ((i & 1) ? 0 : kTreeValueBlocks) : 1;
                 while (ok && i < 2 * vgroups && __any_sync(0xffffffffu, w.next(a))) {
                     const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
                     const int cached = __shfl_sync(0xffffffffu, w.cached_tiles() - w.kt0, 0);
@@ -1401,7 +1385,8 @@ cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm
     const int pairs = num_sms / 2 < kTreeMaxPairs ? num_sms / 2 : kTreeMaxPairs;
     const cudaError_t e =
         args.qcache_layer != nullptr
-            ? launch_source<kCodes>(tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes, pairs, stream)
+            ? (args.kv_lora_rank == 512 ? launch_source<kCodes> : launch_source<kCodesNarrow>)(
+                  tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes, pairs, stream)
         : boxes.key_slots >= 8 ? launch_source<kTma>(tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes, pairs, stream)
                    : launch_source<kRows>(tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes, pairs, stream);
     if (e != cudaSuccess) return e;
