@@ -18,7 +18,7 @@
 namespace pkm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kUnroll = 4;  // heads in flight per thread
 
 // Columns a thread loads: 16 bytes in the interleaved layout, twice 8 bytes (four columns of
@@ -74,6 +74,16 @@ __global__ void __launch_bounds__(kThreads) rope_heads_kernel(const RopeHeadsArg
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int64_t r = it / groups;
         const int h0 = static_cast<int>(it % groups) * group + h_in;
+        const int col = HALF ? u * 4 : u * 8;
+        const uint16_t* x = a.x + r * a.x_row_stride + col;
+        uint16_t* y = a.y + r * a.y_row_stride + col;
+        // the columns first: they need not wait for the position, as the factors do
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int h = h0 + i * heads_per_pass;
+            if (h < a.num_heads) v[i] = load_unit<HALF>(x + h * a.x_head_stride, half_cols);
+        }
         const uint32_t pos = __ldg(a.positions + r);
         if (pos >= static_cast<uint32_t>(a.max_seq_len)) {
             if (threadIdx.x == 0) report(a.status, PKM_ERR_OUT_OF_RANGE);
@@ -83,15 +93,6 @@ __global__ void __launch_bounds__(kThreads) rope_heads_kernel(const RopeHeadsArg
             a.freqs + static_cast<int64_t>(pos) * a.rope_dim + u * 8);
         const float4 c0 = __ldg(fr), c1 = __ldg(fr + 1);
         const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        const int col = HALF ? u * 4 : u * 8;
-        const uint16_t* x = a.x + r * a.x_row_stride + col;
-        uint16_t* y = a.y + r * a.y_row_stride + col;
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int h = h0 + i * heads_per_pass;
-            if (h < a.num_heads) v[i] = load_unit<HALF>(x + h * a.x_head_stride, half_cols);
-        }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             const int h = h0 + i * heads_per_pass;
