@@ -53,19 +53,22 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const CompactAr
     const uint32_t len = __ldg(a.cache_lengths + b);
     const uint32_t count = __ldg(a.counts + b);
     const uint32_t* acc = a.accepted + static_cast<int64_t>(b) * a.max_accepted;
-    // the request as a whole is checked first: it moves completely or not at all
+    // The request as a whole is checked first: it moves completely or not at all.  The list is
+    // read along with its count, and the first table of offsets is filled in passing.
     int bad = 0;
-    if (count > static_cast<uint32_t>(a.max_accepted)) {
-        bad = PKM_ERR_INVALID_ARG;
-    } else {
-        for (uint32_t j = threadIdx.x; j < count; j += kThreads) {
-            const uint32_t t = __ldg(acc + j);
-            if (j > 0 && t <= __ldg(acc + j - 1)) bad = max(bad, int(PKM_ERR_INVALID_ARG));
-            if (slot_offset(a, b, static_cast<uint64_t>(len) + t) < 0 ||
-                slot_offset(a, b, static_cast<uint64_t>(len) + j) < 0)
-                bad = max(bad, int(PKM_ERR_OUT_OF_RANGE));
+    for (int j = threadIdx.x; j < a.max_accepted; j += kThreads) {
+        const uint32_t t = __ldg(acc + j), before = j > 0 ? __ldg(acc + j - 1) : 0u;
+        if (static_cast<uint32_t>(j) >= count) break;
+        if (j > 0 && t <= before) bad = max(bad, int(PKM_ERR_INVALID_ARG));
+        const int64_t from = slot_offset(a, b, static_cast<uint64_t>(len) + t);
+        const int64_t to = slot_offset(a, b, static_cast<uint64_t>(len) + j);
+        if (from < 0 || to < 0) bad = max(bad, int(PKM_ERR_OUT_OF_RANGE));
+        if (j < kTable) {
+            src[j] = from;
+            dst[j] = to;
         }
     }
+    if (count > static_cast<uint32_t>(a.max_accepted)) bad = PKM_ERR_INVALID_ARG;
     const bool any = __syncthreads_or(bad) != 0;
     if (bad != 0 && blockIdx.y == 0) report(a.status, bad);
     if (blockIdx.y == 0 && threadIdx.x == 0 && a.new_lengths != nullptr)
@@ -76,12 +79,14 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const CompactAr
     const int64_t units = static_cast<int64_t>(a.layer_count) * a.planes * per_row;
     for (uint32_t j0 = 0; j0 < count; j0 += kTable) {
         const int n = static_cast<int>(min(count - j0, static_cast<uint32_t>(kTable)));
-        __syncthreads();  // the table's readers of the previous round are done
-        for (int j = threadIdx.x; j < n; j += kThreads) {
-            src[j] = slot_offset(a, b, static_cast<uint64_t>(len) + __ldg(acc + j0 + j));
-            dst[j] = slot_offset(a, b, static_cast<uint64_t>(len) + j0 + j);
+        if (j0 > 0) {
+            __syncthreads();  // the table's readers of the previous round are done
+            for (int j = threadIdx.x; j < n; j += kThreads) {
+                src[j] = slot_offset(a, b, static_cast<uint64_t>(len) + __ldg(acc + j0 + j));
+                dst[j] = slot_offset(a, b, static_cast<uint64_t>(len) + j0 + j);
+            }
+            __syncthreads();
         }
-        __syncthreads();
         for (int64_t u = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x; u < units;
              u += static_cast<int64_t>(gridDim.y) * kThreads) {
             const int piece = static_cast<int>(u % per_row);
