@@ -57,19 +57,33 @@ struct Bars {
 };
 
 // The request a lane's rows belong to.  A lane visits its rows in increasing order, so after
-// one binary search the request only ever moves forward.
+// one search the request only ever moves forward.
 struct RowCursor {
     int b;
     uint32_t lo, hi, cl;  // input_row_offsets[b], input_row_offsets[b + 1], cache_lengths[b]
 
-    __device__ __forceinline__ void init(const CacheWriteArgs& a, int64_t r) {
+    // Lane i of the warp: largest b with row_offsets[b] <= r0 + i, or 0.  For r0 the warp looks at
+    // 32 places at a time (two steps for 1024 requests, where halving takes ten), and the lanes
+    // behind find theirs among the 32 offsets from there on.
+    __device__ __forceinline__ void init(const CacheWriteArgs& a, int64_t r0) {
         const uint32_t* iro = a.row_offsets;
-        int l = 0, h = a.batch;  // largest b with iro[b] <= r (0 when r < iro[0])
+        const int lane = threadIdx.x & 31;
+        int l = 0, h = a.batch;
         while (h - l > 1) {
-            const int mid = (l + h) >> 1;
-            if (static_cast<int64_t>(__ldg(iro + mid)) <= r) l = mid;
-            else h = mid;
+            const int step = (h - l + 31) / 32;
+            const int at = min(l + lane * step, h);
+            const bool below = at < h && static_cast<int64_t>(__ldg(iro + at)) <= r0;
+            const uint32_t m = __ballot_sync(0xffffffffu, below);
+            const int k = m == 0 ? 0 : 31 - __clz(m);
+            h = min(l + (k + 1) * step, h);
+            l += k * step;
         }
+        const uint32_t next = __ldg(iro + min(l + 1 + lane, a.batch));
+        int n = 0;  // offsets behind l's that the lane's row has reached, 31 at most
+#pragma unroll
+        for (int s = 16; s > 0; s /= 2)
+            if (static_cast<int64_t>(__shfl_sync(0xffffffffu, next, n + s - 1)) <= r0 + lane) n += s;
+        l = min(l + n, a.batch - 1);
         b = l;
         lo = __ldg(iro + l);
         hi = __ldg(iro + l + 1);
@@ -131,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t covered = min(static_cast<int64_t>(a.total_rows),
                                     static_cast<int64_t>(__ldg(a.row_offsets + a.batch)));
         RowCursor q;
-        q.init(a, c_begin * kChunkRows + lane);
+        q.init(a, c_begin * kChunkRows);
         for (int64_t k = c_begin; k < c_end; ++k) {
             // lane i < 30: row i of the chunk -> slot and page id (loaded before the stage is
             // free, so that the load overlaps the wait)
