@@ -582,6 +582,13 @@ struct RingPos {
     }
 };
 
+// 32 bytes at once, a whole sector; p has to be 32-byte aligned.
+__device__ __forceinline__ void st_v8(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Stores a warp's 32-row x 64-column bf16 box to global memory in whole 128-byte row
 // segments.  On entry lane r holds row r as 32 packed bf16 pairs in `p`; the rows pass
 // through `stage` (4 KB of shared memory owned by the warp, 16-byte chunk j of row r kept

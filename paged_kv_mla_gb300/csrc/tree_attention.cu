@@ -42,9 +42,11 @@
 namespace pkm {
 namespace {
 
-constexpr int kSoftWarps = 4, kMmaWarp = 4, kQueryWarp = 5, kFetchWarp = 6, kKeyWarp = 8, kValueWarp = 12;
-constexpr int kThreads = 16 * 32;
-constexpr int kSoftRegs = 192, kIssueRegs = 64;  // with 128 for each loader: 4 x 128 in all
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kQueryWarp = 9, kFetchWarp = 10, kKeyWarp = 12, kValueWarp = 16;
+constexpr int kThreads = 20 * 32;
+// Registers of the four-warp groups (two of softmax warps, the issuing warps, two of loaders), of
+// the 5 x 96 that the block starts with: by loads the rows on their way need more.
+constexpr int kIssueRegs = 64, kMoreRegs = 112;
 constexpr int kItemCost = 4;        // an item's start and end, in tiles (7 us against 1.6 us)
 constexpr int kKeys = 128;          // keys of a tile (64 loaded by each CTA as keys)
 constexpr int kBlocks = 9;          // 64-column blocks of a latent row
@@ -123,9 +125,8 @@ constexpr size_t kOffK = kOffQ + size_t(kBlocks - kQueryBlocks) * kBlockBytes;
 constexpr size_t kOffV = kOffK + size_t(kBlocks) * kBlockBytes;
 constexpr size_t kOffP = kOffV + size_t(kValueRing) * 2 * kValueBytes;
 constexpr size_t kOffMax = kOffP + 2 * size_t(kBlockBytes);
-constexpr size_t kOffSum = kOffMax + 2 * 128 * sizeof(float);
-constexpr size_t kOffBars = kOffSum + 128 * sizeof(float);
-constexpr size_t kSmemBytes = kOffBars + sizeof(Bars) + 1024;
+constexpr size_t kOffBars = kOffMax + 2 * 256 * sizeof(float);
+constexpr size_t kSmemBytes = kOffBars + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103a CTA");
 
 // A pair's share of the units of all items, walked item by item.  An item has a unit for each
@@ -174,7 +175,7 @@ struct Walk {
 };
 
 // Counts the units of all requests and cuts out the pair's share; every thread sums a run of
-// requests.  `scratch`: 16 int64 of shared memory.
+// requests.  `scratch`: an int64 of shared memory for every warp.
 __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int64_t* scratch,
                                      int64_t pair, int64_t pairs) {
     const int per = (a.batch + kThreads - 1) / kThreads;
@@ -251,6 +252,12 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
 
 __device__ __forceinline__ uint4 finite8(uint4 v) {
     return make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+}
+
+// Whether there are any: an exponent of ones carries into the sign's place.
+__device__ __forceinline__ bool any_nonfinite(const uint4& v) {
+    const auto top = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
+    return ((top(v.x) | top(v.y) | top(v.z) | top(v.w)) & 0x80008000u) != 0;
 }
 
 // Four e4m3 codes times a scale, each product rounded to fp32 and then to bf16.  The halves that
@@ -344,30 +351,28 @@ struct Piece {
     }
 };
 
-// Bits k of the 64 keys c0 .. c0+63 that token i of the request may attend.
-__device__ __forceinline__ uint64_t attended(const TreeAttentionArgs& a, const Request& r,
-                                             int32_t i, int64_t c0) {
-    const auto low = [](int64_t n) -> uint64_t {
-        return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
-    };
-    const uint64_t exist = low(r.kv - c0);
-    if (a.mask == nullptr) return exist & low(r.len + i + 1 - c0);
-    const int64_t j0 = c0 - r.len;  // draft of the first key
-    uint64_t bits = low(-j0);
-    if (j0 > -64) {
-        const uint32_t* row = a.mask + (r.first + i) * a.mask_words;
-        const int64_t w0 = j0 > 0 ? j0 >> 5 : 0;
-        const auto word = [&](int64_t w) -> uint64_t {
-            return w < a.mask_words ? __ldg(row + w) : 0u;
-        };
-        const uint64_t lo = word(w0) | (word(w0 + 1) << 32);
-        const int sh = static_cast<int>(j0 > 0 ? j0 & 31 : 0);
-        uint64_t m = lo >> sh;
-        if (sh > 0) m |= word(w0 + 2) << (64 - sh);
-        bits |= j0 >= 0 ? m : m << -j0;
+// Which of the 32 keys c0 .. c0+31 a token may attend; the words of its mask that they need are
+// asked for a tile ahead.
+struct Attended {
+    uint32_t word[2];
+
+    __device__ __forceinline__ void fetch(const TreeAttentionArgs& a, const Request& r, int32_t token, int64_t c0) {
+        const int64_t w0 = max(c0 - r.len, static_cast<int64_t>(0)) >> 5;  // of the first draft
+        const uint32_t* row = a.mask + (r.first + token) * a.mask_words + w0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) word[k] = ld_nc_u32_if(row + k, a.mask != nullptr && w0 + k < a.mask_words);
     }
-    return exist & bits;
-}
+    __device__ __forceinline__ uint32_t bits(const TreeAttentionArgs& a, const Request& r, int32_t token, int64_t c0) const {
+        const auto low = [](int64_t n) -> uint32_t {
+            return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+        };
+        const uint32_t exist = low(r.kv - c0);
+        if (a.mask == nullptr) return exist & low(r.len + token + 1 - c0);
+        const int64_t j0 = c0 - r.len;  // draft of the first key
+        if (j0 <= 0) return exist & (low(-j0) | (j0 > -32 ? word[0] << -j0 : 0u));
+        return exist & __funnelshift_r(word[0], word[1], static_cast<uint32_t>(j0 & 31));
+    }
+};
 
 // Block n of a CTA's value blocks: of every four blocks the even CTA has the first two.
 __device__ __forceinline__ int value_block(int rank, int n) { return 4 * (n >> 1) + 2 * rank + (n & 1); }
@@ -578,15 +583,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap tm_k1,
                           const __grid_constant__ CUtensorMap tm_v, const TreeAttentionArgs a,
                           const TreeWorkspace ws, const TreeBoxes tb) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];  // swizzle atoms of 1024 bytes
     uint8_t* sQ = smem + kOffQ;
     uint8_t* sK = smem + kOffK;
     uint8_t* sV = smem + kOffV;
     uint8_t* sP = smem + kOffP;
     float* s_max = reinterpret_cast<float*>(smem + kOffMax);
-    float* s_sum = reinterpret_cast<float*>(smem + kOffSum);
     Bars* bars = reinterpret_cast<Bars*>(smem + kOffBars);
 
     // Values that are the same in every lane pass through a shuffle, from which the compiler
@@ -659,16 +661,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp < kSoftWarps) {
         // ---------------- softmax and epilogue: row = lane of the CTA's 64 ----------------
-        warpgroup_reg_alloc<kSoftRegs>();
+        // Warps w and w + 4 share 32 lanes; lanes 0-63 have the first 64 keys (and half of O's
+        // columns), and each of the two warps takes 32 of the keys (half of the lanes' columns).
+        // With one warp for both a tile of 25 took 2560 cycles, 380 more than its MMAs, and the
+        // end of an item half as long again.
+        if constexpr (SRC == kTma) warpgroup_reg_alloc<kMoreRegs>();
         Walk w(bars);
-        const int half = warp >> 1;                   // which 64 keys, which half of O's columns
+        const int half = warp >> 1 & 1, part = warp >> 2;
         const int row = (warp & 1) * 32 + lane;       // of this CTA's 64
+        const int quarter = (half * 2 + part) * 64 + row;  // place of a row's maximum and sum
         const float scale2 = a.scale * kLog2e;
-        const uint32_t tlane = static_cast<uint32_t>(warp * 32) << 16;
+        const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t p_row = smem_u32(sP) + half * kBlockBytes + row * 128;
-        const uint32_t stage = smem_u32(sP) + warp * 4096;
+        const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         const uint32_t p_full = mapa_shared(smem_u32(&bars->p_full), 0);
         const uint32_t o_empty = mapa_shared(smem_u32(&bars->o_empty), 0);
+        // the four warps that share rows
+        const auto meet = [&] { named_bar_sync(3 + (warp & 1), 128); };
         uint32_t g = 0;
         int32_t left_rows = 0, left_parts = 0;
         int64_t left_first = 0;
@@ -679,65 +688,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int32_t token =
                 min(static_cast<int32_t>(quotient(rr, a.num_heads)), w.r.n - 1);
             float m = -INFINITY, l = 0.0f;
+            Attended mask;
+            const int32_t cached = w.cached_tiles();
+            const auto key0 = [&](int32_t kt) { return static_cast<int64_t>(kt) * kKeys + half * 64 + part * 32; };
+            if (w.kt0 >= cached) mask.fetch(a, w.r, token, key0(w.kt0));
             for (int32_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
+                const bool partial = kt >= cached;
+                uint32_t may = ~0u;
+                if (partial) may = mask.bits(a, w.r, token, key0(kt));
+                if (kt + 1 >= cached && kt + 1 < w.kt1) mask.fetch(a, w.r, token, key0(kt + 1));
                 if (!warp_wait(&bars->s_full[g & 1], (g >> 1) & 1, wc)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t x0[32], x1[32];
-                tmem_ld_x32(tmem + tlane + kScoreCol + (g & 1) * 64, x0);
-                tmem_ld_x32(tmem + tlane + kScoreCol + (g & 1) * 64 + 32, x1);
-                uint32_t lo = ~0u, hi = ~0u;
-                const bool partial = kt >= w.cached_tiles();
-                if (partial) {
-                    const uint64_t bits = attended(a, w.r, token, static_cast<int64_t>(kt) * kKeys + half * 64);
-                    lo = static_cast<uint32_t>(bits);
-                    hi = static_cast<uint32_t>(bits >> 32);
-                }
+                uint32_t x[32];
+                tmem_ld_x32(tmem + tlane + kScoreCol + (g & 1) * 64 + part * 32, x);
                 tmem_ld_wait();
-                float s[64];
+                float s[32];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    mul2(s[2 * k], s[2 * k + 1], __uint_as_float(x0[2 * k]),
-                         __uint_as_float(x0[2 * k + 1]), scale2, scale2);
-                    mul2(s[32 + 2 * k], s[33 + 2 * k], __uint_as_float(x1[2 * k]),
-                         __uint_as_float(x1[2 * k + 1]), scale2, scale2);
-                }
+                for (int k = 0; k < 16; ++k)
+                    mul2(s[2 * k], s[2 * k + 1], __uint_as_float(x[2 * k]),
+                         __uint_as_float(x[2 * k + 1]), scale2, scale2);
                 if (partial) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        s[k] = (lo >> k) & 1u ? s[k] : -INFINITY;
-                        s[32 + k] = (hi >> k) & 1u ? s[32 + k] : -INFINITY;
-                    }
+                    for (int k = 0; k < 32; ++k) s[k] = (may >> k) & 1u ? s[k] : -INFINITY;
                 }
                 float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
 #pragma unroll
-                for (int k = 4; k < 64; k += 4) {
+                for (int k = 4; k < 32; k += 4) {
                     t0 = fmaxf(t0, s[k]);
                     t1 = fmaxf(t1, s[k + 1]);
                     t2 = fmaxf(t2, s[k + 2]);
                     t3 = fmaxf(t3, s[k + 3]);
                 }
-                float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-                // the row's other 64 keys are with lane row + 64 (warp ^ 2)
-                float* mx = s_max + (g & 1) * 128;
-                mx[half * 64 + row] = top;
-                named_bar_sync(3 + (warp & 1), 64);
+                float* mx = s_max + (g & 1) * 256;
+                mx[quarter] = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+                meet();
                 if (*wc.abort_flag) {
                     ok = false;
                     break;
                 }
-                top = fmaxf(top, mx[(half ^ 1) * 64 + row]);
+                const float top = fmaxf(fmaxf(mx[row], mx[64 + row]), fmaxf(mx[128 + row], mx[192 + row]));
                 const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
                 const float m_new = move ? top : m;
                 const float back = move && m > -INFINITY ? exp2_approx(m - m_new) : move ? 0.0f : 1.0f;
                 m = m_new;
                 const float ref = m == -INFINITY ? 0.0f : m;
                 float sum0 = 0.0f, sum1 = 0.0f;
-                uint32_t p[32];
+                uint32_t p[16];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
+                for (int k = 0; k < 16; ++k) {
                     const float e0 = exp2_approx(s[2 * k] - ref);
                     const float e1 = exp2_approx(s[2 * k + 1] - ref);
                     sum0 += e0;
@@ -747,7 +748,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 l = l * back + (sum0 + sum1);
                 // the weights are finished before the wait, not after it
 #pragma unroll
-                for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(p[k]));
+                for (int k = 0; k < 16; ++k) asm volatile("" : "+r"(p[k]));
                 // the previous tile's weights are used up, and O holds it
                 if (g > 0 &&
                     !warp_wait(&bars->o_full, (g - 1) & 1, wc)) {
@@ -756,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (kt > w.kt0 && __any_sync(0xffffffffu, move)) {
                     tc_fence_after();
-                    for (int v = 0; v < 2 * vblocks; ++v) {
+                    for (int v = part * vblocks; v < (part + 1) * vblocks; ++v) {
                         uint32_t o[32];
                         tmem_ld_x32(tmem + tlane + v * 32, o);
                         tmem_ld_wait();
@@ -768,8 +769,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_st_wait();
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    st_shared_v4(p_row + ((j ^ (row & 7)) << 4), p[4 * j], p[4 * j + 1],
+                for (int j = 0; j < 4; ++j)
+                    st_shared_v4(p_row + (((part * 4 + j) ^ (row & 7)) << 4), p[4 * j], p[4 * j + 1],
                                  p[4 * j + 2], p[4 * j + 3]);
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -782,65 +783,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            s_sum[half * 64 + row] = l;
-            named_bar_sync(3 + (warp & 1), 64);
+            // in the place of the last tile's maxima, which all have read when O is complete
+            float* sums = s_max + ((g - 1) & 1) * 256;
+            sums[quarter] = l;
+            meet();
             if (*wc.abort_flag) {
                 ok = false;
                 break;
             }
-            l += s_sum[(half ^ 1) * 64 + row];
+            // the same order in all four warps
+            l = (sums[row] + sums[64 + row]) + (sums[128 + row] + sums[192 + row]);
+            const int v0 = part * vgroups, v1 = v0 + vgroups;  // this warp's blocks of O
             const bool whole = w.kt0 == 0 && w.kt1 == w.r.tiles;
-            const uint32_t valid = __ballot_sync(0xffffffffu, rr < rows_all);
             const int64_t row0 = w.r.first * a.num_heads + rr - lane;  // of this warp's 32
             if (whole) {
                 const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-                uint32_t x0[32], x1[32], p[32];
-                tmem_ld_x32(tmem + tlane, x0);
-                tmem_ld_x32(tmem + tlane + 32, x1);
-                for (int v = 0; v < vblocks; ++v) {
-                    const int col = value_block(half, v) * 64;
+                // A lane stores whole sectors of its row where the output allows: as fast as
+                // through shared memory by TMA (339 us either way for large drafted trees), and
+                // faster than whole lines from there by the lanes (345 us).
+                for (int c = 2 * v0; c < 2 * v1; ++c) {  // 32 columns
+                    const int col = value_block(half, c >> 1) * 64 + (c & 1) * 32;
                     if (col >= R) break;
+                    uint32_t x[32], p[16];
+                    tmem_ld_x32(tmem + tlane + c * 32, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        p[k] = pack_bf16x2(__uint_as_float(x0[2 * k]) * inv,
-                                           __uint_as_float(x0[2 * k + 1]) * inv);
-                        p[16 + k] = pack_bf16x2(__uint_as_float(x1[2 * k]) * inv,
-                                                __uint_as_float(x1[2 * k + 1]) * inv);
+                    for (int k = 0; k < 16; ++k)
+                        p[k] = pack_bf16x2(__uint_as_float(x[2 * k]) * inv, __uint_as_float(x[2 * k + 1]) * inv);
+                    if (rr >= rows_all) continue;
+                    uint16_t* out = a.out + (row0 + lane) * R + col;
+                    if (sectors) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) st_v8(out + 16 * k, p + 8 * k);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st_v4(out + 8 * k, make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]));
                     }
-                    if (v + 1 < vblocks) {  // in flight while this block is stored
-                        tmem_ld_x32(tmem + tlane + (v + 1) * 64, x0);
-                        tmem_ld_x32(tmem + tlane + (v + 1) * 64 + 32, x1);
-                    }
-                    warp_store_rows_32x64(stage, p, a.out + row0 * R + col, R, valid, lane);
                 }
-                tmem_ld_wait();
-                if (half == 0 && rr < rows_all && a.lse != nullptr)
+                if (half + part == 0 && rr < rows_all && a.lse != nullptr)
                     a.lse[row0 + lane] = l != 0.0f ? m * kLn2 + logf(l) : -INFINITY;
             } else {
                 const int64_t slot = 2 * pair + (w.kt0 > 0 ? 0 : 1);
                 // four columns of consecutive rows side by side: whole lines, without staging
                 const int at = rank * 64 + row;
-                float4* part = reinterpret_cast<float4*>(a.workspace + ws.parts) +
+                float4* to = reinterpret_cast<float4*>(a.workspace + ws.parts) +
                                slot * (R / 4) * ws.rows + at;
                 const auto put = [&](int quads, const uint32_t(&x)[32]) {
                     if (rr >= rows_all) return;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        st_v4(part + static_cast<int64_t>(quads + k) * ws.rows,
+                        st_v4(to + static_cast<int64_t>(quads + k) * ws.rows,
                               make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
                 };
-                for (int v = 0; v < vblocks; ++v) {  // 64 columns, whole within R
-                    const int block = value_block(half, v);
-                    if (block * 64 >= R) break;
-                    uint32_t x0[32], x1[32];
-                    tmem_ld_x32(tmem + tlane + v * 64, x0);
-                    tmem_ld_x32(tmem + tlane + v * 64 + 32, x1);
+                for (int c = 2 * v0; c < 2 * v1; ++c) {  // 32 columns
+                    const int col = value_block(half, c >> 1) * 64 + (c & 1) * 32;
+                    if (col >= R) break;
+                    uint32_t x[32];
+                    tmem_ld_x32(tmem + tlane + c * 32, x);
                     tmem_ld_wait();
-                    put(block * 16, x0);
-                    put(block * 16 + 8, x1);
+                    put(col / 4, x);
                 }
-                if (half == 0 && rr < rows_all)
+                if (half + part == 0 && rr < rows_all)
                     reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + at] =
                         make_float2(m, l);
                 if (w.kt0 == 0) {
@@ -855,7 +859,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(o_empty);
         }
-        if (!ok) named_bar_arrive(3 + (warp & 1), 64);  // releases the partner warp
+        if (!ok) named_bar_arrive(3 + (warp & 1), 128);  // releases the warps that share its rows
         if (leader && threadIdx.x == 0) {
             TreeItem* items = reinterpret_cast<TreeItem*>(a.workspace + ws.items);
             items[pair] = TreeItem{left_first, ok ? left_rows : 0, left_parts};
@@ -1017,6 +1021,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else {
         // ---------------- keys and values ----------------
+        if constexpr (SRC != kTma) warpgroup_reg_alloc<kMoreRegs>();
         // Keys: this CTA's 64 of each tile, all columns, warp i bringing blocks i, i + 4 and
         // i + 8, or by boxes of whole groups group i.  Values: all 128 keys, this CTA's
         // columns, warp i bringing block i of its group i / 2 (past the CTA's last block it
@@ -1153,10 +1158,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             const int drafts = static_cast<int>(
                                 max(min(w.r.len, w.r.kv) - pos0, static_cast<int64_t>(0)));
                             const uint32_t from = smem_u32(dst) + (lane & 7) * 16;
-                            for (int r = drafts + (lane >> 3); r < kKeys; r += 4) {
-                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                                if (pos0 + r < w.r.kv) v = finite8(ld_shared_v4(from + r * 128));
-                                st_shared_v4(from + r * 128, v.x, v.y, v.z, v.w);
+                            // eight rows' chunks at a time, hardly ever one to be mended
+#pragma unroll 1
+                            for (int r = drafts & ~31; r < kKeys; r += 32) {
+                                uint4 v[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    v[k] = ld_shared_v4(from + (r + k * 4 + (lane >> 3)) * 128);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    const int x = r + k * 4 + (lane >> 3);
+                                    if (x < drafts || !any_nonfinite(v[k])) continue;
+                                    v[k] = finite8(v[k]);
+                                    st_shared_v4(from + x * 128, v[k].x, v[k].y, v[k].z, v[k].w);
+                                }
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
