@@ -131,7 +131,10 @@ static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103a CTA");
 
 // A pair's share of the units of all items, walked item by item.  An item has a unit for each
 // of its tiles, behind kItemCost units that stand for its start and end.  After next()
-// returned true, the part is tiles [kt0, kt1) of item `item` of request r.
+// returned true, the part is tiles [kt0, kt1) of item `item` of request r, which all roles take
+// from the last to the first: the drafts' tiles, whose masks have to be fetched and whose values
+// looked through, come while the item's start has to be waited for anyhow (taken last they
+// delayed the item's end by 2 to 3 us).
 struct Walk {
     int64_t u;       // first unit behind the part
     int32_t left;    // units of the share behind the part
@@ -283,9 +286,9 @@ __device__ __forceinline__ uint2 dequant4(uint32_t codes, float scale) {
     return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// A row of each tile (a lane's own), moved on a tile at a time: its page id first, on its way
+// A row of each tile (a lane's own), moved back a tile at a time: its page id first, on its way
 // while other work is done, then its place in 16-byte units of the layer (kNoRow past the last
-// row and for ids that the cache does not have, which are reported).
+// row, before the first tile and for ids that the cache does not have, which are reported).
 constexpr uint32_t kNoRow = 0xffffffffu;
 struct Row {
     int32_t left;  // rows from it to the last
@@ -298,8 +301,8 @@ struct Row {
         page = static_cast<int32_t>(lp);
         slot = static_cast<int32_t>(pos - lp * a.page_size);
     }
-    __device__ __forceinline__ void fetch(const uint32_t* table) {
-        id = ld_nc_u32_if(table + page, left > 0);
+    __device__ __forceinline__ void fetch(const uint32_t* table, bool tile) {
+        id = ld_nc_u32_if(table + page, tile && left > 0);
     }
 };
 
@@ -315,17 +318,18 @@ struct Layout {
           page_size(a.page_size),
           tile_pages(kKeys / a.page_size),
           tile_slots(kKeys % a.page_size) {}
-    // The place of the row whose id was fetched, then on to the next tile's.
-    __device__ __forceinline__ void resolve(const TreeAttentionArgs& a, Row& r) const {
-        const bool have = r.left > 0 && r.id < pages;
+    // The place of the row whose id was fetched, then back to the tile before.  `tile`: the part
+    // has the tile.
+    __device__ __forceinline__ void resolve(const TreeAttentionArgs& a, Row& r, bool tile) const {
+        const bool exists = tile && r.left > 0, have = exists && r.id < pages;
         r.unit = have ? r.id * page_units + r.slot * slot_units : kNoRow;
-        if (r.left > 0 && !have) report(a.status, PKM_ERR_OUT_OF_RANGE);
-        r.left -= kKeys;
-        r.page += tile_pages;
-        r.slot += tile_slots;
-        const bool over = r.slot >= page_size;
-        r.page += over ? 1 : 0;
-        r.slot -= over ? page_size : 0;
+        if (exists && !have) report(a.status, PKM_ERR_OUT_OF_RANGE);
+        r.left += kKeys;
+        r.page -= tile_pages;
+        r.slot -= tile_slots;
+        const bool under = r.slot < 0;
+        r.page -= under ? 1 : 0;
+        r.slot += under ? page_size : 0;
     }
 };
 
@@ -487,25 +491,26 @@ __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars,
                                   u9[n] != kNoRow && ninth_c < a.cols);
     };
     while (ok && __any_sync(0xffffffffu, w.next(a))) {
-        const int steps = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0) * sets;
-        const int64_t pos0 = static_cast<int64_t>(w.kt0) * kKeys;
+        const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
+        const int64_t pos0 = static_cast<int64_t>(w.kt1 - 1) * kKeys;
         const int64_t end = min(w.r.kv, static_cast<int64_t>(w.kt1) * kKeys);
         const uint32_t* table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
-        // rows of the tile at hand and behind it that are cached ones, as far as 32 bits say
+        // rows of the tile at hand that are cached ones, if not all (and behind the first draft's
+        // tile less than none)
         int cached = __shfl_sync(
-            0xffffffffu,
-            static_cast<int>(min(w.r.len - pos0, static_cast<int64_t>(INT32_MAX))), 0);
+            0xffffffffu, static_cast<int>(min(w.r.len - pos0, static_cast<int64_t>(kKeys))), 0);
         row.start(a, pos0 + (lane < 16 ? own0 + lane : lane < 24 ? other0 + lane - 16 : 0), end);
-        const auto rows = [&] {  // of the next tile, and the id of the one behind it
-            layout.resolve(a, row);
-            row.fetch(table);
+        const auto rows = [&](int t) {  // of tile t of the part, and the id of the next
+            layout.resolve(a, row, t < tiles);
+            row.fetch(table, t + 1 < tiles);
         };
-        row.fetch(table);
-        rows();
+        row.fetch(table, true);
+        rows(0);
         load(0);
+        int t = 0;
         int set = 0;
 #pragma unroll 1
-        for (int step = 0; step < steps; ++step) {
+        while (t < tiles) {
             ok = plain_wait(&bars->k_empty[set], (g & 1) ^ 1, tries);
             if (set < vgroups) ok = ok && plain_wait(&bars->v_empty[ring.stage], ring.phase ^ 1, tries);
             ok = __all_sync(0xffffffffu, ok);
@@ -514,7 +519,7 @@ __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars,
                 break;
             }
             const int next = set + 1 == sets ? 0 : set + 1;
-            if (next == 0) rows();
+            if (next == 0) rows(t + 1);
             float f[6];
 #pragma unroll
             for (int n = 0; n < 6; ++n)
@@ -564,11 +569,12 @@ __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars,
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(k_full + set * 8);
             if (set < vgroups) ring.next(kValueRing);
-            if (step == 0) ok = queries(w);
+            if (t + set == 0) ok = queries(w);
             if (!ok) break;
             set = next;
             if (set > 0) continue;
-            cached -= kKeys;
+            ++t;
+            cached = min(cached + kKeys, kKeys);
             ++g;
             if (i == 0 && lane == 0) bars->progress = static_cast<int32_t>(g);
         }
@@ -691,12 +697,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Attended mask;
             const int32_t cached = w.cached_tiles();
             const auto key0 = [&](int32_t kt) { return static_cast<int64_t>(kt) * kKeys + half * 64 + part * 32; };
-            if (w.kt0 >= cached) mask.fetch(a, w.r, token, key0(w.kt0));
-            for (int32_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
+            if (w.kt1 > cached) mask.fetch(a, w.r, token, key0(w.kt1 - 1));
+            for (int32_t kt = w.kt1 - 1; kt >= w.kt0; --kt, ++g) {
                 const bool partial = kt >= cached;
                 uint32_t may = ~0u;
                 if (partial) may = mask.bits(a, w.r, token, key0(kt));
-                if (kt + 1 >= cached && kt + 1 < w.kt1) mask.fetch(a, w.r, token, key0(kt + 1));
+                if (kt > cached && kt > w.kt0) mask.fetch(a, w.r, token, key0(kt - 1));
                 if (!warp_wait(&bars->s_full[g & 1], (g >> 1) & 1, wc)) {
                     ok = false;
                     break;
@@ -755,7 +761,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (kt > w.kt0 && __any_sync(0xffffffffu, move)) {
+                if (kt + 1 < w.kt1 && __any_sync(0xffffffffu, move)) {
                     tc_fence_after();
                     for (int v = part * vblocks; v < (part + 1) * vblocks; ++v) {
                         uint32_t o[32];
@@ -986,7 +992,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int bytes = SRC >= kCodes ? R + 2 * (a.cols - R) + 4 * (R / 128) : 2 * a.cols;
         int g = 0;
         while (w.next(a))
-            for (int32_t kt = w.kt0; kt < w.kt1; ++kt, ++g) {
+            for (int32_t kt = w.kt1 - 1; kt >= w.kt0; --kt, ++g) {
                 for (uint32_t n = 0; g - 2 > *progress && n < tries; ++n) __nanosleep(500);
                 for (int x = 0; x < 2; ++x) {
                     const int64_t pos = static_cast<int64_t>(kt) * kKeys + rank * 64 + x * 32 + lane;
@@ -1091,7 +1097,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     fetch(w, 0, q);
                     for (int t = 0; t < tiles; ++t) {
                         if (!idle) {
-                            const int64_t pos0 = static_cast<int64_t>(w.kt0 + t) * kKeys + rank * 64;
+                            const int64_t pos0 = static_cast<int64_t>(w.kt1 - 1 - t) * kKeys + rank * 64;
                             const Place at(a, w.b, lane < boxes ? pos0 + lane * slots : w.r.kv, w.r.kv);
                             for (int blk = wide ? i * kTreeKeyBlocks : i; blk < kblocks; blk += step) {
                                 const uint32_t group = blk < kQueryBlocks ? 0 : 1;
@@ -1121,9 +1127,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int brings = wide ? ((i & 1) ? 0 : kTreeValueBlocks) : 1;
                 while (ok && i < 2 * vgroups && __any_sync(0xffffffffu, w.next(a))) {
                     const int tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
-                    const int cached = __shfl_sync(0xffffffffu, w.cached_tiles() - w.kt0, 0);
+                    const int behind = __shfl_sync(0xffffffffu, w.kt1 - w.cached_tiles(), 0);
                     for (int t = 0; t < tiles; ++t) {
-                        const int64_t pos0 = static_cast<int64_t>(w.kt0 + t) * kKeys;
+                        const int64_t pos0 = static_cast<int64_t>(w.kt1 - 1 - t) * kKeys;
                         const Place at(a, w.b, lane < boxes ? pos0 + lane * slots : w.r.kv, w.r.kv);
                         RingPos mine = ring;
                         if (i >= 2) mine.next(kValueRing);
@@ -1131,7 +1137,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint8_t* dst = sV + s * 2 * kValueBytes + (i & 1) * kValueBytes;
                         ok = issue_wait(&bars->v_empty[s], mine.phase ^ 1);
                         if (!ok) break;
-                        if (t < cached) {
+                        if (t >= behind) {
                             if (lane == 0) {
                                 if (leader) mbar_arrive_expect_tx(&bars->v_full[s], 2 * brings * block);
                                 else mbar_arrive_remote(v_full + s * 8);
@@ -1178,7 +1184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             if (lane == 0) mbar_arrive_remote(v_full + s * 8);
                         }
                         for (int v = 0; v < vgroups; ++v) {
-                            if (t >= cached) own_phase ^= 1u << ring.stage;
+                            if (t < behind) own_phase ^= 1u << ring.stage;
                             ring.next(kValueRing);
                         }
                     }
