@@ -121,6 +121,7 @@ struct TreeAttentionArgs {
     uint8_t* workspace;
     int32_t* status;
     uint64_t timeout_ns;
+    int32_t item_cost;  // start and end of an item, in tiles (filled in by the launcher)
 };
 
 // One kv_matmul problem, already validated.

@@ -42,12 +42,19 @@
 namespace pkm {
 namespace {
 
+// Pages by TMA, bf16 rows by loads, quantised rows whose codes fill both sets of blocks (a rank of
+// 512) and others, whose rope columns lie among them.
+enum Source { kTma, kRows, kCodes, kCodesNarrow };
+
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kQueryWarp = 9, kFetchWarp = 10, kKeyWarp = 12, kValueWarp = 16;
 constexpr int kThreads = 20 * 32;
 // Registers of the four-warp groups (two of softmax warps, the issuing warps, two of loaders), of
 // the 5 x 96 that the block starts with: by loads the rows on their way need more.
 constexpr int kIssueRegs = 64, kMoreRegs = 112;
-constexpr int kItemCost = 4;        // an item's start and end, in tiles (7 us against 1.6 us)
+// An item's start and end, in tiles: 5 us against 1.4 us of a tile by TMA and 3 us of one by loads
+// (2 for both took large drafted trees from 331 to 342 us, 4 for both chains over the quantised
+// cache from 114 to 118 us).
+constexpr int item_cost(Source src) { return src == kTma ? 4 : 2; }
 constexpr int kKeys = 128;          // keys of a tile (64 loaded by each CTA as keys)
 constexpr int kBlocks = 9;          // 64-column blocks of a latent row
 constexpr int kBlockBytes = 64 * 128;
@@ -61,10 +68,6 @@ constexpr uint32_t kQueryCol = 384; // TMEM column of the queries, 32 a block
 constexpr uint64_t kDrainNs = 1000000;  // a role that gave up leaves its loads time to land
 constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
-
-// Pages by TMA, bf16 rows by loads, quantised rows whose codes fill both sets of blocks (a rank of
-// 512) and others, whose rope columns lie among them.
-enum Source { kTma, kRows, kCodes, kCodesNarrow };
 
 // a / b; the 64-bit division is a long routine, and the operands are hardly ever that large.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -80,6 +83,7 @@ struct Request {
     int64_t kv;      // positions that exist: len + n, cut at the page-table row
     int32_t tiles;   // 128-key tiles
     int32_t items;   // 128-row items
+    int32_t units_each;  // units of an item
 
     __device__ __forceinline__ void load(const TreeAttentionArgs& a, int b) {
         const int64_t rows = a.total_rows;
@@ -90,11 +94,11 @@ struct Request {
         len = __ldg(a.cache_lengths + b);
         kv = min(len + n, static_cast<int64_t>(a.max_pages) * a.page_size);
         tiles = static_cast<int32_t>((kv + kKeys - 1) / kKeys);
+        units_each = tiles + a.item_cost;
         items = static_cast<int32_t>((static_cast<int64_t>(n) * a.num_heads + 127) / 128);
     }
-    __device__ __forceinline__ int32_t item_units() const { return tiles + kItemCost; }
     __device__ __forceinline__ int64_t units() const {
-        return n > 0 ? static_cast<int64_t>(item_units()) * items : 0;
+        return n > 0 ? static_cast<int64_t>(units_each) * items : 0;
     }
 };
 
@@ -130,7 +134,7 @@ constexpr size_t kSmemBytes = kOffBars + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103a CTA");
 
 // A pair's share of the units of all items, walked item by item.  An item has a unit for each
-// of its tiles, behind kItemCost units that stand for its start and end.  After next()
+// of its tiles, behind item_cost units that stand for its start and end.  After next()
 // returned true, the part is tiles [kt0, kt1) of item `item` of request r, which all roles take
 // from the last to the first: the drafts' tiles, whose masks have to be fetched and whose values
 // looked through, come while the item's start has to be waited for anyhow (taken last they
@@ -154,7 +158,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const TreeAttentionArgs& a) {
         do {
             if (left <= 0) return false;
-            if (at == r.item_units()) {
+            if (at == r.units_each) {
                 at = 0;
                 if (++item == r.items) {
                     item = 0;
@@ -162,10 +166,10 @@ struct Walk {
                     while (r.units() == 0);
                 }
             }
-            const int32_t take = min(r.item_units() - at, left);
-            kt0 = max(at - kItemCost, 0);
+            const int32_t take = min(r.units_each - at, left);
+            kt0 = max(at - a.item_cost, 0);
             at += take;
-            kt1 = max(at - kItemCost, 0);
+            kt1 = max(at - a.item_cost, 0);
             u += take;
             left -= take;
         } while (kt1 == kt0);  // a share can end within an item's first units
@@ -218,9 +222,9 @@ __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int
                 bars->share = static_cast<int32_t>(quotient(total * (pair + 1), pairs) - u);
                 bars->request = b;
                 bars->first = r;
-                const int32_t item = static_cast<int32_t>(quotient(u - at, r.item_units()));
+                const int32_t item = static_cast<int32_t>(quotient(u - at, r.units_each));
                 bars->item = item;
-                bars->unit = static_cast<int32_t>((u - at) - static_cast<int64_t>(item) * r.item_units());
+                bars->unit = static_cast<int32_t>((u - at) - static_cast<int64_t>(item) * r.units_each);
                 break;
             }
             at += r.units();
@@ -1376,7 +1380,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3)
 
 template <Source SRC>
 cudaError_t launch_source(const CUtensorMap& tm_q, const CUtensorMap& tm_k0, const CUtensorMap& tm_k1,
-                          const CUtensorMap& tm_v, const TreeAttentionArgs& args,
+                          const CUtensorMap& tm_v, TreeAttentionArgs args,
                           const TreeWorkspace& ws, const TreeBoxes& boxes, int pairs,
                           cudaStream_t stream) {
     // once a device: the attribute stays (every thread sets the same value)
@@ -1393,6 +1397,7 @@ cudaError_t launch_source(const CUtensorMap& tm_q, const CUtensorMap& tm_k0, con
         if (e != cudaSuccess) return e;
         if (known) set[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
     }
+    args.item_cost = item_cost(SRC);
     return launch_dependent(tree_attention_kernel<SRC>, static_cast<unsigned>(2 * pairs), kThreads,
                             kSmemBytes, stream, tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes);
 }
