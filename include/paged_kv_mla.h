@@ -425,7 +425,9 @@ size_t mla_tree_attention_paged_workspace_size(int32_t total_rows, int32_t num_h
  *   rope_dim        P: a multiple of 8 with R + P <= 576.
  *   softmax_scale   finite.
  *   tree_mask       device uint32 [total_rows, mask_words], or NULL.
- *   cache           row_elems = R + P; cache_lengths required.
+ *   cache           row_elems = R + P; cache_lengths required.  With a page size that is no
+ *                   multiple of 8 a layer may span at most 64 GiB (PKM_ERR_UNSUPPORTED); rows
+ *                   then come by loads, at about half the speed.
  *   out             device bf16 [total_rows, num_heads, R], 16-byte aligned.
  *   lse             device fp32 [total_rows, num_heads], or NULL.
  *   workspace       device, >= mla_tree_attention_paged_workspace_size(...) bytes, 256-byte
@@ -445,7 +447,8 @@ pkm_status mla_tree_attention_paged(const void* q, const uint32_t* input_row_off
  * mla_tree_attention_paged over a quantised cache: slot(t) is the row that
  * mla_decompress_k_paged_fp8_qcache returns in k_latent_buffer (bf16_rne(fl32(e4m3(code) *
  * scale)) in its first R columns, the bf16 rope columns behind them).  R and P come from the
- * descriptor (R a multiple of 128, at most 512; R + P <= 576; cache_lengths required).
+ * descriptor (R a multiple of 128, at most 512; R + P <= 576; cache_lengths required).  A
+ * layer may span at most 64 GiB (PKM_ERR_UNSUPPORTED).
  */
 pkm_status mla_tree_attention_paged_qcache(const void* q, const uint32_t* input_row_offsets,
                                            int32_t batch, int32_t total_rows,

@@ -209,9 +209,10 @@ class _Descriptor:
         if c is None:
             c = self.__dict__["_c"] = self._new_struct()
         else:
+            table = self.page_table
             c.data = self.data.data_ptr()
-            c.page_table = self.page_table.data_ptr()
-            c.max_pages_per_seq = self.page_table.shape[-1]
+            c.page_table = table.data_ptr()
+            c.max_pages_per_seq = table.shape[-1]
             c.cache_lengths = _ptr(self.cache_lengths)
         return c
 
@@ -413,6 +414,25 @@ def mla_cache_write_paged(latent: torch.Tensor, input_row_offsets: torch.Tensor,
     return _check(code, "mla_cache_write_paged", check)
 
 
+_initialized = torch.cuda.is_initialized
+
+
+def _plain(itemsize: int, *tensors) -> bool:
+    """Whether the tensors are what the C calls take them for, elements of that size without
+    gaps, and lie on the device that the call runs on (None and addresses pass)."""
+    device = torch._C._cuda_getDevice() if _initialized() else -1
+    for t in tensors:
+        if t is None or t.__class__ is int:
+            continue
+        if t.itemsize != itemsize or not t.is_contiguous() or t.get_device() != device:
+            return False
+    return True
+
+
+def _has(n: int, t) -> bool:
+    return t is None or t.__class__ is int or t.numel() == n
+
+
 def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tensor,
                              positions: torch.Tensor, kv_norm_gamma: torch.Tensor,
                              epsilon: float, freqs_cis: torch.Tensor, cache: PagedCache,
@@ -421,14 +441,16 @@ def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tens
                              check: bool = True) -> int:
     """mla_cache_write_paged with row r rotated by freqs_cis[positions[r]] (positions:
     uint32/int32 [total_rows]), wherever its slot is."""
+    rows = latent.shape[0]
+    if not _has(rows, positions) or not _plain(4, positions):
+        return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_at", check)
     c = cache.c_struct()
-    batch = int(input_row_offsets.shape[0]) - 1
+    batch = input_row_offsets.shape[0] - 1
     code = _lib.mla_cache_write_paged_at(_ptr(latent), _ptr(input_row_offsets), _ptr(positions),
-                                         batch, int(latent.shape[0]), int(kv_lora_rank),
-                                         int(rope_dim), _ptr(kv_norm_gamma), float(epsilon),
-                                         _ptr(freqs_cis), int(freqs_cis.shape[0]),
-                                         ctypes.byref(c), int(layer_idx), _ptr(dev_status),
-                                         _stream(stream))
+                                         batch, rows, int(kv_lora_rank), int(rope_dim),
+                                         _ptr(kv_norm_gamma), float(epsilon), _ptr(freqs_cis),
+                                         freqs_cis.shape[0], ctypes.byref(c), int(layer_idx),
+                                         _ptr(dev_status), _stream(stream))
     return _check(code, "mla_cache_write_paged_at", check)
 
 
@@ -438,10 +460,13 @@ def mla_cache_write_paged_qcache_at(latent: torch.Tensor, input_row_offsets: tor
                                     layer_idx: int, dev_status: Optional[torch.Tensor] = None,
                                     stream=None, check: bool = True) -> int:
     """mla_cache_write_paged_qcache with row r rotated by freqs_cis[positions[r]]."""
+    rows = latent.shape[0]
+    if not _has(rows, positions) or not _plain(4, positions):
+        return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_qcache_at", check)
     c = cache.c_struct()
-    batch = int(input_row_offsets.shape[0]) - 1
+    batch = input_row_offsets.shape[0] - 1
     code = _lib.mla_cache_write_paged_qcache_at(_ptr(latent), _ptr(input_row_offsets),
-                                                _ptr(positions), batch, int(latent.shape[0]),
+                                                _ptr(positions), batch, rows,
                                                 _ptr(kv_norm_gamma), float(epsilon),
                                                 _ptr(freqs_cis), int(freqs_cis.shape[0]),
                                                 ctypes.byref(c), int(layer_idx),
@@ -456,13 +481,16 @@ def mla_rope_heads(x: torch.Tensor, positions: torch.Tensor, freqs_cis: torch.Te
     """Rotates x [rows, heads, P] into y [rows, heads, P] (bf16 views with contiguous last
     dimensions; y may be x) by the (cos, sin) pairs of freqs_cis[positions[row]]: pairs
     (2j, 2j + 1), or (j, j + P/2) with `half`."""
-    if x.shape != y.shape or x.dim() != 3 or positions.numel() != x.shape[0] \
-            or freqs_cis.shape[-1] != x.shape[-1] or x.stride(-1) != 1 or y.stride(-1) != 1:
+    shape, sx, sy = x.shape, x.stride(), y.stride()
+    if y.shape != shape or len(shape) != 3 or sx[2] != 1 or sy[2] != 1 or x.itemsize != 2 \
+            or y.itemsize != 2 or not _has(shape[0], positions) \
+            or freqs_cis.shape[-1] != shape[2] or not _plain(4, positions, freqs_cis) \
+            or x.get_device() != freqs_cis.get_device() or y.get_device() != x.get_device():
         return _check(PKM_ERR_INVALID_ARG, "mla_rope_heads", check)
-    code = _lib.mla_rope_heads(_ptr(x), x.stride(0), x.stride(1), _ptr(positions),
-                               int(x.shape[0]), int(x.shape[1]), int(x.shape[2]),
-                               _ptr(freqs_cis), int(freqs_cis.shape[0]), int(bool(half)), _ptr(y),
-                               y.stride(0), y.stride(1), _ptr(dev_status), _stream(stream))
+    code = _lib.mla_rope_heads(x.data_ptr(), sx[0], sx[1], _ptr(positions), shape[0], shape[1],
+                               shape[2], freqs_cis.data_ptr(), freqs_cis.shape[0],
+                               1 if half else 0, y.data_ptr(), sy[0], sy[1], _ptr(dev_status),
+                               _stream(stream))
     return _check(code, "mla_rope_heads", check)
 
 
@@ -472,12 +500,17 @@ def mla_tree_attention_paged_workspace_size(total_rows: int, num_heads: int,
                                                             int(kv_lora_rank)))
 
 
-def _tree_shapes_ok(q, tree_mask, out, lse) -> bool:
+def _tree_shapes_ok(q, offsets, tree_mask, out, lse, workspace, rank, rope) -> bool:
     """Shapes that the C call cannot see; an empty mask would pass for no mask there."""
-    rows, heads = q.shape[0], q.shape[1]
-    return (out.shape[:2] == (rows, heads) and (lse is None or lse.shape == (rows, heads)) and
-            (tree_mask is None or (tree_mask.dim() == 2 and tree_mask.shape[0] == rows and
-                                   tree_mask.shape[1] > 0)))
+    if q.ndim != 3:
+        return False
+    rows, heads, cols = q.shape
+    return (cols == rank + rope and out.shape == (rows, heads, rank) and
+            (lse is None or lse.shape == (rows, heads)) and
+            (tree_mask is None or (tree_mask.ndim == 2 and tree_mask.shape[0] == rows and
+                                   tree_mask.shape[1] > 0)) and
+            _plain(2, q, out) and _plain(4, offsets, tree_mask, lse) and
+            _plain(workspace.itemsize, workspace))
 
 
 def mla_tree_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
@@ -491,15 +524,16 @@ def mla_tree_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
     cache: each over its request's cached tokens and those new ones that its tree_mask row
     (uint32/int32 [total_rows, words], one bit a token; None: the tokens up to itself) names.
     out [total_rows, heads, R] bf16, lse [total_rows, heads] fp32 or None."""
-    if not _tree_shapes_ok(q, tree_mask, out, lse):
+    if not _tree_shapes_ok(q, input_row_offsets, tree_mask, out, lse, workspace, kv_lora_rank,
+                           rope_dim):
         return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged", check)
     c = cache.c_struct()
-    batch = int(input_row_offsets.shape[0]) - 1
+    rows, heads, _ = q.shape
     code = _lib.mla_tree_attention_paged(
-        _ptr(q), _ptr(input_row_offsets), batch, int(q.shape[0]), int(q.shape[1]),
+        q.data_ptr(), input_row_offsets.data_ptr(), input_row_offsets.shape[0] - 1, rows, heads,
         int(kv_lora_rank), int(rope_dim), float(softmax_scale), _ptr(tree_mask),
-        0 if tree_mask is None else int(tree_mask.shape[-1]), ctypes.byref(c), int(layer_idx),
-        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
+        out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
         _ptr(dev_status), _stream(stream))
     return _check(code, "mla_tree_attention_paged", check)
 
@@ -512,17 +546,25 @@ def mla_tree_attention_paged_qcache(q: torch.Tensor, input_row_offsets: torch.Te
                                     dev_status: Optional[torch.Tensor] = None, stream=None,
                                     check: bool = True) -> int:
     """mla_tree_attention_paged over a quantised cache."""
-    if not _tree_shapes_ok(q, tree_mask, out, lse):
+    if not _tree_shapes_ok(q, input_row_offsets, tree_mask, out, lse, workspace,
+                           cache.kv_lora_rank, cache.rope_dim):
         return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged_qcache", check)
     c = cache.c_struct()
-    batch = int(input_row_offsets.shape[0]) - 1
+    rows, heads, _ = q.shape
     code = _lib.mla_tree_attention_paged_qcache(
-        _ptr(q), _ptr(input_row_offsets), batch, int(q.shape[0]), int(q.shape[1]),
+        q.data_ptr(), input_row_offsets.data_ptr(), input_row_offsets.shape[0] - 1, rows, heads,
         float(softmax_scale), _ptr(tree_mask),
-        0 if tree_mask is None else int(tree_mask.shape[-1]), ctypes.byref(c), int(layer_idx),
-        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
+        out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
         _ptr(dev_status), _stream(stream))
     return _check(code, "mla_tree_attention_paged_qcache", check)
+
+
+def _accepted_ok(shape, cache, accepted, counts, new_lengths) -> bool:
+    """One list of accepted drafts, count and new length for each request of the cache."""
+    return (len(shape) == 2 and cache.page_table.shape[0] == shape[0] and
+            _has(shape[0], counts) and _has(shape[0], new_lengths) and
+            _plain(4, accepted, counts, new_lengths))
 
 
 def mla_cache_compact_paged(cache: PagedCache, layer_begin: int, layer_count: int,
@@ -533,10 +575,12 @@ def mla_cache_compact_paged(cache: PagedCache, layer_begin: int, layer_count: in
     """Moves request b's accepted drafts accepted[b, :accepted_counts[b]] (strictly increasing
     indices behind cache_lengths[b]) to the front of its drafted region in every layer of the
     range, and writes the grown lengths to new_lengths."""
+    shape = accepted.shape
+    if not _accepted_ok(shape, cache, accepted, accepted_counts, new_lengths):
+        return _check(PKM_ERR_INVALID_ARG, "mla_cache_compact_paged", check)
     c = cache.c_struct()
-    code = _lib.mla_cache_compact_paged(ctypes.byref(c), int(layer_begin), int(layer_count),
-                                        int(accepted.shape[0]), _ptr(accepted),
-                                        int(accepted.shape[1]), _ptr(accepted_counts),
+    code = _lib.mla_cache_compact_paged(ctypes.byref(c), layer_begin, layer_count, shape[0],
+                                        accepted.data_ptr(), shape[1], _ptr(accepted_counts),
                                         _ptr(new_lengths), _ptr(dev_status), _stream(stream))
     return _check(code, "mla_cache_compact_paged", check)
 
@@ -547,12 +591,13 @@ def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_co
                                    dev_status: Optional[torch.Tensor] = None, stream=None,
                                    check: bool = True) -> int:
     """mla_cache_compact_paged for a quantised cache."""
+    shape = accepted.shape
+    if not _accepted_ok(shape, cache, accepted, accepted_counts, new_lengths):
+        return _check(PKM_ERR_INVALID_ARG, "mla_cache_compact_paged_qcache", check)
     c = cache.c_struct()
-    code = _lib.mla_cache_compact_paged_qcache(ctypes.byref(c), int(layer_begin),
-                                               int(layer_count), int(accepted.shape[0]),
-                                               _ptr(accepted), int(accepted.shape[1]),
-                                               _ptr(accepted_counts), _ptr(new_lengths),
-                                               _ptr(dev_status), _stream(stream))
+    code = _lib.mla_cache_compact_paged_qcache(ctypes.byref(c), layer_begin, layer_count, shape[0],
+                                               accepted.data_ptr(), shape[1], _ptr(accepted_counts),
+                                               _ptr(new_lengths), _ptr(dev_status), _stream(stream))
     return _check(code, "mla_cache_compact_paged_qcache", check)
 
 

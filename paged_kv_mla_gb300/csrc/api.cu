@@ -942,8 +942,6 @@ pkm_status tree_attention(TreeAttentionArgs a, const void* q, const uint32_t* in
     a.workspace = static_cast<uint8_t*>(workspace);
     a.status = dev_status;
     a.timeout_ns = wait_timeout_ns();
-    int sms = 0;
-    if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
     // Query rows and, where the pages are divided by boxes of at least 8 slots (whole swizzle
     // atoms), the cache come by TMA; other pages and quantised rows are loaded row by row.
     // A box holds as many slots of one page as a tile's 64 keys or 128 values and the page
@@ -956,7 +954,9 @@ pkm_status tree_attention(TreeAttentionArgs a, const void* q, const uint32_t* in
     if ((a.qcache_layer != nullptr && span / 16 >= UINT32_MAX - 1) ||
         (a.qcache_layer == nullptr && box < 8 && span / 8 >= UINT32_MAX - 1))
         return PKM_ERR_UNSUPPORTED;
-    // and, where that is all of them and the row has only whole blocks, several blocks
+    int sms = 0;
+    if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
+    // where that is all of them and the row has only whole blocks, a box has several blocks
     const bool whole = a.cols % 64 == 0;
     const bool key_groups = whole && box == 64, value_groups = whole && vbox == 128;
     const auto encode_pages = [&](CUtensorMap* map, int slots, int blocks) {

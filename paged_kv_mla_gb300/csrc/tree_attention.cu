@@ -185,8 +185,9 @@ struct Walk {
 // requests.  `scratch`: an int64 of shared memory for every warp.
 __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int64_t* scratch,
                                      int64_t pair, int64_t pairs) {
-    const int per = (a.batch + kThreads - 1) / kThreads;
-    const int b0 = min(static_cast<int>(threadIdx.x) * per, a.batch), b1 = min(b0 + per, a.batch);
+    const int64_t per = (static_cast<int64_t>(a.batch) + kThreads - 1) / kThreads, all = a.batch;
+    const int b0 = static_cast<int>(min(threadIdx.x * per, all));
+    const int b1 = static_cast<int>(min(b0 + per, all));
     int64_t sum = 0;
     Request r;
     for (int b = b0; b < b1; ++b) {

@@ -279,3 +279,98 @@ def test_drafts_over_tiles_of_many_items(page):
     ctx = [int(x) for x in gen.integers(0, 400, 40)]
     new = [int(x) for x in gen.integers(1, 65, 40)]
     check(make_tree(620 + page, ctx, new, 24, 512, 64, page=page))
+
+
+@pytest.mark.parametrize("rank,rope", [(64, 16), (64, 0), (128, 32), (192, 64), (256, 64),
+                                       (320, 8), (384, 192), (448, 128), (512, 0), (512, 24),
+                                       (512, 64)])
+def test_widths_of_rows_by_loads(rank, rope):
+    """Pages of no multiple of 8 slots."""
+    check(make_tree(630 + rank + rope, [140, 300], [5, 3], 6, rank, rope, page=12))
+
+
+@pytest.mark.parametrize("new", [1, 33, 65, 130, 260])
+@pytest.mark.parametrize("page,quantised", [(12, False), (64, True), (64, False)])
+def test_drafts_over_several_tiles(new, page, quantised):
+    check(make_tree(640 + new, [77, 0, 300], [new, 2, 5], 4, page=page, quantised=quantised))
+
+
+@pytest.mark.parametrize("page,quantised", [(12, False), (32, True), (32, False)])
+def test_falling_and_growing_scores(page, quantised):
+    """Scores that grow towards one end of the history, from which the maximum moves on."""
+    p = make_tree(650, [1500], [1], 4, 512, 64, page=page, tree=False, quantised=quantised)
+    p.q[:, 1] = p.q[:, 0] ^ 0x8000  # head 1: minus head 0's, so one grows where the other falls
+    from spec_util import bf16_bits
+    t = np.arange(1500)
+    c = 512 if quantised else 0  # the rope columns are bf16 in both
+    cells = p.cache[p.layer, p.table[0][t // page], t % page]
+    rope = cells[:, 512:512 + 128].copy().view(np.uint16) if quantised else cells[:, 512:576]
+    direction = bf16_value(p.q[0, 0, 512:])
+    rows = bf16_value(rope) + np.outer(t / 20.0, direction) / np.linalg.norm(direction)
+    bits = bf16_bits(rows)
+    cells[:, c if quantised else 512:c + 128 if quantised else 576] = \
+        bits.view(np.uint8) if quantised else bits
+    p.cache[p.layer, p.table[0][t // page], t % page] = cells
+    check(p)
+
+
+def test_output_between_sectors():
+    """An output that is 16-byte but not 32-byte aligned."""
+    p = make_tree(651, [100, 9], [40, 3], 8, 512, 64, page=64)
+    g = DeviceTree(p)
+    flat = torch.full((g.out.numel() + 8,), OUT_FILL, dtype=torch.int16, device="cuda")
+    g.out = flat[8:].view(g.out.shape)
+    assert g.out.data_ptr() % 32 == 16
+    g.run()
+    out, lse, status = g.results()
+    assert status == 0 and (flat[:8] == flat[0]).all()
+    assert_tree_close(p, out, lse)
+
+
+@pytest.mark.parametrize("page,quantised", [(100, False), (64, True)])
+def test_rows_by_loads_beyond_32_bit_offsets(page, quantised):
+    p = make_tree(652, [70, 200], [2, 3], 4, 512, 64, page=page, layers=1, layer=0,
+                  quantised=quantised)
+    g = DeviceTree(p)
+    L, N, S, E = p.cache.shape
+    stride = 1 << 30 if quantised else 1 << 29  # pages a GiB apart
+    big = torch.full(((N - 1) * stride + S * E,), 0x7F, dtype=g.cache.dtype, device="cuda")
+    for k in range(N):
+        big[k * stride:k * stride + S * E] = g.cache[0, k].flatten()
+    g.desc.data, g.desc.page_stride, g.desc.layer_stride = big, stride, 0
+    g.run()
+    out, lse, status = g.results()
+    assert status == 0
+    assert_tree_close(p, out, lse)
+
+
+def test_one_page_without_a_stride():
+    """A cache of a single page, whose page stride says nothing."""
+    for quantised in (False, True):
+        p = make_tree(653, [100], [3], 4, 512, 64, page=128, layers=1, layer=0, quantised=quantised)
+        used = int(p.table[0, 0])
+        p.cache = p.cache[:, used:used + 1].copy()
+        p.table = np.zeros_like(p.table[:, :1])
+        g = DeviceTree(p)
+        g.desc.page_stride = 0
+        g.run()
+        out, lse, status = g.results()
+        assert status == 0
+        assert_tree_close(p, out, lse)
+
+
+def test_refuses_views_and_host_memory():
+    import paged_kv_mla_gb300 as pkm
+    p = make_tree(654, [20], [3], 4, 512, 64, page=64)
+    g = DeviceTree(p)
+    args = dict(tree_mask=g.mask, lse=g.lse, check=False)
+
+    def call(q=g.q, out=g.out, **kw):
+        return pkm.mla_tree_attention_paged(q, g.offsets, p.scale, g.desc, p.layer, 512, 64, out,
+                                            g.workspace, **{**args, **kw})
+    assert call() == 0
+    assert call(q=g.q.cpu()) == 1
+    assert call(out=torch.zeros(3, 4, 576, dtype=torch.int16, device="cuda")[:, :, :512]) == 1
+    assert call(tree_mask=g.mask.long()) == 1
+    assert call(lse=g.lse.double()) == 1
+    torch.cuda.synchronize()

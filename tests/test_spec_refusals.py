@@ -191,3 +191,31 @@ def test_cache_write_at_needs_positions(pkm):
                                                check=False) == INVALID
     assert pkm.mla_cache_write_paged_at(lat, i32(3), i32(3), g, 1e-6, f, paged(pkm, row_elems=80), 0,
                                         512, 64, stream=0, check=False) == INVALID
+
+
+def test_views_that_the_calls_cannot_see(pkm):
+    """Strided tensors and other element sizes, which the C call would read as plain arrays."""
+    q = b16(3, 2, 640)[:, :, :576]
+    assert attention(pkm, paged(pkm), q=q) == INVALID
+    assert attention(pkm, paged(pkm), out=b16(3, 2, 576)[:, :, :512]) == INVALID
+    assert attention(pkm, paged(pkm), mask=torch.zeros(3, 1, dtype=torch.int64)) == INVALID
+    assert attention(pkm, quant(pkm), q=q) == INVALID
+    cache = paged(pkm)
+    for accepted, counts in ((i32(2, 8)[:, :3], i32(2)), (i32(3, 4), i32(2)), (i32(2, 4), i32(3)),
+                             (i32(2, 4).long(), i32(2))):
+        assert pkm.mla_cache_compact_paged(cache, 0, 1, accepted, counts, stream=0,
+                                           check=False) == INVALID
+    x = b16(3, 2, 64)
+    for positions in (i32(6)[::2], i32(3).long()):
+        assert pkm.mla_rope_heads(x, positions, torch.zeros(8, 64), x, stream=0,
+                                  check=False) == INVALID
+        assert pkm.mla_cache_write_paged_at(b16(3, 576), i32(3), positions, torch.ones(512), 1e-6,
+                                            torch.zeros(8, 64), cache, 0, 512, 64, stream=0,
+                                            check=False) == INVALID
+
+
+def test_layers_too_long_for_loads(pkm):
+    """Rows brought by loads count 16-byte units in 32 bits."""
+    far = dict(page_stride=1 << 35, layer_stride=1 << 37)
+    assert attention(pkm, paged(pkm, page_size=12, **far)) == UNSUPPORTED
+    assert attention(pkm, quant(pkm, **far)) == UNSUPPORTED
