@@ -430,7 +430,8 @@ def _plain(itemsize: int, *tensors) -> bool:
 
 
 def _has(n: int, t) -> bool:
-    return t is None or t.__class__ is int or t.numel() == n
+    """At least n elements, as far as can be seen."""
+    return t is None or t.__class__ is int or t.numel() >= n
 
 
 def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tensor,
@@ -483,7 +484,7 @@ def mla_rope_heads(x: torch.Tensor, positions: torch.Tensor, freqs_cis: torch.Te
     (2j, 2j + 1), or (j, j + P/2) with `half`."""
     shape, sx, sy = x.shape, x.stride(), y.stride()
     if y.shape != shape or len(shape) != 3 or sx[2] != 1 or sy[2] != 1 or x.itemsize != 2 \
-            or y.itemsize != 2 or not _has(shape[0], positions) \
+            or y.itemsize != 2 or positions.numel() != shape[0] \
             or freqs_cis.shape[-1] != shape[2] or not _plain(4, positions, freqs_cis) \
             or x.get_device() != freqs_cis.get_device() or y.get_device() != x.get_device():
         return _check(PKM_ERR_INVALID_ARG, "mla_rope_heads", check)
@@ -561,8 +562,8 @@ def mla_tree_attention_paged_qcache(q: torch.Tensor, input_row_offsets: torch.Te
 
 
 def _accepted_ok(shape, cache, accepted, counts, new_lengths) -> bool:
-    """One list of accepted drafts, count and new length for each request of the cache."""
-    return (len(shape) == 2 and cache.page_table.shape[0] == shape[0] and
+    """A table row, count and new length for each list of accepted drafts (and maybe for more)."""
+    return (len(shape) == 2 and cache.page_table.shape[0] >= shape[0] and
             _has(shape[0], counts) and _has(shape[0], new_lengths) and
             _plain(4, accepted, counts, new_lengths))
 

@@ -201,7 +201,7 @@ def test_views_that_the_calls_cannot_see(pkm):
     assert attention(pkm, paged(pkm), mask=torch.zeros(3, 1, dtype=torch.int64)) == INVALID
     assert attention(pkm, quant(pkm), q=q) == INVALID
     cache = paged(pkm)
-    for accepted, counts in ((i32(2, 8)[:, :3], i32(2)), (i32(3, 4), i32(2)), (i32(2, 4), i32(3)),
+    for accepted, counts in ((i32(2, 8)[:, :3], i32(2)), (i32(3, 4), i32(3)), (i32(2, 4), i32(1)),
                              (i32(2, 4).long(), i32(2))):
         assert pkm.mla_cache_compact_paged(cache, 0, 1, accepted, counts, stream=0,
                                            check=False) == INVALID
