@@ -1214,39 +1214,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
-constexpr int kFewParts = 2;
+constexpr int kJoinBlocks = 3;  // resident on an SM; more would wait for the first to end
+constexpr int kFewParts = 8, kAtATime = 2;  // parts that a warp joins alone, and its loads in flight
+
+// Where the items of the pairs begin among the tasks of one kind, and the item of a task.
+struct JoinTasks {
+    int begins[kTreeMaxPairs + 1];
+
+    // The last pair whose first task is at or before f.
+    __device__ __forceinline__ int pair_of(int f, int pairs) const {
+        int p = 0, behind = pairs;
+        while (behind - p > 1) {
+            const int mid = (p + behind) / 2;
+            if (begins[mid] <= f) p = mid;
+            else behind = mid;
+        }
+        return p;
+    }
+};
 
 // Joins the parts of the items that several pairs share: with M the largest of the parts'
 // maxima, out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same order.
 // A lane has a row and 16 (few parts) or 32 of its columns.  Few parts, as of a batch whose
-// items are cut once or twice, are one warp's task each, all their loads in flight at once;
-// many parts, as of few long histories, are dealt to the warps of a block, which meet in
-// shared memory and then each finish a share of the columns.
-__global__ void __launch_bounds__(kJoinThreads, 3)
+// items are cut a few times, are one warp's task each, two parts' loads in flight at once; many
+// parts, as of few long histories, are dealt to the warps of a block, which meet in shared
+// memory and then each finish a share of the columns.  Bound by latency: some 10 to 40 MB of sums
+// come from L2, and all blocks are resident when the attention ends.
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
     tree_join_kernel(const TreeAttentionArgs a, const TreeWorkspace ws, const int pairs) {
     __shared__ TreeItem items[kTreeMaxPairs];
-    __shared__ int begins[kTreeMaxPairs + 1];  // first task of every item, and their number
+    __shared__ JoinTasks few, many;
     __shared__ float sums[kJoinWarps][32][32], tops[kJoinWarps][32], totals[kJoinWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int R = a.kv_lora_rank;
-    // tasks of a block: 16 columns a warp, or 32 columns for all warps
-    const auto tasks_of = [&](const TreeItem& it) {
-        const int groups = it.parts <= kFewParts ? (R / 16 + kJoinWarps - 1) / kJoinWarps : R / 32;
-        return (it.rows + 31) / 32 * groups;
-    };
+    const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     griddep_launch_dependents();
     griddep_wait();
-    if (warp == 0) {
+    const TreeItem* left = reinterpret_cast<const TreeItem*>(a.workspace + ws.items);
+    if (warp < 2) {  // the first for the items of few parts, the second for the others
         constexpr int kEach = (kTreeMaxPairs + 31) / 32;
+        const int columns = warp == 0 ? R / 16 : R / 32;
+        int* begins = warp == 0 ? few.begins : many.begins;
         int n[kEach], sum = 0;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int p = lane * kEach + k;
             n[k] = 0;
             if (p < pairs) {
-                const TreeItem it = reinterpret_cast<const TreeItem*>(a.workspace + ws.items)[p];
-                items[p] = it;
-                n[k] = it.rows > 0 ? tasks_of(it) : 0;
+                const TreeItem it = left[p];
+                if (warp == 0) items[p] = it;
+                if ((it.parts <= kFewParts) == (warp == 0)) n[k] = (max(it.rows, 0) + 31) / 32 * columns;
             }
             sum += n[k];
         }
@@ -1265,45 +1282,43 @@ __global__ void __launch_bounds__(kJoinThreads, 3)
         }
     }
     __syncthreads();
-    const int tasks = begins[pairs];
     const float2* stats = reinterpret_cast<const float2*>(a.workspace + ws.stats);
     const float4* parts = reinterpret_cast<const float4*>(a.workspace + ws.parts);
-    for (int f = blockIdx.x; f < tasks; f += gridDim.x) {
-        int p = 0, behind = pairs;  // the last item whose first task is at or before f
-        while (behind - p > 1) {
-            const int mid = (p + behind) / 2;
-            if (begins[mid] <= f) p = mid;
-            else behind = mid;
-        }
+    // part k of pair p's item: the pair's second slot, then the first slots of the pairs behind
+    const auto slot = [](int p, int k) -> int64_t {
+        return 2 * static_cast<int64_t>(p + k) + (k == 0 ? 1 : 0);
+    };
+    const int warp_tasks = few.begins[pairs], block_tasks = many.begins[pairs];
+    for (int f = blockIdx.x * kJoinWarps + warp; f < warp_tasks; f += gridDim.x * kJoinWarps) {
+        const int p = few.pair_of(f, pairs);
         const TreeItem it = items[p];
-        const int task = f - begins[p];
-        const int row_groups = (it.rows + 31) / 32;
-        const int row = task % row_groups * 32 + lane;
-        // part k of the item: the pair's second slot, then the first slots of the pairs behind
-        const auto slot = [&](int k) -> int64_t {
-            return 2 * static_cast<int64_t>(p + k) + (k == 0 ? 1 : 0);
-        };
-        if (it.parts <= kFewParts) {
-            const int cg = task / row_groups * kJoinWarps + warp;
-            if (row >= it.rows || cg >= R / 16) continue;
-            float4 v[kFewParts][4];
-            float2 s[kFewParts];
+        const int task = f - few.begins[p], cg = task % (R / 16), row = task / (R / 16) * 32 + lane;
+        if (row >= it.rows) continue;
+        float top = -INFINITY, total = 0.0f;
+        float o[16] = {};
+        for (int k0 = 0; k0 < it.parts; k0 += kAtATime) {
+            float4 v[kAtATime][4];
+            float2 s[kAtATime];
+            float m = top;
 #pragma unroll
-            for (int k = 0; k < kFewParts; ++k) {
+            for (int k = 0; k < kAtATime; ++k) {
                 s[k] = make_float2(-INFINITY, 0.0f);
-                if (k >= it.parts) continue;
-                s[k] = __ldcg(stats + slot(k) * ws.rows + row);
-                const float4* from = parts + (slot(k) * (R / 4) + cg * 4) * ws.rows + row;
+                if (k0 + k >= it.parts) continue;
+                s[k] = __ldcg(stats + slot(p, k0 + k) * ws.rows + row);
+                const float4* from = parts + (slot(p, k0 + k) * (R / 4) + cg * 4) * ws.rows + row;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[k][i] = __ldcg(from + static_cast<int64_t>(i) * ws.rows);
             }
-            float top = -INFINITY, total = 0.0f;
-            float o[16] = {};
 #pragma unroll
-            for (int k = 0; k < kFewParts; ++k) top = fmaxf(top, s[k].x);
+            for (int k = 0; k < kAtATime; ++k) m = fmaxf(m, s[k].x);
+            const float back = top == -INFINITY ? 0.0f : exp2f(top - m);
+            top = m;
+            total *= back;
 #pragma unroll
-            for (int k = 0; k < kFewParts; ++k) {
-                if (k >= it.parts) continue;
+            for (int i = 0; i < 16; ++i) o[i] *= back;
+#pragma unroll
+            for (int k = 0; k < kAtATime; ++k) {
+                if (k0 + k >= it.parts) continue;
                 const float w = s[k].x == -INFINITY ? 0.0f : exp2f(s[k].x - top);
                 total = fmaf(s[k].y, w, total);
 #pragma unroll
@@ -1314,27 +1329,35 @@ __global__ void __launch_bounds__(kJoinThreads, 3)
                     o[4 * i + 3] = fmaf(v[k][i].w, w, o[4 * i + 3]);
                 }
             }
-            const float inv = total != 0.0f ? 1.0f / total : 0.0f;
-            uint16_t* out = a.out + (it.first + row) * R + cg * 16;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                st_v4(out + 8 * i, make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                              pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                              pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                              pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv)));
-            if (a.lse != nullptr && cg == 0)
-                a.lse[it.first + row] = total != 0.0f ? top * kLn2 + logf(total) : -INFINITY;
-            continue;
         }
-        const int cg = task / row_groups;
+        const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+        uint16_t* out = a.out + (it.first + row) * R + cg * 16;
+        uint32_t x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+        if (sectors) {
+            st_v8(out, x);
+        } else {
+            st_v4(out, make_uint4(x[0], x[1], x[2], x[3]));
+            st_v4(out + 8, make_uint4(x[4], x[5], x[6], x[7]));
+        }
+        if (a.lse != nullptr && cg == 0)
+            a.lse[it.first + row] = total != 0.0f ? top * kLn2 + logf(total) : -INFINITY;
+    }
+    for (int f = blockIdx.x; f < block_tasks; f += gridDim.x) {
+        const int p = many.pair_of(f, pairs);
+        const TreeItem it = items[p];
+        const int task = f - many.begins[p];
+        const int row_groups = (it.rows + 31) / 32;
+        const int row = task % row_groups * 32 + lane, cg = task / row_groups;
         const bool live = row < it.rows;
         float top = -INFINITY, total = 0.0f;
         float o[32] = {};
         if (live)
 #pragma unroll 2
             for (int k = warp; k < it.parts; k += kJoinWarps) {
-                const float4* from = parts + (slot(k) * (R / 4) + cg * 8) * ws.rows + row;
-                const float2 s = __ldcg(stats + slot(k) * ws.rows + row);
+                const float4* from = parts + (slot(p, k) * (R / 4) + cg * 8) * ws.rows + row;
+                const float2 s = __ldcg(stats + slot(p, k) * ws.rows + row);
                 float4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = __ldcg(from + static_cast<int64_t>(i) * ws.rows);
@@ -1417,7 +1440,7 @@ cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm
         : boxes.key_slots >= 8 ? launch_source<kTma>(tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes, pairs, stream)
                    : launch_source<kRows>(tm_q, tm_k0, tm_k1, tm_v, args, ws, boxes, pairs, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(tree_join_kernel, static_cast<unsigned>(num_sms) * 4, kJoinThreads, 0,
+    return launch_dependent(tree_join_kernel, static_cast<unsigned>(num_sms) * kJoinBlocks, kJoinThreads, 0,
                             stream, args, ws, pairs);
 }
 
