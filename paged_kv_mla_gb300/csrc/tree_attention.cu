@@ -1214,8 +1214,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
-constexpr int kJoinBlocks = 3;  // resident on an SM; more would wait for the first to end
-constexpr int kFewParts = 8, kAtATime = 2;  // parts that a warp joins alone, and its loads in flight
+// Blocks of an SM, all of them resident when the attention ends: with three the registers for a
+// row's columns spilled (one user 14.2 us instead of 13.2), with four more had to wait for the first.
+constexpr int kJoinBlocks = 2;
+constexpr int kFewParts = 8;  // that a warp joins alone (4 and 16: the same)
 
 // Where the items of the pairs begin among the tasks of one kind, and the item of a task.
 struct JoinTasks {
@@ -1236,10 +1238,10 @@ struct JoinTasks {
 // Joins the parts of the items that several pairs share: with M the largest of the parts'
 // maxima, out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same order.
 // A lane has a row and 16 (few parts) or 32 of its columns.  Few parts, as of a batch whose
-// items are cut a few times, are one warp's task each, two parts' loads in flight at once; many
-// parts, as of few long histories, are dealt to the warps of a block, which meet in shared
-// memory and then each finish a share of the columns.  Bound by latency: some 10 to 40 MB of sums
-// come from L2, and all blocks are resident when the attention ends.
+// items are cut a few times, are one warp's task each; many parts, as of few long histories,
+// are dealt to the warps of a block, which meet in shared memory and then each finish a share
+// of the columns.  Bound by latency: 5 to 9 us behind the attention's end for 10 to 40 MB of sums
+// out of L2, 1 of them to start and 1 to find the tasks.
 __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
     tree_join_kernel(const TreeAttentionArgs a, const TreeWorkspace ws, const int pairs) {
     __shared__ TreeItem items[kTreeMaxPairs];
@@ -1296,38 +1298,23 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
         if (row >= it.rows) continue;
         float top = -INFINITY, total = 0.0f;
         float o[16] = {};
-        for (int k0 = 0; k0 < it.parts; k0 += kAtATime) {
-            float4 v[kAtATime][4];
-            float2 s[kAtATime];
-            float m = top;
+        for (int k = 0; k < it.parts; ++k) {
+            const float2 s = __ldcg(stats + slot(p, k) * ws.rows + row);
+            const float4* from = parts + (slot(p, k) * (R / 4) + cg * 4) * ws.rows + row;
+            float4 v[4];
 #pragma unroll
-            for (int k = 0; k < kAtATime; ++k) {
-                s[k] = make_float2(-INFINITY, 0.0f);
-                if (k0 + k >= it.parts) continue;
-                s[k] = __ldcg(stats + slot(p, k0 + k) * ws.rows + row);
-                const float4* from = parts + (slot(p, k0 + k) * (R / 4) + cg * 4) * ws.rows + row;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[k][i] = __ldcg(from + static_cast<int64_t>(i) * ws.rows);
-            }
-#pragma unroll
-            for (int k = 0; k < kAtATime; ++k) m = fmaxf(m, s[k].x);
-            const float back = top == -INFINITY ? 0.0f : exp2f(top - m);
+            for (int i = 0; i < 4; ++i) v[i] = __ldcg(from + static_cast<int64_t>(i) * ws.rows);
+            const float m = fmaxf(top, s.x);
+            const float f0 = top == -INFINITY ? 0.0f : exp2f(top - m);
+            const float f1 = s.x == -INFINITY ? 0.0f : exp2f(s.x - m);
             top = m;
-            total *= back;
+            total = total * f0 + s.y * f1;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= back;
-#pragma unroll
-            for (int k = 0; k < kAtATime; ++k) {
-                if (k0 + k >= it.parts) continue;
-                const float w = s[k].x == -INFINITY ? 0.0f : exp2f(s[k].x - top);
-                total = fmaf(s[k].y, w, total);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o[4 * i] = fmaf(v[k][i].x, w, o[4 * i]);
-                    o[4 * i + 1] = fmaf(v[k][i].y, w, o[4 * i + 1]);
-                    o[4 * i + 2] = fmaf(v[k][i].z, w, o[4 * i + 2]);
-                    o[4 * i + 3] = fmaf(v[k][i].w, w, o[4 * i + 3]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                o[4 * i] = o[4 * i] * f0 + v[i].x * f1;
+                o[4 * i + 1] = o[4 * i + 1] * f0 + v[i].y * f1;
+                o[4 * i + 2] = o[4 * i + 2] * f0 + v[i].z * f1;
+                o[4 * i + 3] = o[4 * i + 3] * f0 + v[i].w * f1;
             }
         }
         const float inv = total != 0.0f ? 1.0f / total : 0.0f;
