@@ -12,6 +12,10 @@
 // in one layer and makes all of the request's moves for them, so no two threads depend on
 // each other and no barrier is needed; it loads kGroup rows before it stores the first,
 // which the same argument allows, so that their latencies overlap.
+//
+// Bound by latency: a launch, then lengths and list, page ids, rows, one after the other.
+// Measured: 128 requests x 8 rows of 1152 bytes x 16 layers 8.2 us (17 MB: 2.1 TB/s), 10.2 us
+// while the offsets were found twice; one request 6 to 7 us.
 #include "pkm_device.cuh"
 #include "pkm_internal.h"
 

@@ -23,15 +23,27 @@
 // it did not start.  Such parts leave unnormalised fp32 sums, maxima and totals in the
 // workspace and a second kernel joins them; whole items are written directly.
 //
-// Roles of a CTA (16 warps): 0-3 softmax and epilogue, 4 MMA issue (even CTA), 5 queries,
-// 8-11 keys, 12-15 values; the softmax warps take over registers of warps 4-7.  Scores are kept in base 2; the running maximum moves only when
-// a row's new maximum exceeds it by 2^8, since any reference works as long as nothing
-// overflows, so the accumulator is hardly ever rescaled.
+// Roles of a CTA: warps 0-7 softmax and epilogue, 8 MMA issue (even CTA), 9 queries, 10 asks for
+// keys to be brought into L2 ahead of their loads, 12-15 keys, 16-19 values (by loads 12-19 both).
+// Scores are kept in base 2; the running maximum moves only when a row's new maximum exceeds
+// it by 2^8, since any reference works as long as nothing overflows, so the accumulator is
+// hardly ever rescaled.
 //
 // What threads write for the MMAs (weights, rows brought by loads) each CTA's tensor core
 // reads from its own shared memory.  The writer's fence.proxy.async completes before its
 // arrival at the even CTA's barrier, so an arrival of default scope is enough; one with
 // cluster-scope release took 1430 cycles of every tile.
+//
+// Measured (R = 512, P = 64, 128 heads, L2 cold; floor = bytes or operations at the rates of a
+// plain copy and a large library product):
+//   16 trees of 16-64 tokens, histories of 512-4096: 327 us, 1.30 PFLOP/s (0.68).  A tile takes
+//     2600-2700 cycles, of which its MMAs 2176; each CTA's 136 KB a tile are then 50 bytes a cycle
+//     out of L2, which bounds it.  An item's start and end take 5 us more.
+//   64 users x 1 token, histories of 512-4096, pages of 128: 61 us, floor 28 us (3.0 TB/s).  1.5
+//     items a pair: 10 us to start, 20 us of items' starts and ends, 8 us to join.
+//   4 users x 1 token, histories of 32768: 49 us, floor 23 us (3.1 TB/s), likewise.
+//   32 chains of 1-4 tokens over the quantised cache: 109 us, floor 26 us.  Rows brought by loads
+//     are bound by the instructions that convert them: 3 us a tile.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -425,9 +437,10 @@ __device__ __forceinline__ void gave_up(const WaitCtl& wc) {
 // is, finds its page and loads its scale.  When a set is stored the next one is asked for.
 //
 // One copy of the code serves all warps and both sets, with few branches: the warps wait for
-// instructions more than for loads.  A form in which four warps brought all keys and four all
-// values converted 1.9 times as much (182 us instead of 134 for chains over the quantised cache);
-// with a scale of its own for every piece and 64 columns of a row at a time it took 134 us.
+// instructions more than for loads.  For 32 chains over the quantised cache (now 109 us) a form in
+// which four warps brought all keys and four all values, which converts 1.9 times as much, took
+// 182 us; with a scale of its own for every piece and 64 columns of a row at a time 134 instead of
+// 119; sixteen warps, or a second set of registers for the rows on their way, changed nothing.
 template <Source SRC, typename Queries>
 __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars, uint8_t* smem,
                                          uint32_t rank, int i, int kblocks, int vgroups,
