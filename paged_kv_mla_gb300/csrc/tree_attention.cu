@@ -42,7 +42,7 @@
 //   64 users x 1 token, histories of 512-4096, pages of 128: 61 us, floor 28 us (3.0 TB/s).  1.5
 //     items a pair: 10 us to start, 20 us of items' starts and ends, 8 us to join.
 //   4 users x 1 token, histories of 32768: 49 us, floor 23 us (3.1 TB/s), likewise.
-//   32 chains of 1-4 tokens over the quantised cache: 109 us, floor 26 us.  Rows brought by loads
+//   32 chains of 1-4 tokens over the quantised cache: 107 us, floor 26 us.  Rows brought by loads
 //     are bound by the instructions that convert them: 3 us a tile.
 #include <cuda_fp16.h>
 
@@ -244,6 +244,17 @@ __device__ __forceinline__ void plan(const TreeAttentionArgs& a, Bars* bars, int
         }
 }
 
+// Asks for the arrays that the first loads depend on one after the other (offsets, lengths, page
+// table) to be brought into L2, all at once and before they may be read: with the queries' later
+// blocks (see fetch) 0.5 to 2 us of a call with cold inputs.
+__device__ __forceinline__ void prefetch_tables(const TreeAttentionArgs& a) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t line = t * 32;  // 32-bit entries
+    if (line <= a.batch) prefetch_l2(a.row_offsets + line);
+    if (line < a.batch) prefetch_l2(a.cache_lengths + line);
+    if (line < static_cast<int64_t>(a.batch) * a.max_pages) prefetch_l2(a.page_table + line);
+}
+
 // Page and slot of position pos of request b; page -1 (loads as zeros) at or past kv and for
 // ids that the cache does not have, which are reported.
 struct Place {
@@ -437,7 +448,7 @@ __device__ __forceinline__ void gave_up(const WaitCtl& wc) {
 // is, finds its page and loads its scale.  When a set is stored the next one is asked for.
 //
 // One copy of the code serves all warps and both sets, with few branches: the warps wait for
-// instructions more than for loads.  For 32 chains over the quantised cache (now 109 us) a form in
+// instructions more than for loads.  For 32 chains over the quantised cache (now 107 us) a form in
 // which four warps brought all keys and four all values, which converts 1.9 times as much, took
 // 182 us; with a scale of its own for every piece and 64 columns of a row at a time 134 instead of
 // 119; sixteen warps, or a second set of registers for the rows on their way, changed nothing.
@@ -665,7 +676,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     cluster_arrive();  // the barriers are set up; the peer may signal them behind cluster_wait
-    griddep_wait();    // launched while the work before it may still run; reads nothing before
+    prefetch_tables(a);
+    griddep_wait();  // launched while the work before may still run: nothing is read before
     plan(a, bars, reinterpret_cast<int64_t*>(s_max), pair, pairs);
     griddep_launch_dependents();
     tc_fence_before();
@@ -1072,6 +1084,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 8 * kAtOnce; ++k) {
                 const int c = kb * 64 + k * 8;
                 const uint4 v = ld_nc_v4_if(q + c, have && c < a.cols);
+                // the later blocks, fetched only when these have been put away
+                if (kb == 0 && (k & 7) == 0 && have && c + 64 * kAtOnce < a.cols)
+                    prefetch_l2(q + c + 64 * kAtOnce);
                 x[k >> 3][4 * (k & 7)] = v.x;
                 x[k >> 3][4 * (k & 7) + 1] = v.y;
                 x[k >> 3][4 * (k & 7) + 2] = v.z;
