@@ -699,8 +699,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------- softmax and epilogue: row = lane of the CTA's 64 ----------------
         // Warps w and w + 4 share 32 lanes; lanes 0-63 have the first 64 keys (and half of O's
         // columns), and each of the two warps takes 32 of the keys (half of the lanes' columns).
-        // With one warp for both a tile of 25 took 2560 cycles, 380 more than its MMAs, and the
-        // end of an item half as long again.
+        // With one warp for both large drafted trees took 345 us instead of 332.
         if constexpr (SRC == kTma) warpgroup_reg_alloc<kMoreRegs>();
         Walk w(bars);
         const int half = warp >> 1 & 1, part = warp >> 2;
