@@ -42,7 +42,7 @@
 //   64 users x 1 token, histories of 512-4096, pages of 128: 61 us, floor 28 us (3.0 TB/s).  1.5
 //     items a pair: 10 us to start, 20 us of items' starts and ends, 8 us to join.
 //   4 users x 1 token, histories of 32768: 49 us, floor 23 us (3.1 TB/s), likewise.
-//   32 chains of 1-4 tokens over the quantised cache: 107 us, floor 26 us.  Rows brought by loads
+//   32 chains of 1-4 tokens over the quantised cache: 105 us, floor 26 us.  Rows brought by loads
 //     are bound by the instructions that convert them: 3 us a tile.
 #include <cuda_fp16.h>
 
@@ -64,9 +64,9 @@ constexpr int kThreads = 20 * 32;
 // the 5 x 96 that the block starts with: by loads the rows on their way need more.
 constexpr int kIssueRegs = 64, kMoreRegs = 112;
 // An item's start and end, in tiles: 5 us against 1.4 us of a tile by TMA and 3 us of one by loads
-// (2 for both took large drafted trees from 331 to 342 us, 4 for both chains over the quantised
-// cache from 114 to 118 us).
-constexpr int item_cost(Source src) { return src == kTma ? 4 : 2; }
+// (large drafted trees with 2: 342 instead of 331 us, ragged ones with 6: 36.7 instead of 34.7; chains
+// over the quantised cache with 2: 107.6 instead of 104.9, with 3: 109.5).
+constexpr int item_cost(Source src) { return src == kTma ? 4 : 1; }
 constexpr int kKeys = 128;          // keys of a tile (64 loaded by each CTA as keys)
 constexpr int kBlocks = 9;          // 64-column blocks of a latent row
 constexpr int kBlockBytes = 64 * 128;
@@ -448,7 +448,7 @@ __device__ __forceinline__ void gave_up(const WaitCtl& wc) {
 // is, finds its page and loads its scale.  When a set is stored the next one is asked for.
 //
 // One copy of the code serves all warps and both sets, with few branches: the warps wait for
-// instructions more than for loads.  For 32 chains over the quantised cache (now 107 us) a form in
+// instructions more than for loads.  For 32 chains over the quantised cache (now 105 us) a form in
 // which four warps brought all keys and four all values, which converts 1.9 times as much, took
 // 182 us; with a scale of its own for every piece and 64 columns of a row at a time 134 instead of
 // 119; sixteen warps, or a second set of registers for the rows on their way, changed nothing.
