@@ -36,12 +36,12 @@
 //
 // Measured (R = 512, P = 64, 128 heads, L2 cold; floor = bytes or operations at the rates of a
 // plain copy and a large library product):
-//   16 trees of 16-64 tokens, histories of 512-4096: 327 us, 1.30 PFLOP/s (0.68).  A tile takes
-//     2600-2700 cycles, of which its MMAs 2176; each CTA's 136 KB a tile are then 50 bytes a cycle
+//   16 trees of 16-64 tokens, histories of 512-4096: 318 us, 1.34 PFLOP/s (0.70).  A tile takes
+//     2600 cycles, of which its MMAs 2176; each CTA's 136 KB a tile are then 50 bytes a cycle
 //     out of L2, which bounds it.  An item's start and end take 5 us more.
-//   64 users x 1 token, histories of 512-4096, pages of 128: 61 us, floor 28 us (3.0 TB/s).  1.5
-//     items a pair: 10 us to start, 20 us of items' starts and ends, 8 us to join.
-//   4 users x 1 token, histories of 32768: 49 us, floor 23 us (3.1 TB/s), likewise.
+//   64 users x 1 token, histories of 512-4096, pages of 128: 55.5 us, floor 28 us (3.3 TB/s).  1.5
+//     items a pair: 10 us to start, 15 us of items' starts and ends, 8 us to join.
+//   4 users x 1 token, histories of 32768: 44.6 us, floor 23 us (3.4 TB/s), likewise.
 //   32 chains of 1-4 tokens over the quantised cache: 105 us, floor 26 us.  Rows brought by loads
 //     are bound by the instructions that convert them: 3 us a tile.
 #include <cuda_fp16.h>
@@ -1014,15 +1014,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_wait_inl(&bars->mma_done, 0, wc, false);
         }
       } else if (warp == kFetchWarp) {
-        // Asks for the keys of the tile after the next to be brought into L2: the loads
-        // proper are issued when their shared memory is free, too late to wait for DRAM.
+        // Asks for keys to be brought into L2 ahead of their loads, which are issued when their
+        // shared memory is free, too late to wait for DRAM: for wide boxes as soon as the keys of
+        // the tile before are asked for, for other loads, which take longer, two tiles earlier.
+        // (64 users x 1 token, wide boxes: 55.8 us, two tiles earlier 60.4, never 59.0; ragged trees
+        // in small pages 36.0, 34.9, 37.7; chains over the quantised cache 113 and 105.)  With wide
+        // boxes a request's first item alone asks: large drafted trees 315 instead of 323 us.
+        const int ahead = SRC == kTma && tb.key_blocks > 1 ? 0 : 2;
         Walk w(bars);
         volatile int32_t* progress = &bars->progress;
         const int bytes = SRC >= kCodes ? R + 2 * (a.cols - R) + 4 * (R / 128) : 2 * a.cols;
         int g = 0;
         while (w.next(a))
             for (int32_t kt = w.kt1 - 1; kt >= w.kt0; --kt, ++g) {
-                for (uint32_t n = 0; g - 2 > *progress && n < tries; ++n) __nanosleep(500);
+                for (uint32_t n = 0; g - ahead > *progress && n < tries; ++n) __nanosleep(500);
+                if (ahead == 0 && w.item > 0) continue;
                 for (int x = 0; x < 2; ++x) {
                     const int64_t pos = static_cast<int64_t>(kt) * kKeys + rank * 64 + x * 32 + lane;
                     const int64_t row = Place(a, w.b, pos, w.r.kv).offset(a);
