@@ -1027,7 +1027,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int g = 0;
         while (w.next(a))
             for (int32_t kt = w.kt1 - 1; kt >= w.kt0; --kt, ++g) {
-                for (uint32_t n = 0; g - ahead > *progress && n < tries; ++n) __nanosleep(500);
+                for (uint32_t n = 0; g - ahead > *progress && n < tries; ++n) __nanosleep(100);
                 if (ahead == 0 && w.item > 0) continue;
                 for (int x = 0; x < 2; ++x) {
                     const int64_t pos = static_cast<int64_t>(kt) * kKeys + rank * 64 + x * 32 + lane;
