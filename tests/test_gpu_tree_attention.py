@@ -374,3 +374,18 @@ def test_refuses_views_and_host_memory():
     assert call(tree_mask=g.mask.long()) == 1
     assert call(lse=g.lse.double()) == 1
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("page,quantised", [(12, False), (16, True), (64, False)])
+def test_out_of_range_tokens_by_every_source(page, quantised):
+    """Page ids that the cache does not have and a history past the table's row, by loads, from
+    quantised rows and by wide boxes: reported, and the other requests' rows as they would be."""
+    p = make_tree(655, [100, 300, 40], [1, 2, 2], 4, 512, 64, page=page, quantised=quantised)
+    ref = p.reference()
+    p.table[0, 0] = 0x40000000
+    g = DeviceTree(p)
+    g.lengths[2] = 100000
+    g.run()
+    out, lse, status = g.results()
+    assert status == 4
+    assert (np.abs(bf16_value(out[1:3]) - ref[0][1:3]) <= ref[1][1:3]).all()
