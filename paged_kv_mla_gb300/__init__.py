@@ -31,6 +31,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -195,19 +196,33 @@ def _stream(stream) -> Optional[int]:
 
 class _Descriptor:
     """Keeps the C struct of a cache descriptor from call to call, as long as no field is
-    assigned; the tensors' addresses and the table's width are read anew for every call."""
+    assigned; the tensors' addresses and the table's width are read anew for every call.
+
+    Every assignment is followed by a new mark, and a struct is kept together with the mark that
+    was there before its fields were read: one that was built beside an assignment in another
+    thread is not used again.  Each thread keeps its own, so that no other one changes a struct
+    while a call reads it."""
 
     def __setattr__(self, name, value):
-        self.__dict__.pop("_c", None)
         self.__dict__[name] = value
+        self.__dict__["_mark"] = object()
 
     def __getstate__(self):  # copies and pickles make their own
-        return {k: v for k, v in self.__dict__.items() if k != "_c"}
+        return {k: v for k, v in self.__dict__.items() if k not in ("_mark", "_kept")}
 
     def c_struct(self):
-        c = self.__dict__.get("_c")
-        if c is None:
-            c = self.__dict__["_c"] = self._new_struct()
+        d = self.__dict__
+        kept = d.get("_kept")
+        if kept is None:
+            kept = d.setdefault("_kept", threading.local())
+        mark = d.get("_mark")
+        try:
+            c, made = kept.struct
+        except AttributeError:
+            c = made = None
+        if c is None or made is not mark:
+            c = self._new_struct()
+            kept.struct = c, mark
         else:
             table = self.page_table
             c.data = self.data.data_ptr()
@@ -238,10 +253,11 @@ class PagedCache(_Descriptor):
     cache_lengths: Optional[torch.Tensor] = None
 
     def _new_struct(self) -> _CCache:
+        table = self.page_table  # once: another thread may assign it
         return _CCache(self.data.data_ptr(), int(self.layer_stride), int(self.page_stride),
                        int(self.slot_stride), int(self.kv_stride), int(self.num_layers),
                        int(self.num_pages), int(self.page_size), int(self.row_elems),
-                       self.page_table.data_ptr(), int(self.page_table.shape[-1]),
+                       table.data_ptr(), int(table.shape[-1]),
                        _ptr(self.cache_lengths))
 
 
@@ -265,10 +281,11 @@ class QuantCache(_Descriptor):
     cache_lengths: Optional[torch.Tensor] = None
 
     def _new_struct(self) -> _CQuantCache:
+        table = self.page_table  # once: another thread may assign it
         return _CQuantCache(self.data.data_ptr(), int(self.layer_stride), int(self.page_stride),
                             int(self.slot_stride), int(self.num_layers), int(self.num_pages),
                             int(self.page_size), int(self.kv_lora_rank), int(self.rope_dim),
-                            self.page_table.data_ptr(), int(self.page_table.shape[-1]),
+                            table.data_ptr(), int(table.shape[-1]),
                             _ptr(self.cache_lengths))
 
 
