@@ -147,7 +147,8 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
 // (TMA complete_tx, tcgen05.commit) or by arrivals that only hand over tensor-memory
 // accumulators ordered with tcgen05 fences, including arrivals from the other CTA of a pair.
 // A satisfied wait then costs a few tens of cycles, against several hundred for the
-// cluster-scope acquire of mbar_wait_cluster.
+// cluster-scope acquire of mbar_wait_cluster.  Shared memory that threads of the other CTA
+// wrote needs mbar_wait_cluster, or fence_acquire_cluster_smem behind mbar_try_wait_relaxed.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w,
                                           bool obey_abort = true) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -198,9 +199,39 @@ __device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t cluster_addr, ui
 // Arrive on an mbarrier of either CTA of the cluster (shared::cluster address) with the
 // default release-at-CTA semantics.  Used for hand-offs whose data is ordered by tcgen05
 // fences (a TMEM accumulator drained by the epilogue), where a cluster-scope release would
-// only add latency.
+// only add latency.  It publishes no shared memory to the other CTA: see mbar_arrive_publish.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Arrive on an mbarrier of either CTA of the cluster and publish to the cluster what this
+// thread, and threads that it has met, wrote to their CTA's shared memory: a release fence
+// at cluster scope for that memory alone, then a relaxed arrival.  mbar_arrive_cluster
+// releases global memory too and waits for it.  For an MMA of the pair to read it, each
+// writer's fence_proxy_async_smem comes before.
+__device__ __forceinline__ void mbar_arrive_publish(uint32_t cluster_addr) {
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+        : "memory");
+}
+
+// One try at cluster scope that orders nothing; behind one that succeeds,
+// fence_acquire_cluster_smem makes what mbar_arrive_publish published visible.
+__device__ __forceinline__ bool mbar_try_wait_relaxed(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void fence_acquire_cluster_smem() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {

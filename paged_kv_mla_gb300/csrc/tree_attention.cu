@@ -29,10 +29,12 @@
 // it by 2^8, since any reference works as long as nothing overflows, so the accumulator is
 // hardly ever rescaled.
 //
-// What threads write for the MMAs (weights, rows brought by loads) each CTA's tensor core
-// reads from its own shared memory.  The writer's fence.proxy.async completes before its
-// arrival at the even CTA's barrier, so an arrival of default scope is enough; one with
-// cluster-scope release took 1430 cycles of every tile.
+// What threads write for the MMAs (weights, rows brought by loads, values looked through) each
+// CTA's tensor core reads from its own shared memory, on behalf of the even CTA's issuing warp.
+// A writer's fence.proxy.async comes first; its arrival at the even CTA's barrier then publishes
+// shared memory at cluster scope, and the issuer's waits for such arrivals acquire it.  Both are
+// fences for shared memory alone: a cluster-scope release of all memory took 1430 cycles of
+// every tile.
 //
 // Measured (R = 512, P = 64, 128 heads, L2 cold; floor = bytes or operations at the rates of a
 // plain copy and a large library product):
@@ -431,6 +433,15 @@ __device__ __forceinline__ bool plain_wait(uint64_t* bar, uint32_t parity, uint3
     return n < tries;
 }
 
+// The same for phases that writes of the other CTA's threads stand behind.
+__device__ __forceinline__ bool plain_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t tries) {
+    uint32_t n = 0;
+    for (; n < tries && !mbar_try_wait_relaxed(bar, parity); ++n) {
+    }
+    fence_acquire_cluster_smem();
+    return n < tries;
+}
+
 // Records a wait that ran out and ends the CTA's other waits.
 __device__ __forceinline__ void gave_up(const WaitCtl& wc) {
     report(wc.status, PKM_ERR_TIMEOUT);
@@ -596,7 +607,7 @@ __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars,
             load(next);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(k_full + set * 8);
+            if (lane == 0) mbar_arrive_publish(k_full + set * 8);
             if (set < vgroups) ring.next(kValueRing);
             if (t + set == 0) ok = queries(w);
             if (!ok) break;
@@ -810,7 +821,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(p_full);
+                if (lane == 0) mbar_arrive_publish(p_full);
             }
             if (!ok) break;
             if (!warp_wait(&bars->o_full, (g - 1) & 1, wc)) {
@@ -910,6 +921,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
                 failed |= !plain_wait(bar, parity, tries);
             };
+            const auto wait_cluster = [&](uint64_t* bar, uint32_t parity) {
+                failed |= !plain_wait_cluster(bar, parity, tries);
+            };
+            const auto keys_wait = [&](uint64_t* bar, uint32_t parity) {
+                if constexpr (SRC == kTma) wait(bar, parity);
+                else wait_cluster(bar, parity);
+            };
             const uint32_t id_s = idesc_bf16(128, kKeys, false, false);
             const uint32_t id_o = idesc_bf16(128, 256, false, true);
             const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
@@ -922,7 +940,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // O (+)= P V of a tile; `first`: of its item
             const auto values = [&](uint32_t tile, bool first) {
                 const uint32_t ph = tile & 1;
-                wait(&bars->p_full, ph);
+                wait_cluster(&bars->p_full, ph);
                 if (first && item > 1) wait(&bars->o_empty, item & 1);
                 tc_fence_after();
                 const uint32_t keep = first ? 0u : 1u;
@@ -930,10 +948,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int vg = 0; vg < vgroups; ++vg) {
                     const uint32_t v = vring.stage;
                     if (SRC == kTma) {  // by loads they are there with the tile's keys
-                        wait(&bars->v_full[v], vring.phase);
+                        wait_cluster(&bars->v_full[v], vring.phase);
                         tc_fence_after();
                     }
-                                        const uint64_t vd = desc_add_bytes(v_desc, v * 2 * kValueBytes);
+                    const uint64_t vd = desc_add_bytes(v_desc, v * 2 * kValueBytes);
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {  // 64 keys: one block of P
                         const uint64_t pd = desc_add_bytes(p_desc, h * kBlockBytes);
@@ -959,7 +977,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         values(g - 1, first);
                         first = false;
                     }
-                    wait(&bars->k_full[0], g & 1);
+                    keys_wait(&bars->k_full[0], g & 1);
                     tc_fence_after();
                     const int first_blocks = min(kblocks, kQueryBlocks);
 #pragma unroll 1
@@ -973,7 +991,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     mma_commit_pair_elect(&bars->k_empty[0], 3);
                     if (kblocks > kQueryBlocks) {
-                        wait(&bars->k_full[1], g & 1);
+                        keys_wait(&bars->k_full[1], g & 1);
                         tc_fence_after();
 #pragma unroll 1
                         for (int kb = kQueryBlocks; kb < kblocks; ++kb) {
@@ -1228,7 +1246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive_remote(v_full + s * 8);
+                            if (lane == 0) mbar_arrive_publish(v_full + s * 8);
                         }
                         for (int v = 0; v < vgroups; ++v) {
                             if (t < behind) own_phase ^= 1u << ring.stage;
