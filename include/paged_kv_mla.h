@@ -650,12 +650,13 @@ pkm_status kv_matmul_paged_fp8(const void* hidden_state, const uint32_t* input_r
                                void* stream);
 
 /*
- * Failure-detection self check (no counterpart on the pages).  Launches one CTA that waits,
- * with the same bounded mbarrier wait every kernel above uses, on a barrier phase that
- * nothing completes.  After timeout_ms (1..5000) the wait gives up and PKM_ERR_TIMEOUT is
- * merged into *dev_status (device int32, required); the kernel then returns normally and
- * the CUDA context stays usable.  Returns PKM_ERR_INVALID_ARG for a NULL status or a limit
- * out of range.
+ * Failure-detection self check (no counterpart on the pages).  Launches one CTA whose warps
+ * wait, each in one of the forms of the bounded mbarrier wait that the kernels above use, on a
+ * barrier phase that nothing completes.  After timeout_ms (1..5000) the waits give up, and
+ * PKM_ERR_TIMEOUT is merged into *dev_status (device int32, required) when every one of them
+ * did, not earlier and at most half as long again and 5 ms later; the kernel then returns
+ * normally and the CUDA context stays usable.  Returns PKM_ERR_INVALID_ARG for a NULL status or
+ * a limit out of range.
  */
 pkm_status pkm_check_wait_timeout(int32_t* dev_status, uint32_t timeout_ms, void* stream);
 

@@ -266,6 +266,22 @@ static __device__ __noinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t pa
     }
 }
 
+// The wait of warps whose issue loops are fast only while the compiler sees that their lanes stay
+// together: a bare loop with one exit, which the abort flag ends.  Time is kept by the CTA's other
+// warps, whose waits by mbar_wait outlive their limit when this one's phase does not complete and
+// raise the flag; `tries` is a second limit, at 10 ns to 4 us each.  Returns false without the
+// phase.  CLUSTER: for phases that other CTAs' threads complete with mbar_arrive_publish; acquires
+// what they published.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait_flag(uint64_t* bar, uint32_t parity,
+                                               volatile int* abort_flag, uint32_t tries) {
+    bool done;
+    do done = CLUSTER ? mbar_try_wait_relaxed(bar, parity) : mbar_try_wait(bar, parity);
+    while (!done && --tries != 0 && *abort_flag == 0);
+    if (CLUSTER) fence_acquire_cluster_smem();
+    return done;
+}
+
 // All threads of every CTA in the cluster (release / acquire).
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"

@@ -422,32 +422,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, mbar_wait_inl(bar, parity, wc));
 }
 
-// The wait of the issuing warps: a bare loop, limited by its tries (one suspends the thread for
-// about 4 us when the phase is not complete), false when they run out.  Their issue loops are
-// fast only while the compiler sees that the warp stays together: with mbar_wait's exits in
-// the loop, the scores' MMAs took 50 cycles each instead of 30 and a tile 4350 instead of 2400.
-__device__ __forceinline__ bool plain_wait(uint64_t* bar, uint32_t parity, uint32_t tries) {
-    uint32_t n = 0;
-    for (; n < tries && !mbar_try_wait(bar, parity); ++n) {
-    }
-    return n < tries;
-}
-
-// The same for phases that writes of the other CTA's threads stand behind.
-__device__ __forceinline__ bool plain_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t tries) {
-    uint32_t n = 0;
-    for (; n < tries && !mbar_try_wait_relaxed(bar, parity); ++n) {
-    }
-    fence_acquire_cluster_smem();
-    return n < tries;
-}
-
-// Records a wait that ran out and ends the CTA's other waits.
-__device__ __forceinline__ void gave_up(const WaitCtl& wc) {
-    report(wc.status, PKM_ERR_TIMEOUT);
-    *wc.abort_flag = 1;
-}
-
 // Warp i of the eight that bring the rows of a CTA by loads, as keys and as values in one go: the
 // tile's columns come in two sets of four blocks (the ninth block with the second), and of each
 // set a warp brings
@@ -551,13 +525,11 @@ __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars,
         int set = 0;
 #pragma unroll 1
         while (t < tiles) {
-            ok = plain_wait(&bars->k_empty[set], (g & 1) ^ 1, tries);
-            if (set < vgroups) ok = ok && plain_wait(&bars->v_empty[ring.stage], ring.phase ^ 1, tries);
+            ok = mbar_wait_flag(&bars->k_empty[set], (g & 1) ^ 1, wc.abort_flag, tries);
+            if (set < vgroups)
+                ok = ok && mbar_wait_flag(&bars->v_empty[ring.stage], ring.phase ^ 1, wc.abort_flag, tries);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
-                gave_up(wc);
-                break;
-            }
+            if (!ok) break;
             const int next = set + 1 == sets ? 0 : set + 1;
             if (next == 0) rows(t + 1);
             float f[6];
@@ -697,14 +669,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     const WaitCtl wc{&bars->abort_flag, a.status, a.timeout_ns};
-    // between 10 ms and 4 s for the default limit of a second
-    const uint32_t tries = static_cast<uint32_t>(min(a.timeout_ns / 1000, uint64_t{1} << 30));
-    const int64_t sharing = min(pairs, bars->units);  // pairs with a share
+    // The softmax warps keep the time limit: whatever stalls stalls them.  The issuing and
+    // loading warps' waits end with their abort flag, or after tries that take longer.  (With
+    // mbar_wait's exits in the loop the scores' MMAs took 50 cycles each instead of 30.)
+    const uint32_t tries =
+        static_cast<uint32_t>(min(a.timeout_ns / 8, uint64_t{UINT32_MAX}));
     const auto issue_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool ok = __all_sync(0xffffffffu, plain_wait(bar, parity, tries));
-        if (!ok) gave_up(wc);
-        return ok;
+        return __all_sync(0xffffffffu, mbar_wait_flag(bar, parity, wc.abort_flag, tries));
     };
+    const int64_t sharing = min(pairs, bars->units);  // pairs with a share
 
     if (warp < kSoftWarps) {
         // ---------------- softmax and epilogue: row = lane of the CTA's 64 ----------------
@@ -919,10 +892,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // A wait that runs out is looked at once a tile; what is issued until then is not used.
             bool failed = false;
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                failed |= !plain_wait(bar, parity, tries);
+                failed |= !mbar_wait_flag(bar, parity, wc.abort_flag, tries);
             };
             const auto wait_cluster = [&](uint64_t* bar, uint32_t parity) {
-                failed |= !plain_wait_cluster(bar, parity, tries);
+                failed |= !mbar_wait_flag<true>(bar, parity, wc.abort_flag, tries);
             };
             const auto keys_wait = [&](uint64_t* bar, uint32_t parity) {
                 if constexpr (SRC == kTma) wait(bar, parity);
@@ -1016,10 +989,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     first = false;
                 }
                 if (!next_item && t == 1) first = true;
-                if (__any_sync(0xffffffffu, failed)) {
-                    gave_up(wc);
-                    break;
-                }
+                if (__any_sync(0xffffffffu, failed)) break;
                 if (next_item) {
                     if (!__any_sync(0xffffffffu, w.next(a))) break;
                     tiles = __shfl_sync(0xffffffffu, w.kt1 - w.kt0, 0);
@@ -1043,9 +1013,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         volatile int32_t* progress = &bars->progress;
         const int bytes = SRC >= kCodes ? R + 2 * (a.cols - R) + 4 * (R / 128) : 2 * a.cols;
         int g = 0;
-        while (w.next(a))
+        bool ok = true;
+        while (ok && w.next(a))
             for (int32_t kt = w.kt1 - 1; kt >= w.kt0; --kt, ++g) {
-                for (uint32_t n = 0; g - ahead > *progress && n < tries; ++n) __nanosleep(100);
+                // naps of 100 ns on average, as many as make the limit
+                for (uint64_t n = 0; ok && g - ahead > *progress; ++n) {
+                    ok = n < a.timeout_ns / 100 && !*wc.abort_flag;
+                    __nanosleep(100);
+                }
+                if (!ok) break;
                 if (ahead == 0 && w.item > 0) continue;
                 for (int x = 0; x < 2; ++x) {
                     const int64_t pos = static_cast<int64_t>(kt) * kKeys + rank * 64 + x * 32 + lane;
