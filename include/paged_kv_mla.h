@@ -650,6 +650,15 @@ pkm_status kv_matmul_paged_fp8(const void* hidden_state, const uint32_t* input_r
                                void* stream);
 
 /*
+ * Checks without a launch (no counterpart on the pages).  Until it is called with 0, calls of this
+ * thread to mla_tree_attention_paged, mla_rope_heads, mla_cache_write_paged,
+ * mla_cache_compact_paged and their variants make their host checks alone: what these find, or
+ * PKM_ERR_CUDA where the call would go on to the GPU.  For callers that know more of an argument
+ * than its address, a tensor in host memory say, and must not launch with it.
+ */
+void pkm_checks_only(int32_t on);
+
+/*
  * Failure-detection self check (no counterpart on the pages).  Launches one CTA whose warps
  * wait, each in one of the forms of the bounded mbarrier wait that the kernels above use, on a
  * barrier phase that nothing completes.  After timeout_ms (1..5000) the waits give up, and

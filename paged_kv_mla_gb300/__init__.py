@@ -152,6 +152,8 @@ _lib.mla_decompress_k_paged_fp8_noalloc.argtypes = [ctypes.POINTER(_CCache), _u3
                                                     _vp, _vp]
 _lib.mla_decompress_k_paged_fp8_noalloc.restype = ctypes.c_int
 FP8_NOALLOC_SCRATCH_BYTES = 16 << 20
+_lib.pkm_checks_only.argtypes = [_i32]
+_lib.pkm_checks_only.restype = None
 _lib.pkm_check_wait_timeout.argtypes = [_vp, _u32, _vp]
 _lib.pkm_check_wait_timeout.restype = ctypes.c_int
 _lib.pkm_validate_row_offsets.argtypes = [_vp, _i32, _vp, _vp]
@@ -436,14 +438,34 @@ _initialized = torch.cuda.is_initialized
 
 def _plain(itemsize: int, *tensors) -> bool:
     """Whether the tensors are what the C calls take them for, elements of that size without
-    gaps, and lie on the device that the call runs on (None and addresses pass)."""
-    device = torch._C._cuda_getDevice() if _initialized() else -1
+    gaps (None and addresses pass)."""
     for t in tensors:
         if t is None or t.__class__ is int:
             continue
-        if t.itemsize != itemsize or not t.is_contiguous() or t.get_device() != device:
+        if t.itemsize != itemsize or not t.is_contiguous():
             return False
     return True
+
+
+def _here(*tensors) -> bool:
+    """Whether the tensors lie on the device that the call runs on (None and addresses pass).
+    While CUDA is not initialised no tensor does."""
+    device = torch._C._cuda_getDevice() if _initialized() else None
+    for t in tensors:
+        if t is not None and t.__class__ is not int and t.get_device() != device:
+            return False
+    return True
+
+
+def _refuse(f, *args) -> int:
+    """The status of a call whose tensors are not _here: what its own checks find, if anything.
+    `args` end before the stream."""
+    _lib.pkm_checks_only(1)
+    try:
+        code = f(*args, None)
+    finally:
+        _lib.pkm_checks_only(0)
+    return PKM_ERR_INVALID_ARG if code == PKM_ERR_CUDA else code
 
 
 def _has(n: int, t) -> bool:
@@ -464,11 +486,13 @@ def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tens
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_at", check)
     c = cache.c_struct()
     batch = input_row_offsets.shape[0] - 1
-    code = _lib.mla_cache_write_paged_at(_ptr(latent), _ptr(input_row_offsets), _ptr(positions),
-                                         batch, rows, int(kv_lora_rank), int(rope_dim),
-                                         _ptr(kv_norm_gamma), float(epsilon), _ptr(freqs_cis),
-                                         freqs_cis.shape[0], ctypes.byref(c), int(layer_idx),
-                                         _ptr(dev_status), _stream(stream))
+    args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
+            int(kv_lora_rank), int(rope_dim), _ptr(kv_norm_gamma), float(epsilon),
+            _ptr(freqs_cis), freqs_cis.shape[0], ctypes.byref(c), int(layer_idx),
+            _ptr(dev_status))
+    f = _lib.mla_cache_write_paged_at
+    here = _here(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis)
+    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_cache_write_paged_at", check)
 
 
@@ -483,12 +507,12 @@ def mla_cache_write_paged_qcache_at(latent: torch.Tensor, input_row_offsets: tor
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_qcache_at", check)
     c = cache.c_struct()
     batch = input_row_offsets.shape[0] - 1
-    code = _lib.mla_cache_write_paged_qcache_at(_ptr(latent), _ptr(input_row_offsets),
-                                                _ptr(positions), batch, rows,
-                                                _ptr(kv_norm_gamma), float(epsilon),
-                                                _ptr(freqs_cis), int(freqs_cis.shape[0]),
-                                                ctypes.byref(c), int(layer_idx),
-                                                _ptr(dev_status), _stream(stream))
+    args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
+            _ptr(kv_norm_gamma), float(epsilon), _ptr(freqs_cis), int(freqs_cis.shape[0]),
+            ctypes.byref(c), int(layer_idx), _ptr(dev_status))
+    f = _lib.mla_cache_write_paged_qcache_at
+    here = _here(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis)
+    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_cache_write_paged_qcache_at", check)
 
 
@@ -502,13 +526,13 @@ def mla_rope_heads(x: torch.Tensor, positions: torch.Tensor, freqs_cis: torch.Te
     shape, sx, sy = x.shape, x.stride(), y.stride()
     if y.shape != shape or len(shape) != 3 or sx[2] != 1 or sy[2] != 1 or x.itemsize != 2 \
             or y.itemsize != 2 or positions.numel() != shape[0] \
-            or freqs_cis.shape[-1] != shape[2] or not _plain(4, positions, freqs_cis) \
-            or x.get_device() != freqs_cis.get_device() or y.get_device() != x.get_device():
+            or freqs_cis.shape[-1] != shape[2] or not _plain(4, positions, freqs_cis):
         return _check(PKM_ERR_INVALID_ARG, "mla_rope_heads", check)
-    code = _lib.mla_rope_heads(x.data_ptr(), sx[0], sx[1], _ptr(positions), shape[0], shape[1],
-                               shape[2], freqs_cis.data_ptr(), freqs_cis.shape[0],
-                               1 if half else 0, y.data_ptr(), sy[0], sy[1], _ptr(dev_status),
-                               _stream(stream))
+    args = (x.data_ptr(), sx[0], sx[1], _ptr(positions), shape[0], shape[1], shape[2],
+            freqs_cis.data_ptr(), freqs_cis.shape[0], 1 if half else 0, y.data_ptr(), sy[0],
+            sy[1], _ptr(dev_status))
+    f = _lib.mla_rope_heads
+    code = f(*args, _stream(stream)) if _here(x, positions, freqs_cis, y) else _refuse(f, *args)
     return _check(code, "mla_rope_heads", check)
 
 
@@ -547,12 +571,13 @@ def mla_tree_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
         return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged", check)
     c = cache.c_struct()
     rows, heads, _ = q.shape
-    code = _lib.mla_tree_attention_paged(
-        q.data_ptr(), input_row_offsets.data_ptr(), input_row_offsets.shape[0] - 1, rows, heads,
-        int(kv_lora_rank), int(rope_dim), float(softmax_scale), _ptr(tree_mask),
-        0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
-        out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
-        _ptr(dev_status), _stream(stream))
+    args = (q.data_ptr(), input_row_offsets.data_ptr(), input_row_offsets.shape[0] - 1, rows,
+            heads, int(kv_lora_rank), int(rope_dim), float(softmax_scale), _ptr(tree_mask),
+            0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
+            out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes, _ptr(dev_status))
+    f = _lib.mla_tree_attention_paged
+    here = _here(q, input_row_offsets, tree_mask, out, lse, workspace)
+    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_tree_attention_paged", check)
 
 
@@ -569,12 +594,13 @@ def mla_tree_attention_paged_qcache(q: torch.Tensor, input_row_offsets: torch.Te
         return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged_qcache", check)
     c = cache.c_struct()
     rows, heads, _ = q.shape
-    code = _lib.mla_tree_attention_paged_qcache(
-        q.data_ptr(), input_row_offsets.data_ptr(), input_row_offsets.shape[0] - 1, rows, heads,
-        float(softmax_scale), _ptr(tree_mask),
-        0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
-        out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
-        _ptr(dev_status), _stream(stream))
+    args = (q.data_ptr(), input_row_offsets.data_ptr(), input_row_offsets.shape[0] - 1, rows,
+            heads, float(softmax_scale), _ptr(tree_mask),
+            0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
+            out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes, _ptr(dev_status))
+    f = _lib.mla_tree_attention_paged_qcache
+    here = _here(q, input_row_offsets, tree_mask, out, lse, workspace)
+    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_tree_attention_paged_qcache", check)
 
 
@@ -597,9 +623,11 @@ def mla_cache_compact_paged(cache: PagedCache, layer_begin: int, layer_count: in
     if not _accepted_ok(shape, cache, accepted, accepted_counts, new_lengths):
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_compact_paged", check)
     c = cache.c_struct()
-    code = _lib.mla_cache_compact_paged(ctypes.byref(c), layer_begin, layer_count, shape[0],
-                                        accepted.data_ptr(), shape[1], _ptr(accepted_counts),
-                                        _ptr(new_lengths), _ptr(dev_status), _stream(stream))
+    args = (ctypes.byref(c), layer_begin, layer_count, shape[0], accepted.data_ptr(), shape[1],
+            _ptr(accepted_counts), _ptr(new_lengths), _ptr(dev_status))
+    f = _lib.mla_cache_compact_paged
+    here = _here(accepted, accepted_counts, new_lengths)
+    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_cache_compact_paged", check)
 
 
@@ -613,9 +641,11 @@ def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_co
     if not _accepted_ok(shape, cache, accepted, accepted_counts, new_lengths):
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_compact_paged_qcache", check)
     c = cache.c_struct()
-    code = _lib.mla_cache_compact_paged_qcache(ctypes.byref(c), layer_begin, layer_count, shape[0],
-                                               accepted.data_ptr(), shape[1], _ptr(accepted_counts),
-                                               _ptr(new_lengths), _ptr(dev_status), _stream(stream))
+    args = (ctypes.byref(c), layer_begin, layer_count, shape[0], accepted.data_ptr(), shape[1],
+            _ptr(accepted_counts), _ptr(new_lengths), _ptr(dev_status))
+    f = _lib.mla_cache_compact_paged_qcache
+    here = _here(accepted, accepted_counts, new_lengths)
+    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_cache_compact_paged_qcache", check)
 
 

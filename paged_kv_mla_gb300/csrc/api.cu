@@ -38,10 +38,14 @@ uint64_t wait_timeout_ns() {
     return ns;
 }
 
-// Streaming multiprocessors of the current device, cached per device id.  Threads may race
+thread_local bool checks_only = false;  // pkm_checks_only
+
+// Streaming multiprocessors of the current device, cached per device id.  Every launch asks for
+// them behind its checks.  Threads may race
 // to fill an entry; they all store the same value, and the atomics make that well defined.
 cudaError_t current_sm_count(int* out) {
     static std::atomic<int> counts[128] = {};
+    if (checks_only) return cudaErrorInvalidDevice;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -815,6 +819,8 @@ pkm_status cache_compact(CompactArgs a, const uint32_t* accepted, int32_t max_ac
     a.counts = accepted_counts;
     a.new_lengths = new_lengths;
     a.status = dev_status;
+    int sms = 0;
+    if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
     return cuda_status(pkm::launch_cache_compact(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1212,6 +1218,8 @@ pkm_status pkm_validate_row_offsets(const uint32_t* offsets, int32_t batch, int3
     return cuda_status(pkm::launch_validate_offsets(offsets, batch, dev_status,
                                                     static_cast<cudaStream_t>(stream)));
 }
+
+void pkm_checks_only(int32_t on) { checks_only = on != 0; }
 
 pkm_status pkm_check_wait_timeout(int32_t* dev_status, uint32_t timeout_ms, void* stream) {
     if (dev_status == nullptr || timeout_ms == 0 || timeout_ms > 5000) return PKM_ERR_INVALID_ARG;
