@@ -476,7 +476,9 @@ pkm_status mla_tree_attention_paged_qcache(const void* q, const uint32_t* input_
  *   max_accepted     row length of `accepted` (> 0).
  *   accepted         device uint32 [batch, max_accepted].
  *   accepted_counts  device uint32 [batch].
- *   new_lengths      device uint32 [batch], or NULL; not cache->cache_lengths.
+ *   new_lengths      device uint32 [batch], or NULL; without memory in common with
+ *                    cache->cache_lengths, cache->page_table, accepted or accepted_counts
+ *                    (PKM_ERR_INVALID_ARG otherwise).
  *   cache            row_elems a multiple of 8; cache_lengths required.
  * A request whose count exceeds max_accepted or whose drafts do not increase sets
  * PKM_ERR_INVALID_ARG in dev_status, one with a position outside the page table or the cache

@@ -618,7 +618,8 @@ def mla_cache_compact_paged(cache: PagedCache, layer_begin: int, layer_count: in
                             check: bool = True) -> int:
     """Moves request b's accepted drafts accepted[b, :accepted_counts[b]] (strictly increasing
     indices behind cache_lengths[b]) to the front of its drafted region in every layer of the
-    range, and writes the grown lengths to new_lengths."""
+    range, and writes the grown lengths to new_lengths (memory of its own, which none of the
+    other arguments has)."""
     shape = accepted.shape
     if not _accepted_ok(shape, cache, accepted, accepted_counts, new_lengths):
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_compact_paged", check)

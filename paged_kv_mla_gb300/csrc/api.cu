@@ -806,6 +806,12 @@ pkm_status mla_rope_heads(const void* x, int64_t x_row_stride, int64_t x_head_st
 
 namespace {
 
+// Whether n 32-bit words at p and m at q have memory in common.
+bool share_words(const uint32_t* p, int64_t n, const uint32_t* q, int64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + 4 * static_cast<uint64_t>(m) && b < a + 4 * static_cast<uint64_t>(n);
+}
+
 // Body of both compaction entry points, once the cache is described in bytes.
 pkm_status cache_compact(CompactArgs a, const uint32_t* accepted, int32_t max_accepted,
                          const uint32_t* accepted_counts, uint32_t* new_lengths,
@@ -813,7 +819,13 @@ pkm_status cache_compact(CompactArgs a, const uint32_t* accepted, int32_t max_ac
     if (accepted == nullptr || accepted_counts == nullptr || a.data == nullptr ||
         a.page_table == nullptr || a.cache_lengths == nullptr)
         return PKM_ERR_INVALID_ARG;
-    if (new_lengths == a.cache_lengths) return PKM_ERR_INVALID_ARG;
+    // a request's blocks read its table row, length, count and list while one writes its new length
+    if (new_lengths != nullptr &&
+        (share_words(new_lengths, a.batch, a.cache_lengths, a.batch) ||
+         share_words(new_lengths, a.batch, accepted_counts, a.batch) ||
+         share_words(new_lengths, a.batch, accepted, static_cast<int64_t>(a.batch) * max_accepted) ||
+         share_words(new_lengths, a.batch, a.page_table, static_cast<int64_t>(a.batch) * a.max_pages)))
+        return PKM_ERR_INVALID_ARG;
     a.accepted = accepted;
     a.max_accepted = max_accepted;
     a.counts = accepted_counts;

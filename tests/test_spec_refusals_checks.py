@@ -1,0 +1,44 @@
+"""Arguments of the speculative-decoding entry points that read or write the wrong memory: each
+refused by the calls' own checks, whose other verdict is that the call would go on to the GPU."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from test_spec_refusals import INVALID, i32, paged, quant
+
+GOES_ON = 3  # PKM_ERR_CUDA: nothing was found, and nothing may be launched
+
+
+@pytest.fixture()
+def pkm(monkeypatch):
+    """The binding with its checks alone, on host memory taken for the device's."""
+    import __graft_entry__
+    __graft_entry__.build()
+    import paged_kv_mla_gb300 as m
+    monkeypatch.setattr(m, "_here", lambda *tensors: True)
+    m._lib.pkm_checks_only(1)
+    yield m
+    m._lib.pkm_checks_only(0)
+
+
+def compact(pkm, cache, accepted, counts, new, begin=0, count=1):
+    f = pkm.mla_cache_compact_paged_qcache if isinstance(cache, pkm.QuantCache) \
+        else pkm.mla_cache_compact_paged
+    return f(cache, begin, count, accepted, counts, new, stream=0, check=False)
+
+
+@pytest.mark.parametrize("make", [paged, quant])
+def test_new_lengths_share_no_memory(pkm, make):
+    """Blocks of a request's other layers still read what its first block would overwrite."""
+    words = i32(64)
+    acc, cnt, new = words[0:6].view(2, 3), words[6:8], words[8:10]
+    lengths, table = words[10:12], words[12:20].view(2, 4)
+    cache = make(pkm, cache_lengths=lengths, page_table=table)
+    assert compact(pkm, cache, acc, cnt, new) == GOES_ON
+    assert compact(pkm, cache, acc, cnt, None) == GOES_ON
+    assert compact(pkm, cache, acc, cnt, cnt) == INVALID
+    for at in range(0, 20):
+        free = at == 8
+        assert compact(pkm, cache, acc, cnt, words[at:at + 2]) == (GOES_ON if free else INVALID), at
+    assert compact(pkm, cache, acc, cnt, words[20:22]) == GOES_ON
