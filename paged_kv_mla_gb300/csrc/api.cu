@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -812,12 +813,26 @@ bool share_words(const uint32_t* p, int64_t n, const uint32_t* q, int64_t m) {
     return a < b + 4 * static_cast<uint64_t>(m) && b < a + 4 * static_cast<uint64_t>(n);
 }
 
+// Whether a position has bytes of its own in every plane of every layer that is compacted: the
+// threads of one move rows while those of another still read theirs.
+bool planes_apart(const CompactArgs& a) {
+    if (a.page_size > 1 && a.slot_stride < a.payload) return false;
+    if (a.layer_count > 1 && a.layer_stride < a.payload) return false;
+    if (a.planes == 1) return true;
+    // the V plane of a layer between the K planes of the layers around it
+    const int64_t last = a.layer_count - 1;
+    const int64_t below = last > 0 ? std::min(a.kv_stride / a.layer_stride, last) : 0;
+    const int64_t above = std::min(below + 1, last);
+    return std::abs(a.kv_stride - below * a.layer_stride) >= a.payload &&
+           std::abs(a.kv_stride - above * a.layer_stride) >= a.payload;
+}
+
 // Body of both compaction entry points, once the cache is described in bytes.
 pkm_status cache_compact(CompactArgs a, const uint32_t* accepted, int32_t max_accepted,
                          const uint32_t* accepted_counts, uint32_t* new_lengths,
                          int32_t* dev_status, void* stream) {
     if (accepted == nullptr || accepted_counts == nullptr || a.data == nullptr ||
-        a.page_table == nullptr || a.cache_lengths == nullptr)
+        a.page_table == nullptr || a.cache_lengths == nullptr || !planes_apart(a))
         return PKM_ERR_INVALID_ARG;
     // a request's blocks read its table row, length, count and list while one writes its new length
     if (new_lengths != nullptr &&

@@ -42,3 +42,34 @@ def test_new_lengths_share_no_memory(pkm, make):
         free = at == 8
         assert compact(pkm, cache, acc, cnt, words[at:at + 2]) == (GOES_ON if free else INVALID), at
     assert compact(pkm, cache, acc, cnt, words[20:22]) == GOES_ON
+
+
+@pytest.mark.parametrize("make,wide", [(paged, 576), (quant, 656)])
+def test_layers_that_share_rows(pkm, make, wide):
+    """The threads of one layer would move what those of another have yet to read."""
+    def call(count=2, **kw):
+        return compact(pkm, make(pkm, num_layers=3, **kw), i32(2, 3), i32(2), i32(2), count=count)
+
+    assert call() == GOES_ON
+    assert call(layer_stride=0) == INVALID and call(layer_stride=0, count=1) == GOES_ON
+    assert call(layer_stride=wide - 16) == INVALID and call(layer_stride=wide) == GOES_ON
+    assert call(slot_stride=wide - 16) == INVALID
+
+
+def test_planes_that_share_rows(pkm):
+    def call(count=3, **kw):
+        return compact(pkm, paged(pkm, num_layers=3, **kw), i32(2, 3), i32(2), i32(2), count=count)
+
+    apart = dict(layer_stride=1152 * 64, slot_stride=1152, page_stride=1152 * 16)
+    assert call(kv_stride=576, **apart) == GOES_ON
+    assert call(kv_stride=568, **apart) == INVALID
+    assert call(kv_stride=568, count=1, **apart) == INVALID
+    for layers in (1, 2):  # the V plane on a later layer's K plane
+        assert call(kv_stride=layers * 1152 * 64, **apart) == INVALID
+        assert call(kv_stride=layers * 1152 * 64 - 576, **apart) == GOES_ON
+        assert call(kv_stride=layers * 1152 * 64 - 568, **apart) == INVALID
+        assert call(kv_stride=layers * 1152 * 64 + 568, **apart) == INVALID
+        assert call(kv_stride=layers * 1152 * 64 + 576, **apart) == GOES_ON
+    assert call(kv_stride=3 * 1152 * 64, **apart) == GOES_ON  # behind all
+    assert call(kv_stride=1152 * 64, count=1, **apart) == GOES_ON
+    assert call(page_size=1, slot_stride=0, page_stride=576) == GOES_ON
