@@ -372,6 +372,7 @@ pkm_status mla_cache_write_paged_qcache_at(const void* latent,
  *   x_*_stride      elements, multiples of 8 (>= 0; 0 broadcasts).
  *   positions       device uint32 [total_rows]; an entry >= max_seq_len sets
  *                   PKM_ERR_OUT_OF_RANGE in dev_status and leaves that row unwritten.
+ *   num_heads       at most 2^31 - 513.
  *   rope_dim        P: a multiple of 8, at most 256.
  *   freqs_cis       device fp32 [max_seq_len, P], 16-byte aligned: P/2 (cos, sin) pairs per
  *                   position, pair j being the layout's pair j.

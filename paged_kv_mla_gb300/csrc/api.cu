@@ -769,6 +769,8 @@ pkm_status mla_rope_heads(const void* x, int64_t x_row_stride, int64_t x_head_st
         !mult8(y_head_stride))
         return PKM_ERR_INVALID_ARG;
     if (rope_dim % 8 != 0 || rope_dim > 256) return PKM_ERR_UNSUPPORTED;
+    // a thread counts its heads, up to 512 behind the last, in 32 bits
+    if (num_heads > INT32_MAX - 512) return PKM_ERR_UNSUPPORTED;
     // the rows and heads of y must not overlap: heads inside rows, or rows inside heads
     const int64_t r1 = total_rows - 1, h1 = num_heads - 1, p = rope_dim;
     const int64_t wide = static_cast<int64_t>(1) << 62;

@@ -5,7 +5,7 @@ from __future__ import annotations
 import pytest
 import torch
 
-from test_spec_refusals import INVALID, i32, paged, quant
+from test_spec_refusals import INVALID, UNSUPPORTED, i32, paged, quant
 
 GOES_ON = 3  # PKM_ERR_CUDA: nothing was found, and nothing may be launched
 
@@ -73,3 +73,15 @@ def test_planes_that_share_rows(pkm):
     assert call(kv_stride=3 * 1152 * 64, **apart) == GOES_ON  # behind all
     assert call(kv_stride=1152 * 64, count=1, **apart) == GOES_ON
     assert call(page_size=1, slot_stride=0, page_stride=576) == GOES_ON
+
+
+def test_heads_that_a_thread_cannot_count(pkm):
+    """A head behind the last of 2^31 - 1 would get a negative number, and an address."""
+    x, f, pos = torch.zeros(64, dtype=torch.int16), torch.zeros(4, 8), i32(1)
+
+    def call(heads):
+        return pkm._lib.mla_rope_heads(x.data_ptr(), 0, 0, pos.data_ptr(), 1, heads, 8, f.data_ptr(),
+                                       4, 0, x.data_ptr() + 64, 8, 8, None, None)
+
+    assert call(2 ** 31 - 513) == GOES_ON
+    assert call(2 ** 31 - 512) == call(2 ** 31 - 1) == UNSUPPORTED
