@@ -473,6 +473,13 @@ def _has(n: int, t) -> bool:
     return t is None or t.__class__ is int or t.numel() >= n
 
 
+def _cache_ok(cache, batch: int) -> bool:
+    """A table row and a length for each request (and maybe for more)."""
+    table, lengths = cache.page_table, cache.cache_lengths
+    return (table.ndim == 2 and table.shape[0] >= batch and _has(batch, lengths) and
+            _plain(4, table, lengths))
+
+
 def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tensor,
                              positions: torch.Tensor, kv_norm_gamma: torch.Tensor,
                              epsilon: float, freqs_cis: torch.Tensor, cache: PagedCache,
@@ -482,16 +489,17 @@ def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tens
     """mla_cache_write_paged with row r rotated by freqs_cis[positions[r]] (positions:
     uint32/int32 [total_rows]), wherever its slot is."""
     rows = latent.shape[0]
-    if not _has(rows, positions) or not _plain(4, positions):
+    batch = input_row_offsets.shape[0] - 1
+    if not _has(rows, positions) or not _plain(4, positions) or not _cache_ok(cache, batch):
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_at", check)
     c = cache.c_struct()
-    batch = input_row_offsets.shape[0] - 1
     args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
             int(kv_lora_rank), int(rope_dim), _ptr(kv_norm_gamma), float(epsilon),
             _ptr(freqs_cis), freqs_cis.shape[0], ctypes.byref(c), int(layer_idx),
             _ptr(dev_status))
     f = _lib.mla_cache_write_paged_at
-    here = _here(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis)
+    here = _here(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis, cache.data,
+                 cache.page_table, cache.cache_lengths)
     code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_cache_write_paged_at", check)
 
@@ -503,15 +511,16 @@ def mla_cache_write_paged_qcache_at(latent: torch.Tensor, input_row_offsets: tor
                                     stream=None, check: bool = True) -> int:
     """mla_cache_write_paged_qcache with row r rotated by freqs_cis[positions[r]]."""
     rows = latent.shape[0]
-    if not _has(rows, positions) or not _plain(4, positions):
+    batch = input_row_offsets.shape[0] - 1
+    if not _has(rows, positions) or not _plain(4, positions) or not _cache_ok(cache, batch):
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_qcache_at", check)
     c = cache.c_struct()
-    batch = input_row_offsets.shape[0] - 1
     args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
             _ptr(kv_norm_gamma), float(epsilon), _ptr(freqs_cis), int(freqs_cis.shape[0]),
             ctypes.byref(c), int(layer_idx), _ptr(dev_status))
     f = _lib.mla_cache_write_paged_qcache_at
-    here = _here(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis)
+    here = _here(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis, cache.data,
+                 cache.page_table, cache.cache_lengths)
     code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_cache_write_paged_qcache_at", check)
 
@@ -542,7 +551,7 @@ def mla_tree_attention_paged_workspace_size(total_rows: int, num_heads: int,
                                                             int(kv_lora_rank)))
 
 
-def _tree_shapes_ok(q, offsets, tree_mask, out, lse, workspace, rank, rope) -> bool:
+def _tree_shapes_ok(q, offsets, tree_mask, cache, out, lse, workspace, rank, rope) -> bool:
     """Shapes that the C call cannot see; an empty mask would pass for no mask there."""
     if q.ndim != 3:
         return False
@@ -551,6 +560,7 @@ def _tree_shapes_ok(q, offsets, tree_mask, out, lse, workspace, rank, rope) -> b
             (lse is None or lse.shape == (rows, heads)) and
             (tree_mask is None or (tree_mask.ndim == 2 and tree_mask.shape[0] == rows and
                                    tree_mask.shape[1] > 0)) and
+            _cache_ok(cache, offsets.shape[0] - 1) and
             _plain(2, q, out) and _plain(4, offsets, tree_mask, lse) and
             _plain(workspace.itemsize, workspace))
 
@@ -566,8 +576,8 @@ def mla_tree_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
     cache: each over its request's cached tokens and those new ones that its tree_mask row
     (uint32/int32 [total_rows, words], one bit a token; None: the tokens up to itself) names.
     out [total_rows, heads, R] bf16, lse [total_rows, heads] fp32 or None."""
-    if not _tree_shapes_ok(q, input_row_offsets, tree_mask, out, lse, workspace, kv_lora_rank,
-                           rope_dim):
+    if not _tree_shapes_ok(q, input_row_offsets, tree_mask, cache, out, lse, workspace,
+                           kv_lora_rank, rope_dim):
         return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged", check)
     c = cache.c_struct()
     rows, heads, _ = q.shape
@@ -576,7 +586,8 @@ def mla_tree_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
             0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
             out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes, _ptr(dev_status))
     f = _lib.mla_tree_attention_paged
-    here = _here(q, input_row_offsets, tree_mask, out, lse, workspace)
+    here = _here(q, input_row_offsets, tree_mask, out, lse, workspace, cache.data,
+                 cache.page_table, cache.cache_lengths)
     code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_tree_attention_paged", check)
 
@@ -589,7 +600,7 @@ def mla_tree_attention_paged_qcache(q: torch.Tensor, input_row_offsets: torch.Te
                                     dev_status: Optional[torch.Tensor] = None, stream=None,
                                     check: bool = True) -> int:
     """mla_tree_attention_paged over a quantised cache."""
-    if not _tree_shapes_ok(q, input_row_offsets, tree_mask, out, lse, workspace,
+    if not _tree_shapes_ok(q, input_row_offsets, tree_mask, cache, out, lse, workspace,
                            cache.kv_lora_rank, cache.rope_dim):
         return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged_qcache", check)
     c = cache.c_struct()
@@ -599,14 +610,16 @@ def mla_tree_attention_paged_qcache(q: torch.Tensor, input_row_offsets: torch.Te
             0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
             out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes, _ptr(dev_status))
     f = _lib.mla_tree_attention_paged_qcache
-    here = _here(q, input_row_offsets, tree_mask, out, lse, workspace)
+    here = _here(q, input_row_offsets, tree_mask, out, lse, workspace, cache.data,
+                 cache.page_table, cache.cache_lengths)
     code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_tree_attention_paged_qcache", check)
 
 
 def _accepted_ok(shape, cache, accepted, counts, new_lengths) -> bool:
-    """A table row, count and new length for each list of accepted drafts (and maybe for more)."""
-    return (len(shape) == 2 and cache.page_table.shape[0] >= shape[0] and
+    """A table row, length, count and new length for each list of accepted drafts (and maybe for
+    more)."""
+    return (len(shape) == 2 and _cache_ok(cache, shape[0]) and
             _has(shape[0], counts) and _has(shape[0], new_lengths) and
             _plain(4, accepted, counts, new_lengths))
 
@@ -627,7 +640,8 @@ def mla_cache_compact_paged(cache: PagedCache, layer_begin: int, layer_count: in
     args = (ctypes.byref(c), layer_begin, layer_count, shape[0], accepted.data_ptr(), shape[1],
             _ptr(accepted_counts), _ptr(new_lengths), _ptr(dev_status))
     f = _lib.mla_cache_compact_paged
-    here = _here(accepted, accepted_counts, new_lengths)
+    here = _here(accepted, accepted_counts, new_lengths, cache.data, cache.page_table,
+                 cache.cache_lengths)
     code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_cache_compact_paged", check)
 
@@ -645,7 +659,8 @@ def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_co
     args = (ctypes.byref(c), layer_begin, layer_count, shape[0], accepted.data_ptr(), shape[1],
             _ptr(accepted_counts), _ptr(new_lengths), _ptr(dev_status))
     f = _lib.mla_cache_compact_paged_qcache
-    here = _here(accepted, accepted_counts, new_lengths)
+    here = _here(accepted, accepted_counts, new_lengths, cache.data, cache.page_table,
+                 cache.cache_lengths)
     code = f(*args, _stream(stream)) if here else _refuse(f, *args)
     return _check(code, "mla_cache_compact_paged_qcache", check)
 

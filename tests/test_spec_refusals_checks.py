@@ -5,7 +5,7 @@ from __future__ import annotations
 import pytest
 import torch
 
-from test_spec_refusals import INVALID, UNSUPPORTED, i32, paged, quant
+from test_spec_refusals import INVALID, UNSUPPORTED, attention, b16, i32, paged, quant
 
 GOES_ON = 3  # PKM_ERR_CUDA: nothing was found, and nothing may be launched
 
@@ -85,3 +85,47 @@ def test_heads_that_a_thread_cannot_count(pkm):
 
     assert call(2 ** 31 - 513) == GOES_ON
     assert call(2 ** 31 - 512) == call(2 ** 31 - 1) == UNSUPPORTED
+
+
+def attend(pkm, cache, offsets=None, **kw):
+    return attention(pkm, cache, offsets=offsets, **kw)
+
+
+def write(pkm, cache, latent=None, offsets=None, positions=None, gamma=None, freqs=None):
+    args = (b16(3, 576) if latent is None else latent, i32(3) if offsets is None else offsets,
+            i32(3) if positions is None else positions,
+            torch.zeros(512) if gamma is None else gamma, 1e-6,
+            torch.zeros(8, 64) if freqs is None else freqs, cache, 0)
+    if isinstance(cache, pkm.QuantCache):
+        return pkm.mla_cache_write_paged_qcache_at(*args, stream=0, check=False)
+    return pkm.mla_cache_write_paged_at(*args, 512, 64, stream=0, check=False)
+
+
+def move(pkm, cache):
+    return compact(pkm, cache, i32(2, 3), i32(2), i32(2))
+
+
+CALLS = pytest.mark.parametrize("call", [attend, write, move])
+MAKES = pytest.mark.parametrize("make", [paged, quant])
+
+
+@CALLS
+@MAKES
+def test_descriptors_of_fewer_requests(pkm, call, make):
+    """Table rows, lengths and their types as the call's requests need them."""
+    assert call(pkm, make(pkm)) == GOES_ON
+    assert call(pkm, make(pkm, page_table=i32(5, 4), cache_lengths=i32(5))) == GOES_ON
+    for table in (i32(1, 4), i32(8), i32(2, 4).long(), i32(2, 8)[:, :4], i32(2, 4, 1)):
+        assert call(pkm, make(pkm, page_table=table)) == INVALID
+    for lengths in (i32(1), i32(2).long(), i32(4)[::2], None):
+        assert call(pkm, make(pkm, cache_lengths=lengths)) == INVALID
+
+
+@pytest.mark.parametrize("field", ["data", "page_table", "cache_lengths"])
+@CALLS
+@MAKES
+def test_descriptors_in_other_memory(pkm, monkeypatch, call, make, field):
+    cache = make(pkm)
+    there = getattr(cache, field)
+    monkeypatch.setattr(pkm, "_here", lambda *tensors: all(t is not there for t in tensors))
+    assert call(pkm, cache) == INVALID
