@@ -436,13 +436,18 @@ def mla_cache_write_paged(latent: torch.Tensor, input_row_offsets: torch.Tensor,
 _initialized = torch.cuda.is_initialized
 
 
-def _plain(itemsize: int, *tensors) -> bool:
-    """Whether the tensors are what the C calls take them for, elements of that size without
-    gaps (None and addresses pass)."""
+# Element types that the C calls read as what they are named for: bf16 values or their bits.
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_WORD = (torch.int32, torch.uint32)
+_FLOAT = (torch.float32,)
+
+
+def _plain(types: tuple, *tensors) -> bool:
+    """Whether the tensors have one of the types and no gaps (None and addresses pass)."""
     for t in tensors:
         if t is None or t.__class__ is int:
             continue
-        if t.itemsize != itemsize or not t.is_contiguous():
+        if t.dtype not in types or not t.is_contiguous():
             return False
     return True
 
@@ -477,7 +482,7 @@ def _cache_ok(cache, batch: int) -> bool:
     """A table row and a length for each request (and maybe for more)."""
     table, lengths = cache.page_table, cache.cache_lengths
     return (table.ndim == 2 and table.shape[0] >= batch and _has(batch, lengths) and
-            _plain(4, table, lengths))
+            _plain(_WORD, table, lengths))
 
 
 def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tensor,
@@ -490,7 +495,7 @@ def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tens
     uint32/int32 [total_rows]), wherever its slot is."""
     rows = latent.shape[0]
     batch = input_row_offsets.shape[0] - 1
-    if not _has(rows, positions) or not _plain(4, positions) or not _cache_ok(cache, batch):
+    if not _has(rows, positions) or not _plain(_WORD, positions) or not _cache_ok(cache, batch):
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_at", check)
     c = cache.c_struct()
     args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
@@ -512,7 +517,7 @@ def mla_cache_write_paged_qcache_at(latent: torch.Tensor, input_row_offsets: tor
     """mla_cache_write_paged_qcache with row r rotated by freqs_cis[positions[r]]."""
     rows = latent.shape[0]
     batch = input_row_offsets.shape[0] - 1
-    if not _has(rows, positions) or not _plain(4, positions) or not _cache_ok(cache, batch):
+    if not _has(rows, positions) or not _plain(_WORD, positions) or not _cache_ok(cache, batch):
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_qcache_at", check)
     c = cache.c_struct()
     args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
@@ -533,9 +538,10 @@ def mla_rope_heads(x: torch.Tensor, positions: torch.Tensor, freqs_cis: torch.Te
     dimensions; y may be x) by the (cos, sin) pairs of freqs_cis[positions[row]]: pairs
     (2j, 2j + 1), or (j, j + P/2) with `half`."""
     shape, sx, sy = x.shape, x.stride(), y.stride()
-    if y.shape != shape or len(shape) != 3 or sx[2] != 1 or sy[2] != 1 or x.itemsize != 2 \
-            or y.itemsize != 2 or positions.numel() != shape[0] \
-            or freqs_cis.shape[-1] != shape[2] or not _plain(4, positions, freqs_cis):
+    if y.shape != shape or len(shape) != 3 or sx[2] != 1 or sy[2] != 1 \
+            or x.dtype not in _BF16 or y.dtype not in _BF16 or positions.numel() != shape[0] \
+            or freqs_cis.shape[-1] != shape[2] or not _plain(_WORD, positions) \
+            or not _plain(_FLOAT, freqs_cis):
         return _check(PKM_ERR_INVALID_ARG, "mla_rope_heads", check)
     args = (x.data_ptr(), sx[0], sx[1], _ptr(positions), shape[0], shape[1], shape[2],
             freqs_cis.data_ptr(), freqs_cis.shape[0], 1 if half else 0, y.data_ptr(), sy[0],
@@ -561,8 +567,8 @@ def _tree_shapes_ok(q, offsets, tree_mask, cache, out, lse, workspace, rank, rop
             (tree_mask is None or (tree_mask.ndim == 2 and tree_mask.shape[0] == rows and
                                    tree_mask.shape[1] > 0)) and
             _cache_ok(cache, offsets.shape[0] - 1) and
-            _plain(2, q, out) and _plain(4, offsets, tree_mask, lse) and
-            _plain(workspace.itemsize, workspace))
+            _plain(_BF16, q, out) and _plain(_WORD, offsets, tree_mask) and
+            _plain(_FLOAT, lse) and workspace.is_contiguous())
 
 
 def mla_tree_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
@@ -621,7 +627,7 @@ def _accepted_ok(shape, cache, accepted, counts, new_lengths) -> bool:
     more)."""
     return (len(shape) == 2 and _cache_ok(cache, shape[0]) and
             _has(shape[0], counts) and _has(shape[0], new_lengths) and
-            _plain(4, accepted, counts, new_lengths))
+            _plain(_WORD, accepted, counts, new_lengths))
 
 
 def mla_cache_compact_paged(cache: PagedCache, layer_begin: int, layer_count: int,

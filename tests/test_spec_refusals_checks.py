@@ -129,3 +129,57 @@ def test_descriptors_in_other_memory(pkm, monkeypatch, call, make, field):
     there = getattr(cache, field)
     monkeypatch.setattr(pkm, "_here", lambda *tensors: all(t is not there for t in tensors))
     assert call(pkm, cache) == INVALID
+
+
+@MAKES
+@pytest.mark.parametrize("what", [
+    dict(q=torch.float16), dict(out=torch.float16), dict(mask=torch.float32),
+    dict(lse=torch.int32), dict(offsets=torch.float32)])
+def test_attention_types(pkm, make, what):
+    """Elements of the right size and the wrong type, which would be read as other values."""
+    (name, dtype), = what.items()
+    shapes = dict(q=(3, 2, 576), out=(3, 2, 512), mask=(3, 1), lse=(3, 2), offsets=(3,))
+    right = dict(q=torch.bfloat16, out=torch.bfloat16, mask=torch.uint32, lse=torch.float32,
+                 offsets=torch.uint32)
+
+    def call(dtypes):
+        t = {k: torch.zeros(shapes[k], dtype=d) for k, d in dtypes.items()}
+        n = pkm.mla_tree_attention_paged_workspace_size(3, 2, 512)
+        raw = torch.zeros(n + 256, dtype=torch.uint8)
+        kw = dict(tree_mask=t["mask"], lse=t["lse"], stream=0, check=False)
+        ws, cache = raw[-raw.data_ptr() % 256:][:n], make(pkm)
+        if make is quant:
+            return pkm.mla_tree_attention_paged_qcache(t["q"], t["offsets"], 1.0, cache, 0,
+                                                       t["out"], ws, **kw)
+        return pkm.mla_tree_attention_paged(t["q"], t["offsets"], 1.0, cache, 0, 512, 64, t["out"],
+                                            ws, **kw)
+
+    assert call(right) == GOES_ON
+    assert call({**right, name: dtype}) == INVALID
+
+
+def test_rope_types(pkm):
+    def call(x=torch.bfloat16, y=torch.bfloat16, positions=torch.uint32, freqs=torch.float32):
+        return pkm.mla_rope_heads(torch.zeros(3, 4, 16, dtype=x), torch.zeros(3, dtype=positions),
+                                  torch.zeros(4, 16, dtype=freqs), torch.zeros(3, 4, 16, dtype=y),
+                                  stream=0, check=False)
+
+    assert call() == GOES_ON and call(x=torch.int16, y=torch.int16, positions=torch.int32) == GOES_ON
+    assert call(x=torch.float16) == call(y=torch.float16) == INVALID
+    assert call(positions=torch.float32) == call(freqs=torch.int32) == INVALID
+
+
+@CALLS
+@MAKES
+def test_descriptor_types(pkm, call, make):
+    assert call(pkm, make(pkm, page_table=torch.zeros(2, 4))) == INVALID
+    assert call(pkm, make(pkm, cache_lengths=torch.zeros(2))) == INVALID
+
+
+@MAKES
+def test_compaction_types(pkm, make):
+    for bad in range(3):
+        args = [torch.zeros(s, dtype=torch.float32 if i == bad else torch.uint32)
+                for i, s in enumerate([(2, 3), (2,), (2,)])]
+        assert compact(pkm, make(pkm), *args) == INVALID
+    assert compact(pkm, make(pkm), *(a.view(torch.uint32) for a in (i32(2, 3), i32(2), i32(2)))) == GOES_ON
