@@ -485,6 +485,16 @@ def _cache_ok(cache, batch: int) -> bool:
             _plain(_WORD, table, lengths))
 
 
+def _rows_ok(latent, offsets, positions, gamma, freqs, cache, rank, rope) -> bool:
+    """Rows of R + P columns with a position each, R factors of the norm, P of a position (or for a
+    P of 0 any), and a descriptor for the requests that the offsets tell of."""
+    return (latent.ndim == 2 and latent.shape[1] == rank + rope and
+            _has(latent.shape[0], positions) and _has(rank, gamma) and
+            (rope == 0 or (freqs.ndim == 2 and freqs.shape[1] == rope)) and
+            _cache_ok(cache, offsets.shape[0] - 1) and _plain(_BF16, latent) and
+            _plain(_WORD, offsets, positions) and _plain(_FLOAT, gamma, freqs))
+
+
 def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tensor,
                              positions: torch.Tensor, kv_norm_gamma: torch.Tensor,
                              epsilon: float, freqs_cis: torch.Tensor, cache: PagedCache,
@@ -493,11 +503,11 @@ def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tens
                              check: bool = True) -> int:
     """mla_cache_write_paged with row r rotated by freqs_cis[positions[r]] (positions:
     uint32/int32 [total_rows]), wherever its slot is."""
-    rows = latent.shape[0]
-    batch = input_row_offsets.shape[0] - 1
-    if not _has(rows, positions) or not _plain(_WORD, positions) or not _cache_ok(cache, batch):
+    if not _rows_ok(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis, cache,
+                    kv_lora_rank, rope_dim):
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_at", check)
     c = cache.c_struct()
+    rows, batch = latent.shape[0], input_row_offsets.shape[0] - 1
     args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
             int(kv_lora_rank), int(rope_dim), _ptr(kv_norm_gamma), float(epsilon),
             _ptr(freqs_cis), freqs_cis.shape[0], ctypes.byref(c), int(layer_idx),
@@ -515,11 +525,11 @@ def mla_cache_write_paged_qcache_at(latent: torch.Tensor, input_row_offsets: tor
                                     layer_idx: int, dev_status: Optional[torch.Tensor] = None,
                                     stream=None, check: bool = True) -> int:
     """mla_cache_write_paged_qcache with row r rotated by freqs_cis[positions[r]]."""
-    rows = latent.shape[0]
-    batch = input_row_offsets.shape[0] - 1
-    if not _has(rows, positions) or not _plain(_WORD, positions) or not _cache_ok(cache, batch):
+    if not _rows_ok(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis, cache,
+                    cache.kv_lora_rank, cache.rope_dim):
         return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_qcache_at", check)
     c = cache.c_struct()
+    rows, batch = latent.shape[0], input_row_offsets.shape[0] - 1
     args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
             _ptr(kv_norm_gamma), float(epsilon), _ptr(freqs_cis), int(freqs_cis.shape[0]),
             ctypes.byref(c), int(layer_idx), _ptr(dev_status))

@@ -183,3 +183,29 @@ def test_compaction_types(pkm, make):
                 for i, s in enumerate([(2, 3), (2,), (2,)])]
         assert compact(pkm, make(pkm), *args) == INVALID
     assert compact(pkm, make(pkm), *(a.view(torch.uint32) for a in (i32(2, 3), i32(2), i32(2)))) == GOES_ON
+
+
+@MAKES
+def test_rows_to_be_written(pkm, make):
+    """What the cache write at positions takes for rows, offsets and factors."""
+    def call(**kw):
+        return write(pkm, make(pkm), **kw)
+
+    good = dict(latent=torch.zeros(3, 576, dtype=torch.bfloat16), offsets=i32(3).view(torch.uint32),
+                positions=i32(4), gamma=torch.ones(600), freqs=torch.zeros(8, 64))
+    assert call() == call(**good) == GOES_ON
+    for bad in (dict(latent=b16(3, 640)), dict(latent=b16(3, 640)[:, :576]), dict(latent=b16(3 * 576)),
+                dict(latent=torch.zeros(3, 576, dtype=torch.float16)),
+                dict(latent=torch.zeros(3, 576)), dict(offsets=i32(3).long()), dict(offsets=i32(6)[::2]),
+                dict(positions=i32(2)), dict(positions=i32(3).long()), dict(gamma=torch.ones(511)),
+                dict(gamma=torch.ones(512).bfloat16()), dict(gamma=torch.ones(1024)[::2]),
+                dict(freqs=torch.zeros(8, 32)), dict(freqs=torch.zeros(8, 64).bfloat16()),
+                dict(freqs=torch.zeros(8, 128)[:, :64]), dict(freqs=torch.zeros(512))):
+        assert call(**{**good, **bad}) == INVALID, bad.keys()
+
+
+def test_rows_without_rope_columns(pkm):
+    cache = paged(pkm, cols=512)
+    for freqs in (torch.zeros(8, 0), torch.zeros(8, 64), torch.zeros(8)):
+        assert pkm.mla_cache_write_paged_at(b16(3, 512), i32(3), i32(3), torch.ones(512), 1e-6, freqs,
+                                            cache, 0, 512, 0, stream=0, check=False) == GOES_ON
