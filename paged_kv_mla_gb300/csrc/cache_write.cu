@@ -66,7 +66,8 @@ struct RowCursor {
 
     // Lane i of the warp: largest b with row_offsets[b] <= r0 + i, or 0.  For r0 the warp looks at
     // 32 places at a time (two steps for 1024 requests, where halving takes ten), and the lanes
-    // behind find theirs among the 32 offsets from there on.
+    // behind find theirs among the 32 offsets from there on, or behind more empty requests than
+    // that by halving.
     __device__ __forceinline__ void init(const CacheWriteArgs& a, int64_t r0) {
         const uint32_t* iro = a.row_offsets;
         const int lane = threadIdx.x & 31;
@@ -86,6 +87,14 @@ struct RowCursor {
         for (int s = 16; s > 0; s /= 2)
             if (static_cast<int64_t>(__shfl_sync(0xffffffffu, next, n + s - 1)) <= r0 + lane) n += s;
         l = min(l + n, a.batch - 1);
+        if (n == 31) {
+            h = a.batch;
+            while (h - l > 1) {
+                const int mid = l + (h - l) / 2;
+                if (static_cast<int64_t>(__ldg(iro + mid)) <= r0 + lane) l = mid;
+                else h = mid;
+            }
+        }
         b = l;
         lo = __ldg(iro + l);
         hi = __ldg(iro + l + 1);
