@@ -172,7 +172,7 @@ def last_cuda_error() -> str:
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
+    if t.__class__ is not torch.Tensor and not isinstance(t, torch.Tensor):
         return int(t)
     return t.data_ptr()
 
@@ -183,7 +183,8 @@ def _current_stream() -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-if not (hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice")):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None or not hasattr(torch._C, "_cuda_getDevice"):
     def _current_stream() -> int:  # noqa: F811
         return torch.cuda.current_stream().cuda_stream
 
@@ -213,24 +214,27 @@ class _Descriptor:
         return {k: v for k, v in self.__dict__.items() if k not in ("_mark", "_kept")}
 
     def c_struct(self):
+        table, lengths = self.page_table, self.cache_lengths
+        return self._struct_of((self.data.data_ptr(), table.data_ptr(), table.shape[-1],
+                                _ptr(lengths)))
+
+    def _struct_of(self, tensors: tuple):
+        """The struct with what it says of the tensors: data, page_table, max_pages_per_seq and
+        cache_lengths."""
         d = self.__dict__
         kept = d.get("_kept")
         if kept is None:
             kept = d.setdefault("_kept", threading.local())
         mark = d.get("_mark")
         try:
-            c, made = kept.struct
+            c, made, said = kept.struct
         except AttributeError:
-            c = made = None
+            c = made = said = None
         if c is None or made is not mark:
-            c = self._new_struct()
-            kept.struct = c, mark
-        else:
-            table = self.page_table
-            c.data = self.data.data_ptr()
-            c.page_table = table.data_ptr()
-            c.max_pages_per_seq = table.shape[-1]
-            c.cache_lengths = _ptr(self.cache_lengths)
+            c, said = self._new_struct(), None
+        if tensors != said:  # assigning to the struct takes longer than comparing
+            c.data, c.page_table, c.max_pages_per_seq, c.cache_lengths = tensors
+            kept.struct = c, mark, tensors
         return c
 
 
@@ -255,12 +259,9 @@ class PagedCache(_Descriptor):
     cache_lengths: Optional[torch.Tensor] = None
 
     def _new_struct(self) -> _CCache:
-        table = self.page_table  # once: another thread may assign it
-        return _CCache(self.data.data_ptr(), int(self.layer_stride), int(self.page_stride),
-                       int(self.slot_stride), int(self.kv_stride), int(self.num_layers),
-                       int(self.num_pages), int(self.page_size), int(self.row_elems),
-                       table.data_ptr(), int(table.shape[-1]),
-                       _ptr(self.cache_lengths))
+        return _CCache(None, int(self.layer_stride), int(self.page_stride), int(self.slot_stride),
+                       int(self.kv_stride), int(self.num_layers), int(self.num_pages),
+                       int(self.page_size), int(self.row_elems))
 
 
 @dataclass
@@ -283,12 +284,9 @@ class QuantCache(_Descriptor):
     cache_lengths: Optional[torch.Tensor] = None
 
     def _new_struct(self) -> _CQuantCache:
-        table = self.page_table  # once: another thread may assign it
-        return _CQuantCache(self.data.data_ptr(), int(self.layer_stride), int(self.page_stride),
+        return _CQuantCache(None, int(self.layer_stride), int(self.page_stride),
                             int(self.slot_stride), int(self.num_layers), int(self.num_pages),
-                            int(self.page_size), int(self.kv_lora_rank), int(self.rope_dim),
-                            table.data_ptr(), int(table.shape[-1]),
-                            _ptr(self.cache_lengths))
+                            int(self.page_size), int(self.kv_lora_rank), int(self.rope_dim))
 
 
 def _check(code: int, where: str, check: bool) -> int:
@@ -433,66 +431,75 @@ def mla_cache_write_paged(latent: torch.Tensor, input_row_offsets: torch.Tensor,
     return _check(code, "mla_cache_write_paged", check)
 
 
-_initialized = torch.cuda.is_initialized
-
-
 # Element types that the C calls read as what they are named for: bf16 values or their bits.
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _WORD = (torch.int32, torch.uint32)
 _FLOAT = (torch.float32,)
+_Tensor = torch.Tensor
 
 
-def _plain(types: tuple, *tensors) -> bool:
-    """Whether the tensors have one of the types and no gaps (None and addresses pass)."""
-    for t in tensors:
-        if t is None or t.__class__ is int:
+def _look(tensors: tuple) -> tuple:
+    """The device of the tensors in (types, elements at least, tensor) and their addresses.  The
+    device is -1 for host memory or several, -2 if there is none to be seen (None and addresses
+    pass), and None if a tensor has fewer elements, another type or, unless its types are None,
+    gaps.  One pass over all of them: it is much of a small call."""
+    device, addresses = -2, []
+    for types, n, t in tensors:
+        if t.__class__ is not _Tensor and (t is None or t.__class__ is int):
+            addresses.append(t)
             continue
-        if t.dtype not in types or not t.is_contiguous():
-            return False
-    return True
+        if types is not None and (t.dtype not in types or not t.is_contiguous()) \
+                or n > 0 and t.numel() < n:
+            return None, addresses
+        at = t.get_device()
+        if at != device:
+            device = at if device == -2 else -1
+        addresses.append(t.data_ptr())
+    return device, addresses
 
 
-def _here(*tensors) -> bool:
-    """Whether the tensors lie on the device that the call runs on (None and addresses pass).
-    While CUDA is not initialised no tensor does."""
-    device = torch._C._cuda_getDevice() if _initialized() else None
-    for t in tensors:
-        if t is not None and t.__class__ is not int and t.get_device() != device:
-            return False
-    return True
+def _here(device: int) -> bool:
+    """Whether tensors of that device are where the call runs.  (A tensor on a GPU has initialised
+    CUDA; before, there are only others.)"""
+    return device == -2 or (device >= 0 and device == torch._C._cuda_getDevice())
 
 
-def _refuse(f, *args) -> int:
-    """The status of a call whose tensors are not _here: what its own checks find, if anything.
-    `args` end before the stream."""
-    _lib.pkm_checks_only(1)
-    try:
-        code = f(*args, None)
-    finally:
-        _lib.pkm_checks_only(0)
-    return PKM_ERR_INVALID_ARG if code == PKM_ERR_CUDA else code
+def _run(f, where: str, args: tuple, device: int, stream, check: bool) -> int:
+    """f(*args, stream) for tensors of the call's device.  For others the status of what the
+    call's own checks find, if anything, and nothing is launched."""
+    if _here(device):
+        if stream is None and device >= 0 and _raw_stream is not None:
+            code = f(*args, _raw_stream(device))
+        else:
+            code = f(*args, _stream(stream))
+    else:
+        _lib.pkm_checks_only(1)
+        try:
+            code = f(*args, None)
+        finally:
+            _lib.pkm_checks_only(0)
+        if code == PKM_ERR_CUDA:
+            code = PKM_ERR_INVALID_ARG
+    return code if code == PKM_OK else _check(code, where, check)
 
 
-def _has(n: int, t) -> bool:
-    """At least n elements, as far as can be seen."""
-    return t is None or t.__class__ is int or t.numel() >= n
-
-
-def _cache_ok(cache, batch: int) -> bool:
-    """A table row and a length for each request (and maybe for more)."""
-    table, lengths = cache.page_table, cache.cache_lengths
-    return (table.ndim == 2 and table.shape[0] >= batch and _has(batch, lengths) and
-            _plain(_WORD, table, lengths))
-
-
-def _rows_ok(latent, offsets, positions, gamma, freqs, cache, rank, rope) -> bool:
-    """Rows of R + P columns with a position each, R factors of the norm, P of a position (or for a
-    P of 0 any), and a descriptor for the requests that the offsets tell of."""
-    return (latent.ndim == 2 and latent.shape[1] == rank + rope and
-            _has(latent.shape[0], positions) and _has(rank, gamma) and
-            (rope == 0 or (freqs.ndim == 2 and freqs.shape[1] == rope)) and
-            _cache_ok(cache, offsets.shape[0] - 1) and _plain(_BF16, latent) and
-            _plain(_WORD, offsets, positions) and _plain(_FLOAT, gamma, freqs))
+def _write_at(f, where, latent, offsets, positions, gamma, epsilon, freqs, cache, layer_idx, rank,
+              rope, widths, dev_status, stream, check) -> int:
+    """Both cache writes at positions: rows of R + P columns with a position each, R factors of the
+    norm, P of a position (any for a P of 0), and a table row and a length for each request."""
+    table = cache.page_table
+    shape, factors, pages, batch = latent.shape, freqs.shape, table.shape, offsets.shape[0] - 1
+    device, at = _look(((_BF16, 0, latent), (_WORD, 0, offsets), (_WORD, shape[0], positions),
+                        (_FLOAT, rank, gamma), (_FLOAT, 0, freqs), (None, 0, cache.data),
+                        (_WORD, 0, table), (_WORD, batch, cache.cache_lengths)))
+    if device is None or len(shape) != 2 or shape[1] != rank + rope \
+            or (rope != 0 and (len(factors) != 2 or factors[1] != rope)) \
+            or len(pages) != 2 or pages[0] < batch:
+        return _check(PKM_ERR_INVALID_ARG, where, check)
+    c = cache._struct_of((at[5], at[6], pages[1], at[7]))
+    args = (at[0], at[1], at[2], batch, shape[0], *widths, at[3], float(epsilon), at[4], factors[0],
+            ctypes.byref(c), int(layer_idx), _ptr(dev_status))
+    return _run(f, where, args, device, stream, check)
 
 
 def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tensor,
@@ -503,20 +510,10 @@ def mla_cache_write_paged_at(latent: torch.Tensor, input_row_offsets: torch.Tens
                              check: bool = True) -> int:
     """mla_cache_write_paged with row r rotated by freqs_cis[positions[r]] (positions:
     uint32/int32 [total_rows]), wherever its slot is."""
-    if not _rows_ok(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis, cache,
-                    kv_lora_rank, rope_dim):
-        return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_at", check)
-    c = cache.c_struct()
-    rows, batch = latent.shape[0], input_row_offsets.shape[0] - 1
-    args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
-            int(kv_lora_rank), int(rope_dim), _ptr(kv_norm_gamma), float(epsilon),
-            _ptr(freqs_cis), freqs_cis.shape[0], ctypes.byref(c), int(layer_idx),
-            _ptr(dev_status))
-    f = _lib.mla_cache_write_paged_at
-    here = _here(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis, cache.data,
-                 cache.page_table, cache.cache_lengths)
-    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
-    return _check(code, "mla_cache_write_paged_at", check)
+    return _write_at(_lib.mla_cache_write_paged_at, "mla_cache_write_paged_at", latent,
+                     input_row_offsets, positions, kv_norm_gamma, epsilon, freqs_cis, cache,
+                     layer_idx, kv_lora_rank, rope_dim, (int(kv_lora_rank), int(rope_dim)),
+                     dev_status, stream, check)
 
 
 def mla_cache_write_paged_qcache_at(latent: torch.Tensor, input_row_offsets: torch.Tensor,
@@ -525,19 +522,9 @@ def mla_cache_write_paged_qcache_at(latent: torch.Tensor, input_row_offsets: tor
                                     layer_idx: int, dev_status: Optional[torch.Tensor] = None,
                                     stream=None, check: bool = True) -> int:
     """mla_cache_write_paged_qcache with row r rotated by freqs_cis[positions[r]]."""
-    if not _rows_ok(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis, cache,
-                    cache.kv_lora_rank, cache.rope_dim):
-        return _check(PKM_ERR_INVALID_ARG, "mla_cache_write_paged_qcache_at", check)
-    c = cache.c_struct()
-    rows, batch = latent.shape[0], input_row_offsets.shape[0] - 1
-    args = (_ptr(latent), _ptr(input_row_offsets), _ptr(positions), batch, rows,
-            _ptr(kv_norm_gamma), float(epsilon), _ptr(freqs_cis), int(freqs_cis.shape[0]),
-            ctypes.byref(c), int(layer_idx), _ptr(dev_status))
-    f = _lib.mla_cache_write_paged_qcache_at
-    here = _here(latent, input_row_offsets, positions, kv_norm_gamma, freqs_cis, cache.data,
-                 cache.page_table, cache.cache_lengths)
-    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
-    return _check(code, "mla_cache_write_paged_qcache_at", check)
+    return _write_at(_lib.mla_cache_write_paged_qcache_at, "mla_cache_write_paged_qcache_at", latent,
+                     input_row_offsets, positions, kv_norm_gamma, epsilon, freqs_cis, cache,
+                     layer_idx, cache.kv_lora_rank, cache.rope_dim, (), dev_status, stream, check)
 
 
 def mla_rope_heads(x: torch.Tensor, positions: torch.Tensor, freqs_cis: torch.Tensor,
@@ -547,18 +534,15 @@ def mla_rope_heads(x: torch.Tensor, positions: torch.Tensor, freqs_cis: torch.Te
     """Rotates x [rows, heads, P] into y [rows, heads, P] (bf16 views with contiguous last
     dimensions; y may be x) by the (cos, sin) pairs of freqs_cis[positions[row]]: pairs
     (2j, 2j + 1), or (j, j + P/2) with `half`."""
-    shape, sx, sy = x.shape, x.stride(), y.stride()
-    if y.shape != shape or len(shape) != 3 or sx[2] != 1 or sy[2] != 1 \
+    shape, sx, sy, table = x.shape, x.stride(), y.stride(), freqs_cis.shape
+    device, at = _look(((None, 0, x), (None, 0, y), (_WORD, 0, positions), (_FLOAT, 0, freqs_cis)))
+    if device is None or y.shape != shape or len(shape) != 3 or sx[2] != 1 or sy[2] != 1 \
             or x.dtype not in _BF16 or y.dtype not in _BF16 or positions.numel() != shape[0] \
-            or freqs_cis.shape[-1] != shape[2] or not _plain(_WORD, positions) \
-            or not _plain(_FLOAT, freqs_cis):
+            or table[-1] != shape[2]:
         return _check(PKM_ERR_INVALID_ARG, "mla_rope_heads", check)
-    args = (x.data_ptr(), sx[0], sx[1], _ptr(positions), shape[0], shape[1], shape[2],
-            freqs_cis.data_ptr(), freqs_cis.shape[0], 1 if half else 0, y.data_ptr(), sy[0],
-            sy[1], _ptr(dev_status))
-    f = _lib.mla_rope_heads
-    code = f(*args, _stream(stream)) if _here(x, positions, freqs_cis, y) else _refuse(f, *args)
-    return _check(code, "mla_rope_heads", check)
+    args = (at[0], sx[0], sx[1], at[2], shape[0], shape[1], shape[2], at[3], table[0],
+            1 if half else 0, at[1], sy[0], sy[1], _ptr(dev_status))
+    return _run(_lib.mla_rope_heads, "mla_rope_heads", args, device, stream, check)
 
 
 def mla_tree_attention_paged_workspace_size(total_rows: int, num_heads: int,
@@ -567,18 +551,27 @@ def mla_tree_attention_paged_workspace_size(total_rows: int, num_heads: int,
                                                             int(kv_lora_rank)))
 
 
-def _tree_shapes_ok(q, offsets, tree_mask, cache, out, lse, workspace, rank, rope) -> bool:
-    """Shapes that the C call cannot see; an empty mask would pass for no mask there."""
-    if q.ndim != 3:
-        return False
-    rows, heads, cols = q.shape
-    return (cols == rank + rope and out.shape == (rows, heads, rank) and
-            (lse is None or lse.shape == (rows, heads)) and
-            (tree_mask is None or (tree_mask.ndim == 2 and tree_mask.shape[0] == rows and
-                                   tree_mask.shape[1] > 0)) and
-            _cache_ok(cache, offsets.shape[0] - 1) and
-            _plain(_BF16, q, out) and _plain(_WORD, offsets, tree_mask) and
-            _plain(_FLOAT, lse) and workspace.is_contiguous())
+def _attention(f, where, q, offsets, scale, cache, layer_idx, rank, rope, widths, out, workspace,
+               mask, lse, dev_status, stream, check) -> int:
+    """Both attentions, with the shapes that the C call cannot see (an empty mask would pass for no
+    mask there), and a table row and a length for each request."""
+    table = cache.page_table
+    shape, pages, batch, words = q.shape, table.shape, offsets.shape[0] - 1, 0
+    device, at = _look(((_BF16, 0, q), (_WORD, 0, offsets), (_BF16, 0, out), (None, 0, workspace),
+                        (_WORD, 0, mask), (_FLOAT, 0, lse), (None, 0, cache.data), (_WORD, 0, table),
+                        (_WORD, batch, cache.cache_lengths)))
+    if mask is not None:
+        m = mask.shape
+        words = m[1] if len(m) == 2 and m[0] == shape[0] else 0
+    if device is None or len(shape) != 3 or shape[2] != rank + rope \
+            or out.shape != (shape[0], shape[1], rank) or not workspace.is_contiguous() \
+            or (lse is not None and lse.shape != shape[:2]) or (mask is not None and words == 0) \
+            or len(pages) != 2 or pages[0] < batch:
+        return _check(PKM_ERR_INVALID_ARG, where, check)
+    c = cache._struct_of((at[6], at[7], pages[1], at[8]))
+    args = (at[0], at[1], batch, shape[0], shape[1], *widths, float(scale), at[4], words,
+            ctypes.byref(c), int(layer_idx), at[2], at[5], at[3], workspace.nbytes, _ptr(dev_status))
+    return _run(f, where, args, device, stream, check)
 
 
 def mla_tree_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
@@ -592,20 +585,10 @@ def mla_tree_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
     cache: each over its request's cached tokens and those new ones that its tree_mask row
     (uint32/int32 [total_rows, words], one bit a token; None: the tokens up to itself) names.
     out [total_rows, heads, R] bf16, lse [total_rows, heads] fp32 or None."""
-    if not _tree_shapes_ok(q, input_row_offsets, tree_mask, cache, out, lse, workspace,
-                           kv_lora_rank, rope_dim):
-        return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged", check)
-    c = cache.c_struct()
-    rows, heads, _ = q.shape
-    args = (q.data_ptr(), input_row_offsets.data_ptr(), input_row_offsets.shape[0] - 1, rows,
-            heads, int(kv_lora_rank), int(rope_dim), float(softmax_scale), _ptr(tree_mask),
-            0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
-            out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes, _ptr(dev_status))
-    f = _lib.mla_tree_attention_paged
-    here = _here(q, input_row_offsets, tree_mask, out, lse, workspace, cache.data,
-                 cache.page_table, cache.cache_lengths)
-    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
-    return _check(code, "mla_tree_attention_paged", check)
+    return _attention(_lib.mla_tree_attention_paged, "mla_tree_attention_paged", q,
+                      input_row_offsets, softmax_scale, cache, layer_idx, kv_lora_rank, rope_dim,
+                      (int(kv_lora_rank), int(rope_dim)), out, workspace, tree_mask, lse,
+                      dev_status, stream, check)
 
 
 def mla_tree_attention_paged_qcache(q: torch.Tensor, input_row_offsets: torch.Tensor,
@@ -616,28 +599,26 @@ def mla_tree_attention_paged_qcache(q: torch.Tensor, input_row_offsets: torch.Te
                                     dev_status: Optional[torch.Tensor] = None, stream=None,
                                     check: bool = True) -> int:
     """mla_tree_attention_paged over a quantised cache."""
-    if not _tree_shapes_ok(q, input_row_offsets, tree_mask, cache, out, lse, workspace,
-                           cache.kv_lora_rank, cache.rope_dim):
-        return _check(PKM_ERR_INVALID_ARG, "mla_tree_attention_paged_qcache", check)
-    c = cache.c_struct()
-    rows, heads, _ = q.shape
-    args = (q.data_ptr(), input_row_offsets.data_ptr(), input_row_offsets.shape[0] - 1, rows,
-            heads, float(softmax_scale), _ptr(tree_mask),
-            0 if tree_mask is None else tree_mask.shape[1], ctypes.byref(c), int(layer_idx),
-            out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes, _ptr(dev_status))
-    f = _lib.mla_tree_attention_paged_qcache
-    here = _here(q, input_row_offsets, tree_mask, out, lse, workspace, cache.data,
-                 cache.page_table, cache.cache_lengths)
-    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
-    return _check(code, "mla_tree_attention_paged_qcache", check)
+    return _attention(_lib.mla_tree_attention_paged_qcache, "mla_tree_attention_paged_qcache", q,
+                      input_row_offsets, softmax_scale, cache, layer_idx, cache.kv_lora_rank,
+                      cache.rope_dim, (), out, workspace, tree_mask, lse, dev_status, stream, check)
 
 
-def _accepted_ok(shape, cache, accepted, counts, new_lengths) -> bool:
-    """A table row, length, count and new length for each list of accepted drafts (and maybe for
-    more)."""
-    return (len(shape) == 2 and _cache_ok(cache, shape[0]) and
-            _has(shape[0], counts) and _has(shape[0], new_lengths) and
-            _plain(_WORD, accepted, counts, new_lengths))
+def _compact(f, where, cache, layer_begin, layer_count, accepted, counts, new_lengths, dev_status,
+             stream, check) -> int:
+    """Both compactions: a table row, length, count and new length for each list of accepted drafts
+    (and maybe for more)."""
+    table = cache.page_table
+    shape, pages = accepted.shape, table.shape
+    n = shape[0]
+    device, at = _look(((_WORD, 0, accepted), (_WORD, n, counts), (_WORD, n, new_lengths),
+                        (None, 0, cache.data), (_WORD, 0, table), (_WORD, n, cache.cache_lengths)))
+    if device is None or len(shape) != 2 or len(pages) != 2 or pages[0] < n:
+        return _check(PKM_ERR_INVALID_ARG, where, check)
+    c = cache._struct_of((at[3], at[4], pages[1], at[5]))
+    args = (ctypes.byref(c), layer_begin, layer_count, n, at[0], shape[1], at[1], at[2],
+            _ptr(dev_status))
+    return _run(f, where, args, device, stream, check)
 
 
 def mla_cache_compact_paged(cache: PagedCache, layer_begin: int, layer_count: int,
@@ -649,17 +630,8 @@ def mla_cache_compact_paged(cache: PagedCache, layer_begin: int, layer_count: in
     indices behind cache_lengths[b]) to the front of its drafted region in every layer of the
     range, and writes the grown lengths to new_lengths (memory of its own, which none of the
     other arguments has)."""
-    shape = accepted.shape
-    if not _accepted_ok(shape, cache, accepted, accepted_counts, new_lengths):
-        return _check(PKM_ERR_INVALID_ARG, "mla_cache_compact_paged", check)
-    c = cache.c_struct()
-    args = (ctypes.byref(c), layer_begin, layer_count, shape[0], accepted.data_ptr(), shape[1],
-            _ptr(accepted_counts), _ptr(new_lengths), _ptr(dev_status))
-    f = _lib.mla_cache_compact_paged
-    here = _here(accepted, accepted_counts, new_lengths, cache.data, cache.page_table,
-                 cache.cache_lengths)
-    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
-    return _check(code, "mla_cache_compact_paged", check)
+    return _compact(_lib.mla_cache_compact_paged, "mla_cache_compact_paged", cache, layer_begin,
+                    layer_count, accepted, accepted_counts, new_lengths, dev_status, stream, check)
 
 
 def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_count: int,
@@ -668,17 +640,9 @@ def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_co
                                    dev_status: Optional[torch.Tensor] = None, stream=None,
                                    check: bool = True) -> int:
     """mla_cache_compact_paged for a quantised cache."""
-    shape = accepted.shape
-    if not _accepted_ok(shape, cache, accepted, accepted_counts, new_lengths):
-        return _check(PKM_ERR_INVALID_ARG, "mla_cache_compact_paged_qcache", check)
-    c = cache.c_struct()
-    args = (ctypes.byref(c), layer_begin, layer_count, shape[0], accepted.data_ptr(), shape[1],
-            _ptr(accepted_counts), _ptr(new_lengths), _ptr(dev_status))
-    f = _lib.mla_cache_compact_paged_qcache
-    here = _here(accepted, accepted_counts, new_lengths, cache.data, cache.page_table,
-                 cache.cache_lengths)
-    code = f(*args, _stream(stream)) if here else _refuse(f, *args)
-    return _check(code, "mla_cache_compact_paged_qcache", check)
+    return _compact(_lib.mla_cache_compact_paged_qcache, "mla_cache_compact_paged_qcache", cache,
+                    layer_begin, layer_count, accepted, accepted_counts, new_lengths, dev_status,
+                    stream, check)
 
 
 def kv_matmul_paged_fp8_workspace_size(total_rows: int, k_in: int) -> int:

@@ -16,7 +16,7 @@ def pkm(monkeypatch):
     import __graft_entry__
     __graft_entry__.build()
     import paged_kv_mla_gb300 as m
-    monkeypatch.setattr(m, "_here", lambda *tensors: True)
+    monkeypatch.setattr(m, "_here", lambda device: True)
     m._lib.pkm_checks_only(1)
     yield m
     m._lib.pkm_checks_only(0)
@@ -125,10 +125,29 @@ def test_descriptors_of_fewer_requests(pkm, call, make):
 @CALLS
 @MAKES
 def test_descriptors_in_other_memory(pkm, monkeypatch, call, make, field):
-    cache = make(pkm)
-    there = getattr(cache, field)
-    monkeypatch.setattr(pkm, "_here", lambda *tensors: all(t is not there for t in tensors))
-    assert call(pkm, cache) == INVALID
+    """A descriptor's tensor on another device than the rest."""
+    real, devices, cache = pkm._look, [], make(pkm)
+
+    class There:  # stands for the field's tensor
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
+            return 1
+
+    def look(tensors):
+        found = real(tuple((*k, There(t) if t is getattr(cache, field) else t) for *k, t in tensors))
+        devices.append(found[0])
+        return found
+
+    monkeypatch.setattr(pkm, "_look", look)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    monkeypatch.setattr(pkm, "_here", lambda device: device == 0)
+    pkm._lib.pkm_checks_only(0)
+    assert call(pkm, cache) == INVALID and devices == [-1]
 
 
 @MAKES

@@ -23,7 +23,7 @@ def pkm():
 def state(request, pkm, monkeypatch):
     """CUDA as the process has it, and as after the first use of a device 0."""
     if request.param == "initialised":
-        monkeypatch.setattr(pkm, "_initialized", lambda: True)
+        monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
         monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     return request.param
 
@@ -55,20 +55,12 @@ def test_host_memory_is_refused(pkm, state, name):
 @pytest.mark.parametrize("name", NAMES)
 def test_nothing_else_is_wrong_with_them(pkm, monkeypatch, name):
     """The control: but for the memory the calls would go on to the GPU."""
-    seen = []
-    refuse = pkm._refuse
-
-    def look(f, *args):
-        pkm._lib.pkm_checks_only(1)
-        try:
-            seen.append(f(*args, None))
-        finally:
-            pkm._lib.pkm_checks_only(0)
-        return refuse(f, *args)
-
-    monkeypatch.setattr(pkm, "_refuse", look)
-    calls(pkm)[name]()
-    assert seen == [pkm.PKM_ERR_CUDA]
+    monkeypatch.setattr(pkm, "_here", lambda device: True)
+    pkm._lib.pkm_checks_only(1)
+    try:
+        assert calls(pkm)[name]() == pkm.PKM_ERR_CUDA
+    finally:
+        pkm._lib.pkm_checks_only(0)
 
 
 def test_other_findings_come_first(pkm, state):
