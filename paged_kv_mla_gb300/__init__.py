@@ -538,7 +538,7 @@ def mla_rope_heads(x: torch.Tensor, positions: torch.Tensor, freqs_cis: torch.Te
     device, at = _look(((None, 0, x), (None, 0, y), (_WORD, 0, positions), (_FLOAT, 0, freqs_cis)))
     if device is None or y.shape != shape or len(shape) != 3 or sx[2] != 1 or sy[2] != 1 \
             or x.dtype not in _BF16 or y.dtype not in _BF16 or positions.numel() != shape[0] \
-            or table[-1] != shape[2]:
+            or len(table) != 2 or table[1] != shape[2]:
         return _check(PKM_ERR_INVALID_ARG, "mla_rope_heads", check)
     args = (at[0], sx[0], sx[1], at[2], shape[0], shape[1], shape[2], at[3], table[0],
             1 if half else 0, at[1], sy[0], sy[1], _ptr(dev_status))

@@ -228,3 +228,15 @@ def test_rows_without_rope_columns(pkm):
     for freqs in (torch.zeros(8, 0), torch.zeros(8, 64), torch.zeros(8)):
         assert pkm.mla_cache_write_paged_at(b16(3, 512), i32(3), i32(3), torch.ones(512), 1e-6, freqs,
                                             cache, 0, 512, 0, stream=0, check=False) == GOES_ON
+
+
+def test_rope_table_has_a_row_a_position(pkm):
+    """Of a table in another form the rows that there are would be counted wrongly."""
+    x = b16(3, 4, 16)
+
+    def call(f):
+        return pkm.mla_rope_heads(x, i32(3), f, b16(3, 4, 16), stream=0, check=False)
+
+    assert call(torch.zeros(4, 16)) == GOES_ON
+    for f in (torch.zeros(16), torch.zeros(4, 2, 16), torch.zeros(4, 8, 2), torch.zeros(4, 32)):
+        assert call(f) == INVALID
