@@ -367,6 +367,9 @@ pkm_status mla_cache_write_paged_qcache_at(const void* latent,
  * Only those columns of y are written, so x can point into the query projection's output
  * [rows, heads, nope + P] and y into the attention's query [rows, heads, R + P].  A table
  * stretched for long contexts, its values scaled or not, is passed like any other.
+ * The cache writes turn the keys in pairs (2j, 2j+1).  With half = 1 the keys are turned by this
+ * call too, the latent rows' last P columns being the one head of x and y, and then written with
+ * factors (1, 0), which leave them as they are.
  *
  *   x               device bf16, 16-byte aligned, the first rope column of row 0, head 0.
  *   x_*_stride      elements, multiples of 8 (>= 0; 0 broadcasts).
