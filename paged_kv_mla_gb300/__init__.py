@@ -489,7 +489,7 @@ def _write_at(f, where, latent, offsets, positions, gamma, epsilon, freqs, cache
     norm, P of a position (any for a P of 0), and a table row and a length for each request."""
     table = cache.page_table
     shape, factors, pages, batch = latent.shape, freqs.shape, table.shape, offsets.shape[0] - 1
-    device, at = _look(((_BF16, 0, latent), (_WORD, 0, offsets), (_WORD, shape[0], positions),
+    device, at = _look(((_BF16, 0, latent), (_WORD, 0, offsets), (_WORD, shape[0] if shape else 0, positions),
                         (_FLOAT, rank, gamma), (_FLOAT, 0, freqs), (None, 0, cache.data),
                         (_WORD, 0, table), (_WORD, batch, cache.cache_lengths)))
     if device is None or len(shape) != 2 or shape[1] != rank + rope \
@@ -533,7 +533,9 @@ def mla_rope_heads(x: torch.Tensor, positions: torch.Tensor, freqs_cis: torch.Te
                    check: bool = True) -> int:
     """Rotates x [rows, heads, P] into y [rows, heads, P] (bf16 views with contiguous last
     dimensions; y may be x) by the (cos, sin) pairs of freqs_cis[positions[row]]: pairs
-    (2j, 2j + 1), or (j, j + P/2) with `half`."""
+    (2j, 2j + 1), or (j, j + P/2) with `half`.  The cache writes turn keys in pairs (2j, 2j + 1);
+    for queries in the half layout, turn the keys with this call too (x and y the rope columns of
+    the latent rows, one head) and write them with factors (1, 0)."""
     shape, sx, sy, table = x.shape, x.stride(), y.stride(), freqs_cis.shape
     device, at = _look(((None, 0, x), (None, 0, y), (_WORD, 0, positions), (_FLOAT, 0, freqs_cis)))
     if device is None or y.shape != shape or len(shape) != 3 or sx[2] != 1 or sy[2] != 1 \
@@ -562,7 +564,7 @@ def _attention(f, where, q, offsets, scale, cache, layer_idx, rank, rope, widths
                         (_WORD, batch, cache.cache_lengths)))
     if mask is not None:
         m = mask.shape
-        words = m[1] if len(m) == 2 and m[0] == shape[0] else 0
+        words = m[1] if len(m) == 2 and m[:1] == shape[:1] else 0
     if device is None or len(shape) != 3 or shape[2] != rank + rope \
             or out.shape != (shape[0], shape[1], rank) or not workspace.is_contiguous() \
             or (lse is not None and lse.shape != shape[:2]) or (mask is not None and words == 0) \
@@ -610,7 +612,7 @@ def _compact(f, where, cache, layer_begin, layer_count, accepted, counts, new_le
     (and maybe for more)."""
     table = cache.page_table
     shape, pages = accepted.shape, table.shape
-    n = shape[0]
+    n = shape[0] if shape else 0
     device, at = _look(((_WORD, 0, accepted), (_WORD, n, counts), (_WORD, n, new_lengths),
                         (None, 0, cache.data), (_WORD, 0, table), (_WORD, n, cache.cache_lengths)))
     if device is None or len(shape) != 2 or len(pages) != 2 or pages[0] < n:

@@ -240,3 +240,12 @@ def test_rope_table_has_a_row_a_position(pkm):
     assert call(torch.zeros(4, 16)) == GOES_ON
     for f in (torch.zeros(16), torch.zeros(4, 2, 16), torch.zeros(4, 8, 2), torch.zeros(4, 32)):
         assert call(f) == INVALID
+
+
+@MAKES
+def test_tensors_without_dimensions(pkm, make):
+    """Refused like other shapes, not by an error of the binding."""
+    none = torch.zeros((), dtype=torch.int32)
+    assert compact(pkm, make(pkm), none, i32(2), i32(2)) == INVALID
+    assert write(pkm, make(pkm), latent=torch.zeros((), dtype=torch.int16)) == INVALID
+    assert attend(pkm, make(pkm), q=torch.zeros((), dtype=torch.int16), mask=i32(3, 1)) == INVALID
