@@ -23,8 +23,8 @@
 // (fp32 arithmetic, rounded to bf16) straight into their slots with 16-byte stores.
 // Nothing else in the cache is written.  The tokens of a drafted tree take their rotary
 // positions (length + depth) from an array instead: siblings share one, while their slots
-// stay consecutive.  256 trees of 48-64 tokens (14 336 rows) take 15.6 us from cold inputs, 37 MB
-// at 2.4 TB/s: three chunks a CTA, bound by the latencies of their start (request, page id,
+// stay consecutive.  256 trees of 48-64 tokens (14 336 rows) take 15 to 16 us from cold inputs,
+// 37 MB at 2.3 TB/s: three chunks a CTA, bound by the latencies of their start (request, page id,
 // factors, rows); a few trees are a launch.
 //
 // Into a quantised cache (PagedKVCacheCollection's scale_dtype_ / quantization_granularity_)

@@ -13,8 +13,8 @@
 // head; its kUnroll heads are loaded before the first is stored, so that their latencies
 // overlap, and before the row's position, on which only the factors wait.
 //
-// Measured (4096 rows x 128 heads x 64 columns out of 192): 25.0 us with the launch, 5.4 TB/s
-// (0.81 of a plain copy), 21 us under the profiler; position first 28.7 us, then blocks of 256
+// Measured (4096 rows x 128 heads x 64 columns out of 192): 25.4 us with the launch, 5.3 TB/s
+// (0.80 of a plain copy), 21 us under the profiler; position first 28.7 us, then blocks of 256
 // threads 26.7, of 64 25.7; 2 heads in flight 28.4, 8 (blocks of 256) 32.8 us.  A few rows, as
 // of a drafted tree, are a launch (7 us).
 #include "pkm_device.cuh"

@@ -38,14 +38,17 @@
 //
 // Measured (R = 512, P = 64, 128 heads, L2 cold; floor = bytes or operations at the rates of a
 // plain copy and a large library product):
-//   16 trees of 16-64 tokens, histories of 512-4096: 318 us, 1.34 PFLOP/s (0.70).  A tile takes
-//     2600 cycles, of which its MMAs 2176; each CTA's 136 KB a tile are then 50 bytes a cycle
-//     out of L2, which bounds it.  An item's start and end take 5 us more.
+//   16 trees of 16-64 tokens, histories of 512-4096: 319 us, 1.33 PFLOP/s (0.70).  The tensor
+//     cores are at work for 65 % of the attention's 291 us: a tile takes 2600 cycles, of which its
+//     MMAs 2176, and an item's start and end 5 us more, eight times a pair.  L2 gives 13 TB/s, 52 %
+//     of what its counters allow.  The join takes 14 us when nothing overlaps it.
 //   64 users x 1 token, histories of 512-4096, pages of 128: 55.5 us, floor 28 us (3.3 TB/s).  1.5
 //     items a pair: 10 us to start, 15 us of items' starts and ends, 8 us to join.
-//   4 users x 1 token, histories of 32768: 44.6 us, floor 23 us (3.4 TB/s), likewise.
-//   32 chains of 1-4 tokens over the quantised cache: 105 us, floor 26 us.  Rows brought by loads
-//     are bound by the instructions that convert them: 3 us a tile.
+//   4 users x 1 token, histories of 32768: 44.8 us, floor 23 us (3.4 TB/s), likewise.
+//   32 chains of 1-4 tokens over the quantised cache: 106 us, floor 26 us.  Rows brought by loads
+//     are bound by the instructions that convert them: 3 us a tile, and a tile's rows are converted
+//     2.6 times, once for each item of the request and half of them again for the other CTA.
+// The comments at single choices below say what the other side cost when the choice was made.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -66,8 +69,8 @@ constexpr int kThreads = 20 * 32;
 // the 5 x 96 that the block starts with: by loads the rows on their way need more.
 constexpr int kIssueRegs = 64, kMoreRegs = 112;
 // An item's start and end, in tiles: 5 us against 1.4 us of a tile by TMA and 3 us of one by loads
-// (large drafted trees with 2: 342 instead of 331 us, ragged ones with 6: 36.7 instead of 34.7; chains
-// over the quantised cache with 2: 107.6 instead of 104.9, with 3: 109.5).
+// (large drafted trees with 2: 3 % longer, ragged ones with 6: 6 %; chains over the quantised cache
+// with 2: 3 %, with 3: 4 %).
 constexpr int item_cost(Source src) { return src == kTma ? 4 : 1; }
 constexpr int kKeys = 128;          // keys of a tile (64 loaded by each CTA as keys)
 constexpr int kBlocks = 9;          // 64-column blocks of a latent row
@@ -433,10 +436,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 // is, finds its page and loads its scale.  When a set is stored the next one is asked for.
 //
 // One copy of the code serves all warps and both sets, with few branches: the warps wait for
-// instructions more than for loads.  For 32 chains over the quantised cache (now 105 us) a form in
-// which four warps brought all keys and four all values, which converts 1.9 times as much, took
-// 182 us; with a scale of its own for every piece and 64 columns of a row at a time 134 instead of
-// 119; sixteen warps, or a second set of registers for the rows on their way, changed nothing.
+// instructions more than for loads.  For 32 chains over the quantised cache a form in which four
+// warps brought all keys and four all values, which converts 1.9 times as much, took half as long
+// again; a scale of its own for every piece and 64 columns of a row at a time 13 % more; sixteen
+// warps, or a second set of registers for the rows on their way, changed nothing.
 template <Source SRC, typename Queries>
 __device__ __forceinline__ void by_loads(const TreeAttentionArgs& a, Bars* bars, uint8_t* smem,
                                          uint32_t rank, int i, int kblocks, int vgroups,
@@ -683,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------- softmax and epilogue: row = lane of the CTA's 64 ----------------
         // Warps w and w + 4 share 32 lanes; lanes 0-63 have the first 64 keys (and half of O's
         // columns), and each of the two warps takes 32 of the keys (half of the lanes' columns).
-        // With one warp for both large drafted trees took 345 us instead of 332.
+        // With one warp for both large drafted trees took 4 % longer.
         if constexpr (SRC == kTma) warpgroup_reg_alloc<kMoreRegs>();
         Walk w(bars);
         const int half = warp >> 1 & 1, part = warp >> 2;
@@ -754,6 +757,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float back = move && m > -INFINITY ? exp2_approx(m - m_new) : move ? 0.0f : 1.0f;
                 m = m_new;
                 const float ref = m == -INFINITY ? 0.0f : m;
+                // The weights are rounded to bf16, by up to 2^-8 of each: the second product's
+                // operands have one type, and the values are bf16.  Their sum stays in fp32, unrounded.
+                // (Outputs are 2.1e-3 of their size from 64 bits; with weights in fp32 1.7e-3, which
+                // is the rounding of the outputs themselves.)
                 float sum0 = 0.0f, sum1 = 0.0f;
                 uint32_t p[16];
 #pragma unroll
@@ -818,8 +825,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (whole) {
                 const float inv = l != 0.0f ? 1.0f / l : 0.0f;
                 // A lane stores whole sectors of its row where the output allows: as fast as
-                // through shared memory by TMA (339 us either way for large drafted trees), and
-                // faster than whole lines from there by the lanes (345 us).
+                // through shared memory by TMA, and 2 % less for large drafted trees than whole
+                // lines from there by the lanes.
                 for (int c = 2 * v0; c < 2 * v1; ++c) {  // 32 columns
                     const int col = value_block(half, c >> 1) * 64 + (c & 1) * 32;
                     if (col >= R) break;
@@ -1005,9 +1012,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Asks for keys to be brought into L2 ahead of their loads, which are issued when their
         // shared memory is free, too late to wait for DRAM: for wide boxes as soon as the keys of
         // the tile before are asked for, for other loads, which take longer, two tiles earlier.
-        // (64 users x 1 token, wide boxes: 55.8 us, two tiles earlier 60.4, never 59.0; ragged trees
-        // in small pages 36.0, 34.9, 37.7; chains over the quantised cache 113 and 105.)  With wide
-        // boxes a request's first item alone asks: large drafted trees 315 instead of 323 us.
+        // (64 users x 1 token, wide boxes: two tiles earlier 8 % longer, never 6 %; ragged trees in
+        // small pages: one tile ahead 3 % longer, never 8 %; chains over the quantised cache: one
+        // tile ahead 7 %.)  With wide boxes a request's first item alone asks: with all of them
+        // large drafted trees took 2 % longer.
         const int ahead = SRC == kTma && tb.key_blocks > 1 ? 0 : 2;
         Walk w(bars);
         volatile int32_t* progress = &bars->progress;
@@ -1072,7 +1080,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // and the value warp i, two blocks each.  The key warp asks for them to be brought into L2
         // and loads them behind its first tile: loads before would make the keys' page ids wait
         // for them (they share the few scoreboards).  The value warp loads its own before the
-        // values (ragged trees 35.1 us, behind the first tile's 36.8, all by the key warp 36.7).
+        // values (ragged trees: behind the first tile's, or all by the key warp, 5 % longer).
         constexpr int kAtOnce = SRC == kTma ? 2 : 1;  // blocks in flight
         const int first_kb = keys ? 0 : kQueryBlocks / 2, last_kb = first_kb + kQueryBlocks / 2;
         const auto fetch = [&](const Walk& w, int kb, uint32_t(&x)[kAtOnce][32]) {
@@ -1247,7 +1255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
 // Blocks of an SM, all of them resident when the attention ends: with three the registers for a
-// row's columns spilled (one user 14.2 us instead of 13.2), with four more had to wait for the first.
+// row's columns spilled (one user 1 us longer), with four more had to wait for the first.
 constexpr int kJoinBlocks = 2;
 constexpr int kFewParts = 8;  // that a warp joins alone (4 and 16: the same)
 
@@ -1453,9 +1461,9 @@ cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm
     const TreeWorkspace ws = tree_workspace(args.total_rows, args.num_heads, args.kv_lora_rank);
     const int pairs = num_sms / 2 < kTreeMaxPairs ? num_sms / 2 : kTreeMaxPairs;
     // Boxes of at least 8 slots are whole swizzle atoms; smaller ones come by loads (pages of 128 that
-    // way: 64 users x 1 token 100 instead of 61 us, large drafted trees 743 instead of 325).  With a
-    // rank of 512 no rope columns lie in the sets of four blocks, whose code then has no branches
-    // (with them chains over the quantised cache take 141 instead of 107 us).
+    // way: 64 users x 1 token 1.6 times as long, large drafted trees 2.3 times).  With a rank of 512
+    // no rope columns lie in the sets of four blocks, whose code then has no branches (with them
+    // chains over the quantised cache take 1.3 times as long).
     const cudaError_t e =
         args.qcache_layer != nullptr
             ? (args.kv_lora_rank == 512 ? launch_source<kCodes> : launch_source<kCodesNarrow>)(
