@@ -483,9 +483,9 @@ pkm_status mla_tree_attention_paged_qcache(const void* q, const uint32_t* input_
  *   new_lengths      device uint32 [batch], or NULL; without memory in common with
  *                    cache->cache_lengths, cache->page_table, accepted or accepted_counts
  *                    (PKM_ERR_INVALID_ARG otherwise).
- *   cache            row_elems a multiple of 8; cache_lengths required.  The rows of a page, of
- *                    the layers of the range and of both planes may not overlap
- *                    (PKM_ERR_INVALID_ARG).
+ *   cache            row_elems a multiple of 8; cache_lengths required.  Its rows may not
+ *                    overlap (PKM_ERR_INVALID_ARG where the strides of slots, of the range's
+ *                    layers or of the planes show it).
  * A request whose count exceeds max_accepted or whose drafts do not increase sets
  * PKM_ERR_INVALID_ARG in dev_status, one with a position outside the page table or the cache
  * PKM_ERR_OUT_OF_RANGE; such a request moves nothing and keeps its length.

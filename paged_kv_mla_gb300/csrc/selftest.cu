@@ -14,17 +14,18 @@ constexpr int kForms = 3;  // mbar_wait, which keeps time; mbar_wait_flag; that 
 __global__ void wait_timeout_kernel(int32_t* status, uint64_t timeout_ns) {
     __shared__ uint64_t bar;
     __shared__ int abort_flag, found, good;
+    __shared__ uint64_t t0;  // before every warp's wait
     const int form = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
         abort_flag = found = good = 0;
         fence_mbar_init();
+        t0 = globaltimer_ns();
     }
     __syncthreads();
     // no thread ever arrives on `bar`: phase 0 never completes
     const WaitCtl wc{&abort_flag, &found, timeout_ns};
     const uint32_t tries = static_cast<uint32_t>(min(timeout_ns / 8, uint64_t{UINT32_MAX}));
-    const uint64_t t0 = globaltimer_ns();
     bool ok = false;
     if (form == 0) {
         if (lane == 0) ok = mbar_wait(&bar, 0, wc);
