@@ -985,9 +985,11 @@ pkm_status tree_attention(TreeAttentionArgs a, const void* q, const uint32_t* in
     while (vbox > 1 && a.page_size % vbox != 0) vbox /= 2;
     const int box = vbox < 64 ? vbox : 64;
     // loads keep a row as a 32-bit count of 16-byte units inside the layer
-    const int64_t span = a.num_pages * a.page_stride + a.page_size * a.slot_stride;
-    if ((a.qcache_layer != nullptr && span / 16 >= UINT32_MAX - 1) ||
-        (a.qcache_layer == nullptr && box < 8 && span / 8 >= UINT32_MAX - 1))
+    const int64_t limit = (UINT32_MAX - int64_t{1}) * (a.qcache_layer != nullptr ? 16 : 8);
+    const auto fits = [&](int64_t n, int64_t stride) { return stride == 0 || n <= limit / stride; };
+    if ((a.qcache_layer != nullptr || box < 8) &&
+        (!fits(a.num_pages, a.page_stride) || !fits(a.page_size, a.slot_stride) ||
+         a.num_pages * a.page_stride + a.page_size * a.slot_stride >= limit))
         return PKM_ERR_UNSUPPORTED;
     int sms = 0;
     if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);

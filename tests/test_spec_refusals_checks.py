@@ -249,3 +249,21 @@ def test_tensors_without_dimensions(pkm, make):
     assert compact(pkm, make(pkm), none, i32(2), i32(2)) == INVALID
     assert write(pkm, make(pkm), latent=torch.zeros((), dtype=torch.int16)) == INVALID
     assert attend(pkm, make(pkm), q=torch.zeros((), dtype=torch.int16), mask=i32(3, 1)) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(num_pages=2 ** 31 - 1, page_stride=1 << 33),
+                                dict(num_pages=1 << 30, page_stride=1 << 35),
+                                dict(page_size=(1 << 30) + 4, slot_stride=1 << 34)])
+def test_layers_whose_length_passes_64_bits(pkm, kw):
+    """Rows brought by loads count 16-byte units in 32 bits; the product must not wrap to fewer."""
+    assert attend(pkm, paged(pkm, **{"page_size": 12, **kw})) == UNSUPPORTED
+    assert attend(pkm, quant(pkm, **kw)) == UNSUPPORTED
+
+
+def test_longest_layer_for_loads(pkm):
+    units = 2 ** 32 - 2
+    for make, unit, slot in ((paged, 8, 576), (quant, 16, 656)):
+        for over, status in ((0, UNSUPPORTED), (1, GOES_ON)):
+            cache = make(pkm, page_size=12, num_pages=1,
+                         page_stride=units * unit - 12 * slot - over * unit)
+            assert attend(pkm, cache) == status
