@@ -38,7 +38,7 @@
 //
 // Measured (R = 512, P = 64, 128 heads, L2 cold; floor = bytes or operations at the rates of a
 // plain copy and a large library product):
-//   16 trees of 16-64 tokens, histories of 512-4096: 319 us, 1.33 PFLOP/s (0.70).  The tensor
+//   16 trees of 16-64 tokens, histories of 512-4096: 319 to 324 us, 1.32 PFLOP/s (0.69).  The tensor
 //     cores are at work for 65 % of the attention's 291 us: a tile takes 2600 cycles, of which its
 //     MMAs 2176, and an item's start and end 5 us more, eight times a pair.  L2 gives 13 TB/s, 52 %
 //     of what its counters allow.  The join takes 14 us when nothing overlaps it.
@@ -46,8 +46,8 @@
 //     items a pair: 10 us to start, 15 us of items' starts and ends, 8 us to join.
 //   4 users x 1 token, histories of 32768: 44.8 us, floor 23 us (3.4 TB/s), likewise.
 //   32 chains of 1-4 tokens over the quantised cache: 106 us, floor 26 us.  Rows brought by loads
-//     are bound by the instructions that convert them: 3 us a tile, and a tile's rows are converted
-//     2.6 times, once for each item of the request and half of them again for the other CTA.
+//     are bound by the instructions that convert them: 3 us a tile.  A request's rows are converted
+//     for each of its items, 2.6 times here, and half of the values once more for the other CTA.
 // The comments at single choices below say what the other side cost when the choice was made.
 #include <cuda_fp16.h>
 
