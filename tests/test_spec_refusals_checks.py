@@ -1,5 +1,5 @@
 """Arguments of the speculative-decoding entry points that read or write the wrong memory: each
-refused by the calls' own checks, whose other verdict is that the call would go on to the GPU."""
+refused by the calls' own checks, which otherwise say that the call would go on to the GPU."""
 from __future__ import annotations
 
 import pytest
