@@ -29,6 +29,9 @@
  *                               Args): Y = hidden_state . weight on the ragged rows, with
  *                               row i of request b written into the paged K/V cache at
  *                               position cache_lengths[b] + i (bf16, or FP8 block-scaled).
+ *   kv_rope_paged               rotary positions on several axes for new queries and keys, and
+ *                               keys and values stored into that cache.
+ *   kv[_window]_attention_paged attention of new tokens (a chunk, or one) over that cache.
  *
  * Conventions shared by every entry point
  *   - Every tensor argument is DEVICE memory on the current CUDA device, allocated and
@@ -91,7 +94,7 @@ typedef enum {
  *   cache_lengths     device uint32 [batch]: tokens already in the cache per request.  Read
  *                     by every entry point but the decompress ones (and never updated);
  *                     may be NULL for the decompress entry points.
- *   kv_stride         offset of the V plane from the K plane; kv_matmul_paged, and
+ *   kv_stride         offset of the V plane from the K plane; the kv_ calls, and
  *                     mla_cache_compact_paged (0: the cache has one plane).
  */
 typedef struct {
@@ -658,9 +661,126 @@ pkm_status kv_matmul_paged_fp8(const void* hidden_state, const uint32_t* input_r
                                void* stream);
 
 /*
+ * Rotary positions of new queries and keys, and the write of keys and values into the paged
+ * K/V cache.
+ * Source: kv_matmul_ragged_paged (the cache, rows and positions; its keys carry no position) and
+ * mla_prefill_decode_graph_fp8 -- Args freqs_cis.  The pages have one position a token; images
+ * and videos give it one on each axis (time, height, width), text the same on all.
+ *
+ * Row r = input_row_offsets[b] + i (r < total_rows) is request b's new token i, at cache position
+ * cache_lengths[b] + i.  With P = rope_dim, D = head_size and, for pair j < P/2, the factors
+ *     (c_j, s_j) = freqs_cis[positions[pair_axes[j], r], 2j .. 2j+1]
+ * a head's columns x turn into y:
+ *     half = 0: (y[2j], y[2j+1])   = (x[2j] c_j - x[2j+1] s_j, x[2j] s_j + x[2j+1] c_j)
+ *     half = 1: (y[j], y[j+P/2])   = (x[j] c_j - x[j+P/2] s_j, x[j] s_j + x[j+P/2] c_j)
+ *     y[c] = x[c],  P <= c < D
+ * (fp32 arithmetic, one rounding to bf16), and then
+ *     q_out[r, h]                          = y of q[r, h],           h < num_heads
+ *     K plane slot of the position, head h = y of k[r, h],           h < num_kv_heads
+ *     V plane slot of the position, head h = v[r, h], bit for bit    (v != NULL)
+ * Without k (NULL) the keys are in the cache already, as kv_matmul_paged leaves them, and turn
+ * in place.  No other element is written.  A slot belongs to one row of the call.
+ *
+ *   q, k, v          device bf16, 16-byte aligned; element (row, head, column) at
+ *                    row * row_stride + head * head_stride + column, strides in elements,
+ *                    multiples of 8 (>= 0): heads of one projection's output can be given.
+ *   num_heads        query heads; 0 (with q = NULL) turns keys alone.
+ *   q_out            device bf16, 16-byte aligned, strides for which no two heads overlap.  It may
+ *                    be q with the same strides (in place), and may not overlap it otherwise.
+ *   head_size        D: a multiple of 8, at most 256; row_elems = num_kv_heads * D.
+ *   rope_dim         P: a multiple of 8, at most D.
+ *   positions        device uint32 [num_axes, total_rows].  A row with an entry >= max_seq_len on
+ *                    any axis sets PKM_ERR_OUT_OF_RANGE in dev_status and is not written.
+ *   num_axes         1 to 4.
+ *   pair_axes        HOST array [P/2] of axes, below num_axes, read during the call; NULL: axis 0.
+ *   freqs_cis        device fp32 [max_seq_len, P], 16-byte aligned, a (cos, sin) pair a pair.
+ *   kv_cache         cache_lengths required; kv_stride >= row_elems.  Keys and values of a page's
+ *                    slots may not overlap (PKM_ERR_INVALID_ARG where the strides show it).
+ * A position outside the page table or the cache sets PKM_ERR_OUT_OF_RANGE; that row's key and
+ * value are not written.
+ */
+pkm_status kv_rope_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                         int32_t num_heads, void* q_out, int64_t q_out_row_stride,
+                         int64_t q_out_head_stride, const void* k, int64_t k_row_stride,
+                         int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                         int64_t v_head_stride, int32_t num_kv_heads, int32_t head_size,
+                         int32_t rope_dim, const uint32_t* input_row_offsets, int32_t batch,
+                         int32_t total_rows, const uint32_t* positions, int32_t num_axes,
+                         const uint8_t* pair_axes, const float* freqs_cis, int32_t max_seq_len,
+                         int32_t half, const pkm_paged_cache* kv_cache, uint32_t layer_idx,
+                         int32_t* dev_status, void* stream);
+
+/*
+ * Bytes of device workspace kv_attention_paged and kv_window_attention_paged need (0 for invalid
+ * sizes).  Its contents need not be kept or cleared between calls, but calls that may overlap
+ * need one each.
+ */
+size_t kv_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
+                                         int32_t num_kv_heads, int32_t head_size);
+
+/*
+ * Attention of new tokens -- a chunk of a prompt, or one token a request -- over the paged K/V
+ * cache, heads in groups that share keys and values.
+ * Source: kv_matmul_ragged_paged (the cache, its rows and positions); the pages attend only in
+ * the MLA graph, whose Args input_row_offsets, kv_collection, layer_idx and Parameter scale these are.
+ *
+ * Request b has n_b = input_row_offsets[b+1] - input_row_offsets[b] new tokens, whose keys and
+ * values are in the cache already, at positions cache_lengths[b] + i.  For its token i, with
+ * r = input_row_offsets[b] + i (skipped when r >= total_rows), p = cache_lengths[b] + i, head h
+ * and its head of keys g = h / (num_heads / num_kv_heads), over the positions t <= p
+ *     w_t = softmax_t(softmax_scale * sum_c q[r, h, c] * K(t)[g, c])
+ *     out[r, h, c] = bf16( sum_t w_t * V(t)[g, c] )
+ *     lse[r, h]    = log sum_t exp(softmax_scale * sum_c q[r, h, c] * K(t)[g, c])
+ * What a token does not attend has no influence on it, whatever it holds (NaN and infinities
+ * included).  Rows that no request covers are left untouched.  Scores and sums are fp32; the
+ * weights are rounded to bf16 for the second product.  Two calls with the same arguments on the
+ * same device give the same bits.
+ *
+ *   q               device bf16, 16-byte aligned; row r, head h, column c at r * q_row_stride +
+ *                   h * q_head_stride + c, strides in elements, multiples of 8, for which no two
+ *                   heads overlap.
+ *   num_heads       a multiple of num_kv_heads, at most 128 times it; total_rows * num_heads at
+ *                   most 2^31 - 257.
+ *   head_size       64 or 128; row_elems = num_kv_heads * head_size.
+ *   softmax_scale   finite.
+ *   kv_cache        cache_lengths required; kv_stride >= row_elems.
+ *   out             device bf16 [total_rows, num_heads, head_size], 16-byte aligned.
+ *   lse             device fp32 [total_rows, num_heads], or NULL.
+ *   workspace       device, >= kv_attention_paged_workspace_size(...) bytes, 256-byte aligned.
+ * A position past the page-table row or in a page id >= num_pages sets PKM_ERR_OUT_OF_RANGE in
+ * dev_status and is not read; the rows of that request then hold unspecified values.
+ */
+pkm_status kv_attention_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                              const uint32_t* input_row_offsets, int32_t batch,
+                              int32_t total_rows, int32_t num_heads, int32_t num_kv_heads,
+                              int32_t head_size, float softmax_scale,
+                              const pkm_paged_cache* kv_cache, uint32_t layer_idx, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream);
+
+/*
+ * kv_attention_paged over a sliding window: a token at position p attends the positions t <= p
+ * with t > p - window or t < sink_tokens, that is the last `window` ones, itself among them, and
+ * the request's first `sink_tokens` ones, which stay visible.  What lies between is not read: its
+ * table entries may name pages that were given back.
+ *
+ *   window          > 0.
+ *   sink_tokens     >= 0.
+ *   other arguments and errors as for kv_attention_paged; with a window of all positions the two
+ *   calls compute the same.
+ */
+pkm_status kv_window_attention_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                     const uint32_t* input_row_offsets, int32_t batch,
+                                     int32_t total_rows, int32_t num_heads, int32_t num_kv_heads,
+                                     int32_t head_size, float softmax_scale, int32_t window,
+                                     int32_t sink_tokens, const pkm_paged_cache* kv_cache,
+                                     uint32_t layer_idx, void* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
  * Checks without a launch (no counterpart on the pages).  Until it is called with 0, calls of this
  * thread to mla_tree_attention_paged, mla_rope_heads, mla_cache_write_paged,
- * mla_cache_compact_paged and their variants make their host checks alone: what these find, or
+ * mla_cache_compact_paged, kv_rope_paged, kv_attention_paged and their variants make their host checks alone: what these find, or
  * PKM_ERR_CUDA where the call would go on to the GPU.  For callers that know more of an argument
  * than its address, a tensor in host memory say, and must not launch with it.
  */

@@ -23,6 +23,10 @@ Entry points (same names as the C ABI in include/paged_kv_mla.h):
   mla_cache_compact_paged (+ _qcache) accepted drafts moved to the front of their region
   kv_matmul_paged                     kv_matmul_ragged_paged (bf16)
   kv_matmul_paged_fp8                 its FP8 block-scaled form (+ kv_matmul_paged_fp8_workspace_size)
+  kv_rope_paged                       rotary positions on several axes for new queries and keys,
+                                      keys and values stored into the paged K/V cache
+  kv_attention_paged                  attention of new tokens (a chunk, or one) over that cache
+    (+ _workspace_size), kv_window_attention_paged   the same over a sliding window and the first tokens
   pkm_check_wait_timeout              the bounded-wait self-check
   pkm_validate_row_offsets            the opt-in check that an offset array is non-decreasing
   status_string, last_cuda_error      pkm_status_string, pkm_last_cuda_error
@@ -151,6 +155,19 @@ _lib.mla_decompress_k_paged_fp8_noalloc.argtypes = [ctypes.POINTER(_CCache), _u3
                                                     _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp,
                                                     _vp, _vp]
 _lib.mla_decompress_k_paged_fp8_noalloc.restype = ctypes.c_int
+_lib.kv_rope_paged.argtypes = [_vp, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64,
+                               _i64, _i32, _i32, _i32, _vp, _i32, _i32, _vp, _i32, ctypes.c_char_p,
+                               _vp, _i32, _i32, ctypes.POINTER(_CCache), _u32, _vp, _vp]
+_lib.kv_rope_paged.restype = ctypes.c_int
+_lib.kv_attention_paged_workspace_size.argtypes = [_i32, _i32, _i32, _i32]
+_lib.kv_attention_paged_workspace_size.restype = _sz
+_lib.kv_attention_paged.argtypes = [_vp, _i64, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _f32,
+                                    ctypes.POINTER(_CCache), _u32, _vp, _vp, _vp, _sz, _vp, _vp]
+_lib.kv_attention_paged.restype = ctypes.c_int
+_lib.kv_window_attention_paged.argtypes = [_vp, _i64, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _f32,
+                                           _i32, _i32, ctypes.POINTER(_CCache), _u32, _vp, _vp, _vp,
+                                           _sz, _vp, _vp]
+_lib.kv_window_attention_paged.restype = ctypes.c_int
 FP8_NOALLOC_SCRATCH_BYTES = 16 << 20
 _lib.pkm_checks_only.argtypes = [_i32]
 _lib.pkm_checks_only.restype = None
@@ -647,6 +664,107 @@ def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_co
                     stream, check)
 
 
+def _heads_of(t) -> Optional[tuple]:
+    """Row and head stride of a bf16 view [rows, heads, D] with contiguous columns."""
+    strides = t.stride()
+    return strides if len(strides) == 3 and strides[2] == 1 and t.dtype in _BF16 else None
+
+
+def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
+                  freqs_cis: torch.Tensor, kv_cache: PagedCache, layer_idx: int, num_kv_heads: int,
+                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                  pair_axes=None, half: bool = False,
+                  dev_status: Optional[torch.Tensor] = None, stream=None, check: bool = True) -> int:
+    """Turns new queries q [rows, heads, D] into q_out (which may be q) and new keys, and stores
+    keys and values in the paged K/V cache.  k and v: [rows, num_kv_heads, D], or None: keys that
+    are in the cache already turn in place, and values stay.  All are bf16 views with contiguous
+    last dimensions.  positions: uint32/int32 [axes, rows] (or [rows], one axis); pair_axes: the
+    axis of every pair of the P columns of freqs_cis [max_seq_len, P] (P/2 whole numbers on the
+    host, None: axis 0).  Pairs are columns (2j, 2j + 1), or (j, j + P/2) with `half`."""
+    where, table, factors, at_axes = "kv_rope_paged", kv_cache.page_table, freqs_cis.shape, positions.shape
+    pages, batch, axes = table.shape, input_row_offsets.shape[0] - 1, 1 if len(at_axes) == 1 else at_axes[0]
+    rows = at_axes[-1] if 1 <= len(at_axes) <= 2 else -1
+    size = kv_cache.row_elems // num_kv_heads if num_kv_heads > 0 else 0
+    device, at = _look(((_WORD, 0, input_row_offsets), (_WORD, 0, positions), (_FLOAT, 0, freqs_cis),
+                        (None, 0, kv_cache.data), (_WORD, 0, table), (_WORD, batch, kv_cache.cache_lengths),
+                        (None, 0, q), (None, 0, q_out), (None, 0, k), (None, 0, v)))
+    strides, heads = [], 0 if q is None else q.shape[1] if len(q.shape) == 3 else -1
+    ok = device is not None and rows >= 0 and (q is None) == (q_out is None) and len(pages) == 2 \
+        and pages[0] >= batch and len(factors) == 2 and len(input_row_offsets.shape) == 1
+    for t, n in ((q, heads), (q_out, heads), (k, num_kv_heads), (v, num_kv_heads)):
+        st = (0, 0) if t is None else _heads_of(t)
+        ok = ok and st is not None and (t is None or t.shape == (rows, n, size))
+        strides.append(st)
+    if ok and pair_axes is not None:
+        try:
+            pair_axes = bytes(pair_axes)
+        except (TypeError, ValueError):
+            ok = False
+        ok = ok and len(pair_axes) == factors[1] // 2
+    if not ok:
+        return _check(PKM_ERR_INVALID_ARG, where, check)
+    sq, so, sk, sv = strides
+    c = kv_cache._struct_of((at[3], at[4], pages[1], at[5]))
+    args = (at[6], sq[0], sq[1], heads, at[7], so[0], so[1], at[8], sk[0], sk[1], at[9], sv[0], sv[1],
+            num_kv_heads, size, factors[1], at[0], batch, rows, at[1], axes, pair_axes, at[2],
+            factors[0], 1 if half else 0, ctypes.byref(c), int(layer_idx), _ptr(dev_status))
+    return _run(_lib.kv_rope_paged, where, args, device, stream, check)
+
+
+def kv_attention_paged_workspace_size(total_rows: int, num_heads: int, num_kv_heads: int,
+                                      head_size: int) -> int:
+    return int(_lib.kv_attention_paged_workspace_size(int(total_rows), int(num_heads),
+                                                      int(num_kv_heads), int(head_size)))
+
+
+def _kv_attention(f, where, q, offsets, scale, limits, cache, layer_idx, out, workspace, lse,
+                  dev_status, stream, check) -> int:
+    """Both attentions over the K/V cache, with the shapes that the C call cannot see."""
+    table = cache.page_table
+    shape, pages, batch = q.shape, table.shape, offsets.shape[0] - 1
+    device, at = _look(((None, 0, q), (_WORD, 0, offsets), (_BF16, 0, out), (None, 0, workspace),
+                        (_FLOAT, 0, lse), (None, 0, cache.data), (_WORD, 0, table),
+                        (_WORD, batch, cache.cache_lengths)))
+    strides = _heads_of(q)
+    if device is None or strides is None or out.shape != shape or not workspace.is_contiguous() \
+            or (lse is not None and lse.shape != shape[:2]) or len(pages) != 2 or pages[0] < batch \
+            or shape[2] == 0 or cache.row_elems % shape[2] != 0:
+        return _check(PKM_ERR_INVALID_ARG, where, check)
+    c = cache._struct_of((at[5], at[6], pages[1], at[7]))
+    args = (at[0], strides[0], strides[1], at[1], batch, shape[0], shape[1],
+            cache.row_elems // shape[2], shape[2], float(scale), *limits, ctypes.byref(c),
+            int(layer_idx), at[2], at[4], at[3], workspace.nbytes, _ptr(dev_status))
+    return _run(f, where, args, device, stream, check)
+
+
+def kv_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor, softmax_scale: float,
+                       kv_cache: PagedCache, layer_idx: int, out: torch.Tensor,
+                       workspace: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                       dev_status: Optional[torch.Tensor] = None, stream=None,
+                       check: bool = True) -> int:
+    """Attention of the new tokens' queries q [total_rows, heads, D] (a bf16 view with contiguous
+    columns) over the paged K/V cache: each over its request's positions up to its own, whose keys
+    and values the cache holds.  Heads share the row_elems / D heads of keys in equal groups.
+    out [total_rows, heads, D] bf16, lse [total_rows, heads] fp32 or None."""
+    return _kv_attention(_lib.kv_attention_paged, "kv_attention_paged", q, input_row_offsets,
+                         softmax_scale, (), kv_cache, layer_idx, out, workspace, lse, dev_status,
+                         stream, check)
+
+
+def kv_window_attention_paged(q: torch.Tensor, input_row_offsets: torch.Tensor,
+                              softmax_scale: float, window: int, sink_tokens: int,
+                              kv_cache: PagedCache, layer_idx: int, out: torch.Tensor,
+                              workspace: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                              dev_status: Optional[torch.Tensor] = None, stream=None,
+                              check: bool = True) -> int:
+    """kv_attention_paged over the last `window` positions, the token's own among them, and the
+    request's first `sink_tokens` ones."""
+    return _kv_attention(_lib.kv_window_attention_paged, "kv_window_attention_paged", q,
+                         input_row_offsets, softmax_scale, (int(window), int(sink_tokens)), kv_cache,
+                         layer_idx, out, workspace, lse, dev_status, stream, check)
+
+
 def kv_matmul_paged_fp8_workspace_size(total_rows: int, k_in: int) -> int:
     return int(_lib.kv_matmul_paged_fp8_workspace_size(int(total_rows), int(k_in)))
 
@@ -714,7 +832,8 @@ __all__ = ["pkm_check_wait_timeout", "mla_decompress_k_paged_fp8_noalloc",
            "mla_cache_write_paged_at", "mla_cache_write_paged_qcache_at", "mla_rope_heads",
            "mla_tree_attention_paged", "mla_tree_attention_paged_qcache",
            "mla_tree_attention_paged_workspace_size", "mla_cache_compact_paged",
-           "mla_cache_compact_paged_qcache", "status_string", "LIB_PATH", "PKM_OK", "PKM_ERR_INVALID_ARG", "PKM_ERR_UNSUPPORTED",
+           "mla_cache_compact_paged_qcache", "kv_rope_paged", "kv_attention_paged",
+           "kv_attention_paged_workspace_size", "kv_window_attention_paged", "status_string", "LIB_PATH", "PKM_OK", "PKM_ERR_INVALID_ARG", "PKM_ERR_UNSUPPORTED",
            "PKM_ERR_CUDA", "PKM_ERR_OUT_OF_RANGE", "PKM_ERR_TIMEOUT"]
 
 

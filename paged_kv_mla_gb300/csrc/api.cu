@@ -25,6 +25,8 @@ using pkm::KvFp8Extra;
 using pkm::RopeHeadsArgs;
 using pkm::CompactArgs;
 using pkm::TreeAttentionArgs;
+using pkm::KvRopeArgs;
+using pkm::KvAttentionArgs;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool mult8(int64_t v) { return v >= 0 && (v % 8) == 0; }
@@ -700,6 +702,26 @@ pkm_status cache_write(const void* latent, const uint32_t* input_row_offsets, in
 
 }  // namespace
 
+namespace {
+
+// Whether the rows and heads of a strided tensor, `width` columns each, do not overlap: heads
+// inside rows, or rows inside heads.
+bool heads_apart(int64_t rows, int64_t heads, int64_t width, int64_t row_stride,
+                 int64_t head_stride) {
+    const int64_t r1 = rows - 1, h1 = heads - 1;
+    const int64_t wide = static_cast<int64_t>(1) << 62;
+    const auto spans = [&](int64_t n, int64_t stride) {  // n * stride + width, saturated
+        return stride > 0 && n > (wide - width) / stride ? wide : n * stride + width;
+    };
+    const bool heads_inside = (h1 == 0 || head_stride >= width) &&
+                              (r1 == 0 || row_stride >= spans(h1, head_stride));
+    const bool rows_inside = (r1 == 0 || row_stride >= width) &&
+                             (h1 == 0 || head_stride >= spans(r1, row_stride));
+    return heads_inside || rows_inside;
+}
+
+}  // namespace
+
 extern "C" {
 
 pkm_status mla_cache_write_paged(const void* latent, const uint32_t* input_row_offsets,
@@ -771,19 +793,10 @@ pkm_status mla_rope_heads(const void* x, int64_t x_row_stride, int64_t x_head_st
     if (rope_dim % 8 != 0 || rope_dim > 256) return PKM_ERR_UNSUPPORTED;
     // a thread counts its heads, up to 512 behind the last, in 32 bits
     if (num_heads > INT32_MAX - 512) return PKM_ERR_UNSUPPORTED;
-    // the rows and heads of y must not overlap: heads inside rows, or rows inside heads
-    const int64_t r1 = total_rows - 1, h1 = num_heads - 1, p = rope_dim;
-    const int64_t wide = static_cast<int64_t>(1) << 62;
-    const auto spans = [&](int64_t n, int64_t stride) {  // n * stride + p, saturated
-        return stride > 0 && n > (wide - p) / stride ? wide : n * stride + p;
-    };
-    const bool heads_inside = (h1 == 0 || y_head_stride >= p) &&
-                              (r1 == 0 || y_row_stride >= spans(h1, y_head_stride));
-    const bool rows_inside = (r1 == 0 || y_row_stride >= p) &&
-                             (h1 == 0 || y_head_stride >= spans(r1, y_row_stride));
-    if (!heads_inside && !rows_inside) return PKM_ERR_INVALID_ARG;
-    if (x == y && ((r1 > 0 && x_row_stride != y_row_stride) ||
-                   (h1 > 0 && x_head_stride != y_head_stride)))
+    if (!heads_apart(total_rows, num_heads, rope_dim, y_row_stride, y_head_stride))
+        return PKM_ERR_INVALID_ARG;
+    if (x == y && ((total_rows > 1 && x_row_stride != y_row_stride) ||
+                   (num_heads > 1 && x_head_stride != y_head_stride)))
         return PKM_ERR_INVALID_ARG;
     RopeHeadsArgs a{};
     a.x = static_cast<const uint16_t*>(x);
@@ -1240,6 +1253,226 @@ pkm_status kv_matmul_paged_fp8(const void* hidden_state, const uint32_t* input_r
     if (const cudaError_t e = debug_validate(a.row_offsets, a.batch, a.status, stream))
         return cuda_status(e);
     return cuda_status(pkm::launch_kv_matmul_fp8(tm_q, tm_w, a, x, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The cache of the calls on heads of keys and values.
+pkm_status check_kv_cache(const pkm_paged_cache* c, uint32_t layer_idx, int32_t num_kv_heads,
+                          int32_t head_size) {
+    if (c == nullptr || c->data == nullptr || c->page_table == nullptr ||
+        c->cache_lengths == nullptr)
+        return PKM_ERR_INVALID_ARG;
+    if (c->num_layers <= 0 || layer_idx >= static_cast<uint32_t>(c->num_layers) ||
+        c->num_pages <= 0 || c->page_size <= 0 || c->max_pages_per_seq <= 0)
+        return PKM_ERR_INVALID_ARG;
+    if (c->row_elems != static_cast<int64_t>(num_kv_heads) * head_size) return PKM_ERR_INVALID_ARG;
+    if (!mult8(c->layer_stride) || !mult8(c->page_stride) || !mult8(c->slot_stride) ||
+        !mult8(c->kv_stride) || !aligned16(c->data))
+        return PKM_ERR_INVALID_ARG;
+    // the planes are apart: a slot's values do not begin within its keys
+    if (c->kv_stride < c->row_elems) return PKM_ERR_INVALID_ARG;
+    return PKM_OK;
+}
+
+// Body of both attentions over the K/V cache; a window of 0 is none.
+pkm_status kv_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                        const uint32_t* input_row_offsets, int32_t batch, int32_t total_rows,
+                        int32_t num_heads, int32_t num_kv_heads, int32_t head_size,
+                        float softmax_scale, int32_t window, int32_t sink_tokens,
+                        const pkm_paged_cache* kv_cache, uint32_t layer_idx, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                        void* stream) {
+    if (batch < 0 || total_rows < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+        num_heads % num_kv_heads != 0)
+        return PKM_ERR_INVALID_ARG;
+    if (total_rows == 0 || batch == 0) return PKM_OK;
+    if (q == nullptr || input_row_offsets == nullptr || out == nullptr || workspace == nullptr ||
+        !std::isfinite(softmax_scale))
+        return PKM_ERR_INVALID_ARG;
+    if (const pkm_status st = check_kv_cache(kv_cache, layer_idx, num_kv_heads, head_size))
+        return st;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        !mult8(q_row_stride) || !mult8(q_head_stride))
+        return PKM_ERR_INVALID_ARG;
+    // rows and heads of the queries are apart, heads inside rows or rows inside heads
+    if (!heads_apart(total_rows, num_heads, head_size, q_row_stride, q_head_stride))
+        return PKM_ERR_INVALID_ARG;
+    if ((head_size != 64 && head_size != 128) || num_heads / num_kv_heads > 128)
+        return PKM_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(total_rows) * num_heads > INT32_MAX - 256) return PKM_ERR_UNSUPPORTED;
+    if (workspace_bytes <
+        kv_attention_paged_workspace_size(total_rows, num_heads, num_kv_heads, head_size))
+        return PKM_ERR_INVALID_ARG;
+    KvAttentionArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_row_stride = q_row_stride;
+    a.q_head_stride = q_head_stride;
+    a.row_offsets = input_row_offsets;
+    a.batch = batch;
+    a.total_rows = total_rows;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_size = head_size;
+    a.scale = softmax_scale;
+    a.window = window;
+    a.sinks = sink_tokens;
+    a.cache_layer = static_cast<const uint16_t*>(kv_cache->data) +
+                    static_cast<int64_t>(layer_idx) * kv_cache->layer_stride;
+    a.page_stride = kv_cache->page_stride;
+    a.slot_stride = kv_cache->slot_stride;
+    a.kv_stride = kv_cache->kv_stride;
+    a.num_pages = kv_cache->num_pages;
+    a.page_size = kv_cache->page_size;
+    a.max_pages = kv_cache->max_pages_per_seq;
+    a.page_table = kv_cache->page_table;
+    a.cache_lengths = kv_cache->cache_lengths;
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.workspace = static_cast<uint8_t*>(workspace);
+    a.status = dev_status;
+    a.timeout_ns = wait_timeout_ns();
+    int sms = 0;
+    if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
+    if (const cudaError_t e = debug_validate(input_row_offsets, batch, dev_status, stream))
+        return cuda_status(e);
+    return cuda_status(pkm::launch_kv_attention(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+pkm_status kv_rope_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                         int32_t num_heads, void* q_out, int64_t q_out_row_stride,
+                         int64_t q_out_head_stride, const void* k, int64_t k_row_stride,
+                         int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                         int64_t v_head_stride, int32_t num_kv_heads, int32_t head_size,
+                         int32_t rope_dim, const uint32_t* input_row_offsets, int32_t batch,
+                         int32_t total_rows, const uint32_t* positions, int32_t num_axes,
+                         const uint8_t* pair_axes, const float* freqs_cis, int32_t max_seq_len,
+                         int32_t half, const pkm_paged_cache* kv_cache, uint32_t layer_idx,
+                         int32_t* dev_status, void* stream) {
+    if (batch < 0 || total_rows < 0 || num_heads < 0 || num_kv_heads <= 0 || head_size <= 0 ||
+        rope_dim <= 0 || max_seq_len <= 0 || num_axes <= 0)
+        return PKM_ERR_INVALID_ARG;
+    if (total_rows == 0 || batch == 0) return PKM_OK;
+    if (input_row_offsets == nullptr || positions == nullptr || freqs_cis == nullptr)
+        return PKM_ERR_INVALID_ARG;
+    if (num_heads > 0 ? q == nullptr || q_out == nullptr : q != nullptr) return PKM_ERR_INVALID_ARG;
+    if (half != 0 && half != 1) return PKM_ERR_INVALID_ARG;
+    if (const pkm_status st = check_kv_cache(kv_cache, layer_idx, num_kv_heads, head_size))
+        return st;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(freqs_cis))
+        return PKM_ERR_INVALID_ARG;
+    for (const int64_t stride : {q_row_stride, q_head_stride, q_out_row_stride, q_out_head_stride,
+                                 k_row_stride, k_head_stride, v_row_stride, v_head_stride})
+        if (!mult8(stride)) return PKM_ERR_INVALID_ARG;
+    if (rope_dim > head_size) return PKM_ERR_INVALID_ARG;
+    if (head_size % 8 != 0 || head_size > 256 || rope_dim % 8 != 0 || num_axes > 4)
+        return PKM_ERR_UNSUPPORTED;
+    // a thread counts its heads, up to 512 behind the last, in 32 bits
+    if (num_heads > INT32_MAX - 512) return PKM_ERR_UNSUPPORTED;
+    if (num_heads > 0 &&
+        !heads_apart(total_rows, num_heads, head_size, q_out_row_stride, q_out_head_stride))
+        return PKM_ERR_INVALID_ARG;
+    if (q != nullptr && q == q_out &&
+        ((total_rows > 1 && q_row_stride != q_out_row_stride) ||
+         (num_heads > 1 && q_head_stride != q_out_head_stride)))
+        return PKM_ERR_INVALID_ARG;
+    // keys and values of a page's slots are apart: threads of their own write them
+    if (kv_cache->page_size > 1) {
+        const int64_t slot = kv_cache->slot_stride, row = kv_cache->row_elems;
+        if (slot < row) return PKM_ERR_INVALID_ARG;
+        const int64_t last = kv_cache->page_size - 1;
+        const int64_t below = std::min(kv_cache->kv_stride / slot, last);
+        const int64_t above = std::min(below + 1, last);
+        if (v != nullptr && (std::abs(kv_cache->kv_stride - below * slot) < row ||
+                             std::abs(kv_cache->kv_stride - above * slot) < row))
+            return PKM_ERR_INVALID_ARG;
+    }
+    KvRopeArgs a{};
+    for (int j = 0; pair_axes != nullptr && j < rope_dim / 2; ++j) {
+        if (pair_axes[j] >= num_axes) return PKM_ERR_INVALID_ARG;
+        a.unit_axes[j / 4] |= static_cast<uint8_t>(pair_axes[j] << (2 * (j % 4)));
+    }
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.q_row_stride = q_row_stride;
+    a.q_head_stride = q_head_stride;
+    a.q_out_row_stride = q_out_row_stride;
+    a.q_out_head_stride = q_out_head_stride;
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.k_row_stride = k_row_stride;
+    a.k_head_stride = k_head_stride;
+    a.v_row_stride = v_row_stride;
+    a.v_head_stride = v_head_stride;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_size = head_size;
+    a.rope_dim = rope_dim;
+    a.row_offsets = input_row_offsets;
+    a.batch = batch;
+    a.total_rows = total_rows;
+    a.positions = positions;
+    a.num_axes = num_axes;
+    a.freqs = freqs_cis;
+    a.max_seq_len = max_seq_len;
+    a.half = half;
+    a.cache_layer = static_cast<uint16_t*>(kv_cache->data) +
+                    static_cast<int64_t>(layer_idx) * kv_cache->layer_stride;
+    a.page_stride = kv_cache->page_stride;
+    a.slot_stride = kv_cache->slot_stride;
+    a.kv_stride = kv_cache->kv_stride;
+    a.num_pages = kv_cache->num_pages;
+    a.page_size = kv_cache->page_size;
+    a.max_pages = kv_cache->max_pages_per_seq;
+    a.page_table = kv_cache->page_table;
+    a.cache_lengths = kv_cache->cache_lengths;
+    a.status = dev_status;
+    int sms = 0;
+    if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
+    if (const cudaError_t e = debug_validate(input_row_offsets, batch, dev_status, stream))
+        return cuda_status(e);
+    return cuda_status(pkm::launch_kv_rope(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
+                                         int32_t num_kv_heads, int32_t head_size) {
+    if (total_rows < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+        num_heads % num_kv_heads != 0)
+        return 0;
+    return 256;
+}
+
+pkm_status kv_attention_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                              const uint32_t* input_row_offsets, int32_t batch,
+                              int32_t total_rows, int32_t num_heads, int32_t num_kv_heads,
+                              int32_t head_size, float softmax_scale,
+                              const pkm_paged_cache* kv_cache, uint32_t layer_idx, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream) {
+    return kv_attention(q, q_row_stride, q_head_stride, input_row_offsets, batch, total_rows,
+                        num_heads, num_kv_heads, head_size, softmax_scale, 0, 0, kv_cache,
+                        layer_idx, out, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+pkm_status kv_window_attention_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                     const uint32_t* input_row_offsets, int32_t batch,
+                                     int32_t total_rows, int32_t num_heads, int32_t num_kv_heads,
+                                     int32_t head_size, float softmax_scale, int32_t window,
+                                     int32_t sink_tokens, const pkm_paged_cache* kv_cache,
+                                     uint32_t layer_idx, void* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    if (window <= 0 || sink_tokens < 0) return PKM_ERR_INVALID_ARG;
+    return kv_attention(q, q_row_stride, q_head_stride, input_row_offsets, batch, total_rows,
+                        num_heads, num_kv_heads, head_size, softmax_scale, window, sink_tokens,
+                        kv_cache, layer_idx, out, lse, workspace, workspace_bytes, dev_status,
+                        stream);
 }
 
 pkm_status pkm_validate_row_offsets(const uint32_t* offsets, int32_t batch, int32_t* dev_status,

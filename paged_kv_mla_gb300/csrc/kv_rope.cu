@@ -1,0 +1,195 @@
+// kv_rope.cu -- positions of new queries and keys, and the keys' and values' way into the
+// paged K/V cache.
+//
+// kv_matmul_ragged_paged (Modular MAX, nn/kv_cache_ragged) writes keys and values; freqs_cis
+// of mla_prefill_decode_graph_fp8 (attention/gpu/mla_graph) gives the rotary factors.  Here a
+// token has a position on each of up to four axes (time, height, width), and pair j of a
+// head's columns turns by the factor j of the position on the axis that the pair belongs to:
+//     (x0, x1) -> (x0 c - x1 s, x0 s + x1 c)     in fp32, rounded once to bf16,
+// pair j being columns (2j, 2j + 1) or (j, j + P/2).  Columns past the first P are copied.
+//
+// A streaming kernel: every value once in and once out.  An item is one row and a group of
+// its heads (queries, or keys and then values); a thread has a unit of eight columns, which
+// holds four whole pairs, keeps their factors in registers and walks over heads, four loads in
+// flight.  The columns are asked for before the row's position and slot, which hang on a chain
+// of loads (offsets, length, page id).
+#include "pkm_device.cuh"
+#include "pkm_internal.h"
+
+namespace pkm {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kUnroll = 4;  // heads in flight per thread
+
+// Columns of a turned unit: 16 bytes in the interleaved layout, twice 8 bytes (four columns of
+// each half) in the half layout; copied units are 16 bytes in both.
+__device__ __forceinline__ uint4 load_unit(const uint16_t* p, int second) {
+    if (second == 0) return *reinterpret_cast<const uint4*>(p);
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    const uint2 b = *reinterpret_cast<const uint2*>(p + second);
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
+
+__device__ __forceinline__ void store_unit(uint16_t* p, int second, uint4 w) {
+    if (second == 0) {
+        *reinterpret_cast<uint4*>(p) = w;
+    } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w.x, w.y);
+        *reinterpret_cast<uint2*>(p + second) = make_uint2(w.z, w.w);
+    }
+}
+
+template <bool HALF>
+__device__ __forceinline__ uint4 turned(uint4 v, const float (&cs)[8]) {
+    float f[8], o[8];
+    bf16x2_to_f32(v.x, f[0], f[1]);
+    bf16x2_to_f32(v.y, f[2], f[3]);
+    bf16x2_to_f32(v.z, f[4], f[5]);
+    bf16x2_to_f32(v.w, f[6], f[7]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = HALF ? k : 2 * k, j = HALF ? k + 4 : 2 * k + 1;
+        const float c = cs[2 * k], s = cs[2 * k + 1];
+        o[i] = fmaf(f[i], c, -f[j] * s);
+        o[j] = fmaf(f[i], s, f[j] * c);
+    }
+    return make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                      pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+}
+
+// Request of row r, or -1 when none covers it, found by all lanes of a warp: each step looks at
+// 32 entries that divide what is left.
+__device__ __forceinline__ int request_of(const uint32_t* offsets, int batch, uint32_t r) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = batch + 1;  // the last entry at or below r is among lo .. lo + n - 1
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lane * step;
+        const bool below = at < n && __ldg(offsets + lo + at) <= r;
+        const uint32_t m = __ballot_sync(0xffffffffu, below);
+        if ((m & 1u) == 0) return -1;
+        const int k = 31 - __clz(static_cast<int>(m));
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return lo < batch && __ldg(offsets + lo) <= r ? lo : -1;
+}
+
+template <bool HALF>
+__global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a) {
+    const int units = a.head_size / 8;
+    const int heads_per_pass = kThreads / units;
+    const int u = threadIdx.x % units, h_in = threadIdx.x / units;
+    const int group = heads_per_pass * kUnroll;
+    const int q_groups = (a.num_heads + group - 1) / group;
+    const int kv_heads = a.num_kv_heads * (a.v != nullptr ? 2 : 1);
+    const int groups = q_groups + (kv_heads + group - 1) / group;
+    const int64_t items = static_cast<int64_t>(a.total_rows) * groups;
+    const bool turns = u * 8 < a.rope_dim;
+    const int col = HALF && turns ? u * 4 : u * 8;
+    const int second = HALF && turns ? a.rope_dim / 2 : 0;
+    const bool in_use = h_in < heads_per_pass;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int64_t r = it / groups;
+        const int g = static_cast<int>(it % groups);
+        const bool queries = g < q_groups;
+        const int heads = queries ? a.num_heads : kv_heads;
+        const int h0 = (queries ? g : g - q_groups) * group + h_in;
+        const auto source = [&](int h) -> const uint16_t* {
+            if (queries) return a.q + r * a.q_row_stride + h * a.q_head_stride + col;
+            if (h < a.num_kv_heads) return a.k + r * a.k_row_stride + h * a.k_head_stride + col;
+            return a.v + r * a.v_row_stride + (h - a.num_kv_heads) * a.v_head_stride + col;
+        };
+        // the half layout's places are for turned heads: values are copied in whole units
+        const auto is_value = [&](int h) { return !queries && h >= a.num_kv_heads; };
+        uint4 v[kUnroll];
+        const bool from_cache = !queries && a.k == nullptr;  // keys, turned in place
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int h = h0 + i * heads_per_pass;
+            if (!in_use || h >= heads || (from_cache && !is_value(h))) continue;
+            if (is_value(h)) v[i] = load_unit(source(h) - col + u * 8, 0);
+            else v[i] = load_unit(source(h), second);
+        }
+        const int b = request_of(a.row_offsets, a.batch, static_cast<uint32_t>(r));
+        if (b < 0) continue;
+        bool inside = true;
+        for (int x = 0; x < a.num_axes; ++x)
+            inside = inside && __ldg(a.positions + static_cast<int64_t>(x) * a.total_rows + r) <
+                                   static_cast<uint32_t>(a.max_seq_len);
+        int64_t slot = 0;
+        if (!queries) {
+            const uint64_t at = static_cast<uint64_t>(__ldg(a.cache_lengths + b)) +
+                                (static_cast<uint64_t>(r) - __ldg(a.row_offsets + b));
+            const uint64_t page_size = static_cast<uint64_t>(a.page_size);
+            const uint64_t lp = at / page_size;
+            uint32_t page = UINT32_MAX;
+            if (lp < static_cast<uint64_t>(a.max_pages))
+                page = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
+            if (page < static_cast<uint32_t>(a.num_pages))
+                slot = static_cast<int64_t>(page) * a.page_stride +
+                       static_cast<int64_t>(at - lp * page_size) * a.slot_stride;
+            else
+                inside = false;
+        }
+        if (!inside) {
+            if (threadIdx.x == 0) report(a.status, PKM_ERR_OUT_OF_RANGE);
+            continue;
+        }
+        if (!in_use) continue;
+        float cs[8];
+        if (turns) {
+            const uint32_t axes = a.unit_axes[u];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t pos = __ldg(
+                    a.positions + static_cast<int64_t>((axes >> (2 * k)) & 3u) * a.total_rows + r);
+                const float2 f = __ldg(reinterpret_cast<const float2*>(
+                    a.freqs + static_cast<int64_t>(pos) * a.rope_dim + u * 8 + 2 * k));
+                cs[2 * k] = f.x;
+                cs[2 * k + 1] = f.y;
+            }
+        }
+        if (from_cache) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                const int h = h0 + i * heads_per_pass;
+                if (h < heads && !is_value(h) && turns)
+                    v[i] = load_unit(a.cache_layer + slot + h * a.head_size + col, second);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int h = h0 + i * heads_per_pass;
+            if (h >= heads) continue;
+            if (is_value(h)) {
+                uint16_t* to = a.cache_layer + slot + a.kv_stride + (h - a.num_kv_heads) * a.head_size;
+                store_unit(to + u * 8, 0, v[i]);
+                continue;
+            }
+            uint16_t* to = queries ? a.q_out + r * a.q_out_row_stride + h * a.q_out_head_stride
+                                   : a.cache_layer + slot + h * a.head_size;
+            if (turns) store_unit(to + col, second, turned<HALF>(v[i], cs));
+            else if (queries ? a.q != a.q_out : !from_cache) store_unit(to + col, 0, v[i]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_rope(KvRopeArgs args, int num_sms, cudaStream_t stream) {
+    const int group = kThreads / (args.head_size / 8) * kUnroll;
+    const int64_t kv_heads = static_cast<int64_t>(args.num_kv_heads) * (args.v != nullptr ? 2 : 1);
+    const int64_t items = static_cast<int64_t>(args.total_rows) *
+                          ((args.num_heads + group - 1) / group + (kv_heads + group - 1) / group);
+    const int64_t most = static_cast<int64_t>(num_sms) * 64;
+    const unsigned blocks = static_cast<unsigned>(items < most ? items : most);
+    if (args.half)
+        kv_rope_kernel<true><<<blocks, kThreads, 0, stream>>>(args);
+    else
+        kv_rope_kernel<false><<<blocks, kThreads, 0, stream>>>(args);
+    return cudaGetLastError();
+}
+
+}  // namespace pkm
