@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "paged_kv_mla.h"
+#include "kv_internal.h"
 #include "pkm_internal.h"
 
 namespace {
@@ -159,6 +160,48 @@ bool encode_cache_pages(CUtensorMap* map, const void* layer, int32_t cols, int32
     const cuuint32_t box[4] = {64, box_slots, 1, box_blocks};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(layer), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// Rows of heads by strides (elements) as a 3-D tensor {column, head, row}, boxes of
+// {64, box_heads, box_rows}, 128-byte swizzled.
+bool encode_heads(CUtensorMap* map, const void* base, int32_t cols, int32_t heads, int32_t rows,
+                  int64_t head_stride, int64_t row_stride, int32_t box_heads, int32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2,
+                                   static_cast<cuuint64_t>(row_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads),
+                               static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// One plane of a layer of the paged K/V cache, whose pages have a multiple of 8 slots, as a 5-D
+// tensor {64 columns of a block, slot of 8, block, 8 slots, page}; boxes of `slots` slots and one
+// head's blocks.  A box lands as 1 KB tiles of [8 slots x 128 bytes], 128-byte swizzled, those of
+// a head's blocks side by side, so that boxes of any size follow one another in a tile's rows.
+bool encode_kv_pages(CUtensorMap* map, const void* plane, const KvAttentionArgs& a, int32_t slots,
+                     int32_t row_elems) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(row_elems / 64),
+                                static_cast<cuuint64_t>(a.page_size / 8),
+                                static_cast<cuuint64_t>(a.num_pages)};
+    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(a.slot_stride) * 2, 128,
+                                   static_cast<cuuint64_t>(a.slot_stride) * 16,
+                                   static_cast<cuuint64_t>(a.page_stride) * 2};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(a.head_size / 64),
+                               static_cast<cuuint32_t>(slots / 8), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(plane), dims, strides,
               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
@@ -1303,6 +1346,10 @@ pkm_status kv_attention(const void* q, int64_t q_row_stride, int64_t q_head_stri
     if ((head_size != 64 && head_size != 128) || num_heads / num_kv_heads > 128)
         return PKM_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(total_rows) * num_heads > INT32_MAX - 256) return PKM_ERR_UNSUPPORTED;
+    // strides of a tensor map, in bytes below 2^40
+    if ((total_rows > 1 && q_row_stride >= int64_t{1} << 39) ||
+        (num_heads > 1 && q_head_stride >= int64_t{1} << 39))
+        return PKM_ERR_UNSUPPORTED;
     if (workspace_bytes <
         kv_attention_paged_workspace_size(total_rows, num_heads, num_kv_heads, head_size))
         return PKM_ERR_INVALID_ARG;
@@ -1319,6 +1366,8 @@ pkm_status kv_attention(const void* q, int64_t q_row_stride, int64_t q_head_stri
     a.scale = softmax_scale;
     a.window = window;
     a.sinks = sink_tokens;
+    a.sink_tiles = sink_tokens / 128 + (sink_tokens % 128 != 0 ? 1 : 0);
+    a.tile_tokens = pkm::kv_tile_tokens(num_heads, num_kv_heads);
     a.cache_layer = static_cast<const uint16_t*>(kv_cache->data) +
                     static_cast<int64_t>(layer_idx) * kv_cache->layer_stride;
     a.page_stride = kv_cache->page_stride;
@@ -1336,9 +1385,31 @@ pkm_status kv_attention(const void* q, int64_t q_row_stride, int64_t q_head_stri
     a.timeout_ns = wait_timeout_ns();
     int sms = 0;
     if (const cudaError_t e = current_sm_count(&sms)) return cuda_status(e);
+    // Keys and values come by TMA where the pages are divided by boxes of at least 8 slots (whole
+    // swizzle atoms) and the strides fit a tensor map; others are loaded row by row.
+    const int64_t far = static_cast<int64_t>(1) << 39;
+    pkm::KvMaps maps{};
+    maps.slots = 128;
+    while (maps.slots > 0 && a.page_size % maps.slots != 0)
+        maps.slots = maps.slots > 8 ? maps.slots / 2 : 0;
+    if (a.page_stride >= far || a.slot_stride >= far / 8) maps.slots = 0;
+    // the stride of a dimension of one element is of no matter
+    const int64_t row_stride = total_rows > 1 ? q_row_stride : head_size;
+    const int64_t head_stride = num_heads > 1 ? q_head_stride : head_size;
+    const int32_t group = num_heads / num_kv_heads;
+    const uint16_t* values = a.cache_layer + a.kv_stride;
+    if (!encode_heads(&maps.q, q, head_size, num_heads, total_rows, head_stride, row_stride, group,
+                      a.tile_tokens) ||
+        !encode_heads(&maps.q_one, q, head_size, num_heads, total_rows, head_stride, row_stride,
+                      group, 1))
+        return encode_failed();
+    if (maps.slots > 0 &&
+        (!encode_kv_pages(&maps.k, a.cache_layer, a, maps.slots, kv_cache->row_elems) ||
+         !encode_kv_pages(&maps.v, values, a, maps.slots, kv_cache->row_elems)))
+        return encode_failed();
     if (const cudaError_t e = debug_validate(input_row_offsets, batch, dev_status, stream))
         return cuda_status(e);
-    return cuda_status(pkm::launch_kv_attention(a, sms, static_cast<cudaStream_t>(stream)));
+    return cuda_status(pkm::launch_kv_attention(maps, a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -1444,9 +1515,9 @@ pkm_status kv_rope_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
 size_t kv_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
                                          int32_t num_kv_heads, int32_t head_size) {
     if (total_rows < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
-        num_heads % num_kv_heads != 0)
+        num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > 128)
         return 0;
-    return 256;
+    return pkm::kv_workspace(total_rows, num_heads, num_kv_heads, head_size).bytes;
 }
 
 pkm_status kv_attention_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride,

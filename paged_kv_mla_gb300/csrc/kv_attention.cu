@@ -1,88 +1,1096 @@
 // kv_attention.cu -- attention of new tokens over the paged K/V cache that kv_matmul_paged fills.
 //
 // kv_matmul_ragged_paged (Modular MAX, nn/kv_cache_ragged): Args kv_collection (the K and V
-// cache), layer_idx, input_row_offsets.  Heads in groups of num_heads / num_kv_heads share keys
-// and values.  A warp takes one (token, head), its lanes the columns, and walks over the keys
-// with a running maximum and sum.
-#include "pkm_device.cuh"
-#include "pkm_internal.h"
+// cache), layer_idx, input_row_offsets.  Heads in groups of G share keys and values, so the
+// queries of a group's heads are rows of one product:
+//     S = Q K^T  [rows x keys],   O = softmax(scale S) V  [rows x D]
+// with row = token * G + head, and 128 rows of whole tokens make a tile of queries.
+//
+// An item is up to two tiles of one request and one head of keys.  Two tiles (a chunk) take each
+// tile of 128 keys in turn: while the tensor cores work for one, four softmax warps have the
+// other's scores.  One tile (few tokens, a single one above all) takes even and odd tiles of keys
+// in turn, each with sums of its own that are joined at the item's end.  Either way a step is one
+// product of 128 x 128 scores, steps alternate between two stages, and a stage has its scores
+// (which its weights overwrite in place, as the second product's A operand) and its O in tensor
+// memory, and four softmax warps.
+//
+// The key axis of all items is one line of 128-key tiles, cut into equal parts, one for each CTA:
+// a CTA starts at most one item that it does not finish and finishes at most one that it did not
+// start.  Such parts leave unnormalised fp32 sums, maxima and totals in the workspace and a second
+// kernel joins them; whole items are written directly.  A window's items leave out the tiles
+// between the first tokens and the window.
+//
+// Roles of a CTA: warps 0-3 and 4-7 softmax and epilogue of a stage, 8 MMA issue, 9 queries and
+// keys, 10 values, 11 looks values through for infinities and NaN where not every row attends
+// every key (a zero weight must not meet them).  Scores are kept in base 2; the running maximum
+// moves only when a row's new maximum exceeds it by 2^8, since any reference works as long as
+// nothing overflows, so O is hardly ever rescaled.
+#include <atomic>
+
+#include "kv_device.cuh"
+#include "kv_internal.h"
 
 namespace pkm {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kCheckWarp = 11;
+constexpr int kThreads = 12 * 32;
+// Registers of the two softmax groups and of the issuing and loading warps, of the 3 x 168 that
+// the block starts with.
+constexpr int kStartRegs = 168, kSoftRegs = 208, kIssueRegs = 88;
+static_assert(2 * kSoftRegs + kIssueRegs <= 3 * kStartRegs, "registers of the block");
+constexpr int kTile = 128;          // keys of a tile, rows of a tile of queries
+constexpr int kMaxStages = 8;       // tiles of keys or values in flight
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOutCol = 256;   // O of stage s at kOutCol + s * D, scores at s * 128
+constexpr int kItemCost = 1;        // an item's start and end, in tiles
+constexpr uint64_t kDrainNs = 1000000;  // a role that gave up leaves its loads time to land
+constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
-template <int E>  // columns of a lane
-__global__ void __launch_bounds__(kWarps * 32) kv_attention_kernel(const KvAttentionArgs a) {
+// a / b; the 64-bit division is a long routine, and the operands are hardly ever that large.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// Sum of floor((a * i + b) / m) over i < n, for a, b >= 0: Euclid's steps on a and m.
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t sum = 0;
+    while (n > 0) {
+        if (a >= m) {
+            const int64_t k = quotient(a, m);
+            sum += (n & 1 ? n * ((n - 1) / 2) : (n / 2) * (n - 1)) * k;
+            a -= k * m;
+        }
+        if (b >= m) {
+            const int64_t k = quotient(b, m);
+            sum += n * k;
+            b -= k * m;
+        }
+        const int64_t y = a * n + b;
+        if (y < m) break;
+        n = quotient(y, m);
+        b = y - n * m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+
+// One request as the schedule sees it.  Item j has its tokens from j * T on.
+struct Request {
+    int64_t first;   // its first row
+    int64_t len;     // cached tokens before its new ones
+    int32_t n;       // its new tokens (0 too where the page table does not hold them all)
+    int32_t items;   // of one head of keys
+
+    __device__ __forceinline__ bool load(const KvAttentionArgs& a, int b) {
+        const int64_t rows = a.total_rows;
+        const int64_t lo = min(static_cast<int64_t>(__ldg(a.row_offsets + b)), rows);
+        const int64_t hi = min(static_cast<int64_t>(__ldg(a.row_offsets + b + 1)), rows);
+        first = lo;
+        n = hi > lo ? static_cast<int32_t>(hi - lo) : 0;
+        len = __ldg(a.cache_lengths + b);
+        const bool held = len + n <= static_cast<int64_t>(a.max_pages) * a.page_size;
+        if (!held) n = 0;
+        items = (n + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+        return held;
+    }
+    // Tiles that hold the first tokens, and those between them and the window of the token at
+    // position p.
+    __device__ __forceinline__ int32_t gap(const KvAttentionArgs& a, int64_t p) const {
+        if (a.window == 0) return 0;
+        const int64_t from = p - a.window + 1;
+        return from <= 0 ? 0 : max(static_cast<int32_t>(from >> 7) - a.sink_tiles, 0);
+    }
+    __device__ __forceinline__ int32_t tokens(const KvAttentionArgs& a, int32_t j) const {
+        return min(2 * a.tile_tokens, n - j * 2 * a.tile_tokens);
+    }
+    __device__ __forceinline__ int32_t tiles(const KvAttentionArgs& a, int32_t j) const {
+        const int64_t at = len + static_cast<int64_t>(j) * 2 * a.tile_tokens;
+        return static_cast<int32_t>((at + tokens(a, j) + kTile - 1) >> 7) - gap(a, at);
+    }
+    // Units of the items before j < items; an item has kItemCost besides its tiles.
+    __device__ __forceinline__ int64_t units_before(const KvAttentionArgs& a, int64_t j) const {
+        const int64_t t = 2 * a.tile_tokens;
+        int64_t sum = kItemCost * j + floor_sum(j, kTile, t, len + t + kTile - 1);
+        if (a.window > 0) {
+            // the first item whose gap is not below 0
+            const int64_t from = len - a.window + 1 - static_cast<int64_t>(a.sink_tiles) * kTile;
+            const int64_t j0 = from >= 0 ? 0 : quotient(t - 1 - from, t);
+            if (j > j0) sum -= floor_sum(j - j0, kTile, t, from + j0 * t);
+        }
+        return sum;
+    }
+    __device__ __forceinline__ int64_t head_units(const KvAttentionArgs& a) const {
+        return n == 0 ? 0 : units_before(a, items - 1) + tiles(a, items - 1) + kItemCost;
+    }
+};
+
+struct Bars {
+    uint64_t full[kMaxStages];   // a tile of keys or values is there
+    uint64_t empty[kMaxStages];  // its MMAs are done
+    uint64_t own[kMaxStages];    // values that are looked through first are there
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2];          // a step's scores are complete
+    uint64_t p_full[2];          // its weights are written
+    uint64_t o_full[2];          // an item's last step on the stage is done
+    uint64_t o_empty[2];         // its O has been read
+    uint64_t stats_full[2];      // the other stage's maxima and sums, for the stage that joins both
+    uint64_t mma_done;
+    float2 stats[kTile];
+    int64_t scratch[kThreads / 32];
+    int64_t units;               // units of all items
+    int64_t first_unit;          // this CTA's share begins here
+    int64_t share;               // and has so many units
+    int64_t into;                // units of its first request before it
+    int32_t request, head, item, unit;  // its first unit
+    uint32_t nonfinite[8];       // parts, by number, that had infinities or NaN looked through
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <int DB>  // 64-column blocks of a head
+struct Shape {
+    static constexpr int kCols = DB * 64;
+    static constexpr int kBytes = DB * 128 * 128;   // of a tile
+    static constexpr int kStages = DB == 2 ? 5 : 8;
+    static constexpr size_t kOffRing = 2 * size_t(kBytes);
+    static constexpr size_t kOffBars = kOffRing + size_t(kStages) * kBytes;
+    static constexpr size_t kSmem = kOffBars + sizeof(Bars);
+    static_assert(kSmem <= 232448, "shared memory budget of one sm_103a CTA");
+};
+
+// A CTA's share of the units of all items, walked item by item.  After next() returned true the
+// part is tiles [x0, x1) of the item's list, which all roles take from the last to the first.
+struct Walk {
+    int64_t u;       // first unit behind the part
+    int64_t left;    // units of the share behind the part
+    int32_t at;      // unit of the item behind the part
+    int32_t b, head, item;
+    Request r;
+    int32_t units_each;         // units of the item
+    int32_t token0, tokens;     // of the request
+    int32_t tiles, gap, x0, x1;
+
+    __device__ __forceinline__ Walk(const KvAttentionArgs& a, const Bars* bars) {
+        left = bars->share;
+        u = bars->first_unit;
+        b = bars->request;
+        head = bars->head;
+        item = bars->item;
+        at = bars->unit;
+        if (left > 0) {
+            r.load(a, b);
+            set_item(a);
+        }
+    }
+    __device__ __forceinline__ void set_item(const KvAttentionArgs& a) {
+        token0 = item * 2 * a.tile_tokens;
+        tokens = r.tokens(a, item);
+        tiles = r.tiles(a, item);
+        gap = r.gap(a, r.len + token0);
+        units_each = tiles + kItemCost;
+    }
+    __device__ __forceinline__ bool next(const KvAttentionArgs& a) {
+        do {
+            if (left <= 0) return false;
+            if (at == units_each) {
+                at = 0;
+                if (++item == r.items) {
+                    item = 0;
+                    if (++head == a.num_kv_heads) {
+                        head = 0;
+                        do r.load(a, ++b);  // units are left: a request further on has them
+                        while (r.n == 0);
+                    }
+                }
+                set_item(a);
+            }
+            const int32_t take = static_cast<int32_t>(min(static_cast<int64_t>(units_each - at), left));
+            x0 = max(at - kItemCost, 0);
+            at += take;
+            x1 = max(at - kItemCost, 0);
+            u += take;
+            left -= take;
+        } while (x1 == x0);  // a share can end within an item's first units
+        return true;
+    }
+    __device__ __forceinline__ bool wide(const KvAttentionArgs& a) const { return tokens > a.tile_tokens; }
+    __device__ __forceinline__ int32_t tile(const KvAttentionArgs& a, int32_t x) const {
+        return gap > 0 && x >= a.sink_tiles ? x + gap : x;
+    }
+    // Whether some of the tokens, the first of them at position p, do not attend all of the tile.
+    __device__ __forceinline__ bool partial(const KvAttentionArgs& a, int32_t kt, int64_t p, int32_t count) const {
+        const int64_t c0 = static_cast<int64_t>(kt) * kTile;
+        if (c0 + kTile - 1 > p) return true;
+        return a.window > 0 && c0 <= p + count - 1 - a.window && c0 + kTile > a.sinks;
+    }
+    __device__ __forceinline__ bool partial(const KvAttentionArgs& a, int32_t kt) const {
+        return partial(a, kt, r.len + token0, tokens);
+    }
+    // Whether the item reads any of the positions pos .. pos + count - 1 of one page: those past its
+    // last token may have no page yet, and the pages between the first tokens and the window none
+    // any more.
+    __device__ __forceinline__ bool reads(const KvAttentionArgs& a, int64_t pos, int32_t count) const {
+        if (pos >= r.len + token0 + tokens) return false;
+        return a.window == 0 || pos < a.sinks || pos + count > r.len + token0 - a.window + 1;
+    }
+};
+
+// Counts the units of all requests and cuts out the CTA's share; every thread sums a run of
+// requests, and a warp finds the item within the request.
+__device__ __forceinline__ void plan(const KvAttentionArgs& a, Bars* bars) {
+    const int64_t per = (static_cast<int64_t>(a.batch) + kThreads - 1) / kThreads, all = a.batch;
+    const int b0 = static_cast<int>(min(threadIdx.x * per, all));
+    const int b1 = static_cast<int>(min(b0 + per, all));
+    int64_t sum = 0, last = 0;
+    Request r;
+    for (int b = b0; b < b1; ++b) {
+        if (!r.load(a, b)) report(a.status, PKM_ERR_OUT_OF_RANGE);
+        last = r.head_units(a) * a.num_kv_heads;
+        sum += last;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = sum;
+#pragma unroll
+    for (int sh = 1; sh < 32; sh <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, sh);
+        if (lane >= sh) incl += o;
+    }
+    if (lane == 31) bars->scratch[warp] = incl;
+    if (threadIdx.x == 0) bars->share = 0;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += bars->scratch[w];
+        total += bars->scratch[w];
+    }
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+    const int64_t u = blockIdx.x < ctas ? quotient(total * blockIdx.x, ctas) : -1;
+    if (threadIdx.x == 0) bars->units = total;
+    int64_t at = before + incl - sum;
+    if (at <= u && u < at + sum)
+        for (int b = b0; b < b1; ++b) {
+            if (per > 1) {
+                r.load(a, b);
+                last = r.head_units(a) * a.num_kv_heads;
+            }
+            if (u < at + last) {
+                bars->first_unit = u;
+                bars->share = quotient(total * (blockIdx.x + 1), ctas) - u;
+                bars->request = b;
+                bars->into = u - at;
+                break;
+            }
+            at += last;
+        }
+    __syncthreads();
+    if (warp != 0 || bars->share == 0) return;
+    r.load(a, bars->request);
+    const int64_t each = r.head_units(a);
+    const int64_t head = quotient(bars->into, each), into = bars->into - head * each;
+    int64_t lo = 0, n = r.items, passed = 0;  // the last item with no more units before it
+    while (n > 1) {
+        const int64_t step = (n + 31) / 32, j = lane * step;
+        const int64_t units = j < n ? r.units_before(a, lo + j) : INT64_MAX;
+        const uint32_t below = __ballot_sync(0xffffffffu, units <= into);
+        const int k = 31 - __clz(static_cast<int>(below));
+        passed = __shfl_sync(0xffffffffu, units, k);
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    if (lane == 0) {
+        bars->head = static_cast<int32_t>(head);
+        bars->item = static_cast<int32_t>(lo);
+        bars->unit = static_cast<int32_t>(into - passed);
+    }
+}
+
+// Page and slot of position pos of request b if it is read; page -1 (loads as zeros) if not and
+// for ids that the cache does not have, which are reported.
+struct Place {
+    int32_t page, slot;
+    __device__ __forceinline__ Place(const KvAttentionArgs& a, int b, int64_t pos, bool read)
+        : page(-1), slot(0) {
+        if (!read) return;
+        const int64_t lp = quotient(pos, a.page_size);
+        slot = static_cast<int32_t>(pos - lp * a.page_size);
+        const uint32_t id = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
+        if (id < static_cast<uint32_t>(a.num_pages)) page = static_cast<int32_t>(id);
+        else report(a.status, PKM_ERR_OUT_OF_RANGE);
+    }
+    // Offset of the slot in the layer, or -1.
+    __device__ __forceinline__ int64_t offset(const KvAttentionArgs& a) const {
+        return page < 0 ? -1 : page * a.page_stride + slot * a.slot_stride;
+    }
+};
+
+// Infinities and NaN of a packed pair of bf16 become zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+    return w;
+}
+
+// Whether there are any: an exponent of ones carries into the sign's place.
+__device__ __forceinline__ bool any_nonfinite(const uint4& v) {
+    const auto top = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
+    return ((top(v.x) | top(v.y) | top(v.z) | top(v.w)) & 0x80008000u) != 0;
+}
+
+// Makes the infinities and NaN of a tile of values zero; whether there were any before row `end`.
+template <int DB>
+__device__ __forceinline__ bool look_through(uint32_t tile, int64_t end) {
     const int lane = threadIdx.x & 31;
-    const int64_t all = static_cast<int64_t>(a.total_rows) * a.num_heads;
-    const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (task >= all) return;
-    const int64_t r = task / a.num_heads;
-    const int h = static_cast<int>(task % a.num_heads);
-    const int kvh = h / (a.num_heads / a.num_kv_heads);
-    int b = -1;
-    for (int lo = 0, hi = a.batch; b < 0;) {
-        if (hi - lo <= 1) b = lo;
-        else if (__ldg(a.row_offsets + (lo + hi) / 2) <= r) lo = (lo + hi) / 2;
-        else hi = (lo + hi) / 2;
-    }
-    if (r < __ldg(a.row_offsets + b) || r >= __ldg(a.row_offsets + b + 1)) return;
-    const int64_t p = static_cast<int64_t>(__ldg(a.cache_lengths + b)) + r - __ldg(a.row_offsets + b);
-    const uint16_t* q = a.q + r * a.q_row_stride + h * a.q_head_stride + lane * E;
-    float qv[E], o[E] = {};
-    for (int e = 0; e < E; e += 2) bf16x2_to_f32(*reinterpret_cast<const uint32_t*>(q + e), qv[e], qv[e + 1]);
-    float m = -INFINITY, l = 0.0f;
-    int64_t first = 0;
-    if (a.window > 0 && p >= a.window) first = p + 1 - a.window;
-    const int64_t sinks = min(first, static_cast<int64_t>(a.sinks));
-    for (int64_t n = 0; n < sinks + p + 1 - first; ++n) {
-        const int64_t t = n < sinks ? n : first + n - sinks;
-        const int64_t lp = t / a.page_size;
-        uint32_t page = UINT32_MAX;
-        if (lp < a.max_pages) page = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
-        if (page >= static_cast<uint32_t>(a.num_pages)) {
-            if (lane == 0) report(a.status, PKM_ERR_OUT_OF_RANGE);
-            continue;
-        }
-        const uint16_t* k = a.cache_layer + page * a.page_stride + (t % a.page_size) * a.slot_stride +
-                            kvh * a.head_size + lane * E;
-        float s = 0.0f, x[E];
-        for (int e = 0; e < E; e += 2) {
-            bf16x2_to_f32(*reinterpret_cast<const uint32_t*>(k + e), x[e], x[e + 1]);
-            s += qv[e] * x[e] + qv[e + 1] * x[e + 1];
-        }
-        for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= a.scale * kLog2e;
-        const float top = fmaxf(m, s);
-        const float back = m == -INFINITY ? 0.0f : exp2f(m - top);
-        const float w = exp2f(s - top);
-        m = top;
-        l = l * back + w;
-        for (int e = 0; e < E; e += 2) {
-            bf16x2_to_f32(*reinterpret_cast<const uint32_t*>(k + a.kv_stride + e), x[e], x[e + 1]);
-            o[e] = o[e] * back + w * x[e];
-            o[e + 1] = o[e + 1] * back + w * x[e + 1];
+    bool found = false;
+    // 32 lanes take 512 bytes, four rows of a block; the place in the block does not matter
+#pragma unroll 1
+    for (int i = 0; i < DB * 32; i += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = ld_shared_v4(tile + (i + k) * 512 + lane * 16);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (!any_nonfinite(v[k])) continue;
+            const int at = (i + k) * 4 + (lane >> 3);  // row among all blocks' rows
+            const int row = at / (8 * DB) * 8 + (at & 7);
+            found = found || row < end;
+            st_shared_v4(tile + (i + k) * 512 + lane * 16, finite2(v[k].x), finite2(v[k].y),
+                         finite2(v[k].z), finite2(v[k].w));
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(a.out + task * a.head_size + lane * E + e) =
-            pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-    if (lane == 0 && a.lse != nullptr) a.lse[task] = m * kLn2 + logf(l);
+    return __any_sync(0xffffffffu, found);
+}
+
+// Which of the 32 keys from c0 on (relative to the tile) a row attends: those up to hi, from lo on
+// or below sinks.
+__device__ __forceinline__ uint32_t attended(int64_t hi, int64_t lo, int64_t sinks, int c0) {
+    const auto below = [](int64_t n) -> uint32_t {
+        return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+    };
+    return below(hi + 1 - c0) & (~below(lo - c0) | below(sinks - c0));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Waits with all lanes of a warp; the verdict is the same in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
+    return __all_sync(0xffffffffu, mbar_wait_inl(bar, parity, wc));
+}
+
+template <int DB, bool TMA>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attention_kernel(const __grid_constant__ KvMaps maps, const KvAttentionArgs a,
+                        const KvWorkspace ws) {
+    using S = Shape<DB>;
+    constexpr int D = S::kCols;
+    extern __shared__ __align__(1024) uint8_t smem[];  // swizzle atoms of 1024 bytes
+    uint8_t* sQ = smem;
+    uint8_t* ring = smem + S::kOffRing;
+    Bars* bars = reinterpret_cast<Bars*>(smem + S::kOffBars);
+    // the same in every lane, seen by the compiler through the shuffle
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->empty[i], 1);
+            mbar_init(&bars->own[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->q_full[i], 1);
+            mbar_init(&bars->q_empty[i], 1);
+            mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_full[i], 4);
+            mbar_init(&bars->o_full[i], 1);
+            mbar_init(&bars->o_empty[i], 4);
+            mbar_init(&bars->stats_full[i], 4);
+        }
+        mbar_init(&bars->mma_done, 1);
+        for (int i = 0; i < 8; ++i) bars->nonfinite[i] = 0;
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kKeyWarp && lane == 0) {
+        tma_prefetch_map(&maps.q);
+        tma_prefetch_map(&maps.q_one);
+        if (TMA) {
+            tma_prefetch_map(&maps.k);
+            tma_prefetch_map(&maps.v);
+        }
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&bars->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    griddep_wait();  // launched while the work before may still run: nothing is read before
+    plan(a, bars);
+    griddep_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
+    const WaitCtl wc{&bars->abort_flag, a.status, a.timeout_ns};
+    // The softmax warps keep the time limit: whatever stalls stalls them.  The issuing and loading
+    // warps' waits end with their abort flag, or after tries that take longer.
+    const uint32_t tries = static_cast<uint32_t>(min(a.timeout_ns / 8, uint64_t{UINT32_MAX}));
+    const auto issue_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_flag(bar, parity, wc.abort_flag, tries));
+    };
+
+    if (warp < kMmaWarp) {
+        // ---------------- softmax and epilogue: row = lane of tensor memory ----------------
+        warpgroup_reg_alloc<kSoftRegs>();
+        Walk w(a, bars);
+        const int stage = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;
+        const int group = a.num_heads / a.num_kv_heads;
+        const int row_token = row / group, row_head = row - row_token * group;
+        const float scale2 = a.scale * kLog2e;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t scores = lanes + stage * 128;
+        const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+        const int64_t sharing = min(static_cast<int64_t>(gridDim.x), bars->units);
+        uint32_t n = 0, part = 0;
+        uint32_t use_phase = 0, join_phase = 0;  // a bit for each stage
+        KvItem left{0, 0, 0, 0};
+        bool ok = true;
+        while (ok && w.next(a)) {
+            const bool wide = w.wide(a);
+            const int tiles = w.x1 - w.x0, steps = wide ? 2 * tiles : tiles;
+            const int first_stage = n & 1, mine = stage ^ first_stage;  // the stage's first step
+            const int sub = wide ? mine : 0;                            // its tile of queries
+            const int32_t token0 = w.token0 + sub * a.tile_tokens;
+            const int count = min(a.tile_tokens, w.tokens - sub * a.tile_tokens);
+            const bool valid = row_token < count;
+            const bool busy = (warp & 3) * 32 < count * group;  // the warp has rows
+            const int64_t pos0 = w.r.len + token0, pos = pos0 + row_token;
+            float m = -INFINITY, l = 0.0f;
+            for (int x = mine; x < steps; x += 2) {
+                const int32_t kt = w.tile(a, w.x1 - 1 - (wide ? x >> 1 : x));
+                if (!warp_wait(&bars->s_full[stage], ((n + x) >> 1) & 1, wc)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (busy) {
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_ld_x32(scores + k * 32, s[k]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) asm volatile("" : "+r"(s[c >> 5][c & 31]));  // not before
+                    const auto f = [&](int c) -> float { return __uint_as_float(s[c >> 5][c & 31]); };
+                    const bool masked = w.partial(a, kt, pos0, count);
+                    float mul = scale2;
+                    if (masked || scale2 < 0.0f) {
+                        // scaled before masks and maxima, which then need not know the sign
+                        mul = 1.0f;
+                        const int64_t c0 = static_cast<int64_t>(kt) * kTile;
+                        const int64_t lo = a.window > 0 ? pos - a.window + 1 - c0 : 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t may = masked ? attended(pos - c0, lo, a.sinks - c0, k * 32) : ~0u;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const float v = __uint_as_float(s[k][c]) * scale2;
+                                s[k][c] = __float_as_uint((may >> c) & 1u ? v : -INFINITY);
+                            }
+                        }
+                    }
+                    float t0 = f(0), t1 = f(1), t2 = f(2), t3 = f(3);
+#pragma unroll
+                    for (int c = 4; c < 128; c += 4) {
+                        t0 = fmaxf(t0, f(c));
+                        t1 = fmaxf(t1, f(c + 1));
+                        t2 = fmaxf(t2, f(c + 2));
+                        t3 = fmaxf(t3, f(c + 3));
+                    }
+                    const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * mul;
+                    const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+                    const float m_new = move ? top : m;
+                    const float back = move && m > -INFINITY ? exp2_approx(m - m_new) : 1.0f;
+                    m = m_new;
+                    const float ref = m == -INFINITY ? 0.0f : m;
+                    // The stage's step before is done (its MMAs were issued before this step's
+                    // scores), so O holds still.
+                    if (x > mine && __any_sync(0xffffffffu, back != 1.0f)) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld_x32(lanes + kOutCol + stage * D + c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * back);
+                            tmem_st_x32(lanes + kOutCol + stage * D + c, o);
+                        }
+                    }
+                    // The weights are rounded to bf16, by up to 2^-8 of each: the second product's
+                    // operands have one type, and the values are bf16.  Their sum stays in fp32,
+                    // unrounded.
+                    float sum[4] = {};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int c = h * 64 + 2 * k;
+                            float e0, e1;
+                            fma2x(e0, e1, f(c), f(c + 1), mul, mul, -ref, -ref);
+                            e0 = exp2_approx(e0);
+                            e1 = exp2_approx(e1);
+                            add2(sum[2 * (k & 1)], sum[2 * (k & 1) + 1], e0, e1);
+                            p[k] = pack_bf16x2(e0, e1);
+                        }
+                        tmem_st_x32(scores + h * 32, p);
+                    }
+                    l = l * back + ((sum[0] + sum[2]) + (sum[1] + sum[3]));
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_full[stage]);
+            }
+            const bool join = !wide && steps > 1;   // the first step's stage joins both
+            n += steps;
+            ++part;
+            const uint32_t o_phase = use_phase, joined = join_phase >> first_stage & 1;
+            use_phase ^= steps > 1 ? 3u : 1u << first_stage;
+            join_phase ^= join ? 1u << first_stage : 0u;
+            if (!ok || mine >= steps) continue;
+            ok = warp_wait(&bars->o_full[stage], o_phase >> stage & 1, wc);
+            if (!ok) break;
+            if (join && mine == 1) {
+                bars->stats[row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->stats_full[first_stage]);
+                continue;
+            }
+            float f0 = 1.0f, f1 = 0.0f;  // factors of this stage's sums and of the other's
+            if (join) {
+                ok = warp_wait(&bars->o_full[stage ^ 1], o_phase >> (stage ^ 1) & 1, wc) &&
+                     warp_wait(&bars->stats_full[stage], joined, wc);
+                if (!ok) break;
+                const float2 other = bars->stats[row];
+                const float top = fmaxf(m, other.x);
+                f0 = m == -INFINITY ? 0.0f : exp2_approx(m - top);
+                f1 = other.x == -INFINITY ? 0.0f : exp2_approx(other.x - top);
+                l = l * f0 + other.y * f1;
+                m = top;
+            }
+            tc_fence_after();
+            const bool whole = w.x0 == 0 && w.x1 == w.tiles;
+            const float inv = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+            const bool mend = *const_cast<volatile uint32_t*>(&bars->nonfinite[(part - 1) & 7]) == part;
+            const int64_t out_row = (w.r.first + token0 + row_token) * a.num_heads + w.head * group + row_head;
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.x0 > 0 ? 0 : 1);
+            const int slot_row = sub * kTile + row;
+            if (busy) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld_x32(lanes + kOutCol + stage * D + c, o);
+                    if (join) {
+                        uint32_t o1[32];
+                        tmem_ld_x32(lanes + kOutCol + (stage ^ 1) * D + c, o1);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
+                    } else {
+                        tmem_ld_wait();
+                    }
+                    if (valid && mend) {
+                        // values that were made zero for the rows that do not attend them
+                        for (int x = w.x0; x < w.x1; ++x) {
+                            const int32_t kt = w.tile(a, x);
+                            if (!w.partial(a, kt)) continue;
+                            for (int t = 0; t < kTile; ++t) {
+                                const int64_t at = static_cast<int64_t>(kt) * kTile + t;
+                                if (at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks)) continue;
+                                const int64_t from = Place(a, w.b, at, true).offset(a);
+                                if (from < 0) continue;
+                                const uint16_t* v = a.cache_layer + a.kv_stride + from + w.head * D + c;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) {
+                                    const uint32_t bits = __ldg(v + k);
+                                    if ((bits & 0x7f80u) == 0x7f80u)
+                                        o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(bits << 16));
+                                }
+                            }
+                        }
+                    }
+                    if (valid && whole) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            p[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                        uint16_t* to = a.out + out_row * D + c;
+                        if (sectors) {
+                            st_v8(to, p);
+                            st_v8(to + 16, p + 8);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                st_v4(to + 8 * k, make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]));
+                        }
+                    } else if (valid) {
+                        float* to = reinterpret_cast<float*>(a.workspace) + (slot * ws.rows + slot_row) * D + c;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) st_v8(to + 8 * k, o + 8 * k);
+                    }
+                    __syncwarp();
+                }
+                if (valid && whole && a.lse != nullptr)
+                    a.lse[out_row] = l != 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+                if (valid && !whole)
+                    reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + slot_row] = make_float2(m, l);
+            }
+            if (!whole && w.x0 == 0) {
+                const int64_t end = w.u + (w.units_each - w.at);
+                left.row = w.r.first + w.token0;
+                left.head = w.head * group;
+                left.tokens = w.tokens;
+                left.parts = static_cast<int32_t>(quotient(end * sharing - 1, bars->units) - blockIdx.x) + 1;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars->o_empty[stage]);
+                if (join) mbar_arrive(&bars->o_empty[stage ^ 1]);
+            }
+        }
+        // a stage that had no step of the item that is left does not know it: the other writes it
+        if ((warp & 3) == 0 && lane == 0) {
+            KvItem* items = reinterpret_cast<KvItem*>(a.workspace + ws.items);
+            if (!ok) left.tokens = 0;
+            items[2 * blockIdx.x + stage] = left;
+        }
+    } else {
+        warpgroup_reg_dealloc<kIssueRegs>();
+        if (warp == kMmaWarp) {
+            // ---------------- MMA issuer, all lanes together ----------------
+            Walk w(a, bars);
+            // A wait that runs out is looked at once a step; what is issued until then is not used.
+            bool failed = false;
+            const auto wait = [&](uint64_t* bar, uint32_t parity) {
+                failed |= !mbar_wait_flag(bar, parity, wc.abort_flag, tries);
+            };
+            const uint32_t id_s = idesc_bf16(128, kTile, false, false);
+            const uint32_t id_o = idesc_bf16(128, D, false, true);
+            const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(smem_u32(ring), 16, DB * 1024);
+            const uint64_t v_desc = sdesc_sw128(smem_u32(ring), 1024, DB * 1024);
+            // what is to be done for the steps whose values come next, eight bits a stage
+            constexpr uint32_t kAny = 1, kFirst = 2, kLast = 4, kFetch = 8, kRelease = 16;
+            uint32_t ahead = 0;
+            RingPos kpos, vpos;
+            vpos.next(S::kStages);
+            uint32_t n = 0, done = 0, queries = 0;
+            uint32_t empty_phase = 3;  // a bit for each stage; the first wait passes
+            // O (+)= P V of the step `done`
+            const auto values = [&](int s) {
+                const uint32_t st = ahead >> (8 * s);
+                ahead &= ~(0xffu << (8 * s));
+                wait(&bars->p_full[s], (done >> 1) & 1);
+                if (st & kFirst) {
+                    wait(&bars->o_empty[s], empty_phase >> s & 1);
+                    empty_phase ^= 1u << s;
+                }
+                if (st & kFetch) wait(&bars->full[vpos.stage], vpos.phase);
+                tc_fence_after();
+                const uint64_t vd = desc_add_bytes(v_desc, vpos.stage * S::kBytes);
+                const uint32_t d = tmem + kOutCol + s * D, p = tmem + s * 128;
+                const uint32_t keep = st & kFirst ? 0u : 1u;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)  // 16 keys: two atoms of each block
+                    mma_bf16_ts_elect(d, p + 8 * k, desc_add_bytes(vd, k * 2 * DB * 1024), id_o,
+                                      k > 0 ? 1u : keep);
+                if (st & kRelease) {
+                    mma_commit_elect(&bars->empty[vpos.stage]);
+                    vpos.next(S::kStages);
+                    vpos.next(S::kStages);
+                }
+                if (st & kLast) mma_commit_elect(&bars->o_full[s]);
+                ++done;
+            };
+            while (!__any_sync(0xffffffffu, failed) && __any_sync(0xffffffffu, w.next(a))) {
+                const bool wide = __any_sync(0xffffffffu, w.wide(a));
+                const int tiles = __shfl_sync(0xffffffffu, w.x1 - w.x0, 0);
+                const int steps = wide ? 2 * tiles : tiles;
+#pragma unroll 1
+                for (int x = 0; x < steps; ++x, ++n) {
+                    const int s = n & 1;
+                    if (ahead >> (8 * s) & kAny) values(s);
+                    const bool odd = x & 1;
+                    const uint32_t q = wide && odd ? (queries + 1) & 1 : queries & 1;
+                    if (x == 0 || (wide && x == 1)) {
+                        const uint32_t qn = queries + x;
+                        // the step before is not held up by queries that are not there yet
+                        if (!__all_sync(0xffffffffu, mbar_try_wait(&bars->q_full[q], (qn >> 1) & 1)) &&
+                            x == 0 && (ahead >> (8 * (s ^ 1)) & kAny))
+                            values(s ^ 1);
+                        wait(&bars->q_full[q], (qn >> 1) & 1);
+                    }
+                    if (!wide || !odd) wait(&bars->full[kpos.stage], kpos.phase);
+                    tc_fence_after();
+                    const uint64_t qd = desc_add_bytes(q_desc, q * S::kBytes);
+                    const uint64_t kd = desc_add_bytes(k_desc, kpos.stage * S::kBytes);
+#pragma unroll
+                    for (int kb = 0; kb < DB; ++kb)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_elect(tmem + s * 128, desc_add_bytes(qd, kb * 16384 + k * 32),
+                                           desc_add_bytes(kd, kb * 1024 + k * 32), id_s,
+                                           (kb | k) != 0 ? 1u : 0u);
+                    mma_commit_elect(&bars->s_full[s]);
+                    if (!wide || odd) {
+                        mma_commit_elect(&bars->empty[kpos.stage]);
+                        kpos.next(S::kStages);
+                        kpos.next(S::kStages);
+                    }
+                    if (wide ? x >= steps - 2 : x == steps - 1) mma_commit_elect(&bars->q_empty[q]);
+                    ahead |= (kAny | (x < 2 ? kFirst : 0u) | (x >= steps - 2 ? kLast : 0u) |
+                              (!wide || !odd ? kFetch : 0u) | (!wide || odd ? kRelease : 0u))
+                             << (8 * s);
+                    if (__any_sync(0xffffffffu, failed)) break;
+                }
+                queries += wide ? 2 : 1;
+            }
+            if (!__any_sync(0xffffffffu, failed)) {
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    const int s = (n + k) & 1;
+                    if (ahead >> (8 * s) & kAny) values(s);
+                }
+            }
+            mma_commit_elect(&bars->mma_done);
+            mbar_wait_inl(&bars->mma_done, 0, wc, false);
+        } else {
+            // ---------------- queries, keys, values ----------------
+            const bool keys = warp == kKeyWarp;
+            const uint16_t* plane = a.cache_layer + (keys ? 0 : a.kv_stride);
+            Walk w(a, bars);
+            RingPos at;
+            if (!keys) at.next(S::kStages);
+            uint32_t queries = 0, part = 0, own_phase = 0;
+            bool ok = true;
+            const auto next_tile = [&] {
+                at.next(S::kStages);
+                at.next(S::kStages);
+            };
+            const auto load_queries = [&]() -> bool {
+                const int subs = w.wide(a) ? 2 : 1;
+                for (int sub = 0; sub < subs; ++sub, ++queries) {
+                    const uint32_t q = queries & 1;
+                    if (!issue_wait(&bars->q_empty[q], ((queries >> 1) & 1) ^ 1)) return false;
+                    const int group = a.num_heads / a.num_kv_heads;
+                    const int32_t token0 = w.token0 + sub * a.tile_tokens;
+                    const bool one = w.tokens - sub * a.tile_tokens == 1;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&bars->q_full[q], DB * 128 * group * (one ? 1 : a.tile_tokens));
+                    __syncwarp();
+                    if (lane < DB)
+                        tma_load_3d(sQ + q * S::kBytes + lane * 16384, one ? &maps.q_one : &maps.q,
+                                    &bars->q_full[q], lane * 64, w.head * group,
+                                    static_cast<int32_t>(w.r.first + token0));
+                }
+                return true;
+            };
+            // the tile's infinities and NaN, where not every row attends every key
+            const auto mend = [&](uint32_t stage, int32_t kt) {
+                const int64_t end = w.r.len + w.token0 + w.tokens - static_cast<int64_t>(kt) * kTile;
+                if (look_through<DB>(smem_u32(ring) + stage * S::kBytes, end) && lane == 0)
+                    *const_cast<volatile uint32_t*>(&bars->nonfinite[part & 7]) = part + 1;
+            };
+            if constexpr (TMA) {
+                const int slots = maps.slots, boxes = kTile / slots;
+                if (warp == kCheckWarp) {
+                    for (; ok && __any_sync(0xffffffffu, w.next(a)); ++part)
+                        for (int x = w.x1 - 1; ok && x >= w.x0; --x, next_tile()) {
+                            const int32_t kt = w.tile(a, x);
+                            if (!w.partial(a, kt)) continue;
+                            ok = issue_wait(&bars->own[at.stage], (own_phase >> at.stage) & 1);
+                            if (!ok) break;
+                            own_phase ^= 1u << at.stage;
+                            mend(at.stage, kt);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars->full[at.stage]);
+                        }
+                } else {
+                    const CUtensorMap* map = keys ? &maps.k : &maps.v;
+                    while (ok && __any_sync(0xffffffffu, w.next(a))) {
+                        if (keys) ok = load_queries();
+                        for (int x = w.x1 - 1; ok && x >= w.x0; --x, next_tile()) {
+                            const int32_t kt = w.tile(a, x);
+                            const int64_t pos = static_cast<int64_t>(kt) * kTile + lane * slots;
+                            const Place place(a, w.b, pos, lane < boxes && w.reads(a, pos, slots));
+                            ok = issue_wait(&bars->empty[at.stage], at.phase ^ 1);
+                            if (!ok) break;
+                            uint64_t* bar = &bars->full[at.stage];
+                            if (!keys && w.partial(a, kt)) bar = &bars->own[at.stage];
+                            if (lane == 0) mbar_arrive_expect_tx(bar, S::kBytes);
+                            __syncwarp();
+                            if (lane < boxes)
+                                tma_load_5d(ring + at.stage * S::kBytes + lane * slots * DB * 128, map, bar,
+                                            0, 0, w.head * DB, place.slot >> 3, place.page);
+                        }
+                    }
+                }
+                if (!ok) spin_ns(kDrainNs);
+            } else if (warp != kCheckWarp) {
+                // Row by row: a row's 16-byte chunks to their places in the swizzled atoms.  A tile
+                // is handed over when the next one is on its way, or before any longer wait.
+                bool pending = false;
+                uint32_t pending_stage = 0, pending_part = 0;
+                int32_t pending_kt = 0;
+                int64_t pending_end = 0;
+                bool pending_partial = false;
+                const auto hand_over = [&] {
+                    if (pending_partial &&
+                        look_through<DB>(smem_u32(ring) + pending_stage * S::kBytes,
+                                         pending_end - static_cast<int64_t>(pending_kt) * kTile) &&
+                        lane == 0)
+                        *const_cast<volatile uint32_t*>(&bars->nonfinite[pending_part & 7]) = pending_part + 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->full[pending_stage]);
+                    pending = false;
+                };
+                const auto flush = [&] {
+                    cp_async_wait<0>();
+                    __syncwarp();
+                    if (pending) hand_over();
+                };
+                constexpr int kChunks = DB * 8, kRows = 32 / kChunks;  // of a row; rows at once
+                const int chunk = lane % kChunks;
+                for (; ok && __any_sync(0xffffffffu, w.next(a)); ++part) {
+                    if (keys) {
+                        flush();
+                        ok = load_queries();
+                    }
+                    const int64_t end = w.r.len + w.token0 + w.tokens;
+                    for (int x = w.x1 - 1; ok && x >= w.x0; --x, next_tile()) {
+                        const int32_t kt = w.tile(a, x);
+                        int64_t offset[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int64_t pos = static_cast<int64_t>(kt) * kTile + k * 32 + lane;
+                            offset[k] = Place(a, w.b, pos, w.reads(a, pos, 1)).offset(a);
+                        }
+                        if (!__all_sync(0xffffffffu, mbar_try_wait(&bars->empty[at.stage], at.phase ^ 1))) {
+                            flush();
+                            ok = issue_wait(&bars->empty[at.stage], at.phase ^ 1);
+                            if (!ok) break;
+                        }
+                        const uint32_t to = smem_u32(ring) + at.stage * S::kBytes;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll 4
+                            for (int i = 0; i < 32; i += kRows) {
+                                const int in = i + lane / kChunks, r = k * 32 + in;
+                                const int64_t from = __shfl_sync(0xffffffffu, offset[k], in);
+                                cp_async_16(to + (r >> 3) * DB * 1024 + (chunk >> 3) * 1024 + (r & 7) * 128 +
+                                                (((chunk & 7) ^ (r & 7)) << 4),
+                                            plane + (from < 0 ? 0 : from + w.head * D + chunk * 8),
+                                            from < 0 ? 0 : 16);
+                            }
+                        cp_async_commit();
+                        if (pending) {
+                            cp_async_wait<1>();
+                            __syncwarp();
+                            hand_over();
+                        }
+                        pending = true;
+                        pending_stage = at.stage;
+                        pending_part = part;
+                        pending_kt = kt;
+                        pending_end = end;
+                        pending_partial = !keys && w.partial(a, kt);
+                    }
+                }
+                flush();
+                if (!ok) spin_ns(kDrainNs);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
+constexpr int kFewParts = 8;  // that a warp joins alone
+
+// Joins the parts of the items that several CTAs share: with M the largest of the parts' maxima,
+// out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same order.  A warp has
+// a row, its lanes the columns; many parts are dealt to the warps of a block.
+template <int DB>
+__global__ void __launch_bounds__(kJoinThreads)
+    kv_join_kernel(const KvAttentionArgs a, const KvWorkspace ws, const int ctas) {
+    constexpr int D = DB * 64, kCols = 2 * DB;  // columns of a lane
+    __shared__ KvItem items[kKvMaxCtas];
+    __shared__ int begins[2][kKvMaxCtas + 1];  // rows of items of few parts, and of many
+    __shared__ float sums[kJoinWarps][D];
+    __shared__ float2 totals[kJoinWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = a.num_heads / a.num_kv_heads;
+    griddep_launch_dependents();
+    griddep_wait();
+    const KvItem* left = reinterpret_cast<const KvItem*>(a.workspace + ws.items);
+    if (warp < 2) {
+        constexpr int kEach = (kKvMaxCtas + 31) / 32;
+        int n[kEach], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int p = lane * kEach + k;
+            n[k] = 0;
+            if (p < ctas) {
+                const KvItem x = left[2 * p], y = left[2 * p + 1];
+                const KvItem it = x.tokens > 0 ? x : y;
+                if (warp == 0) items[p] = it;
+                if ((it.parts > kFewParts) == (warp == 1)) n[k] = it.tokens * group;
+            }
+            sum += n[k];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, sh);
+            if (lane >= sh) incl += o;
+        }
+        int at = incl - sum;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int p = lane * kEach + k;
+            if (p <= ctas) begins[warp][p] = at;
+            at += n[k];
+        }
+        if (lane == 31) begins[warp][ctas] = incl;
+    }
+    __syncthreads();
+    const float* parts = reinterpret_cast<const float*>(a.workspace);
+    const float2* stats = reinterpret_cast<const float2*>(a.workspace + ws.stats);
+    // warps take rows of few parts, whole blocks those of many
+    for (int pass = 0; pass < 2; ++pass) {
+        const bool many = pass == 1;
+        const int tasks = begins[pass][ctas];
+        const int stride = many ? gridDim.x : gridDim.x * kJoinWarps;
+        for (int f = many ? blockIdx.x : blockIdx.x * kJoinWarps + warp; f < tasks; f += stride) {
+            int p = 0, behind = ctas;
+            while (behind - p > 1) {
+                const int mid = (p + behind) / 2;
+                if (begins[pass][mid] <= f) p = mid;
+                else behind = mid;
+            }
+            const KvItem it = items[p];
+            const int row = f - begins[pass][p];
+            const int token = row / group, head = row - token * group;
+            const int sub = token / a.tile_tokens;
+            const int slot_row = sub * kTile + (token - sub * a.tile_tokens) * group + head;
+            float top = -INFINITY, total = 0.0f, o[kCols] = {};
+#pragma unroll 4
+            for (int k = many ? warp : 0; k < it.parts; k += many ? kJoinWarps : 1) {
+                // the CTA's second slot, then the first slots of those behind
+                const int64_t at = (2 * static_cast<int64_t>(p + k) + (k == 0 ? 1 : 0)) * ws.rows + slot_row;
+                const float2 s = __ldcg(stats + at);
+                float v[kCols];
+#pragma unroll
+                for (int c = 0; c < kCols; c += 2) {
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(parts + at * D + lane * kCols + c));
+                    v[c] = x.x;
+                    v[c + 1] = x.y;
+                }
+                const float m = fmaxf(top, s.x);
+                const float f0 = top == -INFINITY ? 0.0f : exp2f(top - m);
+                const float f1 = s.x == -INFINITY ? 0.0f : exp2f(s.x - m);
+                top = m;
+                total = total * f0 + s.y * f1;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) o[c] = o[c] * f0 + v[c] * f1;
+            }
+            if (many) {
+                if (lane == 0) totals[warp] = make_float2(top, total);
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) sums[warp][lane * kCols + c] = o[c];
+                __syncthreads();
+                top = -INFINITY;
+                total = 0.0f;
+                for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, totals[k].x);
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) o[c] = 0.0f;
+                for (int k = 0; k < kJoinWarps; ++k) {
+                    const float f1 = totals[k].x == -INFINITY ? 0.0f : exp2f(totals[k].x - top);
+                    total = fmaf(totals[k].y, f1, total);
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) o[c] = fmaf(sums[k][lane * kCols + c], f1, o[c]);
+                }
+                __syncthreads();
+                if (warp != 0) continue;
+            }
+            const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+            const int64_t out_row = (it.row + token) * a.num_heads + it.head + head;
+            uint32_t* to = reinterpret_cast<uint32_t*>(a.out + out_row * D + lane * kCols);
+#pragma unroll
+            for (int c = 0; c < kCols; c += 2) to[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+            if (a.lse != nullptr && lane == 0)
+                a.lse[out_row] = total != 0.0f ? top * kLn2 + logf(total) : -INFINITY;
+        }
+    }
+}
+
+template <int DB, bool TMA>
+cudaError_t launch_shape(const KvMaps& maps, const KvAttentionArgs& args, const KvWorkspace& ws,
+                         int ctas, int num_sms, cudaStream_t stream) {
+    constexpr size_t smem = Shape<DB>::kSmem;
+    // once a device: the attribute stays (every thread sets the same value)
+    static std::atomic<uint64_t> set[2] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 128;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (!known || !(set[dev >> 6].load(std::memory_order_relaxed) & bit)) {
+        // the register split takes what the block starts with
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, kv_attention_kernel<DB, TMA>);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs != kStartRegs) return cudaErrorInvalidKernelImage;
+        e = cudaFuncSetAttribute(kv_attention_kernel<DB, TMA>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        if (known) set[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
+    }
+    e = launch_dependent(kv_attention_kernel<DB, TMA>, static_cast<unsigned>(ctas), kThreads, smem,
+                         stream, maps, args, ws);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kv_join_kernel<DB>, static_cast<unsigned>(num_sms) * 2, kJoinThreads, 0,
+                            stream, args, ws, ctas);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attention(KvAttentionArgs args, int, cudaStream_t stream) {
-    const int64_t all = static_cast<int64_t>(args.total_rows) * args.num_heads;
-    const unsigned blocks = static_cast<unsigned>((all + kWarps - 1) / kWarps);
-    if (args.head_size == 64)
-        kv_attention_kernel<2><<<blocks, kWarps * 32, 0, stream>>>(args);
-    else
-        kv_attention_kernel<4><<<blocks, kWarps * 32, 0, stream>>>(args);
-    return cudaGetLastError();
+cudaError_t launch_kv_attention(const KvMaps& maps, KvAttentionArgs args, int num_sms,
+                                cudaStream_t stream) {
+    const KvWorkspace ws =
+        kv_workspace(args.total_rows, args.num_heads, args.num_kv_heads, args.head_size);
+    const int ctas = num_sms < kKvMaxCtas ? num_sms : kKvMaxCtas;
+    const bool tma = maps.slots > 0;
+    const auto launch = args.head_size == 64 ? (tma ? launch_shape<1, true> : launch_shape<1, false>)
+                                             : (tma ? launch_shape<2, true> : launch_shape<2, false>);
+    return launch(maps, args, ws, ctas, num_sms, stream);
 }
 
 }  // namespace pkm

@@ -14,7 +14,7 @@
 // flight.  The columns are asked for before the row's position and slot, which hang on a chain
 // of loads (offsets, length, page id).
 #include "pkm_device.cuh"
-#include "pkm_internal.h"
+#include "kv_internal.h"
 
 namespace pkm {
 namespace {

@@ -124,53 +124,6 @@ struct TreeAttentionArgs {
     int32_t item_cost;  // start and end of an item, in tiles (filled in by the launcher)
 };
 
-// One turn of new queries and keys and the write of keys and values, already validated
-// (strides in elements).
-struct KvRopeArgs {
-    const uint16_t* q;             // [total_rows, num_heads, D] by strides
-    uint16_t* q_out;
-    int64_t q_row_stride, q_head_stride, q_out_row_stride, q_out_head_stride;
-    const uint16_t* k;             // [total_rows, num_kv_heads, D], or null: in the cache already
-    const uint16_t* v;             // likewise, or null: the V plane stays
-    int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride;
-    int32_t num_heads, num_kv_heads, head_size, rope_dim;
-    const uint32_t* row_offsets;   // [batch + 1]
-    int32_t batch, total_rows;
-    const uint32_t* positions;     // [num_axes, total_rows]
-    int32_t num_axes;
-    uint8_t unit_axes[32];         // of the four pairs of every eight columns, two bits each
-    const float* freqs;            // [max_seq_len, P]
-    int32_t max_seq_len;
-    int32_t half;                  // pairs (j, j + P/2) instead of (2j, 2j + 1)
-    uint16_t* cache_layer;         // cache data + layer_idx * layer_stride
-    int64_t page_stride, slot_stride, kv_stride;
-    int32_t num_pages, page_size, max_pages;
-    const uint32_t* page_table;
-    const uint32_t* cache_lengths;
-    int32_t* status;
-};
-
-// One attention over the paged K/V cache, already validated (strides in elements).
-struct KvAttentionArgs {
-    const uint16_t* q;             // [total_rows, num_heads, D] by strides
-    int64_t q_row_stride, q_head_stride;
-    const uint32_t* row_offsets;   // [batch + 1]
-    int32_t batch, total_rows, num_heads, num_kv_heads, head_size;
-    float scale;
-    int32_t window;                // last positions that a token attends, or 0: all
-    int32_t sinks;                 // first positions that it attends besides
-    const uint16_t* cache_layer;   // cache data + layer_idx * layer_stride
-    int64_t page_stride, slot_stride, kv_stride;
-    int32_t num_pages, page_size, max_pages;
-    const uint32_t* page_table;
-    const uint32_t* cache_lengths;
-    uint16_t* out;                 // [total_rows, num_heads, D]
-    float* lse;                    // [total_rows, num_heads], or null
-    uint8_t* workspace;
-    int32_t* status;
-    uint64_t timeout_ns;
-};
-
 // One kv_matmul problem, already validated.
 struct KvMatmulArgs {
     const uint16_t* hidden;        // [M, K] bf16
@@ -273,8 +226,6 @@ cudaError_t launch_kv_matmul_fp8(const CUtensorMap& tm_q, const CUtensorMap& tm_
                                  cudaStream_t stream);
 cudaError_t launch_cache_write(CacheWriteArgs args, int num_sms, cudaStream_t stream);
 cudaError_t launch_rope_heads(RopeHeadsArgs args, int num_sms, cudaStream_t stream);
-cudaError_t launch_kv_rope(KvRopeArgs args, int num_sms, cudaStream_t stream);
-cudaError_t launch_kv_attention(KvAttentionArgs args, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_compact(CompactArgs args, cudaStream_t stream);
 cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_first_keys,
                                   const CUtensorMap& tm_last_keys,
