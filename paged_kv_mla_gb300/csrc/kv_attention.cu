@@ -7,12 +7,13 @@
 // with row = token * G + head, and 128 rows of whole tokens make a tile of queries.
 //
 // An item is up to two tiles of one request and one head of keys.  Two tiles (a chunk) take each
-// tile of 128 keys in turn: while the tensor cores work for one, four softmax warps have the
-// other's scores.  One tile (few tokens, a single one above all) takes even and odd tiles of keys
-// in turn, each with sums of its own that are joined at the item's end.  Either way a step is one
-// product of 128 x 128 scores, steps alternate between two stages, and a stage has its scores
-// (which its weights overwrite in place, as the second product's A operand) and its O in tensor
-// memory, and four softmax warps.
+// tile of 128 keys in turn; one tile (few tokens, a single one above all) takes even and odd tiles
+// of keys in turn, with sums of their own that are joined at the item's end.  Either way a step is
+// one product of 128 x 128 scores, steps alternate between two stages, and a stage has four softmax
+// warps and, in tensor memory, its O and its weights (the second product's A operand).  Scores
+// leave tensor memory as soon as they are there, so that the next step's are computed while these
+// go through the softmax: with D = 128 one place serves both stages, since the values' product of
+// the step two before runs between two steps' scores.
 //
 // The key axis of all items is one line of 128-key tiles, cut into equal parts, one for each CTA:
 // a CTA starts at most one item that it does not finish and finishes at most one that it did not
@@ -20,8 +21,8 @@
 // kernel joins them; whole items are written directly.  A window's items leave out the tiles
 // between the first tokens and the window.
 //
-// Roles of a CTA: warps 0-3 and 4-7 softmax and epilogue of a stage, 8 MMA issue, 9 queries and
-// keys, 10 values, 11 looks values through for infinities and NaN where not every row attends
+// Roles of a CTA: warps 0-3 and 4-7 softmax and epilogue of a stage, 8-11 MMA issue, 12 queries
+// and keys, 13 values, 14 looks values through for infinities and NaN where not every row attends
 // every key (a zero weight must not meet them).  Scores are kept in base 2; the running maximum
 // moves only when a row's new maximum exceeds it by 2^8, since any reference works as long as
 // nothing overflows, so O is hardly ever rescaled.
@@ -33,16 +34,16 @@
 namespace pkm {
 namespace {
 
-constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kCheckWarp = 11;
-constexpr int kThreads = 12 * 32;
-// Registers of the two softmax groups and of the issuing and loading warps, of the 3 x 168 that
-// the block starts with.
-constexpr int kStartRegs = 168, kSoftRegs = 208, kIssueRegs = 88;
-static_assert(2 * kSoftRegs + kIssueRegs <= 3 * kStartRegs, "registers of the block");
+constexpr int kScoreWarp = 8, kOutWarp = 10, kKeyWarp = 12, kValueWarp = 13, kCheckWarp = 14;
+constexpr int kThreads = 16 * 32;
+// Registers of the two softmax groups and of the two of issuing and loading warps, of the 4 x 128
+// that the block starts with.
+constexpr int kStartRegs = 128, kSoftRegs = 200, kIssueRegs = 56;
+static_assert(2 * kSoftRegs + 2 * kIssueRegs <= 4 * kStartRegs, "registers of the block");
 constexpr int kTile = 128;          // keys of a tile, rows of a tile of queries
-constexpr int kMaxStages = 8;       // tiles of keys or values in flight
+constexpr int kMaxStages = 7;       // tiles of keys, or of values, in shared memory
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kOutCol = 256;   // O of stage s at kOutCol + s * D, scores at s * 128
+constexpr uint32_t kWeightCol = 384;    // TMEM column of the weights, 64 a stage
 constexpr int kItemCost = 1;        // an item's start and end, in tiles
 constexpr uint64_t kDrainNs = 1000000;  // a role that gave up leaves its loads time to land
 constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
@@ -130,16 +131,19 @@ struct Request {
 };
 
 struct Bars {
-    uint64_t full[kMaxStages];   // a tile of keys or values is there
-    uint64_t empty[kMaxStages];  // its MMAs are done
-    uint64_t own[kMaxStages];    // values that are looked through first are there
+    uint64_t k_full[kMaxStages];   // a tile of keys is there
+    uint64_t k_empty[kMaxStages];  // its MMAs are done
+    uint64_t v_full[kMaxStages];   // of values
+    uint64_t v_empty[kMaxStages];
+    uint64_t v_own[kMaxStages];    // values that are looked through first are there
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];          // a step's scores are complete
+    uint64_t s_empty[2];         // they have been read
     uint64_t p_full[2];          // its weights are written
-    uint64_t o_full[2];          // an item's last step on the stage is done
+    uint64_t p_empty[2];         // they are used up, and O holds them
     uint64_t o_empty[2];         // its O has been read
     uint64_t stats_full[2];      // the other stage's maxima and sums, for the stage that joins both
-    uint64_t mma_done;
+    uint64_t mma_done[4];
     float2 stats[kTile];
     int64_t scratch[kThreads / 32];
     int64_t units;               // units of all items
@@ -147,7 +151,7 @@ struct Bars {
     int64_t share;               // and has so many units
     int64_t into;                // units of its first request before it
     int32_t request, head, item, unit;  // its first unit
-    uint32_t nonfinite[8];       // parts, by number, that had infinities or NaN looked through
+    uint32_t nonfinite[16];      // parts, by number, that had infinities or NaN looked through
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -156,9 +160,17 @@ template <int DB>  // 64-column blocks of a head
 struct Shape {
     static constexpr int kCols = DB * 64;
     static constexpr int kBytes = DB * 128 * 128;   // of a tile
-    static constexpr int kStages = DB == 2 ? 5 : 8;
-    static constexpr size_t kOffRing = 2 * size_t(kBytes);
-    static constexpr size_t kOffBars = kOffRing + size_t(kStages) * kBytes;
+    // Keys of the step at hand and the next; values of the two steps before it, whose weights are
+    // not ready, and the next.
+    static constexpr int kKeyStages = DB == 2 ? 2 : 5, kValueStages = DB == 2 ? 3 : 7;
+    // TMEM columns of a stage's O and scores; the first kScores of them are places of their own
+    static constexpr int kScores = DB == 2 ? 1 : 2;
+    __device__ static constexpr uint32_t out_col(int stage) { return stage * kCols; }
+    __device__ static constexpr uint32_t score_col(int stage) { return 2 * kCols + (kScores > 1 ? stage * 128 : 0); }
+    static_assert(2 * kCols + kScores * 128 <= kWeightCol, "tensor memory");
+    static constexpr size_t kOffKeys = 2 * size_t(kBytes);
+    static constexpr size_t kOffValues = kOffKeys + size_t(kKeyStages) * kBytes;
+    static constexpr size_t kOffBars = kOffValues + size_t(kValueStages) * kBytes;
     static constexpr size_t kSmem = kOffBars + sizeof(Bars);
     static_assert(kSmem <= 232448, "shared memory budget of one sm_103a CTA");
 };
@@ -182,6 +194,7 @@ struct Walk {
         head = bars->head;
         item = bars->item;
         at = bars->unit;
+        tokens = x0 = x1 = 0;
         if (left > 0) {
             r.load(a, b);
             set_item(a);
@@ -221,15 +234,6 @@ struct Walk {
     __device__ __forceinline__ bool wide(const KvAttentionArgs& a) const { return tokens > a.tile_tokens; }
     __device__ __forceinline__ int32_t tile(const KvAttentionArgs& a, int32_t x) const {
         return gap > 0 && x >= a.sink_tiles ? x + gap : x;
-    }
-    // Whether some of the tokens, the first of them at position p, do not attend all of the tile.
-    __device__ __forceinline__ bool partial(const KvAttentionArgs& a, int32_t kt, int64_t p, int32_t count) const {
-        const int64_t c0 = static_cast<int64_t>(kt) * kTile;
-        if (c0 + kTile - 1 > p) return true;
-        return a.window > 0 && c0 <= p + count - 1 - a.window && c0 + kTile > a.sinks;
-    }
-    __device__ __forceinline__ bool partial(const KvAttentionArgs& a, int32_t kt) const {
-        return partial(a, kt, r.len + token0, tokens);
     }
     // Whether the item reads any of the positions pos .. pos + count - 1 of one page: those past its
     // last token may have no page yet, and the pages between the first tokens and the window none
@@ -365,20 +369,51 @@ __device__ __forceinline__ bool look_through(uint32_t tile, int64_t end) {
     return __any_sync(0xffffffffu, found);
 }
 
-// Which of the 32 keys from c0 on (relative to the tile) a row attends: those up to hi, from lo on
-// or below sinks.
-__device__ __forceinline__ uint32_t attended(int64_t hi, int64_t lo, int64_t sinks, int c0) {
-    const auto below = [](int64_t n) -> uint32_t {
-        return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
-    };
-    return below(hi + 1 - c0) & (~below(lo - c0) | below(sinks - c0));
-}
+// The tiles that not all tokens of a tile of queries attend, the first of them at position p:
+// from `diagonal` on, and those with keys behind the first tokens up to the window's `edge`.
+struct Masked {
+    int32_t diagonal, sinks, edge;
+    __device__ __forceinline__ Masked(const KvAttentionArgs& a, int64_t p, int32_t count)
+        : diagonal(static_cast<int32_t>((p + 1) >> 7)), sinks(a.sinks >> 7), edge(-1) {
+        const int64_t out = p + count - 1 - a.window;  // the last position outside a window
+        if (a.window > 0 && out >= 0) edge = static_cast<int32_t>(out >> 7);
+    }
+    __device__ __forceinline__ bool any(int32_t kt) const {
+        return kt >= diagonal || (kt <= edge && kt >= sinks);
+    }
+};
+
+// Which keys of a tile a token at position p attends: those before `end`, from `lo` on or before
+// `sinks`.
+struct Attended {
+    int32_t end, lo, sinks;
+    __device__ __forceinline__ Attended(const KvAttentionArgs& a, int64_t p, int32_t kt) {
+        const int64_t c0 = static_cast<int64_t>(kt) * kTile;
+        const auto inside = [](int64_t v) -> int32_t {
+            return static_cast<int32_t>(min(max(v, static_cast<int64_t>(0)), static_cast<int64_t>(kTile)));
+        };
+        end = inside(p + 1 - c0);
+        lo = a.window > 0 ? inside(p - a.window + 1 - c0) : 0;
+        sinks = inside(a.sinks - c0);
+    }
+    // of the 32 keys from c on
+    __device__ __forceinline__ uint32_t bits(int32_t c) const {
+        const auto below = [](int32_t n) -> uint32_t {
+            return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+        };
+        return below(end - c) & (~below(lo - c) | below(sinks - c));
+    }
+};
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// A value that is the same in every lane of the warp, through a shuffle, from which the compiler
+// sees that it is: addresses made of it then use uniform registers, where MMAs take their operands.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Waits with all lanes of a warp; the verdict is the same in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
@@ -393,29 +428,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int D = S::kCols;
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzle atoms of 1024 bytes
     uint8_t* sQ = smem;
-    uint8_t* ring = smem + S::kOffRing;
+    uint8_t *sK = smem + S::kOffKeys, *sV = smem + S::kOffValues;
     Bars* bars = reinterpret_cast<Bars*>(smem + S::kOffBars);
     // the same in every lane, seen by the compiler through the shuffle
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&bars->full[i], 1);
-            mbar_init(&bars->empty[i], 1);
-            mbar_init(&bars->own[i], 1);
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&bars->k_full[i], 1);
+            mbar_init(&bars->k_empty[i], 2);
+            mbar_init(&bars->v_full[i], 1);
+            mbar_init(&bars->v_empty[i], 2);
+            mbar_init(&bars->v_own[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
-            mbar_init(&bars->q_empty[i], 1);
+            mbar_init(&bars->q_empty[i], 2);
             mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->s_empty[i], 4);
             mbar_init(&bars->p_full[i], 4);
-            mbar_init(&bars->o_full[i], 1);
+            mbar_init(&bars->p_empty[i], 1);
             mbar_init(&bars->o_empty[i], 4);
             mbar_init(&bars->stats_full[i], 4);
         }
-        mbar_init(&bars->mma_done, 1);
-        for (int i = 0; i < 8; ++i) bars->nonfinite[i] = 0;
+        for (int i = 0; i < 4; ++i) mbar_init(&bars->mma_done[i], 1);
+        for (int i = 0; i < 16; ++i) bars->nonfinite[i] = 0;
         bars->abort_flag = 0;
         fence_mbar_init();
     }
@@ -427,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_prefetch_map(&maps.v);
         }
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         tmem_alloc(&bars->tmem_base, kTmemCols);
         tmem_relinquish();
     }
@@ -446,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait_flag(bar, parity, wc.abort_flag, tries));
     };
 
-    if (warp < kMmaWarp) {
+    if (warp < kScoreWarp) {
         // ---------------- softmax and epilogue: row = lane of tensor memory ----------------
         warpgroup_reg_alloc<kSoftRegs>();
         Walk w(a, bars);
@@ -456,11 +494,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row_token = row / group, row_head = row - row_token * group;
         const float scale2 = a.scale * kLog2e;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t scores = lanes + stage * 128;
+        const uint32_t scores = lanes + S::score_col(stage), weights = lanes + kWeightCol + stage * 64;
+        const uint32_t out = lanes + S::out_col(stage), other_out = lanes + S::out_col(stage ^ 1);
         const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         const int64_t sharing = min(static_cast<int64_t>(gridDim.x), bars->units);
         uint32_t n = 0, part = 0;
-        uint32_t use_phase = 0, join_phase = 0;  // a bit for each stage
+        uint32_t join_phase = 0;  // a bit for each stage
         KvItem left{0, 0, 0, 0};
         bool ok = true;
         while (ok && w.next(a)) {
@@ -473,32 +512,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool valid = row_token < count;
             const bool busy = (warp & 3) * 32 < count * group;  // the warp has rows
             const int64_t pos0 = w.r.len + token0, pos = pos0 + row_token;
+            const Masked masks(a, pos0, count);
             float m = -INFINITY, l = 0.0f;
             for (int x = mine; x < steps; x += 2) {
                 const int32_t kt = w.tile(a, w.x1 - 1 - (wide ? x >> 1 : x));
-                if (!warp_wait(&bars->s_full[stage], ((n + x) >> 1) & 1, wc)) {
+                const uint32_t turn = (n + x) >> 1;  // of the stage
+                if (!warp_wait(&bars->s_full[stage], turn & 1, wc)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (busy) {
+                if (!busy) {
+                    if (lane == 0) mbar_arrive(&bars->s_empty[stage]);
+                    if (turn > 0 && !warp_wait(&bars->p_empty[stage], (turn - 1) & 1, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive(&bars->p_full[stage]);
+                } else {
                     uint32_t s[4][32];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) tmem_ld_x32(scores + k * 32, s[k]);
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 128; ++c) asm volatile("" : "+r"(s[c >> 5][c & 31]));  // not before
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->s_empty[stage]);
                     const auto f = [&](int c) -> float { return __uint_as_float(s[c >> 5][c & 31]); };
-                    const bool masked = w.partial(a, kt, pos0, count);
+                    const bool masked = masks.any(kt);
                     float mul = scale2;
                     if (masked || scale2 < 0.0f) {
                         // scaled before masks and maxima, which then need not know the sign
                         mul = 1.0f;
-                        const int64_t c0 = static_cast<int64_t>(kt) * kTile;
-                        const int64_t lo = a.window > 0 ? pos - a.window + 1 - c0 : 0;
+                        const Attended may_attend(a, pos, kt);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t may = masked ? attended(pos - c0, lo, a.sinks - c0, k * 32) : ~0u;
+                            const uint32_t may = masked ? may_attend.bits(k * 32) : ~0u;
 #pragma unroll
                             for (int c = 0; c < 32; ++c) {
                                 const float v = __uint_as_float(s[k][c]) * scale2;
@@ -508,30 +558,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float t0 = f(0), t1 = f(1), t2 = f(2), t3 = f(3);
 #pragma unroll
-                    for (int c = 4; c < 128; c += 4) {
-                        t0 = fmaxf(t0, f(c));
-                        t1 = fmaxf(t1, f(c + 1));
-                        t2 = fmaxf(t2, f(c + 2));
-                        t3 = fmaxf(t3, f(c + 3));
+                    for (int c = 4; c < 124; c += 8) {
+                        t0 = fmax3(t0, f(c), f(c + 1));
+                        t1 = fmax3(t1, f(c + 2), f(c + 3));
+                        t2 = fmax3(t2, f(c + 4), f(c + 5));
+                        t3 = fmax3(t3, f(c + 6), f(c + 7));
                     }
-                    const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * mul;
+                    t0 = fmax3(t0, f(124), f(125));
+                    t1 = fmax3(t1, f(126), f(127));
+                    const float top = fmaxf(fmax3(t0, t1, t2), t3) * mul;
                     const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
                     const float m_new = move ? top : m;
                     const float back = move && m > -INFINITY ? exp2_approx(m - m_new) : 1.0f;
                     m = m_new;
                     const float ref = m == -INFINITY ? 0.0f : m;
-                    // The stage's step before is done (its MMAs were issued before this step's
-                    // scores), so O holds still.
+                    // the stage's step before is done: O holds still, and its weights' place is free
+                    if (turn > 0 && !warp_wait(&bars->p_empty[stage], (turn - 1) & 1, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                     if (x > mine && __any_sync(0xffffffffu, back != 1.0f)) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
-                            tmem_ld_x32(lanes + kOutCol + stage * D + c, o);
+                            tmem_ld_x32(out + c, o);
                             tmem_ld_wait();
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 o[k] = __float_as_uint(__uint_as_float(o[k]) * back);
-                            tmem_st_x32(lanes + kOutCol + stage * D + c, o);
+                            tmem_st_x32(out + c, o);
                         }
                     }
                     // The weights are rounded to bf16, by up to 2^-8 of each: the second product's
@@ -551,23 +607,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             add2(sum[2 * (k & 1)], sum[2 * (k & 1) + 1], e0, e1);
                             p[k] = pack_bf16x2(e0, e1);
                         }
-                        tmem_st_x32(scores + h * 32, p);
+                        tmem_st_x32(weights + h * 32, p);
                     }
                     l = l * back + ((sum[0] + sum[2]) + (sum[1] + sum[3]));
                     tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->p_full[stage]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_full[stage]);
             }
             const bool join = !wide && steps > 1;   // the first step's stage joins both
+            // the last turns of this stage and of the other one
+            const uint32_t last = (n + mine + (steps - 1 - mine) / 2 * 2) >> 1;
+            const uint32_t other_last = (n + (mine ^ 1) + (steps - 1 - (mine ^ 1)) / 2 * 2) >> 1;
             n += steps;
             ++part;
-            const uint32_t o_phase = use_phase, joined = join_phase >> first_stage & 1;
-            use_phase ^= steps > 1 ? 3u : 1u << first_stage;
+            const uint32_t joined = join_phase >> first_stage & 1;
             join_phase ^= join ? 1u << first_stage : 0u;
             if (!ok || mine >= steps) continue;
-            ok = warp_wait(&bars->o_full[stage], o_phase >> stage & 1, wc);
+            ok = warp_wait(&bars->p_empty[stage], last & 1, wc);
             if (!ok) break;
             if (join && mine == 1) {
                 bars->stats[row] = make_float2(m, l);
@@ -577,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float f0 = 1.0f, f1 = 0.0f;  // factors of this stage's sums and of the other's
             if (join) {
-                ok = warp_wait(&bars->o_full[stage ^ 1], o_phase >> (stage ^ 1) & 1, wc) &&
-                     warp_wait(&bars->stats_full[stage], joined, wc);
+                ok = warp_wait(&bars->stats_full[stage], joined, wc) &&
+                     warp_wait(&bars->p_empty[stage ^ 1], other_last & 1, wc);
                 if (!ok) break;
                 const float2 other = bars->stats[row];
                 const float top = fmaxf(m, other.x);
@@ -590,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const bool whole = w.x0 == 0 && w.x1 == w.tiles;
             const float inv = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
-            const bool mend = *const_cast<volatile uint32_t*>(&bars->nonfinite[(part - 1) & 7]) == part;
+            const bool mend = *const_cast<volatile uint32_t*>(&bars->nonfinite[(part - 1) & 15]) == part;
             const int64_t out_row = (w.r.first + token0 + row_token) * a.num_heads + w.head * group + row_head;
             const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.x0 > 0 ? 0 : 1);
             const int slot_row = sub * kTile + row;
@@ -598,10 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
-                    tmem_ld_x32(lanes + kOutCol + stage * D + c, o);
+                    tmem_ld_x32(out + c, o);
                     if (join) {
                         uint32_t o1[32];
-                        tmem_ld_x32(lanes + kOutCol + (stage ^ 1) * D + c, o1);
+                        tmem_ld_x32(other_out + c, o1);
                         tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
@@ -613,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // values that were made zero for the rows that do not attend them
                         for (int x = w.x0; x < w.x1; ++x) {
                             const int32_t kt = w.tile(a, x);
-                            if (!w.partial(a, kt)) continue;
+                            if (!Masked(a, w.r.len + w.token0, w.tokens).any(kt)) continue;
                             for (int t = 0; t < kTile; ++t) {
                                 const int64_t at = static_cast<int64_t>(kt) * kTile + t;
                                 if (at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks)) continue;
@@ -677,117 +735,106 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         warpgroup_reg_dealloc<kIssueRegs>();
-        if (warp == kMmaWarp) {
-            // ---------------- MMA issuer, all lanes together ----------------
+        if (warp < kKeyWarp) {
+            // ---------------- MMA issuers, all lanes together ----------------
+            // One warp for each product of each stage: the tensor cores queue little work ahead, so
+            // what a warp needs for its waits and descriptors goes by during the others' MMAs.
+            // Both stages wait for all keys, values and queries, and release them, the other stage's
+            // too: a wait cannot tell a phase from the one two before or behind, so that neither may
+            // miss one.
             Walk w(a, bars);
             // A wait that runs out is looked at once a step; what is issued until then is not used.
             bool failed = false;
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
                 failed |= !mbar_wait_flag(bar, parity, wc.abort_flag, tries);
             };
-            const uint32_t id_s = idesc_bf16(128, kTile, false, false);
-            const uint32_t id_o = idesc_bf16(128, D, false, true);
-            const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
-            const uint64_t k_desc = sdesc_sw128(smem_u32(ring), 16, DB * 1024);
-            const uint64_t v_desc = sdesc_sw128(smem_u32(ring), 1024, DB * 1024);
-            // what is to be done for the steps whose values come next, eight bits a stage
-            constexpr uint32_t kAny = 1, kFirst = 2, kLast = 4, kFetch = 8, kRelease = 16;
-            uint32_t ahead = 0;
-            RingPos kpos, vpos;
-            vpos.next(S::kStages);
-            uint32_t n = 0, done = 0, queries = 0;
-            uint32_t empty_phase = 3;  // a bit for each stage; the first wait passes
-            // O (+)= P V of the step `done`
-            const auto values = [&](int s) {
-                const uint32_t st = ahead >> (8 * s);
-                ahead &= ~(0xffu << (8 * s));
-                wait(&bars->p_full[s], (done >> 1) & 1);
-                if (st & kFirst) {
-                    wait(&bars->o_empty[s], empty_phase >> s & 1);
-                    empty_phase ^= 1u << s;
-                }
-                if (st & kFetch) wait(&bars->full[vpos.stage], vpos.phase);
-                tc_fence_after();
-                const uint64_t vd = desc_add_bytes(v_desc, vpos.stage * S::kBytes);
-                const uint32_t d = tmem + kOutCol + s * D, p = tmem + s * 128;
-                const uint32_t keep = st & kFirst ? 0u : 1u;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)  // 16 keys: two atoms of each block
-                    mma_bf16_ts_elect(d, p + 8 * k, desc_add_bytes(vd, k * 2 * DB * 1024), id_o,
-                                      k > 0 ? 1u : keep);
-                if (st & kRelease) {
-                    mma_commit_elect(&bars->empty[vpos.stage]);
-                    vpos.next(S::kStages);
-                    vpos.next(S::kStages);
-                }
-                if (st & kLast) mma_commit_elect(&bars->o_full[s]);
-                ++done;
-            };
+            const bool scores = warp < kOutWarp;
+            const uint32_t stage = warp & 1;
+            const uint32_t id = scores ? idesc_bf16(128, kTile, false, false) : idesc_bf16(128, D, false, true);
+            const uint64_t a_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+            const uint64_t b_desc = scores ? sdesc_sw128(smem_u32(sK), 16, DB * 1024)
+                                           : sdesc_sw128(smem_u32(sV), 1024, DB * 1024);
+            const uint32_t d = tmem + (scores ? S::score_col(stage) : S::out_col(stage));
+            const uint32_t weights = tmem + kWeightCol + stage * 64;
+            uint64_t* full = scores ? bars->k_full : bars->v_full;
+            uint64_t* empty = scores ? bars->k_empty : bars->v_empty;
+            const uint32_t stages = scores ? S::kKeyStages : S::kValueStages;
+            uint32_t n = 0, queries = 0, uses = 0;
+            RingPos at;
             while (!__any_sync(0xffffffffu, failed) && __any_sync(0xffffffffu, w.next(a))) {
                 const bool wide = __any_sync(0xffffffffu, w.wide(a));
-                const int tiles = __shfl_sync(0xffffffffu, w.x1 - w.x0, 0);
-                const int steps = wide ? 2 * tiles : tiles;
+                const int tiles = __shfl_sync(0xffffffffu, w.x1 - w.x0, 0), steps = wide ? 2 * tiles : tiles;
+                const int mine = (n & 1) ^ stage;  // the stage's first step
+                const uint32_t query = queries + (wide ? mine : 0);
+                if (scores)
+                    for (uint32_t q = queries; q < queries + (wide ? 2 : 1); ++q) {
+                        wait(&bars->q_full[q & 1], (q >> 1) & 1);
+                        if ((wide ? q != query : mine >= steps) && lane == 0) mbar_arrive(&bars->q_empty[q & 1]);
+                        __syncwarp();
+                    }
+                const auto pass = [&] {  // over a tile of the other stage
+                    wait(&full[at.stage], at.phase);
+                    if (lane == 0) mbar_arrive(&empty[at.stage]);
+                    __syncwarp();
+                    at.next(stages);
+                };
+                if (!wide && mine == 1) pass();
 #pragma unroll 1
-                for (int x = 0; x < steps; ++x, ++n) {
-                    const int s = n & 1;
-                    if (ahead >> (8 * s) & kAny) values(s);
-                    const bool odd = x & 1;
-                    const uint32_t q = wide && odd ? (queries + 1) & 1 : queries & 1;
-                    if (x == 0 || (wide && x == 1)) {
-                        const uint32_t qn = queries + x;
-                        // the step before is not held up by queries that are not there yet
-                        if (!__all_sync(0xffffffffu, mbar_try_wait(&bars->q_full[q], (qn >> 1) & 1)) &&
-                            x == 0 && (ahead >> (8 * (s ^ 1)) & kAny))
-                            values(s ^ 1);
-                        wait(&bars->q_full[q], (qn >> 1) & 1);
-                    }
-                    if (!wide || !odd) wait(&bars->full[kpos.stage], kpos.phase);
-                    tc_fence_after();
-                    const uint64_t qd = desc_add_bytes(q_desc, q * S::kBytes);
-                    const uint64_t kd = desc_add_bytes(k_desc, kpos.stage * S::kBytes);
+                for (int x = mine; x < steps; x += 2) {
+                    const uint32_t turn = (n + x) >> 1;
+                    const uint64_t bd = desc_add_bytes(b_desc, uniform(at.stage) * S::kBytes);
+                    wait(&full[at.stage], at.phase);
+                    if (scores) {
+                        const uint64_t ad = desc_add_bytes(a_desc, uniform(query & 1) * S::kBytes);
+                        // the scores that were in the place before have been read
+                        const uint32_t before = n + x - S::kScores;
+                        if (n + x >= S::kScores) wait(&bars->s_empty[before & 1], (before >> 1) & 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int kb = 0; kb < DB; ++kb)
 #pragma unroll
-                    for (int kb = 0; kb < DB; ++kb)
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16_elect(d, desc_add_bytes(ad, kb * 16384 + k * 32),
+                                               desc_add_bytes(bd, kb * 1024 + k * 32), id,
+                                               (kb | k) != 0 ? 1u : 0u);
+                        mma_commit_elect(&bars->s_full[stage]);
+                        if (x + 2 >= steps) mma_commit_elect(&bars->q_empty[query & 1]);
+                    } else {
+                        const uint32_t keep = uniform(x == mine ? 0u : 1u);
+                        if (x == mine) wait(&bars->o_empty[stage], (uses++ & 1) ^ 1);
+                        wait(&bars->p_full[stage], turn & 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16_elect(tmem + s * 128, desc_add_bytes(qd, kb * 16384 + k * 32),
-                                           desc_add_bytes(kd, kb * 1024 + k * 32), id_s,
-                                           (kb | k) != 0 ? 1u : 0u);
-                    mma_commit_elect(&bars->s_full[s]);
-                    if (!wide || odd) {
-                        mma_commit_elect(&bars->empty[kpos.stage]);
-                        kpos.next(S::kStages);
-                        kpos.next(S::kStages);
+                            for (int k = 0; k < 4; ++k)  // 16 keys: two atoms of each block
+                                mma_bf16_ts_elect(d, weights + 32 * h + 8 * k,
+                                                  desc_add_bytes(bd, (h * 4 + k) * 2 * DB * 1024), id,
+                                                  (h | k) != 0 ? 1u : keep);
+                        mma_commit_elect(&bars->p_empty[stage]);
                     }
-                    if (wide ? x >= steps - 2 : x == steps - 1) mma_commit_elect(&bars->q_empty[q]);
-                    ahead |= (kAny | (x < 2 ? kFirst : 0u) | (x >= steps - 2 ? kLast : 0u) |
-                              (!wide || !odd ? kFetch : 0u) | (!wide || odd ? kRelease : 0u))
-                             << (8 * s);
+                    mma_commit_elect(&empty[at.stage]);
+                    at.next(stages);
+                    if (!wide && x + 1 < steps) pass();
                     if (__any_sync(0xffffffffu, failed)) break;
                 }
+                n += steps;
                 queries += wide ? 2 : 1;
             }
-            if (!__any_sync(0xffffffffu, failed)) {
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                    const int s = (n + k) & 1;
-                    if (ahead >> (8 * s) & kAny) values(s);
-                }
-            }
-            mma_commit_elect(&bars->mma_done);
-            mbar_wait_inl(&bars->mma_done, 0, wc, false);
-        } else {
+            uint64_t* mma_done = &bars->mma_done[warp - kScoreWarp];
+            mma_commit_elect(mma_done);
+            mbar_wait_inl(mma_done, 0, wc, false);
+        } else if (warp <= kCheckWarp) {
             // ---------------- queries, keys, values ----------------
             const bool keys = warp == kKeyWarp;
             const uint16_t* plane = a.cache_layer + (keys ? 0 : a.kv_stride);
             Walk w(a, bars);
+            uint8_t* tiles = keys ? sK : sV;
+            uint64_t *full = keys ? bars->k_full : bars->v_full, *empty = keys ? bars->k_empty : bars->v_empty;
             RingPos at;
-            if (!keys) at.next(S::kStages);
             uint32_t queries = 0, part = 0, own_phase = 0;
             bool ok = true;
-            const auto next_tile = [&] {
-                at.next(S::kStages);
-                at.next(S::kStages);
-            };
+            const auto next_tile = [&] { at.next(keys ? S::kKeyStages : S::kValueStages); };
             const auto load_queries = [&]() -> bool {
                 const int subs = w.wide(a) ? 2 : 1;
                 for (int sub = 0; sub < subs; ++sub, ++queries) {
@@ -809,46 +856,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the tile's infinities and NaN, where not every row attends every key
             const auto mend = [&](uint32_t stage, int32_t kt) {
                 const int64_t end = w.r.len + w.token0 + w.tokens - static_cast<int64_t>(kt) * kTile;
-                if (look_through<DB>(smem_u32(ring) + stage * S::kBytes, end) && lane == 0)
-                    *const_cast<volatile uint32_t*>(&bars->nonfinite[part & 7]) = part + 1;
+                if (look_through<DB>(smem_u32(sV) + stage * S::kBytes, end) && lane == 0)
+                    *const_cast<volatile uint32_t*>(&bars->nonfinite[part & 15]) = part + 1;
             };
             if constexpr (TMA) {
                 const int slots = maps.slots, boxes = kTile / slots;
                 if (warp == kCheckWarp) {
-                    for (; ok && __any_sync(0xffffffffu, w.next(a)); ++part)
+                    for (; ok && __any_sync(0xffffffffu, w.next(a)); ++part) {
+                        const Masked masks(a, w.r.len + w.token0, w.tokens);
                         for (int x = w.x1 - 1; ok && x >= w.x0; --x, next_tile()) {
                             const int32_t kt = w.tile(a, x);
-                            if (!w.partial(a, kt)) continue;
-                            ok = issue_wait(&bars->own[at.stage], (own_phase >> at.stage) & 1);
+                            if (!masks.any(kt)) continue;
+                            ok = issue_wait(&bars->v_own[at.stage], (own_phase >> at.stage) & 1);
                             if (!ok) break;
                             own_phase ^= 1u << at.stage;
                             mend(at.stage, kt);
                             fence_proxy_async_smem();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars->full[at.stage]);
+                            if (lane == 0) mbar_arrive(&full[at.stage]);
                         }
+                    }
                 } else {
                     const CUtensorMap* map = keys ? &maps.k : &maps.v;
                     while (ok && __any_sync(0xffffffffu, w.next(a))) {
+                        const Masked masks(a, w.r.len + w.token0, w.tokens);
                         if (keys) ok = load_queries();
                         for (int x = w.x1 - 1; ok && x >= w.x0; --x, next_tile()) {
                             const int32_t kt = w.tile(a, x);
                             const int64_t pos = static_cast<int64_t>(kt) * kTile + lane * slots;
                             const Place place(a, w.b, pos, lane < boxes && w.reads(a, pos, slots));
-                            ok = issue_wait(&bars->empty[at.stage], at.phase ^ 1);
+                            ok = issue_wait(&empty[at.stage], at.phase ^ 1);
                             if (!ok) break;
-                            uint64_t* bar = &bars->full[at.stage];
-                            if (!keys && w.partial(a, kt)) bar = &bars->own[at.stage];
+                            uint64_t* bar = &full[at.stage];
+                            if (!keys && masks.any(kt)) bar = &bars->v_own[at.stage];
                             if (lane == 0) mbar_arrive_expect_tx(bar, S::kBytes);
                             __syncwarp();
                             if (lane < boxes)
-                                tma_load_5d(ring + at.stage * S::kBytes + lane * slots * DB * 128, map, bar,
+                                tma_load_5d(tiles + at.stage * S::kBytes + lane * slots * DB * 128, map, bar,
                                             0, 0, w.head * DB, place.slot >> 3, place.page);
                         }
                     }
                 }
                 if (!ok) spin_ns(kDrainNs);
-            } else if (warp != kCheckWarp) {
+            } else if (warp <= kValueWarp) {
                 // Row by row: a row's 16-byte chunks to their places in the swizzled atoms.  A tile
                 // is handed over when the next one is on its way, or before any longer wait.
                 bool pending = false;
@@ -858,13 +908,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool pending_partial = false;
                 const auto hand_over = [&] {
                     if (pending_partial &&
-                        look_through<DB>(smem_u32(ring) + pending_stage * S::kBytes,
+                        look_through<DB>(smem_u32(sV) + pending_stage * S::kBytes,
                                          pending_end - static_cast<int64_t>(pending_kt) * kTile) &&
                         lane == 0)
-                        *const_cast<volatile uint32_t*>(&bars->nonfinite[pending_part & 7]) = pending_part + 1;
+                        *const_cast<volatile uint32_t*>(&bars->nonfinite[pending_part & 15]) = pending_part + 1;
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->full[pending_stage]);
+                    if (lane == 0) mbar_arrive(&full[pending_stage]);
                     pending = false;
                 };
                 const auto flush = [&] {
@@ -880,6 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = load_queries();
                     }
                     const int64_t end = w.r.len + w.token0 + w.tokens;
+                    const Masked masks(a, w.r.len + w.token0, w.tokens);
                     for (int x = w.x1 - 1; ok && x >= w.x0; --x, next_tile()) {
                         const int32_t kt = w.tile(a, x);
                         int64_t offset[4];
@@ -888,12 +939,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int64_t pos = static_cast<int64_t>(kt) * kTile + k * 32 + lane;
                             offset[k] = Place(a, w.b, pos, w.reads(a, pos, 1)).offset(a);
                         }
-                        if (!__all_sync(0xffffffffu, mbar_try_wait(&bars->empty[at.stage], at.phase ^ 1))) {
+                        if (!__all_sync(0xffffffffu, mbar_try_wait(&empty[at.stage], at.phase ^ 1))) {
                             flush();
-                            ok = issue_wait(&bars->empty[at.stage], at.phase ^ 1);
+                            ok = issue_wait(&empty[at.stage], at.phase ^ 1);
                             if (!ok) break;
                         }
-                        const uint32_t to = smem_u32(ring) + at.stage * S::kBytes;
+                        const uint32_t to = smem_u32(tiles) + at.stage * S::kBytes;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
 #pragma unroll 4
@@ -916,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pending_part = part;
                         pending_kt = kt;
                         pending_end = end;
-                        pending_partial = !keys && w.partial(a, kt);
+                        pending_partial = !keys && masks.any(kt);
                     }
                 }
                 flush();
@@ -928,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
