@@ -21,11 +21,12 @@
 // kernel joins them; whole items are written directly.  A window's items leave out the tiles
 // between the first tokens and the window.
 //
-// Roles of a CTA: warps 0-3 and 4-7 softmax and epilogue of a stage, 8-11 MMA issue, 12 queries
-// and keys, 13 values, 14 looks values through for infinities and NaN where not every row attends
-// every key (a zero weight must not meet them).  Scores are kept in base 2; the running maximum
-// moves only when a row's new maximum exceeds it by 2^8, since any reference works as long as
-// nothing overflows, so O is hardly ever rescaled.
+// Roles of a CTA: warps 0-3 and 4-7 the softmax of a stage, 8 and 9 the MMAs of a stage's scores,
+// 10 those of both stages' values, 11 the schedule and all loads, 12-15 the epilogue; these also
+// look values through for infinities and NaN where not every row attends every key, since a zero
+// weight must not meet them.  Scores are kept in base 2; the running maximum moves only when a
+// row's new maximum exceeds it by 2^8, since any reference works as long as nothing overflows, so
+// O is hardly ever rescaled.
 #include <atomic>
 
 #include "kv_device.cuh"
@@ -34,12 +35,12 @@
 namespace pkm {
 namespace {
 
-constexpr int kScoreWarp = 8, kOutWarp = 10, kKeyWarp = 12, kValueWarp = 13, kCheckWarp = 14;
+constexpr int kScoreWarp = 8, kOutWarp = 10, kLoadWarp = 11, kEndWarp = 12;
 constexpr int kThreads = 16 * 32;
-// Registers of the two softmax groups and of the two of issuing and loading warps, of the 4 x 128
-// that the block starts with.
-constexpr int kStartRegs = 128, kSoftRegs = 200, kIssueRegs = 56;
-static_assert(2 * kSoftRegs + 2 * kIssueRegs <= 4 * kStartRegs, "registers of the block");
+// Registers of the two softmax groups, of the issuing and loading warps and of the epilogue, of the
+// 4 x 128 that the block starts with.
+constexpr int kStartRegs = 128, kSoftRegs = 176, kIssueRegs = 56, kEndRegs = 104;
+static_assert(2 * kSoftRegs + kIssueRegs + kEndRegs <= 4 * kStartRegs, "registers of the block");
 constexpr int kTile = 128;          // keys of a tile, rows of a tile of queries
 constexpr int kMaxStages = 7;       // tiles of keys, or of values, in shared memory
 constexpr uint32_t kTmemCols = 512;
@@ -130,6 +131,22 @@ struct Request {
     }
 };
 
+// The part of an item that a CTA has, as its warps see it: tiles [x0, x1) of the item's list, which
+// all take from the last to the first.  Tile x of the list is x, or x + gap from `lead` on.
+struct Part {
+    int64_t pos;         // position of the first token
+    int32_t row, b;      // its row, and the request
+    int32_t tokens, head;
+    int32_t x0, x1, lead, gap;
+    int32_t wide;        // two tiles of queries
+    int32_t whole;       // all tiles of the item
+    int32_t left;        // CTAs that share the item, if it starts here (0: it does not)
+    int32_t diagonal[2], edge[2];  // tiles that a tile of queries' tokens do not all attend (Masked)
+
+    __device__ __forceinline__ int32_t tile(int32_t x) const { return x >= lead ? x + gap : x; }
+};
+constexpr int kParts = 4;  // that the schedule is ahead at most
+
 struct Bars {
     uint64_t k_full[kMaxStages];   // a tile of keys is there
     uint64_t k_empty[kMaxStages];  // its MMAs are done
@@ -141,17 +158,22 @@ struct Bars {
     uint64_t s_empty[2];         // they have been read
     uint64_t p_full[2];          // its weights are written
     uint64_t p_empty[2];         // they are used up, and O holds them
-    uint64_t o_empty[2];         // its O has been read
-    uint64_t stats_full[2];      // the other stage's maxima and sums, for the stage that joins both
-    uint64_t mma_done[4];
-    float2 stats[kTile];
-    int64_t scratch[kThreads / 32];
+    uint64_t stats_full[2];      // a part's maxima and sums on the stage
+    uint64_t o_full[2];          // and its O
+    uint64_t o_empty[2];         // both have been read
+    uint64_t part_full[kParts], part_empty[kParts];
+    uint64_t mma_done[3];
+    Part part[kParts];
+    union {
+        float2 stats[2][kTile];            // of the stages
+        int64_t scratch[kThreads / 32];    // of the plan
+    };
     int64_t units;               // units of all items
     int64_t first_unit;          // this CTA's share begins here
     int64_t share;               // and has so many units
     int64_t into;                // units of its first request before it
     int32_t request, head, item, unit;  // its first unit
-    uint32_t nonfinite[16];      // parts, by number, that had infinities or NaN looked through
+    uint32_t nonfinite[2];       // parts, by number, that had infinities or NaN looked through
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -176,7 +198,7 @@ struct Shape {
 };
 
 // A CTA's share of the units of all items, walked item by item.  After next() returned true the
-// part is tiles [x0, x1) of the item's list, which all roles take from the last to the first.
+// part is tiles [x0, x1) of the item's list.
 struct Walk {
     int64_t u;       // first unit behind the part
     int64_t left;    // units of the share behind the part
@@ -230,10 +252,6 @@ struct Walk {
             left -= take;
         } while (x1 == x0);  // a share can end within an item's first units
         return true;
-    }
-    __device__ __forceinline__ bool wide(const KvAttentionArgs& a) const { return tokens > a.tile_tokens; }
-    __device__ __forceinline__ int32_t tile(const KvAttentionArgs& a, int32_t x) const {
-        return gap > 0 && x >= a.sink_tiles ? x + gap : x;
     }
     // Whether the item reads any of the positions pos .. pos + count - 1 of one page: those past its
     // last token may have no page yet, and the pages between the first tokens and the window none
@@ -345,14 +363,15 @@ __device__ __forceinline__ bool any_nonfinite(const uint4& v) {
     return ((top(v.x) | top(v.y) | top(v.z) | top(v.w)) & 0x80008000u) != 0;
 }
 
-// Makes the infinities and NaN of a tile of values zero; whether there were any before row `end`.
+// Makes the infinities and NaN of a quarter of a tile of values zero; whether there were any before
+// row `end`.
 template <int DB>
-__device__ __forceinline__ bool look_through(uint32_t tile, int64_t end) {
+__device__ __forceinline__ bool look_through(uint32_t tile, int quarter, int64_t end) {
     const int lane = threadIdx.x & 31;
     bool found = false;
     // 32 lanes take 512 bytes, four rows of a block; the place in the block does not matter
 #pragma unroll 1
-    for (int i = 0; i < DB * 32; i += 8) {
+    for (int i = quarter * DB * 8; i < (quarter + 1) * DB * 8; i += 8) {
         uint4 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = ld_shared_v4(tile + (i + k) * 512 + lane * 16);
@@ -369,8 +388,9 @@ __device__ __forceinline__ bool look_through(uint32_t tile, int64_t end) {
     return __any_sync(0xffffffffu, found);
 }
 
-// The tiles that not all tokens of a tile of queries attend, the first of them at position p:
-// from `diagonal` on, and those with keys behind the first tokens up to the window's `edge`.
+// The tiles that not all tokens of a tile of queries attend, the first of them at position p: from
+// `diagonal` on, and those with keys behind the first tokens (from tile `sinks` on) up to the
+// window's `edge`.
 struct Masked {
     int32_t diagonal, sinks, edge;
     __device__ __forceinline__ Masked(const KvAttentionArgs& a, int64_t p, int32_t count)
@@ -378,6 +398,8 @@ struct Masked {
         const int64_t out = p + count - 1 - a.window;  // the last position outside a window
         if (a.window > 0 && out >= 0) edge = static_cast<int32_t>(out >> 7);
     }
+    __device__ __forceinline__ Masked(const KvAttentionArgs& a, int32_t d, int32_t e)
+        : diagonal(d), sinks(a.sinks >> 7), edge(e) {}
     __device__ __forceinline__ bool any(int32_t kt) const {
         return kt >= diagonal || (kt <= edge && kt >= sinks);
     }
@@ -427,8 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     using S = Shape<DB>;
     constexpr int D = S::kCols;
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzle atoms of 1024 bytes
-    uint8_t* sQ = smem;
-    uint8_t *sK = smem + S::kOffKeys, *sV = smem + S::kOffValues;
+    uint8_t *sQ = smem, *sK = smem + S::kOffKeys, *sV = smem + S::kOffValues;
     Bars* bars = reinterpret_cast<Bars*>(smem + S::kOffBars);
     // the same in every lane, seen by the compiler through the shuffle
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -437,9 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&bars->k_full[i], 1);
-            mbar_init(&bars->k_empty[i], 2);
-            mbar_init(&bars->v_full[i], 1);
-            mbar_init(&bars->v_empty[i], 2);
+            mbar_init(&bars->k_empty[i], 2);  // both stages
+            mbar_init(&bars->v_full[i], 4);   // lanes of the loader, or the warps that look through
+            mbar_init(&bars->v_empty[i], 1);
             mbar_init(&bars->v_own[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -449,15 +470,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->s_empty[i], 4);
             mbar_init(&bars->p_full[i], 4);
             mbar_init(&bars->p_empty[i], 1);
-            mbar_init(&bars->o_empty[i], 4);
             mbar_init(&bars->stats_full[i], 4);
+            mbar_init(&bars->o_full[i], 1);
+            mbar_init(&bars->o_empty[i], 4);
+            bars->nonfinite[i] = 0;
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&bars->mma_done[i], 1);
-        for (int i = 0; i < 16; ++i) bars->nonfinite[i] = 0;
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(&bars->part_full[i], 1);
+            mbar_init(&bars->part_empty[i], 15);  // all warps but the loader
+        }
+        for (int i = 0; i < 3; ++i) mbar_init(&bars->mma_done[i], 1);
         bars->abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kKeyWarp && lane == 0) {
+    if (warp == kLoadWarp && lane == 0) {
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.q_one);
         if (TMA) {
@@ -483,39 +509,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto issue_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait_flag(bar, parity, wc.abort_flag, tries));
     };
+    uint32_t parts = 0;  // that the warp has seen
+    Part part;
+    // Takes the next part; false behind the last one, or when a wait ran out.
+    const auto next_part = [&]() -> bool {
+        const uint32_t at = parts % kParts, phase = (parts / kParts) & 1;
+        ++parts;
+        if (!(warp < kScoreWarp ? warp_wait(&bars->part_full[at], phase, wc)
+                                : issue_wait(&bars->part_full[at], phase)))
+            return false;
+        part = bars->part[at];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->part_empty[at]);
+        return __all_sync(0xffffffffu, part.x1 > part.x0);
+    };
+    uint32_t n = 0;  // steps of the parts before
 
     if (warp < kScoreWarp) {
-        // ---------------- softmax and epilogue: row = lane of tensor memory ----------------
+        // ---------------- softmax: row = lane of tensor memory ----------------
         warpgroup_reg_alloc<kSoftRegs>();
-        Walk w(a, bars);
         const int stage = warp >> 2;
         const int row = (warp & 3) * 32 + lane;
         const int group = a.num_heads / a.num_kv_heads;
-        const int row_token = row / group, row_head = row - row_token * group;
+        const int row_token = row / group;
         const float scale2 = a.scale * kLog2e;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t scores = lanes + S::score_col(stage), weights = lanes + kWeightCol + stage * 64;
-        const uint32_t out = lanes + S::out_col(stage), other_out = lanes + S::out_col(stage ^ 1);
-        const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
-        const int64_t sharing = min(static_cast<int64_t>(gridDim.x), bars->units);
-        uint32_t n = 0, part = 0;
-        uint32_t join_phase = 0;  // a bit for each stage
-        KvItem left{0, 0, 0, 0};
+        const uint32_t out = lanes + S::out_col(stage);
+        uint32_t uses = 0;
         bool ok = true;
-        while (ok && w.next(a)) {
-            const bool wide = w.wide(a);
-            const int tiles = w.x1 - w.x0, steps = wide ? 2 * tiles : tiles;
-            const int first_stage = n & 1, mine = stage ^ first_stage;  // the stage's first step
-            const int sub = wide ? mine : 0;                            // its tile of queries
-            const int32_t token0 = w.token0 + sub * a.tile_tokens;
-            const int count = min(a.tile_tokens, w.tokens - sub * a.tile_tokens);
-            const bool valid = row_token < count;
+        while (ok && next_part()) {
+            const int tiles = part.x1 - part.x0, steps = part.wide ? 2 * tiles : tiles;
+            const int mine = stage ^ (n & 1);       // the stage's first step
+            const int sub = part.wide ? mine : 0;   // its tile of queries
+            const int count = min(a.tile_tokens, part.tokens - sub * a.tile_tokens);
             const bool busy = (warp & 3) * 32 < count * group;  // the warp has rows
-            const int64_t pos0 = w.r.len + token0, pos = pos0 + row_token;
-            const Masked masks(a, pos0, count);
+            const int64_t pos = part.pos + sub * a.tile_tokens + row_token;
+            const Masked masks(a, sub ? part.diagonal[1] : part.diagonal[0], sub ? part.edge[1] : part.edge[0]);
             float m = -INFINITY, l = 0.0f;
             for (int x = mine; x < steps; x += 2) {
-                const int32_t kt = w.tile(a, w.x1 - 1 - (wide ? x >> 1 : x));
                 const uint32_t turn = (n + x) >> 1;  // of the stage
                 if (!warp_wait(&bars->s_full[stage], turn & 1, wc)) {
                     ok = false;
@@ -529,450 +561,531 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     if (lane == 0) mbar_arrive(&bars->p_full[stage]);
-                } else {
-                    uint32_t s[4][32];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_ld_x32(scores + k * 32, s[k]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) asm volatile("" : "+r"(s[c >> 5][c & 31]));  // not before
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->s_empty[stage]);
-                    const auto f = [&](int c) -> float { return __uint_as_float(s[c >> 5][c & 31]); };
-                    const bool masked = masks.any(kt);
-                    float mul = scale2;
-                    if (masked || scale2 < 0.0f) {
-                        // scaled before masks and maxima, which then need not know the sign
-                        mul = 1.0f;
-                        const Attended may_attend(a, pos, kt);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t may = masked ? may_attend.bits(k * 32) : ~0u;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                const float v = __uint_as_float(s[k][c]) * scale2;
-                                s[k][c] = __float_as_uint((may >> c) & 1u ? v : -INFINITY);
-                            }
-                        }
-                    }
-                    float t0 = f(0), t1 = f(1), t2 = f(2), t3 = f(3);
-#pragma unroll
-                    for (int c = 4; c < 124; c += 8) {
-                        t0 = fmax3(t0, f(c), f(c + 1));
-                        t1 = fmax3(t1, f(c + 2), f(c + 3));
-                        t2 = fmax3(t2, f(c + 4), f(c + 5));
-                        t3 = fmax3(t3, f(c + 6), f(c + 7));
-                    }
-                    t0 = fmax3(t0, f(124), f(125));
-                    t1 = fmax3(t1, f(126), f(127));
-                    const float top = fmaxf(fmax3(t0, t1, t2), t3) * mul;
-                    const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
-                    const float m_new = move ? top : m;
-                    const float back = move && m > -INFINITY ? exp2_approx(m - m_new) : 1.0f;
-                    m = m_new;
-                    const float ref = m == -INFINITY ? 0.0f : m;
-                    // the stage's step before is done: O holds still, and its weights' place is free
-                    if (turn > 0 && !warp_wait(&bars->p_empty[stage], (turn - 1) & 1, wc)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (x > mine && __any_sync(0xffffffffu, back != 1.0f)) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld_x32(out + c, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * back);
-                            tmem_st_x32(out + c, o);
-                        }
-                    }
-                    // The weights are rounded to bf16, by up to 2^-8 of each: the second product's
-                    // operands have one type, and the values are bf16.  Their sum stays in fp32,
-                    // unrounded.
-                    float sum[4] = {};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int c = h * 64 + 2 * k;
-                            float e0, e1;
-                            fma2x(e0, e1, f(c), f(c + 1), mul, mul, -ref, -ref);
-                            e0 = exp2_approx(e0);
-                            e1 = exp2_approx(e1);
-                            add2(sum[2 * (k & 1)], sum[2 * (k & 1) + 1], e0, e1);
-                            p[k] = pack_bf16x2(e0, e1);
-                        }
-                        tmem_st_x32(weights + h * 32, p);
-                    }
-                    l = l * back + ((sum[0] + sum[2]) + (sum[1] + sum[3]));
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->p_full[stage]);
+                    continue;
                 }
-            }
-            const bool join = !wide && steps > 1;   // the first step's stage joins both
-            // the last turns of this stage and of the other one
-            const uint32_t last = (n + mine + (steps - 1 - mine) / 2 * 2) >> 1;
-            const uint32_t other_last = (n + (mine ^ 1) + (steps - 1 - (mine ^ 1)) / 2 * 2) >> 1;
-            n += steps;
-            ++part;
-            const uint32_t joined = join_phase >> first_stage & 1;
-            join_phase ^= join ? 1u << first_stage : 0u;
-            if (!ok || mine >= steps) continue;
-            ok = warp_wait(&bars->p_empty[stage], last & 1, wc);
-            if (!ok) break;
-            if (join && mine == 1) {
-                bars->stats[row] = make_float2(m, l);
+                uint32_t s[4][32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld_x32(scores + k * 32, s[k]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 128; ++c) asm volatile("" : "+r"(s[c >> 5][c & 31]));  // not before
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->stats_full[first_stage]);
-                continue;
-            }
-            float f0 = 1.0f, f1 = 0.0f;  // factors of this stage's sums and of the other's
-            if (join) {
-                ok = warp_wait(&bars->stats_full[stage], joined, wc) &&
-                     warp_wait(&bars->p_empty[stage ^ 1], other_last & 1, wc);
-                if (!ok) break;
-                const float2 other = bars->stats[row];
-                const float top = fmaxf(m, other.x);
-                f0 = m == -INFINITY ? 0.0f : exp2_approx(m - top);
-                f1 = other.x == -INFINITY ? 0.0f : exp2_approx(other.x - top);
-                l = l * f0 + other.y * f1;
-                m = top;
-            }
-            tc_fence_after();
-            const bool whole = w.x0 == 0 && w.x1 == w.tiles;
-            const float inv = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
-            const bool mend = *const_cast<volatile uint32_t*>(&bars->nonfinite[(part - 1) & 15]) == part;
-            const int64_t out_row = (w.r.first + token0 + row_token) * a.num_heads + w.head * group + row_head;
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.x0 > 0 ? 0 : 1);
-            const int slot_row = sub * kTile + row;
-            if (busy) {
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld_x32(out + c, o);
-                    if (join) {
-                        uint32_t o1[32];
-                        tmem_ld_x32(other_out + c, o1);
-                        tmem_ld_wait();
+                if (lane == 0) mbar_arrive(&bars->s_empty[stage]);
+                const auto f = [&](int c) -> float { return __uint_as_float(s[c >> 5][c & 31]); };
+                float mul = scale2;
+                if (!(scale2 > 0.0f)) {  // scaled before the maximum, which then need not know the sign
+                    mul = 1.0f;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
-                    } else {
-                        tmem_ld_wait();
-                    }
-                    if (valid && mend) {
-                        // values that were made zero for the rows that do not attend them
-                        for (int x = w.x0; x < w.x1; ++x) {
-                            const int32_t kt = w.tile(a, x);
-                            if (!Masked(a, w.r.len + w.token0, w.tokens).any(kt)) continue;
-                            for (int t = 0; t < kTile; ++t) {
-                                const int64_t at = static_cast<int64_t>(kt) * kTile + t;
-                                if (at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks)) continue;
-                                const int64_t from = Place(a, w.b, at, true).offset(a);
-                                if (from < 0) continue;
-                                const uint16_t* v = a.cache_layer + a.kv_stride + from + w.head * D + c;
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    const uint32_t bits = __ldg(v + k);
-                                    if ((bits & 0x7f80u) == 0x7f80u)
-                                        o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(bits << 16));
-                                }
-                            }
-                        }
-                    }
-                    if (valid && whole) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            p[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-                        uint16_t* to = a.out + out_row * D + c;
-                        if (sectors) {
-                            st_v8(to, p);
-                            st_v8(to + 16, p + 8);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                st_v4(to + 8 * k, make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]));
-                        }
-                    } else if (valid) {
-                        float* to = reinterpret_cast<float*>(a.workspace) + (slot * ws.rows + slot_row) * D + c;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) st_v8(to + 8 * k, o + 8 * k);
-                    }
-                    __syncwarp();
+                    for (int c = 0; c < 128; ++c) s[c >> 5][c & 31] = __float_as_uint(f(c) * scale2);
                 }
-                if (valid && whole && a.lse != nullptr)
-                    a.lse[out_row] = l != 0.0f ? m * kLn2 + logf(l) : -INFINITY;
-                if (valid && !whole)
-                    reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + slot_row] = make_float2(m, l);
+                const int32_t kt = part.tile(part.x1 - 1 - (part.wide ? x >> 1 : x));
+                if (masks.any(kt)) {
+                    const Attended may(a, pos, kt);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t bits = may.bits(k * 32);
+                        if (__all_sync(0xffffffffu, bits == ~0u)) continue;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!((bits >> c) & 1u)) s[k][c] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float t0 = f(0), t1 = f(1), t2 = f(2), t3 = f(3);
+#pragma unroll
+                for (int c = 4; c < 124; c += 8) {
+                    t0 = fmax3(t0, f(c), f(c + 1));
+                    t1 = fmax3(t1, f(c + 2), f(c + 3));
+                    t2 = fmax3(t2, f(c + 4), f(c + 5));
+                    t3 = fmax3(t3, f(c + 6), f(c + 7));
+                }
+                t0 = fmax3(t0, f(124), f(125));
+                t1 = fmax3(t1, f(126), f(127));
+                const float top = fmaxf(fmax3(t0, t1, t2), t3) * mul;
+                const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+                const float m_new = move ? top : m;
+                const float back = move && m > -INFINITY ? exp2_approx(m - m_new) : 1.0f;
+                m = m_new;
+                const float ref = m == -INFINITY ? 0.0f : m;
+                // the stage's step before is done: O holds still, and its weights' place is free
+                if (turn > 0 && !warp_wait(&bars->p_empty[stage], (turn - 1) & 1, wc)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (x > mine && __any_sync(0xffffffffu, back != 1.0f)) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld_x16(out + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * back);
+                        tmem_st_x16(out + c, o);
+                    }
+                }
+                // The weights are rounded to bf16, by up to 2^-8 of each: the second product's
+                // operands have one type, and the values are bf16.  Their sum stays in fp32, unrounded.
+                // Sixteen at a time go through the same operation: written value by value, the order
+                // that comes out waits for every exponential, 1550 cycles a step instead of 930.
+                float sum[4] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float e[16];
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2)
+                            fma2x(e[k], e[k + 1], f(h * 64 + g * 16 + k), f(h * 64 + g * 16 + k + 1), mul, mul,
+                                  -ref, -ref);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) e[k] = exp2_approx(e[k]);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            add2(sum[2 * (k & 1)], sum[2 * (k & 1) + 1], e[2 * k], e[2 * k + 1]);
+                            p[g * 8 + k] = pack_bf16x2(e[2 * k], e[2 * k + 1]);
+                        }
+                    }
+                    tmem_st_x32(weights + h * 32, p);
+                }
+                l = l * back + ((sum[0] + sum[2]) + (sum[1] + sum[3]));
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_full[stage]);
             }
-            if (!whole && w.x0 == 0) {
-                const int64_t end = w.u + (w.units_each - w.at);
-                left.row = w.r.first + w.token0;
-                left.head = w.head * group;
-                left.tokens = w.tokens;
-                left.parts = static_cast<int32_t>(quotient(end * sharing - 1, bars->units) - blockIdx.x) + 1;
-            }
-            tc_fence_before();
+            n += steps;
+            if (!ok || mine >= steps) continue;
+            if (uses > 0 && !warp_wait(&bars->o_empty[stage], (uses - 1) & 1, wc)) break;  // read with its O
+            bars->stats[stage][row] = make_float2(m, l);
+            ++uses;
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars->o_empty[stage]);
-                if (join) mbar_arrive(&bars->o_empty[stage ^ 1]);
-            }
+            if (lane == 0) mbar_arrive(&bars->stats_full[stage]);
         }
-        // a stage that had no step of the item that is left does not know it: the other writes it
-        if ((warp & 3) == 0 && lane == 0) {
-            KvItem* items = reinterpret_cast<KvItem*>(a.workspace + ws.items);
-            if (!ok) left.tokens = 0;
-            items[2 * blockIdx.x + stage] = left;
-        }
-    } else {
+    } else if (warp < kEndWarp) {
         warpgroup_reg_dealloc<kIssueRegs>();
-        if (warp < kKeyWarp) {
-            // ---------------- MMA issuers, all lanes together ----------------
-            // One warp for each product of each stage: the tensor cores queue little work ahead, so
-            // what a warp needs for its waits and descriptors goes by during the others' MMAs.
-            // Both stages wait for all keys, values and queries, and release them, the other stage's
-            // too: a wait cannot tell a phase from the one two before or behind, so that neither may
-            // miss one.
-            Walk w(a, bars);
-            // A wait that runs out is looked at once a step; what is issued until then is not used.
-            bool failed = false;
-            const auto wait = [&](uint64_t* bar, uint32_t parity) {
-                failed |= !mbar_wait_flag(bar, parity, wc.abort_flag, tries);
-            };
-            const bool scores = warp < kOutWarp;
+      if (warp < kLoadWarp) {
+        // ---------------- MMA issuers, all lanes together ----------------
+        // The tensor cores queue little work ahead, so what a warp needs for its waits and
+        // descriptors has to go by during the others' MMAs.
+        // A wait that runs out is looked at once a step; what is issued until then is not used.
+        bool failed = false;
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            failed |= !mbar_wait_flag(bar, parity, wc.abort_flag, tries);
+        };
+        const auto go_on = [&] { return !__any_sync(0xffffffffu, failed); };
+        RingPos at;
+        if (warp < kOutWarp) {
+            // The scores of a stage.  Both stages wait for all keys and queries and release them, the
+            // other stage's too: a wait cannot tell a phase from the one two before or behind, so
+            // that neither may miss one.
             const uint32_t stage = warp & 1;
-            const uint32_t id = scores ? idesc_bf16(128, kTile, false, false) : idesc_bf16(128, D, false, true);
-            const uint64_t a_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
-            const uint64_t b_desc = scores ? sdesc_sw128(smem_u32(sK), 16, DB * 1024)
-                                           : sdesc_sw128(smem_u32(sV), 1024, DB * 1024);
-            const uint32_t d = tmem + (scores ? S::score_col(stage) : S::out_col(stage));
-            const uint32_t weights = tmem + kWeightCol + stage * 64;
-            uint64_t* full = scores ? bars->k_full : bars->v_full;
-            uint64_t* empty = scores ? bars->k_empty : bars->v_empty;
-            const uint32_t stages = scores ? S::kKeyStages : S::kValueStages;
-            uint32_t n = 0, queries = 0, uses = 0;
-            RingPos at;
-            while (!__any_sync(0xffffffffu, failed) && __any_sync(0xffffffffu, w.next(a))) {
-                const bool wide = __any_sync(0xffffffffu, w.wide(a));
-                const int tiles = __shfl_sync(0xffffffffu, w.x1 - w.x0, 0), steps = wide ? 2 * tiles : tiles;
+            const uint32_t id = idesc_bf16(128, kTile, false, false);
+            const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, DB * 1024);
+            const uint32_t d = tmem + S::score_col(stage);
+            uint32_t queries = 0;
+            const auto pass = [&] {  // over a tile of the other stage
+                wait(&bars->k_full[at.stage], at.phase);
+                if (lane == 0) mbar_arrive(&bars->k_empty[at.stage]);
+                __syncwarp();
+                at.next(S::kKeyStages);
+            };
+            while (go_on() && next_part()) {
+                const bool wide = __any_sync(0xffffffffu, part.wide != 0);
+                const int tiles = __shfl_sync(0xffffffffu, part.x1 - part.x0, 0), steps = wide ? 2 * tiles : tiles;
                 const int mine = (n & 1) ^ stage;  // the stage's first step
                 const uint32_t query = queries + (wide ? mine : 0);
-                if (scores)
-                    for (uint32_t q = queries; q < queries + (wide ? 2 : 1); ++q) {
-                        wait(&bars->q_full[q & 1], (q >> 1) & 1);
-                        if ((wide ? q != query : mine >= steps) && lane == 0) mbar_arrive(&bars->q_empty[q & 1]);
-                        __syncwarp();
-                    }
-                const auto pass = [&] {  // over a tile of the other stage
-                    wait(&full[at.stage], at.phase);
-                    if (lane == 0) mbar_arrive(&empty[at.stage]);
+                for (uint32_t q = queries; q < queries + (wide ? 2 : 1); ++q) {
+                    wait(&bars->q_full[q & 1], (q >> 1) & 1);
+                    if ((wide ? q != query : mine >= steps) && lane == 0) mbar_arrive(&bars->q_empty[q & 1]);
                     __syncwarp();
-                    at.next(stages);
-                };
+                }
                 if (!wide && mine == 1) pass();
 #pragma unroll 1
                 for (int x = mine; x < steps; x += 2) {
-                    const uint32_t turn = (n + x) >> 1;
-                    const uint64_t bd = desc_add_bytes(b_desc, uniform(at.stage) * S::kBytes);
-                    wait(&full[at.stage], at.phase);
-                    if (scores) {
-                        const uint64_t ad = desc_add_bytes(a_desc, uniform(query & 1) * S::kBytes);
-                        // the scores that were in the place before have been read
-                        const uint32_t before = n + x - S::kScores;
-                        if (n + x >= S::kScores) wait(&bars->s_empty[before & 1], (before >> 1) & 1);
-                        tc_fence_after();
+                    const uint64_t qd = desc_add_bytes(q_desc, uniform(query & 1) * S::kBytes);
+                    const uint64_t kd = desc_add_bytes(k_desc, uniform(at.stage) * S::kBytes);
+                    wait(&bars->k_full[at.stage], at.phase);
+                    // the scores that were in the place before have been read
+                    const uint32_t before = n + x - S::kScores;
+                    if (n + x >= S::kScores) wait(&bars->s_empty[before & 1], (before >> 1) & 1);
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int kb = 0; kb < DB; ++kb)
+                    for (int kb = 0; kb < DB; ++kb)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16_elect(d, desc_add_bytes(ad, kb * 16384 + k * 32),
-                                               desc_add_bytes(bd, kb * 1024 + k * 32), id,
-                                               (kb | k) != 0 ? 1u : 0u);
-                        mma_commit_elect(&bars->s_full[stage]);
-                        if (x + 2 >= steps) mma_commit_elect(&bars->q_empty[query & 1]);
-                    } else {
-                        const uint32_t keep = uniform(x == mine ? 0u : 1u);
-                        if (x == mine) wait(&bars->o_empty[stage], (uses++ & 1) ^ 1);
-                        wait(&bars->p_full[stage], turn & 1);
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)  // 16 keys: two atoms of each block
-                                mma_bf16_ts_elect(d, weights + 32 * h + 8 * k,
-                                                  desc_add_bytes(bd, (h * 4 + k) * 2 * DB * 1024), id,
-                                                  (h | k) != 0 ? 1u : keep);
-                        mma_commit_elect(&bars->p_empty[stage]);
-                    }
-                    mma_commit_elect(&empty[at.stage]);
-                    at.next(stages);
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_elect(d, desc_add_bytes(qd, kb * 16384 + k * 32),
+                                           desc_add_bytes(kd, kb * 1024 + k * 32), id, (kb | k) != 0 ? 1u : 0u);
+                    mma_commit_elect(&bars->s_full[stage]);
+                    if (x + 2 >= steps) mma_commit_elect(&bars->q_empty[query & 1]);
+                    mma_commit_elect(&bars->k_empty[at.stage]);
+                    at.next(S::kKeyStages);
                     if (!wide && x + 1 < steps) pass();
-                    if (__any_sync(0xffffffffu, failed)) break;
+                    if (!go_on()) break;
                 }
                 n += steps;
                 queries += wide ? 2 : 1;
             }
-            uint64_t* mma_done = &bars->mma_done[warp - kScoreWarp];
-            mma_commit_elect(mma_done);
-            mbar_wait_inl(mma_done, 0, wc, false);
-        } else if (warp <= kCheckWarp) {
-            // ---------------- queries, keys, values ----------------
-            const bool keys = warp == kKeyWarp;
-            const uint16_t* plane = a.cache_layer + (keys ? 0 : a.kv_stride);
-            Walk w(a, bars);
-            uint8_t* tiles = keys ? sK : sV;
-            uint64_t *full = keys ? bars->k_full : bars->v_full, *empty = keys ? bars->k_empty : bars->v_empty;
-            RingPos at;
-            uint32_t queries = 0, part = 0, own_phase = 0;
-            bool ok = true;
-            const auto next_tile = [&] { at.next(keys ? S::kKeyStages : S::kValueStages); };
-            const auto load_queries = [&]() -> bool {
-                const int subs = w.wide(a) ? 2 : 1;
-                for (int sub = 0; sub < subs; ++sub, ++queries) {
-                    const uint32_t q = queries & 1;
-                    if (!issue_wait(&bars->q_empty[q], ((queries >> 1) & 1) ^ 1)) return false;
-                    const int group = a.num_heads / a.num_kv_heads;
-                    const int32_t token0 = w.token0 + sub * a.tile_tokens;
-                    const bool one = w.tokens - sub * a.tile_tokens == 1;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&bars->q_full[q], DB * 128 * group * (one ? 1 : a.tile_tokens));
-                    __syncwarp();
-                    if (lane < DB)
-                        tma_load_3d(sQ + q * S::kBytes + lane * 16384, one ? &maps.q_one : &maps.q,
-                                    &bars->q_full[q], lane * 64, w.head * group,
-                                    static_cast<int32_t>(w.r.first + token0));
-                }
-                return true;
-            };
-            // the tile's infinities and NaN, where not every row attends every key
-            const auto mend = [&](uint32_t stage, int32_t kt) {
-                const int64_t end = w.r.len + w.token0 + w.tokens - static_cast<int64_t>(kt) * kTile;
-                if (look_through<DB>(smem_u32(sV) + stage * S::kBytes, end) && lane == 0)
-                    *const_cast<volatile uint32_t*>(&bars->nonfinite[part & 15]) = part + 1;
-            };
-            if constexpr (TMA) {
-                const int slots = maps.slots, boxes = kTile / slots;
-                if (warp == kCheckWarp) {
-                    for (; ok && __any_sync(0xffffffffu, w.next(a)); ++part) {
-                        const Masked masks(a, w.r.len + w.token0, w.tokens);
-                        for (int x = w.x1 - 1; ok && x >= w.x0; --x, next_tile()) {
-                            const int32_t kt = w.tile(a, x);
-                            if (!masks.any(kt)) continue;
-                            ok = issue_wait(&bars->v_own[at.stage], (own_phase >> at.stage) & 1);
-                            if (!ok) break;
-                            own_phase ^= 1u << at.stage;
-                            mend(at.stage, kt);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&full[at.stage]);
-                        }
+        } else {
+            const uint32_t id = idesc_bf16(128, D, false, true);
+            const uint64_t v_desc = sdesc_sw128(smem_u32(sV), 1024, DB * 1024);
+            uint32_t empty_phase = 3;  // a bit for each stage; the first wait passes
+            while (go_on() && next_part()) {
+                const bool wide = __any_sync(0xffffffffu, part.wide != 0);
+                const int tiles = __shfl_sync(0xffffffffu, part.x1 - part.x0, 0), steps = wide ? 2 * tiles : tiles;
+#pragma unroll 1
+                for (int x = 0; x < steps; ++x, ++n) {
+                    const uint32_t stage = uniform(n & 1);
+                    const bool odd = wide && (x & 1);
+                    const uint64_t vd = desc_add_bytes(v_desc, uniform(at.stage) * S::kBytes);
+                    const uint32_t d = tmem + S::out_col(stage), p = tmem + kWeightCol + stage * 64;
+                    const uint32_t keep = uniform(x < 2 ? 0u : 1u);
+                    if (!odd) wait(&bars->v_full[at.stage], at.phase);
+                    if (x < 2) {
+                        wait(&bars->o_empty[stage], empty_phase >> stage & 1);
+                        empty_phase ^= 1u << stage;
                     }
-                } else {
-                    const CUtensorMap* map = keys ? &maps.k : &maps.v;
-                    while (ok && __any_sync(0xffffffffu, w.next(a))) {
-                        const Masked masks(a, w.r.len + w.token0, w.tokens);
-                        if (keys) ok = load_queries();
-                        for (int x = w.x1 - 1; ok && x >= w.x0; --x, next_tile()) {
-                            const int32_t kt = w.tile(a, x);
-                            const int64_t pos = static_cast<int64_t>(kt) * kTile + lane * slots;
-                            const Place place(a, w.b, pos, lane < boxes && w.reads(a, pos, slots));
-                            ok = issue_wait(&empty[at.stage], at.phase ^ 1);
-                            if (!ok) break;
-                            uint64_t* bar = &full[at.stage];
-                            if (!keys && masks.any(kt)) bar = &bars->v_own[at.stage];
-                            if (lane == 0) mbar_arrive_expect_tx(bar, S::kBytes);
-                            __syncwarp();
-                            if (lane < boxes)
-                                tma_load_5d(tiles + at.stage * S::kBytes + lane * slots * DB * 128, map, bar,
-                                            0, 0, w.head * DB, place.slot >> 3, place.page);
-                        }
-                    }
-                }
-                if (!ok) spin_ns(kDrainNs);
-            } else if (warp <= kValueWarp) {
-                // Row by row: a row's 16-byte chunks to their places in the swizzled atoms.  A tile
-                // is handed over when the next one is on its way, or before any longer wait.
-                bool pending = false;
-                uint32_t pending_stage = 0, pending_part = 0;
-                int32_t pending_kt = 0;
-                int64_t pending_end = 0;
-                bool pending_partial = false;
-                const auto hand_over = [&] {
-                    if (pending_partial &&
-                        look_through<DB>(smem_u32(sV) + pending_stage * S::kBytes,
-                                         pending_end - static_cast<int64_t>(pending_kt) * kTile) &&
-                        lane == 0)
-                        *const_cast<volatile uint32_t*>(&bars->nonfinite[pending_part & 15]) = pending_part + 1;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[pending_stage]);
-                    pending = false;
-                };
-                const auto flush = [&] {
-                    cp_async_wait<0>();
-                    __syncwarp();
-                    if (pending) hand_over();
-                };
-                constexpr int kChunks = DB * 8, kRows = 32 / kChunks;  // of a row; rows at once
-                const int chunk = lane % kChunks;
-                for (; ok && __any_sync(0xffffffffu, w.next(a)); ++part) {
-                    if (keys) {
-                        flush();
-                        ok = load_queries();
-                    }
-                    const int64_t end = w.r.len + w.token0 + w.tokens;
-                    const Masked masks(a, w.r.len + w.token0, w.tokens);
-                    for (int x = w.x1 - 1; ok && x >= w.x0; --x, next_tile()) {
-                        const int32_t kt = w.tile(a, x);
-                        int64_t offset[4];
+                    wait(&bars->p_full[stage], (n >> 1) & 1);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int64_t pos = static_cast<int64_t>(kt) * kTile + k * 32 + lane;
-                            offset[k] = Place(a, w.b, pos, w.reads(a, pos, 1)).offset(a);
-                        }
-                        if (!__all_sync(0xffffffffu, mbar_try_wait(&empty[at.stage], at.phase ^ 1))) {
-                            flush();
-                            ok = issue_wait(&empty[at.stage], at.phase ^ 1);
-                            if (!ok) break;
-                        }
-                        const uint32_t to = smem_u32(tiles) + at.stage * S::kBytes;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll 4
-                            for (int i = 0; i < 32; i += kRows) {
-                                const int in = i + lane / kChunks, r = k * 32 + in;
-                                const int64_t from = __shfl_sync(0xffffffffu, offset[k], in);
-                                cp_async_16(to + (r >> 3) * DB * 1024 + (chunk >> 3) * 1024 + (r & 7) * 128 +
-                                                (((chunk & 7) ^ (r & 7)) << 4),
-                                            plane + (from < 0 ? 0 : from + w.head * D + chunk * 8),
-                                            from < 0 ? 0 : 16);
-                            }
-                        cp_async_commit();
-                        if (pending) {
-                            cp_async_wait<1>();
-                            __syncwarp();
-                            hand_over();
-                        }
-                        pending = true;
-                        pending_stage = at.stage;
-                        pending_part = part;
-                        pending_kt = kt;
-                        pending_end = end;
-                        pending_partial = !keys && masks.any(kt);
+                        for (int k = 0; k < 4; ++k)  // 16 keys: two atoms of each block
+                            mma_bf16_ts_elect(d, p + 32 * h + 8 * k,
+                                              desc_add_bytes(vd, (h * 4 + k) * 2 * DB * 1024), id,
+                                              (h | k) != 0 ? 1u : keep);
+                    mma_commit_elect(&bars->p_empty[stage]);
+                    if (x + 2 >= steps) mma_commit_elect(&bars->o_full[stage]);
+                    if (!wide || odd) {
+                        mma_commit_elect(&bars->v_empty[at.stage]);
+                        at.next(S::kValueStages);
                     }
+                    if (!go_on()) break;
                 }
-                flush();
-                if (!ok) spin_ns(kDrainNs);
             }
+        }
+        uint64_t* mma_done = &bars->mma_done[warp - kScoreWarp];
+        mma_commit_elect(mma_done);
+        mbar_wait_inl(mma_done, 0, wc, false);
+      } else {
+        // ---------------- schedule, queries, keys, values ----------------
+        Walk w(a, bars);
+        const int group = a.num_heads / a.num_kv_heads;
+        const int64_t sharing = min(static_cast<int64_t>(gridDim.x), bars->units);
+        RingPos kpos, vpos;
+        uint32_t queries = 0;
+        bool ok = true, more = true;
+        const auto publish = [&]() -> bool {
+            const uint32_t at = parts % kParts;
+            if (!issue_wait(&bars->part_empty[at], ((parts / kParts) & 1) ^ 1)) return false;
+            ++parts;
+            more = __any_sync(0xffffffffu, w.next(a));
+            if (lane == 0) {
+                Part* p = &bars->part[at];
+                p->x0 = p->x1 = 0;
+                if (more) {
+                    const bool wide = w.tokens > a.tile_tokens;
+                    p->pos = w.r.len + w.token0;
+                    p->row = static_cast<int32_t>(w.r.first) + w.token0;
+                    p->b = w.b;
+                    p->tokens = w.tokens;
+                    p->head = w.head;
+                    p->x0 = w.x0;
+                    p->x1 = w.x1;
+                    p->lead = w.gap > 0 ? a.sink_tiles : INT32_MAX;
+                    p->gap = w.gap;
+                    p->wide = wide;
+                    p->whole = w.x0 == 0 && w.x1 == w.tiles;
+                    p->left = 0;
+                    if (w.x0 == 0 && w.x1 < w.tiles) {
+                        const int64_t end = w.u + (w.units_each - w.at);
+                        p->left = static_cast<int32_t>(quotient(end * sharing - 1, bars->units) - blockIdx.x) + 1;
+                    }
+                    for (int i = 0; i < 2; ++i) {
+                        const Masked m(a, p->pos + i * a.tile_tokens,
+                                       min(a.tile_tokens, w.tokens - i * a.tile_tokens));
+                        p->diagonal[i] = m.diagonal;
+                        p->edge[i] = m.edge;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->part_full[at]);
+            return more;
+        };
+        const auto load_queries = [&]() -> bool {
+            const int subs = w.tokens > a.tile_tokens ? 2 : 1;
+            for (int sub = 0; sub < subs; ++sub, ++queries) {
+                const uint32_t q = queries & 1;
+                if (!issue_wait(&bars->q_empty[q], ((queries >> 1) & 1) ^ 1)) return false;
+                const int32_t token0 = w.token0 + sub * a.tile_tokens;
+                const bool one = w.tokens - sub * a.tile_tokens == 1;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&bars->q_full[q], DB * 128 * group * (one ? 1 : a.tile_tokens));
+                __syncwarp();
+                if (lane < DB)
+                    tma_load_3d(sQ + q * S::kBytes + lane * 16384, one ? &maps.q_one : &maps.q,
+                                &bars->q_full[q], lane * 64, w.head * group,
+                                static_cast<int32_t>(w.r.first + token0));
+            }
+            return true;
+        };
+        // Hands values over, or keys: to the MMAs, or to the warps that look them through first.
+        const auto arrive = [&](bool keys, uint32_t stage, bool masked) {
+            if (keys) {
+                if (lane == 0) mbar_arrive(&bars->k_full[stage]);
+            } else if (masked) {
+                if (lane == 0) mbar_arrive(&bars->v_own[stage]);
+            } else if (lane < 4) {
+                mbar_arrive(&bars->v_full[stage]);
+            }
+        };
+        if constexpr (TMA) {
+            const int slots = maps.slots, boxes = kTile / slots;
+            while (ok && publish()) {
+                const Masked masks(a, w.r.len + w.token0, w.tokens);
+                const int32_t lead = w.gap > 0 ? a.sink_tiles : INT32_MAX;
+                ok = load_queries();
+                for (int x = w.x1 - 1; ok && x >= w.x0; --x) {
+                    const int32_t kt = x >= lead ? x + w.gap : x;
+                    const int64_t pos = static_cast<int64_t>(kt) * kTile + lane * slots;
+                    const Place place(a, w.b, pos, lane < boxes && w.reads(a, pos, slots));
+                    ok = issue_wait(&bars->k_empty[kpos.stage], kpos.phase ^ 1);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[kpos.stage], S::kBytes);
+                    __syncwarp();
+                    const uint32_t box = lane * slots * DB * 128;
+                    if (lane < boxes)
+                        tma_load_5d(sK + kpos.stage * S::kBytes + box, &maps.k, &bars->k_full[kpos.stage], 0, 0,
+                                    w.head * DB, place.slot >> 3, place.page);
+                    kpos.next(S::kKeyStages);
+                    ok = issue_wait(&bars->v_empty[vpos.stage], vpos.phase ^ 1);
+                    if (!ok) break;
+                    const bool masked = masks.any(kt);
+                    uint64_t* bar = masked ? &bars->v_own[vpos.stage] : &bars->v_full[vpos.stage];
+                    if (lane == 0) mbar_arrive_expect_tx(bar, S::kBytes);
+                    else if (!masked && lane < 4) mbar_arrive(bar);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_5d(sV + vpos.stage * S::kBytes + box, &maps.v, bar, 0, 0, w.head * DB,
+                                    place.slot >> 3, place.page);
+                    vpos.next(S::kValueStages);
+                }
+            }
+        } else {
+            // Row by row: a row's 16-byte chunks to their places in the swizzled atoms.  A tile is
+            // handed over when the next one is on its way, or before any longer wait.
+            bool pending = false, pending_keys = false, pending_masked = false;
+            uint32_t pending_stage = 0;
+            const auto hand_over = [&] {
+                __syncwarp();
+                fence_proxy_async_smem();
+                __syncwarp();
+                arrive(pending_keys, pending_stage, pending_masked);
+                pending = false;
+            };
+            const auto flush = [&] {
+                cp_async_wait<0>();
+                if (pending) hand_over();
+            };
+            constexpr int kChunks = DB * 8, kRows = 32 / kChunks;  // of a row; rows at once
+            const int chunk = lane % kChunks;
+            while (ok) {
+                flush();
+                if (!publish()) break;
+                const Masked masks(a, w.r.len + w.token0, w.tokens);
+                const int32_t lead = w.gap > 0 ? a.sink_tiles : INT32_MAX;
+                ok = load_queries();
+                for (int y = 0; ok && y < 2 * (w.x1 - w.x0); ++y) {  // keys, then values, of each tile
+                    const bool keys = (y & 1) == 0;
+                    const int x = w.x1 - 1 - (y >> 1);
+                    const int32_t kt = x >= lead ? x + w.gap : x;
+                    RingPos& at = keys ? kpos : vpos;
+                    uint64_t* empty = keys ? &bars->k_empty[at.stage] : &bars->v_empty[at.stage];
+                    if (!__all_sync(0xffffffffu, mbar_try_wait(empty, at.phase ^ 1))) {
+                        flush();
+                        ok = issue_wait(empty, at.phase ^ 1);
+                        if (!ok) break;
+                    }
+                    const uint32_t to = smem_u32(keys ? sK : sV) + at.stage * S::kBytes;
+                    const uint16_t* plane = a.cache_layer + (keys ? 0 : a.kv_stride);
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const int64_t pos = static_cast<int64_t>(kt) * kTile + k * 32 + lane;
+                        const int64_t offset = Place(a, w.b, pos, w.reads(a, pos, 1)).offset(a);
+#pragma unroll 4
+                        for (int i = 0; i < 32; i += kRows) {
+                            const int in = i + lane / kChunks, r = k * 32 + in;
+                            const int64_t from = __shfl_sync(0xffffffffu, offset, in);
+                            cp_async_16(to + (r >> 3) * DB * 1024 + (chunk >> 3) * 1024 + (r & 7) * 128 +
+                                            (((chunk & 7) ^ (r & 7)) << 4),
+                                        plane + (from < 0 ? 0 : from + w.head * D + chunk * 8), from < 0 ? 0 : 16);
+                        }
+                    }
+                    cp_async_commit();
+                    if (pending) {
+                        cp_async_wait<1>();
+                        hand_over();
+                    }
+                    pending = true;
+                    pending_keys = keys;
+                    pending_masked = masks.any(kt);
+                    pending_stage = at.stage;
+                    at.next(keys ? S::kKeyStages : S::kValueStages);
+                }
+            }
+            flush();
+        }
+        if (*wc.abort_flag) spin_ns(kDrainNs);
+      }
+    } else {
+        // ---------------- values looked through, and the epilogue ----------------
+        warpgroup_reg_dealloc<kEndRegs>();
+        const int row = (warp & 3) * 32 + lane;
+        const int group = a.num_heads / a.num_kv_heads;
+        const int row_token = row / group, row_head = row - row_token * group;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+        uint32_t tiles_before = 0, own_phase = 0;
+        uint32_t use = 0;  // phases of the stages' uses, a bit each
+        KvItem left{0, 0, 0, 0};
+        bool ok = true;
+        while (ok && next_part()) {
+            const int tiles = part.x1 - part.x0, steps = part.wide ? 2 * tiles : tiles;
+            // tiles with keys that not every token attends, from the last: those at the diagonal, and
+            // those at the window's edge and between it and the first tokens
+            const Masked masks(a, part.diagonal[0], part.wide ? part.edge[1] : part.edge[0]);
+            int x = part.x1 - 1;
+            while (ok && x >= part.x0) {
+                const int32_t kt = part.tile(x);
+                if (!masks.any(kt)) {
+                    // over those between; a tile at or before the edge lies at or before the edge's
+                    // place in a list with a gap, too
+                    if (kt < masks.sinks) break;
+                    x = min(x - 1, masks.edge >= part.lead ? max(masks.edge - part.gap, part.lead - 1) : masks.edge);
+                    continue;
+                }
+                const uint32_t tile = tiles_before + (part.x1 - 1 - x), at = tile % S::kValueStages;
+                ok = warp_wait(&bars->v_own[at], (own_phase >> at) & 1, wc);
+                if (!ok) break;
+                own_phase ^= 1u << at;
+                const int64_t end = part.pos + part.tokens - static_cast<int64_t>(kt) * kTile;
+                if (look_through<DB>(smem_u32(sV) + at * S::kBytes, warp & 3, end) && lane == 0)
+                    *const_cast<volatile uint32_t*>(&bars->nonfinite[parts & 1]) = parts;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->v_full[at]);
+                --x;
+            }
+            tiles_before += tiles;
+            const int first = n & 1;             // the first step's stage
+            const bool join = !part.wide && steps > 1;
+            n += steps;
+            for (int sub = 0; ok && sub < (part.wide ? 2 : 1); ++sub) {
+                const int stage = first ^ sub;
+                // maxima and sums of a stage's use, and its O complete
+                const auto take = [&](int stage, float2& st) -> bool {
+                    const uint32_t phase = use >> stage & 1;
+                    use ^= 1u << stage;
+                    if (!warp_wait(&bars->stats_full[stage], phase, wc) || !warp_wait(&bars->o_full[stage], phase, wc))
+                        return false;
+                    st = bars->stats[stage][row];
+                    return true;
+                };
+                float2 st, so;
+                float f0 = 1.0f, f1 = 0.0f;  // factors of this stage's sums and of the other's
+                ok = take(stage, st) && (!join || take(stage ^ 1, so));
+                if (!ok) break;
+                if (join) {
+                    const float top = fmaxf(st.x, so.x);
+                    f0 = st.x == -INFINITY ? 0.0f : exp2_approx(st.x - top);
+                    f1 = so.x == -INFINITY ? 0.0f : exp2_approx(so.x - top);
+                    st = make_float2(top, st.y * f0 + so.y * f1);
+                }
+                tc_fence_after();
+                const int count = min(a.tile_tokens, part.tokens - sub * a.tile_tokens);
+                const bool valid = row_token < count, whole = part.whole != 0;
+                const float inv = whole ? (st.y != 0.0f ? 1.0f / st.y : 0.0f) : 1.0f;
+                const bool mend = *const_cast<volatile uint32_t*>(&bars->nonfinite[parts & 1]) == parts;
+                const int64_t out_row =
+                    (static_cast<int64_t>(part.row) + sub * a.tile_tokens + row_token) * a.num_heads +
+                    part.head * group + row_head;
+                const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (part.x0 > 0 ? 0 : 1);
+                const int slot_row = sub * kTile + row;
+                if ((warp & 3) * 32 < count * group) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld_x16(lanes + S::out_col(stage) + c, o);
+                        if (join) {
+                            uint32_t o1[16];
+                            tmem_ld_x16(lanes + S::out_col(stage ^ 1) + c, o1);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
+                        } else {
+                            tmem_ld_wait();
+                        }
+                        if (valid && mend) {
+                            // values that were made zero for the rows that do not attend them
+                            const int64_t pos = part.pos + sub * a.tile_tokens + row_token;
+                            for (int y = part.x0; y < part.x1; ++y) {
+                                const int32_t kt = part.tile(y);
+                                if (!masks.any(kt)) continue;
+                                for (int t = 0; t < kTile; ++t) {
+                                    const int64_t at = static_cast<int64_t>(kt) * kTile + t;
+                                    if (at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks)) continue;
+                                    const int64_t from = Place(a, part.b, at, true).offset(a);
+                                    if (from < 0) continue;
+                                    const uint16_t* v = a.cache_layer + a.kv_stride + from + part.head * D + c;
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) {
+                                        const uint32_t bits = __ldg(v + k);
+                                        if ((bits & 0x7f80u) == 0x7f80u)
+                                            o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(bits << 16));
+                                    }
+                                }
+                            }
+                        }
+                        if (valid && whole) {
+                            uint32_t p[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                p[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                            uint16_t* to = a.out + out_row * D + c;
+                            if (sectors) {
+                                st_v8(to, p);
+                            } else {
+                                st_v4(to, make_uint4(p[0], p[1], p[2], p[3]));
+                                st_v4(to + 8, make_uint4(p[4], p[5], p[6], p[7]));
+                            }
+                        } else if (valid) {
+                            float* to = reinterpret_cast<float*>(a.workspace) + (slot * ws.rows + slot_row) * D + c;
+                            st_v8(to, o);
+                            st_v8(to + 8, o + 8);
+                        }
+                        __syncwarp();
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars->o_empty[stage]);
+                    if (join) mbar_arrive(&bars->o_empty[stage ^ 1]);
+                }
+                if (valid && whole && a.lse != nullptr)
+                    a.lse[out_row] = st.y != 0.0f ? st.x * kLn2 + logf(st.y) : -INFINITY;
+                if (valid && !whole)
+                    reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + slot_row] = st;
+            }
+            if (part.left > 0) left = KvItem{part.row, part.head * group, part.tokens, part.left};
+        }
+        if (warp == kEndWarp && lane == 0) {
+            if (!ok) left.tokens = 0;
+            reinterpret_cast<KvItem*>(a.workspace + ws.items)[blockIdx.x] = left;
         }
     }
 
@@ -1009,8 +1122,7 @@ __global__ void __launch_bounds__(kJoinThreads)
             const int p = lane * kEach + k;
             n[k] = 0;
             if (p < ctas) {
-                const KvItem x = left[2 * p], y = left[2 * p + 1];
-                const KvItem it = x.tokens > 0 ? x : y;
+                const KvItem it = left[p];
                 if (warp == 0) items[p] = it;
                 if ((it.parts > kFewParts) == (warp == 1)) n[k] = it.tokens * group;
             }

@@ -69,7 +69,7 @@ struct KvWorkspace {
     int32_t rows;       // query rows (token, head) that a slot holds
     size_t stats;       // float2 [2 * kKvMaxCtas, rows]: maximum (base 2) and sum, behind
                         // fp32 [2 * kKvMaxCtas, rows, D], unnormalised
-    size_t items;       // KvItem [2 * kKvMaxCtas], a CTA's two stages'
+    size_t items;       // KvItem [kKvMaxCtas]
     size_t bytes;
 };
 
@@ -87,7 +87,7 @@ inline KvWorkspace kv_workspace(int32_t total_rows, int32_t num_heads, int32_t n
     const size_t slots = 2 * kKvMaxCtas;
     w.stats = up(slots * w.rows * head_size * sizeof(float));
     w.items = w.stats + up(slots * w.rows * 2 * sizeof(float));
-    w.bytes = w.items + up(2 * kKvMaxCtas * sizeof(KvItem));
+    w.bytes = w.items + up(kKvMaxCtas * sizeof(KvItem));
     return w;
 }
 
