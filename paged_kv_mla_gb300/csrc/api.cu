@@ -1368,6 +1368,8 @@ pkm_status kv_attention(const void* q, int64_t q_row_stride, int64_t q_head_stri
     a.sinks = sink_tokens;
     a.sink_tiles = sink_tokens / 128 + (sink_tokens % 128 != 0 ? 1 : 0);
     a.tile_tokens = pkm::kv_tile_tokens(num_heads, num_kv_heads);
+    // (page sizes that are powers of two divide 2^64)
+    if (kv_cache->page_size > 1) a.page_inverse = UINT64_MAX / kv_cache->page_size + 1;
     a.cache_layer = static_cast<const uint16_t*>(kv_cache->data) +
                     static_cast<int64_t>(layer_idx) * kv_cache->layer_stride;
     a.page_stride = kv_cache->page_stride;

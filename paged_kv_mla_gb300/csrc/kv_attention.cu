@@ -46,18 +46,22 @@ constexpr int kMaxStages = 7;       // tiles of keys, or of values, in shared me
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWeightCol = 384;    // TMEM column of the weights, 64 a stage
 constexpr int kItemCost = 1;        // an item's start and end, in tiles
+constexpr int kUncut = 6;           // items of fewer units on average are not cut, if there are few
 constexpr uint64_t kDrainNs = 1000000;  // a role that gave up leaves its loads time to land
 constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
-// a / b; the 64-bit division is a long routine, and the operands are hardly ever that large.
+// a / b; the 64-bit division is a long routine, which is there once, and the operands are hardly
+// ever that large.
+static __device__ __noinline__ int64_t long_quotient(int64_t a, int64_t b) { return a / b; }
+
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
+    return long_quotient(a, b);
 }
 
 // Sum of floor((a * i + b) / m) over i < n, for a, b >= 0: Euclid's steps on a and m.
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+static __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
     int64_t sum = 0;
     while (n > 0) {
         if (a >= m) {
@@ -95,7 +99,7 @@ struct Request {
         first = lo;
         n = hi > lo ? static_cast<int32_t>(hi - lo) : 0;
         len = __ldg(a.cache_lengths + b);
-        const bool held = len + n <= static_cast<int64_t>(a.max_pages) * a.page_size;
+        const bool held = n == 0 || len + n <= static_cast<int64_t>(a.max_pages) * a.page_size;
         if (!held) n = 0;
         items = (n + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
         return held;
@@ -166,14 +170,16 @@ struct Bars {
     Part part[kParts];
     union {
         float2 stats[2][kTile];            // of the stages
-        int64_t scratch[kThreads / 32];    // of the plan
+        int64_t scratch[2 * kThreads / 32];  // of the plan
     };
     int64_t units;               // units of all items
     int64_t first_unit;          // this CTA's share begins here
     int64_t share;               // and has so many units
-    int64_t into;                // units of its first request before it
+    int64_t into, each;          // units of its first request before it, and of one of its heads
+    Request first;
     int32_t request, head, item, unit;  // its first unit
-    uint32_t nonfinite[2];       // parts, by number, that had infinities or NaN looked through
+    int32_t ctas;                // that have a share
+    uint32_t nonfinite[4];       // parts, by number, that had infinities or NaN looked through
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -218,7 +224,7 @@ struct Walk {
         at = bars->unit;
         tokens = x0 = x1 = 0;
         if (left > 0) {
-            r.load(a, b);
+            r = bars->first;
             set_item(a);
         }
     }
@@ -263,58 +269,73 @@ struct Walk {
 };
 
 // Counts the units of all requests and cuts out the CTA's share; every thread sums a run of
-// requests, and a warp finds the item within the request.
+// requests, and a warp finds the item within the request.  (Loops that are not unrolled and calls:
+// the code runs once, and is fetched for that.)
 __device__ __forceinline__ void plan(const KvAttentionArgs& a, Bars* bars) {
     const int64_t per = (static_cast<int64_t>(a.batch) + kThreads - 1) / kThreads, all = a.batch;
     const int b0 = static_cast<int>(min(threadIdx.x * per, all));
     const int b1 = static_cast<int>(min(b0 + per, all));
-    int64_t sum = 0, last = 0;
-    Request r;
-    for (int b = b0; b < b1; ++b) {
-        if (!r.load(a, b)) report(a.status, PKM_ERR_OUT_OF_RANGE);
-        last = r.head_units(a) * a.num_kv_heads;
-        sum += last;
-    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl = sum;
-#pragma unroll
-    for (int sh = 1; sh < 32; sh <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, incl, sh);
-        if (lane >= sh) incl += o;
-    }
-    if (lane == 31) bars->scratch[warp] = incl;
+    int64_t sum = 0, items = 0, at = 0, u = -1, ctas = 0, total = 0;
     if (threadIdx.x == 0) bars->share = 0;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += bars->scratch[w];
-        total += bars->scratch[w];
-    }
-    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
-    const int64_t u = blockIdx.x < ctas ? quotient(total * blockIdx.x, ctas) : -1;
-    if (threadIdx.x == 0) bars->units = total;
-    int64_t at = before + incl - sum;
-    if (at <= u && u < at + sum)
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            if (per > 1) {
-                r.load(a, b);
-                last = r.head_units(a) * a.num_kv_heads;
-            }
-            if (u < at + last) {
+            Request r;
+            if (!r.load(a, b) && pass == 0) report(a.status, PKM_ERR_OUT_OF_RANGE);
+            const int64_t each = r.head_units(a), units = each * a.num_kv_heads;
+            if (pass == 0) {
+                sum += units;
+                items += static_cast<int64_t>(r.items) * a.num_kv_heads;
+            } else if (u < at + units) {
                 bars->first_unit = u;
                 bars->share = quotient(total * (blockIdx.x + 1), ctas) - u;
                 bars->request = b;
+                bars->first = r;
+                bars->each = each;
                 bars->into = u - at;
                 break;
             }
-            at += last;
+            at += units;
         }
+        if (pass == 1) break;
+        int64_t incl = sum;
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, incl, sh);
+            if (lane >= sh) incl += o;
+            items += __shfl_xor_sync(0xffffffffu, items, sh);
+        }
+        if (lane == 31) {
+            bars->scratch[warp] = incl;
+            bars->scratch[kThreads / 32 + warp] = items;
+        }
+        __syncthreads();
+        int64_t before = 0;
+        items = 0;
+#pragma unroll 1
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += bars->scratch[w];
+            total += bars->scratch[w];
+            items += bars->scratch[kThreads / 32 + w];
+        }
+        // Few and short items are not cut: their parts would be joined longer than they take.
+        ctas = min(static_cast<int64_t>(gridDim.x), total < items * kUncut ? items : total);
+        if (threadIdx.x == 0) {
+            bars->units = total;
+            bars->ctas = static_cast<int32_t>(ctas);
+        }
+        if (blockIdx.x < ctas) u = quotient(total * blockIdx.x, ctas);
+        at = before + incl - sum;
+        if (u < at || u >= at + sum) break;
+    }
     __syncthreads();
     if (warp != 0 || bars->share == 0) return;
-    r.load(a, bars->request);
-    const int64_t each = r.head_units(a);
-    const int64_t head = quotient(bars->into, each), into = bars->into - head * each;
+    const Request r = bars->first;
+    const int64_t head = quotient(bars->into, bars->each), into = bars->into - head * bars->each;
     int64_t lo = 0, n = r.items, passed = 0;  // the last item with no more units before it
+#pragma unroll 1
     while (n > 1) {
         const int64_t step = (n + 31) / 32, j = lane * step;
         const int64_t units = j < n ? r.units_before(a, lo + j) : INT64_MAX;
@@ -338,7 +359,8 @@ struct Place {
     __device__ __forceinline__ Place(const KvAttentionArgs& a, int b, int64_t pos, bool read)
         : page(-1), slot(0) {
         if (!read) return;
-        const int64_t lp = quotient(pos, a.page_size);
+        // pos / page_size for positions below 2^33: off by less than 2^-31 before rounding down
+        const int64_t lp = a.page_inverse == 0 ? pos : __umul64hi(pos, a.page_inverse);
         slot = static_cast<int32_t>(pos - lp * a.page_size);
         const uint32_t id = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
         if (id < static_cast<uint32_t>(a.num_pages)) page = static_cast<int32_t>(id);
@@ -473,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->stats_full[i], 4);
             mbar_init(&bars->o_full[i], 1);
             mbar_init(&bars->o_empty[i], 4);
-            bars->nonfinite[i] = 0;
         }
+        for (int i = 0; i < 4; ++i) bars->nonfinite[i] = 0;
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&bars->part_full[i], 1);
             mbar_init(&bars->part_empty[i], 15);  // all warps but the loader
@@ -537,8 +559,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t scores = lanes + S::score_col(stage), weights = lanes + kWeightCol + stage * 64;
         const uint32_t out = lanes + S::out_col(stage);
         uint32_t uses = 0;
+        // A wait that runs out is looked at once a part; what is computed until then is not used.
         bool ok = true;
-        while (ok && next_part()) {
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = mbar_wait_inl(bar, parity, wc) && ok;
+            __syncwarp();
+        };
+        while (__all_sync(0xffffffffu, ok) && next_part()) {
             const int tiles = part.x1 - part.x0, steps = part.wide ? 2 * tiles : tiles;
             const int mine = stage ^ (n & 1);       // the stage's first step
             const int sub = part.wide ? mine : 0;   // its tile of queries
@@ -549,17 +576,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.0f;
             for (int x = mine; x < steps; x += 2) {
                 const uint32_t turn = (n + x) >> 1;  // of the stage
-                if (!warp_wait(&bars->s_full[stage], turn & 1, wc)) {
-                    ok = false;
-                    break;
-                }
+                wait(&bars->s_full[stage], turn & 1);
                 tc_fence_after();
                 if (!busy) {
                     if (lane == 0) mbar_arrive(&bars->s_empty[stage]);
-                    if (turn > 0 && !warp_wait(&bars->p_empty[stage], (turn - 1) & 1, wc)) {
-                        ok = false;
-                        break;
-                    }
+                    if (turn > 0) wait(&bars->p_empty[stage], (turn - 1) & 1);
                     if (lane == 0) mbar_arrive(&bars->p_full[stage]);
                     continue;
                 }
@@ -608,10 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = m_new;
                 const float ref = m == -INFINITY ? 0.0f : m;
                 // the stage's step before is done: O holds still, and its weights' place is free
-                if (turn > 0 && !warp_wait(&bars->p_empty[stage], (turn - 1) & 1, wc)) {
-                    ok = false;
-                    break;
-                }
+                if (turn > 0) wait(&bars->p_empty[stage], (turn - 1) & 1);
                 tc_fence_after();
                 if (x > mine && __any_sync(0xffffffffu, back != 1.0f)) {
 #pragma unroll 1
@@ -656,8 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&bars->p_full[stage]);
             }
             n += steps;
-            if (!ok || mine >= steps) continue;
-            if (uses > 0 && !warp_wait(&bars->o_empty[stage], (uses - 1) & 1, wc)) break;  // read with its O
+            if (mine >= steps) continue;
+            if (uses > 0) wait(&bars->o_empty[stage], (uses - 1) & 1);  // read with its O
             bars->stats[stage][row] = make_float2(m, l);
             ++uses;
             __syncwarp();
@@ -773,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- schedule, queries, keys, values ----------------
         Walk w(a, bars);
         const int group = a.num_heads / a.num_kv_heads;
-        const int64_t sharing = min(static_cast<int64_t>(gridDim.x), bars->units);
+        const int64_t sharing = bars->ctas;
         RingPos kpos, vpos;
         uint32_t queries = 0;
         bool ok = true, more = true;
@@ -952,18 +970,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t use = 0;  // phases of the stages' uses, a bit each
         KvItem left{0, 0, 0, 0};
         bool ok = true;
-        while (ok && next_part()) {
-            const int tiles = part.x1 - part.x0, steps = part.wide ? 2 * tiles : tiles;
-            // tiles with keys that not every token attends, from the last: those at the diagonal, and
-            // those at the window's edge and between it and the first tokens
+        // Looks through the values of a part's tiles with keys that not every token attends, from the
+        // last: those at the diagonal, or behind them those at the window's edge and between it and
+        // the first tokens.
+        const auto look = [&](const Part& part, uint32_t number, uint32_t tiles_before, int x, bool diagonal) -> int {
             const Masked masks(a, part.diagonal[0], part.wide ? part.edge[1] : part.edge[0]);
-            int x = part.x1 - 1;
-            while (ok && x >= part.x0) {
+#pragma unroll 1
+            while (x >= part.x0) {
                 const int32_t kt = part.tile(x);
+                if (diagonal ? kt < masks.diagonal : kt < masks.sinks) break;
                 if (!masks.any(kt)) {
-                    // over those between; a tile at or before the edge lies at or before the edge's
-                    // place in a list with a gap, too
-                    if (kt < masks.sinks) break;
+                    // over those between; the edge's place in a list with a gap
                     x = min(x - 1, masks.edge >= part.lead ? max(masks.edge - part.gap, part.lead - 1) : masks.edge);
                     continue;
                 }
@@ -973,17 +990,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 own_phase ^= 1u << at;
                 const int64_t end = part.pos + part.tokens - static_cast<int64_t>(kt) * kTile;
                 if (look_through<DB>(smem_u32(sV) + at * S::kBytes, warp & 3, end) && lane == 0)
-                    *const_cast<volatile uint32_t*>(&bars->nonfinite[parts & 1]) = parts;
+                    *const_cast<volatile uint32_t*>(&bars->nonfinite[number & 3]) = number;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->v_full[at]);
                 --x;
             }
+            return x;
+        };
+        // The next part's values at its diagonal are looked through before this part's epilogue, which
+        // they need not wait for.
+        bool more = next_part();
+        Part ahead = part;
+        int x_ahead = more ? look(ahead, parts, 0, ahead.x1 - 1, true) : 0;
+        while (ok && more) {
+            const uint32_t number = parts;
+            const Part now = ahead;
+            const int tiles = now.x1 - now.x0, steps = now.wide ? 2 * tiles : tiles;
+            look(now, number, tiles_before, x_ahead, false);
             tiles_before += tiles;
+            if (!ok) break;
+            more = next_part();
+            ahead = part;
+            if (more) x_ahead = look(ahead, parts, tiles_before, ahead.x1 - 1, true);
+            if (!ok) break;
             const int first = n & 1;             // the first step's stage
-            const bool join = !part.wide && steps > 1;
+            const bool join = !now.wide && steps > 1;
             n += steps;
-            for (int sub = 0; ok && sub < (part.wide ? 2 : 1); ++sub) {
+            for (int sub = 0; ok && sub < (now.wide ? 2 : 1); ++sub) {
                 const int stage = first ^ sub;
                 // maxima and sums of a stage's use, and its O complete
                 const auto take = [&](int stage, float2& st) -> bool {
@@ -1005,14 +1039,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     st = make_float2(top, st.y * f0 + so.y * f1);
                 }
                 tc_fence_after();
-                const int count = min(a.tile_tokens, part.tokens - sub * a.tile_tokens);
-                const bool valid = row_token < count, whole = part.whole != 0;
+                const int count = min(a.tile_tokens, now.tokens - sub * a.tile_tokens);
+                const bool valid = row_token < count, whole = now.whole != 0;
                 const float inv = whole ? (st.y != 0.0f ? 1.0f / st.y : 0.0f) : 1.0f;
-                const bool mend = *const_cast<volatile uint32_t*>(&bars->nonfinite[parts & 1]) == parts;
+                const bool mend = *const_cast<volatile uint32_t*>(&bars->nonfinite[number & 3]) == number;
                 const int64_t out_row =
-                    (static_cast<int64_t>(part.row) + sub * a.tile_tokens + row_token) * a.num_heads +
-                    part.head * group + row_head;
-                const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (part.x0 > 0 ? 0 : 1);
+                    (static_cast<int64_t>(now.row) + sub * a.tile_tokens + row_token) * a.num_heads +
+                    now.head * group + row_head;
+                const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (now.x0 > 0 ? 0 : 1);
                 const int slot_row = sub * kTile + row;
                 if ((warp & 3) * 32 < count * group) {
 #pragma unroll 1
@@ -1031,16 +1065,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (valid && mend) {
                             // values that were made zero for the rows that do not attend them
-                            const int64_t pos = part.pos + sub * a.tile_tokens + row_token;
-                            for (int y = part.x0; y < part.x1; ++y) {
-                                const int32_t kt = part.tile(y);
+                            const int64_t pos = now.pos + sub * a.tile_tokens + row_token;
+                            const Masked masks(a, now.diagonal[0], now.wide ? now.edge[1] : now.edge[0]);
+                            for (int y = now.x0; y < now.x1; ++y) {
+                                const int32_t kt = now.tile(y);
                                 if (!masks.any(kt)) continue;
                                 for (int t = 0; t < kTile; ++t) {
                                     const int64_t at = static_cast<int64_t>(kt) * kTile + t;
                                     if (at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks)) continue;
-                                    const int64_t from = Place(a, part.b, at, true).offset(a);
+                                    const int64_t from = Place(a, now.b, at, true).offset(a);
                                     if (from < 0) continue;
-                                    const uint16_t* v = a.cache_layer + a.kv_stride + from + part.head * D + c;
+                                    const uint16_t* v = a.cache_layer + a.kv_stride + from + now.head * D + c;
 #pragma unroll
                                     for (int k = 0; k < 16; ++k) {
                                         const uint32_t bits = __ldg(v + k);
@@ -1081,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (valid && !whole)
                     reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + slot_row] = st;
             }
-            if (part.left > 0) left = KvItem{part.row, part.head * group, part.tokens, part.left};
+            if (now.left > 0) left = KvItem{now.row, now.head * group, now.tokens, now.left};
         }
         if (warp == kEndWarp && lane == 0) {
             if (!ok) left.tokens = 0;

@@ -43,6 +43,7 @@ struct KvAttentionArgs {
     int32_t sinks;                 // first positions that it attends besides
     int32_t sink_tiles;            // 128-key tiles that hold them
     int32_t tile_tokens;           // tokens of a 128-row tile of queries
+    uint64_t page_inverse;         // floor(2^64 / page_size) + 1, or 0 for pages of one slot
     const uint16_t* cache_layer;   // cache data + layer_idx * layer_stride
     int64_t page_stride, slot_stride, kv_stride;
     int32_t num_pages, page_size, max_pages;
