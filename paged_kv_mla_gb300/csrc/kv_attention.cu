@@ -394,17 +394,21 @@ __device__ __forceinline__ bool look_through(uint32_t tile, int quarter, int64_t
     // 32 lanes take 512 bytes, four rows of a block; the place in the block does not matter
 #pragma unroll 1
     for (int i = quarter * DB * 8; i < (quarter + 1) * DB * 8; i += 8) {
+        const uint32_t from = tile + i * 512 + lane * 16;
         uint4 v[8];
+        bool bad = false;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = ld_shared_v4(tile + (i + k) * 512 + lane * 16);
+        for (int k = 0; k < 8; ++k) v[k] = ld_shared_v4(from + k * 512);
 #pragma unroll
+        for (int k = 0; k < 8; ++k) bad = bad || any_nonfinite(v[k]);
+        if (!bad) continue;
+#pragma unroll 1
         for (int k = 0; k < 8; ++k) {
-            if (!any_nonfinite(v[k])) continue;
+            const uint4 w = ld_shared_v4(from + k * 512);
+            if (!any_nonfinite(w)) continue;
             const int at = (i + k) * 4 + (lane >> 3);  // row among all blocks' rows
-            const int row = at / (8 * DB) * 8 + (at & 7);
-            found = found || row < end;
-            st_shared_v4(tile + (i + k) * 512 + lane * 16, finite2(v[k].x), finite2(v[k].y),
-                         finite2(v[k].z), finite2(v[k].w));
+            found = found || at / (8 * DB) * 8 + (at & 7) < end;
+            st_shared_v4(from + k * 512, finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
         }
     }
     return __any_sync(0xffffffffu, found);
@@ -554,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = (warp & 3) * 32 + lane;
         const int group = a.num_heads / a.num_kv_heads;
         const int row_token = row / group;
-        const float scale2 = a.scale * kLog2e;
+        const float scale2 = a.scale * kLog2e, mul = scale2 > 0.0f ? scale2 : 1.0f;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t scores = lanes + S::score_col(stage), weights = lanes + kWeightCol + stage * 64;
         const uint32_t out = lanes + S::out_col(stage);
@@ -584,6 +588,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&bars->p_full[stage]);
                     continue;
                 }
+                // Masks are put into the scores where they lie, and so is a scale that is not positive,
+                // which the maximum would have to know: a short loop, since long straight code that runs
+                // once in a while is fetched for hundreds of cycles.
+                const int32_t kt = part.tile(part.x1 - 1 - (part.wide ? x >> 1 : x));
+                if (masks.any(kt) || !(scale2 > 0.0f)) {
+                    const Attended may(a, pos, kt);
+                    const float factor = scale2 > 0.0f ? 1.0f : scale2;
+#pragma unroll 1
+                    for (int c = 0; c < kTile; c += 16) {
+                        const uint32_t bits = may.bits(c) & 0xffffu;
+                        if (__all_sync(0xffffffffu, bits == 0xffffu) && factor == 1.0f) continue;
+                        uint32_t v[16];
+                        tmem_ld_x16(scores + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            v[k] = __float_as_uint((bits >> k) & 1u ? __uint_as_float(v[k]) * factor : -INFINITY);
+                        tmem_st_x16(scores + c, v);
+                    }
+                    tmem_st_wait();
+                }
                 uint32_t s[4][32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld_x32(scores + k * 32, s[k]);
@@ -594,24 +619,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_empty[stage]);
                 const auto f = [&](int c) -> float { return __uint_as_float(s[c >> 5][c & 31]); };
-                float mul = scale2;
-                if (!(scale2 > 0.0f)) {  // scaled before the maximum, which then need not know the sign
-                    mul = 1.0f;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c >> 5][c & 31] = __float_as_uint(f(c) * scale2);
-                }
-                const int32_t kt = part.tile(part.x1 - 1 - (part.wide ? x >> 1 : x));
-                if (masks.any(kt)) {
-                    const Attended may(a, pos, kt);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t bits = may.bits(k * 32);
-                        if (__all_sync(0xffffffffu, bits == ~0u)) continue;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!((bits >> c) & 1u)) s[k][c] = __float_as_uint(-INFINITY);
-                    }
-                }
                 float t0 = f(0), t1 = f(1), t2 = f(2), t3 = f(3);
 #pragma unroll
                 for (int c = 4; c < 124; c += 8) {
@@ -970,50 +977,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t use = 0;  // phases of the stages' uses, a bit each
         KvItem left{0, 0, 0, 0};
         bool ok = true;
-        // Looks through the values of a part's tiles with keys that not every token attends, from the
-        // last: those at the diagonal, or behind them those at the window's edge and between it and
-        // the first tokens.
-        const auto look = [&](const Part& part, uint32_t number, uint32_t tiles_before, int x, bool diagonal) -> int {
-            const Masked masks(a, part.diagonal[0], part.wide ? part.edge[1] : part.edge[0]);
+        Part now;
+        uint32_t number = 0;  // of the part `now`; 0 before the first
+        int x = 0;
+        while (true) {
+            // Values of tiles with keys that not every token attends are looked through, from a part's
+            // last tile: those at the diagonal, then those at the window's edge and between it and the
+            // first tokens.  The next part's diagonal comes before this part's epilogue, for which it
+            // need not wait.
+            bool more = true;
+            const uint32_t following = number + 1;
+            Part p = now;
 #pragma unroll 1
-            while (x >= part.x0) {
-                const int32_t kt = part.tile(x);
-                if (diagonal ? kt < masks.diagonal : kt < masks.sinks) break;
-                if (!masks.any(kt)) {
-                    // over those between; the edge's place in a list with a gap
-                    x = min(x - 1, masks.edge >= part.lead ? max(masks.edge - part.gap, part.lead - 1) : masks.edge);
-                    continue;
+            for (int turn = number > 0 ? 0 : 1; ok && turn < 2; ++turn) {
+                if (turn == 1) {
+                    if (number > 0) tiles_before += now.x1 - now.x0;
+                    more = next_part();
+                    if (!more) break;
+                    p = part;
+                    x = p.x1 - 1;
                 }
-                const uint32_t tile = tiles_before + (part.x1 - 1 - x), at = tile % S::kValueStages;
-                ok = warp_wait(&bars->v_own[at], (own_phase >> at) & 1, wc);
-                if (!ok) break;
-                own_phase ^= 1u << at;
-                const int64_t end = part.pos + part.tokens - static_cast<int64_t>(kt) * kTile;
-                if (look_through<DB>(smem_u32(sV) + at * S::kBytes, warp & 3, end) && lane == 0)
-                    *const_cast<volatile uint32_t*>(&bars->nonfinite[number & 3]) = number;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->v_full[at]);
-                --x;
+                const Masked masks(a, p.diagonal[0], p.wide ? p.edge[1] : p.edge[0]);
+#pragma unroll 1
+                while (x >= p.x0) {
+                    const int32_t kt = p.tile(x);
+                    if (kt < (turn == 1 ? masks.diagonal : masks.sinks)) break;
+                    if (!masks.any(kt)) {
+                        // over those between; the edge's place in a list with a gap
+                        x = min(x - 1, masks.edge >= p.lead ? max(masks.edge - p.gap, p.lead - 1) : masks.edge);
+                        continue;
+                    }
+                    const uint32_t tile = tiles_before + (p.x1 - 1 - x), at = tile % S::kValueStages;
+                    ok = warp_wait(&bars->v_own[at], (own_phase >> at) & 1, wc);
+                    if (!ok) break;
+                    own_phase ^= 1u << at;
+                    const int64_t end = p.pos + p.tokens - static_cast<int64_t>(kt) * kTile;
+                    const uint32_t of = turn == 1 ? following : number;
+                    if (look_through<DB>(smem_u32(sV) + at * S::kBytes, warp & 3, end) && lane == 0)
+                        *const_cast<volatile uint32_t*>(&bars->nonfinite[of & 3]) = of;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->v_full[at]);
+                    --x;
+                }
             }
-            return x;
-        };
-        // The next part's values at its diagonal are looked through before this part's epilogue, which
-        // they need not wait for.
-        bool more = next_part();
-        Part ahead = part;
-        int x_ahead = more ? look(ahead, parts, 0, ahead.x1 - 1, true) : 0;
-        while (ok && more) {
-            const uint32_t number = parts;
-            const Part now = ahead;
+            if (!ok || (number == 0 && !more)) break;
+            if (number == 0) {
+                now = p;
+                number = 1;
+                continue;
+            }
             const int tiles = now.x1 - now.x0, steps = now.wide ? 2 * tiles : tiles;
-            look(now, number, tiles_before, x_ahead, false);
-            tiles_before += tiles;
-            if (!ok) break;
-            more = next_part();
-            ahead = part;
-            if (more) x_ahead = look(ahead, parts, tiles_before, ahead.x1 - 1, true);
-            if (!ok) break;
             const int first = n & 1;             // the first step's stage
             const bool join = !now.wide && steps > 1;
             n += steps;
@@ -1041,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int count = min(a.tile_tokens, now.tokens - sub * a.tile_tokens);
                 const bool valid = row_token < count, whole = now.whole != 0;
-                const float inv = whole ? (st.y != 0.0f ? 1.0f / st.y : 0.0f) : 1.0f;
+                const float inv = whole ? (st.y != 0.0f ? rcp_approx(st.y) : 0.0f) : 1.0f;
                 const bool mend = *const_cast<volatile uint32_t*>(&bars->nonfinite[number & 3]) == number;
                 const int64_t out_row =
                     (static_cast<int64_t>(now.row) + sub * a.tile_tokens + row_token) * a.num_heads +
@@ -1063,39 +1077,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             tmem_ld_wait();
                         }
-                        if (valid && mend) {
-                            // values that were made zero for the rows that do not attend them
-                            const int64_t pos = now.pos + sub * a.tile_tokens + row_token;
-                            const Masked masks(a, now.diagonal[0], now.wide ? now.edge[1] : now.edge[0]);
-                            for (int y = now.x0; y < now.x1; ++y) {
-                                const int32_t kt = now.tile(y);
-                                if (!masks.any(kt)) continue;
-                                for (int t = 0; t < kTile; ++t) {
-                                    const int64_t at = static_cast<int64_t>(kt) * kTile + t;
-                                    if (at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks)) continue;
-                                    const int64_t from = Place(a, now.b, at, true).offset(a);
-                                    if (from < 0) continue;
-                                    const uint16_t* v = a.cache_layer + a.kv_stride + from + now.head * D + c;
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) {
-                                        const uint32_t bits = __ldg(v + k);
-                                        if ((bits & 0x7f80u) == 0x7f80u)
-                                            o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(bits << 16));
-                                    }
-                                }
-                            }
-                        }
                         if (valid && whole) {
-                            uint32_t p[8];
+                            uint32_t h[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                p[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                                h[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
                             uint16_t* to = a.out + out_row * D + c;
                             if (sectors) {
-                                st_v8(to, p);
+                                st_v8(to, h);
                             } else {
-                                st_v4(to, make_uint4(p[0], p[1], p[2], p[3]));
-                                st_v4(to + 8, make_uint4(p[4], p[5], p[6], p[7]));
+                                st_v4(to, make_uint4(h[0], h[1], h[2], h[3]));
+                                st_v4(to + 8, make_uint4(h[4], h[5], h[6], h[7]));
                             }
                         } else if (valid) {
                             float* to = reinterpret_cast<float*>(a.workspace) + (slot * ws.rows + slot_row) * D + c;
@@ -1111,12 +1103,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bars->o_empty[stage]);
                     if (join) mbar_arrive(&bars->o_empty[stage ^ 1]);
                 }
+                if (valid && mend) {
+                    // infinities and NaN that were made zero for the rows that do not attend them
+                    const Masked masks(a, now.diagonal[0], now.wide ? now.edge[1] : now.edge[0]);
+                    const int64_t pos = now.pos + sub * a.tile_tokens + row_token;
+#pragma unroll 1
+                    for (int64_t i = static_cast<int64_t>(tiles) * kTile * (D / 8) - 1; i >= 0; --i) {
+                        const int c = static_cast<int>(i % (D / 8)) * 8, t = static_cast<int>(i / (D / 8) % kTile);
+                        const int32_t kt = now.tile(now.x0 + static_cast<int32_t>(i / (D / 8) / kTile));
+                        const int64_t at = static_cast<int64_t>(kt) * kTile + t;
+                        if (!masks.any(kt) || at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks))
+                            continue;
+                        const int64_t from = Place(a, now.b, at, true).offset(a);
+                        if (from < 0) continue;
+                        const uint16_t* v = a.cache_layer + a.kv_stride + from + now.head * D + c;
+                        if (!any_nonfinite(ld_nc_v4(v))) continue;
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t bits = v[k];
+                            if ((bits & 0x7f80u) != 0x7f80u) continue;
+                            const float x = __uint_as_float(bits << 16);
+                            if (whole) {
+                                uint16_t* o = a.out + out_row * D + c + k;
+                                *o = static_cast<uint16_t>(
+                                    pack_bf16x2(__uint_as_float(static_cast<uint32_t>(*o) << 16) + x, 0.0f));
+                            } else {
+                                reinterpret_cast<float*>(a.workspace)[(slot * ws.rows + slot_row) * D + c + k] += x;
+                            }
+                        }
+                    }
+                }
                 if (valid && whole && a.lse != nullptr)
-                    a.lse[out_row] = st.y != 0.0f ? st.x * kLn2 + logf(st.y) : -INFINITY;
+                    a.lse[out_row] = st.y != 0.0f ? (st.x + __log2f(st.y)) * kLn2 : -INFINITY;
                 if (valid && !whole)
                     reinterpret_cast<float2*>(a.workspace + ws.stats)[slot * ws.rows + slot_row] = st;
             }
             if (now.left > 0) left = KvItem{now.row, now.head * group, now.tokens, now.left};
+            if (!ok || !more) break;
+            now = p;
+            number = following;
         }
         if (warp == kEndWarp && lane == 0) {
             if (!ok) left.tokens = 0;
