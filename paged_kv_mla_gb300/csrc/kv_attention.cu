@@ -45,8 +45,9 @@ constexpr int kTile = 128;          // keys of a tile, rows of a tile of queries
 constexpr int kMaxStages = 7;       // tiles of keys, or of values, in shared memory
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWeightCol = 384;    // TMEM column of the weights, 64 a stage
-constexpr int kItemCost = 1;        // an item's start and end, in tiles
-constexpr int kUncut = 6;           // items of fewer units on average are not cut, if there are few
+// An item's start and end, in tiles (with 1 prompts of many lengths take 4 % longer and small ragged
+// chunks 10 %, with 3 both 1 to 2 %).
+constexpr int kItemCost = 2;
 constexpr uint64_t kDrainNs = 1000000;  // a role that gave up leaves its loads time to land
 constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
@@ -120,6 +121,7 @@ struct Request {
     }
     // Units of the items before j < items; an item has kItemCost besides its tiles.
     __device__ __forceinline__ int64_t units_before(const KvAttentionArgs& a, int64_t j) const {
+        if (j == 0) return 0;
         const int64_t t = 2 * a.tile_tokens;
         int64_t sum = kItemCost * j + floor_sum(j, kTile, t, len + t + kTile - 1);
         if (a.window > 0) {
@@ -170,7 +172,7 @@ struct Bars {
     Part part[kParts];
     union {
         float2 stats[2][kTile];            // of the stages
-        int64_t scratch[2 * kThreads / 32];  // of the plan
+        int64_t scratch[kThreads / 32];  // of the plan
     };
     int64_t units;               // units of all items
     int64_t first_unit;          // this CTA's share begins here
@@ -276,7 +278,7 @@ __device__ __forceinline__ void plan(const KvAttentionArgs& a, Bars* bars) {
     const int b0 = static_cast<int>(min(threadIdx.x * per, all));
     const int b1 = static_cast<int>(min(b0 + per, all));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t sum = 0, items = 0, at = 0, u = -1, ctas = 0, total = 0;
+    int64_t sum = 0, at = 0, u = -1, ctas = 0, total = 0;
     if (threadIdx.x == 0) bars->share = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -287,7 +289,6 @@ __device__ __forceinline__ void plan(const KvAttentionArgs& a, Bars* bars) {
             const int64_t each = r.head_units(a), units = each * a.num_kv_heads;
             if (pass == 0) {
                 sum += units;
-                items += static_cast<int64_t>(r.items) * a.num_kv_heads;
             } else if (u < at + units) {
                 bars->first_unit = u;
                 bars->share = quotient(total * (blockIdx.x + 1), ctas) - u;
@@ -305,23 +306,16 @@ __device__ __forceinline__ void plan(const KvAttentionArgs& a, Bars* bars) {
         for (int sh = 1; sh < 32; sh <<= 1) {
             const int64_t o = __shfl_up_sync(0xffffffffu, incl, sh);
             if (lane >= sh) incl += o;
-            items += __shfl_xor_sync(0xffffffffu, items, sh);
         }
-        if (lane == 31) {
-            bars->scratch[warp] = incl;
-            bars->scratch[kThreads / 32 + warp] = items;
-        }
+        if (lane == 31) bars->scratch[warp] = incl;
         __syncthreads();
         int64_t before = 0;
-        items = 0;
 #pragma unroll 1
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += bars->scratch[w];
             total += bars->scratch[w];
-            items += bars->scratch[kThreads / 32 + w];
         }
-        // Few and short items are not cut: their parts would be joined longer than they take.
-        ctas = min(static_cast<int64_t>(gridDim.x), total < items * kUncut ? items : total);
+        ctas = min(static_cast<int64_t>(gridDim.x), total);
         if (threadIdx.x == 0) {
             bars->units = total;
             bars->ctas = static_cast<int32_t>(ctas);
@@ -350,6 +344,16 @@ __device__ __forceinline__ void plan(const KvAttentionArgs& a, Bars* bars) {
         bars->item = static_cast<int32_t>(lo);
         bars->unit = static_cast<int32_t>(into - passed);
     }
+}
+
+// Asks for the arrays that the first loads depend on one after the other (offsets, lengths, page
+// table) to be brought into L2, all at once and before they may be read.
+__device__ __forceinline__ void prefetch_tables(const KvAttentionArgs& a) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t line = t * 32;  // 32-bit entries
+    if (line <= a.batch) prefetch_l2(a.row_offsets + line);
+    if (line < a.batch) prefetch_l2(a.cache_lengths + line);
+    if (line < static_cast<int64_t>(a.batch) * a.max_pages) prefetch_l2(a.page_table + line);
 }
 
 // Page and slot of position pos of request b if it is read; page -1 (loads as zeros) if not and
@@ -521,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&bars->tmem_base, kTmemCols);
         tmem_relinquish();
     }
+    prefetch_tables(a);
     griddep_wait();  // launched while the work before may still run: nothing is read before
     plan(a, bars);
     griddep_launch_dependents();
@@ -1156,18 +1161,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
-constexpr int kFewParts = 8;  // that a warp joins alone
+constexpr int kJoinBlocks = 4;  // of an SM
+constexpr int kJoinRows = 2;    // that a warp joins at a time
+// Parts that a warp joins alone, and of items of few rows, whose blocks have nothing else to do.
+constexpr int kFewParts = 8, kFewRows = 8, kFewPartsOfFewRows = 2;
 
 // Joins the parts of the items that several CTAs share: with M the largest of the parts' maxima,
-// out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same order.  A warp has
-// a row, its lanes the columns; many parts are dealt to the warps of a block.
+// out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same order.  A warp takes
+// two rows, a lane four columns of one or both of them; rows of many parts are taken one by one by
+// the warps of a block, which share the parts.  Bound by latency, so several rows are on their way.
 template <int DB>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
     kv_join_kernel(const KvAttentionArgs a, const KvWorkspace ws, const int ctas) {
-    constexpr int D = DB * 64, kCols = 2 * DB;  // columns of a lane
+    constexpr int D = DB * 64;
+    constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;  // lanes of a row, rows of a load
+    constexpr int kEach = kJoinRows / kAtOnce;            // rows of a lane
     __shared__ KvItem items[kKvMaxCtas];
-    __shared__ int begins[2][kKvMaxCtas + 1];  // rows of items of few parts, and of many
-    __shared__ float sums[kJoinWarps][D];
+    __shared__ int begins[2][kKvMaxCtas + 1];  // tasks of items of few parts, and of many
+    __shared__ float4 sums[kJoinWarps][32];
     __shared__ float2 totals[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = a.num_heads / a.num_kv_heads;
@@ -1175,16 +1186,18 @@ __global__ void __launch_bounds__(kJoinThreads)
     griddep_wait();
     const KvItem* left = reinterpret_cast<const KvItem*>(a.workspace + ws.items);
     if (warp < 2) {
-        constexpr int kEach = (kKvMaxCtas + 31) / 32;
-        int n[kEach], sum = 0;
+        constexpr int kItems = (kKvMaxCtas + 31) / 32;
+        int n[kItems], sum = 0;
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const int p = lane * kEach + k;
+        for (int k = 0; k < kItems; ++k) {
+            const int p = lane * kItems + k;
             n[k] = 0;
             if (p < ctas) {
                 const KvItem it = left[p];
                 if (warp == 0) items[p] = it;
-                if ((it.parts > kFewParts) == (warp == 1)) n[k] = it.tokens * group;
+                const int rows = it.tokens * group;
+                const bool many = it.parts > (rows > kFewRows ? kFewParts : kFewPartsOfFewRows);
+                if (many == (warp == 1)) n[k] = many ? rows : (rows + kJoinRows - 1) / kJoinRows;
             }
             sum += n[k];
         }
@@ -1196,8 +1209,8 @@ __global__ void __launch_bounds__(kJoinThreads)
         }
         int at = incl - sum;
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const int p = lane * kEach + k;
+        for (int k = 0; k < kItems; ++k) {
+            const int p = lane * kItems + k;
             if (p <= ctas) begins[warp][p] = at;
             at += n[k];
         }
@@ -1206,71 +1219,97 @@ __global__ void __launch_bounds__(kJoinThreads)
     __syncthreads();
     const float* parts = reinterpret_cast<const float*>(a.workspace);
     const float2* stats = reinterpret_cast<const float2*>(a.workspace + ws.stats);
-    // warps take rows of few parts, whole blocks those of many
-    for (int pass = 0; pass < 2; ++pass) {
-        const bool many = pass == 1;
-        const int tasks = begins[pass][ctas];
-        const int stride = many ? gridDim.x : gridDim.x * kJoinWarps;
-        for (int f = many ? blockIdx.x : blockIdx.x * kJoinWarps + warp; f < tasks; f += stride) {
-            int p = 0, behind = ctas;
-            while (behind - p > 1) {
-                const int mid = (p + behind) / 2;
-                if (begins[pass][mid] <= f) p = mid;
-                else behind = mid;
-            }
-            const KvItem it = items[p];
-            const int row = f - begins[pass][p];
-            const int token = row / group, head = row - token * group;
-            const int sub = token / a.tile_tokens;
-            const int slot_row = sub * kTile + (token - sub * a.tile_tokens) * group + head;
-            float top = -INFINITY, total = 0.0f, o[kCols] = {};
-#pragma unroll 4
-            for (int k = many ? warp : 0; k < it.parts; k += many ? kJoinWarps : 1) {
-                // the CTA's second slot, then the first slots of those behind
-                const int64_t at = (2 * static_cast<int64_t>(p + k) + (k == 0 ? 1 : 0)) * ws.rows + slot_row;
-                const float2 s = __ldcg(stats + at);
-                float v[kCols];
-#pragma unroll
-                for (int c = 0; c < kCols; c += 2) {
-                    const float2 x = __ldcg(reinterpret_cast<const float2*>(parts + at * D + lane * kCols + c));
-                    v[c] = x.x;
-                    v[c + 1] = x.y;
-                }
-                const float m = fmaxf(top, s.x);
-                const float f0 = top == -INFINITY ? 0.0f : exp2f(top - m);
-                const float f1 = s.x == -INFINITY ? 0.0f : exp2f(s.x - m);
-                top = m;
-                total = total * f0 + s.y * f1;
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) o[c] = o[c] * f0 + v[c] * f1;
-            }
-            if (many) {
-                if (lane == 0) totals[warp] = make_float2(top, total);
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) sums[warp][lane * kCols + c] = o[c];
-                __syncthreads();
-                top = -INFINITY;
-                total = 0.0f;
-                for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, totals[k].x);
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) o[c] = 0.0f;
-                for (int k = 0; k < kJoinWarps; ++k) {
-                    const float f1 = totals[k].x == -INFINITY ? 0.0f : exp2f(totals[k].x - top);
-                    total = fmaf(totals[k].y, f1, total);
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) o[c] = fmaf(sums[k][lane * kCols + c], f1, o[c]);
-                }
-                __syncthreads();
-                if (warp != 0) continue;
-            }
-            const float inv = total != 0.0f ? 1.0f / total : 0.0f;
-            const int64_t out_row = (it.row + token) * a.num_heads + it.head + head;
-            uint32_t* to = reinterpret_cast<uint32_t*>(a.out + out_row * D + lane * kCols);
-#pragma unroll
-            for (int c = 0; c < kCols; c += 2) to[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
-            if (a.lse != nullptr && lane == 0)
-                a.lse[out_row] = total != 0.0f ? top * kLn2 + logf(total) : -INFINITY;
+    const auto find = [&](const int* begin, int f) -> int {  // the item of a task
+        int p = 0, behind = ctas;
+        while (behind - p > 1) {
+            const int mid = (p + behind) / 2;
+            if (begin[mid] <= f) p = mid;
+            else behind = mid;
         }
+        return p;
+    };
+    struct Row {
+        int64_t out;    // its row of the output
+        int32_t slot;   // and of a part
+    };
+    const auto place = [&](const KvItem& it, int row) -> Row {
+        const int token = row / group, head = row - token * group, sub = token / a.tile_tokens;
+        return Row{(it.row + token) * a.num_heads + it.head + head,
+                   sub * kTile + (token - sub * a.tile_tokens) * group + head};
+    };
+    // part k of the item that CTA p starts: the CTA's second slot, then the first slots of those behind
+    const auto slot = [&](int p, int k) -> int64_t {
+        return (2 * static_cast<int64_t>(p + k) + (k == 0 ? 1 : 0)) * ws.rows;
+    };
+    struct Sum {
+        float top = -INFINITY, total = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        __device__ __forceinline__ void add(float2 s, float4 v) {
+            const float m = fmaxf(top, s.x);
+            const float f0 = top == -INFINITY ? 0.0f : exp2f(top - m);
+            const float f1 = s.x == -INFINITY ? 0.0f : exp2f(s.x - m);
+            top = m;
+            total = total * f0 + s.y * f1;
+            o = make_float4(o.x * f0 + v.x * f1, o.y * f0 + v.y * f1, o.z * f0 + v.z * f1, o.w * f0 + v.w * f1);
+        }
+    };
+    const int col = (lane % kLanes) * 4;
+    const auto finish = [&](const Sum& x, int64_t out) {
+        const float inv = x.total != 0.0f ? 1.0f / x.total : 0.0f;
+        *reinterpret_cast<uint2*>(a.out + out * D + col) =
+            make_uint2(pack_bf16x2(x.o.x * inv, x.o.y * inv), pack_bf16x2(x.o.z * inv, x.o.w * inv));
+        if (a.lse != nullptr && col == 0)
+            a.lse[out] = x.total != 0.0f ? (x.top + __log2f(x.total)) * kLn2 : -INFINITY;
+    };
+    for (int f = blockIdx.x * kJoinWarps + warp; f < begins[0][ctas]; f += gridDim.x * kJoinWarps) {
+        const int p = find(begins[0], f);
+        const KvItem it = items[p];
+        const int row0 = (f - begins[0][p]) * kJoinRows + lane / kLanes, rows = it.tokens * group;
+        Sum x[kEach];
+        Row r[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) r[i] = place(it, min(row0 + i * kAtOnce, rows - 1));
+        for (int k = 0; k < it.parts; ++k) {
+            float2 s[kEach];
+            float4 v[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int64_t at = slot(p, k) + r[i].slot;
+                s[i] = __ldcg(stats + at);
+                v[i] = __ldcg(reinterpret_cast<const float4*>(parts + at * D + col));
+            }
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) x[i].add(s[i], v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (row0 + i * kAtOnce < rows) finish(x[i], r[i].out);
+    }
+    for (int f = blockIdx.x; f < begins[1][ctas]; f += gridDim.x) {
+        const int p = find(begins[1], f);
+        const KvItem it = items[p];
+        const Row r = place(it, f - begins[1][p]);
+        Sum x;
+#pragma unroll 4
+        for (int k = warp * kAtOnce + lane / kLanes; k < it.parts; k += kJoinWarps * kAtOnce) {
+            const int64_t at = slot(p, k) + r.slot;
+            x.add(__ldcg(stats + at), __ldcg(reinterpret_cast<const float4*>(parts + at * D + col)));
+        }
+        if constexpr (kAtOnce == 2) {  // the other half of the lanes had other parts
+            const float2 s = make_float2(__shfl_xor_sync(0xffffffffu, x.top, 16), __shfl_xor_sync(0xffffffffu, x.total, 16));
+            const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, x.o.x, 16), __shfl_xor_sync(0xffffffffu, x.o.y, 16),
+                                         __shfl_xor_sync(0xffffffffu, x.o.z, 16), __shfl_xor_sync(0xffffffffu, x.o.w, 16));
+            x.add(s, v);
+        }
+        if (lane == 0) totals[warp] = make_float2(x.top, x.total);
+        sums[warp][lane] = x.o;
+        __syncthreads();
+        if (warp == 0) {
+            Sum y;
+            for (int k = 0; k < kJoinWarps; ++k) y.add(totals[k], sums[k][lane]);
+            if (lane < kLanes) finish(y, r.out);
+        }
+        __syncthreads();
     }
 }
 
@@ -1299,7 +1338,7 @@ cudaError_t launch_shape(const KvMaps& maps, const KvAttentionArgs& args, const 
     e = launch_dependent(kv_attention_kernel<DB, TMA>, static_cast<unsigned>(ctas), kThreads, smem,
                          stream, maps, args, ws);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kv_join_kernel<DB>, static_cast<unsigned>(num_sms) * 2, kJoinThreads, 0,
+    return launch_dependent(kv_join_kernel<DB>, static_cast<unsigned>(num_sms) * kJoinBlocks, kJoinThreads, 0,
                             stream, args, ws, ctas);
 }
 

@@ -112,12 +112,35 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a) {
             if (is_value(h)) v[i] = load_unit(source(h) - col + u * 8, 0);
             else v[i] = load_unit(source(h), second);
         }
-        const int b = request_of(a.row_offsets, a.batch, static_cast<uint32_t>(r));
-        if (b < 0) continue;
+        // the factors do not wait for the row's request either
         bool inside = true;
+#pragma unroll 1
         for (int x = 0; x < a.num_axes; ++x)
             inside = inside && __ldg(a.positions + static_cast<int64_t>(x) * a.total_rows + r) <
                                    static_cast<uint32_t>(a.max_seq_len);
+        float cs[8] = {};
+        if (inside && turns) {
+            const uint32_t axes = a.unit_axes[u];
+            if (axes == (axes & 3u) * 0x55u) {  // the four pairs are of one axis
+                const uint32_t pos = __ldg(a.positions + static_cast<int64_t>(axes & 3u) * a.total_rows + r);
+                const float4* f = reinterpret_cast<const float4*>(a.freqs + static_cast<int64_t>(pos) * a.rope_dim + u * 8);
+                const float4 f0 = __ldg(f), f1 = __ldg(f + 1);
+                cs[0] = f0.x, cs[1] = f0.y, cs[2] = f0.z, cs[3] = f0.w;
+                cs[4] = f1.x, cs[5] = f1.y, cs[6] = f1.z, cs[7] = f1.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t pos = __ldg(
+                        a.positions + static_cast<int64_t>((axes >> (2 * k)) & 3u) * a.total_rows + r);
+                    const float2 f = __ldg(reinterpret_cast<const float2*>(
+                        a.freqs + static_cast<int64_t>(pos) * a.rope_dim + u * 8 + 2 * k));
+                    cs[2 * k] = f.x;
+                    cs[2 * k + 1] = f.y;
+                }
+            }
+        }
+        const int b = request_of(a.row_offsets, a.batch, static_cast<uint32_t>(r));
+        if (b < 0) continue;
         int64_t slot = 0;
         if (!queries) {
             const uint64_t at = static_cast<uint64_t>(__ldg(a.cache_lengths + b)) +
@@ -138,19 +161,6 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a) {
             continue;
         }
         if (!in_use) continue;
-        float cs[8];
-        if (turns) {
-            const uint32_t axes = a.unit_axes[u];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t pos = __ldg(
-                    a.positions + static_cast<int64_t>((axes >> (2 * k)) & 3u) * a.total_rows + r);
-                const float2 f = __ldg(reinterpret_cast<const float2*>(
-                    a.freqs + static_cast<int64_t>(pos) * a.rope_dim + u * 8 + 2 * k));
-                cs[2 * k] = f.x;
-                cs[2 * k + 1] = f.y;
-            }
-        }
         if (from_cache) {
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
