@@ -664,10 +664,7 @@ def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_co
                     stream, check)
 
 
-def _heads_of(t) -> Optional[tuple]:
-    """Row and head stride of a bf16 view [rows, heads, D] with contiguous columns."""
-    strides = t.stride()
-    return strides if len(strides) == 3 and strides[2] == 1 and t.dtype in _BF16 else None
+_NO_STRIDE = (0, 0)  # of a tensor that is not given
 
 
 def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
@@ -682,20 +679,28 @@ def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
     last dimensions.  positions: uint32/int32 [axes, rows] (or [rows], one axis); pair_axes: the
     axis of every pair of the P columns of freqs_cis [max_seq_len, P] (P/2 whole numbers on the
     host, None: axis 0).  Pairs are columns (2j, 2j + 1), or (j, j + P/2) with `half`."""
-    where, table, factors, at_axes = "kv_rope_paged", kv_cache.page_table, freqs_cis.shape, positions.shape
-    pages, batch, axes = table.shape, input_row_offsets.shape[0] - 1, 1 if len(at_axes) == 1 else at_axes[0]
-    rows = at_axes[-1] if 1 <= len(at_axes) <= 2 else -1
-    size = kv_cache.row_elems // num_kv_heads if num_kv_heads > 0 else 0
+    table, factors, counts = kv_cache.page_table, freqs_cis.shape, positions.shape
+    pages, batch = table.shape, input_row_offsets.shape[0] - 1
     device, at = _look(((_WORD, 0, input_row_offsets), (_WORD, 0, positions), (_FLOAT, 0, freqs_cis),
                         (None, 0, kv_cache.data), (_WORD, 0, table), (_WORD, batch, kv_cache.cache_lengths),
                         (None, 0, q), (None, 0, q_out), (None, 0, k), (None, 0, v)))
-    strides, heads = [], 0 if q is None else q.shape[1] if len(q.shape) == 3 else -1
-    ok = device is not None and rows >= 0 and (q is None) == (q_out is None) and len(pages) == 2 \
-        and pages[0] >= batch and len(factors) == 2 and len(input_row_offsets.shape) == 1
-    for t, n in ((q, heads), (q_out, heads), (k, num_kv_heads), (v, num_kv_heads)):
-        st = (0, 0) if t is None else _heads_of(t)
-        ok = ok and st is not None and (t is None or t.shape == (rows, n, size))
-        strides.append(st)
+    n = len(counts)
+    rows, axes = (counts[0], 1) if n == 1 else (counts[1], counts[0]) if n == 2 else (-1, 0)
+    size = kv_cache.row_elems // num_kv_heads if num_kv_heads > 0 else 0
+    ok = device is not None and rows >= 0 and len(pages) == 2 and pages[0] >= batch and len(factors) == 2 \
+        and (q is None) == (q_out is None)
+    heads, sq, so, sk, sv = 0, _NO_STRIDE, _NO_STRIDE, _NO_STRIDE, _NO_STRIDE
+    if ok and q is not None:
+        shape, sq, so = q.shape, q.stride(), q_out.stride()
+        ok = len(shape) == 3 and shape[0] == rows and shape[2] == size and q_out.shape == shape \
+            and sq[2] == 1 and so[2] == 1 and q.dtype in _BF16 and q_out.dtype in _BF16
+        heads = shape[1] if ok else 0
+    if ok and k is not None:
+        sk = k.stride()
+        ok = k.shape == (rows, num_kv_heads, size) and sk[2] == 1 and k.dtype in _BF16
+    if ok and v is not None:
+        sv = v.stride()
+        ok = v.shape == (rows, num_kv_heads, size) and sv[2] == 1 and v.dtype in _BF16
     if ok and pair_axes is not None:
         try:
             pair_axes = bytes(pair_axes)
@@ -703,13 +708,12 @@ def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
             ok = False
         ok = ok and len(pair_axes) == factors[1] // 2
     if not ok:
-        return _check(PKM_ERR_INVALID_ARG, where, check)
-    sq, so, sk, sv = strides
+        return _check(PKM_ERR_INVALID_ARG, "kv_rope_paged", check)
     c = kv_cache._struct_of((at[3], at[4], pages[1], at[5]))
     args = (at[6], sq[0], sq[1], heads, at[7], so[0], so[1], at[8], sk[0], sk[1], at[9], sv[0], sv[1],
             num_kv_heads, size, factors[1], at[0], batch, rows, at[1], axes, pair_axes, at[2],
-            factors[0], 1 if half else 0, ctypes.byref(c), int(layer_idx), _ptr(dev_status))
-    return _run(_lib.kv_rope_paged, where, args, device, stream, check)
+            factors[0], 1 if half else 0, ctypes.byref(c), layer_idx, _ptr(dev_status))
+    return _run(_lib.kv_rope_paged, "kv_rope_paged", args, device, stream, check)
 
 
 def kv_attention_paged_workspace_size(total_rows: int, num_heads: int, num_kv_heads: int,
@@ -726,10 +730,10 @@ def _kv_attention(f, where, q, offsets, scale, limits, cache, layer_idx, out, wo
     device, at = _look(((None, 0, q), (_WORD, 0, offsets), (_BF16, 0, out), (None, 0, workspace),
                         (_FLOAT, 0, lse), (None, 0, cache.data), (_WORD, 0, table),
                         (_WORD, batch, cache.cache_lengths)))
-    strides = _heads_of(q)
-    if device is None or strides is None or out.shape != shape or not workspace.is_contiguous() \
-            or (lse is not None and lse.shape != shape[:2]) or len(pages) != 2 or pages[0] < batch \
-            or shape[2] == 0 or cache.row_elems % shape[2] != 0:
+    strides = q.stride()
+    if device is None or len(shape) != 3 or strides[2] != 1 or q.dtype not in _BF16 or out.shape != shape \
+            or not workspace.is_contiguous() or (lse is not None and lse.shape != shape[:2]) \
+            or len(pages) != 2 or pages[0] < batch or shape[2] == 0 or cache.row_elems % shape[2] != 0:
         return _check(PKM_ERR_INVALID_ARG, where, check)
     c = cache._struct_of((at[5], at[6], pages[1], at[7]))
     args = (at[0], strides[0], strides[1], at[1], batch, shape[0], shape[1],

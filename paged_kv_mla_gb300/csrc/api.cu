@@ -1302,6 +1302,12 @@ pkm_status kv_matmul_paged_fp8(const void* hidden_state, const uint32_t* input_r
 
 namespace {
 
+// floor(2^64 / page_size) + 1, with which positions below 2^33 are divided by a multiplication;
+// 2^64 / page_size where that is a whole number, and 0 for pages of one slot.
+uint64_t page_inverse(int32_t page_size) {
+    return page_size > 1 ? UINT64_MAX / static_cast<uint64_t>(page_size) + 1 : 0;
+}
+
 // The cache of the calls on heads of keys and values.
 pkm_status check_kv_cache(const pkm_paged_cache* c, uint32_t layer_idx, int32_t num_kv_heads,
                           int32_t head_size) {
@@ -1368,8 +1374,7 @@ pkm_status kv_attention(const void* q, int64_t q_row_stride, int64_t q_head_stri
     a.sinks = sink_tokens;
     a.sink_tiles = sink_tokens / 128 + (sink_tokens % 128 != 0 ? 1 : 0);
     a.tile_tokens = pkm::kv_tile_tokens(num_heads, num_kv_heads);
-    // (page sizes that are powers of two divide 2^64)
-    if (kv_cache->page_size > 1) a.page_inverse = UINT64_MAX / kv_cache->page_size + 1;
+    a.page_inverse = page_inverse(kv_cache->page_size);
     a.cache_layer = static_cast<const uint16_t*>(kv_cache->data) +
                     static_cast<int64_t>(layer_idx) * kv_cache->layer_stride;
     a.page_stride = kv_cache->page_stride;
@@ -1496,6 +1501,7 @@ pkm_status kv_rope_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
     a.freqs = freqs_cis;
     a.max_seq_len = max_seq_len;
     a.half = half;
+    a.page_inverse = page_inverse(kv_cache->page_size);
     a.cache_layer = static_cast<uint16_t*>(kv_cache->data) +
                     static_cast<int64_t>(layer_idx) * kv_cache->layer_stride;
     a.page_stride = kv_cache->page_stride;

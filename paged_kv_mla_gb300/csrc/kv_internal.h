@@ -24,6 +24,7 @@ struct KvRopeArgs {
     const float* freqs;            // [max_seq_len, P]
     int32_t max_seq_len;
     int32_t half;                  // pairs (j, j + P/2) instead of (2j, 2j + 1)
+    uint64_t page_inverse;         // floor(2^64 / page_size) + 1, or 0 for pages of one slot
     uint16_t* cache_layer;         // cache data + layer_idx * layer_stride
     int64_t page_stride, slot_stride, kv_stride;
     int32_t num_pages, page_size, max_pages;

@@ -20,7 +20,8 @@ namespace pkm {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;  // heads in flight per thread
+constexpr int kUnroll = 4;  // heads of an item a thread has
+constexpr int kBlocks = 8;  // of an SM, all resident
 
 // Columns of a turned unit: 16 bytes in the interleaved layout, twice 8 bytes (four columns of
 // each half) in the half layout; copied units are 16 bytes in both.
@@ -77,7 +78,7 @@ __device__ __forceinline__ int request_of(const uint32_t* offsets, int batch, ui
 }
 
 template <bool HALF>
-__global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) kv_rope_kernel(const KvRopeArgs a) {
     const int units = a.head_size / 8;
     const int heads_per_pass = kThreads / units;
     const int u = threadIdx.x % units, h_in = threadIdx.x / units;
@@ -85,74 +86,93 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a) {
     const int q_groups = (a.num_heads + group - 1) / group;
     const int kv_heads = a.num_kv_heads * (a.v != nullptr ? 2 : 1);
     const int groups = q_groups + (kv_heads + group - 1) / group;
-    const int64_t items = static_cast<int64_t>(a.total_rows) * groups;
     const bool turns = u * 8 < a.rope_dim;
     const int col = HALF && turns ? u * 4 : u * 8;
     const int second = HALF && turns ? a.rope_dim / 2 : 0;
     const bool in_use = h_in < heads_per_pass;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t r = it / groups;
-        const int g = static_cast<int>(it % groups);
+    const uint32_t axes = turns ? a.unit_axes[u] : 0;
+    const uint32_t rows = static_cast<uint32_t>(a.total_rows);
+    const uint32_t covered = __ldg(a.row_offsets), behind = __ldg(a.row_offsets + a.batch);
+
+    struct Item {
+        int64_t r;
+        int h0, heads;  // the thread's first head, and behind the last
+        bool queries;
+    };
+    const auto item = [&](uint32_t r, int g) -> Item {
         const bool queries = g < q_groups;
-        const int heads = queries ? a.num_heads : kv_heads;
-        const int h0 = (queries ? g : g - q_groups) * group + h_in;
-        const auto source = [&](int h) -> const uint16_t* {
-            if (queries) return a.q + r * a.q_row_stride + h * a.q_head_stride + col;
-            if (h < a.num_kv_heads) return a.k + r * a.k_row_stride + h * a.k_head_stride + col;
-            return a.v + r * a.v_row_stride + (h - a.num_kv_heads) * a.v_head_stride + col;
-        };
-        // the half layout's places are for turned heads: values are copied in whole units
-        const auto is_value = [&](int h) { return !queries && h >= a.num_kv_heads; };
-        uint4 v[kUnroll];
-        const bool from_cache = !queries && a.k == nullptr;  // keys, turned in place
+        return Item{r, (queries ? g : g - q_groups) * group + h_in, queries ? a.num_heads : kv_heads, queries};
+    };
+    // values are copied in whole units; the half layout's places are for turned heads
+    const auto is_value = [&](const Item& x, int h) { return !x.queries && h >= a.num_kv_heads; };
+    const auto load = [&](const Item& x, uint4 (&v)[kUnroll]) {
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const int h = h0 + i * heads_per_pass;
-            if (!in_use || h >= heads || (from_cache && !is_value(h))) continue;
-            if (is_value(h)) v[i] = load_unit(source(h) - col + u * 8, 0);
-            else v[i] = load_unit(source(h), second);
+            const int h = x.h0 + i * heads_per_pass;
+            if (!in_use || h >= x.heads) continue;
+            if (is_value(x, h))
+                v[i] = load_unit(a.v + x.r * a.v_row_stride + (h - a.num_kv_heads) * a.v_head_stride + u * 8, 0);
+            else if (x.queries)
+                v[i] = load_unit(a.q + x.r * a.q_row_stride + h * a.q_head_stride + col, second);
+            else if (a.k != nullptr)
+                v[i] = load_unit(a.k + x.r * a.k_row_stride + h * a.k_head_stride + col, second);
         }
-        // the factors do not wait for the row's request either
-        bool inside = true;
-#pragma unroll 1
-        for (int x = 0; x < a.num_axes; ++x)
-            inside = inside && __ldg(a.positions + static_cast<int64_t>(x) * a.total_rows + r) <
-                                   static_cast<uint32_t>(a.max_seq_len);
+    };
+    // a block's items are gridDim.x apart in the line of all rows' groups of heads
+    const int step = static_cast<int>(gridDim.x % groups);
+    int g = static_cast<int>(blockIdx.x % groups) - step;
+    uint32_t it = blockIdx.x / groups - gridDim.x / groups;
+    while (true) {
+        it += gridDim.x / groups;
+        g += step;
+        if (g >= groups) {
+            g -= groups;
+            ++it;
+        }
+        if (it >= rows) break;
+        const Item x = item(it, g);
+        uint4 v[kUnroll];
+        load(x, v);
+        // all positions at once; the factors do not wait for the row's request
+        uint32_t pos[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            pos[n] = n < a.num_axes ? __ldg(a.positions + static_cast<int64_t>(n) * a.total_rows + x.r) : 0;
+        bool inside = max(max(pos[0], pos[1]), max(pos[2], pos[3])) < static_cast<uint32_t>(a.max_seq_len);
         float cs[8] = {};
         if (inside && turns) {
-            const uint32_t axes = a.unit_axes[u];
+            const auto factors = [&](uint32_t axis) -> const float* {
+                const uint32_t lo = axis & 1u ? pos[1] : pos[0], hi = axis & 1u ? pos[3] : pos[2];
+                return a.freqs + static_cast<int64_t>(axis & 2u ? hi : lo) * a.rope_dim + u * 8;
+            };
             if (axes == (axes & 3u) * 0x55u) {  // the four pairs are of one axis
-                const uint32_t pos = __ldg(a.positions + static_cast<int64_t>(axes & 3u) * a.total_rows + r);
-                const float4* f = reinterpret_cast<const float4*>(a.freqs + static_cast<int64_t>(pos) * a.rope_dim + u * 8);
+                const float4* f = reinterpret_cast<const float4*>(factors(axes & 3u));
                 const float4 f0 = __ldg(f), f1 = __ldg(f + 1);
                 cs[0] = f0.x, cs[1] = f0.y, cs[2] = f0.z, cs[3] = f0.w;
                 cs[4] = f1.x, cs[5] = f1.y, cs[6] = f1.z, cs[7] = f1.w;
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t pos = __ldg(
-                        a.positions + static_cast<int64_t>((axes >> (2 * k)) & 3u) * a.total_rows + r);
-                    const float2 f = __ldg(reinterpret_cast<const float2*>(
-                        a.freqs + static_cast<int64_t>(pos) * a.rope_dim + u * 8 + 2 * k));
+                    const float2 f = __ldg(reinterpret_cast<const float2*>(factors(axes >> (2 * k) & 3u)) + k);
                     cs[2 * k] = f.x;
                     cs[2 * k + 1] = f.y;
                 }
             }
         }
-        const int b = request_of(a.row_offsets, a.batch, static_cast<uint32_t>(r));
-        if (b < 0) continue;
+        if (it < covered || it >= behind) continue;  // of no request
         int64_t slot = 0;
-        if (!queries) {
-            const uint64_t at = static_cast<uint64_t>(__ldg(a.cache_lengths + b)) +
-                                (static_cast<uint64_t>(r) - __ldg(a.row_offsets + b));
-            const uint64_t page_size = static_cast<uint64_t>(a.page_size);
-            const uint64_t lp = at / page_size;
+        if (!x.queries) {
+            const int b = request_of(a.row_offsets, a.batch, it);
+            if (b < 0) continue;
+            const uint64_t at = static_cast<uint64_t>(__ldg(a.cache_lengths + b)) + (it - __ldg(a.row_offsets + b));
+            // at / page_size for positions below 2^33: off by less than 2^-31 before rounding down
+            const uint64_t lp = a.page_inverse == 0 ? at : __umul64hi(at, a.page_inverse);
             uint32_t page = UINT32_MAX;
             if (lp < static_cast<uint64_t>(a.max_pages))
                 page = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
             if (page < static_cast<uint32_t>(a.num_pages))
                 slot = static_cast<int64_t>(page) * a.page_stride +
-                       static_cast<int64_t>(at - lp * page_size) * a.slot_stride;
+                       static_cast<int64_t>(at - lp * a.page_size) * a.slot_stride;
             else
                 inside = false;
         }
@@ -161,27 +181,28 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a) {
             continue;
         }
         if (!in_use) continue;
+        const bool from_cache = !x.queries && a.k == nullptr;  // keys, turned in place
         if (from_cache) {
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
-                const int h = h0 + i * heads_per_pass;
-                if (h < heads && !is_value(h) && turns)
+                const int h = x.h0 + i * heads_per_pass;
+                if (h < x.heads && !is_value(x, h) && turns)
                     v[i] = load_unit(a.cache_layer + slot + h * a.head_size + col, second);
             }
         }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const int h = h0 + i * heads_per_pass;
-            if (h >= heads) continue;
-            if (is_value(h)) {
+            const int h = x.h0 + i * heads_per_pass;
+            if (h >= x.heads) continue;
+            if (is_value(x, h)) {
                 uint16_t* to = a.cache_layer + slot + a.kv_stride + (h - a.num_kv_heads) * a.head_size;
                 store_unit(to + u * 8, 0, v[i]);
                 continue;
             }
-            uint16_t* to = queries ? a.q_out + r * a.q_out_row_stride + h * a.q_out_head_stride
-                                   : a.cache_layer + slot + h * a.head_size;
+            uint16_t* to = x.queries ? a.q_out + x.r * a.q_out_row_stride + h * a.q_out_head_stride
+                                     : a.cache_layer + slot + h * a.head_size;
             if (turns) store_unit(to + col, second, turned<HALF>(v[i], cs));
-            else if (queries ? a.q != a.q_out : !from_cache) store_unit(to + col, 0, v[i]);
+            else if (x.queries ? a.q != a.q_out : !from_cache) store_unit(to + col, 0, v[i]);
         }
     }
 }
@@ -191,10 +212,10 @@ __global__ void __launch_bounds__(kThreads) kv_rope_kernel(const KvRopeArgs a) {
 cudaError_t launch_kv_rope(KvRopeArgs args, int num_sms, cudaStream_t stream) {
     const int group = kThreads / (args.head_size / 8) * kUnroll;
     const int64_t kv_heads = static_cast<int64_t>(args.num_kv_heads) * (args.v != nullptr ? 2 : 1);
-    const int64_t items = static_cast<int64_t>(args.total_rows) *
-                          ((args.num_heads + group - 1) / group + (kv_heads + group - 1) / group);
-    const int64_t most = static_cast<int64_t>(num_sms) * 64;
-    const unsigned blocks = static_cast<unsigned>(items < most ? items : most);
+    const int64_t groups = (args.num_heads + group - 1) / group + (kv_heads + group - 1) / group;
+    const int64_t items = args.total_rows * groups, most = static_cast<int64_t>(num_sms) * kBlocks;
+    unsigned blocks = static_cast<unsigned>(items < most ? items : most);
+    if (items > most && most % groups == 0) --blocks;  // all blocks meet all groups of heads
     if (args.half)
         kv_rope_kernel<true><<<blocks, kThreads, 0, stream>>>(args);
     else
