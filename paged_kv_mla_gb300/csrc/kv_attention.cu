@@ -543,12 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t parts = 0;  // that the warp has seen
     Part part;
     // Takes the next part; false behind the last one, or when a wait ran out.
-    const auto next_part = [&]() -> bool {
+    const auto next_part = [&](const auto& wait_part) -> bool {
         const uint32_t at = parts % kParts, phase = (parts / kParts) & 1;
         ++parts;
-        if (!(warp < kScoreWarp ? warp_wait(&bars->part_full[at], phase, wc)
-                                : issue_wait(&bars->part_full[at], phase)))
-            return false;
+        if (!wait_part(&bars->part_full[at], phase)) return false;
         part = bars->part[at];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->part_empty[at]);
@@ -574,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_inl(bar, parity, wc) && ok;
             __syncwarp();
         };
-        while (__all_sync(0xffffffffu, ok) && next_part()) {
+        const auto part_wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, wc); };
+        while (__all_sync(0xffffffffu, ok) && next_part(part_wait)) {
             const int tiles = part.x1 - part.x0, steps = part.wide ? 2 * tiles : tiles;
             const int mine = stage ^ (n & 1);       // the stage's first step
             const int sub = part.wide ? mine : 0;   // its tile of queries
@@ -722,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 at.next(S::kKeyStages);
             };
-            while (go_on() && next_part()) {
+            while (go_on() && next_part(issue_wait)) {
                 const bool wide = __any_sync(0xffffffffu, part.wide != 0);
                 const int tiles = __shfl_sync(0xffffffffu, part.x1 - part.x0, 0), steps = wide ? 2 * tiles : tiles;
                 const int mine = (n & 1) ^ stage;  // the stage's first step
@@ -762,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t id = idesc_bf16(128, D, false, true);
             const uint64_t v_desc = sdesc_sw128(smem_u32(sV), 1024, DB * 1024);
             uint32_t empty_phase = 3;  // a bit for each stage; the first wait passes
-            while (go_on() && next_part()) {
+            while (go_on() && next_part(issue_wait)) {
                 const bool wide = __any_sync(0xffffffffu, part.wide != 0);
                 const int tiles = __shfl_sync(0xffffffffu, part.x1 - part.x0, 0), steps = wide ? 2 * tiles : tiles;
 #pragma unroll 1
@@ -978,6 +977,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row_token = row / group, row_head = row - row_token * group;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+        // A part can take longer than the time limit, which the softmax warps keep step by step: the
+        // epilogue's waits end with the abort flag, or after many times the limit.
+        const auto end_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+            bool done = false;
+#pragma unroll 1
+            for (int i = 0; i < 64 && !done && !*wc.abort_flag; ++i)
+                done = mbar_wait_flag(bar, parity, wc.abort_flag, tries);
+            return __all_sync(0xffffffffu, done);
+        };
         uint32_t tiles_before = 0, own_phase = 0;
         uint32_t use = 0;  // phases of the stages' uses, a bit each
         KvItem left{0, 0, 0, 0};
@@ -997,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int turn = number > 0 ? 0 : 1; ok && turn < 2; ++turn) {
                 if (turn == 1) {
                     if (number > 0) tiles_before += now.x1 - now.x0;
-                    more = next_part();
+                    more = next_part(end_wait);
                     if (!more) break;
                     p = part;
                     x = p.x1 - 1;
@@ -1013,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         continue;
                     }
                     const uint32_t tile = tiles_before + (p.x1 - 1 - x), at = tile % S::kValueStages;
-                    ok = warp_wait(&bars->v_own[at], (own_phase >> at) & 1, wc);
+                    ok = end_wait(&bars->v_own[at], (own_phase >> at) & 1);
                     if (!ok) break;
                     own_phase ^= 1u << at;
                     const int64_t end = p.pos + p.tokens - static_cast<int64_t>(kt) * kTile;
@@ -1042,8 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const auto take = [&](int stage, float2& st) -> bool {
                     const uint32_t phase = use >> stage & 1;
                     use ^= 1u << stage;
-                    if (!warp_wait(&bars->stats_full[stage], phase, wc) || !warp_wait(&bars->o_full[stage], phase, wc))
-                        return false;
+                    if (!end_wait(&bars->stats_full[stage], phase) || !end_wait(&bars->o_full[stage], phase)) return false;
                     st = bars->stats[stage][row];
                     return true;
                 };
@@ -1113,27 +1120,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const Masked masks(a, now.diagonal[0], now.wide ? now.edge[1] : now.edge[0]);
                     const int64_t pos = now.pos + sub * a.tile_tokens + row_token;
 #pragma unroll 1
-                    for (int64_t i = static_cast<int64_t>(tiles) * kTile * (D / 8) - 1; i >= 0; --i) {
-                        const int c = static_cast<int>(i % (D / 8)) * 8, t = static_cast<int>(i / (D / 8) % kTile);
-                        const int32_t kt = now.tile(now.x0 + static_cast<int32_t>(i / (D / 8) / kTile));
-                        const int64_t at = static_cast<int64_t>(kt) * kTile + t;
-                        if (!masks.any(kt) || at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks))
-                            continue;
-                        const int64_t from = Place(a, now.b, at, true).offset(a);
-                        if (from < 0) continue;
-                        const uint16_t* v = a.cache_layer + a.kv_stride + from + now.head * D + c;
-                        if (!any_nonfinite(ld_nc_v4(v))) continue;
+                    for (int y = now.x0; y < now.x1; ++y) {
+                        const int64_t first_key = static_cast<int64_t>(now.tile(y)) * kTile;
+                        if (!masks.any(now.tile(y))) continue;
 #pragma unroll 1
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t bits = v[k];
-                            if ((bits & 0x7f80u) != 0x7f80u) continue;
-                            const float x = __uint_as_float(bits << 16);
-                            if (whole) {
-                                uint16_t* o = a.out + out_row * D + c + k;
-                                *o = static_cast<uint16_t>(
-                                    pack_bf16x2(__uint_as_float(static_cast<uint32_t>(*o) << 16) + x, 0.0f));
-                            } else {
-                                reinterpret_cast<float*>(a.workspace)[(slot * ws.rows + slot_row) * D + c + k] += x;
+                        for (int i = 0; i < kTile * (D / 8); ++i) {
+                            const int c = i % (D / 8) * 8;
+                            const int64_t at = first_key + i / (D / 8);
+                            if (at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks)) continue;
+                            const int64_t from = Place(a, now.b, at, true).offset(a);
+                            if (from < 0) continue;
+                            const uint16_t* v = a.cache_layer + a.kv_stride + from + now.head * D + c;
+                            if (!any_nonfinite(ld_nc_v4(v))) continue;
+#pragma unroll 1
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t bits = v[k];
+                                if ((bits & 0x7f80u) != 0x7f80u) continue;
+                                const float x = __uint_as_float(bits << 16);
+                                if (whole) {
+                                    uint16_t* o = a.out + out_row * D + c + k;
+                                    *o = static_cast<uint16_t>(
+                                        pack_bf16x2(__uint_as_float(static_cast<uint32_t>(*o) << 16) + x, 0.0f));
+                                } else {
+                                    reinterpret_cast<float*>(a.workspace)[(slot * ws.rows + slot_row) * D + c + k] += x;
+                                }
                             }
                         }
                     }
