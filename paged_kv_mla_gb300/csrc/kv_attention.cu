@@ -42,7 +42,7 @@ constexpr int kThreads = 16 * 32;
 constexpr int kStartRegs = 128, kSoftRegs = 176, kIssueRegs = 56, kEndRegs = 104;
 static_assert(2 * kSoftRegs + kIssueRegs + kEndRegs <= 4 * kStartRegs, "registers of the block");
 constexpr int kTile = 128;          // keys of a tile, rows of a tile of queries
-constexpr int kMaxStages = 7;       // tiles of keys, or of values, in shared memory
+constexpr int kMaxStages = 6;       // tiles of queries, keys or values in shared memory
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWeightCol = 384;    // TMEM column of the weights, 64 a stage
 // An item's start and end, in tiles (with 1 prompts of many lengths take 4 % longer and small ragged
@@ -159,7 +159,7 @@ struct Bars {
     uint64_t v_full[kMaxStages];   // of values
     uint64_t v_empty[kMaxStages];
     uint64_t v_own[kMaxStages];    // values that are looked through first are there
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full[kMaxStages], q_empty[kMaxStages];
     uint64_t s_full[2];          // a step's scores are complete
     uint64_t s_empty[2];         // they have been read
     uint64_t p_full[2];          // its weights are written
@@ -192,13 +192,17 @@ struct Shape {
     static constexpr int kBytes = DB * 128 * 128;   // of a tile
     // Keys of the step at hand and the next; values of the two steps before it, whose weights are
     // not ready, and the next.
-    static constexpr int kKeyStages = DB == 2 ? 2 : 5, kValueStages = DB == 2 ? 3 : 7;
+    static constexpr int kKeyStages = DB == 2 ? 2 : 4, kValueStages = DB == 2 ? 3 : 6;
+    // Tiles of queries: of the item at hand and, with D = 64, the next.  With D = 128 these come when
+    // the item's last scores are done, behind the next item's first keys and values.
+    static constexpr int kQueryStages = DB == 2 ? 2 : 4;
+    static constexpr int kBeforeQueries = DB == 2 ? 1 : 0;
     // TMEM columns of a stage's O and scores; the first kScores of them are places of their own
     static constexpr int kScores = DB == 2 ? 1 : 2;
     __device__ static constexpr uint32_t out_col(int stage) { return stage * kCols; }
     __device__ static constexpr uint32_t score_col(int stage) { return 2 * kCols + (kScores > 1 ? stage * 128 : 0); }
     static_assert(2 * kCols + kScores * 128 <= kWeightCol, "tensor memory");
-    static constexpr size_t kOffKeys = 2 * size_t(kBytes);
+    static constexpr size_t kOffKeys = size_t(kQueryStages) * kBytes;
     static constexpr size_t kOffValues = kOffKeys + size_t(kKeyStages) * kBytes;
     static constexpr size_t kOffBars = kOffValues + size_t(kValueStages) * kBytes;
     static constexpr size_t kSmem = kOffBars + sizeof(Bars);
@@ -389,16 +393,26 @@ __device__ __forceinline__ bool any_nonfinite(const uint4& v) {
     return ((top(v.x) | top(v.y) | top(v.z) | top(v.w)) & 0x80008000u) != 0;
 }
 
-// Makes the infinities and NaN of a quarter of a tile of values zero; whether there were any before
-// row `end`.
+// Readies a quarter of a tile of values, 32 rows, for tokens that attend some of them: rows that no
+// token attends become zero, infinities and NaN of rows that some tokens attend become zero too, and
+// rows that all attend stay.  Returns whether there were any such.  `none` and `all` have a bit a row.
 template <int DB>
-__device__ __forceinline__ bool look_through(uint32_t tile, int quarter, int64_t end) {
+__device__ __forceinline__ bool look_through(uint32_t tile, int quarter, uint32_t none, uint32_t all) {
     const int lane = threadIdx.x & 31;
+    const bool some = (none | all) != ~0u;
     bool found = false;
     // 32 lanes take 512 bytes, four rows of a block; the place in the block does not matter
 #pragma unroll 1
-    for (int i = quarter * DB * 8; i < (quarter + 1) * DB * 8; i += 8) {
-        const uint32_t from = tile + i * 512 + lane * 16;
+    for (int i = 0; i < DB * 8; i += 8) {
+        const uint32_t from = tile + (quarter * DB * 8 + i) * 512 + lane * 16;
+        const auto row = [&](int k) -> int {
+            const int at = (i + k) * 4 + (lane >> 3);  // among all blocks' rows
+            return at / (8 * DB) * 8 + (at & 7);
+        };
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (none >> row(k) & 1u) st_shared_v4(from + k * 512, 0u, 0u, 0u, 0u);
+        if (!some) continue;
         uint4 v[8];
         bool bad = false;
 #pragma unroll
@@ -409,9 +423,8 @@ __device__ __forceinline__ bool look_through(uint32_t tile, int quarter, int64_t
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) {
             const uint4 w = ld_shared_v4(from + k * 512);
-            if (!any_nonfinite(w)) continue;
-            const int at = (i + k) * 4 + (lane >> 3);  // row among all blocks' rows
-            found = found || at / (8 * DB) * 8 + (at & 7) < end;
+            if (!any_nonfinite(w) || (all >> row(k) & 1u)) continue;
+            found = true;
             st_shared_v4(from + k * 512, finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
         }
     }
@@ -492,10 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->v_full[i], 4);   // lanes of the loader, or the warps that look through
             mbar_init(&bars->v_empty[i], 1);
             mbar_init(&bars->v_own[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
             mbar_init(&bars->q_empty[i], 2);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->s_empty[i], 4);
             mbar_init(&bars->p_full[i], 4);
@@ -566,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t scores = lanes + S::score_col(stage), weights = lanes + kWeightCol + stage * 64;
         const uint32_t out = lanes + S::out_col(stage);
         uint32_t uses = 0;
+        bool next = false;  // the next step's scores are there
         // A wait that runs out is looked at once a part; what is computed until then is not used.
         bool ok = true;
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -581,12 +595,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool busy = (warp & 3) * 32 < count * group;  // the warp has rows
             const int64_t pos = part.pos + sub * a.tile_tokens + row_token;
             const Masked masks(a, sub ? part.diagonal[1] : part.diagonal[0], sub ? part.edge[1] : part.edge[0]);
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f, ref = 0.0f;  // ref: m, or 0 before there is one
             for (int x = mine; x < steps; x += 2) {
                 const uint32_t turn = (n + x) >> 1;  // of the stage
-                wait(&bars->s_full[stage], turn & 1);
+                if (!__all_sync(0xffffffffu, next)) wait(&bars->s_full[stage], turn & 1);
                 tc_fence_after();
                 if (!busy) {
+                    next = false;
                     if (lane == 0) mbar_arrive(&bars->s_empty[stage]);
                     if (turn > 0) wait(&bars->p_empty[stage], (turn - 1) & 1);
                     if (lane == 0) mbar_arrive(&bars->p_full[stage]);
@@ -600,59 +615,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const Attended may(a, pos, kt);
                     const float factor = scale2 > 0.0f ? 1.0f : scale2;
 #pragma unroll 1
-                    for (int c = 0; c < kTile; c += 16) {
-                        const uint32_t bits = may.bits(c) & 0xffffu;
-                        if (__all_sync(0xffffffffu, bits == 0xffffu) && factor == 1.0f) continue;
-                        uint32_t v[16];
-                        tmem_ld_x16(scores + c, v);
-                        tmem_ld_wait();
+                    for (int c = 0; c < kTile; c += 32) {
+                        const uint32_t bits = may.bits(c);
+                        if (__all_sync(0xffffffffu, bits == ~0u) && factor == 1.0f) continue;
+                        uint32_t v[32];
+                        if (__all_sync(0xffffffffu, bits == 0)) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            v[k] = __float_as_uint((bits >> k) & 1u ? __uint_as_float(v[k]) * factor : -INFINITY);
-                        tmem_st_x16(scores + c, v);
+                            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(-INFINITY);
+                        } else {
+                            tmem_ld_x32(scores + c, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = __float_as_uint((bits >> k) & 1u ? __uint_as_float(v[k]) * factor : -INFINITY);
+                        }
+                        tmem_st_x32(scores + c, v);
                     }
                     tmem_st_wait();
                 }
+                // The second half is on its way while the first half's maximum is taken.
                 uint32_t s[4][32];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld_x32(scores + k * 32, s[k]);
+                tmem_ld_x32(scores, s[0]);
+                tmem_ld_x32(scores + 32, s[1]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 128; ++c) asm volatile("" : "+r"(s[c >> 5][c & 31]));  // not before
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->s_empty[stage]);
+                for (int c = 0; c < 64; ++c) asm volatile("" : "+r"(s[c >> 5][c & 31]));  // not before
+                tmem_ld_x32(scores + 64, s[2]);
+                tmem_ld_x32(scores + 96, s[3]);
                 const auto f = [&](int c) -> float { return __uint_as_float(s[c >> 5][c & 31]); };
                 float t0 = f(0), t1 = f(1), t2 = f(2), t3 = f(3);
 #pragma unroll
-                for (int c = 4; c < 124; c += 8) {
+                for (int c = 4; c < 60; c += 8) {
                     t0 = fmax3(t0, f(c), f(c + 1));
                     t1 = fmax3(t1, f(c + 2), f(c + 3));
                     t2 = fmax3(t2, f(c + 4), f(c + 5));
                     t3 = fmax3(t3, f(c + 6), f(c + 7));
                 }
-                t0 = fmax3(t0, f(124), f(125));
-                t1 = fmax3(t1, f(126), f(127));
+                t0 = fmax3(t0, f(60), f(61));
+                t1 = fmax3(t1, f(62), f(63));
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 64; c < 128; ++c) asm volatile("" : "+r"(s[c >> 5][c & 31]));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->s_empty[stage]);
+                // the stage's step before is done: O holds still, and its weights' place is free
+                const bool ready = turn == 0 || mbar_test(&bars->p_empty[stage], (turn - 1) & 1);
+#pragma unroll
+                for (int c = 64; c < 128; c += 8) {
+                    t0 = fmax3(t0, f(c), f(c + 1));
+                    t1 = fmax3(t1, f(c + 2), f(c + 3));
+                    t2 = fmax3(t2, f(c + 4), f(c + 5));
+                    t3 = fmax3(t3, f(c + 6), f(c + 7));
+                }
                 const float top = fmaxf(fmax3(t0, t1, t2), t3) * mul;
                 const bool move = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
-                const float m_new = move ? top : m;
-                const float back = move && m > -INFINITY ? exp2_approx(m - m_new) : 1.0f;
-                m = m_new;
-                const float ref = m == -INFINITY ? 0.0f : m;
-                // the stage's step before is done: O holds still, and its weights' place is free
-                if (turn > 0) wait(&bars->p_empty[stage], (turn - 1) & 1);
-                tc_fence_after();
-                if (x > mine && __any_sync(0xffffffffu, back != 1.0f)) {
+                if (__any_sync(0xffffffffu, move || !ready)) {
+                    if (turn > 0) wait(&bars->p_empty[stage], (turn - 1) & 1);
+                    tc_fence_after();
+                    const float back = move && m > -INFINITY ? exp2_approx(m - top) : 1.0f;
+                    if (x > mine && __any_sync(0xffffffffu, back != 1.0f)) {
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld_x16(out + c, o);
-                        tmem_ld_wait();
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld_x16(out + c, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * back);
-                        tmem_st_x16(out + c, o);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * back);
+                            tmem_st_x16(out + c, o);
+                        }
                     }
+                    l *= back;
+                    if (move) m = ref = top;
                 }
+                tc_fence_after();
                 // The weights are rounded to bf16, by up to 2^-8 of each: the second product's
                 // operands have one type, and the values are bf16.  Their sum stays in fp32, unrounded.
                 // Sixteen at a time go through the same operation: written value by value, the order
@@ -678,7 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_st_x32(weights + h * 32, p);
                 }
-                l = l * back + ((sum[0] + sum[2]) + (sum[1] + sum[3]));
+                l += ((sum[0] + sum[2]) + (sum[1] + sum[3]));
+                next = mbar_test(&bars->s_full[stage], (turn + 1) & 1);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -727,14 +764,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int mine = (n & 1) ^ stage;  // the stage's first step
                 const uint32_t query = queries + (wide ? mine : 0);
                 for (uint32_t q = queries; q < queries + (wide ? 2 : 1); ++q) {
-                    wait(&bars->q_full[q & 1], (q >> 1) & 1);
-                    if ((wide ? q != query : mine >= steps) && lane == 0) mbar_arrive(&bars->q_empty[q & 1]);
+                    wait(&bars->q_full[q % S::kQueryStages], (q / S::kQueryStages) & 1);
+                    if ((wide ? q != query : mine >= steps) && lane == 0)
+                        mbar_arrive(&bars->q_empty[q % S::kQueryStages]);
                     __syncwarp();
                 }
                 if (!wide && mine == 1) pass();
 #pragma unroll 1
                 for (int x = mine; x < steps; x += 2) {
-                    const uint64_t qd = desc_add_bytes(q_desc, uniform(query & 1) * S::kBytes);
+                    const uint64_t qd = desc_add_bytes(q_desc, uniform(query % S::kQueryStages) * S::kBytes);
                     const uint64_t kd = desc_add_bytes(k_desc, uniform(at.stage) * S::kBytes);
                     wait(&bars->k_full[at.stage], at.phase);
                     // the scores that were in the place before have been read
@@ -743,12 +781,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
 #pragma unroll 1
                     for (int kb = 0; kb < DB; ++kb)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16_elect(d, desc_add_bytes(qd, kb * 16384 + k * 32),
-                                           desc_add_bytes(kd, kb * 1024 + k * 32), id, (kb | k) != 0 ? 1u : 0u);
+                        mma4_bf16_elect<2, 2>(d, desc_add_bytes(qd, kb * 16384), desc_add_bytes(kd, kb * 1024), id, kb);
                     mma_commit_elect(&bars->s_full[stage]);
-                    if (x + 2 >= steps) mma_commit_elect(&bars->q_empty[query & 1]);
+                    if (x + 2 >= steps) mma_commit_elect(&bars->q_empty[query % S::kQueryStages]);
                     mma_commit_elect(&bars->k_empty[at.stage]);
                     at.next(S::kKeyStages);
                     if (!wide && x + 1 < steps) pass();
@@ -770,7 +805,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool odd = wide && (x & 1);
                     const uint64_t vd = desc_add_bytes(v_desc, uniform(at.stage) * S::kBytes);
                     const uint32_t d = tmem + S::out_col(stage), p = tmem + kWeightCol + stage * 64;
-                    const uint32_t keep = uniform(x < 2 ? 0u : 1u);
                     if (!odd) wait(&bars->v_full[at.stage], at.phase);
                     if (x < 2) {
                         wait(&bars->o_empty[stage], empty_phase >> stage & 1);
@@ -779,12 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait(&bars->p_full[stage], (n >> 1) & 1);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 16 keys: two atoms of each block
-                            mma_bf16_ts_elect(d, p + 32 * h + 8 * k,
-                                              desc_add_bytes(vd, (h * 4 + k) * 2 * DB * 1024), id,
-                                              (h | k) != 0 ? 1u : keep);
+                    for (int h = 0; h < 2; ++h)  // 16 keys: two atoms of each block
+                        mma4_bf16_ts_elect<DB * 128>(d, p + 32 * h, desc_add_bytes(vd, h * 8 * DB * 1024), id,
+                                                     (x >> 1) | h);
                     mma_commit_elect(&bars->p_empty[stage]);
                     if (x + 2 >= steps) mma_commit_elect(&bars->o_full[stage]);
                     if (!wide || odd) {
@@ -847,8 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto load_queries = [&]() -> bool {
             const int subs = w.tokens > a.tile_tokens ? 2 : 1;
             for (int sub = 0; sub < subs; ++sub, ++queries) {
-                const uint32_t q = queries & 1;
-                if (!issue_wait(&bars->q_empty[q], ((queries >> 1) & 1) ^ 1)) return false;
+                const uint32_t q = queries % S::kQueryStages;
+                if (!issue_wait(&bars->q_empty[q], ((queries / S::kQueryStages) & 1) ^ 1)) return false;
                 const int32_t token0 = w.token0 + sub * a.tile_tokens;
                 const bool one = w.tokens - sub * a.tile_tokens == 1;
                 if (lane == 0)
@@ -876,7 +907,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && publish()) {
                 const Masked masks(a, w.r.len + w.token0, w.tokens);
                 const int32_t lead = w.gap > 0 ? a.sink_tiles : INT32_MAX;
-                ok = load_queries();
+                const int before = max(w.x1 - S::kBeforeQueries, w.x0);  // the last tile before the queries
+                if (S::kBeforeQueries == 0) ok = load_queries();
                 for (int x = w.x1 - 1; ok && x >= w.x0; --x) {
                     const int32_t kt = x >= lead ? x + w.gap : x;
                     const int64_t pos = static_cast<int64_t>(kt) * kTile + lane * slots;
@@ -901,6 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_5d(sV + vpos.stage * S::kBytes + box, &maps.v, bar, 0, 0, w.head * DB,
                                     place.slot >> 3, place.page);
                     vpos.next(S::kValueStages);
+                    if (S::kBeforeQueries > 0 && x == before) ok = load_queries();
                 }
             }
         } else {
@@ -1024,9 +1057,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = end_wait(&bars->v_own[at], (own_phase >> at) & 1);
                     if (!ok) break;
                     own_phase ^= 1u << at;
-                    const int64_t end = p.pos + p.tokens - static_cast<int64_t>(kt) * kTile;
+                    // the key of the lane's row, and whether any token attends it, and all
+                    const int64_t key = static_cast<int64_t>(kt) * kTile + row, last = p.pos + p.tokens - 1;
+                    const bool sink = a.window == 0 || key < a.sinks;
+                    const uint32_t none =
+                        __ballot_sync(0xffffffffu, key > last || !(sink || key > p.pos - a.window));
+                    const uint32_t all = __ballot_sync(0xffffffffu, key <= p.pos && (sink || key > last - a.window));
                     const uint32_t of = turn == 1 ? following : number;
-                    if (look_through<DB>(smem_u32(sV) + at * S::kBytes, warp & 3, end) && lane == 0)
+                    if (look_through<DB>(smem_u32(sV) + at * S::kBytes, warp & 3, none, all) && lane == 0)
                         *const_cast<volatile uint32_t*>(&bars->nonfinite[of & 3]) = of;
                     fence_proxy_async_smem();
                     __syncwarp();
