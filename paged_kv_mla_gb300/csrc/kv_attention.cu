@@ -23,10 +23,25 @@
 //
 // Roles of a CTA: warps 0-3 and 4-7 the softmax of a stage, 8 and 9 the MMAs of a stage's scores,
 // 10 those of both stages' values, 11 the schedule and all loads, 12-15 the epilogue; these also
-// look values through for infinities and NaN where not every row attends every key, since a zero
-// weight must not meet them.  Scores are kept in base 2; the running maximum moves only when a
-// row's new maximum exceeds it by 2^8, since any reference works as long as nothing overflows, so
-// O is hardly ever rescaled.
+// ready values where not every row attends every key, since a zero weight must not meet infinities
+// and NaN: rows that no token attends are cleared, others looked through.  Scores are kept in base 2;
+// the running maximum moves only when a row's new maximum exceeds it by 2^8, since any reference
+// works as long as nothing overflows, so O is hardly ever rescaled (by every new maximum, prompts
+// and windows take 11 to 12 % longer).
+//
+// Bytes: every key and value of the cache once a request and head of keys and per 256 rows of
+// queries, these and the output once.  Measured on a GB300 (6 781 GB/s of a copy, 1 888 TFLOP/s of a
+// matrix product, both measured), whole calls:
+//   4 requests x 1 token, 32 heads of 8, D = 128, 65 536 keys: 164 us, 6.55 TB/s, bound by HBM;
+//   64 x 1 token, 512 to 4096 keys: 105 us, 5.7 TB/s, HBM and the calls' start and join;
+//   1 x 2048 tokens behind 16 384: 370 us, 1.58 PFLOP/s, alone, 396 us and 1.48 PFLOP/s one call after
+//     another, when the power limit lowers the clock.  A step (128 x 128 scores of a stage) takes
+//     1 450 cycles, of which its 16 MMAs take 1 024 and without the softmax 1 205: one place for the
+//     scores of both stages, the chain from scores to weights, and shared memory's bandwidth, which
+//     products with both operands there use up;
+//   2 x 2048 to 4096 tokens, 64 heads of 8, D = 64, the last 1024 keys and the first 4: 199 us.  A
+//     step takes 1 090 cycles, the exponentials 512 of them, an item's three tiles with masks
+//     about a fifth of its time and its start and end a sixth.
 #include <atomic>
 
 #include "kv_device.cuh"
@@ -1210,20 +1225,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
 constexpr int kJoinBlocks = 4;  // of an SM
-constexpr int kJoinRows = 2;    // that a warp joins at a time
+// Rows that a lane joins at a time (with 4, which spill, small ragged chunks take 10 % longer, prompts
+// and single tokens in a window 3 to 5 %).
+constexpr int kJoinRows = 2;
 // Parts that a warp joins alone, and of items of few rows, whose blocks have nothing else to do.
 constexpr int kFewParts = 8, kFewRows = 8, kFewPartsOfFewRows = 2;
 
 // Joins the parts of the items that several CTAs share: with M the largest of the parts' maxima,
-// out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same order.  A warp takes
-// two rows, a lane four columns of one or both of them; rows of many parts are taken one by one by
-// the warps of a block, which share the parts.  Bound by latency, so several rows are on their way.
+// out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, the parts always in the same order.  A lane takes
+// four columns of two rows, a warp two or, with D = 64, four rows (of items of few rows two); rows of
+// many parts are taken one by one by the warps of a block, which share the parts.  The sums are still
+// in L2.  Bound by latency with few rows (7 us by itself, most of it before the launch's end) and by
+// its instructions where every CTA leaves 256 rows of an item (39 000 rows of two parts: 14 us).
 template <int DB>
 __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
     kv_join_kernel(const KvAttentionArgs a, const KvWorkspace ws, const int ctas) {
     constexpr int D = DB * 64;
     constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;  // lanes of a row, rows of a load
-    constexpr int kEach = kJoinRows / kAtOnce;            // rows of a lane
+    const auto task_rows = [](int rows) -> int { return rows > kFewRows ? kJoinRows * kAtOnce : 2; };
     __shared__ KvItem items[kKvMaxCtas];
     __shared__ int begins[2][kKvMaxCtas + 1];  // tasks of items of few parts, and of many
     __shared__ float4 sums[kJoinWarps][32];
@@ -1245,7 +1264,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
                 if (warp == 0) items[p] = it;
                 const int rows = it.tokens * group;
                 const bool many = it.parts > (rows > kFewRows ? kFewParts : kFewPartsOfFewRows);
-                if (many == (warp == 1)) n[k] = many ? rows : (rows + kJoinRows - 1) / kJoinRows;
+                if (many == (warp == 1)) n[k] = many ? rows : (rows + task_rows(rows) - 1) / task_rows(rows);
             }
             sum += n[k];
         }
@@ -1281,7 +1300,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
         int32_t slot;   // and of a part
     };
     const auto place = [&](const KvItem& it, int row) -> Row {
-        const int token = row / group, head = row - token * group, sub = token / a.tile_tokens;
+        const int token = row / group, head = row - token * group, sub = token >= a.tile_tokens ? 1 : 0;
         return Row{(it.row + token) * a.num_heads + it.head + head,
                    sub * kTile + (token - sub * a.tile_tokens) * group + head};
     };
@@ -1294,8 +1313,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         __device__ __forceinline__ void add(float2 s, float4 v) {
             const float m = fmaxf(top, s.x);
-            const float f0 = top == -INFINITY ? 0.0f : exp2f(top - m);
-            const float f1 = s.x == -INFINITY ? 0.0f : exp2f(s.x - m);
+            const float f0 = top == -INFINITY ? 0.0f : exp2_approx(top - m);
+            const float f1 = s.x == -INFINITY ? 0.0f : exp2_approx(s.x - m);
             top = m;
             total = total * f0 + s.y * f1;
             o = make_float4(o.x * f0 + v.x * f1, o.y * f0 + v.y * f1, o.z * f0 + v.z * f1, o.w * f0 + v.w * f1);
@@ -1312,26 +1331,29 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
     for (int f = blockIdx.x * kJoinWarps + warp; f < begins[0][ctas]; f += gridDim.x * kJoinWarps) {
         const int p = find(begins[0], f);
         const KvItem it = items[p];
-        const int row0 = (f - begins[0][p]) * kJoinRows + lane / kLanes, rows = it.tokens * group;
-        Sum x[kEach];
-        Row r[kEach];
+        const int rows = it.tokens * group, each = task_rows(rows);
+        const int row0 = (f - begins[0][p]) * each + lane / kLanes;
+        Sum x[kJoinRows];
+        Row r[kJoinRows];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) r[i] = place(it, min(row0 + i * kAtOnce, rows - 1));
+        for (int i = 0; i < kJoinRows; ++i) r[i] = place(it, min(row0 + i * kAtOnce, rows - 1));
         for (int k = 0; k < it.parts; ++k) {
-            float2 s[kEach];
-            float4 v[kEach];
+            float2 s[kJoinRows];
+            float4 v[kJoinRows];
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
+            for (int i = 0; i < kJoinRows; ++i) {
+                if (i * kAtOnce >= each) break;
                 const int64_t at = slot(p, k) + r[i].slot;
                 s[i] = __ldcg(stats + at);
                 v[i] = __ldcg(reinterpret_cast<const float4*>(parts + at * D + col));
             }
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) x[i].add(s[i], v[i]);
+            for (int i = 0; i < kJoinRows; ++i)
+                if (i * kAtOnce < each) x[i].add(s[i], v[i]);
         }
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (row0 + i * kAtOnce < rows) finish(x[i], r[i].out);
+        for (int i = 0; i < kJoinRows; ++i)
+            if (i * kAtOnce < each && row0 + i * kAtOnce < rows) finish(x[i], r[i].out);
     }
     for (int f = blockIdx.x; f < begins[1][ctas]; f += gridDim.x) {
         const int p = find(begins[1], f);
