@@ -32,14 +32,14 @@
 // Bytes: every key and value of the cache once a request and head of keys and per 256 rows of
 // queries, these and the output once.  Measured on a GB300 (6 781 GB/s of a copy, 1 888 TFLOP/s of a
 // matrix product, both measured), whole calls:
-//   4 requests x 1 token, 32 heads of 8, D = 128, 65 536 keys: 164 us, 6.55 TB/s, bound by HBM;
+//   4 requests x 1 token, 32 heads on 8 of keys, D = 128, 65 536 keys: 164 us, 6.55 TB/s, bound by HBM;
 //   64 x 1 token, 512 to 4096 keys: 105 us, 5.7 TB/s, HBM and the calls' start and join;
 //   1 x 2048 tokens behind 16 384: 370 us, 1.58 PFLOP/s, alone, 396 us and 1.48 PFLOP/s one call after
 //     another, when the power limit lowers the clock.  A step (128 x 128 scores of a stage) takes
 //     1 450 cycles, of which its 16 MMAs take 1 024 and without the softmax 1 205: one place for the
 //     scores of both stages, the chain from scores to weights, and shared memory's bandwidth, which
 //     products with both operands there use up;
-//   2 x 2048 to 4096 tokens, 64 heads of 8, D = 64, the last 1024 keys and the first 4: 199 us.  A
+//   2 x 2048 to 4096 tokens, 64 heads on 8, D = 64, the last 1024 keys and the first 4: 199 us.  A
 //     step takes 1 090 cycles, the exponentials 512 of them, an item's three tiles with masks
 //     about a fifth of its time and its start and end a sixth.
 #include <atomic>
