@@ -684,7 +684,8 @@ pkm_status kv_matmul_paged_fp8(const void* hidden_state, const uint32_t* input_r
  *   q, k, v          device bf16, 16-byte aligned; element (row, head, column) at
  *                    row * row_stride + head * head_stride + column, strides in elements,
  *                    multiples of 8 (>= 0): heads of one projection's output can be given.
- *   num_heads        query heads; 0 (with q = NULL) turns keys alone.
+ *   num_heads        query heads; 0 (with q = NULL) turns keys alone.  A row's heads, num_heads +
+ *                    2 num_kv_heads, are at most 2^31 - 513.
  *   q_out            device bf16, 16-byte aligned, strides for which no two heads overlap.  It may
  *                    be q with the same strides (in place), and may not overlap it otherwise.
  *   head_size        D: a multiple of 8, at most 256; row_elems = num_kv_heads * D.
@@ -744,7 +745,7 @@ size_t kv_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
  *   head_size       64 or 128; row_elems = num_kv_heads * head_size.
  *   softmax_scale   finite.
  *   kv_cache        cache_lengths required; kv_stride >= row_elems.
- *   out             device bf16 [total_rows, num_heads, head_size], 16-byte aligned.
+ *   out             device bf16 [total_rows, num_heads, head_size], 16-byte aligned, apart from q.
  *   lse             device fp32 [total_rows, num_heads], or NULL.
  *   workspace       device, >= kv_attention_paged_workspace_size(...) bytes, 256-byte aligned.
  * A position past the page-table row or in a page id >= num_pages sets PKM_ERR_OUT_OF_RANGE in
@@ -780,9 +781,10 @@ pkm_status kv_window_attention_paged(const void* q, int64_t q_row_stride, int64_
 /*
  * Checks without a launch (no counterpart on the pages).  Until it is called with 0, calls of this
  * thread to mla_tree_attention_paged, mla_rope_heads, mla_cache_write_paged,
- * mla_cache_compact_paged, kv_rope_paged, kv_attention_paged and their variants make their host checks alone: what these find, or
- * PKM_ERR_CUDA where the call would go on to the GPU.  For callers that know more of an argument
- * than its address, a tensor in host memory say, and must not launch with it.
+ * mla_cache_compact_paged, kv_rope_paged, kv_attention_paged and their variants make their host
+ * checks alone: what these find, or PKM_ERR_CUDA where the call would go on to the GPU.  For callers
+ * that know more of an argument than its address, a tensor in host memory say, and must not launch
+ * with it.
  */
 void pkm_checks_only(int32_t on);
 

@@ -1452,8 +1452,8 @@ pkm_status kv_rope_paged(const void* q, int64_t q_row_stride, int64_t q_head_str
     if (rope_dim > head_size) return PKM_ERR_INVALID_ARG;
     if (head_size % 8 != 0 || head_size > 256 || rope_dim % 8 != 0 || num_axes > 4)
         return PKM_ERR_UNSUPPORTED;
-    // a thread counts its heads, up to 512 behind the last, in 32 bits
-    if (num_heads > INT32_MAX - 512) return PKM_ERR_UNSUPPORTED;
+    // a thread counts the heads of a row, up to 512 behind the last, in 32 bits
+    if (num_heads + 2 * static_cast<int64_t>(num_kv_heads) > INT32_MAX - 512) return PKM_ERR_UNSUPPORTED;
     if (num_heads > 0 &&
         !heads_apart(total_rows, num_heads, head_size, q_out_row_stride, q_out_head_stride))
         return PKM_ERR_INVALID_ARG;

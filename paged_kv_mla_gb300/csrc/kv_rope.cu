@@ -8,17 +8,18 @@
 //     (x0, x1) -> (x0 c - x1 s, x0 s + x1 c)     in fp32, rounded once to bf16,
 // pair j being columns (2j, 2j + 1) or (j, j + P/2).  Columns past the first P are copied.
 //
-// A streaming kernel: every value once in and once out.  An item is one row and a group of
-// its heads (queries, or keys and then values); a thread has a unit of eight columns, which
+// A streaming kernel: every value once in and once out.  An item is one row and a group of its
+// heads, in the line of queries, keys and values; a thread has a unit of eight columns, which
 // holds four whole pairs, keeps their factors in registers and walks over heads, four loads in
 // flight.  The columns are asked for before the row's position and slot, which hang on a chain
 // of loads (offsets, length, page id).
 //
 // Bound by the latency of those chains and by how many blocks an SM holds: 5 000 rows of 32 heads of
-// queries and 8 of keys and values, D = 128, three axes (126 MB) take 29 us, 4.3 TB/s.  Blocks that
+// queries and 8 of keys and values, D = 128, three axes (126 MB) take 27 us, 4.7 TB/s.  Blocks that
 // stay and walk over items (39 us with one item a block), all positions of a row loaded at once and
-// divisions by multiplication make it so; 9 to 12 blocks an SM instead of 8 take 29 to 31 us, two
-// heads in flight instead of four 33 to 42.  37 rows take what a call takes from the host, 12 us.
+// divisions by multiplication make it so.  Blocks an SM: 8 take 30.5 us, 9 28.7, 11 and 12, which
+// spill, 32; heads in flight: three 27.3 us, two 31, six (7 blocks) 28.9.  37 rows take what a call
+// takes from the host, 12 us.
 #include "pkm_device.cuh"
 #include "kv_internal.h"
 
@@ -27,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kUnroll = 4;  // heads of an item a thread has
-constexpr int kBlocks = 8;  // of an SM, all resident
+constexpr int kBlocks = 10;  // of an SM, all resident
 
 // Columns of a turned unit: 16 bytes in the interleaved layout, twice 8 bytes (four columns of
 // each half) in the half layout; copied units are 16 bytes in both.
@@ -89,9 +90,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_rope_kernel(const KvRope
     const int heads_per_pass = kThreads / units;
     const int u = threadIdx.x % units, h_in = threadIdx.x / units;
     const int group = heads_per_pass * kUnroll;
-    const int q_groups = (a.num_heads + group - 1) / group;
-    const int kv_heads = a.num_kv_heads * (a.v != nullptr ? 2 : 1);
-    const int groups = q_groups + (kv_heads + group - 1) / group;
+    // the line of a row's heads: queries, keys, values
+    const int first_value = a.num_heads + a.num_kv_heads;
+    const int heads = first_value + (a.v != nullptr ? a.num_kv_heads : 0);
+    const int groups = (heads + group - 1) / group;
     const bool turns = u * 8 < a.rope_dim;
     const int col = HALF && turns ? u * 4 : u * 8;
     const int second = HALF && turns ? a.rope_dim / 2 : 0;
@@ -100,30 +102,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_rope_kernel(const KvRope
     const uint32_t rows = static_cast<uint32_t>(a.total_rows);
     const uint32_t covered = __ldg(a.row_offsets), behind = __ldg(a.row_offsets + a.batch);
 
-    struct Item {
-        int64_t r;
-        int h0, heads;  // the thread's first head, and behind the last
-        bool queries;
-    };
-    const auto item = [&](uint32_t r, int g) -> Item {
-        const bool queries = g < q_groups;
-        return Item{r, (queries ? g : g - q_groups) * group + h_in, queries ? a.num_heads : kv_heads, queries};
-    };
-    // values are copied in whole units; the half layout's places are for turned heads
-    const auto is_value = [&](const Item& x, int h) { return !x.queries && h >= a.num_kv_heads; };
-    const auto load = [&](const Item& x, uint4 (&v)[kUnroll]) {
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int h = x.h0 + i * heads_per_pass;
-            if (!in_use || h >= x.heads) continue;
-            if (is_value(x, h))
-                v[i] = load_unit(a.v + x.r * a.v_row_stride + (h - a.num_kv_heads) * a.v_head_stride + u * 8, 0);
-            else if (x.queries)
-                v[i] = load_unit(a.q + x.r * a.q_row_stride + h * a.q_head_stride + col, second);
-            else if (a.k != nullptr)
-                v[i] = load_unit(a.k + x.r * a.k_row_stride + h * a.k_head_stride + col, second);
-        }
-    };
     // a block's items are gridDim.x apart in the line of all rows' groups of heads
     const int step = static_cast<int>(gridDim.x % groups);
     int g = static_cast<int>(blockIdx.x % groups) - step;
@@ -136,15 +114,26 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_rope_kernel(const KvRope
             ++it;
         }
         if (it >= rows) break;
-        const Item x = item(it, g);
+        const int64_t r = it;
+        const int h0 = g * group + h_in;
         uint4 v[kUnroll];
-        load(x, v);
+        const uint16_t* q = a.q + r * a.q_row_stride + col;
+        const uint16_t* k = a.k + r * a.k_row_stride + col;
+        const uint16_t* values = a.v + r * a.v_row_stride + u * 8;  // copied in whole units
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int h = h0 + i * heads_per_pass;
+            if (!in_use || h >= heads) continue;
+            if (h < a.num_heads) v[i] = load_unit(q + h * a.q_head_stride, second);
+            else if (h >= first_value) v[i] = load_unit(values + (h - first_value) * a.v_head_stride, 0);
+            else if (a.k != nullptr) v[i] = load_unit(k + (h - a.num_heads) * a.k_head_stride, second);
+        }
         // all positions at once; the factors do not wait for the row's request
         uint32_t pos[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-            pos[n] = n < a.num_axes ? __ldg(a.positions + static_cast<int64_t>(n) * a.total_rows + x.r) : 0;
-        bool inside = max(max(pos[0], pos[1]), max(pos[2], pos[3])) < static_cast<uint32_t>(a.max_seq_len);
+            pos[n] = n < a.num_axes ? __ldg(a.positions + static_cast<int64_t>(n) * a.total_rows + r) : 0;
+        const bool inside = max(max(pos[0], pos[1]), max(pos[2], pos[3])) < static_cast<uint32_t>(a.max_seq_len);
         float cs[8] = {};
         if (inside && turns) {
             const auto factors = [&](uint32_t axis) -> const float* {
@@ -158,57 +147,59 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_rope_kernel(const KvRope
                 cs[4] = f1.x, cs[5] = f1.y, cs[6] = f1.z, cs[7] = f1.w;
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = __ldg(reinterpret_cast<const float2*>(factors(axes >> (2 * k) & 3u)) + k);
-                    cs[2 * k] = f.x;
-                    cs[2 * k + 1] = f.y;
+                for (int n = 0; n < 4; ++n) {
+                    const float2 f = __ldg(reinterpret_cast<const float2*>(factors(axes >> (2 * n) & 3u)) + n);
+                    cs[2 * n] = f.x;
+                    cs[2 * n + 1] = f.y;
                 }
             }
         }
         if (it < covered || it >= behind) continue;  // of no request
-        int64_t slot = 0;
-        if (!x.queries) {
-            const int b = request_of(a.row_offsets, a.batch, it);
-            if (b < 0) continue;
-            const uint64_t at = static_cast<uint64_t>(__ldg(a.cache_lengths + b)) + (it - __ldg(a.row_offsets + b));
-            // at / page_size for positions below 2^33: off by less than 2^-31 before rounding down
-            const uint64_t lp = a.page_inverse == 0 ? at : __umul64hi(at, a.page_inverse);
-            uint32_t page = UINT32_MAX;
-            if (lp < static_cast<uint64_t>(a.max_pages))
-                page = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
-            if (page < static_cast<uint32_t>(a.num_pages))
-                slot = static_cast<int64_t>(page) * a.page_stride +
-                       static_cast<int64_t>(at - lp * a.page_size) * a.slot_stride;
-            else
-                inside = false;
-        }
         if (!inside) {
             if (threadIdx.x == 0) report(a.status, PKM_ERR_OUT_OF_RANGE);
             continue;
         }
+        uint16_t* cell = nullptr;  // the row's slot
+        if (g * group + group > a.num_heads) {
+            const int b = request_of(a.row_offsets, a.batch, it);
+            if (b >= 0) {
+                const uint64_t at = static_cast<uint64_t>(__ldg(a.cache_lengths + b)) + (it - __ldg(a.row_offsets + b));
+                // at / page_size for positions below 2^33: off by less than 2^-31 before rounding down
+                const uint64_t lp = a.page_inverse == 0 ? at : __umul64hi(at, a.page_inverse);
+                uint32_t page = UINT32_MAX;
+                if (lp < static_cast<uint64_t>(a.max_pages))
+                    page = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
+                if (page < static_cast<uint32_t>(a.num_pages))
+                    cell = a.cache_layer + static_cast<int64_t>(page) * a.page_stride +
+                           static_cast<int64_t>(at - lp * a.page_size) * a.slot_stride;
+                else if (threadIdx.x == 0)
+                    report(a.status, PKM_ERR_OUT_OF_RANGE);
+            }
+        }
         if (!in_use) continue;
-        const bool from_cache = !x.queries && a.k == nullptr;  // keys, turned in place
-        if (from_cache) {
+        uint16_t* q_out = a.q_out + r * a.q_out_row_stride + col;
+        if (a.k == nullptr && cell != nullptr && turns) {  // keys, turned in place
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
-                const int h = x.h0 + i * heads_per_pass;
-                if (h < x.heads && !is_value(x, h) && turns)
-                    v[i] = load_unit(a.cache_layer + slot + h * a.head_size + col, second);
+                const int h = h0 + i * heads_per_pass;
+                if (h >= a.num_heads && h < first_value)
+                    v[i] = load_unit(cell + (h - a.num_heads) * a.head_size + col, second);
             }
         }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const int h = x.h0 + i * heads_per_pass;
-            if (h >= x.heads) continue;
-            if (is_value(x, h)) {
-                uint16_t* to = a.cache_layer + slot + a.kv_stride + (h - a.num_kv_heads) * a.head_size;
-                store_unit(to + u * 8, 0, v[i]);
+            const int h = h0 + i * heads_per_pass;
+            if (h >= heads) continue;
+            if (h >= first_value) {
+                if (cell != nullptr)
+                    store_unit(cell + a.kv_stride + (h - first_value) * a.head_size + u * 8, 0, v[i]);
                 continue;
             }
-            uint16_t* to = x.queries ? a.q_out + x.r * a.q_out_row_stride + h * a.q_out_head_stride
-                                     : a.cache_layer + slot + h * a.head_size;
-            if (turns) store_unit(to + col, second, turned<HALF>(v[i], cs));
-            else if (x.queries ? a.q != a.q_out : !from_cache) store_unit(to + col, 0, v[i]);
+            const bool query = h < a.num_heads;
+            if (!query && cell == nullptr) continue;
+            uint16_t* to = query ? q_out + h * a.q_out_head_stride : cell + (h - a.num_heads) * a.head_size + col;
+            if (turns) store_unit(to, second, turned<HALF>(v[i], cs));
+            else if (query ? a.q != a.q_out : a.k != nullptr) store_unit(to, 0, v[i]);
         }
     }
 }
@@ -217,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_rope_kernel(const KvRope
 
 cudaError_t launch_kv_rope(KvRopeArgs args, int num_sms, cudaStream_t stream) {
     const int group = kThreads / (args.head_size / 8) * kUnroll;
-    const int64_t kv_heads = static_cast<int64_t>(args.num_kv_heads) * (args.v != nullptr ? 2 : 1);
-    const int64_t groups = (args.num_heads + group - 1) / group + (kv_heads + group - 1) / group;
+    const int64_t heads = args.num_heads + static_cast<int64_t>(args.num_kv_heads) * (args.v != nullptr ? 2 : 1);
+    const int64_t groups = (heads + group - 1) / group;
     const int64_t items = args.total_rows * groups, most = static_cast<int64_t>(num_sms) * kBlocks;
     unsigned blocks = static_cast<unsigned>(items < most ? items : most);
     if (items > most && most % groups == 0) --blocks;  // all blocks meet all groups of heads

@@ -199,6 +199,26 @@ def test_a_padded_batch():
     assert_kv_close(p, out, lse)
 
 
+def test_rows_of_no_request():
+    """Offsets that cover no row at all: nothing is written or reported."""
+    import paged_kv_mla_gb300 as pkm
+    p = make_kv(41, [30, 9], [5, 2], 8, 2, 64, 16)
+    d = DeviceKv(p)
+    for at in (0, 7, 3):
+        d.offsets.fill_(at)
+        d.run()
+        pkm.kv_rope_paged(d.offsets, torch.zeros(7, dtype=torch.int32, device="cuda"),
+                          torch.zeros(1, 64, device="cuda"), d.desc, p.layer, 2, q=d.q, q_out=d.out, dev_status=d.status)
+    out, lse, status = d.results()
+    assert status == 0 and (out == OUT_FILL).all() and (lse == LSE_FILL).all()
+    assert torch.equal(d.cache, DeviceKv(p).cache)
+
+
+@pytest.mark.parametrize("page", [1, 5, 8])
+def test_windows_over_small_pages(page):
+    check(make_kv(42, [700, 0, 90], [40, 3, 1], 8, 2, 64, page, window=150, sinks=9))
+
+
 def test_requests_on_the_same_pages():
     """A common beginning, and one request twice."""
     p = make_kv(38, [100, 100, 64], [20, 20, 40], 8, 2, 128, 16)

@@ -184,6 +184,17 @@ def test_rope_sizes_and_planes(pkm):
     assert rope(pkm, cache(pkm), q=a, q_out=b) == INVALID
 
 
+def test_rope_heads_of_a_row_are_counted(pkm):
+    import paged_kv_mla_gb300 as m
+    cs = cache(pkm).c_struct()
+    t = b16(3 * 8 * 128)
+    f = torch.zeros(16, 128)
+    rest = [t.data_ptr(), 512, 128, t.data_ptr(), 512, 128, 4, 128, 128, i32(3).data_ptr(), 2, 1, i32(3).data_ptr(), 1,
+            None, f.data_ptr(), 16, 0, ctypes.byref(cs), 0, None, None]
+    for heads, status in ((2 ** 31 - 513 - 8, GOES_ON), (2 ** 31 - 512 - 8, UNSUPPORTED), (2 ** 31 - 1, UNSUPPORTED)):
+        assert m._lib.kv_rope_paged(t.data_ptr(), heads * 128, 128, heads, t.data_ptr(), heads * 128, 128, *rest) == status
+
+
 def test_nothing_to_do(lib):
     """No rows, or no requests: fine, and nothing is launched (nor is there a GPU)."""
     c = cache(lib)
