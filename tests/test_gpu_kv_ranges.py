@@ -219,6 +219,13 @@ def test_windows_over_small_pages(page):
     check(make_kv(42, [700, 0, 90], [40, 3, 1], 8, 2, 64, page, window=150, sinks=9))
 
 
+@pytest.mark.parametrize("size", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (130, 0), (300, 200), (1, 129)])
+def test_heads_of_their_own_keys(size, window, sinks):
+    """128 tokens a tile of queries, 256 an item, whose diagonal and edge lie in three tiles each."""
+    check(make_kv(43, [126, 300, 1000], [770, 257, 129], 3, 3, size, 32, window=window, sinks=sinks))
+
+
 def test_requests_on_the_same_pages():
     """A common beginning, and one request twice."""
     p = make_kv(38, [100, 100, 64], [20, 20, 40], 8, 2, 128, 16)
