@@ -857,6 +857,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!issue_wait(&bars->part_empty[at], ((parts / kParts) & 1) ^ 1)) return false;
             ++parts;
             more = __any_sync(0xffffffffu, w.next(a));
+            int left = 0;
+            if (more && w.x0 == 0 && w.x1 < w.tiles) {
+                // those behind this CTA whose shares begin before the item's end: floor(units c / sharing) < end
+                const int64_t end = (w.u + (w.units_each - w.at)) * sharing, units = bars->units;
+                uint32_t begin = ~0u;
+                left = 1;
+                for (int64_t c = blockIdx.x + 1 + lane; begin == ~0u; c += 32) {
+                    begin = __ballot_sync(0xffffffffu, c < sharing && units * c < end);
+                    left += __popc(begin);
+                }
+            }
             if (lane == 0) {
                 Part* p = &bars->part[at];
                 p->x0 = p->x1 = 0;
@@ -873,11 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p->gap = w.gap;
                     p->wide = wide;
                     p->whole = w.x0 == 0 && w.x1 == w.tiles;
-                    p->left = 0;
-                    if (w.x0 == 0 && w.x1 < w.tiles) {
-                        const int64_t end = w.u + (w.units_each - w.at);
-                        p->left = static_cast<int32_t>(quotient(end * sharing - 1, bars->units) - blockIdx.x) + 1;
-                    }
+                    p->left = left;
                     for (int i = 0; i < 2; ++i) {
                         const Masked m(a, p->pos + i * a.tile_tokens,
                                        min(a.tile_tokens, w.tokens - i * a.tile_tokens));

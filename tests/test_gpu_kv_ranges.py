@@ -226,6 +226,39 @@ def test_heads_of_their_own_keys(size, window, sinks):
     check(make_kv(43, [126, 300, 1000], [770, 257, 129], 3, 3, size, 32, window=window, sinks=sinks))
 
 
+def test_a_million_tokens_each():
+    """512 requests of 2^20 tokens on one page: 33 million tiles of keys, whose line is cut with 64-bit
+    products.  The page's keys count 8192 times each, so the weights are the page's."""
+    import paged_kv_mla_gb300 as pkm
+    n, heads, size, page, times = 512, 8, 64, 128, 8192
+    gen = torch.Generator(device="cuda").manual_seed(44)
+    cache = torch.randn(1, 2, page, heads * size, device="cuda", generator=gen).bfloat16()
+    q = torch.randn(n, heads, size, device="cuda", generator=gen).bfloat16()
+    table = torch.zeros(n, times, dtype=torch.int32, device="cuda")
+    offsets = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    desc = pkm.PagedCache(data=cache, page_table=table, layer_stride=0, page_stride=0, kv_stride=page * heads * size,
+                          slot_stride=heads * size, num_layers=1, num_pages=1, page_size=page, row_elems=heads * size,
+                          cache_lengths=torch.full((n,), page * times - 1, dtype=torch.int32, device="cuda"))
+    out, lse = torch.zeros_like(q), torch.zeros(n, heads, device="cuda")
+    ws = torch.empty(pkm.kv_attention_paged_workspace_size(n, heads, heads, size), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkm.kv_attention_paged(q, offsets, size ** -0.5, desc, 0, out, ws, lse, status)
+    assert status.item() == 0
+    k, v = cache[0].double().view(2, page, heads, size)
+    s = torch.einsum("nhc,thc->nht", q.double(), k) * size ** -0.5
+    e = size * 2.0 ** -24 * (torch.einsum("nhc,thc->nht", q.double().abs(), k.abs()) * size ** -0.5).amax(-1)
+    w = s.softmax(-1)
+    ref, spread = torch.einsum("nht,thc->nhc", w, v), torch.einsum("nht,thc->nhc", w, v.abs())
+    # besides a short sum's errors: the running fp32 sum of a stage, which has every other tile, takes
+    # 16 keys at a time, 2^15 times, each at most 2^-23 off if the MMAs cut off; the weights' sum
+    # takes a tile at a time, rounded
+    long = 2.0 ** -8
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -12 + 2 * e[..., None] + 2 * long) * spread
+    assert ((out.double() - ref).abs() <= tol).all()
+    exact = torch.logsumexp(s, -1) + np.log(times)
+    assert ((lse.double() - exact).abs() <= e + long + 2.0 ** -20 * (1 + exact.abs())).all()
+
+
 def test_requests_on_the_same_pages():
     """A common beginning, and one request twice."""
     p = make_kv(38, [100, 100, 64], [20, 20, 40], 8, 2, 128, 16)
