@@ -53,8 +53,9 @@ namespace {
 constexpr int kScoreWarp = 8, kOutWarp = 10, kLoadWarp = 11, kEndWarp = 12;
 constexpr int kThreads = 16 * 32;
 // Registers of the two softmax groups, of the issuing and loading warps and of the epilogue, of the
-// 4 x 128 that the block starts with.
-constexpr int kStartRegs = 128, kSoftRegs = 176, kIssueRegs = 56, kEndRegs = 104;
+// 4 x 128 that the block starts with.  (An epilogue of 104, which spills, and a softmax of 176: 1 %
+// longer; a softmax of 160, which spills, prompts and windows 7 to 8 %; an epilogue of 88: prompts 7 %.)
+constexpr int kStartRegs = 128, kSoftRegs = 168, kIssueRegs = 64, kEndRegs = 112;
 static_assert(2 * kSoftRegs + kIssueRegs + kEndRegs <= 4 * kStartRegs, "registers of the block");
 constexpr int kTile = 128;          // keys of a tile, rows of a tile of queries
 constexpr int kMaxStages = 6;       // tiles of queries, keys or values in shared memory
