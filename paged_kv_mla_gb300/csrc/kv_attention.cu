@@ -34,12 +34,12 @@
 // matrix product, both measured), whole calls:
 //   4 requests x 1 token, 32 heads on 8 of keys, D = 128, 65 536 keys: 164 us, 6.55 TB/s, bound by HBM;
 //   64 x 1 token, 512 to 4096 keys: 105 us, 5.7 TB/s, HBM and the calls' start and join;
-//   1 x 2048 tokens behind 16 384: 370 us, 1.58 PFLOP/s, alone, 396 us and 1.48 PFLOP/s one call after
-//     another, when the power limit lowers the clock.  A step (128 x 128 scores of a stage) takes
+//   1 x 2048 tokens behind 16 384: 370 us, 1.58 PFLOP/s, alone, 393 us and 1.49 PFLOP/s one call after
+//     another, when the power limit lowers the clock (a matrix product then runs at 1.69).  A step (128 x 128 scores of a stage) takes
 //     1 450 cycles, of which its 16 MMAs take 1 024 and without the softmax 1 205: one place for the
 //     scores of both stages, the chain from scores to weights, and shared memory's bandwidth, which
 //     products with both operands there use up;
-//   2 x 2048 to 4096 tokens, 64 heads on 8, D = 64, the last 1024 keys and the first 4: 199 us.  A
+//   2 x 2048 to 4096 tokens, 64 heads on 8, D = 64, the last 1024 keys and the first 4: 195 us.  A
 //     step takes 1 090 cycles, the exponentials 512 of them, an item's three tiles with masks
 //     about a fifth of its time and its start and end a sixth.
 #include <atomic>
@@ -376,23 +376,31 @@ __device__ __forceinline__ void prefetch_tables(const KvAttentionArgs& a) {
     if (line < static_cast<int64_t>(a.batch) * a.max_pages) prefetch_l2(a.page_table + line);
 }
 
-// Page and slot of position pos of request b if it is read; page -1 (loads as zeros) if not and
-// for ids that the cache does not have, which are reported.
+// Page and slot of position pos of request b if it is read.  The page's number is on its way until
+// it is asked for: -1 (loads as zeros) if nothing is read and for ids that the cache does not have,
+// which are reported.
 struct Place {
-    int32_t page, slot;
-    __device__ __forceinline__ Place(const KvAttentionArgs& a, int b, int64_t pos, bool read)
-        : page(-1), slot(0) {
+    uint32_t id;
+    int32_t slot;
+    bool read;
+    __device__ __forceinline__ Place(const KvAttentionArgs& a, int b, int64_t pos, bool read_)
+        : id(0), slot(0), read(read_) {
         if (!read) return;
         // pos / page_size for positions below 2^33: off by less than 2^-31 before rounding down
         const int64_t lp = a.page_inverse == 0 ? pos : __umul64hi(pos, a.page_inverse);
         slot = static_cast<int32_t>(pos - lp * a.page_size);
-        const uint32_t id = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
-        if (id < static_cast<uint32_t>(a.num_pages)) page = static_cast<int32_t>(id);
-        else report(a.status, PKM_ERR_OUT_OF_RANGE);
+        id = __ldg(a.page_table + static_cast<int64_t>(b) * a.max_pages + lp);
+    }
+    __device__ __forceinline__ int32_t page(const KvAttentionArgs& a) const {
+        if (!read) return -1;
+        if (id < static_cast<uint32_t>(a.num_pages)) return static_cast<int32_t>(id);
+        report(a.status, PKM_ERR_OUT_OF_RANGE);
+        return -1;
     }
     // Offset of the slot in the layer, or -1.
     __device__ __forceinline__ int64_t offset(const KvAttentionArgs& a) const {
-        return page < 0 ? -1 : page * a.page_stride + slot * a.slot_stride;
+        const int32_t p = page(a);
+        return p < 0 ? -1 : p * a.page_stride + slot * a.slot_stride;
     }
 };
 
@@ -915,16 +923,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return true;
         };
-        // Hands values over, or keys: to the MMAs, or to the warps that look them through first.
-        const auto arrive = [&](bool keys, uint32_t stage, bool masked) {
-            if (keys) {
-                if (lane == 0) mbar_arrive(&bars->k_full[stage]);
-            } else if (masked) {
-                if (lane == 0) mbar_arrive(&bars->v_own[stage]);
-            } else if (lane < 4) {
-                mbar_arrive(&bars->v_full[stage]);
-            }
-        };
         if constexpr (TMA) {
             const int slots = maps.slots, boxes = kTile / slots;
             while (ok && publish()) {
@@ -936,6 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int32_t kt = x >= lead ? x + w.gap : x;
                     const int64_t pos = static_cast<int64_t>(kt) * kTile + lane * slots;
                     const Place place(a, w.b, pos, lane < boxes && w.reads(a, pos, slots));
+                    const int32_t page = place.page(a);
                     ok = issue_wait(&bars->k_empty[kpos.stage], kpos.phase ^ 1);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[kpos.stage], S::kBytes);
@@ -943,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t box = lane * slots * DB * 128;
                     if (lane < boxes)
                         tma_load_5d(sK + kpos.stage * S::kBytes + box, &maps.k, &bars->k_full[kpos.stage], 0, 0,
-                                    w.head * DB, place.slot >> 3, place.page);
+                                    w.head * DB, place.slot >> 3, page);
                     kpos.next(S::kKeyStages);
                     ok = issue_wait(&bars->v_empty[vpos.stage], vpos.phase ^ 1);
                     if (!ok) break;
@@ -954,21 +953,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane < boxes)
                         tma_load_5d(sV + vpos.stage * S::kBytes + box, &maps.v, bar, 0, 0, w.head * DB,
-                                    place.slot >> 3, place.page);
+                                    place.slot >> 3, page);
                     vpos.next(S::kValueStages);
                     if (S::kBeforeQueries > 0 && x == before) ok = load_queries();
                 }
             }
         } else {
-            // Row by row: a row's 16-byte chunks to their places in the swizzled atoms.  A tile is
-            // handed over when the next one is on its way, or before any longer wait.
-            bool pending = false, pending_keys = false, pending_masked = false;
-            uint32_t pending_stage = 0;
+            // Row by row: a row's 16-byte chunks to their places in the swizzled atoms, keys and values
+            // of a tile together, since a row's place is found once for both.  A tile is handed over
+            // when the next one is on its way, or before any longer wait.  Bound by the warp's
+            // instructions, 6 500 cycles a tile with D = 128: a chunk behind 16 384 keys takes 2.3 times
+            // as long as by TMA, single tokens 1.8 times (keys and values each by themselves, every
+            // row's page asked for when it is due: 3.1 to 3.6 times).
+            bool pending = false, pending_masked = false;
+            uint32_t pending_keys = 0, pending_values = 0;
             const auto hand_over = [&] {
                 __syncwarp();
                 fence_proxy_async_smem();
                 __syncwarp();
-                arrive(pending_keys, pending_stage, pending_masked);
+                if (lane == 0) mbar_arrive(&bars->k_full[pending_keys]);
+                if (pending_masked) {
+                    if (lane == 0) mbar_arrive(&bars->v_own[pending_values]);
+                } else if (lane < 4) {
+                    mbar_arrive(&bars->v_full[pending_values]);
+                }
                 pending = false;
             };
             const auto flush = [&] {
@@ -976,37 +984,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (pending) hand_over();
             };
             constexpr int kChunks = DB * 8, kRows = 32 / kChunks;  // of a row; rows at once
-            const int chunk = lane % kChunks;
+            const int chunk = lane % kChunks, first = lane / kChunks;
             while (ok) {
                 flush();
                 if (!publish()) break;
                 const Masked masks(a, w.r.len + w.token0, w.tokens);
                 const int32_t lead = w.gap > 0 ? a.sink_tiles : INT32_MAX;
+                const uint16_t* columns = a.cache_layer + w.head * D + chunk * 8;
+                const auto place_of = [&](int x, int k) -> Place {  // of the lane's row of 32
+                    const int64_t pos = static_cast<int64_t>(x >= lead ? x + w.gap : x) * kTile + k * 32 + lane;
+                    return Place(a, w.b, pos, x >= w.x0 && w.reads(a, pos, 1));
+                };
+                Place place = place_of(w.x1 - 1, 0);
                 ok = load_queries();
-                for (int y = 0; ok && y < 2 * (w.x1 - w.x0); ++y) {  // keys, then values, of each tile
-                    const bool keys = (y & 1) == 0;
-                    const int x = w.x1 - 1 - (y >> 1);
+                for (int x = w.x1 - 1; ok && x >= w.x0; --x) {
                     const int32_t kt = x >= lead ? x + w.gap : x;
-                    RingPos& at = keys ? kpos : vpos;
-                    uint64_t* empty = keys ? &bars->k_empty[at.stage] : &bars->v_empty[at.stage];
-                    if (!__all_sync(0xffffffffu, mbar_try_wait(empty, at.phase ^ 1))) {
+                    uint64_t *k_empty = &bars->k_empty[kpos.stage], *v_empty = &bars->v_empty[vpos.stage];
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_try_wait(k_empty, kpos.phase ^ 1) && mbar_try_wait(v_empty, vpos.phase ^ 1))) {
                         flush();
-                        ok = issue_wait(empty, at.phase ^ 1);
+                        ok = issue_wait(k_empty, kpos.phase ^ 1) && issue_wait(v_empty, vpos.phase ^ 1);
                         if (!ok) break;
                     }
-                    const uint32_t to = smem_u32(keys ? sK : sV) + at.stage * S::kBytes;
-                    const uint16_t* plane = a.cache_layer + (keys ? 0 : a.kv_stride);
+                    uint32_t keys = smem_u32(sK) + kpos.stage * S::kBytes + (chunk >> 3) * 1024;
+                    uint32_t values = smem_u32(sV) + vpos.stage * S::kBytes + (chunk >> 3) * 1024;
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
-                        const int64_t pos = static_cast<int64_t>(kt) * kTile + k * 32 + lane;
-                        const int64_t offset = Place(a, w.b, pos, w.reads(a, pos, 1)).offset(a);
-#pragma unroll 4
-                        for (int i = 0; i < 32; i += kRows) {
-                            const int in = i + lane / kChunks, r = k * 32 + in;
-                            const int64_t from = __shfl_sync(0xffffffffu, offset, in);
-                            cp_async_16(to + (r >> 3) * DB * 1024 + (chunk >> 3) * 1024 + (r & 7) * 128 +
-                                            (((chunk & 7) ^ (r & 7)) << 4),
-                                        plane + (from < 0 ? 0 : from + w.head * D + chunk * 8), from < 0 ? 0 : 16);
+                        int64_t offset = place.offset(a);
+                        place = place_of(k < 3 ? x : x - 1, (k + 1) & 3);  // comes during these rows
+                        const uint32_t there = __ballot_sync(0xffffffffu, offset >= 0) >> first;
+                        if (offset < 0) offset = 0;
+#pragma unroll 1
+                        for (int i = 0; i < 32; i += 8) {
+#pragma unroll
+                            for (int j = 0; j < 8; j += kRows) {
+                                const int r = j + first;  // of the atom
+                                const uint16_t* from = columns + __shfl_sync(0xffffffffu, offset, i + r);
+                                const uint32_t to = r * 128 + (((chunk & 7) ^ r) << 4), bytes = (there >> (i + j) & 1u) * 16;
+                                cp_async_16(keys + to, from, bytes);
+                                cp_async_16(values + to, from + a.kv_stride, bytes);
+                            }
+                            keys += DB * 1024;
+                            values += DB * 1024;
                         }
                     }
                     cp_async_commit();
@@ -1015,10 +1034,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         hand_over();
                     }
                     pending = true;
-                    pending_keys = keys;
                     pending_masked = masks.any(kt);
-                    pending_stage = at.stage;
-                    at.next(keys ? S::kKeyStages : S::kValueStages);
+                    pending_keys = kpos.stage;
+                    pending_values = vpos.stage;
+                    kpos.next(S::kKeyStages);
+                    vpos.next(S::kValueStages);
                 }
             }
             flush();
