@@ -259,6 +259,34 @@ def test_a_million_tokens_each():
     assert ((lse.double() - exact).abs() <= e + long + 2.0 ** -20 * (1 + exact.abs())).all()
 
 
+@pytest.mark.parametrize("half", [False, True])
+def test_inputs_that_heads_and_rows_share(half):
+    """Queries, keys and values broadcast over heads or rows: as if they were written out."""
+    import paged_kv_mla_gb300 as pkm
+    rows, heads, kv, size, page = 21, 8, 4, 64, 8
+    one = torch.randint(-20000, 20000, (3, rows, 1, size), dtype=torch.int16, device="cuda")
+    row = torch.randint(-20000, 20000, (1, kv, size), dtype=torch.int16, device="cuda")
+    freqs = torch.from_numpy(freqs_table(60, 48)).cuda()
+    at = torch.arange(rows, dtype=torch.int32, device="cuda") * 2
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    table = torch.arange(3, dtype=torch.int32, device="cuda").view(1, 3)
+    results = []
+    for write_out in (False, True):
+        cache = torch.zeros(3, 2, page, kv * size, dtype=torch.int16, device="cuda")
+        desc = pkm.PagedCache(data=cache, page_table=table, layer_stride=0, page_stride=cache.stride(0),
+                              kv_stride=cache.stride(1), slot_stride=cache.stride(2), num_layers=1, num_pages=3,
+                              page_size=page, row_elems=kv * size,
+                              cache_lengths=torch.zeros(1, dtype=torch.int32, device="cuda"))
+        q, k, v = one[0].expand(rows, heads, size), one[1].expand(rows, kv, size), row.expand(rows, kv, size)
+        if write_out:
+            q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        out = torch.zeros(rows, heads, size, dtype=torch.int16, device="cuda")
+        pkm.kv_rope_paged(offsets, at, freqs, desc, 0, kv, q=q, q_out=out, k=k, v=v, half=half)
+        results.append((out, cache))
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+    assert results[0][0].any() and results[0][1].any()
+
+
 def test_requests_on_the_same_pages():
     """A common beginning, and one request twice."""
     p = make_kv(38, [100, 100, 64], [20, 20, 40], 8, 2, 128, 16)
