@@ -34,11 +34,11 @@
 // matrix product, both measured), whole calls:
 //   4 requests x 1 token, 32 heads on 8 of keys, D = 128, 65 536 keys: 164 us, 6.55 TB/s, bound by HBM;
 //   64 x 1 token, 512 to 4096 keys: 105 us, 5.7 TB/s, HBM and the calls' start and join;
-//   1 x 2048 tokens behind 16 384: 370 us, 1.58 PFLOP/s, alone, 393 us and 1.49 PFLOP/s one call after
-//     another, when the power limit lowers the clock (a matrix product then runs at 1.69).  A step (128 x 128 scores of a stage) takes
-//     1 450 cycles, of which its 16 MMAs take 1 024 and without the softmax 1 205: one place for the
-//     scores of both stages, the chain from scores to weights, and shared memory's bandwidth, which
-//     products with both operands there use up;
+//   1 x 2048 tokens behind 16 384: 365 us, 1.60 PFLOP/s, alone, 393 us and 1.49 PFLOP/s one call after
+//     another, when the power limit lowers the clock (a matrix product then runs at 1.69).  A step
+//     (128 x 128 scores of a stage) takes 1 450 cycles, of which its 16 MMAs take 1 024 and without
+//     the softmax 1 205: one place for the scores of both stages, the chain from scores to weights,
+//     and shared memory's bandwidth, which products with both operands there use up;
 //   2 x 2048 to 4096 tokens, 64 heads on 8, D = 64, the last 1024 keys and the first 4: 195 us.  A
 //     step takes 1 090 cycles, the exponentials 512 of them, an item's three tiles with masks
 //     about a fifth of its time and its start and end a sixth.
@@ -61,8 +61,8 @@ constexpr int kTile = 128;          // keys of a tile, rows of a tile of queries
 constexpr int kMaxStages = 6;       // tiles of queries, keys or values in shared memory
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWeightCol = 384;    // TMEM column of the weights, 64 a stage
-// An item's start and end, in tiles (with 1 prompts of many lengths take 4 % longer and small ragged
-// chunks 10 %, with 3 both 1 to 2 %).
+// An item's start and end, in tiles (with 1 prompts of many lengths take 5 % longer and small ragged
+// chunks 18 %, with 3 1.5 and 3 %).
 constexpr int kItemCost = 2;
 constexpr uint64_t kDrainNs = 1000000;  // a role that gave up leaves its loads time to land
 constexpr float kLazy = 8.0f;       // base-2 growth of a maximum that is let pass
@@ -1252,7 +1252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
-constexpr int kJoinBlocks = 4;  // of an SM
+constexpr int kJoinBlocks = 4;  // of an SM (3: small ragged chunks 3 % longer; 5, which spill: 4, and windows 2 %)
 // Rows that a lane joins at a time (with 4, which spill, small ragged chunks take 10 % longer, prompts
 // and single tokens in a window 3 to 5 %).
 constexpr int kJoinRows = 2;
