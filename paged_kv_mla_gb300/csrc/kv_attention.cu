@@ -168,6 +168,10 @@ struct Part {
     __device__ __forceinline__ int32_t tile(int32_t x) const { return x >= lead ? x + gap : x; }
 };
 constexpr int kParts = 4;  // that the schedule is ahead at most
+constexpr int kFound = 8;  // parts whose finds are kept
+// Tiles of a part that are looked through: three at the diagonal of 256 tokens, three at the window's
+// edge, and the last of the first tokens.
+constexpr int kFoundBits = 8;
 
 struct Bars {
     uint64_t k_full[kMaxStages];   // a tile of keys is there
@@ -197,7 +201,11 @@ struct Bars {
     Request first;
     int32_t request, head, item, unit;  // its first unit
     int32_t ctas;                // that have a share
-    uint32_t nonfinite[4];       // parts, by number, that had infinities or NaN looked through
+    // What the epilogue's warps found, by a part's number and the warp: the number's last byte, and a
+    // bit for each tile looked through, counted from the part's last, of whose quarter some rows that
+    // not all tokens attend had infinities or NaN.  A warp is less than eight parts ahead of another:
+    // the schedule keeps four, and a warp has taken the one behind that of its epilogue.
+    uint16_t nonfinite[kFound][4];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -472,6 +480,12 @@ struct Masked {
     }
 };
 
+// Place in a part's list from which to look for masked tiles behind place x, whose tile is not: over
+// those between the diagonal and the window's edge (which has another place in a list with a gap).
+__device__ __forceinline__ int32_t past_whole(const Part& p, const Masked& masks, int32_t x) {
+    return min(x - 1, masks.edge >= p.lead ? max(masks.edge - p.gap, p.lead - 1) : masks.edge);
+}
+
 // Which keys of a tile a token at position p attends: those before `end`, from `lo` on or before
 // `sinks`.
 struct Attended {
@@ -541,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->o_full[i], 1);
             mbar_init(&bars->o_empty[i], 4);
         }
-        for (int i = 0; i < 4; ++i) bars->nonfinite[i] = 0;
+        for (int i = 0; i < kFound * 4; ++i) bars->nonfinite[i / 4][i % 4] = 0;
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&bars->part_full[i], 1);
             mbar_init(&bars->part_empty[i], 15);  // all warps but the loader
@@ -1069,6 +1083,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         Part now;
         uint32_t number = 0;  // of the part `now`; 0 before the first
         int x = 0;
+        uint32_t looked = 0, found = 0;  // tiles of the part looked through, and what the warp found there
+        const auto note = [&](uint32_t part, uint32_t tiles) {
+            *const_cast<volatile uint16_t*>(&bars->nonfinite[part % kFound][warp & 3]) =
+                static_cast<uint16_t>(part << kFoundBits | tiles);
+        };
         while (true) {
             // Values of tiles with keys that not every token attends are looked through, from a part's
             // last tile: those at the diagonal, then those at the window's edge and between it and the
@@ -1085,6 +1104,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!more) break;
                     p = part;
                     x = p.x1 - 1;
+                    looked = found = 0;
+                    if (lane == 0) note(following, 0);
                 }
                 const Masked masks(a, p.diagonal[0], p.wide ? p.edge[1] : p.edge[0]);
 #pragma unroll 1
@@ -1092,8 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int32_t kt = p.tile(x);
                     if (kt < (turn == 1 ? masks.diagonal : masks.sinks)) break;
                     if (!masks.any(kt)) {
-                        // over those between; the edge's place in a list with a gap
-                        x = min(x - 1, masks.edge >= p.lead ? max(masks.edge - p.gap, p.lead - 1) : masks.edge);
+                        x = past_whole(p, masks, x);
                         continue;
                     }
                     const uint32_t tile = tiles_before + (p.x1 - 1 - x), at = tile % S::kValueStages;
@@ -1107,8 +1127,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __ballot_sync(0xffffffffu, key > last || !(sink || key > p.pos - a.window));
                     const uint32_t all = __ballot_sync(0xffffffffu, key <= p.pos && (sink || key > last - a.window));
                     const uint32_t of = turn == 1 ? following : number;
-                    if (look_through<DB>(smem_u32(sV) + at * S::kBytes, warp & 3, none, all) && lane == 0)
-                        *const_cast<volatile uint32_t*>(&bars->nonfinite[of & 3]) = of;
+                    if (look_through<DB>(smem_u32(sV) + at * S::kBytes, warp & 3, none, all)) {
+                        found |= 1u << looked;
+                        if (lane == 0) note(of, found);
+                    }
+                    ++looked;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->v_full[at]);
@@ -1149,7 +1172,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int count = min(a.tile_tokens, now.tokens - sub * a.tile_tokens);
                 const bool valid = row_token < count, whole = now.whole != 0;
                 const float inv = whole ? (st.y != 0.0f ? rcp_approx(st.y) : 0.0f) : 1.0f;
-                const bool mend = *const_cast<volatile uint32_t*>(&bars->nonfinite[number & 3]) == number;
+                // tiles whose quarter had infinities or NaN
+                const auto had = [&](int quarter) -> uint32_t {
+                    const uint32_t w = *const_cast<volatile uint16_t*>(&bars->nonfinite[number % kFound][quarter]);
+                    return w >> kFoundBits == (number & 255u) ? w & ((1u << kFoundBits) - 1u) : 0u;
+                };
+                const uint32_t mend = had(0) | had(1) | had(2) | had(3);
                 const int64_t out_row =
                     (static_cast<int64_t>(now.row) + sub * a.tile_tokens + row_token) * a.num_heads +
                     now.head * group + row_head;
@@ -1196,38 +1224,113 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bars->o_empty[stage]);
                     if (join) mbar_arrive(&bars->o_empty[stage ^ 1]);
                 }
-                if (valid && mend) {
-                    // infinities and NaN that were made zero for the rows that do not attend them
+                if (mend != 0 && (warp & 3) * 32 < count * group) {
+                    // Infinities and NaN that were made zero for the rows that do not attend them.  The
+                    // warp reads the values again, only in the quarters of tiles that had any; each lane
+                    // gathers which columns of its row meet +inf and -inf (NaN: both), and a column gets
+                    // its sum once.  (2048 tokens behind 16 384 with NaN for all new values: 414 us instead
+                    // of 369; a chunk of 4096 in a window of 1024: 517 instead of 197.)
+                    constexpr int kChunks = DB * 8, kRows = 32 / kChunks;  // of a row; rows of a load
+                    constexpr int kAhead = 4;  // loads at once (2 and 8: calls full of NaN 2 to 10 % longer)
                     const Masked masks(a, now.diagonal[0], now.wide ? now.edge[1] : now.edge[0]);
-                    const int64_t pos = now.pos + sub * a.tile_tokens + row_token;
+                    const int64_t pos = now.pos + sub * a.tile_tokens + row_token, last = now.pos + now.tokens - 1;
+                    uint32_t up[2 * DB], down[2 * DB];  // a bit a column
+#pragma unroll
+                    for (int w = 0; w < 2 * DB; ++w) up[w] = down[w] = 0;
+                    uint32_t bit = 1;  // of the tile
 #pragma unroll 1
-                    for (int y = now.x0; y < now.x1; ++y) {
-                        const int64_t first_key = static_cast<int64_t>(now.tile(y)) * kTile;
-                        if (!masks.any(now.tile(y))) continue;
+                    for (int y = now.x1 - 1; y >= now.x0 && bit <= mend;) {
+                        const int32_t kt = now.tile(y);
+                        if (!masks.any(kt)) {
+                            y = past_whole(now, masks, y);
+                            continue;
+                        }
 #pragma unroll 1
-                        for (int i = 0; i < kTile * (D / 8); ++i) {
-                            const int c = i % (D / 8) * 8;
-                            const int64_t at = first_key + i / (D / 8);
-                            if (at > pos || (a.window > 0 && at <= pos - a.window && at >= a.sinks)) continue;
-                            const int64_t from = Place(a, now.b, at, true).offset(a);
-                            if (from < 0) continue;
-                            const uint16_t* v = a.cache_layer + a.kv_stride + from + now.head * D + c;
-                            if (!any_nonfinite(ld_nc_v4(v))) continue;
+                        for (int quarter = 0; quarter < 4; ++quarter) {
+                            if ((had(quarter) & bit) == 0) continue;
+                            const int64_t key0 = static_cast<int64_t>(kt) * kTile + quarter * 32, key = key0 + lane;
+                            // of the keys that some token of the item attends
+                            const bool read =
+                                key <= last && (a.window == 0 || key < a.sinks || key > now.pos - a.window);
+                            const int64_t at = Place(a, now.b, key, read).offset(a);
 #pragma unroll 1
-                            for (int k = 0; k < 8; ++k) {
-                                const uint32_t bits = v[k];
-                                if ((bits & 0x7f80u) != 0x7f80u) continue;
-                                const float x = __uint_as_float(bits << 16);
-                                if (whole) {
-                                    uint16_t* o = a.out + out_row * D + c + k;
-                                    *o = static_cast<uint16_t>(
-                                        pack_bf16x2(__uint_as_float(static_cast<uint32_t>(*o) << 16) + x, 0.0f));
-                                } else {
-                                    reinterpret_cast<float*>(a.workspace)[(slot * ws.rows + slot_row) * D + c + k] += x;
+                            for (int i = 0; i < 32; i += kAhead * kRows) {
+                                uint4 v[kAhead];
+#pragma unroll
+                                for (int j = 0; j < kAhead; ++j) {
+                                    const int64_t from = __shfl_sync(0xffffffffu, at, i + j * kRows + lane / kChunks);
+                                    v[j] = make_uint4(0u, 0u, 0u, 0u);
+                                    if (from >= 0)
+                                        v[j] = ld_nc_v4(a.cache_layer + a.kv_stride + from + now.head * D +
+                                                        lane % kChunks * 8);
+                                }
+#pragma unroll
+                                for (int j = 0; j < kAhead; ++j) {
+                                    if (!__any_sync(0xffffffffu, any_nonfinite(v[j]))) continue;
+                                    // the lane's eight columns in their place among 32
+                                    uint32_t plus = 0, minus = 0;
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) {
+                                        const uint32_t w = k < 2 ? v[j].x : k < 4 ? v[j].y : k < 6 ? v[j].z : v[j].w;
+                                        const uint32_t h = k & 1 ? w >> 16 : w & 0xffffu;
+                                        const uint32_t column = 1u << ((lane & 3) * 8 + k);
+                                        if ((h & 0x7f80u) != 0x7f80u) continue;
+                                        if (h != 0xff80u) plus |= column;
+                                        if (h != 0x7f80u) minus |= column;
+                                    }
+#pragma unroll
+                                    for (int sh = 1; sh < 4; sh <<= 1) {
+                                        plus |= __shfl_xor_sync(0xffffffffu, plus, sh);
+                                        minus |= __shfl_xor_sync(0xffffffffu, minus, sh);
+                                    }
+#pragma unroll
+                                    for (int r = 0; r < kRows; ++r) {
+                                        const int64_t k = key0 + i + j * kRows + r;
+                                        const bool attends =
+                                            k <= pos && (a.window == 0 || k < a.sinks || k > pos - a.window);
+#pragma unroll
+                                        for (int w = 0; w < 2 * DB; ++w) {
+                                            const uint32_t u = __shfl_sync(0xffffffffu, plus, r * kChunks + w * 4);
+                                            const uint32_t d = __shfl_sync(0xffffffffu, minus, r * kChunks + w * 4);
+                                            if (attends) up[w] |= u, down[w] |= d;
+                                        }
+                                    }
                                 }
                             }
                         }
+                        bit <<= 1;
+                        --y;
                     }
+                    // The stores before are the lane's own.
+#pragma unroll
+                    for (int w = 0; w < 2 * DB; ++w) {
+                        if (!valid) up[w] = down[w] = 0;
+#pragma unroll 1
+                        for (uint32_t u = up[w], d = down[w], c = w * 32; (u | d) != 0; u >>= 8, d >>= 8, c += 8) {
+                            if (((u | d) & 0xffu) == 0) continue;
+                            const auto sum = [&](float o, int k) -> float {  // column c + k
+                                if ((d >> k & 1u) != 0) o -= INFINITY;
+                                return (u >> k & 1u) != 0 ? o + INFINITY : o;
+                            };
+                            if (whole) {
+                                uint4* to = reinterpret_cast<uint4*>(a.out + out_row * D + c);
+                                uint4 o = *to;
+                                const auto pair = [&](uint32_t h, int k) -> uint32_t {
+                                    return pack_bf16x2(sum(__uint_as_float(h << 16), k),
+                                                       sum(__uint_as_float(h & 0xffff0000u), k + 1));
+                                };
+                                o = make_uint4(pair(o.x, 0), pair(o.y, 2), pair(o.z, 4), pair(o.w, 6));
+                                *to = o;
+                            } else {
+                                float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.workspace) +
+                                                                       (slot * ws.rows + slot_row) * D + c);
+                                const float4 o0 = to[0], o1 = to[1];
+                                to[0] = make_float4(sum(o0.x, 0), sum(o0.y, 1), sum(o0.z, 2), sum(o0.w, 3));
+                                to[1] = make_float4(sum(o1.x, 4), sum(o1.y, 5), sum(o1.z, 6), sum(o1.w, 7));
+                            }
+                        }
+                    }
+                    __syncwarp();
                 }
                 if (valid && whole && a.lse != nullptr)
                     a.lse[out_row] = st.y != 0.0f ? (st.x + __log2f(st.y)) * kLn2 : -INFINITY;

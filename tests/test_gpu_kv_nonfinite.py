@@ -1,0 +1,97 @@
+"""GPU: attention over the paged K/V cache with values that are not finite in many rows, where several
+blocks share an item, and in windows."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from kv_util import DeviceKv, check, make_kv
+from spec_util import bf16_value
+
+pytestmark = pytest.mark.gpu
+INF, MINUS_INF, NAN = 0x7F80, 0xFF80, 0x7FC0
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import paged_kv_mla_gb300  # noqa: F401
+
+
+def put(p, b, t, values, cols=slice(None)):
+    """Values of request b at positions t."""
+    t = np.asarray(t)
+    row = p.cache[p.layer, p.table[b, t // p.page], 1, t % p.page]
+    row[:, :p.kv_heads * p.size][:, cols] = values
+    p.cache[p.layer, p.table[b, t // p.page], 1, t % p.page] = row
+
+
+@pytest.mark.parametrize("size", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(4, 1), (2, 2), (10, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3), (300, 130)])
+def test_all_new_values(size, heads, kv_heads, window, sinks):
+    """Every new value of one request is a NaN or an infinity, a column's sign by turns; the other
+    requests', in the same items' blocks, are not."""
+    p = make_kv(60, [500, 130, 90], [150, 333, 200], heads, kv_heads, size, 16, window, sinks, layers=1, layer=0)
+    row = np.resize(np.array([NAN, INF, MINUS_INF, INF, INF], np.uint16), kv_heads * size)
+    t = 130 + np.arange(333)
+    put(p, 1, t, row)
+    put(p, 1, t[40::50], row ^ 0x8000)  # both infinities in a column
+    check(p)
+
+
+@pytest.mark.parametrize("size", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (400, 3), (130, 200)])
+@pytest.mark.parametrize("ctx,new", [(4000, 1), (3500, 40), (500, 200)])
+def test_few_in_shared_items(size, window, sinks, ctx, new):
+    p = make_kv(61, [ctx], [new], 4, 1, size, 16, window, sinks, layers=1, layer=0)
+    last = ctx + new - 1
+    for t, c, v in [(2, 0, INF), (129, 7, MINUS_INF), (ctx - 1, 9, NAN), (ctx - 1, 33, INF), (ctx, 33, INF),
+                    (last, 40, MINUS_INF), (last - new // 2, 41, INF), (last, 42, NAN), (ctx, 50, INF),
+                    (last, 50, MINUS_INF), (last - 399, 51, INF), (max(last - 129, 0), 52, MINUS_INF),
+                    (ctx - 300, 53, NAN)]:
+        put(p, 0, [t], v, c)
+    check(p)
+
+
+@pytest.mark.parametrize("size", [64, 128])
+def test_short_items_that_take_turns(size):
+    """Thousands of items of one tile, most of which need no look at their values, behind those that
+    hold infinities."""
+    gen = np.random.default_rng(62)
+    new = gen.choice([1, 1, 1, 2, 3], 4000)
+    ctx = np.where(new == 1, 127, 128 - new)
+    p = make_kv(62, ctx.tolist(), new.tolist(), 2, 1, size, 128, layers=1, layer=0)
+    for b in np.flatnonzero(new > 1)[::2]:
+        put(p, b, [ctx[b] + new[b] - 1], INF, int(gen.integers(size)))
+        put(p, b, [ctx[b]], MINUS_INF, int(gen.integers(size)))
+    check(p)
+
+
+def time_us(d):
+    best = []
+    for _ in range(8):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        d.run()
+        b.record()
+        torch.cuda.synchronize()
+        best.append(a.elapsed_time(b) * 1e3)
+    return min(best)
+
+
+@pytest.mark.parametrize("size,window,sinks", [(128, 0, 0), (64, 512, 4)])
+def test_a_request_that_is_not_finite_does_not_hold_up_others(size, window, sinks):
+    """A diverged request's values cost a second look at its partly attended tiles (1.5 to 1.9 times
+    the call), not one for every row, key and column."""
+    p = make_kv(64, [2000, 1000], [512, 512], 32, 8, size, 128, window, sinks, layers=1, layer=0)
+    clean = time_us(DeviceKv(p))
+    put(p, 1, 1000 + np.arange(512), NAN)
+    d = DeviceKv(p)
+    took = time_us(d)
+    out, _, status = d.results()
+    assert status == 0
+    assert np.isnan(bf16_value(out[512:1024])).all() and np.isfinite(bf16_value(out[:512])).all()
+    assert took < 4 * clean, (took, clean)
