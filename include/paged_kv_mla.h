@@ -733,7 +733,10 @@ size_t kv_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
  *     out[r, h, c] = bf16( sum_t w_t * V(t)[g, c] )
  *     lse[r, h]    = log sum_t exp(softmax_scale * sum_c q[r, h, c] * K(t)[g, c])
  * What a token does not attend has no influence on it, whatever it holds (NaN and infinities
- * included).  Rows that no request covers are left untouched.  Scores and sums are fp32; the
+ * included).  An attended value that is NaN makes its column of out NaN, and an infinity makes it
+ * infinite; where the infinity's weight underflows to 0 in fp32 the column is infinite or NaN, and
+ * which of the two may differ between a chunk and the same token by itself.  Rows that no request
+ * covers are left untouched.  Scores and sums are fp32; the
  * weights are rounded to bf16 for the second product.  Two calls with the same arguments on the
  * same device give the same bits.
  *

@@ -1,5 +1,5 @@
 """GPU: attention over the paged K/V cache with values that are not finite in many rows, where several
-blocks share an item, and in windows."""
+blocks share an item, in windows, and where weights underflow."""
 from __future__ import annotations
 
 import numpy as np
@@ -68,6 +68,32 @@ def test_short_items_that_take_turns(size):
         put(p, b, [ctx[b] + new[b] - 1], INF, int(gen.integers(size)))
         put(p, b, [ctx[b]], MINUS_INF, int(gen.integers(size)))
     check(p)
+
+
+@pytest.mark.parametrize("size", [64, 128])
+@pytest.mark.parametrize("ctx,new", [(300, 1), (200, 180)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 2)])
+def test_weights_that_underflow(size, ctx, new, window, sinks):
+    """Attended infinities whose weights are often 0 in 32 bits: never a finite column; those that
+    are not attended leave theirs as it is."""
+    p = make_kv(63, [ctx], [new], 4, 1, size, 16, window, sinks, layers=1, layer=0, q_std=30.0)
+    clean = p.reference()
+    at = [1, ctx // 2, ctx, ctx + new - 1]
+    for j, t in enumerate(at):
+        put(p, 0, [t], INF, 3 + j)
+    d = DeviceKv(p)
+    d.run()
+    out, lse, status = d.results()
+    assert status == 0
+    seen = p.seen(0)[:, at]  # [new, values]
+    assert seen.any() and (new == 1 or not seen.all())
+    got = bf16_value(out[:new])
+    for j in range(len(at)):
+        with_it = got[seen[:, j], :, 3 + j]
+        assert (np.isnan(with_it) | (with_it == np.inf)).all()
+        got[seen[:, j], :, 3 + j] = clean[0][seen[:, j], :, 3 + j]
+    ref, tol = clean[:2]
+    assert (np.abs(got - ref) <= tol).all()
 
 
 def time_us(d):
