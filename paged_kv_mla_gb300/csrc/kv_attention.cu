@@ -618,7 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t out = lanes + S::out_col(stage);
         uint32_t uses = 0;
         bool next = false;  // the next step's scores are there
-        // A wait that runs out is looked at once a part; what is computed until then is not used.
+        // A wait that runs out is looked at where the next scores have to be waited for, as they have
+        // behind it: their issuer leaves too.  What is computed until then is not used.
         bool ok = true;
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = mbar_wait_inl(bar, parity, wc) && ok;
@@ -636,7 +637,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.0f, ref = 0.0f;  // ref: m, or 0 before there is one
             for (int x = mine; x < steps; x += 2) {
                 const uint32_t turn = (n + x) >> 1;  // of the stage
-                if (!__all_sync(0xffffffffu, next)) wait(&bars->s_full[stage], turn & 1);
+                if (!__all_sync(0xffffffffu, next)) {
+                    wait(&bars->s_full[stage], turn & 1);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                }
                 tc_fence_after();
                 if (!busy) {
                     next = false;
@@ -760,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&bars->p_full[stage]);
             }
             n += steps;
-            if (mine >= steps) continue;
+            if (mine >= steps || !__all_sync(0xffffffffu, ok)) continue;
             if (uses > 0) wait(&bars->o_empty[stage], (uses - 1) & 1);  // read with its O
             bars->stats[stage][row] = make_float2(m, l);
             ++uses;
