@@ -1360,9 +1360,6 @@ pkm_status kv_attention(const void* q, int64_t q_row_stride, int64_t q_head_stri
         kv_attention_paged_workspace_size(total_rows, num_heads, num_kv_heads, head_size))
         return PKM_ERR_INVALID_ARG;
     KvAttentionArgs a{};
-    a.q = static_cast<const uint16_t*>(q);
-    a.q_row_stride = q_row_stride;
-    a.q_head_stride = q_head_stride;
     a.row_offsets = input_row_offsets;
     a.batch = batch;
     a.total_rows = total_rows;

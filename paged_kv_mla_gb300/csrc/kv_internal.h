@@ -33,10 +33,9 @@ struct KvRopeArgs {
     int32_t* status;
 };
 
-// One attention over the paged K/V cache, already validated (strides in elements).
+// One attention over the paged K/V cache, already validated (strides in elements); the queries come
+// by tensor maps.
 struct KvAttentionArgs {
-    const uint16_t* q;             // [total_rows, num_heads, D] by strides
-    int64_t q_row_stride, q_head_stride;
     const uint32_t* row_offsets;   // [batch + 1]
     int32_t batch, total_rows, num_heads, num_kv_heads, head_size;
     float scale;
