@@ -665,6 +665,7 @@ def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_co
 
 
 _NO_STRIDE = (0, 0)  # of a tensor that is not given
+_LISTS = (list, tuple, bytes)  # that bytes() takes item by item
 
 
 def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
@@ -702,8 +703,8 @@ def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
         sv = v.stride()
         ok = v.shape == (rows, num_kv_heads, size) and sv[2] == 1 and v.dtype in _BF16
     if ok and pair_axes is not None:
-        try:
-            pair_axes = bytes(pair_axes)
+        try:  # item by item: bytes() alone takes an array's memory, and a number for a length
+            pair_axes = bytes(pair_axes if pair_axes.__class__ in _LISTS else list(pair_axes))
         except (TypeError, ValueError):
             ok = False
         ok = ok and len(pair_axes) == factors[1] // 2
