@@ -666,6 +666,7 @@ def mla_cache_compact_paged_qcache(cache: QuantCache, layer_begin: int, layer_co
 
 _NO_STRIDE = (0, 0)  # of a tensor that is not given
 _LISTS = (list, tuple, bytes)  # that bytes() takes item by item
+_INT32_MAX = 2 ** 31 - 1  # ctypes cuts larger numbers off without a word
 
 
 def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
@@ -689,7 +690,7 @@ def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
     rows, axes = (counts[0], 1) if n == 1 else (counts[1], counts[0]) if n == 2 else (-1, 0)
     size = kv_cache.row_elems // num_kv_heads if num_kv_heads > 0 else 0
     ok = device is not None and rows >= 0 and len(pages) == 2 and pages[0] >= batch and len(factors) == 2 \
-        and (q is None) == (q_out is None)
+        and (q is None) == (q_out is None) and 0 <= layer_idx <= _INT32_MAX
     heads, sq, so, sk, sv = 0, _NO_STRIDE, _NO_STRIDE, _NO_STRIDE, _NO_STRIDE
     if ok and q is not None:
         shape, sq, so = q.shape, q.stride(), q_out.stride()
@@ -734,7 +735,8 @@ def _kv_attention(f, where, q, offsets, scale, limits, cache, layer_idx, out, wo
     strides = q.stride()
     if device is None or len(shape) != 3 or strides[2] != 1 or q.dtype not in _BF16 or out.shape != shape \
             or not workspace.is_contiguous() or (lse is not None and lse.shape != shape[:2]) \
-            or len(pages) != 2 or pages[0] < batch or shape[2] == 0 or cache.row_elems % shape[2] != 0:
+            or len(pages) != 2 or pages[0] < batch or shape[2] == 0 or cache.row_elems % shape[2] != 0 \
+            or not 0 <= layer_idx <= _INT32_MAX or limits and not (0 <= min(limits) and max(limits) <= _INT32_MAX):
         return _check(PKM_ERR_INVALID_ARG, where, check)
     c = cache._struct_of((at[5], at[6], pages[1], at[7]))
     args = (at[0], strides[0], strides[1], at[1], batch, shape[0], shape[1],

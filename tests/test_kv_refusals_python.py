@@ -33,3 +33,14 @@ def test_axes_of_pairs_in_any_array(pkm, axes, monkeypatch):
     torch.tensor(AXES, dtype=torch.float32), [0.0] * 64, np.array(AXES) + 256, np.array(AXES) - 1], ids=named)
 def test_other_axes_are_refused(pkm, axes):
     assert rope(pkm, cache(pkm), axes=3, pair_axes=axes) == INVALID
+
+
+@pytest.mark.parametrize("n", [2 ** 32, 2 ** 32 + 5, 2 ** 63, -2 ** 32 + 5, 2 ** 31])
+def test_numbers_past_32_bits(pkm, n):
+    """No cut-off: 2^32 + 5 is not a window of 5, nor 2^32 layer 0."""
+    c = cache(pkm)
+    assert attention(pkm, c, window=n) == INVALID and attention(pkm, c, window=7, sinks=n) == INVALID
+    assert attention(pkm, c, layer=n) == INVALID and rope(pkm, c, layer=n) == INVALID
+    assert attention(pkm, c, window=2 ** 31 - 1, sinks=2 ** 31 - 1) == GOES_ON
+    assert attention(pkm, c, window=np.int64(7), sinks=np.int32(1), layer=np.int64(0)) == GOES_ON
+    assert rope(pkm, c, layer=np.int64(0)) == GOES_ON
