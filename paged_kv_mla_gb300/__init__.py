@@ -685,7 +685,7 @@ def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
     pages, batch = table.shape, input_row_offsets.shape[0] - 1
     device, at = _look(((_WORD, 0, input_row_offsets), (_WORD, 0, positions), (_FLOAT, 0, freqs_cis),
                         (None, 0, kv_cache.data), (_WORD, 0, table), (_WORD, batch, kv_cache.cache_lengths),
-                        (None, 0, q), (None, 0, q_out), (None, 0, k), (None, 0, v)))
+                        (None, 0, q), (None, 0, q_out), (None, 0, k), (None, 0, v), (_WORD, 1, dev_status)))
     n = len(counts)
     rows, axes = (counts[0], 1) if n == 1 else (counts[1], counts[0]) if n == 2 else (-1, 0)
     size = kv_cache.row_elems // num_kv_heads if num_kv_heads > 0 else 0
@@ -714,7 +714,7 @@ def kv_rope_paged(input_row_offsets: torch.Tensor, positions: torch.Tensor,
     c = kv_cache._struct_of((at[3], at[4], pages[1], at[5]))
     args = (at[6], sq[0], sq[1], heads, at[7], so[0], so[1], at[8], sk[0], sk[1], at[9], sv[0], sv[1],
             num_kv_heads, size, factors[1], at[0], batch, rows, at[1], axes, pair_axes, at[2],
-            factors[0], 1 if half else 0, ctypes.byref(c), layer_idx, _ptr(dev_status))
+            factors[0], 1 if half else 0, ctypes.byref(c), layer_idx, at[10])
     return _run(_lib.kv_rope_paged, "kv_rope_paged", args, device, stream, check)
 
 
@@ -731,7 +731,7 @@ def _kv_attention(f, where, q, offsets, scale, limits, cache, layer_idx, out, wo
     shape, pages, batch = q.shape, table.shape, offsets.shape[0] - 1
     device, at = _look(((None, 0, q), (_WORD, 0, offsets), (_BF16, 0, out), (None, 0, workspace),
                         (_FLOAT, 0, lse), (None, 0, cache.data), (_WORD, 0, table),
-                        (_WORD, batch, cache.cache_lengths)))
+                        (_WORD, batch, cache.cache_lengths), (_WORD, 1, dev_status)))
     strides = q.stride()
     if device is None or len(shape) != 3 or strides[2] != 1 or q.dtype not in _BF16 or out.shape != shape \
             or not workspace.is_contiguous() or (lse is not None and lse.shape != shape[:2]) \
@@ -741,7 +741,7 @@ def _kv_attention(f, where, q, offsets, scale, limits, cache, layer_idx, out, wo
     c = cache._struct_of((at[5], at[6], pages[1], at[7]))
     args = (at[0], strides[0], strides[1], at[1], batch, shape[0], shape[1],
             cache.row_elems // shape[2], shape[2], float(scale), *limits, ctypes.byref(c),
-            int(layer_idx), at[2], at[4], at[3], workspace.nbytes, _ptr(dev_status))
+            int(layer_idx), at[2], at[4], at[3], workspace.nbytes, at[8])
     return _run(f, where, args, device, stream, check)
 
 

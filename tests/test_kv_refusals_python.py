@@ -44,3 +44,41 @@ def test_numbers_past_32_bits(pkm, n):
     assert attention(pkm, c, window=2 ** 31 - 1, sinks=2 ** 31 - 1) == GOES_ON
     assert attention(pkm, c, window=np.int64(7), sinks=np.int32(1), layer=np.int64(0)) == GOES_ON
     assert rope(pkm, c, layer=np.int64(0)) == GOES_ON
+
+
+@pytest.mark.parametrize("word,status", [
+    (None, GOES_ON), (torch.zeros(1, dtype=torch.int32), GOES_ON), (torch.zeros(1, dtype=torch.int32).view(torch.uint32), GOES_ON),
+    (torch.zeros((), dtype=torch.int32), GOES_ON), (torch.zeros(0, dtype=torch.int32), INVALID),
+    (torch.zeros(1, dtype=torch.int64), INVALID), (torch.zeros(4, dtype=torch.uint8), INVALID)])
+def test_the_status_word(pkm, word, status):
+    c = cache(pkm)
+    q, out, ws = torch.zeros(3, 8, 128, dtype=torch.int16), torch.zeros(3, 8, 128, dtype=torch.int16), workspace(pkm)
+    rows = torch.zeros(3, dtype=torch.int32)
+    kw = dict(dev_status=word, stream=0, check=False)
+    assert pkm.kv_attention_paged(q, rows, 1.0, c, 0, out, ws, **kw) == status
+    assert pkm.kv_window_attention_paged(q, rows, 1.0, 9, 1, c, 0, out, ws, **kw) == status
+    assert pkm.kv_rope_paged(rows, rows, torch.zeros(16, 128), c, 0, 4, q=q, q_out=out, **kw) == status
+
+
+def workspace(pkm):
+    n = pkm.kv_attention_paged_workspace_size(3, 8, 4, 128)
+    raw = torch.zeros(n + 256, dtype=torch.uint8)
+    return raw[-raw.data_ptr() % 256:][:n]
+
+
+@pytest.mark.gpu
+def test_a_status_word_on_the_host():
+    """Beside tensors on the GPU: refused, and nothing is launched that would write to it."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import paged_kv_mla_gb300 as m
+    from kv_util import OUT_FILL, DeviceKv, make_kv
+    d = DeviceKv(make_kv(70, [30], [5], 8, 2, 64, 16))
+    d.status = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(m.PkmError):
+        d.run()
+    with pytest.raises(m.PkmError):
+        m.kv_rope_paged(d.offsets, torch.zeros(5, dtype=torch.int32, device="cuda"), torch.zeros(1, 64, device="cuda"),
+                        d.desc, d.p.layer, 2, q=d.q, q_out=d.out, dev_status=d.status)
+    torch.cuda.synchronize()
+    assert (d.out == OUT_FILL).all()
