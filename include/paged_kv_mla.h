@@ -746,7 +746,7 @@ size_t kv_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
  *   num_heads       a multiple of num_kv_heads, at most 128 times it; total_rows * num_heads at
  *                   most 2^31 - 257.
  *   head_size       64 or 128; row_elems = num_kv_heads * head_size.
- *   softmax_scale   finite.
+ *   softmax_scale   finite, and so is its product with log2(e) in fp32.
  *   kv_cache        cache_lengths required; kv_stride >= row_elems.
  *   out             device bf16 [total_rows, num_heads, head_size], 16-byte aligned, apart from q.
  *   lse             device fp32 [total_rows, num_heads], or NULL.

@@ -1338,8 +1338,9 @@ pkm_status kv_attention(const void* q, int64_t q_row_stride, int64_t q_head_stri
         num_heads % num_kv_heads != 0)
         return PKM_ERR_INVALID_ARG;
     if (total_rows == 0 || batch == 0) return PKM_OK;
+    // scores are kept in base 2: their scale, softmax_scale * log2(e), is finite too
     if (q == nullptr || input_row_offsets == nullptr || out == nullptr || workspace == nullptr ||
-        !std::isfinite(softmax_scale))
+        !std::isfinite(softmax_scale * 1.4426950408889634f))
         return PKM_ERR_INVALID_ARG;
     if (const pkm_status st = check_kv_cache(kv_cache, layer_idx, num_kv_heads, head_size))
         return st;

@@ -46,6 +46,14 @@ def test_numbers_past_32_bits(pkm, n):
     assert rope(pkm, c, layer=np.int64(0)) == GOES_ON
 
 
+@pytest.mark.parametrize("scale,status", [(2.3e38, GOES_ON), (-2.3e38, GOES_ON), (2.4e38, INVALID), (-3.4e38, INVALID),
+                                          (1e39, INVALID)])
+def test_scales_whose_base_2_overflows(pkm, scale, status):
+    """The scores' scale in base 2 would be infinite, and a score of 0 a NaN."""
+    assert attention(pkm, cache(pkm), scale=scale) == status
+    assert attention(pkm, cache(pkm), scale=scale, window=9) == status
+
+
 @pytest.mark.parametrize("word,status", [
     (None, GOES_ON), (torch.zeros(1, dtype=torch.int32), GOES_ON), (torch.zeros(1, dtype=torch.int32).view(torch.uint32), GOES_ON),
     (torch.zeros((), dtype=torch.int32), GOES_ON), (torch.zeros(0, dtype=torch.int32), INVALID),
