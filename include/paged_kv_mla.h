@@ -742,7 +742,8 @@ size_t kv_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
  *
  *   q               device bf16, 16-byte aligned; row r, head h, column c at r * q_row_stride +
  *                   h * q_head_stride + c, strides in elements, multiples of 8, for which no two
- *                   heads overlap.
+ *                   heads overlap: they come by tensor maps, which are asked for whole heads apart.
+ *                   (Heads that share a query: written out first, as kv_rope_paged does.)
  *   num_heads       a multiple of num_kv_heads, at most 128 times it; total_rows * num_heads at
  *                   most 2^31 - 257.
  *   head_size       64 or 128; row_elems = num_kv_heads * head_size.
