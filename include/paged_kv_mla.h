@@ -735,8 +735,8 @@ size_t kv_attention_paged_workspace_size(int32_t total_rows, int32_t num_heads,
  * What a token does not attend has no influence on it, whatever it holds (NaN and infinities
  * included).  An attended value that is NaN makes its column of out NaN, and an infinity makes it
  * infinite; where the infinity's weight underflows to 0 in fp32 the column is infinite or NaN, and
- * which of the two may differ between a chunk and the same token by itself.  Rows that no request
- * covers are left untouched.  Scores and sums are fp32; the
+ * which of the two may differ between a chunk and the same token by itself.  A row whose scores are
+ * all -inf has NaN in out and -inf in lse.  Rows that no request covers are left untouched.  Scores and sums are fp32; the
  * weights are rounded to bf16 for the second product.  Two calls with the same arguments on the
  * same device give the same bits.
  *

@@ -1175,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int count = min(a.tile_tokens, now.tokens - sub * a.tile_tokens);
                 const bool valid = row_token < count, whole = now.whole != 0;
-                const float inv = whole ? (st.y != 0.0f ? rcp_approx(st.y) : 0.0f) : 1.0f;
+                const float inv = whole ? rcp_approx(st.y) : 1.0f;  // a sum of 0, all scores -inf: NaN
                 // tiles whose quarter had infinities or NaN
                 const auto had = [&](int quarter) -> uint32_t {
                     const uint32_t w = *const_cast<volatile uint16_t*>(&bars->nonfinite[number % kFound][quarter]);
@@ -1457,7 +1457,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
     };
     const int col = (lane % kLanes) * 4;
     const auto finish = [&](const Sum& x, int64_t out) {
-        const float inv = x.total != 0.0f ? 1.0f / x.total : 0.0f;
+        const float inv = 1.0f / x.total;  // a sum of 0, all scores -inf: NaN
         *reinterpret_cast<uint2*>(a.out + out * D + col) =
             make_uint2(pack_bf16x2(x.o.x * inv, x.o.y * inv), pack_bf16x2(x.o.z * inv, x.o.w * inv));
         if (a.lse != nullptr && col == 0)

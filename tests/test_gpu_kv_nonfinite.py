@@ -96,6 +96,40 @@ def test_weights_that_underflow(size, ctx, new, window, sinks):
     assert (np.abs(got - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("size", [64, 128])
+@pytest.mark.parametrize("ctx,new", [(20, 1), (3000, 1), (100, 60), (3000, 90)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 2)])
+def test_scores_of_minus_infinity(size, ctx, new, window, sinks):
+    """Keys whose scores are -inf weigh nothing; a row that attends no others is NaN, as 0 / 0 is, and
+    its log-sum-exp -inf."""
+    p = make_kv(65, [ctx, ctx], [new, new], 4, 2, size, 16, window, sinks, layers=1, layer=0)
+    p.q[:, :2, 0] = 0x3F80  # 1, for the heads of the first head of keys
+    t = np.arange(ctx + new)
+    least = t % 3 == 1
+    least[ctx:] = np.arange(new) % 2 == 1
+    where = [np.flatnonzero(least), t]  # some keys of one request, all of the other
+    for b in range(2):
+        p.cache[0, p.table[b, where[b] // 16], 0, where[b] % 16, 0] = MINUS_INF
+    d = DeviceKv(p)
+    d.run()
+    out, lse, status = d.results()
+    assert status == 0
+    assert np.isnan(bf16_value(out[new:2 * new, :2])).all() and (lse[new:2 * new, :2] == -np.inf).all()
+    seen = p.seen
+    p.seen = lambda b: seen(b) & ~least
+    ref = p.reference()
+    p.seen = seen
+    rest = p.reference()
+    some = seen(0) & ~least
+    rows = np.flatnonzero(some.any(1))
+    none = np.flatnonzero(~some.any(1))
+    assert np.isnan(bf16_value(out[none, :2])).all() and (lse[none, :2] == -np.inf).all()
+    for heads, (o, tol, l, l_tol), pick in ((slice(0, 2), ref, rows), (slice(2, 4), rest, np.arange(2 * new))):
+        got = bf16_value(out[pick, heads])
+        assert (np.abs(got - o[pick, heads]) <= tol[pick, heads]).all()
+        assert (np.abs(lse[pick, heads] - l[pick, heads]) <= l_tol[pick, heads]).all()
+
+
 def time_us(d):
     best = []
     for _ in range(8):
